@@ -269,6 +269,137 @@ int pd_decode_attn_noalloc(const void *q, const void *k_cache, const void *v_cac
                            int num_blocks, float inv_sqrt_d, int num_splits, int gqa_pack,
                            void *stream);
 
+/* ---- rotary positions ------------------------------------------------------
+ * The rotation of a query or key row x of head_dim columns at position t: its
+ * first rot_dim columns form rot_dim/2 pairs (a, b), pair i turned by the
+ * angle t * f[i],
+ *     a' = c (a cos(t f[i]) - b sin(t f[i])),  b' = c (b cos(t f[i]) + a sin(t f[i])),
+ * and the columns from rot_dim on are copied.  The layout says which columns
+ * pair up; the scaling rule says what f and c are. */
+#define PD_ROPE_HALF 0        /* pair i is columns (i, i + rot_dim/2) */
+#define PD_ROPE_INTERLEAVED 1 /* pair i is columns (2i, 2i + 1) */
+
+/* Scaling rules, with f0[i] = base^(-2i/rot_dim), s = factor and
+ * n[i] = original_context * f0[i] / (2 pi), the turns pair i makes within the
+ * original context:
+ *   NONE    f = f0
+ *   LINEAR  f = f0 / s (positions interpolated)
+ *   NTK     f0 of the base  base * s^(rot_dim / (rot_dim - 2))  (rot_dim >= 4)
+ *   BANDED  f = f0 (w + (1 - w) / s), w = clamp((n - low) / (high - low), 0, 1):
+ *           pairs of few turns interpolated, pairs of many turns kept
+ *           (low_turns, high_turns; 0 and 0 stand for 1 and 4)
+ *   YARN    f = f0 (1 - r + r / s), r[i] = clamp((i - i0) / max(i1 - i0, 0.001), 0, 1)
+ *           with i0 = max(floor(p(high)), 0), i1 = min(ceil(p(low)), rot_dim - 1),
+ *           p(n) = rot_dim ln(original_context / (2 pi n)) / (2 ln base)
+ *           (low_turns, high_turns; 0 and 0 stand for 1 and 32), and
+ *           c = 0.1 ln(s) + 1 (1 for s <= 1)
+ *   TABLE   f = frequencies[0 .. rot_dim/2)
+ * c is attention_factor where that is > 0, else the rule's (1 but for YARN). */
+#define PD_ROPE_NONE 0
+#define PD_ROPE_LINEAR 1
+#define PD_ROPE_NTK 2
+#define PD_ROPE_BANDED 3
+#define PD_ROPE_YARN 4
+#define PD_ROPE_TABLE 5
+
+typedef struct pd_rope_desc {
+    int head_dim;              /* multiple of 8 in [8, PD_MAX_HEAD_DIM] */
+    int rot_dim;               /* even, 2..head_dim */
+    int layout;                /* PD_ROPE_HALF or PD_ROPE_INTERLEAVED */
+    int scaling;               /* a PD_ROPE_* rule */
+    double base;               /* > 1 (unused by TABLE) */
+    double factor;             /* s > 0 (unused by NONE and TABLE) */
+    double original_context;   /* > 0 (BANDED and YARN) */
+    double low_turns;          /* BANDED and YARN; 0 with high_turns 0: the default */
+    double high_turns;
+    double attention_factor;   /* c; 0: the rule's */
+    const double *frequencies; /* TABLE: rot_dim/2 angles per position, host memory, read during the call */
+} pd_rope_desc;
+
+typedef struct pd_rope pd_rope;
+
+/* The frequencies f (rot_dim/2 doubles) and the factor c of a description, on
+ * the host; either pointer may be NULL.  Returns PD_OK or PD_ERR_INVALID /
+ * PD_ERR_UNSUPPORTED. */
+int pd_rope_frequencies(const pd_rope_desc *desc, double *frequencies, double *attention_factor);
+
+/* Validate a description and lay its table out on the current device (one
+ * small allocation and copy, done before the call returns; nothing later
+ * allocates).  *out receives the handle, which is read-only afterwards and may
+ * serve any number of streams and threads on that device.  Returns PD_OK,
+ * PD_ERR_INVALID, PD_ERR_UNSUPPORTED, PD_ERR_ALLOC or PD_ERR_CUDA. */
+int pd_rope_create(const pd_rope_desc *desc, pd_rope **out);
+
+/* Free the handle (NULL is a no-op).  Synchronises the device first. */
+void pd_rope_destroy(pd_rope *rope);
+
+/* Rotate num_tokens x num_heads rows.
+ *   x, out     BF16, 16-B aligned; row (t, h) starts at element
+ *              t * token_stride + h * head_stride (strides positive multiples of 8 elements; the
+ *              head_dim columns of a row are contiguous).  out is x itself with
+ *              x's strides (in place), or shares no element with it.
+ *   positions  [num_tokens] int32; any value, negative ones turn backwards.
+ *   inverse    0, or 1 for the rotation by minus the angles with the same
+ *              factor c: the transposed map, which takes gradients of out to
+ *              gradients of x (and undoes the rotation where c is 1).
+ * Angles are reduced exactly (64-bit fixed-point turns), so far positions cost
+ * no accuracy; the arithmetic is FP32, rounded to BF16 once.
+ * Returns PD_OK, PD_ERR_INVALID (also for a handle of another device than the
+ * current one) or PD_ERR_CUDA. */
+int pd_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride, int64_t x_head_stride,
+                  const int32_t *positions, void *out, int64_t out_token_stride,
+                  int64_t out_head_stride, int num_tokens, int num_heads, int inverse, void *stream);
+
+/* ---- append to the paged cache ---------------------------------------------
+ * Put new tokens' keys and values into the paged cache pd_decode_attn reads,
+ * rotating the keys, and the queries on the way, by their positions.
+ *   rope          the rotation, of the same head_dim; NULL: none (q and k are copied).
+ *   q             [num_tokens, num_q_heads, head_dim] BF16, or NULL: no queries
+ *                 (then q_out is not written and num_q_heads is ignored).
+ *   k, v          [num_tokens, num_kv_heads, head_dim] BF16.
+ *   *_token_stride  elements from one token to the next (a multiple of 8, at
+ *                 least heads * head_dim: the rows of a token are contiguous),
+ *                 so q, k and v may be slices of one fused projection.
+ *   q_out         [num_tokens, num_q_heads, head_dim] BF16, contiguous; may be q
+ *                 itself where q is contiguous, else shares no element with it.
+ *   k_cache, v_cache  [num_blocks, block_size, num_kv_heads, head_dim] BF16.
+ *   block_table   [num_seqs, max_blocks_per_seq] int32, as for pd_decode_attn.
+ *   context_lens  [num_seqs] int32: tokens of each sequence AFTER the append,
+ *                 the lengths the following pd_decode_attn takes.
+ *   token_starts  [num_seqs + 1] int32, non-decreasing: rows token_starts[s] to
+ *                 token_starts[s+1] - 1 are the new tokens of sequence s, its
+ *                 last ones.  Rows before token_starts[0] and from
+ *                 token_starts[num_seqs] on belong to no sequence: nothing of
+ *                 them is read or written.  NULL: one token per sequence
+ *                 (num_tokens == num_seqs), none for a sequence of length 0.
+ * A token whose position is negative or beyond its block table raises
+ * PD_DEV_BAD_CONTEXT_LEN and is left out (q_out too); one whose block id is
+ * outside [0, num_blocks) raises PD_DEV_BAD_BLOCK_ID and its key and value are
+ * left out.  Two tokens that name the same cache slot (tables that share a
+ * block the batch writes) race for it: the caller keeps written blocks apart.
+ * q, k, v, q_out and the caches are 16-B aligned.  Shape limits are
+ * pd_decode_attn's.  Nothing is allocated.
+ * Returns PD_OK, PD_ERR_INVALID, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
+int pd_append_kv(const pd_rope *rope, const void *q, int64_t q_token_stride, const void *k,
+                 int64_t k_token_stride, const void *v, int64_t v_token_stride, void *q_out,
+                 void *k_cache, void *v_cache, const int32_t *block_table, int max_blocks_per_seq,
+                 const int32_t *context_lens, const int32_t *token_starts, int num_tokens,
+                 int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                 int num_blocks, void *stream);
+
+/* pd_append_kv into an FP8 cache of E4M3 codes: the code of a key (value) x is
+ * x / k_scale (x / v_scale), taken in FP32 from the unrounded rotation and
+ * rounded once to the nearest E4M3 value (ties to even), saturating at +-448.
+ * A NaN becomes a NaN code, which is no valid cache content.
+ *   k_scale, v_scale  finite, positive.
+ * head_dim must be a multiple of 16, as for pd_decode_attn_fp8. */
+int pd_append_kv_fp8(const pd_rope *rope, const void *q, int64_t q_token_stride, const void *k,
+                     int64_t k_token_stride, const void *v, int64_t v_token_stride, void *q_out,
+                     void *k_cache, void *v_cache, float k_scale, float v_scale,
+                     const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens,
+                     const int32_t *token_starts, int num_tokens, int num_seqs, int num_q_heads,
+                     int num_kv_heads, int head_dim, int block_size, int num_blocks, void *stream);
+
 /* ---- tiled decode (tiled_attention.rs page) ------------------------------ */
 
 /* TiledAttentionDims: the state is sized for max_seqs sequences. */
@@ -391,8 +522,8 @@ int pd_device_status(int *flags);
  * call either. */
 
 /* TEST HOOK.  Make the next `count` device allocations of pd_tiled_create
- * (state m, l, o, then the run partials) fail as if the device were out of
- * memory (host-side fault injection). */
+ * (state m, l, o, then the run partials) and pd_rope_create (the table) fail as
+ * if the device were out of memory (host-side fault injection). */
 void pd_debug_fail_next_allocs(int count);
 
 /* TEST HOOK.  Tuning for launch-shape experiments, applied to the following launches

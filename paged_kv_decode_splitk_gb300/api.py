@@ -94,6 +94,112 @@ def run_paged(inp: PagedInputs, num_splits: int | None = None, gqa_pack: bool | 
                        pack, out, ws, stream, getattr(w, "k_scale", 1.0), getattr(w, "v_scale", 1.0))
 
 
+def _rows(name: str, t, shape) -> None:
+    """t is a BF16 [tokens, heads, head_dim] tensor of the given shape (None: any size) on the current
+    device, its rows contiguous."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name}: a BF16 tensor [tokens, heads, head_dim] is wanted, not {t.dtype} {tuple(t.shape)}")
+    for have, want in zip(t.shape, shape):
+        if want is not None and have != want:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: the columns of a row have to be contiguous")
+    _on_device(name, t)
+
+
+def _on_device(name: str, t) -> None:
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}"
+                         if torch.cuda.is_available() else f"{name} is on {t.device}: a CUDA tensor is wanted")
+
+
+def _indices(name: str, t, shape) -> None:
+    """t is a contiguous int32 tensor of the given shape (None: any size) on the current device."""
+    if t.dtype != torch.int32 or t.dim() != len(shape) or not t.is_contiguous() or any(
+            w is not None and h != w for h, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: a contiguous int32 tensor of shape {tuple(shape)} is wanted, not {t.dtype} "
+                         f"{tuple(t.shape)}")
+    _on_device(name, t)
+
+
+def _caches(k_cache, v_cache, num_kv_heads: int, head_dim: int) -> None:
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c.dim() != 4 or c.shape[2] != num_kv_heads or c.shape[3] != head_dim or not c.is_contiguous():
+            raise ValueError(f"{name}: a contiguous tensor [num_blocks, block_size, {num_kv_heads}, {head_dim}] is "
+                             f"wanted, not {tuple(c.shape)}")
+        if c.dtype not in (torch.bfloat16, torch.uint8):
+            raise ValueError(f"{name}: BF16, or uint8 for E4M3 codes, not {c.dtype}")
+        _on_device(name, c)
+    if k_cache.dtype != v_cache.dtype or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache have one type and one shape")
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors allocated here for a launch on another stream than the current one are not reused before it is done."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+
+
+def rope(rotation: pd.Rope, x, positions, out=None, inverse: bool = False, stream=None):
+    """Rotary positions: x [T, H, D] BF16 (strided in tokens and heads, e.g. the q and k heads of a fused
+    projection) rotated by positions [T] int32; returns out [T, H, D] (contiguous unless given; x itself
+    rotates in place).  inverse turns back: the map that takes gradients of out to gradients of x."""
+    _rows("x", x, (None, None, rotation.head_dim))
+    _indices("positions", positions, (x.shape[0],))
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        _used_on(stream, out)
+    else:
+        _rows("out", out, x.shape)
+    pd.pd_rope_apply(rotation, x, positions, out, inverse, stream)
+    return out
+
+
+def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, token_starts=None, q_out=None,
+              k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """Append new tokens to the paged cache: k [T, Hkv, D] rotated (rotation: a pd.Rope, or None for none) and
+    v as they are, at the last positions of context_lens [S] (lengths after the append); q [T, Hq, D] (or
+    None) rotated on the way and returned as q_out [T, Hq, D].  token_starts [S + 1] says which rows each
+    sequence has; None: one each.  uint8 caches hold E4M3 codes of x / k_scale and x / v_scale.  Rows of no
+    sequence are left as they were, in q_out too."""
+    if k.dim() != 3:
+        raise ValueError(f"k: a BF16 tensor [tokens, kv heads, head_dim] is wanted, not {tuple(k.shape)}")
+    T, Hkv, D = k.shape
+    S = context_lens.shape[0]
+    _rows("k", k, k.shape)
+    _rows("v", v, k.shape)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is not None and t.dim() == 3 and t.shape[1] > 1 and t.stride(1) != D:
+            raise ValueError(f"{name}: the heads of a token have to lie side by side")
+    _caches(k_cache, v_cache, Hkv, D)
+    _indices("context_lens", context_lens, (None,))
+    _indices("block_table", block_table, (S, None))
+    if token_starts is not None:
+        _indices("token_starts", token_starts, (S + 1,))
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        _rows("q", q, (T, None, D))
+        if q_out is None:
+            q_out = torch.empty((T, q.shape[1], D), dtype=torch.bfloat16, device=q.device)
+            _used_on(stream, q_out)
+        else:
+            _rows("q_out", q_out, q.shape)
+            if not q_out.is_contiguous():
+                raise ValueError("q_out has to be contiguous")
+    if k_cache.dtype == torch.uint8:
+        pd.pd_append_kv_fp8(rotation, q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
+                            token_starts, stream)
+    else:
+        pd.pd_append_kv(rotation, q, k, v, q_out, k_cache, v_cache, block_table, context_lens, token_starts, stream)
+    return q_out
+
+
 class TiledInputs:
     """Device copies of a workloads.TiledWorkload."""
 

@@ -71,7 +71,7 @@ std::string trim_lower(const char *text) {
 
 bool is_off_word(const std::string &w) { return w == "0" || w == "off" || w == "false" || w == "no"; }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using pd::aligned16;
 
 // ---- device status word ------------------------------------------------------------
 __device__ unsigned int g_status;
@@ -332,8 +332,31 @@ int check_shape(int num_q_heads, int num_kv_heads, int head_dim, int block_size)
 
 }  // namespace
 
+namespace {
+std::atomic<int> g_fail_allocs{0};
+}
+
 namespace pd {
 int report_error(int code, const char *message) { return fail(code, "%s", message); }
+int report(int code, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return code;
+}
+int report_ok() { return ok(); }
+int report_cuda(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+int check_shape(int num_q_heads, int num_kv_heads, int head_dim, int block_size) {
+    return ::check_shape(num_q_heads, num_kv_heads, head_dim, block_size);
+}
+unsigned int *device_status_word(int *err) { return status_ptr(err); }
+bool inject_alloc_failure() {
+    int inject = g_fail_allocs.load();
+    while (inject > 0 && !g_fail_allocs.compare_exchange_weak(inject, inject - 1)) {
+    }
+    return inject > 0;
+}
 }  // namespace pd
 
 struct pd_tiled {
@@ -353,10 +376,6 @@ size_t run_partials_floats(const pd_tiled_dims &d) {
            (static_cast<size_t>(d.head_dim) + 2);
 }
 }  // namespace
-
-namespace {
-std::atomic<int> g_fail_allocs{0};
-}
 
 extern "C" {
 
@@ -731,10 +750,7 @@ int pd_tiled_create(const pd_tiled_dims *dims, pd_tiled **out) {
     size_t sizes[4] = {mb, lb, ob, run_partials_floats(*dims) * sizeof(float)};
     for (int i = 0; i < 4; ++i) {
         void *p = nullptr;
-        int inject = g_fail_allocs.load();
-        while (inject > 0 && !g_fail_allocs.compare_exchange_weak(inject, inject - 1)) {
-        }
-        if (inject > 0) {
+        if (pd::inject_alloc_failure()) {
             e = cudaErrorMemoryAllocation;
         } else {
             e = cudaMalloc(&p, sizes[i] > 0 ? sizes[i] : 16);

@@ -161,6 +161,18 @@ struct MergeParams {
 // Record an error message for pd_last_error() and return `code`.
 int report_error(int code, const char *message);
 
+// What every entry point shares (pd_api.cu): a formatted report, the cleared
+// message of a call that succeeds, a CUDA error (which it takes off the
+// runtime's record), the shape limits, the device's status word (null: *err
+// says why) and whether the test hook asks the next allocation to fail.
+int report(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+int report_ok();
+int report_cuda(cudaError_t e, const char *what);
+int check_shape(int num_q_heads, int num_kv_heads, int head_dim, int block_size);
+unsigned int *device_status_word(int *err);
+bool inject_alloc_failure();
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // Dynamic shared memory a unit CTA needs (kv8: FP8 cache).
 int unit_smem_bytes(int dpad, int rows, int stages, bool kv8);
 

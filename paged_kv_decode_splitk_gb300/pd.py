@@ -43,6 +43,18 @@ PD_DEV_BAD_CONTEXT_LEN = 2
 PD_DEV_BAD_TILE_COUNT = 4
 PD_DEV_WAIT_TIMEOUT = 8
 
+PD_ROPE_HALF = 0
+PD_ROPE_INTERLEAVED = 1
+PD_ROPE_NONE = 0
+PD_ROPE_LINEAR = 1
+PD_ROPE_NTK = 2
+PD_ROPE_BANDED = 3
+PD_ROPE_YARN = 4
+PD_ROPE_TABLE = 5
+
+ROPE_LAYOUTS = {"half": PD_ROPE_HALF, "interleaved": PD_ROPE_INTERLEAVED}
+ROPE_SCALINGS = {"none": PD_ROPE_NONE, "linear": PD_ROPE_LINEAR, "ntk": PD_ROPE_NTK, "banded": PD_ROPE_BANDED,
+                 "yarn": PD_ROPE_YARN, "table": PD_ROPE_TABLE}
 POLICY_NAMES = {"legacy": PD_POLICY_LEGACY, "auto": PD_POLICY_AUTO, "pinned": PD_POLICY_PINNED}
 
 
@@ -67,6 +79,14 @@ class pd_tiled_source(ctypes.Structure):
                 ("tile_blocks", ctypes.c_void_p), ("tile_block_counts", ctypes.c_void_p),
                 ("blk_stride", ctypes.c_int64), ("tok_stride", ctypes.c_int64),
                 ("kvh_stride", ctypes.c_int64), ("last_block_valid_slots", ctypes.c_int)]
+
+
+class pd_rope_desc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("scaling", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_context", ctypes.c_double), ("low_turns", ctypes.c_double),
+                ("high_turns", ctypes.c_double), ("attention_factor", ctypes.c_double),
+                ("frequencies", ctypes.POINTER(ctypes.c_double))]
 
 
 _lock = threading.Lock()
@@ -98,6 +118,14 @@ _SIGS = {
                                 _I, _I, _I, _I, ctypes.c_float, _I, _VP, _SZ, _I, _VP]),
     "pd_decode_attn_noalloc": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _I,
                                     ctypes.c_float, _I, _I, _VP]),
+    "pd_rope_frequencies": (_I, [_VP, _VP, _VP]),
+    "pd_rope_create": (_I, [_VP, _VP]),
+    "pd_rope_destroy": (None, [_VP]),
+    "pd_rope_apply": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I64, _I, _I, _I, _VP]),
+    "pd_append_kv": (_I, [_VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I,
+                          _I, _I, _I, _VP]),
+    "pd_append_kv_fp8": (_I, [_VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _VP, ctypes.c_float, ctypes.c_float,
+                              _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _VP]),
     "pd_tiled_validate": (_I, [_VP]),
     "pd_tiled_state_bytes": (_I, [_VP, _VP, _VP, _VP, _VP]),
     "pd_tiled_create": (_I, [_VP, _VP]),
@@ -294,6 +322,121 @@ def pd_decode_attn_noalloc(q, k_cache, v_cache, block_table, context_lens, out, 
                                       float(inv_sqrt_d), int(num_splits), int(gqa_pack),
                                       _stream(stream))
     return _check(rc)
+
+
+# ---- rotary positions and the append to the paged cache ------------------------------
+
+def rope_desc(head_dim: int, rot_dim: int | None = None, *, layout="half", base: float = 10000.0, scaling="none",
+              factor: float = 1.0, original_context: float = 0.0, low_turns: float = 0.0, high_turns: float = 0.0,
+              attention_factor: float = 0.0, frequencies=None) -> pd_rope_desc:
+    """A pd_rope_desc (see pd.h).  layout and scaling by name or value; frequencies (a sequence of
+    rot_dim/2 floats) choose the table rule."""
+    rot = head_dim if rot_dim is None else rot_dim
+    if frequencies is not None:
+        scaling = PD_ROPE_TABLE
+        freq = [float(f) for f in frequencies]
+        if len(freq) != rot // 2:
+            raise ValueError(f"rope: {len(freq)} frequencies for rot_dim {rot}: rot_dim/2 are wanted")
+        table = (ctypes.c_double * max(1, len(freq)))(*freq)
+    else:
+        table = None
+    for name, value, names in (("layout", layout, ROPE_LAYOUTS), ("scaling", scaling, ROPE_SCALINGS)):
+        if isinstance(value, str) and value not in names:
+            raise ValueError(f"rope: unknown {name} {value!r}: one of {', '.join(names)}")
+    return pd_rope_desc(head_dim, rot, ROPE_LAYOUTS.get(layout, layout), ROPE_SCALINGS.get(scaling, scaling), base, factor,
+                        original_context, low_turns, high_turns, attention_factor,
+                        ctypes.cast(table, ctypes.POINTER(ctypes.c_double)) if table is not None else None)
+
+
+def pd_rope_frequencies(desc: pd_rope_desc) -> tuple[list[float], float]:
+    """The angles per position (rot_dim/2) and the factor on cosine and sine of a description."""
+    f = (ctypes.c_double * max(1, desc.rot_dim // 2))()
+    c = ctypes.c_double()
+    _check(lib().pd_rope_frequencies(ctypes.byref(desc), f, ctypes.byref(c)))
+    return list(f)[: desc.rot_dim // 2], c.value
+
+
+def pd_rope_create(desc: pd_rope_desc) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().pd_rope_create(ctypes.byref(desc), ctypes.byref(h)))
+    return h.value
+
+
+def pd_rope_destroy(handle: int) -> None:
+    lib().pd_rope_destroy(handle)
+
+
+class Rope:
+    """Owner of a pd_rope handle: one model's rotary positions on the current device."""
+
+    def __init__(self, head_dim, rot_dim=None, **options):
+        self.handle = None
+        self.desc = rope_desc(head_dim, rot_dim, **options)
+        self.head_dim, self.rot_dim = self.desc.head_dim, self.desc.rot_dim
+        self.handle = pd_rope_create(self.desc)
+
+    def frequencies(self):
+        return pd_rope_frequencies(self.desc)
+
+    def close(self):
+        if self.handle:
+            pd_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _handle(rope):
+    if rope is None:
+        return None
+    h = rope.handle if isinstance(rope, Rope) else rope
+    if not h:
+        raise ValueError("the rotation's handle is closed")
+    return h
+
+
+def _token_stride(t) -> int:
+    """Elements from one token's rows to the next of [T, H, D] (any value serves a single token)."""
+    n, h, d = t.shape
+    return t.stride(0) if n > 1 else h * d
+
+
+def pd_rope_apply(rope, x, positions, out, inverse: bool = False, stream=None) -> int:
+    """out [T, H, D] <- x [T, H, D] rotated by positions [T] (see pd.h); strided in tokens and heads."""
+    T, H, D = x.shape
+    return _check(lib().pd_rope_apply(_handle(rope), x.data_ptr(), _token_stride(x), x.stride(1) if H > 1 else D,
+                                      positions.data_ptr(), out.data_ptr(), _token_stride(out),
+                                      out.stride(1) if H > 1 else D, T, H, int(inverse), _stream(stream)))
+
+
+def pd_append_kv(rope, q, k, v, q_out, k_cache, v_cache, block_table, context_lens, token_starts=None, stream=None,
+                 num_blocks: int | None = None) -> int:
+    """New tokens' keys (rotated) and values into a BF16 cache, q rotated into q_out (see pd.h).  q, k, v
+    [T, H, D] strided in tokens; rope a Rope or None; q and q_out None for keys and values alone."""
+    T, Hkv, D = k.shape
+    nb, bs = k_cache.shape[0], k_cache.shape[1]
+    return _check(lib().pd_append_kv(
+        _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
+        _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        block_table.shape[1], context_lens.data_ptr(), _ptr(token_starts), T, context_lens.shape[0],
+        0 if q is None else q.shape[1], Hkv, D, bs, nb if num_blocks is None else num_blocks, _stream(stream)))
+
+
+def pd_append_kv_fp8(rope, q, k, v, q_out, k_cache, v_cache, k_scale: float, v_scale: float, block_table, context_lens,
+                     token_starts=None, stream=None, num_blocks: int | None = None) -> int:
+    """pd_append_kv into an FP8 cache (uint8 E4M3 codes of x / k_scale and x / v_scale)."""
+    T, Hkv, D = k.shape
+    nb, bs = k_cache.shape[0], k_cache.shape[1]
+    return _check(lib().pd_append_kv_fp8(
+        _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
+        _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), float(k_scale), float(v_scale),
+        block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), _ptr(token_starts), T,
+        context_lens.shape[0], 0 if q is None else q.shape[1], Hkv, D, bs, nb if num_blocks is None else num_blocks,
+        _stream(stream)))
 
 
 # ---- tiled ---------------------------------------------------------------------------

@@ -86,6 +86,7 @@ extern "C" {
 #define PD_DEV_BAD_CONTEXT_LEN 2 /* a context length < 0 or > max_blocks_per_seq*block_size: clamped */
 #define PD_DEV_BAD_TILE_COUNT 4  /* a tile_block_counts entry < 0 or > tile_capacity: clamped */
 #define PD_DEV_WAIT_TIMEOUT 8    /* a bounded wait on a copy ran out: that output is garbage */
+#define PD_DEV_BAD_GROUPS 16     /* group_starts not non-decreasing within the batch: no prefix was read */
 
 /* Split-count policies (Module attn_splitk page, enum SplitkPolicy). */
 typedef enum { PD_POLICY_LEGACY = 0, PD_POLICY_AUTO = 1, PD_POLICY_PINNED = 2 } pd_policy;
@@ -268,6 +269,47 @@ int pd_decode_attn_noalloc(const void *q, const void *k_cache, const void *v_cac
                            int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                            int num_blocks, float inv_sqrt_d, int num_splits, int gqa_pack,
                            void *stream);
+
+/* ---- decode behind shared prefixes ------------------------------------------
+ * pd_decode_attn_prefix: one decode step of a batch whose sequences come in
+ * groups that share a prefix.  A sequence of group g attends to the group's
+ * prefix_lens[g] prefix tokens and then to its own context_lens[s] tokens,
+ *     out[s,h,:] = softmax(q[s,h,:] . [K_prefix; K_own]^T * inv_sqrt_d) . [V_prefix; V_own],
+ * what pd_decode_attn computes where every sequence's table begins with the
+ * prefix's blocks; here a prefix is read and multiplied once for the whole group.
+ *   prefix_table  [num_groups, max_prefix_blocks] int32: the prefix's blocks.
+ *   prefix_lens   [num_groups] int32 (0 allowed).
+ *   group_starts  [num_groups + 1] int32, non-decreasing within 0..num_seqs:
+ *                 group g has sequences group_starts[g] to group_starts[g+1] - 1;
+ *                 sequences of no group have their own tokens only.  NULL: one
+ *                 group of the whole batch (num_groups == 1).  Values that
+ *                 are not so raise PD_DEV_BAD_GROUPS and no prefix is read.
+ *   block_table, context_lens  of the sequences' own tokens (0 allowed; a
+ *                 sequence with neither prefix nor own tokens gets 0).
+ *   num_splits    of the own tokens, 1..PD_MAX_DECODE_SPLITS.
+ *   workspace     >= pd_prefix_workspace_bytes(...) bytes, 16-B aligned, always
+ *                 needed; contents ignored on entry, scratch on return.
+ * The other arguments are pd_decode_attn's, its errors too: a prefix length
+ * outside its table is clamped (PD_DEV_BAD_CONTEXT_LEN), a block id outside the
+ * cache reads zeros (PD_DEV_BAD_BLOCK_ID).  Cache slots past a length may hold
+ * anything.  The weights of prefix tokens are rounded to BF16 (f16 over an FP8
+ * cache) before they meet V.  The same call on the same data gives the same
+ * bits; unlike pd_decode_attn's, they depend on the batch (how a prefix is cut
+ * depends on every group).
+ * Returns PD_OK, PD_ERR_INVALID, PD_ERR_WORKSPACE, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
+#define PD_MAX_PREFIX_GROUPS 256
+
+size_t pd_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                                 int head_dim, int num_splits);
+
+int pd_decode_attn_prefix(const void *q, const void *k_cache, const void *v_cache,
+                          const int32_t *prefix_table, int max_prefix_blocks,
+                          const int32_t *prefix_lens, const int32_t *group_starts, int num_groups,
+                          const int32_t *block_table, int max_blocks_per_seq,
+                          const int32_t *context_lens, void *out, int num_seqs, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                          float inv_sqrt_d, int num_splits, void *workspace,
+                          size_t workspace_bytes, void *stream);
 
 /* ---- rotary positions ------------------------------------------------------
  * The rotation of a query or key row x of head_dim columns at position t: its

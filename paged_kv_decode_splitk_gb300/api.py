@@ -94,44 +94,57 @@ def run_paged(inp: PagedInputs, num_splits: int | None = None, gqa_pack: bool | 
                        pack, out, ws, stream, getattr(w, "k_scale", 1.0), getattr(w, "v_scale", 1.0))
 
 
-def _rows(name: str, t, shape) -> None:
-    """t is a BF16 [tokens, heads, head_dim] tensor of the given shape (None: any size) on the current
-    device, its rows contiguous."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{name}: a BF16 tensor [tokens, heads, head_dim] is wanted, not {t.dtype} {tuple(t.shape)}")
-    for have, want in zip(t.shape, shape):
-        if want is not None and have != want:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
-    if t.stride(2) != 1:
-        raise ValueError(f"{name}: the columns of a row have to be contiguous")
-    _on_device(name, t)
+# Argument checks.  Each is one cheap test of what a call needs; only where it fails is the argument looked
+# at again for the message, since at a decode step the checks cost as much as the launch.
+_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
 
 
-def _on_device(name: str, t) -> None:
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}"
-                         if torch.cuda.is_available() else f"{name} is on {t.device}: a CUDA tensor is wanted")
+def _refuse(name: str, t, kind: str, shape, device: int):
+    want = f"{name}: {kind} [{', '.join('any' if n is None else str(n) for n in shape)}] on the current device"
+    if t.get_device() != device:
+        raise ValueError(f"{want} (cuda:{device}) is wanted, it is on {t.device}")
+    raise ValueError(f"{want} is wanted, not {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _indices(name: str, t, shape) -> None:
-    """t is a contiguous int32 tensor of the given shape (None: any size) on the current device."""
-    if t.dtype != torch.int32 or t.dim() != len(shape) or not t.is_contiguous() or any(
-            w is not None and h != w for h, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: a contiguous int32 tensor of shape {tuple(shape)} is wanted, not {t.dtype} "
-                         f"{tuple(t.shape)}")
-    _on_device(name, t)
+def _current_device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else 0
 
 
-def _caches(k_cache, v_cache, num_kv_heads: int, head_dim: int) -> None:
+def _rows(name: str, t, tokens, heads, head_dim: int, device: int, side_by_side: bool) -> None:
+    """t is BF16 [tokens, heads, head_dim] (None: any) on the device, its rows contiguous; side_by_side: the
+    heads of a token too."""
+    if t.dtype is _BF16 and t.dim() == 3 and t.get_device() == device:
+        n, h, d = t.shape
+        st = t.stride()
+        if (d == head_dim and st[2] == 1 and (tokens is None or n == tokens) and (heads is None or h == heads)
+                and (not side_by_side or st[1] == d or h == 1)):
+            return
+    _refuse(name, t, "BF16 with contiguous rows" + (" and a token's heads side by side" if side_by_side else ""),
+            (tokens, heads, head_dim), device)
+
+
+def _indices(name: str, t, shape, device: int) -> None:
+    """t is contiguous int32 of the shape (None: any size) on the device."""
+    if t.dtype is _I32 and t.dim() == len(shape) and t.is_contiguous() and t.get_device() == device:
+        if all([w is None or h == w for h, w in zip(t.shape, shape)]):
+            return
+    _refuse(name, t, "contiguous int32", shape, device)
+
+
+def _caches(k_cache, v_cache, num_kv_heads: int, head_dim: int, device: int) -> None:
+    kind = k_cache.dtype
+    if k_cache.dim() == 4 and (kind is _BF16 or kind is _U8):
+        shape = k_cache.shape
+        if (shape[2] == num_kv_heads and shape[3] == head_dim and v_cache.shape == shape and v_cache.dtype is kind
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and k_cache.get_device() == device
+                and v_cache.get_device() == device):
+            return
     for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dim() != 4 or c.shape[2] != num_kv_heads or c.shape[3] != head_dim or not c.is_contiguous():
-            raise ValueError(f"{name}: a contiguous tensor [num_blocks, block_size, {num_kv_heads}, {head_dim}] is "
-                             f"wanted, not {tuple(c.shape)}")
-        if c.dtype not in (torch.bfloat16, torch.uint8):
-            raise ValueError(f"{name}: BF16, or uint8 for E4M3 codes, not {c.dtype}")
-        _on_device(name, c)
-    if k_cache.dtype != v_cache.dtype or k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache have one type and one shape")
+        if (c.dtype not in (_BF16, _U8) or c.dim() != 4 or c.shape[2:] != (num_kv_heads, head_dim)
+                or not c.is_contiguous() or c.get_device() != device):
+            _refuse(name, c, "contiguous BF16, or uint8 for E4M3 codes,", (None, None, num_kv_heads, head_dim), device)
+    raise ValueError(f"k_cache and v_cache have one type and one shape, not {kind} {tuple(k_cache.shape)} and "
+                     f"{v_cache.dtype} {tuple(v_cache.shape)}")
 
 
 def _used_on(stream, *tensors) -> None:
@@ -148,13 +161,15 @@ def rope(rotation: pd.Rope, x, positions, out=None, inverse: bool = False, strea
     """Rotary positions: x [T, H, D] BF16 (strided in tokens and heads, e.g. the q and k heads of a fused
     projection) rotated by positions [T] int32; returns out [T, H, D] (contiguous unless given; x itself
     rotates in place).  inverse turns back: the map that takes gradients of out to gradients of x."""
-    _rows("x", x, (None, None, rotation.head_dim))
-    _indices("positions", positions, (x.shape[0],))
+    dev = _current_device()
+    _rows("x", x, None, None, rotation.head_dim, dev, False)
+    T, H, D = x.shape
+    _indices("positions", positions, (T,), dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty((T, H, D), dtype=_BF16, device=x.device)
         _used_on(stream, out)
     else:
-        _rows("out", out, x.shape)
+        _rows("out", out, T, H, D, dev, False)
     pd.pd_rope_apply(rotation, x, positions, out, inverse, stream)
     return out
 
@@ -166,38 +181,82 @@ def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, to
     None) rotated on the way and returned as q_out [T, Hq, D].  token_starts [S + 1] says which rows each
     sequence has; None: one each.  uint8 caches hold E4M3 codes of x / k_scale and x / v_scale.  Rows of no
     sequence are left as they were, in q_out too."""
+    dev = _current_device()
     if k.dim() != 3:
-        raise ValueError(f"k: a BF16 tensor [tokens, kv heads, head_dim] is wanted, not {tuple(k.shape)}")
+        _refuse("k", k, "BF16", (None, None, None), dev)
     T, Hkv, D = k.shape
+    _rows("k", k, T, Hkv, D, dev, True)
+    _rows("v", v, T, Hkv, D, dev, True)
+    _caches(k_cache, v_cache, Hkv, D, dev)
+    _indices("context_lens", context_lens, (None,), dev)
     S = context_lens.shape[0]
-    _rows("k", k, k.shape)
-    _rows("v", v, k.shape)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is not None and t.dim() == 3 and t.shape[1] > 1 and t.stride(1) != D:
-            raise ValueError(f"{name}: the heads of a token have to lie side by side")
-    _caches(k_cache, v_cache, Hkv, D)
-    _indices("context_lens", context_lens, (None,))
-    _indices("block_table", block_table, (S, None))
+    _indices("block_table", block_table, (S, None), dev)
     if token_starts is not None:
-        _indices("token_starts", token_starts, (S + 1,))
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-    else:
-        _rows("q", q, (T, None, D))
+        _indices("token_starts", token_starts, (S + 1,), dev)
+    if q is not None:
+        _rows("q", q, T, None, D, dev, True)
+        Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, q.shape[1], D), dtype=torch.bfloat16, device=q.device)
+            q_out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
             _used_on(stream, q_out)
         else:
-            _rows("q_out", q_out, q.shape)
+            _rows("q_out", q_out, T, Hq, D, dev, True)
             if not q_out.is_contiguous():
                 raise ValueError("q_out has to be contiguous")
-    if k_cache.dtype == torch.uint8:
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_cache.dtype is _U8:
         pd.pd_append_kv_fp8(rotation, q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
                             token_starts, stream)
     else:
         pd.pd_append_kv(rotation, q, k, v, q_out, k_cache, v_cache, block_table, context_lens, token_starts, stream)
     return q_out
+
+
+def prefix_workspace(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int, head_dim: int, num_splits: int,
+                     device) -> torch.Tensor:
+    n = pd.pd_prefix_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, num_splits)
+    return torch.empty(n, dtype=_U8, device=device)
+
+
+def decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens,
+                       inv_sqrt_d: float, num_splits: int, out=None, ws=None, stream=None, k_scale: float = 1.0,
+                       v_scale: float = 1.0):
+    """Decode attention behind shared prefixes: sequences group_starts[g] to group_starts[g + 1] - 1 (None: the whole
+    batch, one group) attend to the prefix_lens[g] tokens prefix_table[g] names, then to their own context_lens
+    tokens; a prefix is read once for its group.  Returns out [S, Hq, D] BF16.  uint8 caches are FP8 E4M3 codes
+    with per-tensor scales."""
+    dev = _current_device()
+    if q.dim() != 3 or not q.is_contiguous():
+        _refuse("q", q, "contiguous BF16", (None, None, None), dev)
+    S, Hq, D = q.shape
+    _rows("q", q, S, Hq, D, dev, True)
+    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    _caches(k_cache, v_cache, Hkv, D, dev)
+    _indices("prefix_lens", prefix_lens, (None,), dev)
+    G = prefix_lens.shape[0]
+    _indices("prefix_table", prefix_table, (G, None), dev)
+    if group_starts is not None:
+        _indices("group_starts", group_starts, (G + 1,), dev)
+    _indices("context_lens", context_lens, (S,), dev)
+    _indices("block_table", block_table, (S, None), dev)
+    if out is None:
+        out = torch.empty((S, Hq, D), dtype=_BF16, device=q.device)
+        _used_on(stream, out)
+    else:
+        _rows("out", out, S, Hq, D, dev, True)
+        if not out.is_contiguous():
+            raise ValueError("out has to be contiguous")
+    if ws is None:
+        ws = prefix_workspace(S, G, Hq, max(1, Hkv), D, num_splits, q.device)
+        _used_on(stream, ws)
+    if k_cache.dtype is _U8:
+        pd.pd_decode_attn_prefix_fp8(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_lens, group_starts,
+                                     block_table, context_lens, out, inv_sqrt_d, num_splits, ws, stream)
+    else:
+        pd.pd_decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens,
+                                 out, inv_sqrt_d, num_splits, ws, stream)
+    return out
 
 
 class TiledInputs:

@@ -537,12 +537,16 @@ int pd_split_chunk_tokens(int context_len, int num_splits, int block_size) {
 namespace {
 // pd_decode_attn over a BF16 cache (kv8 false) or an FP8 E4M3 cache with
 // per-tensor scales (kv8 true); one body so that both take the same checks,
-// split geometry, launch choices and merge.
+// split geometry, launch choices and merge.  own_o, own_ml, view: the own-token
+// pass of pd_decode_attn_prefix, which keeps every split's partial there and has
+// no merge of its own (pd::launch_own_partials).
 int decode_impl(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
                 int max_blocks_per_seq, const int32_t *context_lens, void *out, int num_seqs,
                 int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
                 float inv_sqrt_d, int num_splits, void *workspace, size_t workspace_bytes, int gqa_pack,
-                void *stream, bool kv8, float k_scale, float v_scale) {
+                void *stream, bool kv8, float k_scale, float v_scale, float *own_o = nullptr, float *own_ml = nullptr,
+                pd::KvView *view = nullptr) {
+    const bool own = view != nullptr;
     if (gqa_pack < PD_GQA_PACK_OFF || gqa_pack > PD_GQA_PACK_SPLITK)
         return fail(PD_ERR_INVALID, "gqa_pack must be 0, 1 or 2");
     if (gqa_pack) {
@@ -577,7 +581,7 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
                     max_blocks_per_seq, num_blocks);
     if (static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
         return fail(PD_ERR_INVALID, "max_blocks_per_seq * block_size overflows int32");
-    if (num_splits > 1) {
+    if (num_splits > 1 && !own) {
         const size_t need = pd_workspace_bytes(num_seqs, num_q_heads, head_dim, num_splits);
         if (!workspace || workspace_bytes < need)
             return fail(PD_ERR_WORKSPACE, "split-K workspace of %zu bytes needed, %zu given%s", need,
@@ -629,8 +633,8 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
     p.min_kv_per_split = PD_MIN_KV_PER_SPLIT;
     p.out = static_cast<__nv_bfloat16 *>(out);
     float *ws = static_cast<float *>(workspace);
-    p.ws_o = num_splits > 1 ? ws : nullptr;
-    p.ws_ml = num_splits > 1 ? ws + static_cast<size_t>(num_seqs) * num_q_heads * num_splits * head_dim
+    p.ws_o = own ? own_o : num_splits > 1 ? ws : nullptr;
+    p.ws_ml = own ? own_ml : num_splits > 1 ? ws + static_cast<size_t>(num_seqs) * num_q_heads * num_splits * head_dim
                              : nullptr;
     p.num_seqs = num_seqs;
     p.num_q_heads = num_q_heads;
@@ -662,6 +666,15 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
     int stages_seq = default_stages_seq(dpad, kv8);
     if (pd::unit_smem_bytes(dpad, rows, stages_seq, kv8) > max_smem_optin()) stages_seq = stages;
     const bool hl = !packed && G <= 4;
+    if (own) {
+        view->k = tk;
+        view->v = tv;
+        view->tok_dim = tok_dim;
+        const cudaError_t e = kv8 ? dispatch_unit<pd::kModeOwn, true>(dpad, gn, hl, false, &tk, &tv, p, units, stages_seq, st)
+                                  : dispatch_unit<pd::kModeOwn, false>(dpad, gn, hl, false, &tk, &tv, p, units, stages_seq, st);
+        if (e != cudaSuccess) return cuda_fail(e, "own-token pass launch");
+        return ok();
+    }
     cudaError_t e = kv8 ? dispatch_unit<pd::kModePaged, true>(dpad, gn, hl, packed, &tk, &tv, p, units, stages_seq, st)
                         : dispatch_unit<pd::kModePaged, false>(dpad, gn, hl, packed, &tk, &tv, p, units, stages_seq, st);
     if (e != cudaSuccess) return cuda_fail(e, "unit kernel launch");
@@ -687,6 +700,20 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
     return ok();
 }
 }  // namespace
+
+}  // extern "C"
+
+int pd::launch_own_partials(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                            int max_blocks_per_seq, const int32_t *context_lens, void *out, int num_seqs,
+                            int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                            float inv_sqrt_d, int num_splits, float *own_o, float *own_ml, void *stream, bool kv8,
+                            float k_scale, float v_scale, KvView *view) {
+    return decode_impl(q, k_cache, v_cache, block_table, max_blocks_per_seq, context_lens, out, num_seqs,
+                       num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, inv_sqrt_d, num_splits, nullptr, 0,
+                       PD_GQA_PACK_OFF, stream, kv8, k_scale, v_scale, own_o, own_ml, view);
+}
+
+extern "C" {
 
 int pd_decode_attn(const void *q, const void *k_cache, const void *v_cache,
                    const int32_t *block_table, int max_blocks_per_seq,

@@ -90,6 +90,7 @@ enum UnitMode : int {
     kModePaged = 0,     // pd_decode_attn: block_table gather, split ranges, out / workspace
     kModeTiled = 1,     // pd_tiled_step: tile list, fold into the running state
     kModeTiledRun = 2,  // pd_tiled_run: every call's tile list at once, one partial per call
+    kModeOwn = 3,       // pd_decode_attn_prefix: the sequences' own tokens, always as partials
 };
 
 // Sources (step_tile calls) one fused pd_tiled_run launch serves at most.
@@ -157,6 +158,23 @@ struct MergeParams {
     int max_tokens;  // max_blocks_per_seq * block_size (context lengths are clamped to it)
     FastDiv fd_hq, fd_split, fd_bs;  // num_q_heads, num_splits, block_size
 };
+
+// The tensor maps of a paged cache's K and V (tok_dim: the map dimension of the
+// token coordinate).
+struct KvView {
+    CUtensorMap k, v;
+    int tok_dim;
+};
+
+// The own-token pass of pd_decode_attn_prefix (pd_api.cu): pd_decode_attn's
+// checks and its partial pass over every split, each non-empty split's (o, m, l)
+// written to own_o [rows, N, D] and own_ml [rows, N, 2]; no merge, `out` only
+// checked.  *view receives the maps it read through.
+int launch_own_partials(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                        int max_blocks_per_seq, const int32_t *context_lens, void *out, int num_seqs,
+                        int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                        float inv_sqrt_d, int num_splits, float *own_o, float *own_ml, void *stream, bool kv8,
+                        float k_scale, float v_scale, KvView *view);
 
 // Record an error message for pd_last_error() and return `code`.
 int report_error(int code, const char *message);

@@ -1,0 +1,609 @@
+// pd_prefix.cuh -- the shared-prefix pass of pd_decode_attn_prefix: attention
+// partials of every sequence of a group over the group's one prefix.
+//
+// What it computes.  A group's query rows of one KV head (its sequences times
+// the query heads that share the head) all meet the same P keys and values, so
+// their scores are one matrix product, S = Q K^T, and their outputs another,
+// O = exp2(S - m) V.  Per segment (a row block of up to 256 rows, a KV head, a
+// run of key tiles) the pass writes each row's partial in base 2,
+//   m  a reference (the largest score so far, or up to 8 below it),
+//   l = sum_t 2^(x_t - m),  o = sum_t 2^(x_t - m) V[t],   x_t = q.K[t] scale log2(e),
+// which the merge folds with the other segments' and with the partials of the
+// sequence's own tokens.
+//
+// GB300 mapping.
+//   * Work is counted in units (row block, KV head, tile of kTile tokens) in one
+//     line over all groups; CTA c of C takes units [W c / C, W (c + 1) / C): every
+//     SM gets the same number of tiles whatever the shapes, and a CTA's partial
+//     of item i goes to slot i + c (item and CTA both only grow along the line,
+//     so slots are distinct, and at most items + C).
+//   * One warp loads: K and V tiles by TMA boxes of 16 tokens x 64 columns,
+//     gathered through the group's block table into a ring of tiles (128-byte
+//     swizzle).  One warp issues tcgen05.mma: S (128 rows x kTile tokens) from
+//     shared memory into TMEM, O += P V with P read from TMEM.  Two groups of
+//     four warps do the softmax, a thread per row, S read from and P (BF16)
+//     written back to TMEM over it; a row's O is rescaled in TMEM only when its
+//     maximum passes its reference by more than 8.
+//   * Two streams keep the tensor core and the softmax both busy: with more than
+//     128 rows each stream has 128 of them and both use every tile; with fewer,
+//     the streams take the tiles in turn (each its own O), and the merge folds
+//     the two halves.  At head dims above 128 one O fills TMEM: one stream, its
+//     S double-buffered.
+//   * P is rounded to BF16 (half a step: 2^-9 to 2^-8 of each weight), the form
+//     the tensor core multiplies with a BF16 V; l sums the unrounded weights in
+//     FP32, S, O, m and l are FP32.  An FP8 cache is converted to f16 tiles
+//     (exactly), and P is f16 there (2^-12 to 2^-11).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "pd.h"
+#include "pd_device.cuh"
+#include "pd_prefix.h"
+#include "pd_tcgen05.cuh"
+
+namespace pd {
+namespace prefix {
+
+constexpr int kRowTile = 128;   // rows of one MMA
+constexpr int kRegionBars = 32;
+
+// Shared-memory plan (bytes from the 1024-aligned base).
+template <int DPAD, bool KV8>
+struct Plan {
+    static constexpr bool kOne = DPAD > 128;  // one stream, S double-buffered
+    static constexpr int kTile = tile_tokens(DPAD);
+    static constexpr int kBlock = block_rows(DPAD);
+    static constexpr int kStageBytes = kTile * DPAD * 2;
+    static constexpr int kStages = KV8 ? 3 : (DPAD == 64 ? 6 : 4);
+    static constexpr int kRawBytes = KV8 ? kTile * DPAD : 0;
+    static constexpr int kRawStages = KV8 ? 3 : 0;
+    static constexpr int kQBytes = (kOne ? 1 : 2) * kRowTile * DPAD * 2;
+    static constexpr int q = 0;
+    static constexpr int ring = q + kQBytes;
+    static constexpr int raw = ring + kStages * kStageBytes;
+    static constexpr int groups = raw + kRawStages * kRawBytes;
+    static constexpr int bars = groups + kMaxGroups * static_cast<int>(sizeof(GroupPlan));
+    static constexpr int misc = bars + kRegionBars * 8;
+    static constexpr int total = 1024 + misc + 64;
+    static constexpr int kThreads = KV8 ? 512 : 384;
+};
+
+// The block of rows and the run of tiles a CTA works on at a time.
+struct Segment {
+    int kvh, tile0, n, plen, slot;
+    int row0;   // first row of the block within the group
+    int rows;   // rows of the block
+    int seq0;   // the group's first sequence
+    int group;
+    bool two;   // more than kRowTile rows: both streams use every tile
+};
+
+template <int BR>
+__device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_groups, long long &u, long long u1,
+                                             int cta, Segment &s) {
+    if (u >= u1) return false;
+    int lo = 0, n = num_groups;  // the last group that begins at or before unit u
+    while (n > 1) {
+        const int half = n >> 1;
+        if (grp[lo + half].first_unit <= u) {
+            lo += half;
+            n -= half;
+        } else {
+            n = half;
+        }
+    }
+    const GroupPlan g = grp[lo];
+    const long long local = u - g.first_unit;
+    const long long item = local / g.tiles;
+    s.tile0 = static_cast<int>(local - item * g.tiles);
+    const long long left = u1 - u;
+    s.n = left < g.tiles - s.tile0 ? static_cast<int>(left) : g.tiles - s.tile0;
+    s.kvh = static_cast<int>(item / g.blocks);
+    s.row0 = (static_cast<int>(item) - s.kvh * g.blocks) * BR;
+    s.rows = min(BR, g.rows - s.row0);
+    s.plen = g.tokens;
+    s.seq0 = g.first_seq;
+    s.group = lo;
+    s.slot = g.first_item + static_cast<int>(item) + cta;
+    s.two = s.rows > kRowTile;
+    u += s.n;
+    return true;
+}
+
+// The groups' units and items, by one warp: running sums over chunks of 32
+// groups.  Returns false (on every lane) where group_starts is not
+// non-decreasing within the batch or asks for more items than the workspace holds.
+template <int DPAD>
+__device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *grp, long long *total, int lane, bool flag) {
+    long long units = 0;
+    int items = 0;
+    bool bad = false;
+    for (int base = 0; base < p.num_groups; base += 32) {
+        const int g = base + lane;
+        GroupPlan r = {};
+        long long mine = 0;
+        int it = 0;
+        if (g < p.num_groups) {
+            const int a = p.group_starts ? p.group_starts[g] : 0;
+            const int b = p.group_starts ? p.group_starts[g + 1] : p.num_seqs;
+            int len = p.prefix_lens[g];
+            const int most = p.max_prefix_blocks * static_cast<int>(p.block_size.d);
+            if (len < 0 || len > most) {
+                if (flag) dev::flag_status(p.status, PD_DEV_BAD_CONTEXT_LEN);
+                len = len < 0 ? 0 : most;
+            }
+            bad |= a < 0 || b < a || b > p.num_seqs;
+            r.first_seq = a;
+            r.rows = bad ? 0 : (b - a) * p.group;
+            r.blocks = (r.rows + block_rows(DPAD) - 1) / block_rows(DPAD);
+            r.tokens = len;
+            r.tiles = (len + tile_tokens(DPAD) - 1) / tile_tokens(DPAD);
+            it = r.tiles > 0 ? r.blocks * p.num_kv_heads : 0;
+            mine = static_cast<long long>(it) * r.tiles;
+        }
+        long long su = mine;
+        int si = it;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long ou = __shfl_up_sync(0xffffffffu, su, off);
+            const int oi = __shfl_up_sync(0xffffffffu, si, off);
+            if (lane >= off) {
+                su += ou;
+                si += oi;
+            }
+        }
+        r.first_unit = units + su - mine;
+        r.first_item = items + si - it;
+        if (g < p.num_groups) grp[g] = r;
+        units += __shfl_sync(0xffffffffu, su, 31);
+        items += __shfl_sync(0xffffffffu, si, 31);
+        if (items > p.max_items) break;
+    }
+    bad = __any_sync(0xffffffffu, bad) || items > p.max_items;
+    if (bad && flag) dev::flag_status(p.status, PD_DEV_BAD_GROUPS);
+    *total = bad ? 0 : units;
+    return !bad;
+}
+
+// Bounded wait of a whole warp, which also ends when another warp of the CTA
+// gave up.  The answer is the same on every lane (the warp goes on to aligned
+// instructions together).
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    bool ok = dev::mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = dev::global_timer_ns();
+        while (!(ok = dev::mbar_try_wait(bar, parity))) {
+            if (*gave_up) break;
+            if (dev::global_timer_ns() - t0 > 2000000000ull) {
+                *gave_up = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <bool KV8>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return KV8 ? dev::pack_f16x2(lo, hi) : dev::pack_bf16x2(lo, hi);
+}
+
+template <int DPAD, bool KV8>
+__global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
+    prefix_kernel(const __grid_constant__ KvMaps<1> maps, const __grid_constant__ PrefixParams p) {
+    using L = Plan<DPAD, KV8>;
+    constexpr int BN = L::kTile;
+    constexpr int BR = L::kBlock;
+    constexpr int NST = L::kStages;
+    constexpr bool ONE = L::kOne;
+    constexpr int CHUNKS = DPAD / 8;  // 16-byte chunks of a 16-bit row
+    constexpr uint32_t kDescS = tc::instr_desc(KV8 ? 0 : 1, kRowTile, BN, false);
+    constexpr uint32_t kDescO = tc::instr_desc(KV8 ? 0 : 1, kRowTile, DPAD, true);
+    const float kNegInf = -__int_as_float(0x7f800000);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t base = dev::smem_addr(smem);
+    GroupPlan *grp = reinterpret_cast<GroupPlan *>(smem + L::groups);
+    // barriers: full[NST], empty[NST], raw_full[3], raw_empty[3], s_full[2],
+    // p_full[2], o_done[2], q_full[2], tail
+    const uint32_t bars = base + L::bars;
+    const uint32_t bar_full = bars, bar_empty = bar_full + 8 * NST, bar_rfull = bar_empty + 8 * NST,
+                   bar_rempty = bar_rfull + 24, bar_s = bar_rempty + 24, bar_p = bar_s + 16, bar_o = bar_p + 16,
+                   bar_q = bar_o + 16, bar_tail = bar_q + 16;
+    static_assert(2 * NST + 15 <= kRegionBars, "barrier region");
+    long long *total_s = reinterpret_cast<long long *>(smem + L::misc);
+    volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc + 8);
+    uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 16);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- set-up that reads no global memory -----------------------------------
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            dev::mbar_init(bar_full + 8 * i, KV8 ? 128 : 1);
+            dev::mbar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            dev::mbar_init(bar_rfull + 8 * i, 1);
+            dev::mbar_init(bar_rempty + 8 * i, 128);
+        }
+        for (int i = 0; i < 2; ++i) {
+            dev::mbar_init(bar_s + 8 * i, 1);
+            dev::mbar_init(bar_p + 8 * i, 128);
+            dev::mbar_init(bar_o + 8 * i, 1);
+            dev::mbar_init(bar_q + 8 * i, 128);
+        }
+        dev::mbar_init(bar_tail, 1);
+        dev::fence_mbar_init();
+        *gave_up = 0;
+        dev::prefetch_tensormap(&maps.k[0]);
+        dev::prefetch_tensormap(&maps.v[0]);
+    }
+    if (warp == 1) tc::tmem_alloc_512(dev::smem_addr(tmem_s));
+    dev::griddep_wait();  // q, the caches, tables and lengths are final
+    if (warp == 0) {
+        long long total;
+        const bool good = plan_groups<DPAD>(p, grp, &total, lane, blockIdx.x == 0);
+        if (lane == 0) *total_s = total;
+        __syncwarp();
+        if (blockIdx.x == 0) {  // the merge finds each row's partials from this
+            for (int g = lane; g < p.num_groups; g += 32) {
+                GroupPlan r = grp[g];
+                if (!good) r.tiles = 0;
+                p.plan_groups[g] = r;
+            }
+            if (lane == 0) *p.plan_total = total;
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_s;
+    const long long W = *total_s;
+    const int C = W < gridDim.x ? static_cast<int>(W) : static_cast<int>(gridDim.x);
+    const int cta = blockIdx.x;
+    long long u = 0, u1 = 0;
+    if (cta < C) {
+        u = W * cta / C;
+        u1 = W * (cta + 1) / C;
+    }
+    const int bs = static_cast<int>(p.block_size.d);
+    const int D = p.head_dim;
+    Segment sg;
+
+    if (warp == 0) {
+        // ---- loads: K and V tiles in the order the products take them ------------
+        constexpr int NCH = BN / kTileTokens;                // 16-token boxes of a tile
+        constexpr int COLS = KV8 ? (DPAD < 128 ? DPAD : 128) : kBoxCols;  // columns of a box
+        constexpr int NBOX = NCH * (DPAD / COLS);
+        constexpr int DEPTH = KV8 ? L::kRawStages : NST;
+        constexpr int BYTES = KV8 ? L::kRawBytes : L::kStageBytes;
+        const uint32_t full = KV8 ? bar_rfull : bar_full, empty = KV8 ? bar_rempty : bar_empty;
+        const uint32_t stage0 = base + (KV8 ? L::raw : L::ring);
+        const uint64_t policy = dev::l2_evict_first_policy();
+        const int chunk = lane % NCH, col = lane / NCH;
+        int st = 0;
+        uint32_t ph = 0;  // phase of the stage about to be filled
+        uint32_t tail_ph = 0;
+        bool ok = true;
+        long long issued = 0;
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
+            const int32_t *ids = p.prefix_table + static_cast<long long>(sg.group) * p.max_prefix_blocks;
+            const int ahead = ONE || !sg.two ? 2 : 1;
+            auto load = [&](bool is_v, int j) {
+                const int tok = (sg.tile0 + j) * BN + chunk * kTileTokens;
+                const int blk = fast_div(tok, p.block_size);
+                int id = p.num_blocks;  // past the prefix: zeros
+                if (lane < NBOX && tok < sg.plen) {
+                    id = __ldg(ids + blk);
+                    if (id < 0 || id >= p.num_blocks) {
+                        dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
+                        id = p.num_blocks;
+                    }
+                }
+                if (!wait_bar(empty + 8 * st, ph ^ 1, gave_up)) return false;
+                const uint32_t dst = stage0 + st * BYTES;
+                const int nv = sg.plen - (sg.tile0 + j) * BN;  // live tokens of the tile
+                // A tile's box of live and dead tokens holds whatever the cache's
+                // slots past the prefix hold; a dead V row must not reach the
+                // product (0 x NaN), so those rows are zeroed before it is handed on.
+                const bool tail = !KV8 && is_v && nv < BN && (nv & (kTileTokens - 1));
+                const uint32_t bar = tail ? bar_tail : full + 8 * st;
+                if (lane == 0) dev::mbar_arrive_expect_tx(bar, BYTES);
+                __syncwarp();
+                if (lane < NBOX) {
+                    const int sub = tok - blk * bs;
+                    dev::tma_load_4d(dst + col * (BN * (KV8 ? COLS : 128)) + chunk * (kTileTokens * (KV8 ? COLS : 128)),
+                                     is_v ? &maps.v[0] : &maps.k[0], bar, col * COLS, p.tok_dim == 1 ? sub : sg.kvh,
+                                     p.tok_dim == 1 ? sg.kvh : sub, id, policy);
+                }
+                if (tail) {
+                    if (!wait_bar(bar_tail, tail_ph, gave_up)) return false;
+                    tail_ph ^= 1;
+                    uint8_t *tile = smem + L::ring + st * BYTES;
+                    const int end = (nv + kTileTokens - 1) / kTileTokens * kTileTokens;
+                    for (int b = 0; b < DPAD / 64; ++b)
+                        for (int i = nv * 8 + lane; i < end * 8; i += 32)
+                            *reinterpret_cast<uint4 *>(tile + b * (BN * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+                    tc::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) arrive(full + 8 * st);
+                }
+                ++issued;
+                if (++st == DEPTH) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                return true;
+            };
+            for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
+                if (i < sg.n) ok = load(false, i);
+                const int v = i - ahead + 1;
+                if (ok && v >= 0) ok = load(true, v);
+            }
+        }
+        if (!ok && lane == 0) {
+            // a wait ran out: let the copies in flight land before the CTA ends
+            dev::flag_status(p.status, PD_DEV_WAIT_TIMEOUT);
+            const long long last = issued < DEPTH ? issued : DEPTH;
+            for (long long i = issued - last; i < issued; ++i)
+                dev::mbar_wait_bounded(full + 8 * static_cast<int>(i % DEPTH), static_cast<uint32_t>((i / DEPTH) & 1),
+                                       100000000ull);
+        }
+    } else if (warp == 1) {
+        // ---- products ---------------------------------------------------------------
+        int st = 0;
+        uint32_t ph = 0;
+        uint32_t pph[2] = {0, 0}, qph[2] = {0, 0};
+        bool ok = true;
+        const uint32_t qa = base + L::q, ra = base + L::ring;
+        // the next tile of the ring (K or V), once it has landed
+        auto take = [&](int &stage) {
+            if (!wait_bar(bar_full + 8 * st, ph, gave_up)) return false;
+            stage = st;
+            if (++st == NST) {
+                st = 0;
+                ph ^= 1;
+            }
+            tc::fence_after();
+            return true;
+        };
+        auto scores = [&](int buf, int qt, int stage) {
+            if (lane == 0) {
+                const uint32_t qd = qa + qt * (kRowTile * DPAD * 2), kd = ra + stage * L::kStageBytes;
+#pragma unroll
+                for (int k = 0; k < DPAD / 16; ++k)
+                    tc::mma_ss(tmem + buf * 128, tc::smem_desc(qd + (k / 4) * (kRowTile * 128) + (k % 4) * 32, 16),
+                               tc::smem_desc(kd + (k / 4) * (BN * 128) + (k % 4) * 32, 16), kDescS, k > 0);
+                tc::commit(bar_s + 8 * buf);
+            }
+            __syncwarp();
+        };
+        auto values = [&](int buf, int o, int stage, bool accumulate, bool done) {
+            if (lane == 0) {
+                const uint32_t vd = ra + stage * L::kStageBytes;
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k)
+                    tc::mma_ts(tmem + 256 + o * DPAD, tmem + buf * 128 + k * 8, tc::smem_desc(vd + k * 2048, BN * 128), kDescO,
+                               accumulate || k > 0);
+                if (done) tc::commit(bar_o + 8 * o);
+            }
+            __syncwarp();
+        };
+        auto release = [&](int stage) {
+            if (lane == 0) tc::commit(bar_empty + 8 * stage);
+            __syncwarp();
+        };
+        auto weights = [&](int buf) {
+            if (!wait_bar(bar_p + 8 * buf, pph[buf], gave_up)) return false;
+            pph[buf] ^= 1;
+            tc::fence_after();
+            return true;
+        };
+        auto queries = [&](int t) {
+            if (!wait_bar(bar_q + 8 * t, qph[t], gave_up)) return false;
+            qph[t] ^= 1;
+            tc::fence_after();
+            return true;
+        };
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
+            const int n = sg.n;
+            int ks = 0, vs = 0;
+            ok = queries(0) && take(ks);
+            if (!ok) break;
+            scores(0, 0, ks);
+            if (!ONE && sg.two) {
+                if (!(ok = queries(1))) break;
+                scores(1, 1, ks);
+                release(ks);
+                for (int j = 0; ok && j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    if (!(ok = take(vs))) break;
+                    for (int t = 0; ok && t < 2; ++t) {
+                        if (!(ok = weights(t))) break;
+                        values(t, t, vs, j > 0, !more);
+                        if (more) {
+                            if (t == 0 && !(ok = take(ks))) break;
+                            scores(t, t, ks);
+                        }
+                    }
+                    if (!ok) break;
+                    release(vs);
+                    if (more) release(ks);
+                }
+            } else {
+                release(ks);
+                if (n > 1) {
+                    if (!(ok = take(ks))) break;
+                    scores(1, 0, ks);
+                    release(ks);
+                }
+                for (int j = 0; ok && j < n; ++j) {
+                    const int t = j & 1;
+                    if (!(ok = take(vs) && weights(t))) break;
+                    values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= n);
+                    release(vs);
+                    if (j + 2 < n) {
+                        if (!(ok = take(ks))) break;
+                        scores(t, 0, ks);
+                        release(ks);
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            // let the products in flight end before TMEM is freed
+            tc::commit(bar_tail);
+            dev::mbar_wait_bounded(bar_tail, 0, 100000000ull);
+        }
+    } else if (warp >= 4 && warp < (ONE ? 8 : 12)) {
+        // ---- softmax: a thread per row -----------------------------------------------
+        const int t = (warp - 4) >> 2;            // the stream
+        const int r = (warp & 3) * 32 + lane;     // the row of its tile
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t to = tmem + lanes + 256 + t * DPAD;
+        uint32_t sph[2] = {0, 0}, oph = 0;
+        bool ok = true;
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
+            const bool two = sg.two;
+            float scale = p.scale_log2;
+            // -- this stream's query rows into shared memory (128-byte swizzle); with
+            // at most 128 rows the streams share stream 0's
+            if (two || t == 0) {
+                uint8_t *qt = smem + L::q + t * (kRowTile * DPAD * 2);
+                constexpr int STEPS = CHUNKS;  // 32 rows x CHUNKS chunks over 32 lanes
+#pragma unroll 4
+                for (int i = 0; i < STEPS; ++i) {
+                    const int e = i * 32 + lane;
+                    const int row = (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;
+                    const int gr = t * kRowTile + row;  // row of the block
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (gr < sg.rows && c * 8 < D) {
+                        const int x = sg.row0 + gr;
+                        const int sq = fast_div(x, p.fd_group);
+                        const long long at = (static_cast<long long>(sg.seq0 + sq) * p.num_q_heads + sg.kvh * p.group +
+                                              (x - sq * p.group)) * D + c * 8;
+                        v = __ldg(reinterpret_cast<const uint4 *>(p.q + at));
+                        if (p.negative) {
+                            v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(qt + (c / 8) * (kRowTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+                }
+                tc::fence_async_shared();
+                arrive(bar_q + 8 * t);
+            }
+            float m = kNegInf, l = 0.f;
+            bool first = true;
+            const int step = ONE || two ? 1 : 2;
+            for (int j = step == 2 ? t : 0; j < sg.n; j += step) {
+                const int buf = ONE ? (j & 1) : t;
+                const uint32_t ts = tmem + lanes + buf * 128;
+                if (!(ok = wait_bar(bar_s + 8 * buf, sph[buf], gave_up))) break;
+                sph[buf] ^= 1;
+                tc::fence_after();
+                const int nv = sg.plen - (sg.tile0 + j) * BN;
+                float mx = kNegInf;
+#pragma unroll
+                for (int c = 0; c < BN; c += 32) {
+                    uint32_t x[32];
+                    tc::ld_32x32(ts + c, x);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, c + i < nv ? __uint_as_float(x[i]) : kNegInf);
+                }
+                mx *= scale;
+                const float m_old = m;
+                if (mx > m + 8.f || first) m = mx;
+                const float alpha = first ? 1.f : dev::exp2_approx(m_old - m);
+                const bool move = !first && m != m_old;
+                if (ONE && !first) {
+                    // the last product onto O has to be done before O is touched or added to
+                    if (!(ok = wait_bar(bar_o, oph, gave_up))) break;
+                    oph ^= 1;
+                    tc::fence_after();
+                }
+                if (__any_sync(0xffffffffu, move)) {
+                    l *= alpha;
+#pragma unroll 1
+                    for (int c = 0; c < DPAD; c += 32) {
+                        uint32_t x[32];
+                        tc::ld_32x32(to + c, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
+                        tc::st_32x32(to + c, x);
+                    }
+                }
+                first = false;
+                const float off = m == kNegInf ? 0.f : m;
+                float sum = 0.f;
+                // (P of 64 columns goes over S columns that both passes have read)
+                uint32_t pk[BN / 2];
+#pragma unroll
+                for (int c = 0; c < BN; c += 32) {
+                    uint32_t x[32];
+                    tc::ld_32x32(ts + c, x);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float a = __uint_as_float(x[i]), b = __uint_as_float(x[i + 1]);
+                        const float ea = c + i < nv ? dev::exp2_approx(fmaf(a, scale, -off)) : 0.f;
+                        const float eb = c + i + 1 < nv ? dev::exp2_approx(fmaf(b, scale, -off)) : 0.f;
+                        sum += ea + eb;
+                        pk[(c + i) / 2] = pack2<KV8>(ea, eb);
+                    }
+                }
+                l += sum;
+#pragma unroll
+                for (int c = 0; c < BN / 2; c += 32) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = pk[c + i];
+                    tc::st_32x32(ts + c, x);
+                }
+                tc::wait_st();
+                tc::fence_before();
+                arrive(bar_p + 8 * buf);
+            }
+            if (!ok) break;
+            // -- the partial of this row
+            const int gr = two ? t * kRowTile + r : r;
+            const bool live = gr < sg.rows;
+            const long long at = static_cast<long long>(sg.slot) * BR + t * kRowTile + r;
+            if (live) *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(m, l);
+            if (!first) {
+                if (!(ok = wait_bar(bar_o + 8 * t, oph, gave_up))) break;
+                oph ^= 1;
+                tc::fence_after();
+                float *o = p.part_o + (static_cast<long long>(sg.slot) * (DPAD / 8)) * (BR * 8) + (t * kRowTile + r) * 8;
+#pragma unroll 1
+                for (int c = 0; c < DPAD; c += 32) {
+                    uint32_t x[32];
+                    tc::ld_32x32(to + c, x);
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<uint4 *>(o + ((c + i) / 8) * (BR * 8) + (i & 4)) =
+                                make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    }
+                }
+                tc::fence_before();
+            }
+        }
+    }
+    dev::griddep_launch_dependents();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 1) tc::tmem_free_512(tmem);
+}
+
+}  // namespace prefix
+}  // namespace pd

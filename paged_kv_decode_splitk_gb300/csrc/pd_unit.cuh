@@ -196,7 +196,10 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
     constexpr bool KV1BAR = KV8 && DPAD == 128;
     constexpr int TILE_BYTES = kTileTokens * DPAD * (KV8 ? 1 : 2);  // one landed K or V tile
     constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-    static_assert(!KV8 || MODE == kModePaged, "FP8 caches are a paged-mode source");
+    // kModeOwn is paged mode with every non-empty split kept as a partial (for
+    // a merge with the partials of another pass)
+    constexpr bool PAGED = MODE == kModePaged || MODE == kModeOwn;
+    static_assert(!KV8 || PAGED, "FP8 caches are a paged-mode source");
     constexpr bool RUN = MODE == kModeTiledRun;
     constexpr int RT = 8 * GN;         // query rows per CTA
     constexpr int OSTRIDE = DPAD + 4;  // padded row stride of o in shared memory
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
         u /= C;
     }
     int split = 0;  // paged: the split; fused tiled run: the source (step_tile call)
-    if constexpr (MODE == kModePaged) {
+    if constexpr (PAGED) {
         const int un = fast_div(u, p.fd_split);
         split = u - un * p.num_splits;
         u = un;
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
     if (!RUN && p.prefetch_tiles > 0) {
         int t0 = 0, t1 = 0, ss = s;
         const int32_t *ids;
-        if constexpr (MODE == kModePaged) {
+        if constexpr (PAGED) {
             ss = p.lpt ? longest_first(true) : s;
             int L = __ldcg(p.context_lens + ss);
             L = L < 0 ? 0 : (L > Lmax ? Lmax : L);
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
     }
 
     dev::griddep_wait();  // the previous kernel's writes (q, caches, tables, out) are visible
-    if constexpr (MODE == kModePaged) {
+    if constexpr (PAGED) {
         if (p.lpt) s = longest_first(false);
     }
     const int G = PACKED ? PD_GQA : p.group;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
     int tok0 = 0, tok1 = 0;
     bool direct = true;  // paged: write normalised output instead of a partial
     const int32_t *ids_base;
-    if constexpr (MODE == kModePaged) {
+    if constexpr (PAGED) {
         int L = p.context_lens[s];
         if (L < 0 || L > Lmax) {
             if (tid == 0 && part == 0 && split == 0 && qt == 0 && kvh == 0)
@@ -401,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
         const long long a = static_cast<long long>(split) * chunk;
         tok0 = static_cast<int>(a < L ? a : L);
         tok1 = static_cast<int>(a + chunk < L ? a + chunk : L);
-        direct = L <= chunk;  // at most one non-empty split
+        direct = MODE == kModePaged && L <= chunk;  // at most one non-empty split
         ids_base = p.block_table + static_cast<long long>(s) * p.max_blocks_per_seq;
         if (tok0 >= tok1) {
             // Empty split.  Split 0 of an empty sequence owns the zero output.
-            if (L == 0 && split == 0 && part == 0) {
+            if (MODE == kModePaged && L == 0 && split == 0 && part == 0) {
                 for (int e = tid; e < Gt * (D / 2); e += kThreads) {
                     const int g = e / (D / 2), d = (e - g * (D / 2)) * 2;
                     *reinterpret_cast<uint32_t *>(p.out + (static_cast<long long>(s) * Hq + h0 + g) * D + d) = 0u;
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
     if (C > 1 && part >= V) return;
     // A paged unit of one part: its result is that part's, in either layout
     // (no fold into a running result, no hand-off between ranks).
-    const bool solo = MODE == kModePaged && V == 1;
+    const bool solo = PAGED && V == 1;
 
     // ---- q to shared memory (the barriers were initialised at the start) ----------
     // Over an FP8 cache the products run in f16: q is staged as f16 scaled by a
@@ -787,8 +790,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const float m_old = m_run[nt][c];
-                    const float m_new = MODE == kModePaged ? (cmx[c] > m_old + 8.f ? cmx[c] : m_old)
-                                                           : fmaxf(m_old, cmx[c]);
+                    const float m_new = PAGED ? (cmx[c] > m_old + 8.f ? cmx[c] : m_old) : fmaxf(m_old, cmx[c]);
                     alpha[nt][c] = dev::exp2_approx(m_old - m_new);
                     const float e0 = dev::exp2_approx(x[c] - m_new);
                     const float e1 = dev::exp2_approx(x[c + 2] - m_new);
@@ -1002,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
                 }
         __syncthreads();
 
-        if constexpr (MODE == kModePaged && !PACKED) {
+        if constexpr (PAGED && !PACKED) {
             if (solo) {
                 // A unit of one part: each output pair straight from the warp
                 // partials, with the operations, in the order, of the general
@@ -1185,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
         }
         const long long row = static_cast<long long>(s) * Hq + h0 + g;
         float fa = 0.f, fb = 0.f;
-        if constexpr (MODE == kModePaged || RUN) {
+        if constexpr (PAGED || RUN) {
             // a split's, or a fused run's call's, partial [o, m, l]
             if (RUN || !direct) {
                 p.ws_ml[(row * p.num_splits + split) * 2 + 0] = M;
@@ -1245,7 +1247,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
             acc0 *= p.v_scale;
             acc1 *= p.v_scale;
         }
-        if constexpr (MODE == kModePaged || RUN) {
+        if constexpr (PAGED || RUN) {
             if (!RUN && direct) {
                 const float Lsum = fx[i * 4 + 1];
                 const bool pos = fx[i * 4 + 3] > 0.f;

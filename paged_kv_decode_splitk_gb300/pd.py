@@ -42,6 +42,7 @@ PD_DEV_BAD_BLOCK_ID = 1
 PD_DEV_BAD_CONTEXT_LEN = 2
 PD_DEV_BAD_TILE_COUNT = 4
 PD_DEV_WAIT_TIMEOUT = 8
+PD_DEV_BAD_GROUPS = 16
 
 PD_ROPE_HALF = 0
 PD_ROPE_INTERLEAVED = 1
@@ -118,6 +119,9 @@ _SIGS = {
                                 _I, _I, _I, _I, ctypes.c_float, _I, _VP, _SZ, _I, _VP]),
     "pd_decode_attn_noalloc": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _I,
                                     ctypes.c_float, _I, _I, _VP]),
+    "pd_prefix_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "pd_decode_attn_prefix": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _I,
+                                   ctypes.c_float, _I, _VP, _SZ, _VP]),
     "pd_rope_frequencies": (_I, [_VP, _VP, _VP]),
     "pd_rope_create": (_I, [_VP, _VP]),
     "pd_rope_destroy": (None, [_VP]),
@@ -147,6 +151,8 @@ _SIGS = {
 def lib():
     """Load libpd.so (built by `__graft_entry__.build()` / `build.py`)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -187,11 +193,20 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_torch_stream = None  # () -> the current stream's address
+
+
 def _stream(stream) -> int | None:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    global _torch_stream
+    if _torch_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        current = torch.cuda.current_device
+        # the raw handle costs 0.1 us where a Stream object costs 3
+        _torch_stream = (lambda: raw(current())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _torch_stream()
 
 
 # ---- policy -----------------------------------------------------------------
@@ -324,6 +339,27 @@ def pd_decode_attn_noalloc(q, k_cache, v_cache, block_table, context_lens, out, 
     return _check(rc)
 
 
+# ---- decode behind shared prefixes ----------------------------------------------------
+
+def pd_prefix_workspace_bytes(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                              num_splits: int) -> int:
+    return lib().pd_prefix_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, num_splits)
+
+
+def pd_decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens, out,
+                          inv_sqrt_d: float, num_splits: int, workspace, stream=None, num_blocks: int | None = None) -> int:
+    """out[S, Hq, D] <- decode attention behind shared prefixes (see pd.h): prefix_table [G, max_prefix_blocks],
+    prefix_lens [G], group_starts [G + 1] or None (one group), the rest as for pd_decode_attn."""
+    S, Hq, D = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    G, mpb = prefix_table.shape
+    return _check(lib().pd_decode_attn_prefix(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_table.data_ptr(), mpb, prefix_lens.data_ptr(),
+        _ptr(group_starts), G, block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), out.data_ptr(), S, Hq,
+        Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d, num_splits, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
 # ---- rotary positions and the append to the paged cache ------------------------------
 
 def rope_desc(head_dim: int, rot_dim: int | None = None, *, layout="half", base: float = 10000.0, scaling="none",
@@ -410,7 +446,7 @@ def pd_rope_apply(rope, x, positions, out, inverse: bool = False, stream=None) -
     T, H, D = x.shape
     return _check(lib().pd_rope_apply(_handle(rope), x.data_ptr(), _token_stride(x), x.stride(1) if H > 1 else D,
                                       positions.data_ptr(), out.data_ptr(), _token_stride(out),
-                                      out.stride(1) if H > 1 else D, T, H, int(inverse), _stream(stream)))
+                                      out.stride(1) if H > 1 else D, T, H, inverse, _stream(stream)))
 
 
 def pd_append_kv(rope, q, k, v, q_out, k_cache, v_cache, block_table, context_lens, token_starts=None, stream=None,
@@ -418,25 +454,26 @@ def pd_append_kv(rope, q, k, v, q_out, k_cache, v_cache, block_table, context_le
     """New tokens' keys (rotated) and values into a BF16 cache, q rotated into q_out (see pd.h).  q, k, v
     [T, H, D] strided in tokens; rope a Rope or None; q and q_out None for keys and values alone."""
     T, Hkv, D = k.shape
-    nb, bs = k_cache.shape[0], k_cache.shape[1]
+    nb, bs = k_cache.shape[:2]
+    S, mb = block_table.shape
     return _check(lib().pd_append_kv(
         _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
-        _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-        block_table.shape[1], context_lens.data_ptr(), _ptr(token_starts), T, context_lens.shape[0],
-        0 if q is None else q.shape[1], Hkv, D, bs, nb if num_blocks is None else num_blocks, _stream(stream)))
+        _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
+        context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
+        nb if num_blocks is None else num_blocks, _stream(stream)))
 
 
 def pd_append_kv_fp8(rope, q, k, v, q_out, k_cache, v_cache, k_scale: float, v_scale: float, block_table, context_lens,
                      token_starts=None, stream=None, num_blocks: int | None = None) -> int:
     """pd_append_kv into an FP8 cache (uint8 E4M3 codes of x / k_scale and x / v_scale)."""
     T, Hkv, D = k.shape
-    nb, bs = k_cache.shape[0], k_cache.shape[1]
+    nb, bs = k_cache.shape[:2]
+    S, mb = block_table.shape
     return _check(lib().pd_append_kv_fp8(
         _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
-        _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), float(k_scale), float(v_scale),
-        block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), _ptr(token_starts), T,
-        context_lens.shape[0], 0 if q is None else q.shape[1], Hkv, D, bs, nb if num_blocks is None else num_blocks,
-        _stream(stream)))
+        _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, block_table.data_ptr(),
+        mb, context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
+        nb if num_blocks is None else num_blocks, _stream(stream)))
 
 
 # ---- tiled ---------------------------------------------------------------------------

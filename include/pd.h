@@ -311,6 +311,17 @@ int pd_decode_attn_prefix(const void *q, const void *k_cache, const void *v_cach
                           float inv_sqrt_d, int num_splits, void *workspace,
                           size_t workspace_bytes, void *stream);
 
+/* pd_decode_attn_prefix over an FP8 cache of E4M3 codes with per-tensor scales,
+ * as pd_decode_attn_fp8 reads it (head_dim a multiple of 16). */
+int pd_decode_attn_prefix_fp8(const void *q, const void *k_cache, const void *v_cache, float k_scale,
+                              float v_scale, const int32_t *prefix_table, int max_prefix_blocks,
+                              const int32_t *prefix_lens, const int32_t *group_starts,
+                              int num_groups, const int32_t *block_table, int max_blocks_per_seq,
+                              const int32_t *context_lens, void *out, int num_seqs,
+                              int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                              int num_blocks, float inv_sqrt_d, int num_splits, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
 /* ---- rotary positions ------------------------------------------------------
  * The rotation of a query or key row x of head_dim columns at position t: its
  * first rot_dim columns form rot_dim/2 pairs (a, b), pair i turned by the

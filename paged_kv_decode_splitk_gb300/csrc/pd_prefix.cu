@@ -289,7 +289,8 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     p.plan_total = reinterpret_cast<long long *>(ws + lay.plan_total);
     const int dpad = dpad_of(head_dim);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = dispatch_prefix<false>(dpad, &view.k, &view.v, p, ctas, st);
+    cudaError_t e = kv8 ? dispatch_prefix<true>(dpad, &view.k, &view.v, p, ctas, st)
+                        : dispatch_prefix<false>(dpad, &view.k, &view.v, p, ctas, st);
     if (e != cudaSuccess) return report_cuda(e, "prefix pass launch");
 
     MergeParams m = {};
@@ -343,6 +344,19 @@ int pd_decode_attn_prefix(const void *q, const void *k_cache, const void *v_cach
                           float inv_sqrt_d, int num_splits, void *workspace, size_t workspace_bytes, void *stream) {
     return pd::prefix::decode_prefix_impl("pd_decode_attn_prefix", q, k_cache, v_cache, false, 1.f, 1.f, prefix_table,
                                           max_prefix_blocks, prefix_lens, group_starts, num_groups, block_table,
+                                          max_blocks_per_seq, context_lens, out, num_seqs, num_q_heads, num_kv_heads,
+                                          head_dim, block_size, num_blocks, inv_sqrt_d, num_splits, workspace,
+                                          workspace_bytes, stream);
+}
+
+int pd_decode_attn_prefix_fp8(const void *q, const void *k_cache, const void *v_cache, float k_scale, float v_scale,
+                              const int32_t *prefix_table, int max_prefix_blocks, const int32_t *prefix_lens,
+                              const int32_t *group_starts, int num_groups, const int32_t *block_table,
+                              int max_blocks_per_seq, const int32_t *context_lens, void *out, int num_seqs, int num_q_heads,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks, float inv_sqrt_d,
+                              int num_splits, void *workspace, size_t workspace_bytes, void *stream) {
+    return pd::prefix::decode_prefix_impl("pd_decode_attn_prefix_fp8", q, k_cache, v_cache, true, k_scale, v_scale,
+                                          prefix_table, max_prefix_blocks, prefix_lens, group_starts, num_groups, block_table,
                                           max_blocks_per_seq, context_lens, out, num_seqs, num_q_heads, num_kv_heads,
                                           head_dim, block_size, num_blocks, inv_sqrt_d, num_splits, workspace,
                                           workspace_bytes, stream);

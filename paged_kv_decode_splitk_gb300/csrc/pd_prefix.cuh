@@ -49,6 +49,7 @@ namespace prefix {
 
 constexpr int kRowTile = 128;   // rows of one MMA
 constexpr int kRegionBars = 32;
+constexpr int kConverters = 64;  // threads that turn FP8 tiles into f16 ones
 
 // Shared-memory plan (bytes from the 1024-aligned base).
 template <int DPAD, bool KV8>
@@ -67,8 +68,9 @@ struct Plan {
     static constexpr int groups = raw + kRawStages * kRawBytes;
     static constexpr int bars = groups + kMaxGroups * static_cast<int>(sizeof(GroupPlan));
     static constexpr int misc = bars + kRegionBars * 8;
-    static constexpr int total = 1024 + misc + 64;
-    static constexpr int kThreads = KV8 ? 512 : 384;
+    static constexpr int row_scale = misc + 64;  // FP8: each query row's softmax scale
+    static constexpr int total = 1024 + row_scale + (KV8 ? 2 * 2 * kRowTile * 4 : 0);
+    static constexpr int kThreads = 384;
 };
 
 // The block of rows and the run of tiles a CTA works on at a time.
@@ -229,12 +231,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     // ---- set-up that reads no global memory -----------------------------------
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
-            dev::mbar_init(bar_full + 8 * i, KV8 ? 128 : 1);
+            dev::mbar_init(bar_full + 8 * i, KV8 ? kConverters : 1);
             dev::mbar_init(bar_empty + 8 * i, 1);
         }
         for (int i = 0; i < 3; ++i) {
             dev::mbar_init(bar_rfull + 8 * i, 1);
-            dev::mbar_init(bar_rempty + 8 * i, 128);
+            dev::mbar_init(bar_rempty + 8 * i, kConverters);
         }
         for (int i = 0; i < 2; ++i) {
             dev::mbar_init(bar_s + 8 * i, 1);
@@ -465,6 +467,62 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             tc::commit(bar_tail);
             dev::mbar_wait_bounded(bar_tail, 0, 100000000ull);
         }
+    } else if (KV8 && warp < 4) {
+        // ---- FP8: each landed tile of codes into an f16 tile of the ring -------------
+        // (exact: every E4M3 value is an f16 value; k_scale is in the softmax
+        // scale, v_scale in the merge).  A quarter-warp takes two rows x 64 codes,
+        // the second row of the neighbouring 64 codes: its loads and its stores
+        // each cover the 32 banks once under the swizzle.  V rows past the prefix
+        // are zeroed on the way.
+        constexpr int CPR = DPAD / 16;               // 16-code chunks of a row
+        constexpr int ITEMS = BN / 2 * (CPR / 4);    // (row pair, 64 codes)
+        const int me = (warp - 2) * 4 + (lane >> 3), j = lane & 7;
+        int rs = 0, st = 0;
+        uint32_t rph = 0, ph = 0;
+        bool ok = true;
+        auto convert = [&](bool is_v, int nv) {
+            if (!wait_bar(bar_rfull + 8 * rs, rph, gave_up) || !wait_bar(bar_empty + 8 * st, ph ^ 1, gave_up)) return false;
+            const uint8_t *src = smem + L::raw + rs * L::kRawBytes;
+            uint8_t *dst = smem + L::ring + st * L::kStageBytes;
+#pragma unroll 4
+            for (int i = me; i < ITEMS; i += kConverters / 8) {
+                const int kb = i % (CPR / 4), row = i / (CPR / 4) * 2 + (j >> 2);
+                const int c = 4 * (CPR >= 8 ? kb ^ (j >> 2) : kb) + (j & 3);
+                const uint8_t *at = DPAD < 128 ? src + row * DPAD + c * 16
+                                               : src + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                uint4 v = *reinterpret_cast<const uint4 *>(at);
+                if (is_v && row >= nv) v = make_uint4(0, 0, 0, 0);
+                uint4 lo, hi;
+                dev::e4m3x4_to_f16x4(v.x, lo.x, lo.y);
+                dev::e4m3x4_to_f16x4(v.y, lo.z, lo.w);
+                dev::e4m3x4_to_f16x4(v.z, hi.x, hi.y);
+                dev::e4m3x4_to_f16x4(v.w, hi.z, hi.w);
+                uint8_t *box = dst + (c / 4) * (BN * 128) + row * 128;
+                const int u2 = (2 * c) & 7;
+                *reinterpret_cast<uint4 *>(box + ((u2 ^ (row & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4 *>(box + (((u2 + 1) ^ (row & 7)) << 4)) = hi;
+            }
+            tc::fence_async_shared();
+            arrive(bar_full + 8 * st);
+            arrive(bar_rempty + 8 * rs);
+            if (++rs == L::kRawStages) {
+                rs = 0;
+                rph ^= 1;
+            }
+            if (++st == NST) {
+                st = 0;
+                ph ^= 1;
+            }
+            return true;
+        };
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
+            const int ahead = ONE || !sg.two ? 2 : 1;
+            for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
+                if (i < sg.n) ok = convert(false, BN);
+                const int v = i - ahead + 1;
+                if (ok && v >= 0) ok = convert(true, sg.plen - (sg.tile0 + v) * BN);
+            }
+        }
     } else if (warp >= 4 && warp < (ONE ? 8 : 12)) {
         // ---- softmax: a thread per row -----------------------------------------------
         const int t = (warp - 4) >> 2;            // the stream
@@ -473,9 +531,18 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         const uint32_t to = tmem + lanes + 256 + t * DPAD;
         uint32_t sph[2] = {0, 0}, oph = 0;
         bool ok = true;
+        // FP8: the rows' scales, in turn in two places: the other stream may still
+        // have to read the last segment's when this one's are written (it has by
+        // the time a third segment begins: its weights of the first went before)
+        float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
+        int turn = 0;
         while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
             const bool two = sg.two;
             float scale = p.scale_log2;
+            if constexpr (KV8) {
+                row_scale = reinterpret_cast<float *>(smem + L::row_scale) + turn * 2 * kRowTile;
+                turn ^= 1;
+            }
             // -- this stream's query rows into shared memory (128-byte swizzle); with
             // at most 128 rows the streams share stream 0's
             if (two || t == 0) {
@@ -497,6 +564,27 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                             v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
                         }
                     }
+                    if constexpr (KV8) {
+                        // f16 rows under a power of two that brings the row's largest
+                        // |q| into [2^14, 2^15), exactly but for values 2^-28 below it;
+                        // its inverse joins the row's softmax scale
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        float big = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            big = fmaxf(big, fmaxf(fabsf(dev::bf16_lo_f32(w[k])), fabsf(dev::bf16_hi_f32(w[k]))));
+#pragma unroll
+                        for (int off = 1; off < CHUNKS; off <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+                        const int ex = (__float_as_int(big) >> 23) & 0xff;  // big < 2^(ex - 126)
+                        const int up = min(max(141 - ex, -126), 127);       // times 2^up: below 2^15
+                        const float f = __int_as_float((127 + up) << 23);
+                        if (c == 0) row_scale[t * kRowTile + row] = p.scale_log2 * (up < 127 ? __int_as_float((127 - up) << 23)
+                                                                                             : 5.877471754111438e-39f);
+                        v.x = dev::pack_f16x2(dev::bf16_lo_f32(w[0]) * f, dev::bf16_hi_f32(w[0]) * f);
+                        v.y = dev::pack_f16x2(dev::bf16_lo_f32(w[1]) * f, dev::bf16_hi_f32(w[1]) * f);
+                        v.z = dev::pack_f16x2(dev::bf16_lo_f32(w[2]) * f, dev::bf16_hi_f32(w[2]) * f);
+                        v.w = dev::pack_f16x2(dev::bf16_lo_f32(w[3]) * f, dev::bf16_hi_f32(w[3]) * f);
+                    }
                     *reinterpret_cast<uint4 *>(qt + (c / 8) * (kRowTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
                 }
                 tc::fence_async_shared();
@@ -511,6 +599,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (!(ok = wait_bar(bar_s + 8 * buf, sph[buf], gave_up))) break;
                 sph[buf] ^= 1;
                 tc::fence_after();
+                if (KV8 && first) scale = row_scale[(two ? t * kRowTile : 0) + r];
                 const int nv = sg.plen - (sg.tile0 + j) * BN;
                 float mx = kNegInf;
 #pragma unroll

@@ -2,3 +2,4 @@
 #include "pd_prefix_launch.cuh"
 
 PD_INSTANTIATE_PREFIX(256, false)
+PD_INSTANTIATE_PREFIX(256, true)

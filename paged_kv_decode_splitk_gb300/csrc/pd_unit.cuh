@@ -466,7 +466,9 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
         qmax = fmaxf(fmaxf(stats[0], stats[1]), fmaxf(stats[2], stats[3]));
         // qmax < 2^(E - 126) for a normal float with biased exponent E
         const int ex = ((__float_as_int(qmax) >> 23) & 0xff) - 126;
-        const int kq = ex > 15 ? (ex - 15 < 126 ? ex - 15 : 126) : 0;
+        // The own-token mode brings small q up as well (the shared-prefix pass
+        // beside it does): below 2^-14 f16 would lose their bits.
+        const int kq = MODE == kModeOwn ? max(-126, min(126, ex - 15)) : ex > 15 ? (ex - 15 < 126 ? ex - 15 : 126) : 0;
         const float down = __int_as_float((127 - kq) << 23);
         scale_log2 = p.scale_log2 * __int_as_float((127 + kq) << 23);
 #pragma unroll

@@ -122,6 +122,8 @@ _SIGS = {
     "pd_prefix_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "pd_decode_attn_prefix": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _I,
                                    ctypes.c_float, _I, _VP, _SZ, _VP]),
+    "pd_decode_attn_prefix_fp8": (_I, [_VP, _VP, _VP, ctypes.c_float, ctypes.c_float, _VP, _I, _VP, _VP, _I, _VP, _I, _VP,
+                                       _VP, _I, _I, _I, _I, _I, _I, ctypes.c_float, _I, _VP, _SZ, _VP]),
     "pd_rope_frequencies": (_I, [_VP, _VP, _VP]),
     "pd_rope_create": (_I, [_VP, _VP]),
     "pd_rope_destroy": (None, [_VP]),
@@ -357,6 +359,20 @@ def pd_decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_table.data_ptr(), mpb, prefix_lens.data_ptr(),
         _ptr(group_starts), G, block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), out.data_ptr(), S, Hq,
         Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d, num_splits, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def pd_decode_attn_prefix_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, prefix_table, prefix_lens, group_starts,
+                              block_table, context_lens, out, inv_sqrt_d: float, num_splits: int, workspace, stream=None,
+                              num_blocks: int | None = None) -> int:
+    """pd_decode_attn_prefix over an FP8 cache (uint8 E4M3 codes, K = value * k_scale, V = value * v_scale)."""
+    S, Hq, D = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    G, mpb = prefix_table.shape
+    return _check(lib().pd_decode_attn_prefix_fp8(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, prefix_table.data_ptr(), mpb,
+        prefix_lens.data_ptr(), _ptr(group_starts), G, block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
+        out.data_ptr(), S, Hq, Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d, num_splits, _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

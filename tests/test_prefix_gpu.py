@@ -160,11 +160,24 @@ SHAPES = {  # sizes, prefix lengths, own lengths, Hq, Hkv, D, block size, sequen
 }
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("name", SHAPES)
-def test_prefix(name):
+def test_prefix(name, fp8):
     sizes, plens, lens, Hq, Hkv, D, bs, lead, tail = SHAPES[name]
-    b = Batch(sizes, plens, lens, Hq, Hkv, D, bs, lead=lead, tail=tail, seed=len(name))
+    if fp8 and D % 16:
+        pytest.skip("E4M3 caches take head dims of 16")
+    b = Batch(sizes, plens, lens, Hq, Hkv, D, bs, fp8, lead=lead, tail=tail, seed=len(name))
     b.check(b.run(), name)
+
+
+@pytest.mark.parametrize("size", [2.0**-20, 1.0, 2.0**20])
+def test_prefix_fp8_query_sizes(size):
+    """Queries far below and above f16's range over an FP8 cache: the scores stay ordinary through the scale."""
+    for rows in (3, 50):
+        b = Batch([rows], [500], [9] * rows, 8, 2, 128, fp8=True, seed=12, q_scale=size)
+        b.scale /= size
+        b.q[:, 0] = 0
+        b.check(b.run(), f"q of {size}")
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])

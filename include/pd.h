@@ -286,7 +286,8 @@ int pd_decode_attn_noalloc(const void *q, const void *k_cache, const void *v_cac
  *                 are not so raise PD_DEV_BAD_GROUPS and no prefix is read.
  *   block_table, context_lens  of the sequences' own tokens (0 allowed; a
  *                 sequence with neither prefix nor own tokens gets 0).
- *   num_splits    of the own tokens, 1..PD_MAX_DECODE_SPLITS.
+ *   num_splits    the most splits the own tokens are cut into, 1..PD_MAX_DECODE_SPLITS
+ *                 (fewer are used where fewer fill the GPU).
  *   workspace     >= pd_prefix_workspace_bytes(...) bytes, 16-B aligned, always
  *                 needed; contents ignored on entry, scratch on return.
  * The other arguments are pd_decode_attn's, its errors too: a prefix length

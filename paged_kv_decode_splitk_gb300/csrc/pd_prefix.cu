@@ -19,6 +19,7 @@ namespace {
 
 static_assert(kMaxGroups == PD_MAX_PREFIX_GROUPS, "pd.h");
 
+constexpr int kOwnUnits = 152 * 8;  // units of the own-token pass that are enough
 constexpr int kMergeWarps = 8;
 constexpr int kMergeCols = 128;  // columns of a row one warp merges (4 per lane)
 constexpr int kMergeBatch = 8;   // partials whose o are loaded together
@@ -56,17 +57,25 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const __
     dev::griddep_wait();
 
     // ---- the row's group: the last one that begins at or before the sequence ----
-    int below = 0;
-    for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-        const int g = g0 + lane;
-        below += __popc(__ballot_sync(0xffffffffu, g < p.num_groups && p.plan_groups[g].first_seq <= s));
-    }
-    const long long W = *p.plan_total;
     int L = p.context_lens[s];
+    const long long W = *p.plan_total;
+    GroupPlan g = {};
+    for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
+        GroupPlan mine = {};
+        if (g0 + lane < p.num_groups) mine = p.plan_groups[g0 + lane];
+        const int below = __popc(__ballot_sync(0xffffffffu, g0 + lane < p.num_groups && mine.first_seq <= s));
+        if (below == 0) break;
+        const int src = below - 1;
+        g.first_unit = __shfl_sync(0xffffffffu, mine.first_unit, src);
+        g.first_item = __shfl_sync(0xffffffffu, mine.first_item, src);
+        g.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
+        g.first_seq = __shfl_sync(0xffffffffu, mine.first_seq, src);
+        g.rows = __shfl_sync(0xffffffffu, mine.rows, src);
+        g.blocks = __shfl_sync(0xffffffffu, mine.blocks, src);
+    }
     int nparts = 0, halves = 1;    // prefix slots of the row; halves of a slot it has
     long long first = 0;           // (slot, row) of its first partial
-    if (below > 0 && W > 0) {
-        const GroupPlan g = p.plan_groups[below - 1];
+    if (W > 0) {
         const int x = (s - g.first_seq) * p.group + (h - kvh * p.group);
         if (g.tiles > 0 && x < g.rows) {
             const int block = x / BR, r = x - block * BR;
@@ -99,40 +108,46 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const __
         return p.part_o + ((sl * (p.dpad / 8) + d0 / 8) * BR + r) * 8 + (d0 & 4);
     };
 
-    // ---- the largest reference ----
-    float M = kNegInf;
-    for (int i = lane; i < total; i += 32) {
-        const float2 v = *reinterpret_cast<const float2 *>(ml_of(i));
-        if (v.y != 0.f) M = fmaxf(M, v.x);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-
-    // ---- the fold ----
-    float lsum = 0.f;
+    // ---- the fold, 32 partials at a time: lane i has (m, l) of partial i ----
+    float M = kNegInf, lsum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < total; i0 += 32) {
-        float2 v = make_float2(kNegInf, 0.f);
-        if (i0 + lane < total) v = *reinterpret_cast<const float2 *>(ml_of(i0 + lane));
-        // a partial without a token has l = 0 and its o was not written
-        const float w = v.y != 0.f ? dev::exp2_approx(v.x - M) : 0.f;
-        const float wl = v.y != 0.f ? w * v.y : 0.f;
-        const float wo = i0 + lane < nparts ? w * p.v_scale : w;
-        const bool dead = v.y == 0.f;
         const int n = min(32, total - i0);
-        for (int j0 = 0; j0 < n; j0 += kMergeBatch) {
-            float4 o[kMergeBatch];
+        float2 v = make_float2(kNegInf, 0.f);
+        if (lane < n) v = *reinterpret_cast<const float2 *>(ml_of(i0 + lane));
+        float4 o[kMergeBatch];
 #pragma unroll
-            for (int j = 0; j < kMergeBatch; ++j)
-                o[j] = cols && j0 + j < n ? *reinterpret_cast<const float4 *>(o_of(i0 + j0 + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < kMergeBatch; ++j)  // (asked for together with m and l)
+            o[j] = cols && j < n ? *reinterpret_cast<const float4 *>(o_of(i0 + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        // a partial without a token has l = 0, and its o was not written
+        const bool dead = v.y == 0.f;
+        float top = dead ? kNegInf : v.x;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float Mn = fmaxf(M, top);
+        const float keep = M == kNegInf ? 0.f : dev::exp2_approx(M - Mn);
+        M = Mn;
+        const float w = dead ? 0.f : dev::exp2_approx(v.x - M);
+        float wl = dead ? 0.f : w * v.y;
+        const float wo = i0 + lane < nparts ? w * p.v_scale : w;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
+        lsum = lsum * keep + wl;
+        acc.x *= keep;
+        acc.y *= keep;
+        acc.z *= keep;
+        acc.w *= keep;
+        for (int j0 = 0; j0 < n; j0 += kMergeBatch) {
+            if (j0 > 0) {
+#pragma unroll
+                for (int j = 0; j < kMergeBatch; ++j)
+                    o[j] = cols && j0 + j < n ? *reinterpret_cast<const float4 *>(o_of(i0 + j0 + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
 #pragma unroll
             for (int j = 0; j < kMergeBatch; ++j) {
-                const int src = (j0 + j) & 31;
-                const float wj = __shfl_sync(0xffffffffu, wo, src);
-                const float lj = __shfl_sync(0xffffffffu, wl, src);
-                const bool skip = __shfl_sync(0xffffffffu, dead, src) || j0 + j >= n;
-                if (!skip) {
-                    lsum += lj;
+                const float wj = __shfl_sync(0xffffffffu, wo, (j0 + j) & 31);
+                const bool skip = __shfl_sync(0xffffffffu, dead, (j0 + j) & 31);
+                if (j0 + j < n && !skip) {
                     acc.x = fmaf(o[j].x, wj, acc.x);
                     acc.y = fmaf(o[j].y, wj, acc.y);
                     acc.z = fmaf(o[j].z, wj, acc.z);
@@ -239,6 +254,13 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
         return report(PD_ERR_INVALID, "%s: max_prefix_blocks * block_size overflows int32", what);
     if (static_cast<long long>(num_seqs) * num_q_heads > 0x7fffffffLL - 256)
         return report(PD_ERR_INVALID, "%s: launch too large (%d sequences)", what, num_seqs);
+    // num_splits is the most the own tokens are cut into.  A split has at least
+    // PD_MIN_KV_PER_SPLIT tokens, so a table holds no more than `fit` of them; and
+    // once units fill the GPU several times, more only add partials to fold.
+    const int fit = (max_blocks * static_cast<long long>(block_size) + PD_MIN_KV_PER_SPLIT - 1) / PD_MIN_KV_PER_SPLIT;
+    const long long units = static_cast<long long>(num_seqs) * num_kv_heads;
+    const long long fill = (kOwnUnits + units - 1) / units;
+    num_splits = static_cast<int>(std::max(1ll, std::min(static_cast<long long>(num_splits), std::min<long long>(fit, fill))));
     const Layout lay = layout_of(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, num_splits);
     if (lay.max_items > 0x7fffffffLL - kMaxCtas) return report(PD_ERR_INVALID, "%s: launch too large", what);
     if (!workspace || workspace_bytes < lay.end)

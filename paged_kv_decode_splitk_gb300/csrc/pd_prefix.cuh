@@ -48,6 +48,7 @@ namespace pd {
 namespace prefix {
 
 constexpr int kRowTile = 128;   // rows of one MMA
+constexpr int kBoundThreads = 512;  // (for 128 registers a thread: 384 threads leave a quarter of them free)
 constexpr int kRegionBars = 32;
 constexpr int kConverters = 64;  // threads that turn FP8 tiles into f16 ones
 
@@ -198,7 +199,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <int DPAD, bool KV8>
-__global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
+__global__ void __launch_bounds__(kBoundThreads, 1)
     prefix_kernel(const __grid_constant__ KvMaps<1> maps, const __grid_constant__ PrefixParams p) {
     using L = Plan<DPAD, KV8>;
     constexpr int BN = L::kTile;
@@ -301,16 +302,19 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
             const int32_t *ids = p.prefix_table + static_cast<long long>(sg.group) * p.max_prefix_blocks;
             const int ahead = ONE || !sg.two ? 2 : 1;
-            auto load = [&](bool is_v, int j) {
+            // this lane's box of tile j: its block id (past the prefix, or bad: one
+            // outside the cache, which reads zeros), asked for two tiles ahead
+            auto id_of = [&](int j) -> int {
+                const int tok = (sg.tile0 + j) * BN + chunk * kTileTokens;
+                if (lane >= NBOX || j >= sg.n || tok >= sg.plen) return p.num_blocks;
+                return __ldg(ids + fast_div(tok, p.block_size));
+            };
+            auto load = [&](bool is_v, int j, int id) {
                 const int tok = (sg.tile0 + j) * BN + chunk * kTileTokens;
                 const int blk = fast_div(tok, p.block_size);
-                int id = p.num_blocks;  // past the prefix: zeros
-                if (lane < NBOX && tok < sg.plen) {
-                    id = __ldg(ids + blk);
-                    if (id < 0 || id >= p.num_blocks) {
-                        dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
-                        id = p.num_blocks;
-                    }
+                if (id < 0 || id > p.num_blocks || (id == p.num_blocks && lane < NBOX && tok < sg.plen)) {
+                    dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
+                    id = p.num_blocks;
                 }
                 if (!wait_bar(empty + 8 * st, ph ^ 1, gave_up)) return false;
                 const uint32_t dst = stage0 + st * BYTES;
@@ -347,10 +351,15 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 }
                 return true;
             };
+            int id_last = 0, id_now = id_of(0), id_next = id_of(1);
             for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
-                if (i < sg.n) ok = load(false, i);
+                const int id_after = id_of(i + 2);
+                if (i < sg.n) ok = load(false, i, id_now);
                 const int v = i - ahead + 1;
-                if (ok && v >= 0) ok = load(true, v);
+                if (ok && v >= 0) ok = load(true, v, ahead == 1 ? id_now : id_last);
+                id_last = id_now;
+                id_now = id_next;
+                id_next = id_after;
             }
         }
         if (!ok && lane == 0) {
@@ -601,13 +610,35 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 tc::fence_after();
                 if (KV8 && first) scale = row_scale[(two ? t * kRowTile : 0) + r];
                 const int nv = sg.plen - (sg.tile0 + j) * BN;
+                // -- the largest score of the tile's live tokens.  S is read from TMEM
+                // twice (for the maximum, then for the weights), 32 columns at a
+                // time with the next 32 on their way, which leaves registers for
+                // a CTA of the own-token pass beside this one.
+                uint32_t xa[32], xb[32];
+                tc::ld_32x32(ts, xa);
                 float mx = kNegInf;
+                auto largest = [&](const uint32_t (&x)[32], int c) {
+                    float m0 = kNegInf, m1 = kNegInf;
+                    if (nv - c >= 32) {
 #pragma unroll
-                for (int c = 0; c < BN; c += 32) {
-                    uint32_t x[32];
-                    tc::ld_32x32(ts + c, x);
+                        for (int i = 0; i < 32; i += 4) {
+                            m0 = fmaxf(fmaxf(m0, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                            m1 = fmaxf(fmaxf(m1, __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
+                        }
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, c + i < nv ? __uint_as_float(x[i]) : kNegInf);
+                        for (int i = 0; i < 32; ++i) m0 = fmaxf(m0, c + i < nv ? __uint_as_float(x[i]) : kNegInf);
+                    }
+                    mx = fmaxf(mx, fmaxf(m0, m1));
+                };
+#pragma unroll
+                for (int c = 0; c < BN; c += 64) {
+                    tc::wait_ld(xa);
+                    tc::ld_32x32(ts + c + 32, xb);
+                    largest(xa, c);
+                    tc::wait_ld(xb);
+                    tc::ld_32x32(ts + (c + 64) % BN, xa);  // in the end the first columns again
+                    largest(xb, c + 32);
                 }
                 mx *= scale;
                 const float m_old = m;
@@ -626,6 +657,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     for (int c = 0; c < DPAD; c += 32) {
                         uint32_t x[32];
                         tc::ld_32x32(to + c, x);
+                        tc::wait_ld(x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
                         tc::st_32x32(to + c, x);
@@ -633,30 +665,40 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 }
                 first = false;
                 const float off = m == kNegInf ? 0.f : m;
-                float sum = 0.f;
-                // (P of 64 columns goes over S columns that both passes have read)
-                uint32_t pk[BN / 2];
-#pragma unroll
-                for (int c = 0; c < BN; c += 32) {
-                    uint32_t x[32];
-                    tc::ld_32x32(ts + c, x);
+                // -- the weights; P goes over S columns that were read before it
+                const uint64_t scale2 = tc::pack_f32x2(scale, scale), off2 = tc::pack_f32x2(-off, -off);
+                uint64_t sum2 = 0;
+                auto weigh = [&](const uint32_t (&x)[32], int c) {
+                    uint32_t pk[16];
+                    const bool whole = nv - c >= 32;
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        const float a = __uint_as_float(x[i]), b = __uint_as_float(x[i + 1]);
-                        const float ea = c + i < nv ? dev::exp2_approx(fmaf(a, scale, -off)) : 0.f;
-                        const float eb = c + i + 1 < nv ? dev::exp2_approx(fmaf(b, scale, -off)) : 0.f;
-                        sum += ea + eb;
-                        pk[(c + i) / 2] = pack2<KV8>(ea, eb);
+                        float ea, eb;
+                        tc::unpack_f32x2(tc::fma_f32x2(tc::pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2),
+                                         ea, eb);
+                        ea = dev::exp2_approx(ea);
+                        eb = dev::exp2_approx(eb);
+                        if (!whole) {
+                            ea = c + i < nv ? ea : 0.f;
+                            eb = c + i + 1 < nv ? eb : 0.f;
+                        }
+                        sum2 = tc::add_f32x2(sum2, tc::pack_f32x2(ea, eb));
+                        pk[i / 2] = pack2<KV8>(ea, eb);
                     }
-                }
-                l += sum;
+                    tc::st_32x16(ts + c / 2, pk);
+                };
 #pragma unroll
-                for (int c = 0; c < BN / 2; c += 32) {
-                    uint32_t x[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = pk[c + i];
-                    tc::st_32x32(ts + c, x);
+                for (int c = 0; c < BN; c += 64) {
+                    tc::wait_ld(xa);
+                    tc::ld_32x32(ts + c + 32, xb);
+                    weigh(xa, c);
+                    tc::wait_ld(xb);
+                    if (c + 64 < BN) tc::ld_32x32(ts + c + 64, xa);
+                    weigh(xb, c + 32);
                 }
+                float sa, sb;
+                tc::unpack_f32x2(sum2, sa, sb);
+                l += sa + sb;
                 tc::wait_st();
                 tc::fence_before();
                 arrive(bar_p + 8 * buf);
@@ -676,6 +718,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 for (int c = 0; c < DPAD; c += 32) {
                     uint32_t x[32];
                     tc::ld_32x32(to + c, x);
+                    tc::wait_ld(x);
                     if (live) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)

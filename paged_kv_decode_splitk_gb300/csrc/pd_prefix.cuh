@@ -6,7 +6,8 @@
 // their scores are one matrix product, S = Q K^T, and their outputs another,
 // O = exp2(S - m) V.  Per segment (a row block of up to 256 rows, a KV head, a
 // run of key tiles) the pass writes each row's partial in base 2,
-//   m  a reference (the largest score so far, or up to 8 below it),
+//   m  a reference (the largest score of the row's first tile, raised by whole
+//      numbers when weights pass 2^15),
 //   l = sum_t 2^(x_t - m),  o = sum_t 2^(x_t - m) V[t],   x_t = q.K[t] scale log2(e),
 // which the merge folds with the other segments' and with the partials of the
 // sequence's own tokens.
@@ -22,8 +23,9 @@
 //     swizzle).  One warp issues tcgen05.mma: S (128 rows x kTile tokens) from
 //     shared memory into TMEM, O += P V with P read from TMEM.  Two groups of
 //     four warps do the softmax, a thread per row, S read from and P (BF16)
-//     written back to TMEM over it; a row's O is rescaled in TMEM only when its
-//     maximum passes its reference by more than 8.
+//     written back to TMEM over it.  The reference need not be the maximum, so
+//     after the first tile none is taken: an exponential, half a multiply-add,
+//     half an add and half a conversion per score is all there is.
 //   * Two streams keep the tensor core and the softmax both busy: with more than
 //     128 rows each stream has 128 of them and both use every tile; with fewer,
 //     the streams take the tiles in turn (each its own O), and the merge folds
@@ -196,6 +198,69 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 template <bool KV8>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return KV8 ? dev::pack_f16x2(lo, hi) : dev::pack_bf16x2(lo, hi);
+}
+
+// Sum of 32 weights above which a row's reference is raised.
+constexpr float kLift = 32768.f;
+
+// The largest of a row's scores in columns [c, BN), live ones (below nv) only.
+template <int BN>
+__device__ __forceinline__ float largest_score(uint32_t ts, int c, int nv) {
+    const float kNegInf = -__int_as_float(0x7f800000);
+    float mx = kNegInf;
+#pragma unroll 1
+    for (; c < BN; c += 32) {
+        uint32_t x[32];
+        tc::ld_32x32(ts + c, x);
+        tc::wait_ld(x);
+        float m0 = kNegInf, m1 = kNegInf;
+        if (nv - c >= 32) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                m0 = fmaxf(fmaxf(m0, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                m1 = fmaxf(fmaxf(m1, __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m0 = fmaxf(m0, c + i < nv ? __uint_as_float(x[i]) : kNegInf);
+        }
+        mx = fmaxf(mx, fmaxf(m0, m1));
+    }
+    return mx;
+}
+
+// Raises the references of the rows that ask for it above every score in
+// columns [c, BN), by a whole number, and scales what was weighed against the
+// old ones (l, O, and this tile's P of the columns before c) by that power of two.
+template <int BN, int DPAD, bool KV8>
+__device__ __forceinline__ void raise_reference(uint32_t ts, uint32_t to, int c, int nv, float scale, bool over, float &m,
+                                                float &l) {
+    const float d = largest_score<BN>(ts, c, nv) * scale - m;
+    const float k = over && d > 0.f ? ceilf(d) : 0.f;
+    const float f = k < 127.f ? __int_as_float((127 - static_cast<int>(k)) << 23) : 0.f;
+    m += k;
+    l *= f;
+#pragma unroll 1
+    for (int i = 0; i < DPAD; i += 32) {
+        uint32_t x[32];
+        tc::ld_32x32(to + i, x);
+        tc::wait_ld(x);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+        tc::st_32x32(to + i, x);
+    }
+#pragma unroll 1
+    for (int i = 0; i < c / 2; i += 16) {
+        uint32_t x[32];  // (16 columns of P; the 16 behind them are read along)
+        tc::ld_32x32(ts + i, x);
+        tc::wait_ld(x);
+        uint32_t y[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            y[e] = KV8 ? dev::pack_f16x2(dev::f16_lo_f32(x[e]) * f, dev::f16_hi_f32(x[e]) * f)
+                       : dev::pack_bf16x2(dev::bf16_lo_f32(x[e]) * f, dev::bf16_hi_f32(x[e]) * f);
+        tc::st_32x16(ts + i, y);
+    }
 }
 
 template <int DPAD, bool KV8>
@@ -557,7 +622,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             if (two || t == 0) {
                 uint8_t *qt = smem + L::q + t * (kRowTile * DPAD * 2);
                 constexpr int STEPS = CHUNKS;  // 32 rows x CHUNKS chunks over 32 lanes
-#pragma unroll 4
+#pragma unroll 8
                 for (int i = 0; i < STEPS; ++i) {
                     const int e = i * 32 + lane;
                     const int row = (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;
@@ -610,84 +675,64 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                 tc::fence_after();
                 if (KV8 && first) scale = row_scale[(two ? t * kRowTile : 0) + r];
                 const int nv = sg.plen - (sg.tile0 + j) * BN;
-                // -- the largest score of the tile's live tokens.  S is read from TMEM
-                // twice (for the maximum, then for the weights), 32 columns at a
-                // time with the next 32 on their way, which leaves registers for
-                // a CTA of the own-token pass beside this one.
-                uint32_t xa[32], xb[32];
-                tc::ld_32x32(ts, xa);
-                float mx = kNegInf;
-                auto largest = [&](const uint32_t (&x)[32], int c) {
-                    float m0 = kNegInf, m1 = kNegInf;
-                    if (nv - c >= 32) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            m0 = fmaxf(fmaxf(m0, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-                            m1 = fmaxf(fmaxf(m1, __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) m0 = fmaxf(m0, c + i < nv ? __uint_as_float(x[i]) : kNegInf);
-                    }
-                    mx = fmaxf(mx, fmaxf(m0, m1));
-                };
-#pragma unroll
-                for (int c = 0; c < BN; c += 64) {
-                    tc::wait_ld(xa);
-                    tc::ld_32x32(ts + c + 32, xb);
-                    largest(xa, c);
-                    tc::wait_ld(xb);
-                    tc::ld_32x32(ts + (c + 64) % BN, xa);  // in the end the first columns again
-                    largest(xb, c + 32);
+                // -- A row's reference m is the largest score of its first tile; after
+                // that no maximum is taken: weights may be as large as kLift, and
+                // only when a row's weights of 32 columns sum to more does its warp
+                // look at the scores again and raise m (by a whole number, so that
+                // P, l and O are scaled exactly).  FP32 and BF16 hold such weights as
+                // exactly as weights below 1; kLift is what f16 holds.
+                if (__any_sync(0xffffffffu, m == kNegInf)) {
+                    const float mx = largest_score<BN>(ts, 0, nv) * scale;
+                    m = m == kNegInf ? mx : m;
                 }
-                mx *= scale;
-                const float m_old = m;
-                if (mx > m + 8.f || first) m = mx;
-                const float alpha = first ? 1.f : dev::exp2_approx(m_old - m);
-                const bool move = !first && m != m_old;
-                if (ONE && !first) {
-                    // the last product onto O has to be done before O is touched or added to
-                    if (!(ok = wait_bar(bar_o, oph, gave_up))) break;
-                    oph ^= 1;
-                    tc::fence_after();
-                }
-                if (__any_sync(0xffffffffu, move)) {
-                    l *= alpha;
-#pragma unroll 1
-                    for (int c = 0; c < DPAD; c += 32) {
-                        uint32_t x[32];
-                        tc::ld_32x32(to + c, x);
-                        tc::wait_ld(x);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
-                        tc::st_32x32(to + c, x);
-                    }
-                }
+                bool waited = !ONE || first;  // the last product onto O is known to be done
                 first = false;
-                const float off = m == kNegInf ? 0.f : m;
-                // -- the weights; P goes over S columns that were read before it
-                const uint64_t scale2 = tc::pack_f32x2(scale, scale), off2 = tc::pack_f32x2(-off, -off);
-                uint64_t sum2 = 0;
+                float off = m == kNegInf ? 0.f : m;
+                bool lifted = false;
+                const uint64_t scale2 = tc::pack_f32x2(scale, scale);
                 auto weigh = [&](const uint32_t (&x)[32], int c) {
                     uint32_t pk[16];
-                    const bool whole = nv - c >= 32;
+                    float sa, sb;
+                    auto compute = [&] {
+                        const bool whole = nv - c >= 32;
+                        const uint64_t off2 = tc::pack_f32x2(-off, -off);
+                        uint64_t sum2 = 0;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float ea, eb;
-                        tc::unpack_f32x2(tc::fma_f32x2(tc::pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2),
-                                         ea, eb);
-                        ea = dev::exp2_approx(ea);
-                        eb = dev::exp2_approx(eb);
-                        if (!whole) {
-                            ea = c + i < nv ? ea : 0.f;
-                            eb = c + i + 1 < nv ? eb : 0.f;
+                        for (int i = 0; i < 32; i += 2) {
+                            float ea, eb;
+                            tc::unpack_f32x2(
+                                tc::fma_f32x2(tc::pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2), ea, eb);
+                            ea = dev::exp2_approx(ea);
+                            eb = dev::exp2_approx(eb);
+                            if (!whole) {
+                                ea = c + i < nv ? ea : 0.f;
+                                eb = c + i + 1 < nv ? eb : 0.f;
+                            }
+                            sum2 = tc::add_f32x2(sum2, tc::pack_f32x2(ea, eb));
+                            pk[i / 2] = pack2<KV8>(ea, eb);
                         }
-                        sum2 = tc::add_f32x2(sum2, tc::pack_f32x2(ea, eb));
-                        pk[i / 2] = pack2<KV8>(ea, eb);
+                        tc::unpack_f32x2(sum2, sa, sb);
+                    };
+                    compute();
+                    const bool over = !(sa + sb <= kLift);
+                    if (!lifted && __any_sync(0xffffffffu, over)) {
+                        lifted = true;
+                        if (!waited) {
+                            ok = wait_bar(bar_o, oph, gave_up);
+                            oph ^= 1;
+                            waited = true;
+                        }
+                        tc::fence_after();
+                        raise_reference<BN, DPAD, KV8>(ts, to, c, nv, scale, over, m, l);
+                        off = m == kNegInf ? 0.f : m;
+                        compute();
                     }
-                    tc::st_32x16(ts + c / 2, pk);
+                    l += sa + sb;
+                    tc::st_32x16(ts + c / 2, pk);  // over S columns that were read before
                 };
-#pragma unroll
+                uint32_t xa[32], xb[32];
+                tc::ld_32x32(ts, xa);
+#pragma unroll 1
                 for (int c = 0; c < BN; c += 64) {
                     tc::wait_ld(xa);
                     tc::ld_32x32(ts + c + 32, xb);
@@ -696,9 +741,11 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                     if (c + 64 < BN) tc::ld_32x32(ts + c + 64, xa);
                     weigh(xb, c + 32);
                 }
-                float sa, sb;
-                tc::unpack_f32x2(sum2, sa, sb);
-                l += sa + sb;
+                if (ONE && !waited) {  // (each phase of the barrier is waited for, in order)
+                    ok = wait_bar(bar_o, oph, gave_up) && ok;
+                    oph ^= 1;
+                }
+                if (!ok) break;
                 tc::wait_st();
                 tc::fence_before();
                 arrive(bar_p + 8 * buf);

@@ -127,11 +127,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 // else), so repeated launches over the same cache skip the host-side encode.
 struct KvMapKey {
     const void *base;
-    int head_dim, block_size, num_kv_heads, elem, box_cols, swz128;
+    int head_dim, block_size, num_kv_heads, elem, box_cols, swz128, box_tokens;
     long long num_blocks, blk_stride, tok_stride, kvh_stride;
     bool operator==(const KvMapKey &o) const {
         return base == o.base && head_dim == o.head_dim && block_size == o.block_size &&
                num_kv_heads == o.num_kv_heads && elem == o.elem && box_cols == o.box_cols && swz128 == o.swz128 &&
+               box_tokens == o.box_tokens &&
                num_blocks == o.num_blocks && blk_stride == o.blk_stride && tok_stride == o.tok_stride &&
                kvh_stride == o.kvh_stride;
     }
@@ -150,17 +151,18 @@ unsigned long long g_map_clock = 0;
 int encode_kv_map_uncached(CUtensorMap *map, int *tok_dim, const void *base, int head_dim,
                            int block_size, int num_kv_heads, long long num_blocks,
                            long long blk_stride, long long tok_stride, long long kvh_stride, int elem,
-                           int box_cols, int swz128);
+                           int box_cols, int swz128, int box_tokens);
 
 // 4-D tensor map of a K or V view (strides in elements), boxes of box_cols
-// columns x 16 tokens.  elem 2: BF16, 64 columns with the 128-byte swizzle;
+// columns x box_tokens (16) tokens.  elem 2: BF16, 64 columns with the 128-byte swizzle;
 // elem 1: FP8 E4M3 codes, either 128 columns with the 128-byte swizzle (the K
 // operand read straight from the tile) or one unswizzled box of the padded head
 // dim (V, converted to f16 first; every FP8 tile at head dim 64).
 int encode_kv_map(CUtensorMap *map, int *tok_dim, const void *base, int head_dim, int block_size,
                   int num_kv_heads, long long num_blocks, long long blk_stride, long long tok_stride,
-                  long long kvh_stride, int elem = 2, int box_cols = pd::kBoxCols, int swz128 = 1) {
-    const KvMapKey key = {base, head_dim, block_size, num_kv_heads, elem, box_cols, swz128, num_blocks,
+                  long long kvh_stride, int elem = 2, int box_cols = pd::kBoxCols, int swz128 = 1,
+                  int box_tokens = pd::kTileTokens) {
+    const KvMapKey key = {base, head_dim, block_size, num_kv_heads, elem, box_cols, swz128, box_tokens, num_blocks,
                           blk_stride, tok_stride, kvh_stride};
     std::lock_guard<std::mutex> lock(g_map_mu);
     int victim = 0;
@@ -174,7 +176,7 @@ int encode_kv_map(CUtensorMap *map, int *tok_dim, const void *base, int head_dim
         if (g_maps[i].stamp < g_maps[victim].stamp) victim = i;
     }
     int rc = encode_kv_map_uncached(map, tok_dim, base, head_dim, block_size, num_kv_heads, num_blocks,
-                                    blk_stride, tok_stride, kvh_stride, elem, box_cols, swz128);
+                                    blk_stride, tok_stride, kvh_stride, elem, box_cols, swz128, box_tokens);
     if (rc != PD_OK) return rc;
     g_maps[victim].key = key;
     g_maps[victim].map = *map;
@@ -186,7 +188,7 @@ int encode_kv_map(CUtensorMap *map, int *tok_dim, const void *base, int head_dim
 int encode_kv_map_uncached(CUtensorMap *map, int *tok_dim, const void *base, int head_dim,
                            int block_size, int num_kv_heads, long long num_blocks,
                            long long blk_stride, long long tok_stride, long long kvh_stride, int elem,
-                           int box_cols, int swz128) {
+                           int box_cols, int swz128, int box_tokens) {
     auto enc = encoder();
     if (!enc) return cuda_fail(g_encode_err, "cuTensorMapEncodeTiled entry point");
     const bool tok_first = tok_stride <= kvh_stride;
@@ -199,7 +201,7 @@ int encode_kv_map_uncached(CUtensorMap *map, int *tok_dim, const void *base, int
     if (tok_first) {
         dims[1] = block_size;
         strides[0] = static_cast<cuuint64_t>(tok_stride) * elem;
-        box[1] = pd::kTileTokens;
+        box[1] = static_cast<cuuint32_t>(box_tokens);
         dims[2] = num_kv_heads;
         strides[1] = static_cast<cuuint64_t>(kvh_stride) * elem;
         box[2] = 1;
@@ -209,7 +211,7 @@ int encode_kv_map_uncached(CUtensorMap *map, int *tok_dim, const void *base, int
         box[1] = 1;
         dims[2] = block_size;
         strides[1] = static_cast<cuuint64_t>(tok_stride) * elem;
-        box[2] = pd::kTileTokens;
+        box[2] = static_cast<cuuint32_t>(box_tokens);
     }
     dims[3] = static_cast<cuuint64_t>(num_blocks);
     strides[2] = static_cast<cuuint64_t>(blk_stride) * elem;
@@ -667,9 +669,13 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
     if (pd::unit_smem_bytes(dpad, rows, stages_seq, kv8) > max_smem_optin()) stages_seq = stages;
     const bool hl = !packed && G <= 4;
     if (own) {
-        view->k = tk;
-        view->v = tv;
-        view->tok_dim = tok_dim;
+        const void *caches[2] = {k_cache, v_cache};
+        CUtensorMap *wide[2] = {&view->k, &view->v};
+        for (int i = 0; i < 2; ++i) {
+            rc = encode_kv_map(wide[i], &view->tok_dim, caches[i], head_dim, block_size, num_kv_heads, num_blocks, blk_s, tok_s,
+                               kvh_s, elem, box_k, !kv8 || k_direct, view->box_tokens);
+            if (rc != PD_OK) return rc;
+        }
         const cudaError_t e = kv8 ? dispatch_unit<pd::kModeOwn, true>(dpad, gn, hl, false, &tk, &tv, p, units, stages_seq, st)
                                   : dispatch_unit<pd::kModeOwn, false>(dpad, gn, hl, false, &tk, &tv, p, units, stages_seq, st);
         if (e != cudaSuccess) return cuda_fail(e, "own-token pass launch");

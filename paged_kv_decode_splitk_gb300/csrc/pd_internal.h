@@ -159,17 +159,18 @@ struct MergeParams {
     FastDiv fd_hq, fd_split, fd_bs;  // num_q_heads, num_splits, block_size
 };
 
-// The tensor maps of a paged cache's K and V (tok_dim: the map dimension of the
-// token coordinate).
+// The tensor maps of a paged cache's K and V with boxes of box_tokens tokens
+// (tok_dim: the map dimension of the token coordinate).
 struct KvView {
     CUtensorMap k, v;
     int tok_dim;
+    int box_tokens;
 };
 
 // The own-token pass of pd_decode_attn_prefix (pd_api.cu): pd_decode_attn's
 // checks and its partial pass over every split, each non-empty split's (o, m, l)
 // written to own_o [rows, N, D] and own_ml [rows, N, 2]; no merge, `out` only
-// checked.  *view receives the maps it read through.
+// checked.  *view receives maps of the same cache with view->box_tokens tokens a box.
 int launch_own_partials(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
                         int max_blocks_per_seq, const int32_t *context_lens, void *out, int num_seqs,
                         int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,

@@ -274,6 +274,8 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     // The sequences' own tokens: the unit kernel over every split, always as
     // partials (this also checks the tensors both passes read).
     KvView view;
+    view.box_tokens = 16;  // as many as divide a block and a tile: fewer, larger boxes
+    while (view.box_tokens < tile_tokens(dpad_of(head_dim)) && block_size % (2 * view.box_tokens) == 0) view.box_tokens *= 2;
     rc = launch_own_partials(q, k_cache, v_cache, block_table, max_blocks, context_lens, out, num_seqs, num_q_heads,
                              num_kv_heads, head_dim, block_size, num_blocks, inv_sqrt_d, num_splits, own_o, own_ml, stream,
                              kv8, k_scale, v_scale, &view);
@@ -302,6 +304,7 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     p.block_size = make_fastdiv(block_size);
     p.fd_group = make_fastdiv(group);
     p.tok_dim = view.tok_dim;
+    p.box_tokens = view.box_tokens;
     p.scale_log2 = static_cast<float>(std::fabs(scale));
     p.negative = scale < 0;
     p.max_items = static_cast<int>(lay.max_items);

@@ -18,8 +18,8 @@
 //     SM gets the same number of tiles whatever the shapes, and a CTA's partial
 //     of item i goes to slot i + c (item and CTA both only grow along the line,
 //     so slots are distinct, and at most items + C).
-//   * One warp loads: K and V tiles by TMA boxes of 16 tokens x 64 columns,
-//     gathered through the group's block table into a ring of tiles (128-byte
+//   * One warp loads: K and V tiles by TMA boxes of 64 columns x as many
+//     tokens as lie together in a cache block (16 to a whole tile), gathered through the group's block table into a ring of tiles (128-byte
 //     swizzle).  One warp issues tcgen05.mma: S (128 rows x kTile tokens) from
 //     shared memory into TMEM, O += P V with P read from TMEM.  Two groups of
 //     four warps do the softmax, a thread per row, S read from and P (BF16)
@@ -350,9 +350,9 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
 
     if (warp == 0) {
         // ---- loads: K and V tiles in the order the products take them ------------
-        constexpr int NCH = BN / kTileTokens;                // 16-token boxes of a tile
         constexpr int COLS = KV8 ? (DPAD < 128 ? DPAD : 128) : kBoxCols;  // columns of a box
-        constexpr int NBOX = NCH * (DPAD / COLS);
+        const int CT = p.box_tokens;                         // tokens of a box
+        const int NCH = BN / CT, NBOX = NCH * (DPAD / COLS);
         constexpr int DEPTH = KV8 ? L::kRawStages : NST;
         constexpr int BYTES = KV8 ? L::kRawBytes : L::kStageBytes;
         const uint32_t full = KV8 ? bar_rfull : bar_full, empty = KV8 ? bar_rempty : bar_empty;
@@ -370,12 +370,12 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             // this lane's box of tile j: its block id (past the prefix, or bad: one
             // outside the cache, which reads zeros), asked for two tiles ahead
             auto id_of = [&](int j) -> int {
-                const int tok = (sg.tile0 + j) * BN + chunk * kTileTokens;
+                const int tok = (sg.tile0 + j) * BN + chunk * CT;
                 if (lane >= NBOX || j >= sg.n || tok >= sg.plen) return p.num_blocks;
                 return __ldg(ids + fast_div(tok, p.block_size));
             };
             auto load = [&](bool is_v, int j, int id) {
-                const int tok = (sg.tile0 + j) * BN + chunk * kTileTokens;
+                const int tok = (sg.tile0 + j) * BN + chunk * CT;
                 const int blk = fast_div(tok, p.block_size);
                 if (id < 0 || id > p.num_blocks || (id == p.num_blocks && lane < NBOX && tok < sg.plen)) {
                     dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
@@ -387,13 +387,13 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                 // A tile's box of live and dead tokens holds whatever the cache's
                 // slots past the prefix hold; a dead V row must not reach the
                 // product (0 x NaN), so those rows are zeroed before it is handed on.
-                const bool tail = !KV8 && is_v && nv < BN && (nv & (kTileTokens - 1));
+                const bool tail = !KV8 && is_v && nv < BN && (nv & (CT - 1));
                 const uint32_t bar = tail ? bar_tail : full + 8 * st;
                 if (lane == 0) dev::mbar_arrive_expect_tx(bar, BYTES);
                 __syncwarp();
                 if (lane < NBOX) {
                     const int sub = tok - blk * bs;
-                    dev::tma_load_4d(dst + col * (BN * (KV8 ? COLS : 128)) + chunk * (kTileTokens * (KV8 ? COLS : 128)),
+                    dev::tma_load_4d(dst + col * (BN * (KV8 ? COLS : 128)) + chunk * (CT * (KV8 ? COLS : 128)),
                                      is_v ? &maps.v[0] : &maps.k[0], bar, col * COLS, p.tok_dim == 1 ? sub : sg.kvh,
                                      p.tok_dim == 1 ? sg.kvh : sub, id, policy);
                 }
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                     if (!wait_bar(bar_tail, tail_ph, gave_up)) return false;
                     tail_ph ^= 1;
                     uint8_t *tile = smem + L::ring + st * BYTES;
-                    const int end = (nv + kTileTokens - 1) / kTileTokens * kTileTokens;
+                    const int end = (nv + CT - 1) & ~(CT - 1);
                     for (int b = 0; b < DPAD / 64; ++b)
                         for (int i = nv * 8 + lane; i < end * 8; i += 32)
                             *reinterpret_cast<uint4 *>(tile + b * (BN * 128) + i * 16) = make_uint4(0, 0, 0, 0);

@@ -34,6 +34,7 @@ struct PrefixParams {
     int num_seqs, num_q_heads, num_kv_heads, group, head_dim;
     FastDiv block_size, fd_group;
     int tok_dim;
+    int box_tokens;     // tokens of a TMA box: a power of two from 16 that divides the block and the tile
     float scale_log2;   // |scale| log2(e) (times k_scale)
     int negative;       // the scale is negative: q changes sign instead
     int max_items;

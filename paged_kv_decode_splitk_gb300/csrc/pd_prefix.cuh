@@ -292,7 +292,9 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc + 8);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 16);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the warp's number from one lane, so that the compiler knows it to be the
+    // same on all: the product warp's operands then live in uniform registers)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     // ---- set-up that reads no global memory -----------------------------------
     if (tid == 0) {
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *tmem_s;
+    constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
     const long long W = *total_s;
     const int C = W < gridDim.x ? static_cast<int>(W) : static_cast<int>(gridDim.x);
     const int cta = blockIdx.x;
@@ -453,30 +455,31 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             tc::fence_after();
             return true;
         };
+        const uint64_t q_desc = tc::smem_desc(qa, 16), k_desc = tc::smem_desc(ra, 16), v_desc = tc::smem_desc(ra, BN * 128);
+        const bool issuer = tc::elect_one();
         auto scores = [&](int buf, int qt, int stage) {
-            if (lane == 0) {
-                const uint32_t qd = qa + qt * (kRowTile * DPAD * 2), kd = ra + stage * L::kStageBytes;
+            const uint64_t qd = q_desc + qt * (kRowTile * DPAD * 2 / 16), kd = k_desc + stage * (L::kStageBytes / 16);
+            if (issuer) {
 #pragma unroll
                 for (int k = 0; k < DPAD / 16; ++k)
-                    tc::mma_ss(tmem + buf * 128, tc::smem_desc(qd + (k / 4) * (kRowTile * 128) + (k % 4) * 32, 16),
-                               tc::smem_desc(kd + (k / 4) * (BN * 128) + (k % 4) * 32, 16), kDescS, k > 0);
+                    tc::mma_ss(tmem + buf * 128, qd + ((k / 4) * (kRowTile * 128) + (k % 4) * 32) / 16,
+                               kd + ((k / 4) * (BN * 128) + (k % 4) * 32) / 16, kDescS, k > 0);
                 tc::commit(bar_s + 8 * buf);
             }
             __syncwarp();
         };
         auto values = [&](int buf, int o, int stage, bool accumulate, bool done) {
-            if (lane == 0) {
-                const uint32_t vd = ra + stage * L::kStageBytes;
+            const uint64_t vd = v_desc + stage * (L::kStageBytes / 16);
+            if (issuer) {
 #pragma unroll
                 for (int k = 0; k < BN / 16; ++k)
-                    tc::mma_ts(tmem + 256 + o * DPAD, tmem + buf * 128 + k * 8, tc::smem_desc(vd + k * 2048, BN * 128), kDescO,
-                               accumulate || k > 0);
+                    tc::mma_ts(tmem + 256 + o * DPAD, tmem + buf * 128 + k * 8, vd + k * (2048 / 16), kDescO, accumulate || k > 0);
                 if (done) tc::commit(bar_o + 8 * o);
             }
             __syncwarp();
         };
         auto release = [&](int stage) {
-            if (lane == 0) tc::commit(bar_empty + 8 * stage);
+            if (issuer) tc::commit(bar_empty + 8 * stage);
             __syncwarp();
         };
         auto weights = [&](int buf) {
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                 }
             }
         }
-        if (!ok && lane == 0) {
+        if (!ok && issuer) {
             // let the products in flight end before TMEM is freed
             tc::commit(bar_tail);
             dev::mbar_wait_bounded(bar_tail, 0, 100000000ull);
@@ -781,7 +784,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 1) tc::tmem_free_512(tmem);
+    if (warp == 1) tc::tmem_free_512(*tmem_s);
 }
 
 }  // namespace prefix

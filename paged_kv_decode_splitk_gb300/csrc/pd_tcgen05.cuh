@@ -93,6 +93,13 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 }
 
 // ---- matrix products -----------------------------------------------------------
+// One lane of a whole warp, always the same: who issues products and commits.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 // Instruction descriptor of kind::f16 with FP32 accumulation: type 0 f16, 1
 // bf16 (both operands the same); A is K-major; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t instr_desc(int type, int m, int n, bool b_mn_major) {

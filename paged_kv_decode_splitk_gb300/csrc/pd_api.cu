@@ -652,7 +652,7 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
     p.max_parts = max_parts_for(dpad, false, kv8, packed_splits);
     p.stages = stages;
     p.lpt = default_lpt(num_seqs);
-    p.prefetch_tiles = kPrefetchBytes / (2 * pd::kTileTokens * dpad * 2);
+    p.prefetch_tiles = own ? 0 : kPrefetchBytes / (2 * pd::kTileTokens * dpad * 2);
     p.tok_dim = tok_dim;
     // An FP8 cache's K scale multiplies every score: fold it into the softmax scale.
     p.scale_log2 = static_cast<float>(static_cast<double>(inv_sqrt_d) * (kv8 ? static_cast<double>(k_scale) : 1.0) *
@@ -668,7 +668,7 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
     int stages_seq = default_stages_seq(dpad, kv8);
     if (pd::unit_smem_bytes(dpad, rows, stages_seq, kv8) > max_smem_optin()) stages_seq = stages;
     const bool hl = !packed && G <= 4;
-    if (own) {
+    if (own && !own_o) {  // the checks and the maps alone
         const void *caches[2] = {k_cache, v_cache};
         CUtensorMap *wide[2] = {&view->k, &view->v};
         for (int i = 0; i < 2; ++i) {
@@ -676,6 +676,9 @@ int decode_impl(const void *q, const void *k_cache, const void *v_cache, const i
                                kvh_s, elem, box_k, !kv8 || k_direct, view->box_tokens);
             if (rc != PD_OK) return rc;
         }
+        return ok();
+    }
+    if (own) {
         const cudaError_t e = kv8 ? dispatch_unit<pd::kModeOwn, true>(dpad, gn, hl, false, &tk, &tv, p, units, stages_seq, st)
                                   : dispatch_unit<pd::kModeOwn, false>(dpad, gn, hl, false, &tk, &tv, p, units, stages_seq, st);
         if (e != cudaSuccess) return cuda_fail(e, "own-token pass launch");

@@ -138,6 +138,7 @@ struct UnitParams {
     FastDiv fd_split;    // num_splits (paged mode; 1 otherwise): split geometry and unit decode
     FastDiv fd_bs;       // block_size
     FastDiv fd_kvh;      // num_kv_heads
+    unsigned own_ctas;   // kModeOwn: CTAs of the units (one cluster more is launched)
     int cluster;      // CTAs per unit: 1 (parts in sequence) or max_parts (one part per CTA)
     int max_parts;    // parts a unit's range is cut into at most
     int stages;       // pipeline stages per warp
@@ -168,9 +169,11 @@ struct KvView {
 };
 
 // The own-token pass of pd_decode_attn_prefix (pd_api.cu): pd_decode_attn's
-// checks and its partial pass over every split, each non-empty split's (o, m, l)
-// written to own_o [rows, N, D] and own_ml [rows, N, 2]; no merge, `out` only
-// checked.  *view receives maps of the same cache with view->box_tokens tokens a box.
+// partial pass over every split, each non-empty split's (o, m, l) written to
+// own_o [rows, N, D] and own_ml [rows, N, 2]; no merge.  It has to follow the
+// shared-prefix pass on the stream directly, and ends after it.  With own_o null:
+// pd_decode_attn's checks alone (`out` among them), and *view receives maps of
+// the cache with view->box_tokens tokens a box.
 int launch_own_partials(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
                         int max_blocks_per_seq, const int32_t *context_lens, void *out, int num_seqs,
                         int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,

@@ -271,14 +271,15 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     float *own_o = reinterpret_cast<float *>(ws + lay.own_o);
     float *own_ml = reinterpret_cast<float *>(ws + lay.own_ml);
 
-    // The sequences' own tokens: the unit kernel over every split, always as
-    // partials (this also checks the tensors both passes read).
     KvView view;
     view.box_tokens = 16;  // as many as divide a block and a tile: fewer, larger boxes
     while (view.box_tokens < tile_tokens(dpad_of(head_dim)) && block_size % (2 * view.box_tokens) == 0) view.box_tokens *= 2;
-    rc = launch_own_partials(q, k_cache, v_cache, block_table, max_blocks, context_lens, out, num_seqs, num_q_heads,
-                             num_kv_heads, head_dim, block_size, num_blocks, inv_sqrt_d, num_splits, own_o, own_ml, stream,
-                             kv8, k_scale, v_scale, &view);
+    auto own_pass = [&](float *o, float *ml) {
+        return launch_own_partials(q, k_cache, v_cache, block_table, max_blocks, context_lens, out, num_seqs, num_q_heads,
+                                   num_kv_heads, head_dim, block_size, num_blocks, inv_sqrt_d, num_splits, o, ml, stream, kv8,
+                                   k_scale, v_scale, &view);
+    };
+    rc = own_pass(nullptr, nullptr);  // every argument is checked before anything is launched
     if (rc != PD_OK) return rc;
 
     int err = PD_OK;
@@ -317,6 +318,10 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     cudaError_t e = kv8 ? dispatch_prefix<true>(dpad, &view.k, &view.v, p, ctas, st)
                         : dispatch_prefix<false>(dpad, &view.k, &view.v, p, ctas, st);
     if (e != cudaSuccess) return report_cuda(e, "prefix pass launch");
+    // Beside it, the sequences' own tokens: the prefix pass is bound by its
+    // products where rows are many, this one by memory.
+    rc = own_pass(own_o, own_ml);
+    if (rc != PD_OK) return rc;
 
     MergeParams m = {};
     m.plan_groups = p.plan_groups;

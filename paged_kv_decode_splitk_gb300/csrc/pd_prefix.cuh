@@ -337,6 +337,9 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    // Everything before this grid is done: the own-token pass, which needs nothing
+    // of this one, may start wherever there is room.
+    dev::griddep_launch_dependents();
     constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
     const long long W = *total_s;
     const int C = W < gridDim.x ? static_cast<int>(W) : static_cast<int>(gridDim.x);
@@ -780,7 +783,6 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             }
         }
     }
-    dev::griddep_launch_dependents();
     tc::fence_before();
     __syncthreads();
     tc::fence_after();

@@ -243,6 +243,15 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
 
     // ---- which unit (launch geometry only) ------------------------------------
     const int C = p.cluster;
+    // The own-token pass runs beside the shared-prefix pass, which let it launch
+    // only after waiting for everything before it: it waits for nothing itself.
+    // One cluster more than the units need waits for the prefix pass, so that this
+    // grid's end is the end of both (the merge waits for this grid).
+    if (MODE == kModeOwn && blockIdx.x >= p.own_ctas) {
+        dev::griddep_launch_dependents();
+        dev::griddep_wait();
+        return;
+    }
     int part = 0;
     int u = blockIdx.x;
     if (C > 1) {
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
         }
     }
 
-    dev::griddep_wait();  // the previous kernel's writes (q, caches, tables, out) are visible
+    if (MODE != kModeOwn) dev::griddep_wait();  // the previous kernel's writes (q, caches, tables, out) are visible
     if constexpr (PAGED) {
         if (p.lpt) s = longest_first(false);
     }

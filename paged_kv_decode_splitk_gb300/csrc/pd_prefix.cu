@@ -24,8 +24,8 @@ constexpr int kMergeWarps = 8;
 constexpr int kMergeCols = 128;  // columns of a row one warp merges (4 per lane)
 constexpr int kMergeBatch = 8;   // partials whose o are loaded together
 
-// The CTA whose range [W c / C, W (c + 1) / C) holds unit u.
-__device__ __forceinline__ int cta_of_unit(long long u, int C, long long W) {
+// The team whose range [W c / C, W (c + 1) / C) holds unit u.
+__device__ __forceinline__ int team_of_unit(long long u, int C, long long W) {
     const long long num = (u + 1) * C - 1;
     if (num < 0x7fffffffLL)
         return static_cast<int>(static_cast<unsigned>(num) / static_cast<unsigned>(W));
@@ -33,8 +33,8 @@ __device__ __forceinline__ int cta_of_unit(long long u, int C, long long W) {
 }
 
 // One warp per (sequence, query head, 128 columns) folds the row's partials:
-// first those of its prefix, in the order of the CTAs that made them (both
-// streams' halves where they took the tiles in turn), then its own splits.
+// first those of its prefix, in the order of the teams that made them (both
+// CTAs' where they took the tiles in turn), then its own splits.
 // With M the largest reference and w_i = 2^(m_i - M),
 //   out = sum_i w_i o_i / sum_i w_i l_i,
 // 0 where the row has no token at all.  Bound by latency on small batches (the
@@ -73,20 +73,24 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const __
         g.rows = __shfl_sync(0xffffffffu, mine.rows, src);
         g.blocks = __shfl_sync(0xffffffffu, mine.blocks, src);
     }
-    int nparts = 0, halves = 1;    // prefix slots of the row; halves of a slot it has
+    int nparts = 0, step = 2;      // prefix slots of the row, 2 apart, or (both CTAs') 1
     long long first = 0;           // (slot, row) of its first partial
     if (W > 0) {
         const int x = (s - g.first_seq) * p.group + (h - kvh * p.group);
         if (g.tiles > 0 && x < g.rows) {
             const int block = x / BR, r = x - block * BR;
-            const int item = kvh * g.blocks + block;
-            const long long u = g.first_unit + static_cast<long long>(item) * g.tiles;
-            const int C = W < p.ctas ? static_cast<int>(W) : p.ctas;
-            const int c = cta_of_unit(lane == 0 ? u : u + g.tiles - 1, C, W);
+            const int pairs = g.blocks >> 1, odd = g.blocks & 1, of_single = (g.tiles + 1) >> 1;
+            const bool pair = block < 2 * pairs;
+            const int item = block >> 1, places = pair ? g.tiles : of_single;
+            const long long u = g.first_unit + kvh * (static_cast<long long>(pairs) * g.tiles + (odd ? of_single : 0)) +
+                                static_cast<long long>(item) * g.tiles;
+            const int C = teams_of(W, p.teams);
+            const int c = team_of_unit(lane == 0 ? u : u + places - 1, C, W);
             const int c0 = __shfl_sync(0xffffffffu, c, 0), c1 = __shfl_sync(0xffffffffu, c, 1);
-            halves = p.dpad <= 128 && g.rows - block * BR <= BR / 2 ? 2 : 1;
-            nparts = (c1 - c0 + 1) * halves;
-            first = static_cast<long long>(g.first_item + item + c0) * BR + r;
+            step = pair ? 2 : 1;
+            nparts = (c1 - c0 + 1) * (pair ? 1 : 2);
+            const long long slot = 2ll * (g.first_item + kvh * (pairs + odd) + item + c0) + (pair ? block & 1 : 0);
+            first = slot * BR + r;
         }
     }
     L = L < 0 ? 0 : (L > p.max_tokens ? p.max_tokens : L);
@@ -97,13 +101,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const __
     // where partial i lies: (m, l) and, for this lane's columns, o
     auto ml_of = [&](int i) -> const float * {
         if (i >= nparts) return p.own_ml + (row * N + (i - nparts)) * 2;
-        const int slot = halves == 2 ? i >> 1 : i;
-        return p.part_ml + (first + static_cast<long long>(slot) * BR + (halves == 2 && (i & 1) ? BR / 2 : 0)) * 2;
+        return p.part_ml + (first + static_cast<long long>(i * step) * BR) * 2;
     };
     auto o_of = [&](int i) -> const float * {
         if (i >= nparts) return p.own_o + (row * N + (i - nparts)) * D + d0;
-        const int slot = halves == 2 ? i >> 1 : i;
-        const long long at = first + static_cast<long long>(slot) * BR + (halves == 2 && (i & 1) ? BR / 2 : 0);
+        const long long at = first + static_cast<long long>(i * step) * BR;
         const long long sl = at / BR, r = at - sl * BR;
         return p.part_o + ((sl * (p.dpad / 8) + d0 / 8) * BR + r) * 8 + (d0 & 4);
     };
@@ -209,10 +211,10 @@ Layout layout_of(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads
     };
     const int BR = block_rows(dpad_of(head_dim));
     const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads * num_splits;
-    // every group's rows end in at most one block that is not full
+    // every group's rows end in at most one item that is not full
     l.max_items = static_cast<long long>(num_kv_heads) *
-                  (num_groups + static_cast<long long>(num_seqs) * (num_q_heads / num_kv_heads) / BR);
-    const size_t slots = static_cast<size_t>(l.max_items) + kMaxCtas;
+                  (num_groups + static_cast<long long>(num_seqs) * (num_q_heads / num_kv_heads) / (2 * BR));
+    const size_t slots = 2 * (static_cast<size_t>(l.max_items) + kMaxTeams);
     l.own_o = take(rows * head_dim * sizeof(float));
     l.own_ml = take(rows * 2 * sizeof(float));
     l.plan_total = take(sizeof(long long));
@@ -224,11 +226,11 @@ Layout layout_of(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads
 }
 
 template <bool KV8>
-cudaError_t dispatch_prefix(int dpad, const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int ctas,
+cudaError_t dispatch_prefix(int dpad, const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int teams,
                             cudaStream_t st) {
-    if (dpad == 64) return launch_prefix<64, KV8>(tk, tv, p, ctas, st);
-    if (dpad == 128) return launch_prefix<128, KV8>(tk, tv, p, ctas, st);
-    return launch_prefix<256, KV8>(tk, tv, p, ctas, st);
+    if (dpad == 64) return launch_prefix<64, KV8>(tk, tv, p, teams, st);
+    if (dpad == 128) return launch_prefix<128, KV8>(tk, tv, p, teams, st);
+    return launch_prefix<256, KV8>(tk, tv, p, teams, st);
 }
 
 int decode_prefix_impl(const char *what, const void *q, const void *k_cache, const void *v_cache, bool kv8, float k_scale,
@@ -262,7 +264,7 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     const long long fill = (kOwnUnits + units - 1) / units;
     num_splits = static_cast<int>(std::max(1ll, std::min(static_cast<long long>(num_splits), std::min<long long>(fit, fill))));
     const Layout lay = layout_of(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, num_splits);
-    if (lay.max_items > 0x7fffffffLL - kMaxCtas) return report(PD_ERR_INVALID, "%s: launch too large", what);
+    if (lay.max_items > 0x3fffffffLL - kMaxTeams) return report(PD_ERR_INVALID, "%s: launch too large", what);
     if (!workspace || workspace_bytes < lay.end)
         return report(PD_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", what, lay.end,
                       workspace ? workspace_bytes : static_cast<size_t>(0), workspace ? "" : " (null)");
@@ -287,7 +289,7 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     p.status = device_status_word(&err);
     if (!p.status) return err;
     const int sms = sm_count_of_device();
-    const int ctas = sms < 1 ? 1 : std::min(sms, kMaxCtas);
+    const int teams = sms < 2 ? 1 : std::min(sms / 2, kMaxTeams);
     const int group = num_q_heads / num_kv_heads;
     const double scale = static_cast<double>(inv_sqrt_d) * (kv8 ? static_cast<double>(k_scale) : 1.0) * 1.4426950408889634;
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -315,8 +317,8 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     p.plan_total = reinterpret_cast<long long *>(ws + lay.plan_total);
     const int dpad = dpad_of(head_dim);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = kv8 ? dispatch_prefix<true>(dpad, &view.k, &view.v, p, ctas, st)
-                        : dispatch_prefix<false>(dpad, &view.k, &view.v, p, ctas, st);
+    cudaError_t e = kv8 ? dispatch_prefix<true>(dpad, &view.k, &view.v, p, teams, st)
+                        : dispatch_prefix<false>(dpad, &view.k, &view.v, p, teams, st);
     if (e != cudaSuccess) return report_cuda(e, "prefix pass launch");
     // Beside it, the sequences' own tokens: the prefix pass is bound by its
     // products where rows are many, this one by memory.
@@ -342,7 +344,7 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     m.num_splits = num_splits;
     m.min_kv_per_split = PD_MIN_KV_PER_SPLIT;
     m.max_tokens = max_blocks * block_size;
-    m.ctas = ctas;
+    m.teams = teams;
     m.v_scale = kv8 ? v_scale : 1.f;
     m.fd_hq = make_fastdiv(num_q_heads);
     m.fd_group = make_fastdiv(group);

@@ -13,11 +13,16 @@
 // sequence's own tokens.
 //
 // GB300 mapping.
-//   * Work is counted in units (row block, KV head, tile of kTile tokens) in one
-//     line over all groups; CTA c of C takes units [W c / C, W (c + 1) / C): every
-//     SM gets the same number of tiles whatever the shapes, and a CTA's partial
-//     of item i goes to slot i + c (item and CTA both only grow along the line,
-//     so slots are distinct, and at most items + C).
+//   * CTAs work in teams of two, a cluster.  Two row blocks of a KV head are a
+//     team's item: each CTA has one, both need the same K and V tiles, and each
+//     loads half of every tile and multicasts it to both, which halves what the
+//     SMs draw from L2.  A row block left over is an item too: there the CTAs take
+//     the tiles in turn.
+//   * Work is counted in units (item, a tile for both CTAs) in one line over all
+//     groups; team c of C takes units [W c / C, W (c + 1) / C): every SM gets the
+//     same number of tiles whatever the shapes, and a team's partials of item i go
+//     to slots 2 (i + c) and 2 (i + c) + 1 (item and team both only grow along the
+//     line, so slots are distinct, and there are at most items + C of them).
 //   * One warp loads: K and V tiles by TMA boxes of 64 columns x as many
 //     tokens as lie together in a cache block (16 to a whole tile), gathered through the group's block table into a ring of tiles (128-byte
 //     swizzle).  One warp issues tcgen05.mma: S (128 rows x kTile tokens) from
@@ -28,8 +33,7 @@
 //     half an add and half a conversion per score is all there is.
 //   * Two streams keep the tensor core and the softmax both busy: with more than
 //     128 rows each stream has 128 of them and both use every tile; with fewer,
-//     the streams take the tiles in turn (each its own O), and the merge folds
-//     the two halves.  At head dims above 128 one O fills TMEM: one stream, its
+//     the streams take the tiles in turn (each its own O), folded in the end.  At head dims above 128 one O fills TMEM: one stream, its
 //     S double-buffered.
 //   * P is rounded to BF16 (half a step: 2^-9 to 2^-8 of each weight), the form
 //     the tensor core multiplies with a BF16 V; l sums the unrounded weights in
@@ -50,7 +54,6 @@ namespace pd {
 namespace prefix {
 
 constexpr int kRowTile = 128;   // rows of one MMA
-constexpr int kBoundThreads = 512;  // (for 128 registers a thread: 384 threads leave a quarter of them free)
 constexpr int kRegionBars = 32;
 constexpr int kConverters = 64;  // threads that turn FP8 tiles into f16 ones
 
@@ -72,23 +75,28 @@ struct Plan {
     static constexpr int bars = groups + kMaxGroups * static_cast<int>(sizeof(GroupPlan));
     static constexpr int misc = bars + kRegionBars * 8;
     static constexpr int row_scale = misc + 64;  // FP8: each query row's softmax scale
-    static constexpr int total = 1024 + row_scale + (KV8 ? 2 * 2 * kRowTile * 4 : 0);
+    static constexpr int stream_ml = row_scale + (KV8 ? 2 * 2 * kRowTile * 4 : 0);  // (m, l) of the streams' rows
+    static constexpr int total = 1024 + stream_ml + (kOne ? 0 : 2 * kRowTile * 8);
     static constexpr int kThreads = 384;
 };
 
 // The block of rows and the run of tiles a CTA works on at a time.
 struct Segment {
-    int kvh, tile0, n, plen, slot;
+    int kvh, plen, slot;
+    int tile0, stride;  // tile j of the run is tile0 + j stride
+    int n;      // places in the run: the same for both CTAs of the team
+    int live;   // tiles of this CTA: n, or one less where the last place has no tile
     int row0;   // first row of the block within the group
     int rows;   // rows of the block
     int seq0;   // the group's first sequence
     int group;
     bool two;   // more than kRowTile rows: both streams use every tile
+    bool pair;  // both CTAs use the same tiles
 };
 
 template <int BR>
 __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_groups, long long &u, long long u1,
-                                             int cta, Segment &s) {
+                                             int team, int rank, Segment &s) {
     if (u >= u1) return false;
     int lo = 0, n = num_groups;  // the last group that begins at or before unit u
     while (n > 1) {
@@ -101,18 +109,28 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
         }
     }
     const GroupPlan g = grp[lo];
+    const int pairs = g.blocks >> 1, odd = g.blocks & 1;
+    const long long of_pairs = static_cast<long long>(pairs) * g.tiles;
+    const int of_single = (g.tiles + 1) >> 1;
+    const long long per_head = of_pairs + (odd ? of_single : 0);
     const long long local = u - g.first_unit;
-    const long long item = local / g.tiles;
-    s.tile0 = static_cast<int>(local - item * g.tiles);
+    s.kvh = static_cast<int>(local / per_head);
+    const long long rem = local - s.kvh * per_head;
+    s.pair = rem < of_pairs;
+    const int item = s.pair ? static_cast<int>(rem / g.tiles) : pairs;
+    const int at = static_cast<int>(rem - static_cast<long long>(item) * g.tiles);  // place within the item
+    const int places = s.pair ? g.tiles : of_single;
     const long long left = u1 - u;
-    s.n = left < g.tiles - s.tile0 ? static_cast<int>(left) : g.tiles - s.tile0;
-    s.kvh = static_cast<int>(item / g.blocks);
-    s.row0 = (static_cast<int>(item) - s.kvh * g.blocks) * BR;
+    s.n = left < places - at ? static_cast<int>(left) : places - at;
+    s.stride = s.pair ? 1 : 2;
+    s.tile0 = s.pair ? at : 2 * at + rank;
+    s.live = s.tile0 + (s.n - 1) * s.stride < g.tiles ? s.n : s.n - 1;
+    s.row0 = (s.pair ? 2 * item + rank : 2 * pairs) * BR;
     s.rows = min(BR, g.rows - s.row0);
     s.plen = g.tokens;
     s.seq0 = g.first_seq;
     s.group = lo;
-    s.slot = g.first_item + static_cast<int>(item) + cta;
+    s.slot = 2 * (g.first_item + s.kvh * (pairs + odd) + item + team) + rank;
     s.two = s.rows > kRowTile;
     u += s.n;
     return true;
@@ -146,8 +164,11 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
             r.blocks = (r.rows + block_rows(DPAD) - 1) / block_rows(DPAD);
             r.tokens = len;
             r.tiles = (len + tile_tokens(DPAD) - 1) / tile_tokens(DPAD);
-            it = r.tiles > 0 ? r.blocks * p.num_kv_heads : 0;
-            mine = static_cast<long long>(it) * r.tiles;
+            const int pairs = r.blocks >> 1, odd = r.blocks & 1;
+            if (r.tiles > 0) {
+                it = (pairs + odd) * p.num_kv_heads;
+                mine = (static_cast<long long>(pairs) * r.tiles + odd * ((r.tiles + 1) >> 1)) * p.num_kv_heads;
+            }
         }
         long long su = mine;
         int si = it;
@@ -264,7 +285,7 @@ __device__ __forceinline__ void raise_reference(uint32_t ts, uint32_t to, int c,
 }
 
 template <int DPAD, bool KV8>
-__global__ void __launch_bounds__(kBoundThreads, 1)
+__global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     prefix_kernel(const __grid_constant__ KvMaps<1> maps, const __grid_constant__ PrefixParams p) {
     using L = Plan<DPAD, KV8>;
     constexpr int BN = L::kTile;
@@ -282,12 +303,12 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
     const uint32_t base = dev::smem_addr(smem);
     GroupPlan *grp = reinterpret_cast<GroupPlan *>(smem + L::groups);
     // barriers: full[NST], empty[NST], raw_full[3], raw_empty[3], s_full[2],
-    // p_full[2], o_done[2], q_full[2], tail
+    // p_full[2], o_done[2], q_full[2], tail, streams
     const uint32_t bars = base + L::bars;
     const uint32_t bar_full = bars, bar_empty = bar_full + 8 * NST, bar_rfull = bar_empty + 8 * NST,
                    bar_rempty = bar_rfull + 24, bar_s = bar_rempty + 24, bar_p = bar_s + 16, bar_o = bar_p + 16,
-                   bar_q = bar_o + 16, bar_tail = bar_q + 16;
-    static_assert(2 * NST + 15 <= kRegionBars, "barrier region");
+                   bar_q = bar_o + 16, bar_tail = bar_q + 16, bar_x = bar_tail + 8;
+    static_assert(2 * NST + 16 <= kRegionBars, "barrier region");
     long long *total_s = reinterpret_cast<long long *>(smem + L::misc);
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc + 8);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 16);
@@ -295,16 +316,19 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
     // (the warp's number from one lane, so that the compiler knows it to be the
     // same on all: the product warp's operands then live in uniform registers)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int rank = blockIdx.x & 1, team = blockIdx.x >> 1;  // clusters are of two CTAs
 
     // ---- set-up that reads no global memory -----------------------------------
     if (tid == 0) {
+        // a stage is free once both CTAs of the team have used it: either may be
+        // the next to write a half of it
         for (int i = 0; i < NST; ++i) {
             dev::mbar_init(bar_full + 8 * i, KV8 ? kConverters : 1);
-            dev::mbar_init(bar_empty + 8 * i, 1);
+            dev::mbar_init(bar_empty + 8 * i, KV8 ? 1 : 2);
         }
         for (int i = 0; i < 3; ++i) {
             dev::mbar_init(bar_rfull + 8 * i, 1);
-            dev::mbar_init(bar_rempty + 8 * i, kConverters);
+            dev::mbar_init(bar_rempty + 8 * i, 2 * kConverters / 32);
         }
         for (int i = 0; i < 2; ++i) {
             dev::mbar_init(bar_s + 8 * i, 1);
@@ -313,11 +337,13 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             dev::mbar_init(bar_q + 8 * i, 128);
         }
         dev::mbar_init(bar_tail, 1);
+        dev::mbar_init(bar_x, 256);
         dev::fence_mbar_init();
         *gave_up = 0;
         dev::prefetch_tensormap(&maps.k[0]);
         dev::prefetch_tensormap(&maps.v[0]);
     }
+    dev::cluster_arrive_relaxed();
     if (warp == 1) tc::tmem_alloc_512(dev::smem_addr(tmem_s));
     dev::griddep_wait();  // q, the caches, tables and lengths are final
     if (warp == 0) {
@@ -334,6 +360,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             if (lane == 0) *p.plan_total = total;
         }
     }
+    dev::cluster_wait();  // the peer's barriers are initialised
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -342,12 +369,11 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
     dev::griddep_launch_dependents();
     constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
     const long long W = *total_s;
-    const int C = W < gridDim.x ? static_cast<int>(W) : static_cast<int>(gridDim.x);
-    const int cta = blockIdx.x;
+    const int C = teams_of(W, gridDim.x / 2);
     long long u = 0, u1 = 0;
-    if (cta < C) {
-        u = W * cta / C;
-        u1 = W * (cta + 1) / C;
+    if (team < C) {
+        u = W * team / C;
+        u1 = W * (team + 1) / C;
     }
     const int bs = static_cast<int>(p.block_size.d);
     const int D = p.head_dim;
@@ -369,38 +395,47 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
         uint32_t tail_ph = 0;
         bool ok = true;
         long long issued = 0;
-        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const int32_t *ids = p.prefix_table + static_cast<long long>(sg.group) * p.max_prefix_blocks;
             const int ahead = ONE || !sg.two ? 2 : 1;
+            // of a shared tile each CTA loads every other box, for both
+            const bool mine = lane < NBOX && (!sg.pair || (lane & 1) == rank);
             // this lane's box of tile j: its block id (past the prefix, or bad: one
             // outside the cache, which reads zeros), asked for two tiles ahead
             auto id_of = [&](int j) -> int {
-                const int tok = (sg.tile0 + j) * BN + chunk * CT;
-                if (lane >= NBOX || j >= sg.n || tok >= sg.plen) return p.num_blocks;
+                const int tok = (sg.tile0 + j * sg.stride) * BN + chunk * CT;
+                if (!mine || j >= sg.live || tok >= sg.plen) return p.num_blocks;
                 return __ldg(ids + fast_div(tok, p.block_size));
             };
             auto load = [&](bool is_v, int j, int id) {
-                const int tok = (sg.tile0 + j) * BN + chunk * CT;
-                const int blk = fast_div(tok, p.block_size);
-                if (id < 0 || id > p.num_blocks || (id == p.num_blocks && lane < NBOX && tok < sg.plen)) {
+                const int first = (sg.tile0 + j * sg.stride) * BN, tok = first + chunk * CT;
+                if (mine && j < sg.live && tok < sg.plen && (id < 0 || id >= p.num_blocks)) {
                     dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
                     id = p.num_blocks;
                 }
                 if (!wait_bar(empty + 8 * st, ph ^ 1, gave_up)) return false;
                 const uint32_t dst = stage0 + st * BYTES;
-                const int nv = sg.plen - (sg.tile0 + j) * BN;  // live tokens of the tile
+                const int nv = sg.plen - first;  // live tokens of the tile
                 // A tile's box of live and dead tokens holds whatever the cache's
                 // slots past the prefix hold; a dead V row must not reach the
                 // product (0 x NaN), so those rows are zeroed before it is handed on.
-                const bool tail = !KV8 && is_v && nv < BN && (nv & (CT - 1));
+                const bool tail = !KV8 && is_v && j < sg.live && nv < BN && (nv & (CT - 1));
                 const uint32_t bar = tail ? bar_tail : full + 8 * st;
-                if (lane == 0) dev::mbar_arrive_expect_tx(bar, BYTES);
-                __syncwarp();
-                if (lane < NBOX) {
-                    const int sub = tok - blk * bs;
-                    dev::tma_load_4d(dst + col * (BN * (KV8 ? COLS : 128)) + chunk * (CT * (KV8 ? COLS : 128)),
-                                     is_v ? &maps.v[0] : &maps.k[0], bar, col * COLS, p.tok_dim == 1 ? sub : sg.kvh,
-                                     p.tok_dim == 1 ? sg.kvh : sub, id, policy);
+                if (j >= sg.live) {  // a place without a tile: nothing lands
+                    if (lane == 0) arrive(bar);
+                } else {
+                    if (lane == 0) dev::mbar_arrive_expect_tx(bar, BYTES);
+                    __syncwarp();
+                    if (mine) {
+                        const int sub = tok - fast_div(tok, p.block_size) * bs;
+                        const uint32_t to = dst + col * (BN * (KV8 ? COLS : 128)) + chunk * (CT * (KV8 ? COLS : 128));
+                        const CUtensorMap *map = is_v ? &maps.v[0] : &maps.k[0];
+                        const int c1 = p.tok_dim == 1 ? sub : sg.kvh, c2 = p.tok_dim == 1 ? sg.kvh : sub;
+                        if (sg.pair)
+                            tc::tma_load_4d_both(to, map, bar, col * COLS, c1, c2, id, policy);
+                        else
+                            dev::tma_load_4d(to, map, bar, col * COLS, c1, c2, id, policy);
+                    }
                 }
                 if (tail) {
                     if (!wait_bar(bar_tail, tail_ph, gave_up)) return false;
@@ -432,6 +467,9 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                 id_next = id_after;
             }
         }
+        // every release of a stage by either CTA has arrived here before this CTA ends
+        for (long long i = issued < DEPTH ? 0 : issued - DEPTH; ok && i < issued; ++i)
+            ok = wait_bar(empty + 8 * static_cast<int>(i % DEPTH), static_cast<uint32_t>((i / DEPTH) & 1), gave_up);
         if (!ok && lane == 0) {
             // a wait ran out: let the copies in flight land before the CTA ends
             dev::flag_status(p.status, PD_DEV_WAIT_TIMEOUT);
@@ -482,7 +520,12 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             __syncwarp();
         };
         auto release = [&](int stage) {
-            if (issuer) tc::commit(bar_empty + 8 * stage);
+            if (issuer) {
+                if (KV8)
+                    tc::commit(bar_empty + 8 * stage);
+                else
+                    tc::commit_both(bar_empty + 8 * stage);
+            }
             __syncwarp();
         };
         auto weights = [&](int buf) {
@@ -497,48 +540,52 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             tc::fence_after();
             return true;
         };
-        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
-            const int n = sg.n;
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
+            const int n = sg.n, live = sg.live;
             int ks = 0, vs = 0;
-            ok = queries(0) && take(ks);
-            if (!ok) break;
-            scores(0, 0, ks);
+            if (live > 0 && !(ok = queries(0))) break;
             if (!ONE && sg.two) {
-                if (!(ok = queries(1))) break;
-                scores(1, 1, ks);
+                if (!(ok = take(ks))) break;
+                if (live > 0) {
+                    scores(0, 0, ks);
+                    if (!(ok = queries(1))) break;
+                    scores(1, 1, ks);
+                }
                 release(ks);
                 for (int j = 0; ok && j < n; ++j) {
-                    const bool more = j + 1 < n;
                     if (!(ok = take(vs))) break;
+                    const bool now = j < live, more = j + 1 < live;
                     for (int t = 0; ok && t < 2; ++t) {
-                        if (!(ok = weights(t))) break;
-                        values(t, t, vs, j > 0, !more);
-                        if (more) {
-                            if (t == 0 && !(ok = take(ks))) break;
-                            scores(t, t, ks);
+                        if (now) {
+                            if (!(ok = weights(t))) break;
+                            values(t, t, vs, j > 0, !more);
                         }
+                        if (t == 0 && j + 1 < n && !(ok = take(ks))) break;
+                        if (more) scores(t, t, ks);
                     }
                     if (!ok) break;
                     release(vs);
-                    if (more) release(ks);
+                    if (j + 1 < n) release(ks);
                 }
             } else {
-                release(ks);
-                if (n > 1) {
-                    if (!(ok = take(ks))) break;
-                    scores(1, 0, ks);
+                // scores of tile j, whose keys are the next of the ring
+                auto next_scores = [&](int j) {
+                    if (j >= n) return true;
+                    if (!take(ks)) return false;
+                    if (j < live) scores(j & 1, 0, ks);
                     release(ks);
-                }
+                    return true;
+                };
+                ok = next_scores(0) && next_scores(1);
                 for (int j = 0; ok && j < n; ++j) {
-                    const int t = j & 1;
-                    if (!(ok = take(vs) && weights(t))) break;
-                    values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= n);
-                    release(vs);
-                    if (j + 2 < n) {
-                        if (!(ok = take(ks))) break;
-                        scores(t, 0, ks);
-                        release(ks);
+                    if (!(ok = take(vs))) break;
+                    if (j < live) {
+                        const int t = j & 1;
+                        if (!(ok = weights(t))) break;
+                        values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= live);
                     }
+                    release(vs);
+                    ok = next_scores(j + 2);
                 }
             }
         }
@@ -556,35 +603,38 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
         // are zeroed on the way.
         constexpr int CPR = DPAD / 16;               // 16-code chunks of a row
         constexpr int ITEMS = BN / 2 * (CPR / 4);    // (row pair, 64 codes)
-        const int me = (warp - 2) * 4 + (lane >> 3), j = lane & 7;
+        const int me = (warp - 2) * 4 + (lane >> 3), j8 = lane & 7;
         int rs = 0, st = 0;
         uint32_t rph = 0, ph = 0;
         bool ok = true;
-        auto convert = [&](bool is_v, int nv) {
+        auto convert = [&](bool live, bool is_v, int nv) {
             if (!wait_bar(bar_rfull + 8 * rs, rph, gave_up) || !wait_bar(bar_empty + 8 * st, ph ^ 1, gave_up)) return false;
             const uint8_t *src = smem + L::raw + rs * L::kRawBytes;
             uint8_t *dst = smem + L::ring + st * L::kStageBytes;
+            if (live) {
 #pragma unroll 4
-            for (int i = me; i < ITEMS; i += kConverters / 8) {
-                const int kb = i % (CPR / 4), row = i / (CPR / 4) * 2 + (j >> 2);
-                const int c = 4 * (CPR >= 8 ? kb ^ (j >> 2) : kb) + (j & 3);
-                const uint8_t *at = DPAD < 128 ? src + row * DPAD + c * 16
-                                               : src + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-                uint4 v = *reinterpret_cast<const uint4 *>(at);
-                if (is_v && row >= nv) v = make_uint4(0, 0, 0, 0);
-                uint4 lo, hi;
-                dev::e4m3x4_to_f16x4(v.x, lo.x, lo.y);
-                dev::e4m3x4_to_f16x4(v.y, lo.z, lo.w);
-                dev::e4m3x4_to_f16x4(v.z, hi.x, hi.y);
-                dev::e4m3x4_to_f16x4(v.w, hi.z, hi.w);
-                uint8_t *box = dst + (c / 4) * (BN * 128) + row * 128;
-                const int u2 = (2 * c) & 7;
-                *reinterpret_cast<uint4 *>(box + ((u2 ^ (row & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4 *>(box + (((u2 + 1) ^ (row & 7)) << 4)) = hi;
+                for (int i = me; i < ITEMS; i += kConverters / 8) {
+                    const int kb = i % (CPR / 4), row = i / (CPR / 4) * 2 + (j8 >> 2);
+                    const int c = 4 * (CPR >= 8 ? kb ^ (j8 >> 2) : kb) + (j8 & 3);
+                    const uint8_t *at = DPAD < 128 ? src + row * DPAD + c * 16
+                                                   : src + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                    uint4 v = *reinterpret_cast<const uint4 *>(at);
+                    if (is_v && row >= nv) v = make_uint4(0, 0, 0, 0);
+                    uint4 lo, hi;
+                    dev::e4m3x4_to_f16x4(v.x, lo.x, lo.y);
+                    dev::e4m3x4_to_f16x4(v.y, lo.z, lo.w);
+                    dev::e4m3x4_to_f16x4(v.z, hi.x, hi.y);
+                    dev::e4m3x4_to_f16x4(v.w, hi.z, hi.w);
+                    uint8_t *box = dst + (c / 4) * (BN * 128) + row * 128;
+                    const int u2 = (2 * c) & 7;
+                    *reinterpret_cast<uint4 *>(box + ((u2 ^ (row & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4 *>(box + (((u2 + 1) ^ (row & 7)) << 4)) = hi;
+                }
+                tc::fence_async_shared();
             }
-            tc::fence_async_shared();
             arrive(bar_full + 8 * st);
-            arrive(bar_rempty + 8 * rs);
+            __syncwarp();
+            if (lane < 2) dev::mbar_arrive_cluster(dev::map_to_rank(bar_rempty + 8 * rs, lane));  // free for both CTAs
             if (++rs == L::kRawStages) {
                 rs = 0;
                 rph ^= 1;
@@ -595,12 +645,12 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             }
             return true;
         };
-        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const int ahead = ONE || !sg.two ? 2 : 1;
             for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
-                if (i < sg.n) ok = convert(false, BN);
+                if (i < sg.n) ok = convert(i < sg.live, false, BN);
                 const int v = i - ahead + 1;
-                if (ok && v >= 0) ok = convert(true, sg.plen - (sg.tile0 + v) * BN);
+                if (ok && v >= 0) ok = convert(v < sg.live, true, sg.plen - (sg.tile0 + v * sg.stride) * BN);
             }
         }
     } else if (warp >= 4 && warp < (ONE ? 8 : 12)) {
@@ -609,14 +659,14 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
         const int r = (warp & 3) * 32 + lane;     // the row of its tile
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t to = tmem + lanes + 256 + t * DPAD;
-        uint32_t sph[2] = {0, 0}, oph = 0;
+        uint32_t sph[2] = {0, 0}, oph[2] = {0, 0}, xph = 0;
         bool ok = true;
         // FP8: the rows' scales, in turn in two places: the other stream may still
         // have to read the last segment's when this one's are written (it has by
         // the time a third segment begins: its weights of the first went before)
         float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
         int turn = 0;
-        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, cta, sg)) {
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const bool two = sg.two;
             float scale = p.scale_log2;
             if constexpr (KV8) {
@@ -625,7 +675,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             }
             // -- this stream's query rows into shared memory (128-byte swizzle); with
             // at most 128 rows the streams share stream 0's
-            if (two || t == 0) {
+            if ((two || t == 0) && sg.live > 0) {
                 uint8_t *qt = smem + L::q + t * (kRowTile * DPAD * 2);
                 constexpr int STEPS = CHUNKS;  // 32 rows x CHUNKS chunks over 32 lanes
 #pragma unroll 8
@@ -673,14 +723,14 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
             float m = kNegInf, l = 0.f;
             bool first = true;
             const int step = ONE || two ? 1 : 2;
-            for (int j = step == 2 ? t : 0; j < sg.n; j += step) {
+            for (int j = step == 2 ? t : 0; j < sg.live; j += step) {
                 const int buf = ONE ? (j & 1) : t;
                 const uint32_t ts = tmem + lanes + buf * 128;
                 if (!(ok = wait_bar(bar_s + 8 * buf, sph[buf], gave_up))) break;
                 sph[buf] ^= 1;
                 tc::fence_after();
                 if (KV8 && first) scale = row_scale[(two ? t * kRowTile : 0) + r];
-                const int nv = sg.plen - (sg.tile0 + j) * BN;
+                const int nv = sg.plen - (sg.tile0 + j * sg.stride) * BN;
                 // -- A row's reference m is the largest score of its first tile; after
                 // that no maximum is taken: weights may be as large as kLift, and
                 // only when a row's weights of 32 columns sum to more does its warp
@@ -724,8 +774,8 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                     if (!lifted && __any_sync(0xffffffffu, over)) {
                         lifted = true;
                         if (!waited) {
-                            ok = wait_bar(bar_o, oph, gave_up);
-                            oph ^= 1;
+                            ok = wait_bar(bar_o, oph[0], gave_up);
+                            oph[0] ^= 1;
                             waited = true;
                         }
                         tc::fence_after();
@@ -748,8 +798,8 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                     weigh(xb, c + 32);
                 }
                 if (ONE && !waited) {  // (each phase of the barrier is waited for, in order)
-                    ok = wait_bar(bar_o, oph, gave_up) && ok;
-                    oph ^= 1;
+                    ok = wait_bar(bar_o, oph[0], gave_up) && ok;
+                    oph[0] ^= 1;
                 }
                 if (!ok) break;
                 tc::wait_st();
@@ -757,36 +807,90 @@ __global__ void __launch_bounds__(kBoundThreads, 1)
                 arrive(bar_p + 8 * buf);
             }
             if (!ok) break;
-            // -- the partial of this row
-            const int gr = two ? t * kRowTile + r : r;
-            const bool live = gr < sg.rows;
-            const long long at = static_cast<long long>(sg.slot) * BR + t * kRowTile + r;
-            if (live) *reinterpret_cast<float2 *>(p.part_ml + at * 2) = make_float2(m, l);
-            if (!first) {
-                if (!(ok = wait_bar(bar_o + 8 * t, oph, gave_up))) break;
-                oph ^= 1;
-                tc::fence_after();
-                float *o = p.part_o + (static_cast<long long>(sg.slot) * (DPAD / 8)) * (BR * 8) + (t * kRowTile + r) * 8;
-#pragma unroll 1
-                for (int c = 0; c < DPAD; c += 32) {
-                    uint32_t x[32];
-                    tc::ld_32x32(to + c, x);
-                    tc::wait_ld(x);
-                    if (live) {
+            // -- the partial of this row: o [slot][DPAD / 8][BR][8], (m, l) [slot][BR]
+            const long long at = static_cast<long long>(sg.slot) * BR;
+            float *o = p.part_o + at * DPAD;
+            auto store = [&](int row, int c, const uint32_t (&x)[32]) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(o + ((c + i) / 8) * (BR * 8) + (i & 4)) =
-                                make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<uint4 *>(o + (static_cast<long long>((c + i) / 8) * BR + row) * 8 + (i & 4)) =
+                        make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            };
+            if (ONE || two) {
+                const int row = t * kRowTile + r;
+                const bool in = row < sg.rows;
+                if (in) *reinterpret_cast<float2 *>(p.part_ml + (at + row) * 2) = make_float2(m, l);
+                if (sg.live > 0) {
+                    if (!(ok = wait_bar(bar_o + 8 * t, oph[t], gave_up))) break;
+                    oph[0] ^= 1;
+                    oph[1] ^= 1;
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < DPAD; c += 32) {
+                        uint32_t x[32];
+                        tc::ld_32x32(to + c, x);
+                        tc::wait_ld(x);
+                        if (in) store(row, c, x);
+                    }
+                    tc::fence_before();
+                }
+            } else {
+                // the streams' two partials of the row, folded: each stream then writes
+                // half of the columns
+                float2 *ml = reinterpret_cast<float2 *>(smem + L::stream_ml);
+                ml[t * kRowTile + r] = make_float2(m, l);
+                arrive(bar_x);
+                if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
+                xph ^= 1;
+                for (int k = 0; k < 2 && ok; ++k) {
+                    if (k < sg.live) {
+                        ok = wait_bar(bar_o + 8 * k, oph[k], gave_up);
+                        oph[k] ^= 1;
                     }
                 }
-                tc::fence_before();
+                if (!ok) break;
+                tc::fence_after();
+                const float2 a = ml[r], b = ml[kRowTile + r];
+                const float M = fmaxf(a.y == 0.f ? kNegInf : a.x, b.y == 0.f ? kNegInf : b.x);
+                const float fa = a.y == 0.f ? 0.f : dev::exp2_approx(a.x - M), fb = b.y == 0.f ? 0.f : dev::exp2_approx(b.x - M);
+                const bool in = r < sg.rows;
+                if (in && t == 0)
+                    *reinterpret_cast<float2 *>(p.part_ml + (at + r) * 2) =
+                        make_float2(M, (a.y == 0.f ? 0.f : a.y * fa) + (b.y == 0.f ? 0.f : b.y * fb));
+                if (sg.live > 0) {
+#pragma unroll 1
+                    for (int c = t * (DPAD / 2); c < (t + 1) * (DPAD / 2); c += 32) {
+                        uint32_t x[32], y[32];
+                        tc::ld_32x32(tmem + lanes + 256 + c, x);
+                        tc::wait_ld(x);
+                        if (sg.live > 1) {
+                            tc::ld_32x32(tmem + lanes + 256 + DPAD + c, y);
+                            tc::wait_ld(y);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float xa = fa == 0.f ? 0.f : __uint_as_float(x[i]) * fa;
+                            x[i] = __float_as_uint(sg.live > 1 && fb != 0.f ? fmaf(__uint_as_float(y[i]), fb, xa) : xa);
+                        }
+                        if (in) store(r, c, x);
+                    }
+                    tc::fence_before();
+                }
+                // both streams have read both O before either lets one be overwritten
+                arrive(bar_x);
+                if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
+                xph ^= 1;
             }
         }
     }
+    // The peer may still send halves of tiles and release stages: shared memory
+    // stays until both are done.
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     if (warp == 1) tc::tmem_free_512(*tmem_s);
+    dev::cluster_arrive_relaxed();
+    dev::cluster_wait();
 }
 
 }  // namespace prefix

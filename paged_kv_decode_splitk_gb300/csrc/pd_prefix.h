@@ -8,15 +8,25 @@ namespace pd {
 namespace prefix {
 
 constexpr int kMaxGroups = 256;   // PD_MAX_PREFIX_GROUPS
-constexpr int kMaxCtas = 152;     // CTAs of the prefix pass at most (sizes the workspace)
+constexpr int kMaxTeams = 76;     // teams of two CTAs of the prefix pass at most (sizes the workspace)
 
 // Keys of a tile: 128, or 64 where a tile of 128 would leave no ring (D > 128).
 __host__ __device__ constexpr int tile_tokens(int dpad) { return dpad > 128 ? 64 : 128; }
 // Query rows of an item: two 128-row tiles, or one where its O fills TMEM.
 __host__ __device__ constexpr int block_rows(int dpad) { return dpad > 128 ? 128 : 256; }
 
-// One group on the line of work units (row block, KV head, tile).  Items are
-// its (KV head, row block) pairs, KV head first.
+// Teams that share W units: all there are, but each at least kMinUnits (a team
+// more is a partial more of each of its rows to write and fold).
+constexpr int kMinUnits = 1;
+__host__ __device__ inline int teams_of(long long W, int most) {
+    const long long n = (W + kMinUnits - 1) / kMinUnits;
+    return n < most ? static_cast<int>(n) : most;
+}
+
+// One group on the line of work units.  An item is two row blocks of a KV head,
+// which a team's CTAs work on side by side (a unit is a tile), or a block left
+// over, whose tiles they take in turn (a unit is two tiles); per KV head the pairs
+// come first.
 struct GroupPlan {
     long long first_unit;
     int first_item;
@@ -38,7 +48,7 @@ struct PrefixParams {
     float scale_log2;   // |scale| log2(e) (times k_scale)
     int negative;       // the scale is negative: q changes sign instead
     int max_items;
-    float *part_ml;     // [slot][block rows] (m, l)
+    float *part_ml;     // [slot][block rows] (m, l); a team's item has two slots, one for each CTA
     float *part_o;      // [slot][dpad / 8][block rows][8]
     GroupPlan *plan_groups;
     long long *plan_total;
@@ -53,13 +63,13 @@ struct MergeParams {
     const int32_t *context_lens;
     __nv_bfloat16 *out;
     int num_groups, num_seqs, num_q_heads, num_kv_heads, group, head_dim, dpad;
-    int num_splits, min_kv_per_split, max_tokens, ctas;
+    int num_splits, min_kv_per_split, max_tokens, teams;
     float v_scale;      // of the prefix partials (an FP8 cache; the own-token pass applies its own)
     FastDiv fd_hq, fd_group, fd_split, fd_bs;
 };
 
 template <int DPAD, bool KV8>
-cudaError_t launch_prefix(const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int ctas,
+cudaError_t launch_prefix(const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int teams,
                           cudaStream_t stream);
 
 }  // namespace prefix

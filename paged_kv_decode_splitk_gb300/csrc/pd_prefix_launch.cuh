@@ -11,7 +11,7 @@ namespace pd {
 namespace prefix {
 
 template <int DPAD, bool KV8>
-cudaError_t launch_prefix(const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int ctas,
+cudaError_t launch_prefix(const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int teams,
                           cudaStream_t stream) {
     auto kern = prefix_kernel<DPAD, KV8>;
     static std::mutex mu;
@@ -31,15 +31,19 @@ cudaError_t launch_prefix(const CUtensorMap *tk, const CUtensorMap *tv, const Pr
         }
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * teams));
     cfg.blockDim = dim3(Plan<DPAD, KV8>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     KvMaps<1> maps;
     maps.k[0] = *tk;
     maps.v[0] = *tv;

@@ -379,8 +379,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     const int D = p.head_dim;
     Segment sg;
 
-    if (warp == 0) {
+    if (warp == 0 || (!KV8 && warp == 2)) {
         // ---- loads: K and V tiles in the order the products take them ------------
+        // (a warp for each where two are free: a box takes its warp some 150 cycles)
         constexpr int COLS = KV8 ? (DPAD < 128 ? DPAD : 128) : kBoxCols;  // columns of a box
         const int CT = p.box_tokens;                         // tokens of a box
         const int NCH = BN / CT, NBOX = NCH * (DPAD / COLS);
@@ -407,7 +408,16 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (!mine || j >= sg.live || tok >= sg.plen) return p.num_blocks;
                 return __ldg(ids + fast_div(tok, p.block_size));
             };
+            auto next_stage = [&] {
+                ++issued;
+                if (++st == DEPTH) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                return true;
+            };
             auto load = [&](bool is_v, int j, int id) {
+                if (!KV8 && is_v != (warp == 2)) return next_stage();  // the other warp's
                 const int first = (sg.tile0 + j * sg.stride) * BN, tok = first + chunk * CT;
                 if (mine && j < sg.live && tok < sg.plen && (id < 0 || id >= p.num_blocks)) {
                     dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
@@ -449,12 +459,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) arrive(full + 8 * st);
                 }
-                ++issued;
-                if (++st == DEPTH) {
-                    st = 0;
-                    ph ^= 1;
-                }
-                return true;
+                return next_stage();
             };
             int id_last = 0, id_now = id_of(0), id_next = id_of(1);
             for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {

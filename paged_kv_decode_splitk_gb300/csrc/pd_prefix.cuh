@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
 
     if (warp == 0 || (!KV8 && warp == 2)) {
         // ---- loads: K and V tiles in the order the products take them ------------
-        // (a warp for each where two are free: a box takes its warp some 150 cycles)
+        // (a warp for each where two are free)
         constexpr int COLS = KV8 ? (DPAD < 128 ? DPAD : 128) : kBoxCols;  // columns of a box
         const int CT = p.box_tokens;                         // tokens of a box
         const int NCH = BN / CT, NBOX = NCH * (DPAD / COLS);
@@ -401,13 +401,19 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const int ahead = ONE || !sg.two ? 2 : 1;
             // of a shared tile each CTA loads every other box, for both
             const bool mine = lane < NBOX && (!sg.pair || (lane & 1) == rank);
-            // this lane's box of tile j: its block id (past the prefix, or bad: one
-            // outside the cache, which reads zeros), asked for two tiles ahead
-            auto id_of = [&](int j) -> int {
-                const int tok = (sg.tile0 + j * sg.stride) * BN + chunk * CT;
-                if (!mine || j >= sg.live || tok >= sg.plen) return p.num_blocks;
-                return __ldg(ids + fast_div(tok, p.block_size));
+            // Block ids, 32 boxes' rows (chunks of CT tokens) at a time: lane l of `now`
+            // has chunk 32 w + l of the run, `then` the 32 after them, asked for a
+            // window ahead.  Past the prefix, and for a bad id (-1), it is one
+            // outside the cache, which reads zeros.
+            const int lg = 31 - __clz(NCH);
+            auto ids_of = [&](int w) -> int {
+                const int c = 32 * w + lane, j = c >> lg;
+                const int tok = (sg.tile0 + j * sg.stride) * BN + (c & (NCH - 1)) * CT;
+                if (j >= sg.live || tok >= sg.plen) return p.num_blocks;
+                const int id = __ldg(ids + fast_div(tok, p.block_size));
+                return id >= 0 && id < p.num_blocks ? id : -1;
             };
+            int w = 0, now = ids_of(0), then = ids_of(1), before = now;
             auto next_stage = [&] {
                 ++issued;
                 if (++st == DEPTH) {
@@ -416,11 +422,19 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 }
                 return true;
             };
-            auto load = [&](bool is_v, int j, int id) {
+            auto load = [&](bool is_v, int j) {
                 if (!KV8 && is_v != (warp == 2)) return next_stage();  // the other warp's
                 const int first = (sg.tile0 + j * sg.stride) * BN, tok = first + chunk * CT;
-                if (mine && j < sg.live && tok < sg.plen && (id < 0 || id >= p.num_blocks)) {
-                    dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
+                const int wj = j << lg >> 5;
+                if (wj > w) {
+                    w = wj;
+                    before = now;
+                    now = then;
+                    then = ids_of(w + 1);
+                }
+                int id = __shfl_sync(0xffffffffu, wj == w ? now : before, ((j << lg) + chunk) & 31);
+                if (id < 0) {
+                    if (mine) dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
                     id = p.num_blocks;
                 }
                 if (!wait_bar(empty + 8 * st, ph ^ 1, gave_up)) return false;
@@ -461,15 +475,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 }
                 return next_stage();
             };
-            int id_last = 0, id_now = id_of(0), id_next = id_of(1);
             for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
-                const int id_after = id_of(i + 2);
-                if (i < sg.n) ok = load(false, i, id_now);
+                if (i < sg.n) ok = load(false, i);
                 const int v = i - ahead + 1;
-                if (ok && v >= 0) ok = load(true, v, ahead == 1 ? id_now : id_last);
-                id_last = id_now;
-                id_now = id_next;
-                id_next = id_after;
+                if (ok && v >= 0) ok = load(true, v);
             }
         }
         // every release of a stage by either CTA has arrived here before this CTA ends

@@ -212,6 +212,20 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     return __all_sync(0xffffffffu, ok);
 }
 
+// The same for one thread.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    if (dev::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = dev::global_timer_ns();
+    while (!dev::mbar_try_wait(bar, parity)) {
+        if (*gave_up) return false;
+        if (dev::global_timer_ns() - t0 > 2000000000ull) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -221,42 +235,59 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return KV8 ? dev::pack_f16x2(lo, hi) : dev::pack_bf16x2(lo, hi);
 }
 
-// Sum of 32 weights above which a row's reference is raised.
+// Sum of a tile's weights above which a row's reference is raised.
 constexpr float kLift = 32768.f;
 
-// The largest of a row's scores in columns [c, BN), live ones (below nv) only.
+// The largest of a row's live scores (columns below nv) of a tile.
 template <int BN>
-__device__ __forceinline__ float largest_score(uint32_t ts, int c, int nv) {
+__device__ __forceinline__ float largest_of(const uint32_t (&x)[BN], int nv) {
     const float kNegInf = -__int_as_float(0x7f800000);
-    float mx = kNegInf;
-#pragma unroll 1
-    for (; c < BN; c += 32) {
-        uint32_t x[32];
-        tc::ld_32x32(ts + c, x);
-        tc::wait_ld(x);
-        float m0 = kNegInf, m1 = kNegInf;
-        if (nv - c >= 32) {
+    float m0 = kNegInf, m1 = kNegInf;
+    if (nv >= BN) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                m0 = fmaxf(fmaxf(m0, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-                m1 = fmaxf(fmaxf(m1, __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m0 = fmaxf(m0, c + i < nv ? __uint_as_float(x[i]) : kNegInf);
+        for (int i = 0; i < BN; i += 4) {
+            m0 = fmaxf(fmaxf(m0, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+            m1 = fmaxf(fmaxf(m1, __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
         }
-        mx = fmaxf(mx, fmaxf(m0, m1));
+    } else {
+#pragma unroll
+        for (int i = 0; i < BN; ++i) m0 = fmaxf(m0, i < nv ? __uint_as_float(x[i]) : kNegInf);
     }
-    return mx;
+    return fmaxf(m0, m1);
 }
 
-// Raises the references of the rows that ask for it above every score in
-// columns [c, BN), by a whole number, and scales what was weighed against the
-// old ones (l, O, and this tile's P of the columns before c) by that power of two.
-template <int BN, int DPAD, bool KV8>
-__device__ __forceinline__ void raise_reference(uint32_t ts, uint32_t to, int c, int nv, float scale, bool over, float &m,
-                                                float &l) {
-    const float d = largest_score<BN>(ts, c, nv) * scale - m;
+// The weights 2^(x scale - m) of a row's tile, rounded to pairs of BF16 (f16),
+// and their sum before that; 0 past the live columns.
+template <int BN, bool KV8>
+__device__ __forceinline__ float weigh(const uint32_t (&x)[BN], int nv, float scale, float m, uint32_t (&pk)[BN / 2]) {
+    const float off = m == -__int_as_float(0x7f800000) ? 0.f : m;
+    const uint64_t scale2 = tc::pack_f32x2(scale, scale), off2 = tc::pack_f32x2(-off, -off);
+    uint64_t sum[4] = {0, 0, 0, 0};
+    const bool whole = nv >= BN;
+#pragma unroll
+    for (int i = 0; i < BN; i += 2) {
+        float a, b;
+        tc::unpack_f32x2(tc::fma_f32x2(tc::pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2), a, b);
+        a = dev::exp2_approx(a);
+        b = dev::exp2_approx(b);
+        if (!whole) {
+            a = i < nv ? a : 0.f;
+            b = i + 1 < nv ? b : 0.f;
+        }
+        sum[(i / 2) & 3] = tc::add_f32x2(sum[(i / 2) & 3], tc::pack_f32x2(a, b));
+        pk[i / 2] = pack2<KV8>(a, b);
+    }
+    float a, b;
+    tc::unpack_f32x2(tc::add_f32x2(tc::add_f32x2(sum[0], sum[1]), tc::add_f32x2(sum[2], sum[3])), a, b);
+    return a + b;
+}
+
+// Raises the references of the rows that ask for it to `top` at least, by a
+// whole number, and scales l and O, which were weighed against the old ones, by
+// that power of two.
+template <int DPAD>
+__device__ __forceinline__ void raise_reference(uint32_t to, float top, bool over, float &m, float &l) {
+    const float d = top - m;
     const float k = over && d > 0.f ? ceilf(d) : 0.f;
     const float f = k < 127.f ? __int_as_float((127 - static_cast<int>(k)) << 23) : 0.f;
     m += k;
@@ -269,18 +300,6 @@ __device__ __forceinline__ void raise_reference(uint32_t ts, uint32_t to, int c,
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
         tc::st_32x32(to + i, x);
-    }
-#pragma unroll 1
-    for (int i = 0; i < c / 2; i += 16) {
-        uint32_t x[32];  // (16 columns of P; the 16 behind them are read along)
-        tc::ld_32x32(ts + i, x);
-        tc::wait_ld(x);
-        uint32_t y[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            y[e] = KV8 ? dev::pack_f16x2(dev::f16_lo_f32(x[e]) * f, dev::f16_hi_f32(x[e]) * f)
-                       : dev::pack_bf16x2(dev::bf16_lo_f32(x[e]) * f, dev::bf16_hi_f32(x[e]) * f);
-        tc::st_32x16(ts + i, y);
     }
 }
 
@@ -378,6 +397,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     const int bs = static_cast<int>(p.block_size.d);
     const int D = p.head_dim;
     Segment sg;
+    // Registers: a softmax thread holds a whole tile row.  384 threads were
+    // launched with 168 each: 128 x 88 + 256 x 208 is what all of them have.
+    static_assert(L::kThreads == 384 && 88 + 2 * 208 <= 3 * 168, "the shares add up to the launch's registers");
+
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
 
     if (warp == 0 || (!KV8 && warp == 2)) {
         // ---- loads: K and V tiles in the order the products take them ------------
@@ -493,122 +518,125 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                                        100000000ull);
         }
     } else if (warp == 1) {
-        // ---- products ---------------------------------------------------------------
-        int st = 0;
-        uint32_t ph = 0;
-        uint32_t pph[2] = {0, 0}, qph[2] = {0, 0};
-        bool ok = true;
-        const uint32_t qa = base + L::q, ra = base + L::ring;
-        // the next tile of the ring (K or V), once it has landed
-        auto take = [&](int &stage) {
-            if (!wait_bar(bar_full + 8 * st, ph, gave_up)) return false;
-            stage = st;
-            if (++st == NST) {
-                st = 0;
-                ph ^= 1;
-            }
-            tc::fence_after();
-            return true;
-        };
-        const uint64_t q_desc = tc::smem_desc(qa, 16), k_desc = tc::smem_desc(ra, 16), v_desc = tc::smem_desc(ra, BN * 128);
-        const bool issuer = tc::elect_one();
-        auto scores = [&](int buf, int qt, int stage) {
-            const uint64_t qd = q_desc + qt * (kRowTile * DPAD * 2 / 16), kd = k_desc + stage * (L::kStageBytes / 16);
-            if (issuer) {
+        // ---- products: one thread issues them all, in the order S, P V, S, ... of
+        // the streams in turn.  What it waits for is looked at as early as the order
+        // allows: the queue of products is short, and whatever this thread spends
+        // between two of them the tensor core may spend idle.
+        if (tc::elect_one()) {
+            int st = 0;
+            uint32_t ph = 0, pph = 0, qph = 0;  // phases: of the ring; a bit for each stream
+            bool ok = true;
+            const uint32_t qa = base + L::q, ra = base + L::ring;
+            const uint64_t q_desc = tc::smem_desc(qa, 16), k_desc = tc::smem_desc(ra, 16), v_desc = tc::smem_desc(ra, BN * 128);
+            // the next tile of the ring (K or V), once it has landed
+            auto take = [&](int &stage) {
+                stage = st;
+                if (!wait_one(bar_full + 8 * st, ph, gave_up)) return false;
+                if (++st == NST) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                return true;
+            };
+            auto scores = [&](int buf, int qt, int stage) {
+                const uint64_t qd = q_desc + qt * (kRowTile * DPAD * 2 / 16), kd = k_desc + stage * (L::kStageBytes / 16);
+                tc::fence_after();
 #pragma unroll
                 for (int k = 0; k < DPAD / 16; ++k)
                     tc::mma_ss(tmem + buf * 128, qd + ((k / 4) * (kRowTile * 128) + (k % 4) * 32) / 16,
                                kd + ((k / 4) * (BN * 128) + (k % 4) * 32) / 16, kDescS, k > 0);
                 tc::commit(bar_s + 8 * buf);
-            }
-            __syncwarp();
-        };
-        auto values = [&](int buf, int o, int stage, bool accumulate, bool done) {
-            const uint64_t vd = v_desc + stage * (L::kStageBytes / 16);
-            if (issuer) {
+            };
+            auto values = [&](int buf, int o, int stage, bool accumulate, bool done) {
+                const uint64_t vd = v_desc + stage * (L::kStageBytes / 16);
+                tc::fence_after();
 #pragma unroll
                 for (int k = 0; k < BN / 16; ++k)
                     tc::mma_ts(tmem + 256 + o * DPAD, tmem + buf * 128 + k * 8, vd + k * (2048 / 16), kDescO, accumulate || k > 0);
                 if (done) tc::commit(bar_o + 8 * o);
-            }
-            __syncwarp();
-        };
-        auto release = [&](int stage) {
-            if (issuer) {
+            };
+            auto release = [&](int stage) {
                 if (KV8)
                     tc::commit(bar_empty + 8 * stage);
                 else
                     tc::commit_both(bar_empty + 8 * stage);
-            }
-            __syncwarp();
-        };
-        auto weights = [&](int buf) {
-            if (!wait_bar(bar_p + 8 * buf, pph[buf], gave_up)) return false;
-            pph[buf] ^= 1;
-            tc::fence_after();
-            return true;
-        };
-        auto queries = [&](int t) {
-            if (!wait_bar(bar_q + 8 * t, qph[t], gave_up)) return false;
-            qph[t] ^= 1;
-            tc::fence_after();
-            return true;
-        };
-        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
-            const int n = sg.n, live = sg.live;
-            int ks = 0, vs = 0;
-            if (live > 0 && !(ok = queries(0))) break;
-            if (!ONE && sg.two) {
+            };
+            auto weights = [&](int buf) {
+                const bool got = wait_one(bar_p + 8 * buf, (pph >> buf) & 1, gave_up);
+                pph ^= 1u << buf;
+                return got;
+            };
+            auto queries = [&](int t) {
+                const bool got = wait_one(bar_q + 8 * t, (qph >> t) & 1, gave_up);
+                qph ^= 1u << t;
+                return got;
+            };
+            while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
+                const int n = sg.n, live = sg.live;
+                int ks = 0, vs = 0;
+                if (live > 0 && !(ok = queries(0))) break;
                 if (!(ok = take(ks))) break;
-                if (live > 0) {
-                    scores(0, 0, ks);
-                    if (!(ok = queries(1))) break;
-                    scores(1, 1, ks);
-                }
-                release(ks);
-                for (int j = 0; ok && j < n; ++j) {
-                    if (!(ok = take(vs))) break;
-                    const bool now = j < live, more = j + 1 < live;
-                    for (int t = 0; ok && t < 2; ++t) {
-                        if (now) {
-                            if (!(ok = weights(t))) break;
-                            values(t, t, vs, j > 0, !more);
-                        }
-                        if (t == 0 && j + 1 < n && !(ok = take(ks))) break;
-                        if (more) scores(t, t, ks);
+                if (!ONE && sg.two) {
+                    if (live > 0) {
+                        scores(0, 0, ks);
+                        if (!(ok = queries(1))) break;
+                        scores(1, 1, ks);
                     }
-                    if (!ok) break;
-                    release(vs);
-                    if (j + 1 < n) release(ks);
-                }
-            } else {
-                // scores of tile j, whose keys are the next of the ring
-                auto next_scores = [&](int j) {
-                    if (j >= n) return true;
-                    if (!take(ks)) return false;
-                    if (j < live) scores(j & 1, 0, ks);
                     release(ks);
-                    return true;
-                };
-                ok = next_scores(0) && next_scores(1);
-                for (int j = 0; ok && j < n; ++j) {
                     if (!(ok = take(vs))) break;
-                    if (j < live) {
-                        const int t = j & 1;
-                        if (!(ok = weights(t))) break;
-                        values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= live);
+                    for (int j = 0; ok && j < n; ++j) {
+                        const bool now = j < live, more = j + 1 < live, next = j + 1 < n;
+                        const int v = vs;
+                        if (next && !(ok = take(ks))) break;
+                        if (now) {
+                            if (!(ok = weights(0))) break;
+                            values(0, 0, v, j > 0, !more);
+                        }
+                        if (more) scores(0, 0, ks);
+                        if (now) {
+                            if (!(ok = weights(1))) break;
+                            values(1, 1, v, j > 0, !more);
+                        }
+                        release(v);  // (before the scores: a commit waits for all that came before)
+                        if (more) scores(1, 1, ks);
+                        if (next) {
+                            release(ks);
+                            ok = take(vs);
+                        }
                     }
-                    release(vs);
-                    ok = next_scores(j + 2);
+                } else {
+                    // scores of tile j, whose keys are the next of the ring
+                    auto next_scores = [&](int j) {
+                        if (j < live) scores(j & 1, 0, ks);
+                        release(ks);
+                    };
+                    next_scores(0);
+                    if (n > 1) {
+                        if (!(ok = take(ks))) break;
+                        next_scores(1);
+                    }
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (!(ok = take(vs))) break;
+                        const bool next = j + 2 < n;
+                        if (next && !(ok = take(ks))) break;
+                        if (j < live) {
+                            const int t = j & 1;
+                            if (!(ok = weights(t))) break;
+                            values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= live);
+                        }
+                        release(vs);
+                        if (next) next_scores(j + 2);
+                    }
                 }
             }
+            if (!ok) {
+                // let the products in flight end before TMEM is freed
+                tc::commit(bar_tail);
+                dev::mbar_wait_bounded(bar_tail, 0, 100000000ull);
+            }
         }
-        if (!ok && issuer) {
-            // let the products in flight end before TMEM is freed
-            tc::commit(bar_tail);
-            dev::mbar_wait_bounded(bar_tail, 0, 100000000ull);
-        }
-    } else if (KV8 && warp < 4) {
+        __syncwarp();
+    } else if (KV8) {
         // ---- FP8: each landed tile of codes into an f16 tile of the ring -------------
         // (exact: every E4M3 value is an f16 value; k_scale is in the softmax
         // scale, v_scale in the merge).  A quarter-warp takes two rows x 64 codes,
@@ -667,13 +695,16 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (ok && v >= 0) ok = convert(v < sg.live, true, sg.plen - (sg.tile0 + v * sg.stride) * BN);
             }
         }
-    } else if (warp >= 4 && warp < (ONE ? 8 : 12)) {
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (warp < (ONE ? 8 : 12)) {
         // ---- softmax: a thread per row -----------------------------------------------
         const int t = (warp - 4) >> 2;            // the stream
         const int r = (warp & 3) * 32 + lane;     // the row of its tile
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t to = tmem + lanes + 256 + t * DPAD;
-        uint32_t sph[2] = {0, 0}, oph[2] = {0, 0}, xph = 0;
+        uint32_t sph = 0, oph = 0, xph = 0;  // phases, a bit for each buffer or stream
         bool ok = true;
         // FP8: the rows' scales, in turn in two places: the other stream may still
         // have to read the last segment's when this one's are written (it has by
@@ -740,80 +771,44 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             for (int j = step == 2 ? t : 0; j < sg.live; j += step) {
                 const int buf = ONE ? (j & 1) : t;
                 const uint32_t ts = tmem + lanes + buf * 128;
-                if (!(ok = wait_bar(bar_s + 8 * buf, sph[buf], gave_up))) break;
-                sph[buf] ^= 1;
+                if (!(ok = wait_bar(bar_s + 8 * buf, (sph >> buf) & 1, gave_up))) break;
+                sph ^= 1u << buf;
                 tc::fence_after();
                 if (KV8 && first) scale = row_scale[(two ? t * kRowTile : 0) + r];
                 const int nv = sg.plen - (sg.tile0 + j * sg.stride) * BN;
                 // -- A row's reference m is the largest score of its first tile; after
                 // that no maximum is taken: weights may be as large as kLift, and
-                // only when a row's weights of 32 columns sum to more does its warp
-                // look at the scores again and raise m (by a whole number, so that
-                // P, l and O are scaled exactly).  FP32 and BF16 hold such weights as
-                // exactly as weights below 1; kLift is what f16 holds.
+                // only when a row's weights of a tile sum to more does its warp look
+                // at the scores again and raise m (by a whole number, so that l and O
+                // are scaled exactly).  FP32 and BF16 hold such weights as exactly as
+                // weights below 1; kLift is what f16 holds.
+                uint32_t x[BN];
+                tc::ld_columns<BN>(ts, x);
                 if (__any_sync(0xffffffffu, m == kNegInf)) {
-                    const float mx = largest_score<BN>(ts, 0, nv) * scale;
+                    const float mx = largest_of<BN>(x, nv) * scale;
                     m = m == kNegInf ? mx : m;
                 }
+                uint32_t pk[BN / 2];
+                float sum = weigh<BN, KV8>(x, nv, scale, m, pk);
                 bool waited = !ONE || first;  // the last product onto O is known to be done
                 first = false;
-                float off = m == kNegInf ? 0.f : m;
-                bool lifted = false;
-                const uint64_t scale2 = tc::pack_f32x2(scale, scale);
-                auto weigh = [&](const uint32_t (&x)[32], int c) {
-                    uint32_t pk[16];
-                    float sa, sb;
-                    auto compute = [&] {
-                        const bool whole = nv - c >= 32;
-                        const uint64_t off2 = tc::pack_f32x2(-off, -off);
-                        uint64_t sum2 = 0;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float ea, eb;
-                            tc::unpack_f32x2(
-                                tc::fma_f32x2(tc::pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2), ea, eb);
-                            ea = dev::exp2_approx(ea);
-                            eb = dev::exp2_approx(eb);
-                            if (!whole) {
-                                ea = c + i < nv ? ea : 0.f;
-                                eb = c + i + 1 < nv ? eb : 0.f;
-                            }
-                            sum2 = tc::add_f32x2(sum2, tc::pack_f32x2(ea, eb));
-                            pk[i / 2] = pack2<KV8>(ea, eb);
-                        }
-                        tc::unpack_f32x2(sum2, sa, sb);
-                    };
-                    compute();
-                    const bool over = !(sa + sb <= kLift);
-                    if (!lifted && __any_sync(0xffffffffu, over)) {
-                        lifted = true;
-                        if (!waited) {
-                            ok = wait_bar(bar_o, oph[0], gave_up);
-                            oph[0] ^= 1;
-                            waited = true;
-                        }
+                const bool over = !(sum <= kLift);
+                if (__any_sync(0xffffffffu, over)) {
+                    if (!waited) {
+                        ok = wait_bar(bar_o, oph & 1, gave_up);
+                        oph ^= 1;
+                        waited = true;
                         tc::fence_after();
-                        raise_reference<BN, DPAD, KV8>(ts, to, c, nv, scale, over, m, l);
-                        off = m == kNegInf ? 0.f : m;
-                        compute();
                     }
-                    l += sa + sb;
-                    tc::st_32x16(ts + c / 2, pk);  // over S columns that were read before
-                };
-                uint32_t xa[32], xb[32];
-                tc::ld_32x32(ts, xa);
-#pragma unroll 1
-                for (int c = 0; c < BN; c += 64) {
-                    tc::wait_ld(xa);
-                    tc::ld_32x32(ts + c + 32, xb);
-                    weigh(xa, c);
-                    tc::wait_ld(xb);
-                    if (c + 64 < BN) tc::ld_32x32(ts + c + 64, xa);
-                    weigh(xb, c + 32);
+                    tc::ld_columns<BN>(ts, x);
+                    raise_reference<DPAD>(to, largest_of<BN>(x, nv) * scale, over, m, l);
+                    sum = weigh<BN, KV8>(x, nv, scale, m, pk);
                 }
+                l += sum;
+                tc::st_columns<BN / 2>(ts, pk);  // over S, which has been read
                 if (ONE && !waited) {  // (each phase of the barrier is waited for, in order)
-                    ok = wait_bar(bar_o, oph[0], gave_up) && ok;
-                    oph[0] ^= 1;
+                    ok = wait_bar(bar_o, oph & 1, gave_up) && ok;
+                    oph ^= 1;
                 }
                 if (!ok) break;
                 tc::wait_st();
@@ -835,9 +830,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 const bool in = row < sg.rows;
                 if (in) *reinterpret_cast<float2 *>(p.part_ml + (at + row) * 2) = make_float2(m, l);
                 if (sg.live > 0) {
-                    if (!(ok = wait_bar(bar_o + 8 * t, oph[t], gave_up))) break;
-                    oph[0] ^= 1;
-                    oph[1] ^= 1;
+                    if (!(ok = wait_bar(bar_o + 8 * t, (oph >> t) & 1, gave_up))) break;
+                    oph ^= 3;
                     tc::fence_after();
 #pragma unroll 1
                     for (int c = 0; c < DPAD; c += 32) {
@@ -858,8 +852,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 xph ^= 1;
                 for (int k = 0; k < 2 && ok; ++k) {
                     if (k < sg.live) {
-                        ok = wait_bar(bar_o + 8 * k, oph[k], gave_up);
-                        oph[k] ^= 1;
+                        ok = wait_bar(bar_o + 8 * k, (oph >> k) & 1, gave_up);
+                        oph ^= 1u << k;
                     }
                 }
                 if (!ok) break;
@@ -896,6 +890,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 xph ^= 1;
             }
         }
+    }
     }
     // The peer may still send halves of tiles and release stages: shared memory
     // stays until both are done.

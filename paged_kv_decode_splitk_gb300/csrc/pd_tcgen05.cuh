@@ -53,13 +53,15 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ void st_32x16(uint32_t addr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+// No instruction: r's values were waited for (by another register's wait).
+__device__ __forceinline__ void hold(uint32_t (&r)[32]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void st_32x32(uint32_t addr, const uint32_t (&r)[32]) {
     asm volatile(
@@ -71,6 +73,21 @@ __device__ __forceinline__ void st_32x32(uint32_t addr, const uint32_t (&r)[32])
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+
+// N columns (a multiple of 32) at once, loaded together and waited for.
+template <int N>
+__device__ __forceinline__ void ld_columns(uint32_t addr, uint32_t (&r)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) ld_32x32(addr + c, reinterpret_cast<uint32_t(&)[32]>(r[c]));
+    wait_ld(reinterpret_cast<uint32_t(&)[32]>(r[0]));
+#pragma unroll
+    for (int c = 32; c < N; c += 32) hold(reinterpret_cast<uint32_t(&)[32]>(r[c]));
+}
+template <int N>
+__device__ __forceinline__ void st_columns(uint32_t addr, const uint32_t (&r)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) st_32x32(addr + c, reinterpret_cast<const uint32_t(&)[32]>(r[c]));
 }
 
 // Two FP32 operations in one instruction, on the halves of 64-bit registers.

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -21,8 +22,7 @@ static_assert(kMaxGroups == PD_MAX_PREFIX_GROUPS, "pd.h");
 
 constexpr int kOwnUnits = 152 * 8;  // units of the own-token pass that are enough
 constexpr int kMergeWarps = 8;
-constexpr int kMergeCols = 128;  // columns of a row one warp merges (4 per lane)
-constexpr int kMergeBatch = 8;   // partials whose o are loaded together
+constexpr int kMergeBatch = 4;   // partials whose o are loaded together
 
 // The team whose range [W c / C, W (c + 1) / C) holds unit u.
 __device__ __forceinline__ int team_of_unit(long long u, int C, long long W) {
@@ -32,61 +32,70 @@ __device__ __forceinline__ int team_of_unit(long long u, int C, long long W) {
     return static_cast<int>(num / W);
 }
 
-// One warp per (sequence, query head, 128 columns) folds the row's partials:
-// first those of its prefix, in the order of the teams that made them (both
-// CTAs' where they took the tiles in turn), then its own splits.
-// With M the largest reference and w_i = 2^(m_i - M),
+// DPAD / 8 lanes per (sequence, query head), 8 columns each, fold the row's
+// partials: first those of its prefix, in the order of the teams that made them
+// (both CTAs' where they took the tiles in turn), then its own splits.  With M the
+// largest reference and w_i = 2^(m_i - M),
 //   out = sum_i w_i o_i / sum_i w_i l_i,
 // 0 where the row has no token at all.  Bound by latency on small batches (the
-// chain: group, plan, (m, l), o) and by reading the partials from L2 on large.
-__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const __grid_constant__ MergeParams p) {
+// chain is the plan, then m, l and o together) and by reading the partials from
+// L2 on large ones; 64 registers keep four blocks on an SM, so that a batch of
+// 8192 rows is one wave.
+template <int DPAD>
+__global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const __grid_constant__ MergeParams p) {
+    constexpr int LPR = DPAD / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+    constexpr int BR = block_rows(DPAD);
     const float kNegInf = -__int_as_float(0x7f800000);
     dev::griddep_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int D = p.head_dim, N = p.num_splits;
-    const int BR = block_rows(p.dpad);
-    const int chunks = D > kMergeCols ? 2 : 1;
-    const long long item_id = static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
-    if (item_id >= static_cast<long long>(p.num_seqs) * p.num_q_heads * chunks) return;
-    const long long row = item_id >> (chunks - 1);
-    const int d0 = static_cast<int>(item_id - row * chunks) * kMergeCols + lane * 4;
-    const bool cols = d0 < D;
-    const int s = fast_div(static_cast<int>(row), p.fd_hq);
-    const int h = static_cast<int>(row - static_cast<long long>(s) * p.num_q_heads);
-    const int kvh = fast_div(h, p.fd_group);
+    const int lane = threadIdx.x & 31, sub = lane % LPR, mine = lane / LPR, head_lane = mine * LPR;
+    const int D = p.head_dim, N = p.num_splits, rows = p.num_seqs * p.num_q_heads;
+    const int row = (blockIdx.x * kMergeWarps + (threadIdx.x >> 5)) * RPW + mine;
+    const int d0 = sub * 8;
+    const bool in = row < rows, cols = in && d0 < D;
+    const int s = in ? fast_div(row, p.fd_hq) : 0;
+    const int h = row - s * p.num_q_heads;
+    const int kvh = in ? fast_div(h, p.fd_group) : 0;
     dev::griddep_wait();
 
     // ---- the row's group: the last one that begins at or before the sequence ----
-    int L = p.context_lens[s];
+    int L = in ? p.context_lens[s] : 0;
     const long long W = *p.plan_total;
     GroupPlan g = {};
     for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-        GroupPlan mine = {};
-        if (g0 + lane < p.num_groups) mine = p.plan_groups[g0 + lane];
-        const int below = __popc(__ballot_sync(0xffffffffu, g0 + lane < p.num_groups && mine.first_seq <= s));
-        if (below == 0) break;
-        const int src = below - 1;
-        g.first_unit = __shfl_sync(0xffffffffu, mine.first_unit, src);
-        g.first_item = __shfl_sync(0xffffffffu, mine.first_item, src);
-        g.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
-        g.first_seq = __shfl_sync(0xffffffffu, mine.first_seq, src);
-        g.rows = __shfl_sync(0xffffffffu, mine.rows, src);
-        g.blocks = __shfl_sync(0xffffffffu, mine.blocks, src);
+        GroupPlan one = {};
+        if (g0 + lane < p.num_groups) one = p.plan_groups[g0 + lane];
+        int below = 0;
+#pragma unroll
+        for (int r = 0; r < RPW; ++r) {
+            const int sr = __shfl_sync(0xffffffffu, s, r * LPR);
+            const unsigned b = __ballot_sync(0xffffffffu, g0 + lane < p.num_groups && one.first_seq <= sr);
+            if (mine == r) below = __popc(b);
+        }
+        const int src = below > 0 ? below - 1 : 0;
+        GroupPlan f;
+        f.first_unit = __shfl_sync(0xffffffffu, one.first_unit, src);
+        f.first_item = __shfl_sync(0xffffffffu, one.first_item, src);
+        f.tiles = __shfl_sync(0xffffffffu, one.tiles, src);
+        f.first_seq = __shfl_sync(0xffffffffu, one.first_seq, src);
+        f.rows = __shfl_sync(0xffffffffu, one.rows, src);
+        f.blocks = __shfl_sync(0xffffffffu, one.blocks, src);
+        if (below > 0) g = f;
     }
     int nparts = 0, step = 2;      // prefix slots of the row, 2 apart, or (both CTAs') 1
     long long first = 0;           // (slot, row) of its first partial
-    if (W > 0) {
-        const int x = (s - g.first_seq) * p.group + (h - kvh * p.group);
-        if (g.tiles > 0 && x < g.rows) {
-            const int block = x / BR, r = x - block * BR;
-            const int pairs = g.blocks >> 1, odd = g.blocks & 1, of_single = (g.tiles + 1) >> 1;
-            const bool pair = block < 2 * pairs;
-            const int item = block >> 1, places = pair ? g.tiles : of_single;
-            const long long u = g.first_unit + kvh * (static_cast<long long>(pairs) * g.tiles + (odd ? of_single : 0)) +
-                                static_cast<long long>(item) * g.tiles;
-            const int C = teams_of(W, p.teams);
-            const int c = team_of_unit(lane == 0 ? u : u + places - 1, C, W);
-            const int c0 = __shfl_sync(0xffffffffu, c, 0), c1 = __shfl_sync(0xffffffffu, c, 1);
+    const int x = (s - g.first_seq) * p.group + (h - kvh * p.group);
+    const bool has = W > 0 && in && g.tiles > 0 && x < g.rows;
+    {
+        const int block = has ? x / BR : 0, r = x - block * BR;
+        const int pairs = g.blocks >> 1, odd = g.blocks & 1, of_single = (g.tiles + 1) >> 1;
+        const bool pair = block < 2 * pairs;
+        const int item = block >> 1, places = pair ? g.tiles : of_single;
+        const long long u = g.first_unit + kvh * (static_cast<long long>(pairs) * g.tiles + (odd ? of_single : 0)) +
+                            static_cast<long long>(item) * g.tiles;
+        const int C = teams_of(W, p.teams);
+        const int c = has ? team_of_unit(sub == 0 ? u : u + places - 1, C, W) : 0;
+        const int c0 = __shfl_sync(0xffffffffu, c, head_lane), c1 = __shfl_sync(0xffffffffu, c, head_lane + 1);
+        if (has) {
             step = pair ? 2 : 1;
             nparts = (c1 - c0 + 1) * (pair ? 1 : 2);
             const long long slot = 2ll * (g.first_item + kvh * (pairs + odd) + item + c0) + (pair ? block & 1 : 0);
@@ -95,81 +104,91 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const __
     }
     L = L < 0 ? 0 : (L > p.max_tokens ? p.max_tokens : L);
     const int chunk = split_chunk_tokens_fd(L, p.fd_split, p.fd_bs, p.min_kv_per_split);
-    const int own = L > 0 ? (L + chunk - 1) / chunk : 0;
-    const int total = nparts + own;
+    const int total = nparts + (L > 0 ? (L + chunk - 1) / chunk : 0);
 
     // where partial i lies: (m, l) and, for this lane's columns, o
     auto ml_of = [&](int i) -> const float * {
-        if (i >= nparts) return p.own_ml + (row * N + (i - nparts)) * 2;
-        return p.part_ml + (first + static_cast<long long>(i * step) * BR) * 2;
+        if (i >= nparts) return p.own_ml + (static_cast<long long>(row) * N + (i - nparts)) * 2;
+        return p.part_ml + (first + i * step * BR) * 2;
     };
+    const float *part = p.part_o + (first / BR * LPR + sub) * (BR * 8) + (first % BR) * 8;
     auto o_of = [&](int i) -> const float * {
-        if (i >= nparts) return p.own_o + (row * N + (i - nparts)) * D + d0;
-        const long long at = first + static_cast<long long>(i * step) * BR;
-        const long long sl = at / BR, r = at - sl * BR;
-        return p.part_o + ((sl * (p.dpad / 8) + d0 / 8) * BR + r) * 8 + (d0 & 4);
+        if (i >= nparts) return p.own_o + (static_cast<long long>(row) * N + (i - nparts)) * D + d0;
+        return part + static_cast<long long>(i) * step * (LPR * BR * 8);
     };
 
-    // ---- the fold, 32 partials at a time: lane i has (m, l) of partial i ----
-    float M = kNegInf, lsum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < total; i0 += 32) {
-        const int n = min(32, total - i0);
-        float2 v = make_float2(kNegInf, 0.f);
-        if (lane < n) v = *reinterpret_cast<const float2 *>(ml_of(i0 + lane));
-        float4 o[kMergeBatch];
+    // ---- the fold, LPR partials at a time: lane i of the row has (m, l) of partial i ----
+    int most = total;  // (all rows of a warp go through the loops together)
 #pragma unroll
-        for (int j = 0; j < kMergeBatch; ++j)  // (asked for together with m and l)
-            o[j] = cols && j < n ? *reinterpret_cast<const float4 *>(o_of(i0 + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int off = LPR; off < 32; off <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+    float M = kNegInf, lsum = 0.f;
+    float acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+    for (int i0 = 0; i0 < most; i0 += LPR) {
+        float2 v = make_float2(kNegInf, 0.f);
+        if (i0 + sub < total) v = *reinterpret_cast<const float2 *>(ml_of(i0 + sub));
+        float4 o[kMergeBatch][2];
+        auto ask = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < kMergeBatch; ++j) {
+                o[j][0] = o[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (cols && i0 + j0 + j < total) {
+                    const float4 *at = reinterpret_cast<const float4 *>(o_of(i0 + j0 + j));
+                    o[j][0] = at[0];
+                    o[j][1] = at[1];
+                }
+            }
+        };
+        ask(0);  // (together with m and l)
         // a partial without a token has l = 0, and its o was not written
         const bool dead = v.y == 0.f;
         float top = dead ? kNegInf : v.x;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        for (int off = LPR / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
         const float Mn = fmaxf(M, top);
         const float keep = M == kNegInf ? 0.f : dev::exp2_approx(M - Mn);
         M = Mn;
         const float w = dead ? 0.f : dev::exp2_approx(v.x - M);
         float wl = dead ? 0.f : w * v.y;
-        const float wo = i0 + lane < nparts ? w * p.v_scale : w;
+        const float wo = i0 + sub < nparts ? w * p.v_scale : w;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
+        for (int off = LPR / 2; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
         lsum = lsum * keep + wl;
-        acc.x *= keep;
-        acc.y *= keep;
-        acc.z *= keep;
-        acc.w *= keep;
-        for (int j0 = 0; j0 < n; j0 += kMergeBatch) {
-            if (j0 > 0) {
 #pragma unroll
-                for (int j = 0; j < kMergeBatch; ++j)
-                    o[j] = cols && j0 + j < n ? *reinterpret_cast<const float4 *>(o_of(i0 + j0 + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+        for (int k = 0; k < 8; ++k) acc[k] *= keep;
+        for (int j0 = 0; j0 < min(LPR, most - i0); j0 += kMergeBatch) {
+            if (j0 > 0) ask(j0);
 #pragma unroll
             for (int j = 0; j < kMergeBatch; ++j) {
-                const float wj = __shfl_sync(0xffffffffu, wo, (j0 + j) & 31);
-                const bool skip = __shfl_sync(0xffffffffu, dead, (j0 + j) & 31);
-                if (j0 + j < n && !skip) {
-                    acc.x = fmaf(o[j].x, wj, acc.x);
-                    acc.y = fmaf(o[j].y, wj, acc.y);
-                    acc.z = fmaf(o[j].z, wj, acc.z);
-                    acc.w = fmaf(o[j].w, wj, acc.w);
+                const int src = head_lane + ((j0 + j) & (LPR - 1));
+                const float wj = __shfl_sync(0xffffffffu, wo, src);
+                const bool skip = __shfl_sync(0xffffffffu, dead, src);
+                if (i0 + j0 + j < total && !skip) {
+                    acc[0] = fmaf(o[j][0].x, wj, acc[0]);
+                    acc[1] = fmaf(o[j][0].y, wj, acc[1]);
+                    acc[2] = fmaf(o[j][0].z, wj, acc[2]);
+                    acc[3] = fmaf(o[j][0].w, wj, acc[3]);
+                    acc[4] = fmaf(o[j][1].x, wj, acc[4]);
+                    acc[5] = fmaf(o[j][1].y, wj, acc[5]);
+                    acc[6] = fmaf(o[j][1].z, wj, acc[6]);
+                    acc[7] = fmaf(o[j][1].w, wj, acc[7]);
                 }
             }
         }
     }
     if (!cols) return;
-    const bool none = lsum == 0.f;
-    uint2 pk;
-    pk.x = dev::pack_bf16x2(none ? 0.f : __fdiv_rn(acc.x, lsum), none ? 0.f : __fdiv_rn(acc.y, lsum));
-    pk.y = dev::pack_bf16x2(none ? 0.f : __fdiv_rn(acc.z, lsum), none ? 0.f : __fdiv_rn(acc.w, lsum));
-    *reinterpret_cast<uint2 *>(p.out + row * D + d0) = pk;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = lsum == 0.f ? 0.f : __fdiv_rn(acc[k], lsum);
+    *reinterpret_cast<uint4 *>(p.out + static_cast<long long>(row) * D + d0) =
+        make_uint4(dev::pack_bf16x2(acc[0], acc[1]), dev::pack_bf16x2(acc[2], acc[3]), dev::pack_bf16x2(acc[4], acc[5]),
+                   dev::pack_bf16x2(acc[6], acc[7]));
 }
 
 cudaError_t launch_prefix_merge(const MergeParams &p, cudaStream_t stream) {
-    const long long items = static_cast<long long>(p.num_seqs) * p.num_q_heads * (p.head_dim > kMergeCols ? 2 : 1);
+    const int rows = p.num_seqs * p.num_q_heads, of_block = kMergeWarps * (256 / p.dpad);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((items + kMergeWarps - 1) / kMergeWarps));
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + of_block - 1) / of_block));
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -177,7 +196,9 @@ cudaError_t launch_prefix_merge(const MergeParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_merge_kernel, p);
+    if (p.dpad == 64) return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<64>, p);
+    if (p.dpad == 128) return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<128>, p);
+    return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<256>, p);
 }
 
 int sm_count_of_device() {
@@ -308,7 +329,9 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     p.fd_group = make_fastdiv(group);
     p.tok_dim = view.tok_dim;
     p.box_tokens = view.box_tokens;
-    p.scale_log2 = static_cast<float>(std::fabs(scale));
+    // A scale of 0 becomes the smallest above it: a masked score, -infinity, then
+    // still weighs 0, and every other still (all but) nothing against its reference.
+    p.scale_log2 = std::max(static_cast<float>(std::fabs(scale)), FLT_MIN);
     p.negative = scale < 0;
     p.max_items = static_cast<int>(lay.max_items);
     p.part_ml = reinterpret_cast<float *>(ws + lay.part_ml);

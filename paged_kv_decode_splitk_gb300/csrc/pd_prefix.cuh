@@ -45,6 +45,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <cfloat>
+
 #include "pd.h"
 #include "pd_device.cuh"
 #include "pd_prefix.h"
@@ -238,42 +240,39 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // Sum of a tile's weights above which a row's reference is raised.
 constexpr float kLift = 32768.f;
 
-// The largest of a row's live scores (columns below nv) of a tile.
+// Scores of the columns past the live ones become -infinity.
 template <int BN>
-__device__ __forceinline__ float largest_of(const uint32_t (&x)[BN], int nv) {
-    const float kNegInf = -__int_as_float(0x7f800000);
-    float m0 = kNegInf, m1 = kNegInf;
-    if (nv >= BN) {
+__device__ __forceinline__ void mask_columns(uint32_t (&x)[BN], int nv) {
 #pragma unroll
-        for (int i = 0; i < BN; i += 4) {
-            m0 = fmaxf(fmaxf(m0, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-            m1 = fmaxf(fmaxf(m1, __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
-        }
-    } else {
+    for (int i = 0; i < BN; ++i)
+        if (i >= nv) x[i] = 0xff800000u;
+}
+
+// The largest of a row's scores of a tile.
+template <int BN>
+__device__ __forceinline__ float largest_of(const uint32_t (&x)[BN]) {
+    float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[1]);
 #pragma unroll
-        for (int i = 0; i < BN; ++i) m0 = fmaxf(m0, i < nv ? __uint_as_float(x[i]) : kNegInf);
+    for (int i = 2; i < BN; i += 2) {
+        m0 = fmaxf(m0, __uint_as_float(x[i]));
+        m1 = fmaxf(m1, __uint_as_float(x[i + 1]));
     }
     return fmaxf(m0, m1);
 }
 
 // The weights 2^(x scale - m) of a row's tile, rounded to pairs of BF16 (f16),
-// and their sum before that; 0 past the live columns.
+// and their sum before that (scale > 0, so that a masked score weighs 0).
 template <int BN, bool KV8>
-__device__ __forceinline__ float weigh(const uint32_t (&x)[BN], int nv, float scale, float m, uint32_t (&pk)[BN / 2]) {
+__device__ __forceinline__ float weigh(const uint32_t (&x)[BN], float scale, float m, uint32_t (&pk)[BN / 2]) {
     const float off = m == -__int_as_float(0x7f800000) ? 0.f : m;
     const uint64_t scale2 = tc::pack_f32x2(scale, scale), off2 = tc::pack_f32x2(-off, -off);
     uint64_t sum[4] = {0, 0, 0, 0};
-    const bool whole = nv >= BN;
 #pragma unroll
     for (int i = 0; i < BN; i += 2) {
         float a, b;
         tc::unpack_f32x2(tc::fma_f32x2(tc::pack_f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2), a, b);
         a = dev::exp2_approx(a);
         b = dev::exp2_approx(b);
-        if (!whole) {
-            a = i < nv ? a : 0.f;
-            b = i + 1 < nv ? b : 0.f;
-        }
         sum[(i / 2) & 3] = tc::add_f32x2(sum[(i / 2) & 3], tc::pack_f32x2(a, b));
         pk[i / 2] = pack2<KV8>(a, b);
     }
@@ -722,45 +721,54 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             // at most 128 rows the streams share stream 0's
             if ((two || t == 0) && sg.live > 0) {
                 uint8_t *qt = smem + L::q + t * (kRowTile * DPAD * 2);
-                constexpr int STEPS = CHUNKS;  // 32 rows x CHUNKS chunks over 32 lanes
-#pragma unroll 8
-                for (int i = 0; i < STEPS; ++i) {
-                    const int e = i * 32 + lane;
-                    const int row = (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;
-                    const int gr = t * kRowTile + row;  // row of the block
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (gr < sg.rows && c * 8 < D) {
-                        const int x = sg.row0 + gr;
-                        const int sq = fast_div(x, p.fd_group);
-                        const long long at = (static_cast<long long>(sg.seq0 + sq) * p.num_q_heads + sg.kvh * p.group +
-                                              (x - sq * p.group)) * D + c * 8;
-                        v = __ldg(reinterpret_cast<const uint4 *>(p.q + at));
-                        if (p.negative) {
-                            v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+                // 32 rows x CHUNKS chunks over 32 lanes, sixteen loads in flight at once
+                constexpr int BATCH = CHUNKS < 16 ? CHUNKS : 16;
+#pragma unroll 1
+                for (int i0 = 0; i0 < CHUNKS; i0 += BATCH) {
+                    uint4 v[BATCH];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int e = (i0 + i) * 32 + lane;
+                        const int gr = t * kRowTile + (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;  // row of the block, chunk
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (gr < sg.rows && c * 8 < D) {
+                            const int x = sg.row0 + gr;
+                            const int sq = fast_div(x, p.fd_group);
+                            v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                p.q + (static_cast<long long>(sg.seq0 + sq) * p.num_q_heads + sg.kvh * p.group + (x - sq * p.group)) * D +
+                                c * 8));
                         }
                     }
-                    if constexpr (KV8) {
-                        // f16 rows under a power of two that brings the row's largest
-                        // |q| into [2^14, 2^15), exactly but for values 2^-28 below it;
-                        // its inverse joins the row's softmax scale
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                        float big = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            big = fmaxf(big, fmaxf(fabsf(dev::bf16_lo_f32(w[k])), fabsf(dev::bf16_hi_f32(w[k]))));
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int e = (i0 + i) * 32 + lane;
+                        const int row = (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;
+                        if (p.negative) {
+                            v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
+                        }
+                        if constexpr (KV8) {
+                            // f16 rows under a power of two that brings the row's largest
+                            // |q| into [2^14, 2^15), exactly but for values 2^-28 below it;
+                            // its inverse joins the row's softmax scale
+                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                            float big = 0.f;
 #pragma unroll
-                        for (int off = 1; off < CHUNKS; off <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-                        const int ex = (__float_as_int(big) >> 23) & 0xff;  // big < 2^(ex - 126)
-                        const int up = min(max(141 - ex, -126), 127);       // times 2^up: below 2^15
-                        const float f = __int_as_float((127 + up) << 23);
-                        if (c == 0) row_scale[t * kRowTile + row] = p.scale_log2 * (up < 127 ? __int_as_float((127 - up) << 23)
-                                                                                             : 5.877471754111438e-39f);
-                        v.x = dev::pack_f16x2(dev::bf16_lo_f32(w[0]) * f, dev::bf16_hi_f32(w[0]) * f);
-                        v.y = dev::pack_f16x2(dev::bf16_lo_f32(w[1]) * f, dev::bf16_hi_f32(w[1]) * f);
-                        v.z = dev::pack_f16x2(dev::bf16_lo_f32(w[2]) * f, dev::bf16_hi_f32(w[2]) * f);
-                        v.w = dev::pack_f16x2(dev::bf16_lo_f32(w[3]) * f, dev::bf16_hi_f32(w[3]) * f);
+                            for (int k = 0; k < 4; ++k)
+                                big = fmaxf(big, fmaxf(fabsf(dev::bf16_lo_f32(w[k])), fabsf(dev::bf16_hi_f32(w[k]))));
+#pragma unroll
+                            for (int off = 1; off < CHUNKS; off <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+                            const int ex = (__float_as_int(big) >> 23) & 0xff;  // big < 2^(ex - 126)
+                            const int up = min(max(141 - ex, -126), 127);       // times 2^up: below 2^15
+                            const float f = __int_as_float((127 + up) << 23);
+                            const float down = up < 127 ? __int_as_float((127 - up) << 23) : 5.877471754111438e-39f;  // 2^-up
+                            if (c == 0) row_scale[t * kRowTile + row] = fmaxf(p.scale_log2 * down, FLT_MIN);
+                            v[i].x = dev::pack_f16x2(dev::bf16_lo_f32(w[0]) * f, dev::bf16_hi_f32(w[0]) * f);
+                            v[i].y = dev::pack_f16x2(dev::bf16_lo_f32(w[1]) * f, dev::bf16_hi_f32(w[1]) * f);
+                            v[i].z = dev::pack_f16x2(dev::bf16_lo_f32(w[2]) * f, dev::bf16_hi_f32(w[2]) * f);
+                            v[i].w = dev::pack_f16x2(dev::bf16_lo_f32(w[3]) * f, dev::bf16_hi_f32(w[3]) * f);
+                        }
+                        *reinterpret_cast<uint4 *>(qt + (c / 8) * (kRowTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[i];
                     }
-                    *reinterpret_cast<uint4 *>(qt + (c / 8) * (kRowTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
                 }
                 tc::fence_async_shared();
                 arrive(bar_q + 8 * t);
@@ -782,28 +790,30 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 // at the scores again and raise m (by a whole number, so that l and O
                 // are scaled exactly).  FP32 and BF16 hold such weights as exactly as
                 // weights below 1; kLift is what f16 holds.
-                uint32_t x[BN];
-                tc::ld_columns<BN>(ts, x);
-                if (__any_sync(0xffffffffu, m == kNegInf)) {
-                    const float mx = largest_of<BN>(x, nv) * scale;
-                    m = m == kNegInf ? mx : m;
-                }
-                uint32_t pk[BN / 2];
-                float sum = weigh<BN, KV8>(x, nv, scale, m, pk);
+                uint32_t x[BN], pk[BN / 2];
+                float sum;
+                bool fresh = m == kNegInf, over = false;  // rows that take, or raise, their reference now
                 bool waited = !ONE || first;  // the last product onto O is known to be done
-                first = false;
-                const bool over = !(sum <= kLift);
-                if (__any_sync(0xffffffffu, over)) {
+                for (bool again = false;; again = true) {
+                    tc::ld_columns<BN>(ts, x);
+                    if (nv < BN) mask_columns<BN>(x, nv);
+                    if (__any_sync(0xffffffffu, fresh || over)) {
+                        const float mx = largest_of<BN>(x) * scale;
+                        if (fresh) m = mx;
+                        if (again) raise_reference<DPAD>(to, mx, over, m, l);
+                    }
+                    sum = weigh<BN, KV8>(x, scale, m, pk);
+                    over = !(sum <= kLift);
+                    fresh = false;
+                    if (again || !__any_sync(0xffffffffu, over)) break;
                     if (!waited) {
                         ok = wait_bar(bar_o, oph & 1, gave_up);
                         oph ^= 1;
                         waited = true;
                         tc::fence_after();
                     }
-                    tc::ld_columns<BN>(ts, x);
-                    raise_reference<DPAD>(to, largest_of<BN>(x, nv) * scale, over, m, l);
-                    sum = weigh<BN, KV8>(x, nv, scale, m, pk);
                 }
+                first = false;
                 l += sum;
                 tc::st_columns<BN / 2>(ts, pk);  // over S, which has been read
                 if (ONE && !waited) {  // (each phase of the barrier is waited for, in order)

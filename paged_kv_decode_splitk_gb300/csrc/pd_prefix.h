@@ -45,7 +45,7 @@ struct PrefixParams {
     FastDiv block_size, fd_group;
     int tok_dim;
     int box_tokens;     // tokens of a TMA box: a power of two from 16 that divides the block and the tile
-    float scale_log2;   // |scale| log2(e) (times k_scale)
+    float scale_log2;   // |scale| log2(e) (times k_scale), above 0
     int negative;       // the scale is negative: q changes sign instead
     int max_items;
     float *part_ml;     // [slot][block rows] (m, l); a team's item has two slots, one for each CTA

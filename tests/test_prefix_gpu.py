@@ -192,9 +192,11 @@ def test_prefix_rising_scores(D):
         b.check(b.run(), f"rising, {rows} sequences")
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("scale", [-0.09, 0.0, 1.0])
-def test_prefix_any_scale(scale):
-    b = Batch([5, 40], [300, 450], [20] * 45, 8, 2, 128, seed=3)
+def test_prefix_any_scale(scale, fp8):
+    b = Batch([5, 40], [300, 450], [20] * 45, 8, 2, 128, fp8=fp8, seed=3)
+    b.q[1] = 0
     b.scale = scale
     b.check(b.run(), f"scale {scale}")
 

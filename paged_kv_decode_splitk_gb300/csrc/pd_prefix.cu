@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const
         f.tiles = __shfl_sync(0xffffffffu, one.tiles, src);
         f.first_seq = __shfl_sync(0xffffffffu, one.first_seq, src);
         f.rows = __shfl_sync(0xffffffffu, one.rows, src);
-        f.blocks = __shfl_sync(0xffffffffu, one.blocks, src);
+        f.items = __shfl_sync(0xffffffffu, one.items, src);
         if (below > 0) g = f;
     }
     int nparts = 0, step = 2;      // prefix slots of the row, 2 apart, or (both CTAs') 1
@@ -86,20 +86,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const
     const int x = (s - g.first_seq) * p.group + (h - kvh * p.group);
     const bool has = W > 0 && in && g.tiles > 0 && x < g.rows;
     {
-        const int block = has ? x / BR : 0, r = x - block * BR;
-        const int pairs = g.blocks >> 1, odd = g.blocks & 1, of_single = (g.tiles + 1) >> 1;
-        const bool pair = block < 2 * pairs;
-        const int item = block >> 1, places = pair ? g.tiles : of_single;
-        const long long u = g.first_unit + kvh * (static_cast<long long>(pairs) * g.tiles + (odd ? of_single : 0)) +
-                            static_cast<long long>(item) * g.tiles;
+        constexpr int IR = item_rows(DPAD);
+        const int item = has ? x / IR : 0, r = x - item * IR;
+        const int of_item = min(IR, g.rows - item * IR), half = (of_item + 1) >> 1;
+        const bool pair = is_pair(of_item, p.kv8 != 0, IR);
+        const int places = pair ? g.tiles : (g.tiles + 1) >> 1;
+        const long long u = g.first_unit + kvh * g.head_units(IR, p.kv8 != 0) + static_cast<long long>(item) * g.tiles;
         const int C = teams_of(W, p.teams);
         const int c = has ? team_of_unit(sub == 0 ? u : u + places - 1, C, W) : 0;
         const int c0 = __shfl_sync(0xffffffffu, c, head_lane), c1 = __shfl_sync(0xffffffffu, c, head_lane + 1);
         if (has) {
+            const int second = pair && r >= half;
             step = pair ? 2 : 1;
             nparts = (c1 - c0 + 1) * (pair ? 1 : 2);
-            const long long slot = 2ll * (g.first_item + kvh * (pairs + odd) + item + c0) + (pair ? block & 1 : 0);
-            first = slot * BR + r;
+            first = (2ll * (g.first_item + kvh * g.items + item + c0) + second) * BR + (second ? r - half : r);
         }
     }
     L = L < 0 ? 0 : (L > p.max_tokens ? p.max_tokens : L);
@@ -234,7 +234,7 @@ Layout layout_of(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads
     const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads * num_splits;
     // every group's rows end in at most one item that is not full
     l.max_items = static_cast<long long>(num_kv_heads) *
-                  (num_groups + static_cast<long long>(num_seqs) * (num_q_heads / num_kv_heads) / (2 * BR));
+                  (num_groups + static_cast<long long>(num_seqs) * (num_q_heads / num_kv_heads) / item_rows(dpad_of(head_dim)));
     const size_t slots = 2 * (static_cast<size_t>(l.max_items) + kMaxTeams);
     l.own_o = take(rows * head_dim * sizeof(float));
     l.own_ml = take(rows * 2 * sizeof(float));
@@ -364,6 +364,7 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     m.group = group;
     m.head_dim = head_dim;
     m.dpad = dpad;
+    m.kv8 = kv8;
     m.num_splits = num_splits;
     m.min_kv_per_split = PD_MIN_KV_PER_SPLIT;
     m.max_tokens = max_blocks * block_size;

@@ -13,11 +13,11 @@
 // sequence's own tokens.
 //
 // GB300 mapping.
-//   * CTAs work in teams of two, a cluster.  Two row blocks of a KV head are a
-//     team's item: each CTA has one, both need the same K and V tiles, and each
-//     loads half of every tile and multicasts it to both, which halves what the
-//     SMs draw from L2.  A row block left over is an item too: there the CTAs take
-//     the tiles in turn.
+//   * CTAs work in teams of two, a cluster.  A team's item is up to 512 rows of a
+//     KV head (256 at head dims above 128): each CTA has half of them, both need
+//     the same K and V tiles, and each loads half of every tile and multicasts it
+//     to both, which halves what the SMs draw from L2.  With few rows both have all
+//     of them and take the tiles in turn.
 //   * Work is counted in units (item, a tile for both CTAs) in one line over all
 //     groups; team c of C takes units [W c / C, W (c + 1) / C): every SM gets the
 //     same number of tiles whatever the shapes, and a team's partials of item i go
@@ -88,15 +88,15 @@ struct Segment {
     int tile0, stride;  // tile j of the run is tile0 + j stride
     int n;      // places in the run: the same for both CTAs of the team
     int live;   // tiles of this CTA: n, or one less where the last place has no tile
-    int row0;   // first row of the block within the group
-    int rows;   // rows of the block
+    int row0;   // first row of this CTA within the group
+    int rows;   // rows of this CTA
     int seq0;   // the group's first sequence
     int group;
     bool two;   // more than kRowTile rows: both streams use every tile
     bool pair;  // both CTAs use the same tiles
 };
 
-template <int BR>
+template <int BR, bool KV8>
 __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_groups, long long &u, long long u1,
                                              int team, int rank, Segment &s) {
     if (u >= u1) return false;
@@ -111,29 +111,29 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
         }
     }
     const GroupPlan g = grp[lo];
-    const int pairs = g.blocks >> 1, odd = g.blocks & 1;
-    const long long of_pairs = static_cast<long long>(pairs) * g.tiles;
-    const int of_single = (g.tiles + 1) >> 1;
-    const long long per_head = of_pairs + (odd ? of_single : 0);
+    const long long per_head = g.head_units(2 * BR, KV8);
     const long long local = u - g.first_unit;
     s.kvh = static_cast<int>(local / per_head);
     const long long rem = local - s.kvh * per_head;
-    s.pair = rem < of_pairs;
-    const int item = s.pair ? static_cast<int>(rem / g.tiles) : pairs;
+    int item = static_cast<int>(rem / g.tiles);  // (the last item may have fewer units, never more)
     const int at = static_cast<int>(rem - static_cast<long long>(item) * g.tiles);  // place within the item
-    const int places = s.pair ? g.tiles : of_single;
+    const int rows = min(2 * BR, g.rows - item * 2 * BR);
+    s.pair = is_pair(rows, KV8, 2 * BR);
+    const int places = s.pair ? g.tiles : (g.tiles + 1) >> 1;
     const long long left = u1 - u;
     s.n = left < places - at ? static_cast<int>(left) : places - at;
     s.stride = s.pair ? 1 : 2;
     s.tile0 = s.pair ? at : 2 * at + rank;
     s.live = s.tile0 + (s.n - 1) * s.stride < g.tiles ? s.n : s.n - 1;
-    s.row0 = (s.pair ? 2 * item + rank : 2 * pairs) * BR;
-    s.rows = min(BR, g.rows - s.row0);
+    const int half = (rows + 1) >> 1;
+    s.row0 = item * 2 * BR + (s.pair && rank ? half : 0);
+    s.rows = !s.pair ? rows : rank ? rows - half : half;
     s.plen = g.tokens;
     s.seq0 = g.first_seq;
     s.group = lo;
-    s.slot = 2 * (g.first_item + s.kvh * (pairs + odd) + item + team) + rank;
+    s.slot = 2 * (g.first_item + s.kvh * g.items + item + team) + rank;
     s.two = s.rows > kRowTile;
+    if (s.n < 1) return false;  // (never; the walk over the units ends all the same)
     u += s.n;
     return true;
 }
@@ -141,7 +141,7 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
 // The groups' units and items, by one warp: running sums over chunks of 32
 // groups.  Returns false (on every lane) where group_starts is not
 // non-decreasing within the batch or asks for more items than the workspace holds.
-template <int DPAD>
+template <int DPAD, bool KV8>
 __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *grp, long long *total, int lane, bool flag) {
     long long units = 0;
     int items = 0;
@@ -163,13 +163,12 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
             bad |= a < 0 || b < a || b > p.num_seqs;
             r.first_seq = a;
             r.rows = bad ? 0 : (b - a) * p.group;
-            r.blocks = (r.rows + block_rows(DPAD) - 1) / block_rows(DPAD);
+            r.items = (r.rows + item_rows(DPAD) - 1) / item_rows(DPAD);
             r.tokens = len;
             r.tiles = (len + tile_tokens(DPAD) - 1) / tile_tokens(DPAD);
-            const int pairs = r.blocks >> 1, odd = r.blocks & 1;
-            if (r.tiles > 0) {
-                it = (pairs + odd) * p.num_kv_heads;
-                mine = (static_cast<long long>(pairs) * r.tiles + odd * ((r.tiles + 1) >> 1)) * p.num_kv_heads;
+            if (r.tiles > 0 && r.items > 0) {
+                it = r.items * p.num_kv_heads;
+                mine = r.head_units(item_rows(DPAD), KV8) * p.num_kv_heads;
             }
         }
         long long su = mine;
@@ -366,7 +365,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     dev::griddep_wait();  // q, the caches, tables and lengths are final
     if (warp == 0) {
         long long total;
-        const bool good = plan_groups<DPAD>(p, grp, &total, lane, blockIdx.x == 0);
+        const bool good = plan_groups<DPAD, KV8>(p, grp, &total, lane, blockIdx.x == 0);
         if (lane == 0) *total_s = total;
         __syncwarp();
         if (blockIdx.x == 0) {  // the merge finds each row's partials from this
@@ -420,7 +419,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         uint32_t tail_ph = 0;
         bool ok = true;
         long long issued = 0;
-        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
+        while (ok && next_segment<BR, KV8>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const int32_t *ids = p.prefix_table + static_cast<long long>(sg.group) * p.max_prefix_blocks;
             const int ahead = ONE || !sg.two ? 2 : 1;
             // of a shared tile each CTA loads every other box, for both
@@ -570,7 +569,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 qph ^= 1u << t;
                 return got;
             };
-            while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
+            while (ok && next_segment<BR, KV8>(grp, p.num_groups, u, u1, team, rank, sg)) {
                 const int n = sg.n, live = sg.live;
                 int ks = 0, vs = 0;
                 if (live > 0 && !(ok = queries(0))) break;
@@ -643,8 +642,17 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         // each cover the 32 banks once under the swizzle.  V rows past the prefix
         // are zeroed on the way.
         constexpr int CPR = DPAD / 16;               // 16-code chunks of a row
-        constexpr int ITEMS = BN / 2 * (CPR / 4);    // (row pair, 64 codes)
+        constexpr int KB = CPR / 4;                  // 64-code blocks of a row
+        constexpr int ROWS = kConverters / 8 / KB * 2;  // rows all quarter-warps take at a time
+        // a thread's rows share their place in the swizzle, or it flips by half a row
+        // from one to the next
+        constexpr int FLIP = ROWS % 8 ? 64 : 0;
+        static_assert(ROWS % 4 == 0 && BN % (2 * ROWS) == 0, "rows of a thread");
         const int me = (warp - 2) * 4 + (lane >> 3), j8 = lane & 7;
+        const int row0 = me / KB * 2 + (j8 >> 2), c = 4 * (KB > 1 ? (me % KB) ^ (j8 >> 2) : 0) + (j8 & 3);
+        const int from = DPAD < 128 ? row0 * DPAD + c * 16 : (c / 8) * (BN * 128) + row0 * 128 + (((c & 7) ^ (row0 & 7)) << 4);
+        const int to = (c / 4) * (BN * 128) + row0 * 128, u2 = (2 * c) & 7;
+        const int to_lo = to + ((u2 ^ (row0 & 7)) << 4), to_hi = to + (((u2 + 1) ^ (row0 & 7)) << 4);
         int rs = 0, st = 0;
         uint32_t rph = 0, ph = 0;
         bool ok = true;
@@ -653,23 +661,31 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const uint8_t *src = smem + L::raw + rs * L::kRawBytes;
             uint8_t *dst = smem + L::ring + st * L::kStageBytes;
             if (live) {
-#pragma unroll 4
-                for (int i = me; i < ITEMS; i += kConverters / 8) {
-                    const int kb = i % (CPR / 4), row = i / (CPR / 4) * 2 + (j8 >> 2);
-                    const int c = 4 * (CPR >= 8 ? kb ^ (j8 >> 2) : kb) + (j8 & 3);
-                    const uint8_t *at = DPAD < 128 ? src + row * DPAD + c * 16
-                                                   : src + (c / 8) * (BN * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-                    uint4 v = *reinterpret_cast<const uint4 *>(at);
-                    if (is_v && row >= nv) v = make_uint4(0, 0, 0, 0);
-                    uint4 lo, hi;
-                    dev::e4m3x4_to_f16x4(v.x, lo.x, lo.y);
-                    dev::e4m3x4_to_f16x4(v.y, lo.z, lo.w);
-                    dev::e4m3x4_to_f16x4(v.z, hi.x, hi.y);
-                    dev::e4m3x4_to_f16x4(v.w, hi.z, hi.w);
-                    uint8_t *box = dst + (c / 4) * (BN * 128) + row * 128;
-                    const int u2 = (2 * c) & 7;
-                    *reinterpret_cast<uint4 *>(box + ((u2 ^ (row & 7)) << 4)) = lo;
-                    *reinterpret_cast<uint4 *>(box + (((u2 + 1) ^ (row & 7)) << 4)) = hi;
+                // (eight loads before the first store, which the compiler would
+                // not move them over)
+                constexpr int N = BN / ROWS, BATCH = N < 8 ? N : 8;
+#pragma unroll 1
+                for (int k0 = 0; k0 < N; k0 += BATCH) {
+                    uint4 v[BATCH];
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k)
+                        v[k] = *reinterpret_cast<const uint4 *>(src + (k & 1 ? from ^ FLIP : from) +
+                                                              (k0 + k) * (ROWS * (DPAD < 128 ? DPAD : 128)));
+                    if (is_v && nv < BN) {
+#pragma unroll
+                        for (int k = 0; k < BATCH; ++k)
+                            if (row0 + (k0 + k) * ROWS >= nv) v[k] = make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        uint4 lo, hi;
+                        dev::e4m3x4_to_f16x4(v[k].x, lo.x, lo.y);
+                        dev::e4m3x4_to_f16x4(v[k].y, lo.z, lo.w);
+                        dev::e4m3x4_to_f16x4(v[k].z, hi.x, hi.y);
+                        dev::e4m3x4_to_f16x4(v[k].w, hi.z, hi.w);
+                        *reinterpret_cast<uint4 *>(dst + (k & 1 ? to_lo ^ FLIP : to_lo) + (k0 + k) * (ROWS * 128)) = lo;
+                        *reinterpret_cast<uint4 *>(dst + (k & 1 ? to_hi ^ FLIP : to_hi) + (k0 + k) * (ROWS * 128)) = hi;
+                    }
                 }
                 tc::fence_async_shared();
             }
@@ -686,7 +702,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             }
             return true;
         };
-        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
+        while (ok && next_segment<BR, KV8>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const int ahead = ONE || !sg.two ? 2 : 1;
             for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
                 if (i < sg.n) ok = convert(i < sg.live, false, BN);
@@ -710,7 +726,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         // the time a third segment begins: its weights of the first went before)
         float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
         int turn = 0;
-        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
+        while (ok && next_segment<BR, KV8>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const bool two = sg.two;
             float scale = p.scale_log2;
             if constexpr (KV8) {

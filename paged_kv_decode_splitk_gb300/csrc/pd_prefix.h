@@ -12,8 +12,25 @@ constexpr int kMaxTeams = 76;     // teams of two CTAs of the prefix pass at mos
 
 // Keys of a tile: 128, or 64 where a tile of 128 would leave no ring (D > 128).
 __host__ __device__ constexpr int tile_tokens(int dpad) { return dpad > 128 ? 64 : 128; }
-// Query rows of an item: two 128-row tiles, or one where its O fills TMEM.
+// Query rows a CTA takes at most: two 128-row tiles, or one where its O fills TMEM.
 __host__ __device__ constexpr int block_rows(int dpad) { return dpad > 128 ? 128 : 256; }
+// Query rows of an item at most: a block for each CTA of a team.
+__host__ __device__ constexpr int item_rows(int dpad) { return 2 * block_rows(dpad); }
+
+// How an item's rows go to the two CTAs of a team: half of them each, with every
+// tile for both; or, where they are few, all to both, which take the tiles in
+// turn.  Up to 128 rows a half would be a 128-row product half empty (32
+// sequences of 4 heads, 32768 tokens: 41 us in turn, 45 us by halves; 64: by
+// halves, which makes half as many partials, 50 us, in turn 54).  Over an FP8
+// cache every tile a CTA uses it also has to convert, so up to 256 rows go to
+// both (the same 32 sequences: 67 us in turn, 89 us by halves).  Rows in turn are
+// never more than one CTA takes, so a full item is always by halves.
+__host__ __device__ constexpr bool is_pair(int rows, bool kv8, int of_item) {
+    return rows > (kv8 && of_item > 256 ? 256 : 128);
+}
+static_assert(is_pair(item_rows(64), true, item_rows(64)) && is_pair(item_rows(256), true, item_rows(256)) &&
+                  is_pair(block_rows(256) + 1, true, item_rows(256)) && is_pair(block_rows(64) + 1, true, item_rows(64)),
+              "full items are by halves, and so is what one CTA cannot take");
 
 // Teams that share W units: all there are, but each at least kMinUnits (a team
 // more is a partial more of each of its rows to write and fold).
@@ -23,18 +40,25 @@ __host__ __device__ inline int teams_of(long long W, int most) {
     return n < most ? static_cast<int>(n) : most;
 }
 
-// One group on the line of work units.  An item is two row blocks of a KV head,
-// which a team's CTAs work on side by side (a unit is a tile), or a block left
-// over, whose tiles they take in turn (a unit is two tiles); per KV head the pairs
-// come first.
+// One group on the line of work units.  Its items are, for each KV head, the
+// item_rows-row pieces of its query rows; a unit of a pair item is a tile, of one
+// whose tiles are taken in turn, two.
 struct GroupPlan {
     long long first_unit;
     int first_item;
     int tiles;      // of the prefix; 0: nothing to do
     int first_seq;
     int rows;       // sequences x query heads of a KV head
-    int blocks;     // row blocks
+    int items;      // of a KV head
     int tokens;     // of the prefix
+
+    // units of a KV head, and of its last item, which alone may have few rows
+    __host__ __device__ int last_units(int of_item, bool kv8) const {
+        return is_pair(rows - (items - 1) * of_item, kv8, of_item) ? tiles : (tiles + 1) >> 1;
+    }
+    __host__ __device__ long long head_units(int of_item, bool kv8) const {
+        return static_cast<long long>(items - 1) * tiles + last_units(of_item, kv8);
+    }
 };
 
 struct PrefixParams {
@@ -64,6 +88,7 @@ struct MergeParams {
     __nv_bfloat16 *out;
     int num_groups, num_seqs, num_q_heads, num_kv_heads, group, head_dim, dpad;
     int num_splits, min_kv_per_split, max_tokens, teams;
+    int kv8;
     float v_scale;      // of the prefix partials (an FP8 cache; the own-token pass applies its own)
     FastDiv fd_hq, fd_group, fd_split, fd_bs;
 };

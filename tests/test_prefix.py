@@ -1,6 +1,7 @@
 """CPU tests of decode attention behind shared prefixes: the workspace and every refusal, none of which reaches a kernel."""
 
 import math
+import random
 
 import pytest
 import torch
@@ -16,6 +17,70 @@ def test_workspace():
     least = rows * (128 + 2) * 4 + (items + 152) * 256 * (128 + 2) * 4
     assert least <= n(64, 1, 32, 8, 128, 10) <= least + 32 * 256 + 6 * 256
     assert n(64, 3, 32, 8, 128, 10) > n(64, 1, 32, 8, 128, 10)
+
+
+def _walk(G, Hkv, groups, BR, tile, fp8, teams):
+    """The prefix pass's division of work, restated: every (group, KV head, item, CTA or both, tile) by the CTA that
+    takes it, which has to be exactly one, and the slots the merge reads for it."""
+    IR = 2 * BR
+
+    def pair(rows):
+        return rows > (256 if fp8 and IR > 256 else 128)
+
+    plan, W, first_item = [], 0, 0
+    for seqs, tokens in groups:
+        rows = seqs * G
+        items, tiles = -(-rows // IR), -(-tokens // tile)
+        head = (items - 1) * tiles + (tiles if pair(rows - (items - 1) * IR) else (tiles + 1) // 2)
+        units = head * Hkv if items and tiles else 0
+        plan.append((W, first_item, tiles, rows, items, head))
+        W, first_item = W + units, first_item + (items * Hkv if units else 0)
+    C, slots, used = min(W, teams), {}, {}
+    for team in range(C):
+        for rank in (0, 1):
+            u, end = W * team // C, W * (team + 1) // C
+            while u < end:
+                gi = max(i for i, g in enumerate(plan) if g[0] <= u)
+                first_unit, item0, tiles, rows, items, head = plan[gi]
+                kvh, rem = divmod(u - first_unit, head)
+                item = rem // tiles
+                at, r = rem - item * tiles, min(IR, rows - item * IR)
+                n = min(end - u, (tiles if pair(r) else (tiles + 1) // 2) - at)
+                assert n >= 1 and kvh < Hkv and item < items  # the walk goes on, within the group
+                half = (r + 1) // 2
+                assert 0 < (r if not pair(r) else r - half if rank else half) <= BR  # rows one CTA can take
+                slot = 2 * (item0 + kvh * items + item + team) + rank
+                assert used.setdefault(slot, (gi, kvh, item, team, rank)) == (gi, kvh, item, team, rank)
+                for t in range(at, at + n) if pair(r) else range(2 * at + rank, min(tiles, 2 * (at + n)), 2):
+                    key = (gi, kvh, item, rank if pair(r) else None, t)
+                    assert key not in slots
+                    slots[key] = slot
+                u += n
+    assert not used or max(used) < 2 * (first_item + teams)
+    for gi, (first_unit, item0, tiles, rows, items, head) in enumerate(plan):
+        for kvh in range(Hkv if tiles else 0):
+            for item in range(items):
+                r = min(IR, rows - item * IR)
+                places = tiles if pair(r) else (tiles + 1) // 2
+                u = first_unit + kvh * head + item * tiles
+                c0, c1 = ((u + 1) * C - 1) // W, ((u + places) * C - 1) // W  # the teams the merge reads
+                for rank in (0, 1) if pair(r) else (None,):
+                    mine = {slots[gi, kvh, item, rank, t] for t in range(tiles)}
+                    ranks = (0, 1) if rank is None else (rank,)
+                    assert mine <= {2 * (item0 + kvh * items + item + c) + k for c in range(c0, c1 + 1) for k in ranks}
+    return first_item
+
+
+@pytest.mark.parametrize("BR,tile", [(256, 128), (128, 64)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_work_division(BR, tile, fp8):
+    rng = random.Random(7)
+    for _ in range(150):
+        G, Hkv = rng.choice([1, 2, 3, 4, 7, 8, 16]), rng.choice([1, 2, 8])
+        groups = [(rng.choice([0, 1, 2, 5, 20, 32, 40, 64, 100]), rng.choice([0, 1, 17, 64, 100, 128, 129, 700, 3000]))
+                  for _ in range(rng.randint(1, 5))]
+        items = _walk(G, Hkv, groups, BR, tile, fp8, rng.choice([1, 3, 76]))
+        assert items <= Hkv * (len(groups) + sum(n for n, _ in groups) * G // (2 * BR))  # what the workspace is sized for
 
 
 def _call(**change):

@@ -40,16 +40,20 @@ __device__ __forceinline__ int team_of_unit(long long u, int C, long long W) {
 // 0 where the row has no token at all.  Bound by latency on small batches (the
 // chain is the plan, then m, l and o together) and by reading the partials from
 // L2 on large ones; 64 registers keep four blocks on an SM, so that a batch of
-// 8192 rows is one wave.
+// 8192 rows is one wave.  Fewer rows have several lines of lanes each, which
+// share the partials.
 template <int DPAD>
 __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const __grid_constant__ MergeParams p) {
     constexpr int LPR = DPAD / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
     constexpr int BR = block_rows(DPAD);
     const float kNegInf = -__int_as_float(0x7f800000);
     dev::griddep_launch_dependents();
+    __shared__ float fold[kMergeWarps * 32][9];   // ways > 1: each thread's columns
+    __shared__ float2 fold_ml[kMergeWarps * RPW];
     const int lane = threadIdx.x & 31, sub = lane % LPR, mine = lane / LPR, head_lane = mine * LPR;
+    const int line = threadIdx.x / LPR, ways = p.ways, way = line & (ways - 1);  // a row has `ways` lines of lanes
     const int D = p.head_dim, N = p.num_splits, rows = p.num_seqs * p.num_q_heads;
-    const int row = (blockIdx.x * kMergeWarps + (threadIdx.x >> 5)) * RPW + mine;
+    const int row = blockIdx.x * (kMergeWarps * RPW / ways) + line / ways;
     const int d0 = sub * 8;
     const bool in = row < rows, cols = in && d0 < D;
     const int s = in ? fast_div(row, p.fd_hq) : 0;
@@ -104,15 +108,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const
     }
     L = L < 0 ? 0 : (L > p.max_tokens ? p.max_tokens : L);
     const int chunk = split_chunk_tokens_fd(L, p.fd_split, p.fd_bs, p.min_kv_per_split);
-    const int total = nparts + (L > 0 ? (L + chunk - 1) / chunk : 0);
+    // (this line's share: partials way, way + ways, ...)
+    const int all = nparts + (L > 0 ? (L + chunk - 1) / chunk : 0);
+    const int total = all > way ? (all - way + ways - 1) / ways : 0;
 
-    // where partial i lies: (m, l) and, for this lane's columns, o
-    auto ml_of = [&](int i) -> const float * {
+    // where partial i of the share lies: (m, l) and, for this lane's columns, o
+    auto ml_of = [&](int k) -> const float * {
+        const int i = way + k * ways;
         if (i >= nparts) return p.own_ml + (static_cast<long long>(row) * N + (i - nparts)) * 2;
         return p.part_ml + (first + i * step * BR) * 2;
     };
     const float *part = p.part_o + (first / BR * LPR + sub) * (BR * 8) + (first % BR) * 8;
-    auto o_of = [&](int i) -> const float * {
+    auto o_of = [&](int k) -> const float * {
+        const int i = way + k * ways;
         if (i >= nparts) return p.own_o + (static_cast<long long>(row) * N + (i - nparts)) * D + d0;
         return part + static_cast<long long>(i) * step * (LPR * BR * 8);
     };
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const
         M = Mn;
         const float w = dead ? 0.f : dev::exp2_approx(v.x - M);
         float wl = dead ? 0.f : w * v.y;
-        const float wo = i0 + sub < nparts ? w * p.v_scale : w;
+        const float wo = way + (i0 + sub) * ways < nparts ? w * p.v_scale : w;
 #pragma unroll
         for (int off = LPR / 2; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
         lsum = lsum * keep + wl;
@@ -177,6 +185,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const
             }
         }
     }
+    if (ways > 1) {
+        // the lines of a row, folded in order by its first
+        if (sub == 0) fold_ml[line] = make_float2(M, lsum);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) fold[threadIdx.x][k] = acc[k];
+        __syncthreads();
+        if (way > 0) return;
+        float Mall = M;
+        for (int k = 1; k < ways; ++k) Mall = fmaxf(Mall, fold_ml[line + k].x);
+        const float f0 = M == kNegInf ? 0.f : dev::exp2_approx(M - Mall);
+        lsum *= f0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] *= f0;
+        for (int w = 1; w < ways; ++w) {
+            const float2 ml = fold_ml[line + w];
+            const float f = ml.x == kNegInf ? 0.f : dev::exp2_approx(ml.x - Mall);
+            lsum = fmaf(ml.y, f, lsum);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = fmaf(fold[threadIdx.x + w * LPR][k], f, acc[k]);
+        }
+    }
     if (!cols) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = lsum == 0.f ? 0.f : __fdiv_rn(acc[k], lsum);
@@ -186,7 +215,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const
 }
 
 cudaError_t launch_prefix_merge(const MergeParams &p, cudaStream_t stream) {
-    const int rows = p.num_seqs * p.num_q_heads, of_block = kMergeWarps * (256 / p.dpad);
+    const int rows = p.num_seqs * p.num_q_heads, of_block = kMergeWarps * (256 / p.dpad) / p.ways;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((rows + of_block - 1) / of_block));
     cfg.blockDim = dim3(kMergeWarps * 32);
@@ -364,6 +393,10 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     m.group = group;
     m.head_dim = head_dim;
     m.dpad = dpad;
+    // as many lines a row as one wave has room for, 8 at most
+    const long long lanes = static_cast<long long>(num_seqs) * num_q_heads * (dpad / 8);
+    m.ways = 1;
+    while (m.ways < 8 && 2 * m.ways * lanes <= 152 * 4 * kMergeWarps * 32) m.ways *= 2;
     m.kv8 = kv8;
     m.num_splits = num_splits;
     m.min_kv_per_split = PD_MIN_KV_PER_SPLIT;

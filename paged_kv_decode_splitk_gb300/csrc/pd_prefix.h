@@ -88,7 +88,7 @@ struct MergeParams {
     __nv_bfloat16 *out;
     int num_groups, num_seqs, num_q_heads, num_kv_heads, group, head_dim, dpad;
     int num_splits, min_kv_per_split, max_tokens, teams;
-    int kv8;
+    int kv8, ways;
     float v_scale;      // of the prefix partials (an FP8 cache; the own-token pass applies its own)
     FastDiv fd_hq, fd_group, fd_split, fd_bs;
 };

@@ -39,11 +39,11 @@ __device__ __forceinline__ int team_of_unit(long long u, int C, long long W) {
 //   out = sum_i w_i o_i / sum_i w_i l_i,
 // 0 where the row has no token at all.  Bound by latency on small batches (the
 // chain is the plan, then m, l and o together) and by reading the partials from
-// L2 on large ones; 64 registers keep four blocks on an SM, so that a batch of
-// 8192 rows is one wave.  Fewer rows have several lines of lanes each, which
+// L2 on large ones; three blocks fit an SM, so that a batch of 8192 rows is little
+// more than a wave.  Fewer rows have several lines of lanes each, which
 // share the partials.
 template <int DPAD>
-__global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const __grid_constant__ MergeParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 3) prefix_merge_kernel(const __grid_constant__ MergeParams p) {
     constexpr int LPR = DPAD / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
     constexpr int BR = block_rows(DPAD);
     const float kNegInf = -__int_as_float(0x7f800000);
@@ -118,13 +118,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const
         if (i >= nparts) return p.own_ml + (static_cast<long long>(row) * N + (i - nparts)) * 2;
         return p.part_ml + (first + i * step * BR) * 2;
     };
-    const float *part = p.part_o + (first / BR * LPR + sub) * (BR * 8) + (first % BR) * 8;
-    auto o_of = [&](int k) -> const float * {
-        const int i = way + k * ways;
-        if (i >= nparts) return p.own_o + (static_cast<long long>(row) * N + (i - nparts)) * D + d0;
-        return part + static_cast<long long>(i) * step * (LPR * BR * 8);
-    };
-
+    // (chunk k of a row of 32 columns lies at k xor the row's number mod 8: this
+    // lane's two chunks are in one sector, in turned order for odd rows)
+    const int prow = static_cast<int>(first % BR), flip = prow & 7;
+    const float *part = p.part_o + ((first / BR * (DPAD / 32) + d0 / 32) * BR + prow) * 32;
+    const int lo = ((d0 % 32 / 4) ^ flip) * 4, hi = ((d0 % 32 / 4 + 1) ^ flip) * 4;
     // ---- the fold, LPR partials at a time: lane i of the row has (m, l) of partial i ----
     int most = total;  // (all rows of a warp go through the loops together)
 #pragma unroll
@@ -142,9 +140,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) prefix_merge_kernel(const
             for (int j = 0; j < kMergeBatch; ++j) {
                 o[j][0] = o[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (cols && i0 + j0 + j < total) {
-                    const float4 *at = reinterpret_cast<const float4 *>(o_of(i0 + j0 + j));
-                    o[j][0] = at[0];
-                    o[j][1] = at[1];
+                    const int i = way + (i0 + j0 + j) * ways;
+                    const bool of_prefix = i < nparts;
+                    const float *at = of_prefix ? part + static_cast<long long>(i) * step * (DPAD * BR)
+                                                : p.own_o + (static_cast<long long>(row) * N + (i - nparts)) * D + d0;
+                    o[j][0] = *reinterpret_cast<const float4 *>(at + (of_prefix ? lo : 0));
+                    o[j][1] = *reinterpret_cast<const float4 *>(at + (of_prefix ? hi : 4));
                 }
             }
         };
@@ -396,7 +397,7 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     // as many lines a row as one wave has room for, 8 at most
     const long long lanes = static_cast<long long>(num_seqs) * num_q_heads * (dpad / 8);
     m.ways = 1;
-    while (m.ways < 8 && 2 * m.ways * lanes <= 152 * 4 * kMergeWarps * 32) m.ways *= 2;
+    while (m.ways < 8 && 2 * m.ways * lanes <= 152 * 3 * kMergeWarps * 32) m.ways *= 2;
     m.kv8 = kv8;
     m.num_splits = num_splits;
     m.min_kv_per_split = PD_MIN_KV_PER_SPLIT;

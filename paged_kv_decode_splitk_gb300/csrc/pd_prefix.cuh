@@ -734,7 +734,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 turn ^= 1;
             }
             // -- this stream's query rows into shared memory (128-byte swizzle); with
-            // at most 128 rows the streams share stream 0's
+            // at most 128 rows the streams share stream 0's.  (The last segment's
+            // partials have to have left from there.)
+            if (lane == 0) tc::bulk_wait_read<0>();
+            __syncwarp();
             if ((two || t == 0) && sg.live > 0) {
                 uint8_t *qt = smem + L::q + t * (kRowTile * DPAD * 2);
                 // 32 rows x CHUNKS chunks over 32 lanes, sixteen loads in flight at once
@@ -842,14 +845,31 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 arrive(bar_p + 8 * buf);
             }
             if (!ok) break;
-            // -- the partial of this row: o [slot][DPAD / 8][BR][8], (m, l) [slot][BR]
+            // -- the partial of this row: (m, l) [slot][BR], o [slot][DPAD / 32][BR][32].
+            // 32 columns at a time go through the shared memory of this warp's own
+            // query rows (their products are done) and out as one copy of 4 KB, the
+            // 16-byte chunks of a row by their place xor the row's, here (no bank is
+            // hit twice) and in the workspace.
             const long long at = static_cast<long long>(sg.slot) * BR;
-            float *o = p.part_o + at * DPAD;
-            auto store = [&](int row, int c, const uint32_t (&x)[32]) {
+            constexpr int kBufs = DPAD / 64;
+            uint8_t *stage = smem + L::q + t * (kRowTile * DPAD * 2) + (warp & 3) * 4096;
+            const int warp_row = (ONE || two ? t * kRowTile : 0) + (warp & 3) * 32;  // of the block
+            int copies = 0;
+            auto store = [&](int c, const uint32_t (&x)[32]) {
+                uint8_t *buf = stage + copies % kBufs * (kRowTile * 128);
+                if (copies >= kBufs) {
+                    if (lane == 0) tc::bulk_wait_read<kBufs - 1>();
+                    __syncwarp();
+                }
+                ++copies;
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<uint4 *>(o + (static_cast<long long>((c + i) / 8) * BR + row) * 8 + (i & 4)) =
-                        make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    *reinterpret_cast<uint4 *>(buf + lane * 128 + (((i / 4) ^ (lane & 7)) << 4)) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                tc::fence_async_shared();
+                __syncwarp();
+                if (lane == 0 && warp_row < sg.rows)
+                    tc::bulk_store(p.part_o + ((static_cast<long long>(sg.slot) * (DPAD / 32) + c / 32) * BR + warp_row) * 32,
+                                   dev::smem_addr(buf), 4096);
             };
             if (ONE || two) {
                 const int row = t * kRowTile + r;
@@ -864,7 +884,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         uint32_t x[32];
                         tc::ld_32x32(to + c, x);
                         tc::wait_ld(x);
-                        if (in) store(row, c, x);
+                        store(c, x);
                     }
                     tc::fence_before();
                 }
@@ -906,7 +926,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                             const float xa = fa == 0.f ? 0.f : __uint_as_float(x[i]) * fa;
                             x[i] = __float_as_uint(sg.live > 1 && fb != 0.f ? fmaf(__uint_as_float(y[i]), fb, xa) : xa);
                         }
-                        if (in) store(r, c, x);
+                        store(c, x);
                     }
                     tc::fence_before();
                 }
@@ -918,6 +938,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         }
     }
     }
+    if (warp >= 4 && lane == 0) tc::bulk_wait_all();
     // The peer may still send halves of tiles and release stages: shared memory
     // stays until both are done.
     tc::fence_before();

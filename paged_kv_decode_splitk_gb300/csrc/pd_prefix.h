@@ -73,7 +73,7 @@ struct PrefixParams {
     int negative;       // the scale is negative: q changes sign instead
     int max_items;
     float *part_ml;     // [slot][block rows] (m, l); a team's item has two slots, one for each CTA
-    float *part_o;      // [slot][dpad / 8][block rows][8]
+    float *part_o;      // [slot][dpad / 32][block rows][32], 16-byte chunks swapped by row
     GroupPlan *plan_groups;
     long long *plan_total;
     unsigned int *status;

@@ -174,5 +174,18 @@ __device__ __forceinline__ void tma_load_4d_both(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// A copy of shared memory to global memory (16-byte aligned, a multiple of 16
+// bytes), a group of its own; waits for all but N of this thread's groups to have
+// been read from shared memory, and for all of them to be done.
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 }  // namespace tc
 }  // namespace pd

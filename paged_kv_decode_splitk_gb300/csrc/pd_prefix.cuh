@@ -96,6 +96,12 @@ struct Segment {
     bool pair;  // both CTAs use the same tiles
 };
 
+// a / b, in 32 bits where both fit (a fifth of the instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if ((a | b) >> 32 == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
+
 template <int BR, bool KV8>
 __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_groups, long long &u, long long u1,
                                              int team, int rank, Segment &s) {
@@ -113,9 +119,9 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
     const GroupPlan g = grp[lo];
     const long long per_head = g.head_units(2 * BR, KV8);
     const long long local = u - g.first_unit;
-    s.kvh = static_cast<int>(local / per_head);
+    s.kvh = static_cast<int>(quotient(local, per_head));
     const long long rem = local - s.kvh * per_head;
-    int item = static_cast<int>(rem / g.tiles);  // (the last item may have fewer units, never more)
+    const int item = static_cast<int>(quotient(rem, g.tiles));  // (the last item may have fewer units, never more)
     const int at = static_cast<int>(rem - static_cast<long long>(item) * g.tiles);  // place within the item
     const int rows = min(2 * BR, g.rows - item * 2 * BR);
     s.pair = is_pair(rows, KV8, 2 * BR);
@@ -389,8 +395,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     const int C = teams_of(W, gridDim.x / 2);
     long long u = 0, u1 = 0;
     if (team < C) {
-        u = W * team / C;
-        u1 = W * (team + 1) / C;
+        u = quotient(W * team, C);
+        u1 = quotient(W * (team + 1), C);
     }
     const int bs = static_cast<int>(p.block_size.d);
     const int D = p.head_dim;

@@ -94,9 +94,10 @@ def run_paged(inp: PagedInputs, num_splits: int | None = None, gqa_pack: bool | 
                        pack, out, ws, stream, getattr(w, "k_scale", 1.0), getattr(w, "v_scale", 1.0))
 
 
-# Argument checks.  A decode step's launch takes a few microseconds, so a call
-# first makes one test of everything it needs, and only where that fails goes
-# through the arguments one by one for the message.
+# The calls of a decode step launch in a few microseconds, so they first try the
+# library's CPython module, which takes arguments that are just as they should be
+# (pd_binding.c); only what it declines is checked here, one by one, for the message,
+# and goes through the ctypes binding.
 _BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
 
 
@@ -166,25 +167,15 @@ def rope(rotation: pd.Rope, x, positions, out=None, inverse: bool = False, strea
     """Rotary positions: x [T, H, D] BF16 (strided in tokens and heads, e.g. the q and k heads of a fused
     projection) rotated by positions [T] int32; returns out [T, H, D] (contiguous unless given; x itself
     rotates in place).  inverse turns back: the map that takes gradients of out to gradients of x."""
-    shape, dev = x.shape, pd.current_device()
-    st = x.stride()
-    if not (x.dtype is _BF16 and len(shape) == 3 and shape[2] == rotation.head_dim and st[2] == 1 and x.get_device() == dev
-            and positions.dtype is _I32 and positions.shape == shape[:1] and positions.is_contiguous()
-            and positions.get_device() == dev and out is None):
-        _check_rope(rotation, x, positions, out, dev)
-    T, H, D = shape
+    if stream is None:
+        done = pd.quick().rope(pd._handle(rotation), rotation.head_dim, x, positions, out, inverse)
+        if done is not NotImplemented:
+            return done
+    _check_rope(rotation, x, positions, out, pd.current_device())
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=x.device)
-        if stream is not None:
-            _used_on(stream, out)
-        so = (H * D, D)
-    else:
-        so = out.stride()
-    rc = pd.lib().pd_rope_apply(
-        pd._handle(rotation), x.data_ptr(), st[0] if T > 1 else H * D, st[1] if H > 1 else D, positions.data_ptr(),
-        out.data_ptr(), so[0] if T > 1 else H * D, so[1] if H > 1 else D, T, H, inverse, pd._stream(stream))
-    if rc < 0:
-        pd._check(rc)
+        out = torch.empty(x.shape, dtype=_BF16, device=x.device)
+        _used_on(stream, out)
+    pd.pd_rope_apply(rotation, x, positions, out, inverse, stream)
     return out
 
 
@@ -217,52 +208,20 @@ def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, to
     None) rotated on the way and returned as q_out [T, Hq, D].  token_starts [S + 1] says which rows each
     sequence has; None: one each.  uint8 caches hold E4M3 codes of x / k_scale and x / v_scale.  Rows of no
     sequence are left as they were, in q_out too."""
-    dev = pd.current_device()
-    shape, tables, cache, kind = k.shape, block_table.shape, k_cache.shape, k_cache.dtype
-    sk, sv = k.stride(), v.stride()
-    if not (len(shape) == 3 and len(tables) == 2 and len(cache) == 4 and cache[2:] == shape[1:] and v.shape == shape
-            and (kind is _BF16 or kind is _U8) and v_cache.dtype is kind and v_cache.shape == cache
-            and k.dtype is _BF16 and v.dtype is _BF16 and sk[2] == 1 and sv[2] == 1
-            and (sk[1] == sv[1] == shape[2] or shape[1] == 1) and context_lens.shape == tables[:1]
-            and context_lens.dtype is _I32 and block_table.dtype is _I32 and k_cache.is_contiguous()
-            and v_cache.is_contiguous() and block_table.is_contiguous() and context_lens.is_contiguous()
-            and k.get_device() == v.get_device() == k_cache.get_device() == v_cache.get_device()
-            == block_table.get_device() == context_lens.get_device() == dev
-            and (token_starts is None or (token_starts.dtype is _I32 and token_starts.shape == (tables[0] + 1,)
-                                          and token_starts.is_contiguous() and token_starts.get_device() == dev))):
-        _check_append(q, k, v, k_cache, v_cache, block_table, context_lens, token_starts, q_out, dev)
-    T, Hkv, D = shape
-    if q is None:
-        Hq, qp, qs, op = 0, None, 0, None
-        if q_out is not None:
-            raise ValueError("q_out without q")
+    if stream is None and q is not None:
+        done = pd.quick().append_kv(pd._handle(rotation) or 0, 0 if rotation is None else rotation.head_dim, q, k, v, k_cache,
+                                    v_cache, block_table, context_lens, token_starts, q_out, k_scale, v_scale)
+        if done is not NotImplemented:
+            return done
+    _check_append(q, k, v, k_cache, v_cache, block_table, context_lens, token_starts, q_out, pd.current_device())
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+        _used_on(stream, q_out)
+    if k_cache.dtype is _U8:
+        pd.pd_append_kv_fp8(rotation, q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
+                            token_starts, stream)
     else:
-        sq, sh = q.stride(), q.shape
-        if not (q.dtype is _BF16 and len(sh) == 3 and sh[0] == T and sh[2] == D and sq[2] == 1 and q.get_device() == dev
-                and (sq[1] == D or sh[1] == 1) and q_out is None):
-            _check_append(q, k, v, k_cache, v_cache, block_table, context_lens, token_starts, q_out, dev)
-        Hq = sh[1]
-        if q_out is None:
-            q_out = torch.empty(sh, dtype=_BF16, device=q.device)
-            if stream is not None:
-                _used_on(stream, q_out)
-        qp, qs, op = q.data_ptr(), sq[0] if T > 1 else Hq * D, q_out.data_ptr()
-    one = Hkv * D  # (a single token's stride may be anything)
-    L = pd.lib()
-    if kind is _U8:
-        rc = L.pd_append_kv_fp8(
-            pd._handle(rotation), qp, qs, k.data_ptr(), sk[0] if T > 1 else one, v.data_ptr(), sv[0] if T > 1 else one, op,
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, block_table.data_ptr(), tables[1],
-            context_lens.data_ptr(), None if token_starts is None else token_starts.data_ptr(), T, tables[0], Hq, Hkv, D,
-            cache[1], cache[0], pd._stream(stream))
-    else:
-        rc = L.pd_append_kv(
-            pd._handle(rotation), qp, qs, k.data_ptr(), sk[0] if T > 1 else one, v.data_ptr(), sv[0] if T > 1 else one, op,
-            k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), tables[1], context_lens.data_ptr(),
-            None if token_starts is None else token_starts.data_ptr(), T, tables[0], Hq, Hkv, D, cache[1], cache[0],
-            pd._stream(stream))
-    if rc < 0:
-        pd._check(rc)
+        pd.pd_append_kv(rotation, q, k, v, q_out, k_cache, v_cache, block_table, context_lens, token_starts, stream)
     return q_out
 
 
@@ -298,46 +257,26 @@ def decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_sta
     batch, one group) attend to the prefix_lens[g] tokens prefix_table[g] names, then to their own context_lens
     tokens; a prefix is read once for its group.  Returns out [S, Hq, D] BF16.  uint8 caches are FP8 E4M3 codes
     with per-tensor scales."""
-    dev = pd.current_device()
-    shape, cache, kind, tables, prefixes = q.shape, k_cache.shape, k_cache.dtype, block_table.shape, prefix_table.shape
-    if not (len(shape) == 3 and len(cache) == 4 and len(tables) == 2 and len(prefixes) == 2 and q.dtype is _BF16
-            and (kind is _BF16 or kind is _U8) and v_cache.dtype is kind and v_cache.shape == cache and cache[3] == shape[2]
-            and context_lens.shape == shape[:1] and tables[0] == shape[0] and prefix_lens.shape == prefixes[:1]
-            and block_table.dtype is _I32 and context_lens.dtype is _I32 and prefix_table.dtype is _I32
-            and prefix_lens.dtype is _I32 and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and block_table.is_contiguous() and context_lens.is_contiguous() and prefix_table.is_contiguous()
-            and prefix_lens.is_contiguous()
-            and q.get_device() == k_cache.get_device() == v_cache.get_device() == block_table.get_device()
-            == context_lens.get_device() == prefix_table.get_device() == prefix_lens.get_device() == dev and out is None
-            and (group_starts is None or (group_starts.dtype is _I32 and group_starts.shape == (prefixes[0] + 1,)
-                                          and group_starts.is_contiguous() and group_starts.get_device() == dev))):
-        _check_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens, out, dev)
-    S, Hq, D = shape
-    G, L = prefixes[0], pd.lib()
+    if stream is None:
+        done = pd.quick().decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table,
+                                             context_lens, inv_sqrt_d, num_splits, out, ws, k_scale, v_scale)
+        if done is not NotImplemented:
+            return done
+    _check_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens, out,
+                  pd.current_device())
+    S, Hq, D = q.shape
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
-        if stream is not None:
-            _used_on(stream, out)
+        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+        _used_on(stream, out)
     if ws is None:
-        ws_bytes = L.pd_prefix_workspace_bytes(S, G, Hq, cache[2], D, num_splits)
-        ws = torch.empty(ws_bytes, dtype=_U8, device=q.device)
-        if stream is not None:
-            _used_on(stream, ws)
+        ws = prefix_workspace(S, prefix_lens.shape[0], Hq, max(1, k_cache.shape[2]), D, num_splits, q.device)
+        _used_on(stream, ws)
+    if k_cache.dtype is _U8:
+        pd.pd_decode_attn_prefix_fp8(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_lens, group_starts,
+                                     block_table, context_lens, out, inv_sqrt_d, num_splits, ws, stream)
     else:
-        ws_bytes = ws.numel() * ws.element_size()
-    gs = None if group_starts is None else group_starts.data_ptr()
-    if kind is _U8:
-        rc = L.pd_decode_attn_prefix_fp8(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, prefix_table.data_ptr(), prefixes[1],
-            prefix_lens.data_ptr(), gs, G, block_table.data_ptr(), tables[1], context_lens.data_ptr(), out.data_ptr(), S, Hq,
-            cache[2], D, cache[1], cache[0], inv_sqrt_d, num_splits, ws.data_ptr(), ws_bytes, pd._stream(stream))
-    else:
-        rc = L.pd_decode_attn_prefix(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_table.data_ptr(), prefixes[1], prefix_lens.data_ptr(),
-            gs, G, block_table.data_ptr(), tables[1], context_lens.data_ptr(), out.data_ptr(), S, Hq, cache[2], D, cache[1],
-            cache[0], inv_sqrt_d, num_splits, ws.data_ptr(), ws_bytes, pd._stream(stream))
-    if rc < 0:
-        pd._check(rc)
+        pd.pd_decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens,
+                                 out, inv_sqrt_d, num_splits, ws, stream)
     return out
 
 

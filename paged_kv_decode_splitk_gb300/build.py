@@ -1,4 +1,5 @@
-"""Build libpd.so (the C-ABI CUDA library) in-tree with nvcc for sm_103a.
+"""Build libpd.so (the C-ABI CUDA library) in-tree with nvcc for sm_103a, and the
+CPython module over it (pd_binding.so) with gcc.
 
 Each translation unit compiles in its own nvcc process, in parallel; the
 objects and the shared library land in ``paged_kv_decode_splitk_gb300/_build``.
@@ -9,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpd.so")
+BINDING = os.path.join(BUILD, "pd_binding.so")
 
 SOURCES = ["pd_api.cu", "pd_small.cu", "pd_unit_d64.cu", "pd_unit_d128.cu", "pd_unit_d256.cu",
            "pd_unit_fp8_d64.cu", "pd_unit_fp8_d128.cu", "pd_unit_fp8_d256.cu", "pd_noalloc.cu", "pd_rope.cu",
@@ -72,6 +75,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fvisibility=hidden"]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "pd_binding.c")
+    if force or _stale(BINDING, [src, LIB, os.path.join(INCLUDE, "pd.h")]):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-Wextra", "-Wno-cast-function-type", "-fPIC", "-fvisibility=hidden", "-shared",
+               f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", src, LIB, "-Wl,-rpath,$ORIGIN", "-o", tmp]
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, BINDING)
     return LIB
 
 

@@ -172,6 +172,31 @@ def lib():
     return _lib
 
 
+_quick = None
+
+
+def quick():
+    """The CPython module over the library (csrc/pd_binding.c), built beside it: api.py's first try at a call."""
+    global _quick
+    if _quick is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch
+
+        lib()
+        path = os.path.join(PKG, "_build", "pd_binding.so")
+        if not os.path.exists(path):
+            raise PdLibraryError(f"{path} is missing: build it with `python -m paged_kv_decode_splitk_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("pd_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pd_binding", loader))
+        loader.exec_module(module)
+        current_device()
+        module.setup(torch.bfloat16, torch.uint8, torch.int32, torch.empty, _torch_device, _torch_stream)
+        _quick = module
+    return _quick
+
+
 def header_symbols() -> list[str]:
     """Function names include/pd.h declares."""
     text = open(HEADER).read()

@@ -423,8 +423,8 @@ int pd_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride, in
  *   token_starts  [num_seqs + 1] int32, non-decreasing: rows token_starts[s] to
  *                 token_starts[s+1] - 1 are the new tokens of sequence s, its
  *                 last ones.  Rows before token_starts[0] and from
- *                 token_starts[num_seqs] on belong to no sequence: nothing of
- *                 them is read or written.  NULL: one token per sequence
+ *                 token_starts[num_seqs] on belong to no sequence: nothing is
+ *                 written for them.  NULL: one token per sequence
  *                 (num_tokens == num_seqs), none for a sequence of length 0.
  * A token whose position is negative or beyond its block table raises
  * PD_DEV_BAD_CONTEXT_LEN and is left out (q_out too); one whose block id is

@@ -27,6 +27,7 @@
 #include "pd.h"
 #include "pd_device.cuh"
 #include "pd_internal.h"
+#include "pd_tcgen05.cuh"
 
 struct pd_rope {
     int head_dim, rot_dim, layout, device;
@@ -118,6 +119,17 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16 *p, const float (&f)[W]
     else
         *p = __float2bfloat16_rn(f[0]);
 }
+template <int W>
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const Vec<W> &v) {
+    if constexpr (W == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    else if constexpr (W == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(v.w[0], v.w[1]);
+    else if constexpr (W == 2)
+        *reinterpret_cast<uint32_t *>(p) = v.w[0];
+    else
+        *reinterpret_cast<unsigned short *>(p) = static_cast<unsigned short>(v.w[0]);
+}
 // Two values -> two E4M3 codes (lo in the low byte), nearest even, saturating.
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     uint16_t d;
@@ -190,22 +202,32 @@ struct Unit {
         a = load_vec<W>(row + ca);
         if (HALF && !pass) b = load_vec<W>(row + cb);
     }
-    // rotated values of the columns at a (fa) and, HALF, at b (fb)
+    // rotated values of the columns at a (fa) and, HALF, at b (fb), two pairs' (or
+    // both of a pair's) products an instruction
     __device__ __forceinline__ void rotate(const Turn<kPairs> &t, float (&fa)[W], float (&fb)[W]) const {
-        if constexpr (HALF) {
+        if constexpr (HALF && W > 1) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float x = elem<W>(a, i), y = elem<W>(b, i);
-                fa[i] = fmaf(x, t.c[i], -(y * t.s[i]));
-                fb[i] = fmaf(y, t.c[i], x * t.s[i]);
+            for (int i = 0; i < W; i += 2) {
+                const uint64_t x = tc::pack_f32x2(elem<W>(a, i), elem<W>(a, i + 1)), y = tc::pack_f32x2(elem<W>(b, i), elem<W>(b, i + 1));
+                const uint64_t c = tc::pack_f32x2(t.c[i], t.c[i + 1]), s = tc::pack_f32x2(t.s[i], t.s[i + 1]);
+                const uint64_t m = tc::pack_f32x2(-t.s[i], -t.s[i + 1]);
+                tc::unpack_f32x2(tc::fma_f32x2(x, c, tc::mul_f32x2(y, m)), fa[i], fa[i + 1]);
+                tc::unpack_f32x2(tc::fma_f32x2(y, c, tc::mul_f32x2(x, s)), fb[i], fb[i + 1]);
             }
+        } else if constexpr (HALF) {
+            const float x = elem<W>(a, 0), y = elem<W>(b, 0);
+            fa[0] = fmaf(x, t.c[0], -(y * t.s[0]));
+            fb[0] = fmaf(y, t.c[0], x * t.s[0]);
         } else {
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) {
                 const float x = elem<W>(a, 2 * i), y = elem<W>(a, 2 * i + 1);
                 const bool live = i < t.live;
-                fa[2 * i] = live ? fmaf(x, t.c[i], -(y * t.s[i])) : x;
-                fa[2 * i + 1] = live ? fmaf(y, t.c[i], x * t.s[i]) : y;
+                float u, v;
+                tc::unpack_f32x2(tc::fma_f32x2(tc::pack_f32x2(x, y), tc::pack_f32x2(t.c[i], t.c[i]),
+                                               tc::mul_f32x2(tc::pack_f32x2(y, x), tc::pack_f32x2(-t.s[i], t.s[i]))), u, v);
+                fa[2 * i] = live ? u : x;
+                fa[2 * i + 1] = live ? v : y;
             }
         }
     }
@@ -269,13 +291,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     for (int r = 0; r < ROWS; ++r) {
         const int h = slot + r * step;
         if (h < p.heads) {
-            float fa[W], fb[W];
-            if (pass)
-                un[r].plain(fa, fb);
-            else
+            __nv_bfloat16 *at = o + h * p.o_head;
+            if (pass) {
+                store_vec<W>(at + ca, un[r].a);
+            } else {
+                float fa[W], fb[W];
                 un[r].rotate(t, fa, fb);
-            store_bf16<W>(o + h * p.o_head + ca, fa);
-            if (HALF && !pass) store_bf16<W>(o + h * p.o_head + cb, fb);
+                store_bf16<W>(at + ca, fa);
+                if (HALF) store_bf16<W>(at + cb, fb);
+            }
         }
     }
 }
@@ -390,27 +414,31 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
         const int h = slot + r * step;
         if (h < rows) {
             const int hk = h - p.q_heads, hv = hk - p.kv_heads;
-            float fa[W], fb[W];
-            if (pass || hv >= 0)
-                un[r].plain(fa, fb);
-            else
-                un[r].rotate(t, fa, fb);
-            if (hk < 0) {
-                __nv_bfloat16 *o = p.q_out + (static_cast<long long>(tok) * p.q_heads + h) * D;
-                store_bf16<W>(o + ca, fa);
-                if (HALF && !pass) store_bf16<W>(o + cb, fb);
-            } else if (!bad) {
-                const long long at = (cell + (hv < 0 ? hk : hv)) * D;
-                void *cache = hv < 0 ? p.k_cache : p.v_cache;
-                if constexpr (KV8) {
+            const bool copied = pass || hv >= 0;
+            const long long at = (cell + (hv < 0 ? hk : hv)) * D;  // in a cache
+            if (KV8 && hk >= 0) {
+                if (!bad) {
+                    float fa[W], fb[W];
+                    if (copied)
+                        un[r].plain(fa, fb);
+                    else
+                        un[r].rotate(t, fa, fb);
                     const float scale = hv < 0 ? p.k_scale : p.v_scale;
-                    uint8_t *o = static_cast<uint8_t *>(cache) + at;
+                    uint8_t *o = static_cast<uint8_t *>(hv < 0 ? p.k_cache : p.v_cache) + at;
                     store_e4m3<W>(o + ca, fa, scale);
                     if (HALF && !pass) store_e4m3<W>(o + cb, fb, scale);
+                }
+            } else if (hk < 0 || !bad) {
+                __nv_bfloat16 *o = hk < 0 ? p.q_out + (static_cast<long long>(tok) * p.q_heads + h) * D
+                                          : static_cast<__nv_bfloat16 *>(hv < 0 ? p.k_cache : p.v_cache) + at;
+                if (copied) {
+                    store_vec<W>(o + ca, un[r].a);
+                    if (HALF && !pass) store_vec<W>(o + cb, un[r].b);
                 } else {
-                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(cache) + at;
+                    float fa[W], fb[W];
+                    un[r].rotate(t, fa, fb);
                     store_bf16<W>(o + ca, fa);
-                    if (HALF && !pass) store_bf16<W>(o + cb, fb);
+                    if (HALF) store_bf16<W>(o + cb, fb);
                 }
             }
         }

@@ -442,10 +442,10 @@ int pd_append_kv(const pd_rope *rope, const void *q, int64_t q_token_stride, con
                  int num_blocks, void *stream);
 
 /* pd_append_kv into an FP8 cache of E4M3 codes: the code of a key (value) x is
- * x / k_scale (x / v_scale), taken in FP32 from the unrounded rotation and
+ * x times 1 / k_scale (1 / v_scale), all in FP32 from the unrounded rotation, and
  * rounded once to the nearest E4M3 value (ties to even), saturating at +-448.
  * A NaN becomes a NaN code, which is no valid cache content.
- *   k_scale, v_scale  finite, positive.
+ *   k_scale, v_scale  positive, finite, neither they nor 1 over them subnormal.
  * head_dim must be a multiple of 16, as for pd_decode_attn_fp8. */
 int pd_append_kv_fp8(const pd_rope *rope, const void *q, int64_t q_token_stride, const void *k,
                      int64_t k_token_stride, const void *v, int64_t v_token_stride, void *q_out,

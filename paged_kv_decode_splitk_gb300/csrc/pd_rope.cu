@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <new>
@@ -51,6 +52,7 @@ struct RowPlan {
     FastDiv slots;   // threads that share a token's rows
     int pair_units;
     int half;        // rot_dim / 2
+    int pitch;       // of the table of sines and cosines
     FastDiv fd_half;
     const unsigned long long *turns;
     float factor;
@@ -73,7 +75,7 @@ struct AppendParams {
     long long q_tok, k_tok, v_tok;
     __nv_bfloat16 *q_out;
     void *k_cache, *v_cache;
-    float k_scale, v_scale;
+    float k_scale, v_scale;   // of a code: 1 over the cache's scales
     const int32_t *block_table, *context_lens, *token_starts;
     int max_blocks, num_seqs, num_blocks;
     int q_heads, kv_heads, head_dim;
@@ -141,9 +143,13 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[W], floa
     uint32_t c[W >= 2 ? W / 2 : 1];
     if constexpr (W >= 2) {
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) c[i] = pack_e4m3x2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale));
+        for (int i = 0; i < W / 2; ++i) {
+            float x, y;
+            tc::unpack_f32x2(tc::mul_f32x2(tc::pack_f32x2(f[2 * i], f[2 * i + 1]), tc::pack_f32x2(scale, scale)), x, y);
+            c[i] = pack_e4m3x2(x, y);
+        }
     } else {
-        c[0] = pack_e4m3x2(__fdiv_rn(f[0], scale), 0.f);
+        c[0] = pack_e4m3x2(f[0] * scale, 0.f);
     }
     if constexpr (W == 8)
         *reinterpret_cast<uint2 *>(p) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
@@ -156,11 +162,13 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[W], floa
 }
 
 // Cosines and sines of the tokens of a block, times the factor: pair i of the
-// block's token j at j * half + i.  A token has units * slots threads and at most
+// block's token j at j * pitch + i.  A token has units * slots threads and at most
 // 8 pairs a unit (4 where a unit is 8 neighbouring columns), so the block's 256
 // threads touch at most 256 / (units * slots) + 2 tokens and this many pairs.
-constexpr int kTableMax = 256 * 8 + 2 * 16 * 8;
-struct TurnTable {
+// Rows are a multiple of 4 pairs apart, for 16-byte loads.
+constexpr int kTableMax = (256 * 8 + 2 * 16 * 8 + 3 * (256 + 2) + 3) / 4 * 4;
+static_assert(kTableMax % 4 == 0, "the sines begin at a multiple of 16 bytes");
+struct __align__(16) TurnTable {
     float c[kTableMax], s[kTableMax];
 };
 __device__ __forceinline__ void fill_turn(const RowPlan &p, TurnTable &tab, int at, int pair, int position) {
@@ -180,15 +188,24 @@ struct Turn {
     int live;  // pairs that turn: an interleaved unit may end in copied columns
 };
 template <int N>
+__device__ __forceinline__ void load_turn(const float *p, float (&v)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(p + i);
+            v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = p[i];
+    }
+}
+template <int N>
 __device__ __forceinline__ Turn<N> turn_of(const RowPlan &p, const TurnTable &tab, int token, int first) {
     Turn<N> t;
     t.live = p.half - first;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = token * p.half + min(first + i, p.half - 1);
-        t.c[i] = tab.c[at];
-        t.s[i] = tab.s[at];
-    }
+    load_turn<N>(tab.c + token * p.pitch + first, t.c);  // (past `live`: of the row's padding)
+    load_turn<N>(tab.s + token * p.pitch + first, t.s);
     return t;
 }
 
@@ -280,7 +297,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
     for (int e = threadIdx.x; e < (last - first + 1) * p.plan.half; e += kRopeThreads) {
         const int j = fast_div(e, p.plan.fd_half);
-        fill_turn(p.plan, tab, e, e - j * p.plan.half, p.positions[first + j]);
+        fill_turn(p.plan, tab, e + j * (p.plan.pitch - p.plan.half), e - j * p.plan.half, p.positions[first + j]);
     }
     __syncthreads();
     if (!in) return;
@@ -398,7 +415,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
     __syncthreads();
     for (int e = threadIdx.x; e < count * p.plan.half; e += kRopeThreads) {
         const int j = fast_div(e, p.plan.fd_half);
-        fill_turn(p.plan, tab, e, e - j * p.plan.half, place[j][0]);
+        fill_turn(p.plan, tab, e + j * (p.plan.pitch - p.plan.half), e - j * p.plan.half, place[j][0]);
     }
     __syncthreads();
     if (!in) return;
@@ -464,6 +481,7 @@ RowPlan plan_rows(int head_dim, int rot_dim, int layout, int w, const unsigned l
     RowPlan p = {};
     p.half = rot_dim / 2;
     p.fd_half = make_fastdiv(p.half);
+    p.pitch = (p.half + 3) / 4 * 4;
     if (layout == PD_ROPE_HALF) {
         p.pair_units = p.half / w;
         p.units = make_fastdiv(p.pair_units + (head_dim - rot_dim) / w);
@@ -542,8 +560,10 @@ int append_impl(const char *what, const pd_rope *rope, const void *q, int64_t q_
     if (kv8) {
         if (head_dim % 16 != 0)
             return report(PD_ERR_UNSUPPORTED, "FP8 cache: head_dim %d must be a multiple of 16", head_dim);
-        if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale <= 0.f || v_scale <= 0.f)
-            return report(PD_ERR_INVALID, "FP8 cache: k_scale and v_scale must be finite and positive");
+        if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || !(k_scale >= FLT_MIN) ||
+            !(v_scale >= FLT_MIN) || !(1.f / k_scale >= FLT_MIN) || !(1.f / v_scale >= FLT_MIN))
+            return report(PD_ERR_INVALID, "FP8 cache: k_scale and v_scale must be finite, positive and no subnormal numbers, nor their "
+                                          "reciprocals");
     }
     if (num_tokens < 0 || num_seqs < 0)
         return report(PD_ERR_INVALID, "%s: num_tokens %d, num_seqs %d", what, num_tokens, num_seqs);
@@ -593,8 +613,8 @@ int append_impl(const char *what, const pd_rope *rope, const void *q, int64_t q_
     p.q_out = static_cast<__nv_bfloat16 *>(q_out);
     p.k_cache = k_cache;
     p.v_cache = v_cache;
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
+    p.k_scale = 1.f / k_scale;
+    p.v_scale = 1.f / v_scale;
     p.block_table = block_table;
     p.context_lens = context_lens;
     p.token_starts = token_starts;

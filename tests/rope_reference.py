@@ -49,7 +49,7 @@ def bf16_bound(ref, size):
 
 
 # E4M3 rounds by at most 2^-4 of the value, or half its smallest step, 2^-10; the FP32 error of the value, in
-# units of the code, comes before it (its division by the scale adds 2^-24 of the value).
+# units of the code, comes before it (the reciprocal of the scale and the product with it add 2^-23 of the value).
 def e4m3_bound(code_ref, size, scale):
     before = 2.0**-20 * size / scale + 2.0**-23 * np.abs(code_ref)
     return np.maximum(2.0**-4 * np.abs(code_ref), 2.0**-10) + 1.25 * before

@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) prefix_merge_kernel(const
 
     // ---- the row's group: the last one that begins at or before the sequence ----
     int L = in ? p.context_lens[s] : 0;
-    const long long W = *p.plan_total;
+    const PlanTotal plan = *p.plan_total;
+    const long long W = plan.units;
     GroupPlan g = {};
     for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
         GroupPlan one = {};
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) prefix_merge_kernel(const
         const bool pair = is_pair(of_item, p.kv8 != 0, IR);
         const int places = pair ? g.tiles : (g.tiles + 1) >> 1;
         const long long u = g.first_unit + kvh * g.head_units(IR, p.kv8 != 0) + static_cast<long long>(item) * g.tiles;
-        const int C = teams_of(W, p.teams);
+        const int C = plan.teams;
         const int c = has ? team_of_unit(sub == 0 ? u : u + places - 1, C, W) : 0;
         const int c0 = __shfl_sync(0xffffffffu, c, head_lane), c1 = __shfl_sync(0xffffffffu, c, head_lane + 1);
         if (has) {
@@ -268,7 +269,7 @@ Layout layout_of(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads
     const size_t slots = 2 * (static_cast<size_t>(l.max_items) + kMaxTeams);
     l.own_o = take(rows * head_dim * sizeof(float));
     l.own_ml = take(rows * 2 * sizeof(float));
-    l.plan_total = take(sizeof(long long));
+    l.plan_total = take(sizeof(PlanTotal));
     l.plan_groups = take(sizeof(GroupPlan) * kMaxGroups);
     l.part_ml = take(slots * BR * 2 * sizeof(float));
     l.part_o = take(slots * BR * dpad_of(head_dim) * sizeof(float));
@@ -347,6 +348,8 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     p.prefix_table = prefix_table;
     p.prefix_lens = prefix_lens;
     p.group_starts = group_starts;
+    p.context_lens = context_lens;
+    p.max_own_tokens = max_blocks * block_size;
     p.num_groups = num_groups;
     p.max_prefix_blocks = max_prefix_blocks;
     p.num_blocks = num_blocks;
@@ -367,7 +370,7 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     p.part_ml = reinterpret_cast<float *>(ws + lay.part_ml);
     p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
     p.plan_groups = reinterpret_cast<GroupPlan *>(ws + lay.plan_groups);
-    p.plan_total = reinterpret_cast<long long *>(ws + lay.plan_total);
+    p.plan_total = reinterpret_cast<PlanTotal *>(ws + lay.plan_total);
     const int dpad = dpad_of(head_dim);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = kv8 ? dispatch_prefix<true>(dpad, &view.k, &view.v, p, teams, st)
@@ -402,7 +405,6 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     m.num_splits = num_splits;
     m.min_kv_per_split = PD_MIN_KV_PER_SPLIT;
     m.max_tokens = max_blocks * block_size;
-    m.teams = teams;
     m.v_scale = kv8 ? v_scale : 1.f;
     m.fd_hq = make_fastdiv(num_q_heads);
     m.fd_group = make_fastdiv(group);

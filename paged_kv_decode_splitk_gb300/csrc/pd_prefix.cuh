@@ -144,12 +144,39 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
     return true;
 }
 
+// How many teams share the prefixes' units.  The own-token pass runs on the SMs
+// the prefix pass leaves, and the step is shortest where both end together: with
+// n SMs, C teams, units of B us in all and U the own pass's time on one SM,
+//   B / C = U / (n - 2 C).
+// Half of U is taken, since teams too few cost more than teams too many.  Measured
+// (us, all 76 teams -> about as many as this gives): 64 sequences behind 8192
+// tokens 47.3 -> 41.2 (24 teams; 16: 52.1), 256 behind 32768 136 -> 124 (60), six
+// groups of wide heads 32.3 -> 30.7 (48), 32 behind 16385 over FP8 51.3 -> 46.9
+// (48).  A team has four units or more beyond the first eight teams: each is a
+// partial more of all its rows to write and fold (256 units without own tokens:
+// 19.7 us on 76 teams, 17.0 on 32).
+__device__ __forceinline__ int share_units(long long units, float units_us, float own_us, int most) {
+    const int c = static_cast<int>(ceilf(__fdividef(2.f * most * units_us, 0.5f * own_us + 2.f * units_us)));
+    const long long enough = max((units + 3) / 4, min(units, 8ll));
+    return static_cast<int>(max(1ll, min(enough, static_cast<long long>(min(c, most)))));
+}
+
+// The time of a unit on a team, measured (us): the conversion bounds an FP8 tile;
+// two full row tiles of products a pair's; one, and memory, the others'.
+template <int DPAD, bool KV8>
+__device__ __forceinline__ float unit_time(int rows) {
+    const bool pair = is_pair(rows, KV8, item_rows(DPAD));
+    const float us = KV8 ? 2.1f : pair ? (rows > 2 * kRowTile ? 1.4f : 0.9f) : DPAD == 256 ? 1.f : 1.3f;
+    return DPAD == 64 ? 0.6f * us : us;
+}
+
 // The groups' units and items, by one warp: running sums over chunks of 32
 // groups.  Returns false (on every lane) where group_starts is not
 // non-decreasing within the batch or asks for more items than the workspace holds.
 template <int DPAD, bool KV8>
-__device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *grp, long long *total, int lane, bool flag) {
+__device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *grp, long long *units_all, float *time_us, int lane, bool flag) {
     long long units = 0;
+    float time = 0.f;  // of the units, this lane's share
     int items = 0;
     bool bad = false;
     for (int base = 0; base < p.num_groups; base += 32) {
@@ -175,6 +202,7 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
             if (r.tiles > 0 && r.items > 0) {
                 it = r.items * p.num_kv_heads;
                 mine = r.head_units(item_rows(DPAD), KV8) * p.num_kv_heads;
+                time += mine * unit_time<DPAD, KV8>(min(r.rows, item_rows(DPAD)));
             }
         }
         long long su = mine;
@@ -197,7 +225,10 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
     }
     bad = __any_sync(0xffffffffu, bad) || items > p.max_items;
     if (bad && flag) dev::flag_status(p.status, PD_DEV_BAD_GROUPS);
-    *total = bad ? 0 : units;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) time += __shfl_xor_sync(0xffffffffu, time, off);
+    *units_all = bad ? 0 : units;
+    *time_us = time;
     return !bad;
 }
 
@@ -332,9 +363,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                    bar_rempty = bar_rfull + 24, bar_s = bar_rempty + 24, bar_p = bar_s + 16, bar_o = bar_p + 16,
                    bar_q = bar_o + 16, bar_tail = bar_q + 16, bar_x = bar_tail + 8;
     static_assert(2 * NST + 16 <= kRegionBars, "barrier region");
-    long long *total_s = reinterpret_cast<long long *>(smem + L::misc);
-    volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc + 8);
-    uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 16);
+    long long *units_s = reinterpret_cast<long long *>(smem + L::misc);
+    unsigned *own_s = reinterpret_cast<unsigned *>(smem + L::misc + 8);  // sixteens of the sequences' own tokens
+    float *time_s = reinterpret_cast<float *>(smem + L::misc + 16);
+    volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc + 20);
+    uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 24);
 
     // (the warp's number from one lane, so that the compiler knows it to be the
     // same on all: the product warp's operands then live in uniform registers)
@@ -363,16 +396,22 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         dev::mbar_init(bar_x, 256);
         dev::fence_mbar_init();
         *gave_up = 0;
+        *own_s = 0;
         dev::prefetch_tensormap(&maps.k[0]);
         dev::prefetch_tensormap(&maps.v[0]);
     }
     dev::cluster_arrive_relaxed();
     if (warp == 1) tc::tmem_alloc_512(dev::smem_addr(tmem_s));
+    __syncthreads();      // (the sum of the own tokens starts at zero)
     dev::griddep_wait();  // q, the caches, tables and lengths are final
     if (warp == 0) {
-        long long total;
-        const bool good = plan_groups<DPAD, KV8>(p, grp, &total, lane, blockIdx.x == 0);
-        if (lane == 0) *total_s = total;
+        long long units;
+        float time;
+        const bool good = plan_groups<DPAD, KV8>(p, grp, &units, &time, lane, blockIdx.x == 0);
+        if (lane == 0) {
+            *units_s = units;
+            *time_s = time;
+        }
         __syncwarp();
         if (blockIdx.x == 0) {  // the merge finds each row's partials from this
             for (int g = lane; g < p.num_groups; g += 32) {
@@ -380,8 +419,14 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (!good) r.tiles = 0;
                 p.plan_groups[g] = r;
             }
-            if (lane == 0) *p.plan_total = total;
         }
+    } else if (warp > 1) {  // the sequences' own tokens (a sum of integers: the same in every CTA)
+        long long own = 0;
+#pragma unroll 4
+        for (int s = tid - 64; s < p.num_seqs; s += L::kThreads - 64) own += min(max(p.context_lens[s], 0), p.max_own_tokens);
+        // in sixteens, and no more of them than 32 bits hold from 320 threads
+        const unsigned sum = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(min(own >> 4, 1ll << 23)));
+        if (lane == 0 && sum) atomicAdd(own_s, sum);
     }
     dev::cluster_wait();  // the peer's barriers are initialised
     tc::fence_before();
@@ -391,8 +436,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     // of this one, may start wherever there is room.
     dev::griddep_launch_dependents();
     constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
-    const long long W = *total_s;
-    const int C = teams_of(W, gridDim.x / 2);
+    const long long W = *units_s;
+    // (the own pass draws 5.4 MB of a BF16 cache a us from all SMs, 2.8 of FP8 codes)
+    const float own_us = static_cast<float>(*own_s) * (p.num_kv_heads * p.head_dim * (KV8 ? 32.f / 2.8e6f : 64.f / 5.4e6f)) * gridDim.x;
+    const int C = W > 0 ? share_units(W, *time_s, own_us, gridDim.x / 2) : 0;
+    if (blockIdx.x == 0 && tid == 0) *p.plan_total = {W, C, 0};
     long long u = 0, u1 = 0;
     if (team < C) {
         u = quotient(W * team, C);

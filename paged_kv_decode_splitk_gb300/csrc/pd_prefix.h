@@ -32,13 +32,13 @@ static_assert(is_pair(item_rows(64), true, item_rows(64)) && is_pair(item_rows(2
                   is_pair(block_rows(256) + 1, true, item_rows(256)) && is_pair(block_rows(64) + 1, true, item_rows(64)),
               "full items are by halves, and so is what one CTA cannot take");
 
-// Teams that share W units: all there are, but each at least kMinUnits (a team
-// more is a partial more of each of its rows to write and fold).
-constexpr int kMinUnits = 1;
-__host__ __device__ inline int teams_of(long long W, int most) {
-    const long long n = (W + kMinUnits - 1) / kMinUnits;
-    return n < most ? static_cast<int>(n) : most;
-}
+// What the prefix pass found the work to be: units in all, and the teams that
+// share them.
+struct PlanTotal {
+    long long units;
+    int teams;
+    int pad;
+};
 
 // One group on the line of work units.  Its items are, for each KV head, the
 // item_rows-row pieces of its query rows; a unit of a pair item is a tile, of one
@@ -65,6 +65,8 @@ struct PrefixParams {
     const __nv_bfloat16 *q;
     const int32_t *prefix_table, *prefix_lens, *group_starts;
     int num_groups, max_prefix_blocks, num_blocks;
+    const int32_t *context_lens;   // of the own tokens, with the most a table holds
+    int max_own_tokens;
     int num_seqs, num_q_heads, num_kv_heads, group, head_dim;
     FastDiv block_size, fd_group;
     int tok_dim;
@@ -75,19 +77,19 @@ struct PrefixParams {
     float *part_ml;     // [slot][block rows] (m, l); a team's item has two slots, one for each CTA
     float *part_o;      // [slot][dpad / 32][block rows][32], 16-byte chunks swapped by row
     GroupPlan *plan_groups;
-    long long *plan_total;
+    PlanTotal *plan_total;
     unsigned int *status;
 };
 
 struct MergeParams {
     const GroupPlan *plan_groups;
-    const long long *plan_total;
+    const PlanTotal *plan_total;
     const float *part_ml, *part_o;   // the prefix pass's
     const float *own_o, *own_ml;     // [rows, N, D] and [rows, N, 2]: the own-token pass's
     const int32_t *context_lens;
     __nv_bfloat16 *out;
     int num_groups, num_seqs, num_q_heads, num_kv_heads, group, head_dim, dpad;
-    int num_splits, min_kv_per_split, max_tokens, teams;
+    int num_splits, min_kv_per_split, max_tokens;
     int kv8, ways;
     float v_scale;      // of the prefix partials (an FP8 cache; the own-token pass applies its own)
     FastDiv fd_hq, fd_group, fd_split, fd_bs;

@@ -297,6 +297,10 @@ int pd_decode_attn_noalloc(const void *q, const void *k_cache, const void *v_cac
  * cache) before they meet V.  The same call on the same data gives the same
  * bits; unlike pd_decode_attn's, they depend on the batch (how a prefix is cut
  * depends on every group).
+ * A step's new tokens come behind the own tokens.  Where a prefix ends with a
+ * block, pd_append_kv takes tables that begin with the prefix's blocks and the
+ * lengths of prefix and own tokens together, and so rotates by whole positions;
+ * elsewhere pd_rope_apply rotates first and pd_append_kv copies.
  * Returns PD_OK, PD_ERR_INVALID, PD_ERR_WORKSPACE, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
 #define PD_MAX_PREFIX_GROUPS 256
 
@@ -391,7 +395,9 @@ void pd_rope_destroy(pd_rope *rope);
  *   x, out     BF16, 16-B aligned; row (t, h) starts at element
  *              t * token_stride + h * head_stride (strides positive multiples of 8 elements; the
  *              head_dim columns of a row are contiguous).  out is x itself with
- *              x's strides (in place), or shares no element with it.
+ *              x's strides (in place), or shares no element with it; no two of
+ *              its rows overlap (a token's heads lie within the token stride,
+ *              or a head's tokens within the head stride).
  *   positions  [num_tokens] int32; any value, negative ones turn backwards.
  *   inverse    0, or 1 for the rotation by minus the angles with the same
  *              factor c: the transposed map, which takes gradients of out to

@@ -804,6 +804,14 @@ int pd_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride, in
                           static_cast<long long>(s));
     if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
         return report(PD_ERR_INVALID, "pd_rope_apply: in place (out == x) needs equal strides");
+    // rows of out that share elements would be written by several threads: a token's
+    // heads lie within its stride, or a head's tokens within the head's
+    const int64_t T = num_tokens, H = num_heads, D = rope->head_dim, ot = out_token_stride, oh = out_head_stride;
+    const bool by_token = (H == 1 || oh >= D) && (T == 1 || (ot >= D && (ot - D) / oh >= H - 1));
+    const bool by_head = (T == 1 || ot >= D) && (H == 1 || (oh >= D && (oh - D) / ot >= T - 1));
+    if (!by_token && !by_head)
+        return report(PD_ERR_INVALID, "pd_rope_apply: rows of out overlap (strides %lld and %lld, %d tokens of %d heads)",
+                      static_cast<long long>(ot), static_cast<long long>(oh), num_tokens, num_heads);
     RopeParams p = {};
     const int w = unit_width(rope->layout, rope->rot_dim);
     p.plan = plan_rows(rope->head_dim, rope->rot_dim, rope->layout, w, rope->turns, rope->factor, inverse != 0);

@@ -68,7 +68,8 @@ cudaError_t launch_unit(const CUtensorMap *tmk, const CUtensorMap *tmv, const Un
     p.cluster = C;
     const long long grid_x = units * C;
     p.own_ctas = static_cast<unsigned>(grid_x);
-    if (grid_x + C > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int own = MODE == kModeOwn ? C : 0;  // the cluster that waits for the shared-prefix pass
+    if (grid_x + own > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     // A grid of many short units (several waves, one CTA per unit) keeps more
     // loads in flight with a deeper ring per warp; a single-wave grid keeps
     // the shallower one and more CTAs per SM.  Stages change no result.
@@ -101,7 +102,7 @@ cudaError_t launch_unit(const CUtensorMap *tmk, const CUtensorMap *tmv, const Un
         }
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid_x + (MODE == kModeOwn ? C : 0)));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid_x + own));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes);
     cfg.stream = stream;

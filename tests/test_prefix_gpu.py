@@ -308,3 +308,96 @@ def test_prefix_empty_batch():
     out = api.decode_attn_prefix(b.q[:0], b.kc, b.vc, i32(b.ptable), i32(b.plens), None, i32(b.table)[:0], i32(b.lens)[:0],
                                  b.scale, 2, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert out.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("plens", [[128, 64], [130, 77]], ids=["whole blocks", "ragged"])
+def test_steps_of_a_batch_in_one_graph(plens, fp8):
+    """Steps of a served batch: the new tokens rotated and appended behind each sequence's own, then the attention over
+    the group's prefix and those, all in one captured graph that counts the lengths itself.  Where a prefix ends with a
+    block, the append takes tables that begin with its blocks; else the tokens are rotated first, by their positions."""
+    steps, Hq, Hkv, D = 3, 8, 2, 64
+    lens = [0, 15, 16, 31, 5, 200, 47]
+    whole = plens[0] % 16 == 0
+    b = Batch([3, 2], plens, [n + steps for n in lens], Hq, Hkv, D, fp8=fp8, lead=1, tail=1, seed=9)
+    S = len(lens)
+    rope = pd.Rope(D, base=500000.0, layout="interleaved")
+    groups = [next((g for g in range(2) if b.starts[g] <= s < b.starts[g + 1]), None) for s in range(S)]
+    spans = i32([0 if g is None else plens[g] for g in groups])
+    tables = i32(b.padded([([] if g is None else b.rows[g]) + b.rows[2 + s] for s, g in enumerate(groups)]))
+    own, qkv = i32(lens), torch.empty(S, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device=DEV)
+    ptable, plens, starts, table = i32(b.ptable), i32(b.plens), i32(b.starts), i32(b.table)
+    ws = api.prefix_workspace(S, 2, Hq, Hkv, D, 4, DEV)
+    q, k, v = qkv.split([Hq, Hkv, Hkv], 1)
+
+    def step():
+        own.add_(1)
+        kr = api.rope(rope, k, own + spans - 1)
+        if whole:
+            qr = api.append_kv(rope, q, k, v, b.kc, b.vc, tables, own + spans, k_scale=b.k_scale, v_scale=b.v_scale)
+        else:
+            qr = api.rope(rope, q, own + spans - 1)
+            api.append_kv(None, None, kr, v, b.kc, b.vc, table, own, k_scale=b.k_scale, v_scale=b.v_scale)
+        return qr, kr, api.decode_attn_prefix(qr, b.kc, b.vc, ptable, plens, starts, table, own, b.scale, 4, ws=ws, k_scale=b.k_scale,
+                                              v_scale=b.v_scale)
+
+    kept = b.kc.clone(), b.vc.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    qkv.zero_()
+    with torch.cuda.stream(side):
+        step()  # (everything is loaded before the capture)
+    torch.cuda.synchronize()
+    own.copy_(i32(lens))
+    b.kc.copy_(kept[0])
+    b.vc.copy_(kept[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        qr, kr, out = step()
+    for n in range(1, steps + 1):
+        qkv.copy_(randn(S, Hq + 2 * Hkv, D, seed=20 + n))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert own.tolist() == [m + n for m in lens] and torch.equal(qr, api.rope(rope, q, own + spans - 1))
+        for s in range(S):
+            i = lens[s] + n - 1
+            block, slot = b.rows[2 + s][i // 16], i % 16
+            if fp8:
+                # (the fused append rounds once: off by half a step of E4M3, 2^-4, or of its subnormals, from the rotation,
+                # and that from the rounded one by half a step of BF16)
+                got, want = b.value(b.kc[block, slot], b.k_scale), kr[s].double()
+                assert torch.all((got - want).abs() <= want.abs() * (2.0**-4 * (1 + 2.0**-8) + 2.0**-8) + 0.5 * 2.0**-10)
+                assert torch.equal(b.vc[block, slot], (v[s].float() * 4).to(torch.float8_e4m3fn).view(torch.uint8))
+            else:
+                assert torch.equal(b.kc[block, slot], kr[s]) and torch.equal(b.vc[block, slot], v[s])
+        b.q, b.lens = qr, [m + n for m in lens]
+        ref, bound = b.reference()
+        assert torch.all((out.double() - ref).abs() <= bound)
+
+
+def test_quick_calls_take_what_fits_and_leave_the_rest():
+    """The CPython module answers calls that are as it needs them, with the bits of the other way, and declines others."""
+    quick = pd.quick()
+    b = Batch([2], [40], [3, 17], 8, 2, 64, seed=3)
+    rope = pd.Rope(64)
+    x, pos = randn(2, 8, 64, seed=1), i32([5, 9])
+    far = torch.cuda.current_stream().cuda_stream
+    assert torch.equal(quick.rope(rope.handle, 64, x, pos, None, False), api.rope(rope, x, pos, stream=far))
+    for bad in ((x.float(), pos, None, 0), (x, pos.long(), None, 0), (x, pos[:1], None, 0), (x, pos.cpu(), None, 0), (x[0], pos, None, 0),
+                (x, pos, x[:1], 0), (x, pos, None, 2), (x.cpu(), pos, None, 0), ("x", pos, None, 0), (x, None, None, 0),
+                (x.transpose(1, 2), pos, None, 0)):
+        assert quick.rope(rope.handle, 64, *bad) is NotImplemented
+    assert quick.rope(rope.handle, 128, x, pos, None, 0) is NotImplemented
+    args = [b.q, b.kc, b.vc, i32(b.ptable), i32(b.plens), i32(b.starts), i32(b.table), i32(b.lens), b.scale, 2, None, None, 1.0, 1.0]
+    out = quick.decode_attn_prefix(*args)
+    assert torch.equal(out, b.run(splits=2, stream=far))
+    for i, bad in ((0, b.q.float()), (0, b.q[:1]), (1, b.kc[1:]), (1, b.kc.transpose(0, 1)), (2, b.vc.cpu()), (3, args[3][:, ::2]), (4, args[4].long()),
+                   (5, args[5][:1]), (6, args[6][0]), (7, None), (8, "a"), (9, 0), (9, 5000), (10, out[:1]), (11, out), (12, None)):
+        assert quick.decode_attn_prefix(*args[:i], bad, *args[i + 1:]) is NotImplemented, (i, bad)
+    assert quick.decode_attn_prefix(*args[:-1]) is NotImplemented
+    k, v = randn(2, 2, 64, seed=2), randn(2, 2, 64, seed=4)
+    more = [rope.handle, 64, x, k, v, b.kc, b.vc, i32(b.table), i32(b.lens), None, None, 1.0, 1.0]
+    assert torch.equal(quick.append_kv(*more), api.rope(rope, x, i32([2, 16])))
+    for i, bad in ((1, 128), (2, None), (2, x[:1]), (3, k[:, :1]), (4, v.float()), (5, b.vc[1:]), (7, more[7][:1]), (8, more[8].cpu()), (9, pos), (10, x[:1]),
+                   (11, "a")):
+        assert quick.append_kv(*more[:i], bad, *more[i + 1:]) is NotImplemented, (i, bad)

@@ -158,6 +158,16 @@ def test_rope_handle_refusals():
         pd._check(pd.lib().pd_rope_apply(rope.handle, x.data_ptr() + 2, 128, 64, pos.data_ptr(), x.data_ptr(), 128, 64, 1, 1, 0, None))
     with pytest.raises(pd.PdError):
         pd._check(pd.lib().pd_rope_apply(rope.handle, x.data_ptr(), 128, 64, pos.data_ptr(), x.data_ptr(), 128, 64, 2, 2, 2, None))
+    out = torch.empty(4096, dtype=torch.bfloat16, device=DEV)
+    for T, H, token, head in ((2, 2, 64, 64), (3, 2, 128, 32), (3, 3, 192, 128), (2, 2, 8, 64), (3, 1, 32, 64)):  # overlapping rows
+        with pytest.raises(pd.PdError, match="overlap"):
+            pd._check(pd.lib().pd_rope_apply(rope.handle, out.data_ptr(), 192, 64, i32([0] * T).data_ptr(), out.data_ptr() + 2048,
+                                             token, head, T, H, 0, None))
+    for view in (torch.empty(2, 3, 64, dtype=torch.bfloat16, device=DEV).transpose(0, 1), torch.empty(2, 2, 96, dtype=torch.bfloat16,
+                 device=DEV)[..., :64]):  # and rows that do not
+        x = randn(*view.shape)
+        pos = i32(range(len(x)))
+        assert torch.equal(api.rope(rope, x, pos, out=view), api.rope(rope, x, pos))
     rope.close()
     with pytest.raises(ValueError, match="closed"):
         api.rope(rope, x, pos)

@@ -161,24 +161,26 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[W], floa
         *p = static_cast<uint8_t>(c[0]);
 }
 
-// Cosines and sines of the tokens of a block, times the factor: pair i of the
-// block's token j at j * pitch + i.  A token has units * slots threads and at most
-// 8 pairs a unit (4 where a unit is 8 neighbouring columns), so the block's 256
-// threads touch at most 256 / (units * slots) + 2 tokens and this many pairs.
-// Rows are a multiple of 4 pairs apart, for 16-byte loads.
-constexpr int kTableMax = (256 * 8 + 2 * 16 * 8 + 3 * (256 + 2) + 3) / 4 * 4;
-static_assert(kTableMax % 4 == 0, "the sines begin at a multiple of 16 bytes");
-struct __align__(16) TurnTable {
-    float c[kTableMax], s[kTableMax];
+// Cosines and sines of the tokens of a block, times the factor, in dynamic
+// shared memory: pair i of the block's token j at j * pitch + i, the sines `span`
+// behind the cosines.  Rows are a multiple of 4 pairs, for 16-byte loads.
+struct TurnTable {
+    float *c;
+    int span;
 };
-__device__ __forceinline__ void fill_turn(const RowPlan &p, TurnTable &tab, int at, int pair, int position) {
+extern __shared__ __align__(16) float turn_smem[];
+
+// Tokens that a block's threads touch at most, where a token has `per` threads.
+int block_tokens(int per) { return (kRopeThreads - 2) / per + 2; }
+
+__device__ __forceinline__ void fill_turn(const RowPlan &p, const TurnTable &tab, int at, int pair, int position) {
     const unsigned long long a = static_cast<unsigned long long>(static_cast<long long>(position)) * p.turns[pair];
     // x half-turns: the upper 32 bits, signed, over 2^31
     const float x = static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f;
     float s, c;
     sincospif(x, &s, &c);
     tab.c[at] = c * p.factor;
-    tab.s[at] = s * (p.factor * p.sign);
+    tab.c[tab.span + at] = s * (p.factor * p.sign);
 }
 
 // The pairs of one thread.
@@ -205,7 +207,7 @@ __device__ __forceinline__ Turn<N> turn_of(const RowPlan &p, const TurnTable &ta
     Turn<N> t;
     t.live = p.half - first;
     load_turn<N>(tab.c + token * p.pitch + first, t.c);  // (past `live`: of the row's padding)
-    load_turn<N>(tab.s + token * p.pitch + first, t.s);
+    load_turn<N>(tab.c + tab.span + token * p.pitch + first, t.s);
     return t;
 }
 
@@ -271,9 +273,11 @@ __device__ __forceinline__ void unit_columns(const RowPlan &p, int u, int &ca, i
     }
 }
 
+template <bool HALF>
+constexpr int kBlocks = HALF ? 3 : 5;  // an SM's blocks
+
 template <bool HALF, int W, int ROWS>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ TurnTable tab;
+__global__ void __launch_bounds__(kRopeThreads, kBlocks<HALF>) rope_kernel(const __grid_constant__ RopeParams p) {
     dev::griddep_launch_dependents();
     const int id = blockIdx.x * kRopeThreads + threadIdx.x;
     const int n = fast_div(id, p.plan.units);
@@ -282,6 +286,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int slot = n - tok * static_cast<int>(p.plan.slots.d);
     const int first = fast_div(fast_div(blockIdx.x * kRopeThreads, p.plan.units), p.plan.slots);  // the block's tokens
     const int last = fast_div(fast_div(min(blockIdx.x * kRopeThreads + kRopeThreads, p.threads) - 1, p.plan.units), p.plan.slots);
+    const TurnTable tab = {turn_smem, (last - first + 1) * p.plan.pitch};
     int ca, cb;
     bool pass;
     unit_columns<HALF, W>(p.plan, u, ca, cb, pass);
@@ -339,8 +344,7 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t *starts, int num
 }
 
 template <bool HALF, int W, bool KV8, int ROWS>
-__global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_constant__ AppendParams p) {
-    __shared__ TurnTable tab;
+__global__ void __launch_bounds__(kRopeThreads, kBlocks<HALF>) append_kernel(const __grid_constant__ AppendParams p) {
     __shared__ int place[kRopeThreads + 2][2];  // of the block's tokens: position (-1: left out) and cache cell (-1: no block)
     dev::griddep_launch_dependents();
     const int id = blockIdx.x * kRopeThreads + threadIdx.x;
@@ -352,6 +356,7 @@ __global__ void __launch_bounds__(kRopeThreads) append_kernel(const __grid_const
     const int first = fast_div(fast_div(blockIdx.x * kRopeThreads, p.plan.units), p.plan.slots);  // the block's tokens
     const int count = fast_div(fast_div(min(blockIdx.x * kRopeThreads + kRopeThreads, p.threads) - 1, p.plan.units), p.plan.slots) -
                       first + 1;
+    const TurnTable tab = {turn_smem, count * p.plan.pitch};
     int ca, cb;
     bool pass;
     unit_columns<HALF, W>(p.plan, u, ca, cb, pass);
@@ -500,6 +505,8 @@ cudaError_t launch_rows(Kernel kern, const Params &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((p.threads + kRopeThreads - 1) / kRopeThreads));
     cfg.blockDim = dim3(kRopeThreads);
+    const int per = static_cast<int>(p.plan.units.d * p.plan.slots.d);
+    cfg.dynamicSmemBytes = static_cast<size_t>(block_tokens(per)) * p.plan.pitch * 2 * sizeof(float);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -276,7 +276,7 @@ __device__ __forceinline__ void unit_columns(const RowPlan &p, int u, int &ca, i
 // Blocks an SM has room for.  More hide the wait for the loads and the table: with
 // neighbouring pairs 5 (48 registers) instead of 4 take 8191 tokens of wide heads
 // from 25.1 to 23.4 us.  Pairs halves apart hold twice the columns, and at 4 (64
-// registers) they spill: 120 MB a step goes from 119 to 135 us.
+// registers) they spill: prompts of 805 MB go from 119 to 135 us.
 template <bool HALF>
 constexpr int kBlocks = HALF ? 3 : 5;
 

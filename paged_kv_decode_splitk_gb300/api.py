@@ -96,7 +96,7 @@ def run_paged(inp: PagedInputs, num_splits: int | None = None, gqa_pack: bool | 
 
 # The calls of a decode step launch in a few microseconds, so they first try the
 # library's CPython module, which takes arguments that are just as they should be
-# (pd_binding.c); only what it declines is checked here, one by one, for the message,
+# (pd_binding.cpp); only what it declines is checked here, one by one, for the message,
 # and goes through the ctypes binding.
 _BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
 

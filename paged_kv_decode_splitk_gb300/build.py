@@ -1,5 +1,5 @@
 """Build libpd.so (the C-ABI CUDA library) in-tree with nvcc for sm_103a, and the
-CPython module over it (pd_binding.so) with gcc.
+CPython module between it and torch's tensors (pd_binding.so) with g++.
 
 Each translation unit compiles in its own nvcc process, in parallel; the
 objects and the shared library land in ``paged_kv_decode_splitk_gb300/_build``.
@@ -7,7 +7,9 @@ objects and the shared library land in ``paged_kv_decode_splitk_gb300/_build``.
 
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -60,6 +62,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    # (torch found, not imported: the machine that builds need not load it)
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    src, obj = os.path.join(CSRC, "pd_binding.cpp"), os.path.join(BUILD, "pd_binding.o")
+    if force or _stale(obj, [src, os.path.join(INCLUDE, "pd.h"), os.path.join(torch, "version.py")]):
+        cuda = os.path.dirname(os.path.dirname(shutil.which(nvcc) or nvcc))
+        cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-fvisibility=hidden", f"-I{INCLUDE}", "-isystem", f"{torch}/include",
+               "-isystem", f"{torch}/include/torch/csrc/api/include", "-isystem", f"{cuda}/include",
+               f"-I{sysconfig.get_paths()['include']}", "-c", src, "-o", obj]
+        procs.append(("pd_binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -69,18 +80,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
         msg = "\n".join(f"--- {src}\n{log}" for src, log in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"the compiler failed:\n{msg}")
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fvisibility=hidden"]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
-    src = os.path.join(CSRC, "pd_binding.c")
-    if force or _stale(BINDING, [src, LIB, os.path.join(INCLUDE, "pd.h")]):
+    if force or _stale(BINDING, [obj, LIB]):
         tmp = BINDING + f".tmp{os.getpid()}"
-        cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-Wextra", "-Wno-cast-function-type", "-fPIC", "-fvisibility=hidden", "-shared",
-               f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", src, LIB, "-Wl,-rpath,$ORIGIN", "-o", tmp]
-        subprocess.run(cmd, check=True)
+        libs = [f"-l{name}" for name in ("torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda")]
+        subprocess.run(["g++", "-shared", obj, LIB, f"-L{torch}/lib", *libs, "-Wl,-rpath,$ORIGIN", "-o", tmp], check=True)
         os.replace(tmp, BINDING)
     return LIB
 

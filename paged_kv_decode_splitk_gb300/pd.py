@@ -176,13 +176,13 @@ _quick = None
 
 
 def quick():
-    """The CPython module over the library (csrc/pd_binding.c), built beside it: api.py's first try at a call."""
+    """The CPython module over the library (csrc/pd_binding.cpp), built beside it: api.py's first try at a call."""
     global _quick
     if _quick is None:
         import importlib.machinery
         import importlib.util
 
-        import torch
+        import torch  # noqa: F401  (its libraries, which the module is linked to)
 
         lib()
         path = os.path.join(PKG, "_build", "pd_binding.so")
@@ -191,8 +191,6 @@ def quick():
         loader = importlib.machinery.ExtensionFileLoader("pd_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pd_binding", loader))
         loader.exec_module(module)
-        current_device()
-        module.setup(torch.bfloat16, torch.uint8, torch.int32, torch.empty, _torch_device, _torch_stream)
         _quick = module
     return _quick
 

@@ -267,6 +267,12 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same once for a warp, behind what all its lanes did (32 arrivals at one
+// barrier are served one by one).
+__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane) {
+    __syncwarp();
+    if (lane == 0) arrive(bar);
+}
 
 template <bool KV8>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -379,7 +385,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         // a stage is free once both CTAs of the team have used it: either may be
         // the next to write a half of it
         for (int i = 0; i < NST; ++i) {
-            dev::mbar_init(bar_full + 8 * i, KV8 ? kConverters : 1);
+            dev::mbar_init(bar_full + 8 * i, KV8 ? kConverters / 32 : 1);
             dev::mbar_init(bar_empty + 8 * i, KV8 ? 1 : 2);
         }
         for (int i = 0; i < 3; ++i) {
@@ -388,12 +394,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             dev::mbar_init(bar_s + 8 * i, 1);
-            dev::mbar_init(bar_p + 8 * i, 128);
+            dev::mbar_init(bar_p + 8 * i, 4);
             dev::mbar_init(bar_o + 8 * i, 1);
-            dev::mbar_init(bar_q + 8 * i, 128);
+            dev::mbar_init(bar_q + 8 * i, 4);
         }
         dev::mbar_init(bar_tail, 1);
-        dev::mbar_init(bar_x, 256);
+        dev::mbar_init(bar_x, 8);
         dev::fence_mbar_init();
         *gave_up = 0;
         *own_s = 0;
@@ -743,9 +749,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 }
                 tc::fence_async_shared();
             }
-            arrive(bar_full + 8 * st);
-            __syncwarp();
-            if (lane < 2) dev::mbar_arrive_cluster(dev::map_to_rank(bar_rempty + 8 * rs, lane));  // free for both CTAs
+            arrive_warp(bar_full + 8 * st, lane);
+            // free for both CTAs (the reads have returned their values; an arrival that
+            // also ordered this warp's writes for the peer took half a microsecond)
+            if (lane < 2) dev::mbar_arrive_cluster_relaxed(dev::map_to_rank(bar_rempty + 8 * rs, lane));
             if (++rs == L::kRawStages) {
                 rs = 0;
                 rph ^= 1;
@@ -844,7 +851,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     }
                 }
                 tc::fence_async_shared();
-                arrive(bar_q + 8 * t);
+                arrive_warp(bar_q + 8 * t, lane);
             }
             float m = kNegInf, l = 0.f;
             bool first = true;
@@ -896,7 +903,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (!ok) break;
                 tc::wait_st();
                 tc::fence_before();
-                arrive(bar_p + 8 * buf);
+                arrive_warp(bar_p + 8 * buf, lane);
             }
             if (!ok) break;
             // -- the partial of this row: (m, l) [slot][BR], o [slot][DPAD / 32][BR][32].
@@ -947,7 +954,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 // half of the columns
                 float2 *ml = reinterpret_cast<float2 *>(smem + L::stream_ml);
                 ml[t * kRowTile + r] = make_float2(m, l);
-                arrive(bar_x);
+                arrive_warp(bar_x, lane);
                 if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
                 xph ^= 1;
                 for (int k = 0; k < 2 && ok; ++k) {
@@ -985,7 +992,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     tc::fence_before();
                 }
                 // both streams have read both O before either lets one be overwritten
-                arrive(bar_x);
+                arrive_warp(bar_x, lane);
                 if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
                 xph ^= 1;
             }

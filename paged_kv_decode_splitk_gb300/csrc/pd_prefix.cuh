@@ -146,19 +146,35 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
 
 // How many teams share the prefixes' units.  The own-token pass runs on the SMs
 // the prefix pass leaves, and the step is shortest where both end together: with
-// n SMs, C teams, units of B us in all and U the own pass's time on one SM,
+// n SMs, C teams, units (and the start and end of items) of B us in all and U the
+// own pass's time on one SM,
 //   B / C = U / (n - 2 C).
-// Half of U is taken, since teams too few cost more than teams too many.  Measured
+// Of U's loads half is taken, since teams too few cost more than teams too many,
+// but at least what its units cost when they have next to no tokens: where all SMs
+// went to the prefixes the own pass began 4 us before the end, at theirs.  Measured
 // (us, all 76 teams -> about as many as this gives): 64 sequences behind 8192
 // tokens 47.3 -> 41.2 (24 teams; 16: 52.1), 256 behind 32768 136 -> 124 (60), six
 // groups of wide heads 32.3 -> 30.7 (48), 32 behind 16385 over FP8 51.3 -> 46.9
 // (48).  A team has four units or more beyond the first eight teams: each is a
 // partial more of all its rows to write and fold (256 units without own tokens:
-// 19.7 us on 76 teams, 17.0 on 32).
-__device__ __forceinline__ int share_units(long long units, float units_us, float own_us, int most) {
-    const int c = static_cast<int>(ceilf(__fdividef(2.f * most * units_us, 0.5f * own_us + 2.f * units_us)));
+// 19.7 us on 76 teams, 17.0 on 32).  Where the items have as many units each
+// (`even`) and there are teams enough, a count that gives every item whole teams
+// spares those that would end one item and begin the next (256 units of 8 items
+// over FP8: 21.5 us on 64 teams, 26.7 on 60), if it is near or costs less than that.
+__device__ __forceinline__ int share_units(long long units, int items, bool even, float units_us, float own_us, int most) {
+    constexpr float item_us = 3.f;  // to begin and end an item
+    const float all_us = units_us + item_us * items;
     const long long enough = max((units + 3) / 4, min(units, 8ll));
-    return static_cast<int>(max(1ll, min(enough, static_cast<long long>(min(c, most)))));
+    int c = static_cast<int>(ceilf(__fdividef(2.f * most * all_us, own_us + 2.f * all_us)));
+    c = static_cast<int>(max(1ll, min(enough, static_cast<long long>(min(c, most)))));
+    if (even && c >= items) {
+        const int down = c - static_cast<int>(static_cast<unsigned>(c) % static_cast<unsigned>(items)), up = down + items;
+        if (down != c && up <= most && 16 * up <= 17 * c)
+            c = up;
+        else if (units_us * (c - down) <= item_us * static_cast<float>(c) * down)
+            c = down;
+    }
+    return c;
 }
 
 // The time of a unit on a team, measured (us): the conversion bounds an FP8 tile;
@@ -166,18 +182,20 @@ __device__ __forceinline__ int share_units(long long units, float units_us, floa
 template <int DPAD, bool KV8>
 __device__ __forceinline__ float unit_time(int rows) {
     const bool pair = is_pair(rows, KV8, item_rows(DPAD));
-    const float us = KV8 ? 2.1f : pair ? (rows > 2 * kRowTile ? 1.4f : 0.9f) : DPAD == 256 ? 1.f : 1.3f;
-    return DPAD == 64 ? 0.6f * us : us;
+    const float us = KV8 ? 1.6f : pair ? (rows > 2 * kRowTile ? 1.4f : 0.9f) : DPAD == 256 ? 1.f : 1.3f;
+    return DPAD == 64 ? (KV8 ? 0.8f : 0.6f) * us : us;
 }
 
 // The groups' units and items, by one warp: running sums over chunks of 32
 // groups.  Returns false (on every lane) where group_starts is not
 // non-decreasing within the batch or asks for more items than the workspace holds.
 template <int DPAD, bool KV8>
-__device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *grp, long long *units_all, float *time_us, int lane, bool flag) {
+__device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *grp, long long *units_all, float *time_us, int *items_all,
+                                            int lane, bool flag) {
     long long units = 0;
     float time = 0.f;  // of the units, this lane's share
     int items = 0;
+    unsigned few = 0xffffffffu, many = 0;  // units of an item, at least and at most
     bool bad = false;
     for (int base = 0; base < p.num_groups; base += 32) {
         const int g = base + lane;
@@ -202,6 +220,8 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
             if (r.tiles > 0 && r.items > 0) {
                 it = r.items * p.num_kv_heads;
                 mine = r.head_units(item_rows(DPAD), KV8) * p.num_kv_heads;
+                few = min(few, static_cast<unsigned>(r.last_units(item_rows(DPAD), KV8)));
+                many = max(many, static_cast<unsigned>(r.items > 1 ? r.tiles : r.last_units(item_rows(DPAD), KV8)));
                 time += mine * unit_time<DPAD, KV8>(min(r.rows, item_rows(DPAD)));
             }
         }
@@ -229,6 +249,8 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
     for (int off = 16; off > 0; off >>= 1) time += __shfl_xor_sync(0xffffffffu, time, off);
     *units_all = bad ? 0 : units;
     *time_us = time;
+    const bool even = __reduce_min_sync(0xffffffffu, few) == __reduce_max_sync(0xffffffffu, many);
+    *items_all = even ? items : -items;
     return !bad;
 }
 
@@ -371,6 +393,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     static_assert(2 * NST + 16 <= kRegionBars, "barrier region");
     long long *units_s = reinterpret_cast<long long *>(smem + L::misc);
     unsigned *own_s = reinterpret_cast<unsigned *>(smem + L::misc + 8);  // sixteens of the sequences' own tokens
+    int *items_s = reinterpret_cast<int *>(smem + L::misc + 12);  // below 0: of unequal units
     float *time_s = reinterpret_cast<float *>(smem + L::misc + 16);
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc + 20);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 24);
@@ -413,10 +436,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     if (warp == 0) {
         long long units;
         float time;
-        const bool good = plan_groups<DPAD, KV8>(p, grp, &units, &time, lane, blockIdx.x == 0);
+        int items;
+        const bool good = plan_groups<DPAD, KV8>(p, grp, &units, &time, &items, lane, blockIdx.x == 0);
         if (lane == 0) {
             *units_s = units;
             *time_s = time;
+            *items_s = items;
         }
         __syncwarp();
         if (blockIdx.x == 0) {  // the merge finds each row's partials from this
@@ -444,8 +469,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
     const long long W = *units_s;
     // (the own pass draws 5.4 MB of a BF16 cache a us from all SMs, 2.8 of FP8 codes)
-    const float own_us = static_cast<float>(*own_s) * (p.num_kv_heads * p.head_dim * (KV8 ? 32.f / 2.8e6f : 64.f / 5.4e6f)) * gridDim.x;
-    const int C = W > 0 ? share_units(W, *time_s, own_us, gridDim.x / 2) : 0;
+    const float own_us = fmaxf(0.5f * static_cast<float>(*own_s) * (p.num_kv_heads * p.head_dim * (KV8 ? 32.f / 2.8e6f : 64.f / 5.4e6f)) * gridDim.x,
+                               0.35f * static_cast<float>(p.num_seqs) * p.num_kv_heads);
+    const int C = W > 0 ? share_units(W, abs(*items_s), *items_s > 0, *time_s, own_us, gridDim.x / 2) : 0;
     if (blockIdx.x == 0 && tid == 0) *p.plan_total = {W, C, 0};
     long long u = 0, u1 = 0;
     if (team < C) {

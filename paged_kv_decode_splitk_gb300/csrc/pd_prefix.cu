@@ -397,7 +397,8 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     m.group = group;
     m.head_dim = head_dim;
     m.dpad = dpad;
-    // as many lines a row as one wave has room for, 8 at most
+    // as many lines a row as one wave has room for, 8 at most (a third more, into a
+    // second wave: 64 sequences behind 8192 tokens 41.2 -> 44.6 us)
     const long long lanes = static_cast<long long>(num_seqs) * num_q_heads * (dpad / 8);
     m.ways = 1;
     while (m.ways < 8 && 2 * m.ways * lanes <= 152 * 3 * kMergeWarps * 32) m.ways *= 2;

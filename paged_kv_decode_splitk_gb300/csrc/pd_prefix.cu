@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) prefix_merge_kernel(const
         constexpr int IR = item_rows(DPAD);
         const int item = has ? x / IR : 0, r = x - item * IR;
         const int of_item = min(IR, g.rows - item * IR), half = (of_item + 1) >> 1;
-        const bool pair = is_pair(of_item, p.kv8 != 0, IR);
+        const bool pair = is_pair(of_item, IR);
         const int places = pair ? g.tiles : (g.tiles + 1) >> 1;
-        const long long u = g.first_unit + kvh * g.head_units(IR, p.kv8 != 0) + static_cast<long long>(item) * g.tiles;
+        const long long u = g.first_unit + kvh * g.head_units(IR) + static_cast<long long>(item) * g.tiles;
         const int C = plan.teams;
         const int c = has ? team_of_unit(sub == 0 ? u : u + places - 1, C, W) : 0;
         const int c0 = __shfl_sync(0xffffffffu, c, head_lane), c1 = __shfl_sync(0xffffffffu, c, head_lane + 1);
@@ -402,7 +402,6 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     const long long lanes = static_cast<long long>(num_seqs) * num_q_heads * (dpad / 8);
     m.ways = 1;
     while (m.ways < 8 && 2 * m.ways * lanes <= 152 * 3 * kMergeWarps * 32) m.ways *= 2;
-    m.kv8 = kv8;
     m.num_splits = num_splits;
     m.min_kv_per_split = PD_MIN_KV_PER_SPLIT;
     m.max_tokens = max_blocks * block_size;

@@ -16,16 +16,17 @@
 //   * CTAs work in teams of two, a cluster.  A team's item is up to 512 rows of a
 //     KV head (256 at head dims above 128): each CTA has half of them, both need
 //     the same K and V tiles, and each loads half of every tile and multicasts it
-//     to both, which halves what the SMs draw from L2.  With few rows both have all
-//     of them and take the tiles in turn.
+//     to both, which halves what the SMs draw from L2.  Rows that one CTA can take
+//     both have, and they take the tiles in turn.
 //   * Work is counted in units (item, a tile for both CTAs) in one line over all
 //     groups; team c of C takes units [W c / C, W (c + 1) / C): every SM gets the
 //     same number of tiles whatever the shapes, and a team's partials of item i go
 //     to slots 2 (i + c) and 2 (i + c) + 1 (item and team both only grow along the
 //     line, so slots are distinct, and there are at most items + C of them).
-//   * One warp loads: K and V tiles by TMA boxes of 64 columns x as many
-//     tokens as lie together in a cache block (16 to a whole tile), gathered through the group's block table into a ring of tiles (128-byte
-//     swizzle).  One warp issues tcgen05.mma: S (128 rows x kTile tokens) from
+//   * One warp (two where none has to convert) loads: K and V tiles by TMA boxes of
+//     64 columns x as many tokens as lie together in a cache block (16 to a whole
+//     tile), gathered through the group's block table into a ring of tiles
+//     (128-byte swizzle).  One warp issues tcgen05.mma: S (128 rows x kTile tokens) from
 //     shared memory into TMEM, O += P V with P read from TMEM.  Two groups of
 //     four warps do the softmax, a thread per row, S read from and P (BF16)
 //     written back to TMEM over it.  The reference need not be the maximum, so
@@ -33,12 +34,18 @@
 //     half an add and half a conversion per score is all there is.
 //   * Two streams keep the tensor core and the softmax both busy: with more than
 //     128 rows each stream has 128 of them and both use every tile; with fewer,
-//     the streams take the tiles in turn (each its own O), folded in the end.  At head dims above 128 one O fills TMEM: one stream, its
-//     S double-buffered.
+//     the streams take the tiles in turn (each its own O), folded in the end.  At
+//     head dims above 128 one O fills TMEM: one stream, its S double-buffered.
 //   * P is rounded to BF16 (half a step: 2^-9 to 2^-8 of each weight), the form
 //     the tensor core multiplies with a BF16 V; l sums the unrounded weights in
 //     FP32, S, O, m and l are FP32.  An FP8 cache is converted to f16 tiles
 //     (exactly), and P is f16 there (2^-12 to 2^-11).
+//
+// What bounds it, measured (8 KV heads, head dim 128, us per 1024 more prefix
+// tokens): 1024 rows 2.33, the tensor core (2.24 at the library product's rate); 128
+// rows 0.62 and 256 rows 0.67, HBM (0.62); FP8 0.66 at 128 and 256 rows, the two
+// warps that convert (HBM: 0.31).  The rest is the chain of three launches, 10 us of
+// the smallest step's 12.
 #pragma once
 
 #include <cuda.h>
@@ -102,7 +109,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return a / b;
 }
 
-template <int BR, bool KV8>
+template <int BR>
 __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_groups, long long &u, long long u1,
                                              int team, int rank, Segment &s) {
     if (u >= u1) return false;
@@ -117,14 +124,14 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
         }
     }
     const GroupPlan g = grp[lo];
-    const long long per_head = g.head_units(2 * BR, KV8);
+    const long long per_head = g.head_units(2 * BR);
     const long long local = u - g.first_unit;
     s.kvh = static_cast<int>(quotient(local, per_head));
     const long long rem = local - s.kvh * per_head;
     const int item = static_cast<int>(quotient(rem, g.tiles));  // (the last item may have fewer units, never more)
     const int at = static_cast<int>(rem - static_cast<long long>(item) * g.tiles);  // place within the item
     const int rows = min(2 * BR, g.rows - item * 2 * BR);
-    s.pair = is_pair(rows, KV8, 2 * BR);
+    s.pair = is_pair(rows, 2 * BR);
     const int places = s.pair ? g.tiles : (g.tiles + 1) >> 1;
     const long long left = u1 - u;
     s.n = left < places - at ? static_cast<int>(left) : places - at;
@@ -181,8 +188,8 @@ __device__ __forceinline__ int share_units(long long units, int items, bool even
 // two full row tiles of products a pair's; one, and memory, the others'.
 template <int DPAD, bool KV8>
 __device__ __forceinline__ float unit_time(int rows) {
-    const bool pair = is_pair(rows, KV8, item_rows(DPAD));
-    const float us = KV8 ? 1.6f : pair ? (rows > 2 * kRowTile ? 1.4f : 0.9f) : DPAD == 256 ? 1.f : 1.3f;
+    const bool pair = is_pair(rows, item_rows(DPAD));
+    const float us = KV8 || (!pair && rows > kRowTile) ? 1.6f : pair ? (DPAD == 256 ? 0.9f : 1.4f) : DPAD == 256 ? 1.f : 1.3f;
     return DPAD == 64 ? (KV8 ? 0.8f : 0.6f) * us : us;
 }
 
@@ -219,9 +226,9 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
             r.tiles = (len + tile_tokens(DPAD) - 1) / tile_tokens(DPAD);
             if (r.tiles > 0 && r.items > 0) {
                 it = r.items * p.num_kv_heads;
-                mine = r.head_units(item_rows(DPAD), KV8) * p.num_kv_heads;
-                few = min(few, static_cast<unsigned>(r.last_units(item_rows(DPAD), KV8)));
-                many = max(many, static_cast<unsigned>(r.items > 1 ? r.tiles : r.last_units(item_rows(DPAD), KV8)));
+                mine = r.head_units(item_rows(DPAD)) * p.num_kv_heads;
+                few = min(few, static_cast<unsigned>(r.last_units(item_rows(DPAD))));
+                many = max(many, static_cast<unsigned>(r.items > 1 ? r.tiles : r.last_units(item_rows(DPAD))));
                 time += mine * unit_time<DPAD, KV8>(min(r.rows, item_rows(DPAD)));
             }
         }
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         uint32_t tail_ph = 0;
         bool ok = true;
         long long issued = 0;
-        while (ok && next_segment<BR, KV8>(grp, p.num_groups, u, u1, team, rank, sg)) {
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const int32_t *ids = p.prefix_table + static_cast<long long>(sg.group) * p.max_prefix_blocks;
             const int ahead = ONE || !sg.two ? 2 : 1;
             // of a shared tile each CTA loads every other box, for both
@@ -655,7 +662,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 qph ^= 1u << t;
                 return got;
             };
-            while (ok && next_segment<BR, KV8>(grp, p.num_groups, u, u1, team, rank, sg)) {
+            while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
                 const int n = sg.n, live = sg.live;
                 int ks = 0, vs = 0;
                 if (live > 0 && !(ok = queries(0))) break;
@@ -789,7 +796,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             }
             return true;
         };
-        while (ok && next_segment<BR, KV8>(grp, p.num_groups, u, u1, team, rank, sg)) {
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const int ahead = ONE || !sg.two ? 2 : 1;
             for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
                 if (i < sg.n) ok = convert(i < sg.live, false, BN);
@@ -813,7 +820,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         // the time a third segment begins: its weights of the first went before)
         float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
         int turn = 0;
-        while (ok && next_segment<BR, KV8>(grp, p.num_groups, u, u1, team, rank, sg)) {
+        while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const bool two = sg.two;
             float scale = p.scale_log2;
             if constexpr (KV8) {

@@ -17,20 +17,13 @@ __host__ __device__ constexpr int block_rows(int dpad) { return dpad > 128 ? 128
 // Query rows of an item at most: a block for each CTA of a team.
 __host__ __device__ constexpr int item_rows(int dpad) { return 2 * block_rows(dpad); }
 
-// How an item's rows go to the two CTAs of a team: half of them each, with every
-// tile for both; or, where they are few, all to both, which take the tiles in
-// turn.  Up to 128 rows a half would be a 128-row product half empty (32
-// sequences of 4 heads, 32768 tokens: 41 us in turn, 45 us by halves; 64: by
-// halves, which makes half as many partials, 50 us, in turn 54).  Over an FP8
-// cache every tile a CTA uses it also has to convert, so up to 256 rows go to
-// both (the same 32 sequences: 67 us in turn, 89 us by halves).  Rows in turn are
-// never more than one CTA takes, so a full item is always by halves.
-__host__ __device__ constexpr bool is_pair(int rows, bool kv8, int of_item) {
-    return rows > (kv8 && of_item > 256 ? 256 : 128);
-}
-static_assert(is_pair(item_rows(64), true, item_rows(64)) && is_pair(item_rows(256), true, item_rows(256)) &&
-                  is_pair(block_rows(256) + 1, true, item_rows(256)) && is_pair(block_rows(64) + 1, true, item_rows(64)),
-              "full items are by halves, and so is what one CTA cannot take");
+// How an item's rows go to the two CTAs of a team: as many as one CTA can take go
+// to both, which take the tiles in turn; more, half to each, with every tile for
+// both.  In turn the CTAs need not keep step (8 KV heads, 32768 tokens: 128 rows
+// 41 us in turn, 45 by halves; 256 rows 40.4 and 43.9), but make twice as many
+// partials (8192 tokens: 24.2 and 23.5); over an FP8 cache each converts half of
+// the tiles (128 rows: 67 us in turn, 89 by halves when a tile took it longer).
+__host__ __device__ constexpr bool is_pair(int rows, int of_item) { return rows > of_item / 2; }
 
 // What the prefix pass found the work to be: units in all, and the teams that
 // share them.
@@ -53,11 +46,11 @@ struct GroupPlan {
     int tokens;     // of the prefix
 
     // units of a KV head, and of its last item, which alone may have few rows
-    __host__ __device__ int last_units(int of_item, bool kv8) const {
-        return is_pair(rows - (items - 1) * of_item, kv8, of_item) ? tiles : (tiles + 1) >> 1;
+    __host__ __device__ int last_units(int of_item) const {
+        return is_pair(rows - (items - 1) * of_item, of_item) ? tiles : (tiles + 1) >> 1;
     }
-    __host__ __device__ long long head_units(int of_item, bool kv8) const {
-        return static_cast<long long>(items - 1) * tiles + last_units(of_item, kv8);
+    __host__ __device__ long long head_units(int of_item) const {
+        return static_cast<long long>(items - 1) * tiles + last_units(of_item);
     }
 };
 
@@ -90,7 +83,7 @@ struct MergeParams {
     __nv_bfloat16 *out;
     int num_groups, num_seqs, num_q_heads, num_kv_heads, group, head_dim, dpad;
     int num_splits, min_kv_per_split, max_tokens;
-    int kv8, ways;
+    int ways;           // lines of lanes a row has
     float v_scale;      // of the prefix partials (an FP8 cache; the own-token pass applies its own)
     FastDiv fd_hq, fd_group, fd_split, fd_bs;
 };

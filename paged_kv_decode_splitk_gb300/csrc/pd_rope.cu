@@ -14,7 +14,11 @@
 // All its loads are in flight while the block works out the sines and cosines of
 // its few tokens, one or two a thread, into shared memory; a thread working out
 // its own, four to eight, was bound by their instructions where only a part of
-// the head turns (64 single tokens of 40 heads: 2.25 -> 1.72 us).
+// the head turns (64 single tokens of 40 heads: 2.25 -> 1.72 us).  Measured against a
+// plain copy's rate: 671 MB rotated in 96 us (103%), 151 MB of rows turned in part
+// in 23.4 (95%), 805 MB of new tokens in 119 (99%), 154 MB into an FP8 cache in 31.4
+// (72%; four times as many tokens 87%: what is left is the start, the lookups and
+// the last wave).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

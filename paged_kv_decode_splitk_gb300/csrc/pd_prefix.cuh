@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     const uint32_t bar_full = bars, bar_empty = bar_full + 8 * NST, bar_rfull = bar_empty + 8 * NST,
                    bar_rempty = bar_rfull + 24, bar_s = bar_rempty + 24, bar_p = bar_s + 16, bar_o = bar_p + 16,
                    bar_q = bar_o + 16, bar_tail = bar_q + 16, bar_x = bar_tail + 8;
-    static_assert(2 * NST + 16 <= kRegionBars, "barrier region");
+    const uint32_t bar_land = bar_rfull;  // (no raw stages: a last tile's landing, a barrier a stage)
+    static_assert(2 * NST + 16 <= kRegionBars && (KV8 || NST <= 6), "barrier region");
     long long *units_s = reinterpret_cast<long long *>(smem + L::misc);
     unsigned *own_s = reinterpret_cast<unsigned *>(smem + L::misc + 8);  // sixteens of the sequences' own tokens
     int *items_s = reinterpret_cast<int *>(smem + L::misc + 12);  // below 0: of unequal units
@@ -418,10 +419,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             dev::mbar_init(bar_full + 8 * i, KV8 ? kConverters / 32 : 1);
             dev::mbar_init(bar_empty + 8 * i, KV8 ? 1 : 2);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; KV8 && i < 3; ++i) {
             dev::mbar_init(bar_rfull + 8 * i, 1);
             dev::mbar_init(bar_rempty + 8 * i, 2 * kConverters / 32);
         }
+        for (int i = 0; !KV8 && i < NST; ++i) dev::mbar_init(bar_land + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
             dev::mbar_init(bar_s + 8 * i, 1);
             dev::mbar_init(bar_p + 8 * i, 4);
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         const int chunk = lane % NCH, col = lane / NCH;
         int st = 0;
         uint32_t ph = 0;  // phase of the stage about to be filled
-        uint32_t tail_ph = 0;
+        uint32_t land_ph = 0;  // of the landing barriers, a bit each
         bool ok = true;
         long long issued = 0;
         while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
@@ -558,9 +560,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 const int nv = sg.plen - first;  // live tokens of the tile
                 // A tile's box of live and dead tokens holds whatever the cache's
                 // slots past the prefix hold; a dead V row must not reach the
-                // product (0 x NaN), so those rows are zeroed before it is handed on.
+                // product (0 x NaN), so those rows are zeroed before it is handed on.  It
+                // lands at a barrier of its stage: the peer sends its boxes as soon as the
+                // stage is free, which may be before this CTA has seen its last tail land.
                 const bool tail = !KV8 && is_v && j < sg.live && nv < BN && (nv & (CT - 1));
-                const uint32_t bar = tail ? bar_tail : full + 8 * st;
+                const uint32_t bar = (tail ? bar_land : full) + 8 * st;
                 if (j >= sg.live) {  // a place without a tile: nothing lands
                     if (lane == 0) arrive(bar);
                 } else {
@@ -578,8 +582,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     }
                 }
                 if (tail) {
-                    if (!wait_bar(bar_tail, tail_ph, gave_up)) return false;
-                    tail_ph ^= 1;
+                    const uint32_t lph = (land_ph >> st) & 1;
+                    land_ph ^= 1u << st;
+                    if (!wait_bar(bar, lph, gave_up)) {
+                        if (lane == 0) dev::mbar_wait_bounded(bar, lph, 100000000ull);  // (its copies land before the CTA ends)
+                        return false;
+                    }
                     uint8_t *tile = smem + L::ring + st * BYTES;
                     const int end = (nv + CT - 1) & ~(CT - 1);
                     for (int b = 0; b < DPAD / 64; ++b)

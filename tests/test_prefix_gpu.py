@@ -157,6 +157,10 @@ SHAPES = {  # sizes, prefix lengths, own lengths, Hq, Hkv, D, block size, sequen
     "group of 16": ([20], [400], [30] * 20, 32, 2, 64, 16, 0, 0),
     "many groups": ([2] * 70, [(37 * i) % 300 for i in range(70)], [3] * 140, 4, 2, 64, 16, 0, 0),
     "heads": ([9], [600], [20] * 9, 32, 32, 128, 16, 0, 0),
+    # items of one or two tiles that end inside a cache block, one after another, their rows in halves
+    "short halves": ([33] * 8, [1, 127, 90, 17, 130, 3, 65, 255], [1] * 264, 64, 8, 80, 80, 0, 0),
+    "short halves, narrow": ([33] * 8, [1, 127, 90, 17, 130, 3, 65, 255], [1] * 264, 64, 8, 64, 16, 0, 0),
+    "short halves, wide": ([17] * 8, [1, 63, 45, 17, 66, 3, 65, 127], [1] * 136, 64, 8, 256, 32, 0, 0),
 }
 
 

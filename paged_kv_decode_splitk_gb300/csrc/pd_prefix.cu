@@ -84,6 +84,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) prefix_merge_kernel(const
         f.first_seq = __shfl_sync(0xffffffffu, one.first_seq, src);
         f.rows = __shfl_sync(0xffffffffu, one.rows, src);
         f.items = __shfl_sync(0xffffffffu, one.items, src);
+        f.first_team = __shfl_sync(0xffffffffu, one.first_team, src);
+        f.teams = __shfl_sync(0xffffffffu, one.teams, src);
+        f.last_teams = __shfl_sync(0xffffffffu, one.last_teams, src);
         if (below > 0) g = f;
     }
     int nparts = 0, step = 2;      // prefix slots of the row, 2 apart, or (both CTAs') 1
@@ -98,8 +101,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) prefix_merge_kernel(const
         const int places = pair ? g.tiles : (g.tiles + 1) >> 1;
         const long long u = g.first_unit + kvh * g.head_units(IR) + static_cast<long long>(item) * g.tiles;
         const int C = plan.teams;
-        const int c = has ? team_of_unit(sub == 0 ? u : u + places - 1, C, W) : 0;
-        const int c0 = __shfl_sync(0xffffffffu, c, head_lane), c1 = __shfl_sync(0xffffffffu, c, head_lane + 1);
+        int c0, c1;
+        if (plan.whole) {
+            c0 = g.first_team + kvh * ((g.items - 1) * g.teams + g.last_teams) + item * g.teams;
+            c1 = c0 + (item == g.items - 1 ? g.last_teams : g.teams) - 1;
+        } else {
+            const int c = has ? team_of_unit(sub == 0 ? u : u + places - 1, C, W) : 0;
+            c0 = __shfl_sync(0xffffffffu, c, head_lane), c1 = __shfl_sync(0xffffffffu, c, head_lane + 1);
+        }
         if (has) {
             const int second = pair && r >= half;
             step = pair ? 2 : 1;

@@ -22,7 +22,8 @@
 //     groups; team c of C takes units [W c / C, W (c + 1) / C): every SM gets the
 //     same number of tiles whatever the shapes, and a team's partials of item i go
 //     to slots 2 (i + c) and 2 (i + c) + 1 (item and team both only grow along the
-//     line, so slots are distinct, and there are at most items + C of them).
+//     line, so slots are distinct, and there are at most items + C of them).  Where
+//     teams are enough, every item has whole teams instead, its units shared evenly.
 //   * One warp (two where none has to convert) loads: K and V tiles by TMA boxes of
 //     64 columns x as many tokens as lie together in a cache block (16 to a whole
 //     tile), gathered through the group's block table into a ring of tiles
@@ -162,7 +163,7 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
 // (us, all 76 teams -> about as many as this gives): 64 sequences behind 8192
 // tokens 47.3 -> 41.2 (24 teams; 16: 52.1), 256 behind 32768 136 -> 124 (60), six
 // groups of wide heads 32.3 -> 30.7 (48), 32 behind 16385 over FP8 51.3 -> 46.9
-// (48).  A team has four units or more beyond the first eight teams: each is a
+// (48).  A team has four units or more beyond the first eight teams, or an item: each is a
 // partial more of all its rows to write and fold (256 units without own tokens:
 // 19.7 us on 76 teams, 17.0 on 32).  Where the items have as many units each
 // (`even`) and there are teams enough, a count that gives every item whole teams
@@ -171,7 +172,7 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
 __device__ __forceinline__ int share_units(long long units, int items, bool even, float units_us, float own_us, int most) {
     constexpr float item_us = 3.f;  // to begin and end an item
     const float all_us = units_us + item_us * items;
-    const long long enough = max((units + 3) / 4, min(units, 8ll));
+    const long long enough = max((units + 3) / 4, min(units, max(8ll, static_cast<long long>(items))));
     int c = static_cast<int>(ceilf(__fdividef(2.f * most * all_us, own_us + 2.f * all_us)));
     c = static_cast<int>(max(1ll, min(enough, static_cast<long long>(min(c, most)))));
     if (even && c >= items) {
@@ -184,6 +185,64 @@ __device__ __forceinline__ int share_units(long long units, int items, bool even
     return c;
 }
 
+// Teams of an item with at most about `run` units each (no more than it has units).
+__device__ __forceinline__ int teams_of(int units, int run) {
+    return max(1, static_cast<int>(ceilf(__fmaf_rn(static_cast<float>(units), __fdividef(1.f, static_cast<float>(run)), -1e-3f))));
+}
+__device__ __forceinline__ int head_teams(const GroupPlan &g, int of_item, int run) {
+    return g.tiles && g.items ? (g.items - 1) * teams_of(g.tiles, run) + teams_of(g.last_units(of_item), run) : 0;
+}
+// a / b of whole numbers from 0 and 1 to 255
+__device__ __forceinline__ int small_quotient(int a, int b) {
+    return static_cast<int>((static_cast<float>(a) + 0.5f) * __fdividef(1.f, static_cast<float>(b)));
+}
+
+// Whole teams for every item, where there are teams enough: a team that ends one
+// item and begins the next spends 3 us on that (6 over FP8, where the ring of
+// converted tiles fills anew), often more than its share of units is worth (three
+// groups of wide FP8 heads 30.3 us on 52 teams in one line, 22 on 44 or 56 that
+// happen to end with the items; 256 units of 8 items 18.3 on 48 teams, 23 on 44).
+// The warp's lanes try the most units of a team, from the line's share on; the
+// least with no more than about c teams is taken if it costs no more than that.
+// Returns it (0: one line) and the teams.  Where teams have a unit each, the line
+// has whole teams already.
+__device__ __forceinline__ int whole_teams(const GroupPlan *grp, int num_groups, int kv_heads, int of_item, long long units, int &c,
+                                           int most, int items, float unit_us, float item_us, int lane) {
+    const int limit = min(most, c + c / 16);
+    if (units <= c || items > limit || num_groups > 32) return 0;
+    const float even = __fdividef(static_cast<float>(units), static_cast<float>(c));
+    const int share = static_cast<int>(ceilf(even)), run = share + lane * ((share + 15) / 16);
+    int teams = 0;
+    for (int g = 0; g < num_groups; ++g) teams += kv_heads * head_teams(grp[g], of_item, run);
+    const unsigned fits = __ballot_sync(0xffffffffu, teams <= limit);
+    if (!fits) return 0;
+    const int best = __ffs(fits) - 1, least = __shfl_sync(0xffffffffu, run, best), n = __shfl_sync(0xffffffffu, teams, best);
+    if ((static_cast<float>(least) - even) * unit_us > item_us) return 0;
+    c = n;
+    return least;
+}
+
+// The units of a team where items have whole teams.
+__device__ __forceinline__ void whole_range(const GroupPlan *grp, int kv_heads, int of_item, int run, int team, long long &u,
+                                            long long &u1) {
+    int g = 0, n;
+    while (team >= (n = kv_heads * head_teams(grp[g], of_item, run))) {
+        team -= n;
+        ++g;
+    }
+    const GroupPlan r = grp[g];
+    const int last = r.last_units(of_item), of_last = teams_of(last, run);
+    const int of_one = r.items > 1 ? teams_of(r.tiles, run) : of_last, head = (r.items - 1) * of_one + of_last;
+    const int kvh = small_quotient(team, head), at = team - kvh * head;
+    const int item = min(small_quotient(at, of_one), r.items - 1);
+    const bool ends = item == r.items - 1;
+    // even shares, the first ones a unit longer
+    const int part = at - item * of_one, places = ends ? last : r.tiles, teams = ends ? of_last : of_one;
+    const int least = places / teams, longer = places - least * teams;
+    u = r.first_unit + kvh * r.head_units(of_item) + static_cast<long long>(item) * r.tiles + least * part + min(part, longer);
+    u1 = u + least + (part < longer);
+}
+
 // The time of a unit on a team, measured (us): the conversion bounds an FP8 tile;
 // two full row tiles of products a pair's; one, and memory, the others'.
 template <int DPAD, bool KV8>
@@ -194,15 +253,14 @@ __device__ __forceinline__ float unit_time(int rows) {
 }
 
 // The groups' units and items, by one warp: running sums over chunks of 32
-// groups.  Returns false (on every lane) where group_starts is not
-// non-decreasing within the batch or asks for more items than the workspace holds.
+// groups.  No units where group_starts is not non-decreasing within the batch or
+// asks for more items than the workspace holds.
 template <int DPAD, bool KV8>
-__device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *grp, long long *units_all, float *time_us, int *items_all,
-                                            int lane, bool flag) {
+__device__ __forceinline__ void plan_groups(const PrefixParams &p, GroupPlan *grp, long long *units_all, float *time_us, int *items_all, int lane,
+                                            bool flag) {
     long long units = 0;
     float time = 0.f;  // of the units, this lane's share
     int items = 0;
-    unsigned few = 0xffffffffu, many = 0;  // units of an item, at least and at most
     bool bad = false;
     for (int base = 0; base < p.num_groups; base += 32) {
         const int g = base + lane;
@@ -227,8 +285,6 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
             if (r.tiles > 0 && r.items > 0) {
                 it = r.items * p.num_kv_heads;
                 mine = r.head_units(item_rows(DPAD)) * p.num_kv_heads;
-                few = min(few, static_cast<unsigned>(r.last_units(item_rows(DPAD))));
-                many = max(many, static_cast<unsigned>(r.items > 1 ? r.tiles : r.last_units(item_rows(DPAD))));
                 time += mine * unit_time<DPAD, KV8>(min(r.rows, item_rows(DPAD)));
             }
         }
@@ -256,9 +312,7 @@ __device__ __forceinline__ bool plan_groups(const PrefixParams &p, GroupPlan *gr
     for (int off = 16; off > 0; off >>= 1) time += __shfl_xor_sync(0xffffffffu, time, off);
     *units_all = bad ? 0 : units;
     *time_us = time;
-    const bool even = __reduce_min_sync(0xffffffffu, few) == __reduce_max_sync(0xffffffffu, many);
-    *items_all = even ? items : -items;
-    return !bad;
+    *items_all = items;
 }
 
 // Bounded wait of a whole warp, which also ends when another warp of the CTA
@@ -373,7 +427,9 @@ __device__ __forceinline__ void raise_reference(uint32_t to, float top, bool ove
     }
 }
 
-template <int DPAD, bool KV8>
+// MULTI: more than one group.  (The rule that gives every item whole teams lies in
+// the way of a call with one group, which has no use for it: 0.4 us of 15.)
+template <int DPAD, bool KV8, bool MULTI>
 __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     prefix_kernel(const __grid_constant__ KvMaps<1> maps, const __grid_constant__ PrefixParams p) {
     using L = Plan<DPAD, KV8>;
@@ -401,10 +457,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     static_assert(2 * NST + 16 <= kRegionBars && (KV8 || NST <= 6), "barrier region");
     long long *units_s = reinterpret_cast<long long *>(smem + L::misc);
     unsigned *own_s = reinterpret_cast<unsigned *>(smem + L::misc + 8);  // sixteens of the sequences' own tokens
-    int *items_s = reinterpret_cast<int *>(smem + L::misc + 12);  // below 0: of unequal units
+    int *items_s = reinterpret_cast<int *>(smem + L::misc + 12);
     float *time_s = reinterpret_cast<float *>(smem + L::misc + 16);
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc + 20);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 24);
+    long long *range_s = reinterpret_cast<long long *>(smem + L::misc + 32);
+    int *share_s = reinterpret_cast<int *>(smem + L::misc + 48);  // teams, and the most units of one
 
     // (the warp's number from one lane, so that the compiler knows it to be the
     // same on all: the product warp's operands then live in uniform registers)
@@ -446,19 +504,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         long long units;
         float time;
         int items;
-        const bool good = plan_groups<DPAD, KV8>(p, grp, &units, &time, &items, lane, blockIdx.x == 0);
+        plan_groups<DPAD, KV8>(p, grp, &units, &time, &items, lane, blockIdx.x == 0);
         if (lane == 0) {
             *units_s = units;
             *time_s = time;
             *items_s = items;
-        }
-        __syncwarp();
-        if (blockIdx.x == 0) {  // the merge finds each row's partials from this
-            for (int g = lane; g < p.num_groups; g += 32) {
-                GroupPlan r = grp[g];
-                if (!good) r.tiles = 0;
-                p.plan_groups[g] = r;
-            }
         }
     } else if (warp > 1) {  // the sequences' own tokens (a sum of integers: the same in every CTA)
         long long own = 0;
@@ -476,16 +526,62 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     // of this one, may start wherever there is room.
     dev::griddep_launch_dependents();
     constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
-    const long long W = *units_s;
     // (the own pass draws 5.4 MB of a BF16 cache a us from all SMs, 2.8 of FP8 codes)
+    const long long W = *units_s;
     const float own_us = fmaxf(0.5f * static_cast<float>(*own_s) * (p.num_kv_heads * p.head_dim * (KV8 ? 32.f / 2.8e6f : 64.f / 5.4e6f)) * gridDim.x,
                                0.35f * static_cast<float>(p.num_seqs) * p.num_kv_heads);
-    const int C = W > 0 ? share_units(W, abs(*items_s), *items_s > 0, *time_s, own_us, gridDim.x / 2) : 0;
-    if (blockIdx.x == 0 && tid == 0) *p.plan_total = {W, C, 0};
+    int C = 0;
     long long u = 0, u1 = 0;
-    if (team < C) {
-        u = quotient(W * team, C);
-        u1 = quotient(W * (team + 1), C);
+    if constexpr (!MULTI) {
+        if (W > 0) C = share_units(W, *items_s, grp[0].last_units(item_rows(DPAD)) == quotient(W, *items_s), *time_s, own_us, gridDim.x / 2);
+        if (blockIdx.x == 0 && tid == 0) {  // the merge finds each row's partials from this
+            *p.plan_total = {W, C, 0};
+            p.plan_groups[0] = grp[0];
+        }
+        if (team < C) {
+            u = quotient(W * team, C);
+            u1 = quotient(W * (team + 1), C);
+        }
+    } else {
+        if (warp == 0) {  // (by one warp: twelve would share the issue slots)
+            int run = 0;
+            if (W > 0) {
+                C = share_units(W, *items_s, false, *time_s, own_us, gridDim.x / 2);
+                run = whole_teams(grp, p.num_groups, p.num_kv_heads, item_rows(DPAD), W, C, gridDim.x / 2, *items_s,
+                                  __fdividef(*time_s, static_cast<float>(W)), KV8 ? 6.f : 3.f, lane);
+                if (team < C && run > 0) {
+                    whole_range(grp, p.num_kv_heads, item_rows(DPAD), run, team, u, u1);
+                } else if (team < C) {
+                    u = quotient(W * team, C);
+                    u1 = quotient(W * (team + 1), C);
+                }
+            }
+            if (lane == 0) {
+                range_s[0] = u;
+                range_s[1] = u1;
+                share_s[0] = C;
+                share_s[1] = run;
+            }
+        }
+        __syncthreads();
+        u = range_s[0];
+        u1 = range_s[1];
+        C = share_s[0];
+        if (blockIdx.x == 0 && warp == 1) {
+            const int run = share_s[1];
+            if (lane == 0) *p.plan_total = {W, C, run > 0};
+            for (int g = lane; g < p.num_groups; g += 32) {
+                GroupPlan r = grp[g];
+                r.first_team = r.teams = r.last_teams = 0;
+                if (run > 0) {
+                    for (int k = 0; k < g; ++k) r.first_team += p.num_kv_heads * head_teams(grp[k], item_rows(DPAD), run);
+                    r.teams = teams_of(r.tiles, run);
+                    r.last_teams = teams_of(r.last_units(item_rows(DPAD)), run);
+                }
+                p.plan_groups[g] = r;
+            }
+            __syncwarp();
+        }
     }
     const int bs = static_cast<int>(p.block_size.d);
     const int D = p.head_dim;

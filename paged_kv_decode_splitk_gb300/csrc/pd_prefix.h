@@ -25,12 +25,12 @@ __host__ __device__ constexpr int item_rows(int dpad) { return 2 * block_rows(dp
 // the tiles (128 rows: 67 us in turn, 89 by halves when a tile took it longer).
 __host__ __device__ constexpr bool is_pair(int rows, int of_item) { return rows > of_item / 2; }
 
-// What the prefix pass found the work to be: units in all, and the teams that
-// share them.
+// What the prefix pass found the work to be: units in all, the teams that share
+// them, and whether every item has whole teams.
 struct PlanTotal {
     long long units;
     int teams;
-    int pad;
+    int whole;
 };
 
 // One group on the line of work units.  Its items are, for each KV head, the
@@ -44,6 +44,7 @@ struct GroupPlan {
     int rows;       // sequences x query heads of a KV head
     int items;      // of a KV head
     int tokens;     // of the prefix
+    int first_team, teams, last_teams;  // whole teams: of an item, and of a KV head's last
 
     // units of a KV head, and of its last item, which alone may have few rows
     __host__ __device__ int last_units(int of_item) const {

@@ -10,10 +10,10 @@
 namespace pd {
 namespace prefix {
 
-template <int DPAD, bool KV8>
-cudaError_t launch_prefix(const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int teams,
-                          cudaStream_t stream) {
-    auto kern = prefix_kernel<DPAD, KV8>;
+template <int DPAD, bool KV8, bool MULTI>
+cudaError_t launch_prefix_as(const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int teams,
+                             cudaStream_t stream) {
+    auto kern = prefix_kernel<DPAD, KV8, MULTI>;
     static std::mutex mu;
     static bool configured[64] = {false};
     int dev = 0;
@@ -48,6 +48,13 @@ cudaError_t launch_prefix(const CUtensorMap *tk, const CUtensorMap *tv, const Pr
     maps.k[0] = *tk;
     maps.v[0] = *tv;
     return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+template <int DPAD, bool KV8>
+cudaError_t launch_prefix(const CUtensorMap *tk, const CUtensorMap *tv, const PrefixParams &p, int teams,
+                          cudaStream_t stream) {
+    return p.num_groups > 1 ? launch_prefix_as<DPAD, KV8, true>(tk, tv, p, teams, stream)
+                            : launch_prefix_as<DPAD, KV8, false>(tk, tv, p, teams, stream);
 }
 
 }  // namespace prefix

@@ -15,11 +15,11 @@ def test_workspace():
     # the own partials; one slot for each CTA and each item: a block of 256 rows of (m, l) and o
     rows, items = 64 * 32 * 10, 8 * (1 + 64 * 4 // 256)
     least = rows * (128 + 2) * 4 + (items + 152) * 256 * (128 + 2) * 4
-    assert least <= n(64, 1, 32, 8, 128, 10) <= least + 32 * 256 + 6 * 256
+    assert least <= n(64, 1, 32, 8, 128, 10) <= least + 48 * 256 + 6 * 256
     assert n(64, 3, 32, 8, 128, 10) > n(64, 1, 32, 8, 128, 10)
 
 
-def _walk(G, Hkv, groups, BR, tile, teams):
+def _walk(G, Hkv, groups, BR, tile, teams, whole):
     """The prefix pass's division of work, restated: every (group, KV head, item, CTA or both, tile) by the CTA that
     takes it, which has to be exactly one, and the slots the merge reads for it."""
     IR = 2 * BR
@@ -35,10 +35,37 @@ def _walk(G, Hkv, groups, BR, tile, teams):
         units = head * Hkv if items and tiles else 0
         plan.append((W, first_item, tiles, rows, items, head))
         W, first_item = W + units, first_item + (items * Hkv if units else 0)
-    C, slots, used = min(W, teams), {}, {}
-    for team in range(C):
+    C, slots, used, run, base = min(W, teams), {}, {}, 0, [0]
+
+    def places_of(rows, items, tiles, item):
+        return tiles if item < items - 1 or pair(rows - (items - 1) * IR) else (tiles + 1) // 2
+
+    def head_teams(tiles, rows, items, run):
+        return sum(-(-places_of(rows, items, tiles, i) // run) for i in range(items)) if tiles else 0
+
+    if whole and W:  # whole teams for every item, where they are enough
+        for run in range(-(-W // C), 3 * W):
+            if sum(Hkv * head_teams(t, r, i, run) for _, _, t, r, i, _ in plan) <= teams:
+                break
+        else:
+            run = 0
+    if run:
+        ranges = []
+        for first_unit, _, tiles, rows, items, head in plan:
+            for kvh in range(Hkv if tiles else 0):
+                for item in range(items):
+                    n, u = places_of(rows, items, tiles, item), first_unit + kvh * head + item * tiles
+                    parts = -(-n // run)
+                    at = [u + n // parts * k + min(k, n % parts) for k in range(parts + 1)]
+                    ranges += list(zip(at, at[1:]))
+            base.append(len(ranges))
+        C = len(ranges)
+        assert C <= teams and all(a < b <= a + run for a, b in ranges)
+    else:
+        ranges = [(W * c // C, W * (c + 1) // C) for c in range(C)]
+    for team, (begin, end) in enumerate(ranges):
         for rank in (0, 1):
-            u, end = W * team // C, W * (team + 1) // C
+            u = begin
             while u < end:
                 gi = max(i for i, g in enumerate(plan) if g[0] <= u)
                 first_unit, item0, tiles, rows, items, head = plan[gi]
@@ -64,6 +91,9 @@ def _walk(G, Hkv, groups, BR, tile, teams):
                 places = tiles if pair(r) else (tiles + 1) // 2
                 u = first_unit + kvh * head + item * tiles
                 c0, c1 = ((u + 1) * C - 1) // W, ((u + places) * C - 1) // W  # the teams the merge reads
+                if run:
+                    c0 = base[gi] + kvh * head_teams(tiles, rows, items, run) + item * -(-tiles // run)
+                    c1 = c0 + -(-places // run) - 1
                 for rank in (0, 1) if pair(r) else (None,):
                     mine = {slots[gi, kvh, item, rank, t] for t in range(tiles)}
                     ranks = (0, 1) if rank is None else (rank,)
@@ -78,7 +108,7 @@ def test_work_division(BR, tile):
         G, Hkv = rng.choice([1, 2, 3, 4, 7, 8, 16]), rng.choice([1, 2, 8])
         groups = [(rng.choice([0, 1, 2, 5, 20, 32, 40, 64, 100]), rng.choice([0, 1, 17, 64, 100, 128, 129, 700, 3000]))
                   for _ in range(rng.randint(1, 5))]
-        items = _walk(G, Hkv, groups, BR, tile, rng.choice([1, 3, 24, 76]))
+        items = _walk(G, Hkv, groups, BR, tile, rng.choice([1, 3, 24, 76]), rng.random() < 0.6)
         assert items <= Hkv * (len(groups) + sum(n for n, _ in groups) * G // (2 * BR))  # what the workspace is sized for
 
 

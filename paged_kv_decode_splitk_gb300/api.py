@@ -56,11 +56,28 @@ class PagedInputs:
                                 else max_decode_seqs)
 
 
-def workspace(num_seqs: int, num_q_heads: int, head_dim: int, num_splits: int, device) -> torch.Tensor | None:
+def _fresh(shape, dtype, device, stream):
+    """An uninitialised tensor that a launch on `stream` (a torch stream or a handle; None: the current one) writes.  It is
+    allocated in that stream's order, since what the current stream has freed it may still have to write; and it is not
+    reused before what the current stream does with it until it is freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream, device=device)
+    if s.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def workspace(num_seqs: int, num_q_heads: int, head_dim: int, num_splits: int, device, stream=None) -> torch.Tensor | None:
+    """The split-K workspace of a call (None where it needs none); stream: of a call on another stream than the current one."""
     n = pd.pd_workspace_bytes(num_seqs, num_q_heads, head_dim, num_splits)
     if num_splits <= 1 or n == 0:
         return None
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _fresh(n, torch.uint8, device, stream)
 
 
 def decode_attn(q, k_cache, v_cache, block_table, context_lens, inv_sqrt_d: float, num_splits: int,
@@ -71,9 +88,9 @@ def decode_attn(q, k_cache, v_cache, block_table, context_lens, inv_sqrt_d: floa
     are FP8 E4M3 codes with per-tensor scales k_scale / v_scale."""
     S, Hq, D = q.shape
     if out is None:
-        out = torch.empty((S, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _fresh((S, Hq, D), torch.bfloat16, q.device, stream)
     if ws is None and num_splits > 1:
-        ws = workspace(S, Hq, D, num_splits, q.device)
+        ws = workspace(S, Hq, D, num_splits, q.device, stream)
     if k_cache.dtype == torch.uint8:
         rc = pd.pd_decode_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, out,
                                    inv_sqrt_d, num_splits, ws, gqa_pack, stream)
@@ -145,16 +162,6 @@ def _caches(k_cache, v_cache, num_kv_heads: int, head_dim: int, device: int) -> 
                      f"{v_cache.dtype} {tuple(v_cache.shape)}")
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tensors allocated here for a launch on another stream than the current one are not reused before it is done."""
-    if stream is None:
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
-
-
 def _check_rope(rotation, x, positions, out, dev: int) -> None:
     _rows("x", x, None, None, rotation.head_dim, dev, False)
     T, H, D = x.shape
@@ -173,8 +180,7 @@ def rope(rotation: pd.Rope, x, positions, out=None, inverse: bool = False, strea
             return done
     _check_rope(rotation, x, positions, out, pd.current_device())
     if out is None:
-        out = torch.empty(x.shape, dtype=_BF16, device=x.device)
-        _used_on(stream, out)
+        out = _fresh(x.shape, _BF16, x.device, stream)
     pd.pd_rope_apply(rotation, x, positions, out, inverse, stream)
     return out
 
@@ -215,8 +221,7 @@ def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, to
             return done
     _check_append(q, k, v, k_cache, v_cache, block_table, context_lens, token_starts, q_out, pd.current_device())
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=_BF16, device=q.device)
-        _used_on(stream, q_out)
+        q_out = _fresh(q.shape, _BF16, q.device, stream)
     if k_cache.dtype is _U8:
         pd.pd_append_kv_fp8(rotation, q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, block_table, context_lens,
                             token_starts, stream)
@@ -226,9 +231,10 @@ def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, to
 
 
 def prefix_workspace(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int, head_dim: int, num_splits: int,
-                     device) -> torch.Tensor:
+                     device, stream=None) -> torch.Tensor:
+    """The workspace of a decode_attn_prefix; stream: of a call on another stream than the current one."""
     n = pd.pd_prefix_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, num_splits)
-    return torch.empty(n, dtype=_U8, device=device)
+    return _fresh(n, _U8, device, stream)
 
 
 def _check_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens, out, dev: int) -> None:
@@ -266,11 +272,9 @@ def decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_sta
                   pd.current_device())
     S, Hq, D = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
-        _used_on(stream, out)
+        out = _fresh(q.shape, _BF16, q.device, stream)
     if ws is None:
-        ws = prefix_workspace(S, prefix_lens.shape[0], Hq, max(1, k_cache.shape[2]), D, num_splits, q.device)
-        _used_on(stream, ws)
+        ws = prefix_workspace(S, prefix_lens.shape[0], Hq, max(1, k_cache.shape[2]), D, num_splits, q.device, stream)
     if k_cache.dtype is _U8:
         pd.pd_decode_attn_prefix_fp8(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_lens, group_starts,
                                      block_table, context_lens, out, inv_sqrt_d, num_splits, ws, stream)
@@ -310,8 +314,7 @@ def run_tiled(inp: TiledInputs, tiled: pd.Tiled | None = None, out=None, stream=
     try:
         strides = tiled.scratch_pool_strides() if tw.layout == "scratch" else tiled.paged_strides()
         if out is None:
-            out = torch.empty((tw.num_seqs, tw.num_q_heads, tw.head_dim), dtype=torch.bfloat16,
-                              device=inp.device)
+            out = _fresh((tw.num_seqs, tw.num_q_heads, tw.head_dim), torch.bfloat16, inp.device, stream)
         tiled.begin(tw.num_seqs, stream)
         for c in range(tw.num_calls):
             tiled.step(inp.q, inp.k_pool, inp.v_pool, inp.tile_blocks[c], inp.tile_counts[c],
@@ -361,8 +364,7 @@ def run_tiled_mixed(inp: MixedTiledInputs, tiled: pd.Tiled | None = None, out=No
                          mw.tile_capacity)
     try:
         if out is None:
-            out = torch.empty((mw.num_seqs, mw.num_q_heads, mw.head_dim), dtype=torch.bfloat16,
-                              device=inp.device)
+            out = _fresh((mw.num_seqs, mw.num_q_heads, mw.head_dim), torch.bfloat16, inp.device, stream)
         tiled.run(inp.q, inp.sources(tiled), out, mw.num_seqs, stream)
     finally:
         if own:

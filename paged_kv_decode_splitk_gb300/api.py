@@ -237,7 +237,7 @@ def prefix_workspace(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_he
     return _fresh(n, _U8, device, stream)
 
 
-def _check_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens, out, dev: int) -> None:
+def _check_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens, out, ws, dev: int) -> None:
     if q.dim() != 3 or not q.is_contiguous():
         _refuse("q", q, "contiguous BF16", (None, None, None), dev)
     S, Hq, D = q.shape
@@ -254,6 +254,8 @@ def _check_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, 
         _rows("out", out, S, Hq, D, dev, True)
         if not out.is_contiguous():
             raise ValueError("out has to be contiguous")
+    if ws is not None and not (ws.is_contiguous() and ws.get_device() == dev):
+        _refuse("ws", ws, "a contiguous buffer", (None,), dev)
 
 
 def decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens,
@@ -268,7 +270,7 @@ def decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_sta
                                              context_lens, inv_sqrt_d, num_splits, out, ws, k_scale, v_scale)
         if done is not NotImplemented:
             return done
-    _check_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens, out,
+    _check_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table, context_lens, out, ws,
                   pd.current_device())
     S, Hq, D = q.shape
     if out is None:

@@ -150,3 +150,17 @@ def test_api_refuses_tensors():
                    dict(prefix_lens=i32(2).long())):
         with pytest.raises(ValueError):
             api.decode_attn_prefix(**{**good, **change})
+
+
+def test_api_refuses_workspaces():
+    """A workspace that is not one buffer, or not on the device of the call (the CPU stands in for both sides here)."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    args = (bf(3, 8, 64), bf(4, 16, 2, 64), bf(4, 16, 2, 64), i32(2, 2), i32(2), i32(3), i32(3, 2), i32(3), None)
+    api._check_prefix(*args, None, -1)
+    api._check_prefix(*args, torch.zeros(64, dtype=torch.uint8), -1)
+    with pytest.raises(ValueError, match="ws"):
+        api._check_prefix(*args, torch.zeros(64, dtype=torch.uint8)[::2], -1)
+    here = type("T", (), {"get_device": lambda self: 0, "is_contiguous": lambda self: True, "device": "cuda:0"})
+    with pytest.raises(ValueError, match="ws"):
+        api._check_prefix(*args, here(), -1)

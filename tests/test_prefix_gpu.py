@@ -405,3 +405,14 @@ def test_quick_calls_take_what_fits_and_leave_the_rest():
     for i, bad in ((1, 128), (2, None), (2, x[:1]), (3, k[:, :1]), (4, v.float()), (5, b.vc[1:]), (7, more[7][:1]), (8, more[8].cpu()), (9, pos), (10, x[:1]),
                    (11, "a")):
         assert quick.append_kv(*more[:i], bad, *more[i + 1:]) is NotImplemented, (i, bad)
+
+
+def test_workspaces_elsewhere_are_refused():
+    b = Batch([2], [40], [3, 17], 8, 2, 64, seed=3)
+    n = api.prefix_workspace(2, 1, 8, 2, 64, 3, DEV).numel()
+    far = torch.cuda.current_stream().cuda_stream
+    for stream in (None, far):
+        for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2]):
+            with pytest.raises(ValueError, match="ws"):
+                b.run(ws=ws, stream=stream)
+        b.check(b.run(ws=torch.empty(n // 4 + 1, dtype=torch.float32, device=DEV), stream=stream))

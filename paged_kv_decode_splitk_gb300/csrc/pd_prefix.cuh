@@ -13,11 +13,12 @@
 // sequence's own tokens.
 //
 // GB300 mapping.
-//   * CTAs work in teams of two, a cluster.  A team's item is up to 512 rows of a
-//     KV head (256 at head dims above 128): each CTA has half of them, both need
-//     the same K and V tiles, and each loads half of every tile and multicasts it
-//     to both, which halves what the SMs draw from L2.  Rows that one CTA can take
-//     both have, and they take the tiles in turn.
+//   * CTAs work in teams of two.  A team's item is up to 512 rows of a KV head (256
+//     at head dims above 128): each CTA has half of them, and both load every tile,
+//     the second time from L2.  Rows that one CTA can take both have, and they take
+//     the tiles in turn.  The two share nothing but the plan: every copy and
+//     barrier is of one CTA (halves of a tile copied by each for both took as
+//     long: 126.9 us whole, 127.3 in halves, 256 sequences behind 32768 tokens).
 //   * Work is counted in units (item, a tile for both CTAs) in one line over all
 //     groups; team c of C takes units [W c / C, W (c + 1) / C): every SM gets the
 //     same number of tiles whatever the shapes, and a team's partials of item i go
@@ -94,14 +95,13 @@ struct Plan {
 struct Segment {
     int kvh, plen, slot;
     int tile0, stride;  // tile j of the run is tile0 + j stride
-    int n;      // places in the run: the same for both CTAs of the team
-    int live;   // tiles of this CTA: n, or one less where the last place has no tile
+    int n;      // tiles of the run (0: the last place of an item taken in turn has but one, the other CTA's)
     int row0;   // first row of this CTA within the group
     int rows;   // rows of this CTA
     int seq0;   // the group's first sequence
     int group;
     bool two;   // more than kRowTile rows: both streams use every tile
-    bool pair;  // both CTAs use the same tiles
+    bool pair;  // both CTAs use the same tiles, half of the rows each
 };
 
 // a / b, in 32 bits where both fit (a fifth of the instructions).
@@ -135,10 +135,10 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
     s.pair = is_pair(rows, 2 * BR);
     const int places = s.pair ? g.tiles : (g.tiles + 1) >> 1;
     const long long left = u1 - u;
-    s.n = left < places - at ? static_cast<int>(left) : places - at;
+    const int taken = left < places - at ? static_cast<int>(left) : places - at;  // of them
     s.stride = s.pair ? 1 : 2;
     s.tile0 = s.pair ? at : 2 * at + rank;
-    s.live = s.tile0 + (s.n - 1) * s.stride < g.tiles ? s.n : s.n - 1;
+    s.n = s.tile0 + (taken - 1) * s.stride < g.tiles ? taken : taken - 1;
     const int half = (rows + 1) >> 1;
     s.row0 = item * 2 * BR + (s.pair && rank ? half : 0);
     s.rows = !s.pair ? rows : rank ? rows - half : half;
@@ -147,8 +147,8 @@ __device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_group
     s.group = lo;
     s.slot = 2 * (g.first_item + s.kvh * g.items + item + team) + rank;
     s.two = s.rows > kRowTile;
-    if (s.n < 1) return false;  // (never; the walk over the units ends all the same)
-    u += s.n;
+    if (taken < 1) return false;  // (never; the walk over the units ends all the same)
+    u += taken;
     return true;
 }
 
@@ -467,19 +467,17 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     // (the warp's number from one lane, so that the compiler knows it to be the
     // same on all: the product warp's operands then live in uniform registers)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int rank = blockIdx.x & 1, team = blockIdx.x >> 1;  // clusters are of two CTAs
+    const int rank = blockIdx.x & 1, team = blockIdx.x >> 1;
 
     // ---- set-up that reads no global memory -----------------------------------
     if (tid == 0) {
-        // a stage is free once both CTAs of the team have used it: either may be
-        // the next to write a half of it
         for (int i = 0; i < NST; ++i) {
             dev::mbar_init(bar_full + 8 * i, KV8 ? kConverters / 32 : 1);
-            dev::mbar_init(bar_empty + 8 * i, KV8 ? 1 : 2);
+            dev::mbar_init(bar_empty + 8 * i, 1);
         }
         for (int i = 0; KV8 && i < 3; ++i) {
             dev::mbar_init(bar_rfull + 8 * i, 1);
-            dev::mbar_init(bar_rempty + 8 * i, 2 * kConverters / 32);
+            dev::mbar_init(bar_rempty + 8 * i, kConverters / 32);
         }
         for (int i = 0; !KV8 && i < NST; ++i) dev::mbar_init(bar_land + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
@@ -496,7 +494,6 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         dev::prefetch_tensormap(&maps.k[0]);
         dev::prefetch_tensormap(&maps.v[0]);
     }
-    dev::cluster_arrive_relaxed();
     if (warp == 1) tc::tmem_alloc_512(dev::smem_addr(tmem_s));
     __syncthreads();      // (the sum of the own tokens starts at zero)
     dev::griddep_wait();  // q, the caches, tables and lengths are final
@@ -518,7 +515,6 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         const unsigned sum = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(min(own >> 4, 1ll << 23)));
         if (lane == 0 && sum) atomicAdd(own_s, sum);
     }
-    dev::cluster_wait();  // the peer's barriers are initialised
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -613,8 +609,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const int32_t *ids = p.prefix_table + static_cast<long long>(sg.group) * p.max_prefix_blocks;
             const int ahead = ONE || !sg.two ? 2 : 1;
-            // of a shared tile each CTA loads every other box, for both
-            const bool mine = lane < NBOX && (!sg.pair || (lane & 1) == rank);
+            const bool mine = lane < NBOX;  // a box a lane
             // Block ids, 32 boxes' rows (chunks of CT tokens) at a time: lane l of `now`
             // has chunk 32 w + l of the run, `then` the 32 after them, asked for a
             // window ahead.  Past the prefix, and for a bad id (-1), it is one
@@ -623,7 +618,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             auto ids_of = [&](int w) -> int {
                 const int c = 32 * w + lane, j = c >> lg;
                 const int tok = (sg.tile0 + j * sg.stride) * BN + (c & (NCH - 1)) * CT;
-                if (j >= sg.live || tok >= sg.plen) return p.num_blocks;
+                if (j >= sg.n || tok >= sg.plen) return p.num_blocks;
                 const int id = __ldg(ids + fast_div(tok, p.block_size));
                 return id >= 0 && id < p.num_blocks ? id : -1;
             };
@@ -657,25 +652,17 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 // A tile's box of live and dead tokens holds whatever the cache's
                 // slots past the prefix hold; a dead V row must not reach the
                 // product (0 x NaN), so those rows are zeroed before it is handed on.  It
-                // lands at a barrier of its stage: the peer sends its boxes as soon as the
-                // stage is free, which may be before this CTA has seen its last tail land.
-                const bool tail = !KV8 && is_v && j < sg.live && nv < BN && (nv & (CT - 1));
+                // lands at a barrier of its stage.
+                const bool tail = !KV8 && is_v && nv < BN && (nv & (CT - 1));
                 const uint32_t bar = (tail ? bar_land : full) + 8 * st;
-                if (j >= sg.live) {  // a place without a tile: nothing lands
-                    if (lane == 0) arrive(bar);
-                } else {
-                    if (lane == 0) dev::mbar_arrive_expect_tx(bar, BYTES);
-                    __syncwarp();
-                    if (mine) {
-                        const int sub = tok - fast_div(tok, p.block_size) * bs;
-                        const uint32_t to = dst + col * (BN * (KV8 ? COLS : 128)) + chunk * (CT * (KV8 ? COLS : 128));
-                        const CUtensorMap *map = is_v ? &maps.v[0] : &maps.k[0];
-                        const int c1 = p.tok_dim == 1 ? sub : sg.kvh, c2 = p.tok_dim == 1 ? sg.kvh : sub;
-                        if (sg.pair)
-                            tc::tma_load_4d_both(to, map, bar, col * COLS, c1, c2, id, policy);
-                        else
-                            dev::tma_load_4d(to, map, bar, col * COLS, c1, c2, id, policy);
-                    }
+                if (lane == 0) dev::mbar_arrive_expect_tx(bar, BYTES);
+                __syncwarp();
+                if (mine) {
+                    const int sub = tok - fast_div(tok, p.block_size) * bs;
+                    const uint32_t to = dst + col * (BN * (KV8 ? COLS : 128)) + chunk * (CT * (KV8 ? COLS : 128));
+                    const CUtensorMap *map = is_v ? &maps.v[0] : &maps.k[0];
+                    const int c1 = p.tok_dim == 1 ? sub : sg.kvh, c2 = p.tok_dim == 1 ? sg.kvh : sub;
+                    dev::tma_load_4d(to, map, bar, col * COLS, c1, c2, id, policy);
                 }
                 if (tail) {
                     const uint32_t lph = (land_ph >> st) & 1;
@@ -701,7 +688,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (ok && v >= 0) ok = load(true, v);
             }
         }
-        // every release of a stage by either CTA has arrived here before this CTA ends
+        // every release of a stage has arrived before this CTA ends
         for (long long i = issued < DEPTH ? 0 : issued - DEPTH; ok && i < issued; ++i)
             ok = wait_bar(empty + 8 * static_cast<int>(i % DEPTH), static_cast<uint32_t>((i / DEPTH) & 1), gave_up);
         if (!ok && lane == 0) {
@@ -750,12 +737,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     tc::mma_ts(tmem + 256 + o * DPAD, tmem + buf * 128 + k * 8, vd + k * (2048 / 16), kDescO, accumulate || k > 0);
                 if (done) tc::commit(bar_o + 8 * o);
             };
-            auto release = [&](int stage) {
-                if (KV8)
-                    tc::commit(bar_empty + 8 * stage);
-                else
-                    tc::commit_both(bar_empty + 8 * stage);
-            };
+            auto release = [&](int stage) { tc::commit(bar_empty + 8 * stage); };
             auto weights = [&](int buf) {
                 const bool got = wait_one(bar_p + 8 * buf, (pph >> buf) & 1, gave_up);
                 pph ^= 1u << buf;
@@ -767,34 +749,29 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 return got;
             };
             while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
-                const int n = sg.n, live = sg.live;
+                const int n = sg.n;
+                if (n == 0) continue;
                 int ks = 0, vs = 0;
-                if (live > 0 && !(ok = queries(0))) break;
+                if (!(ok = queries(0))) break;
                 if (!(ok = take(ks))) break;
                 if (!ONE && sg.two) {
-                    if (live > 0) {
-                        scores(0, 0, ks);
-                        if (!(ok = queries(1))) break;
-                        scores(1, 1, ks);
-                    }
+                    scores(0, 0, ks);
+                    if (!(ok = queries(1))) break;
+                    scores(1, 1, ks);
                     release(ks);
                     if (!(ok = take(vs))) break;
                     for (int j = 0; ok && j < n; ++j) {
-                        const bool now = j < live, more = j + 1 < live, next = j + 1 < n;
+                        const bool more = j + 1 < n;
                         const int v = vs;
-                        if (next && !(ok = take(ks))) break;
-                        if (now) {
-                            if (!(ok = weights(0))) break;
-                            values(0, 0, v, j > 0, !more);
-                        }
+                        if (more && !(ok = take(ks))) break;
+                        if (!(ok = weights(0))) break;
+                        values(0, 0, v, j > 0, !more);
                         if (more) scores(0, 0, ks);
-                        if (now) {
-                            if (!(ok = weights(1))) break;
-                            values(1, 1, v, j > 0, !more);
-                        }
+                        if (!(ok = weights(1))) break;
+                        values(1, 1, v, j > 0, !more);
                         release(v);  // (before the scores: a commit waits for all that came before)
-                        if (more) scores(1, 1, ks);
-                        if (next) {
+                        if (more) {
+                            scores(1, 1, ks);
                             release(ks);
                             ok = take(vs);
                         }
@@ -802,7 +779,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 } else {
                     // scores of tile j, whose keys are the next of the ring
                     auto next_scores = [&](int j) {
-                        if (j < live) scores(j & 1, 0, ks);
+                        scores(j & 1, 0, ks);
                         release(ks);
                     };
                     next_scores(0);
@@ -814,11 +791,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         if (!(ok = take(vs))) break;
                         const bool next = j + 2 < n;
                         if (next && !(ok = take(ks))) break;
-                        if (j < live) {
-                            const int t = j & 1;
-                            if (!(ok = weights(t))) break;
-                            values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= live);
-                        }
+                        const int t = j & 1;
+                        if (!(ok = weights(t))) break;
+                        values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= n);
                         release(vs);
                         if (next) next_scores(j + 2);
                     }
@@ -853,47 +828,45 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         int rs = 0, st = 0;
         uint32_t rph = 0, ph = 0;
         bool ok = true;
-        auto convert = [&](bool live, bool is_v, int nv) {
+        long long handed = 0;
+        auto convert = [&](bool is_v, int nv) {
             if (!wait_bar(bar_rfull + 8 * rs, rph, gave_up) || !wait_bar(bar_empty + 8 * st, ph ^ 1, gave_up)) return false;
             const uint8_t *src = smem + L::raw + rs * L::kRawBytes;
             uint8_t *dst = smem + L::ring + st * L::kStageBytes;
-            if (live) {
-                // (eight loads before the first store, which the compiler would
-                // not move them over)
-                constexpr int N = BN / ROWS, BATCH = N < 8 ? N : 8;
+            // (eight loads before the first store, which the compiler would
+            // not move them over)
+            constexpr int N = BN / ROWS, BATCH = N < 8 ? N : 8;
 #pragma unroll 1
-                for (int k0 = 0; k0 < N; k0 += BATCH) {
-                    uint4 v[BATCH];
+            for (int k0 = 0; k0 < N; k0 += BATCH) {
+                uint4 v[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k)
+                    v[k] = *reinterpret_cast<const uint4 *>(src + (k & 1 ? from ^ FLIP : from) +
+                                                          (k0 + k) * (ROWS * (DPAD < 128 ? DPAD : 128)));
+                if (is_v && nv < BN) {
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k)
-                        v[k] = *reinterpret_cast<const uint4 *>(src + (k & 1 ? from ^ FLIP : from) +
-                                                              (k0 + k) * (ROWS * (DPAD < 128 ? DPAD : 128)));
-                    if (is_v && nv < BN) {
-#pragma unroll
-                        for (int k = 0; k < BATCH; ++k)
-                            if (row0 + (k0 + k) * ROWS >= nv) v[k] = make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int k = 0; k < BATCH; ++k) {
-                        uint4 lo, hi;
-                        dev::e4m3x4_to_f16x4(v[k].x, lo.x, lo.y);
-                        dev::e4m3x4_to_f16x4(v[k].y, lo.z, lo.w);
-                        dev::e4m3x4_to_f16x4(v[k].z, hi.x, hi.y);
-                        dev::e4m3x4_to_f16x4(v[k].w, hi.z, hi.w);
-                        *reinterpret_cast<uint4 *>(dst + (k & 1 ? to_lo ^ FLIP : to_lo) + (k0 + k) * (ROWS * 128)) = lo;
-                        *reinterpret_cast<uint4 *>(dst + (k & 1 ? to_hi ^ FLIP : to_hi) + (k0 + k) * (ROWS * 128)) = hi;
-                    }
+                        if (row0 + (k0 + k) * ROWS >= nv) v[k] = make_uint4(0, 0, 0, 0);
                 }
-                tc::fence_async_shared();
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    uint4 lo, hi;
+                    dev::e4m3x4_to_f16x4(v[k].x, lo.x, lo.y);
+                    dev::e4m3x4_to_f16x4(v[k].y, lo.z, lo.w);
+                    dev::e4m3x4_to_f16x4(v[k].z, hi.x, hi.y);
+                    dev::e4m3x4_to_f16x4(v[k].w, hi.z, hi.w);
+                    *reinterpret_cast<uint4 *>(dst + (k & 1 ? to_lo ^ FLIP : to_lo) + (k0 + k) * (ROWS * 128)) = lo;
+                    *reinterpret_cast<uint4 *>(dst + (k & 1 ? to_hi ^ FLIP : to_hi) + (k0 + k) * (ROWS * 128)) = hi;
+                }
             }
+            tc::fence_async_shared();
             arrive_warp(bar_full + 8 * st, lane);
-            // free for both CTAs (the reads have returned their values; an arrival that
-            // also ordered this warp's writes for the peer took half a microsecond)
-            if (lane < 2) dev::mbar_arrive_cluster_relaxed(dev::map_to_rank(bar_rempty + 8 * rs, lane));
+            arrive_warp(bar_rempty + 8 * rs, lane);  // (the reads come before the loads that refill it)
             if (++rs == L::kRawStages) {
                 rs = 0;
                 rph ^= 1;
             }
+            ++handed;
             if (++st == NST) {
                 st = 0;
                 ph ^= 1;
@@ -903,11 +876,14 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         while (ok && next_segment<BR>(grp, p.num_groups, u, u1, team, rank, sg)) {
             const int ahead = ONE || !sg.two ? 2 : 1;
             for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
-                if (i < sg.n) ok = convert(i < sg.live, false, BN);
+                if (i < sg.n) ok = convert(false, BN);
                 const int v = i - ahead + 1;
-                if (ok && v >= 0) ok = convert(v < sg.live, true, sg.plen - (sg.tile0 + v * sg.stride) * BN);
+                if (ok && v >= 0) ok = convert(true, sg.plen - (sg.tile0 + v * sg.stride) * BN);
             }
         }
+        // every release of a stage has arrived before this CTA ends
+        for (long long i = handed < NST ? 0 : handed - NST; ok && i < handed; ++i)
+            ok = wait_bar(bar_empty + 8 * static_cast<int>(i % NST), static_cast<uint32_t>((i / NST) & 1), gave_up);
     }
     } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -936,7 +912,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             // partials have to have left from there.)
             if (lane == 0) tc::bulk_wait_read<0>();
             __syncwarp();
-            if ((two || t == 0) && sg.live > 0) {
+            if ((two || t == 0) && sg.n > 0) {
                 uint8_t *qt = smem + L::q + t * (kRowTile * DPAD * 2);
                 // 32 rows x CHUNKS chunks over 32 lanes, sixteen loads in flight at once
                 constexpr int BATCH = CHUNKS < 16 ? CHUNKS : 16;
@@ -993,7 +969,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             float m = kNegInf, l = 0.f;
             bool first = true;
             const int step = ONE || two ? 1 : 2;
-            for (int j = step == 2 ? t : 0; j < sg.live; j += step) {
+            for (int j = step == 2 ? t : 0; j < sg.n; j += step) {
                 const int buf = ONE ? (j & 1) : t;
                 const uint32_t ts = tmem + lanes + buf * 128;
                 if (!(ok = wait_bar(bar_s + 8 * buf, (sph >> buf) & 1, gave_up))) break;
@@ -1073,7 +1049,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 const int row = t * kRowTile + r;
                 const bool in = row < sg.rows;
                 if (in) *reinterpret_cast<float2 *>(p.part_ml + (at + row) * 2) = make_float2(m, l);
-                if (sg.live > 0) {
+                if (sg.n > 0) {
                     if (!(ok = wait_bar(bar_o + 8 * t, (oph >> t) & 1, gave_up))) break;
                     oph ^= 3;
                     tc::fence_after();
@@ -1095,7 +1071,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
                 xph ^= 1;
                 for (int k = 0; k < 2 && ok; ++k) {
-                    if (k < sg.live) {
+                    if (k < sg.n) {
                         ok = wait_bar(bar_o + 8 * k, (oph >> k) & 1, gave_up);
                         oph ^= 1u << k;
                     }
@@ -1109,20 +1085,20 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (in && t == 0)
                     *reinterpret_cast<float2 *>(p.part_ml + (at + r) * 2) =
                         make_float2(M, (a.y == 0.f ? 0.f : a.y * fa) + (b.y == 0.f ? 0.f : b.y * fb));
-                if (sg.live > 0) {
+                if (sg.n > 0) {
 #pragma unroll 1
                     for (int c = t * (DPAD / 2); c < (t + 1) * (DPAD / 2); c += 32) {
                         uint32_t x[32], y[32];
                         tc::ld_32x32(tmem + lanes + 256 + c, x);
                         tc::wait_ld(x);
-                        if (sg.live > 1) {
+                        if (sg.n > 1) {
                             tc::ld_32x32(tmem + lanes + 256 + DPAD + c, y);
                             tc::wait_ld(y);
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const float xa = fa == 0.f ? 0.f : __uint_as_float(x[i]) * fa;
-                            x[i] = __float_as_uint(sg.live > 1 && fb != 0.f ? fmaf(__uint_as_float(y[i]), fb, xa) : xa);
+                            x[i] = __float_as_uint(sg.n > 1 && fb != 0.f ? fmaf(__uint_as_float(y[i]), fb, xa) : xa);
                         }
                         store(c, x);
                     }
@@ -1137,14 +1113,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     }
     }
     if (warp >= 4 && lane == 0) tc::bulk_wait_all();
-    // The peer may still send halves of tiles and release stages: shared memory
-    // stays until both are done.
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     if (warp == 1) tc::tmem_free_512(*tmem_s);
-    dev::cluster_arrive_relaxed();
-    dev::cluster_wait();
 }
 
 }  // namespace prefix

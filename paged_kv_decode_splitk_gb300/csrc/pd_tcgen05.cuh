@@ -159,26 +159,6 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// The same on the barrier at this address in both CTAs of a cluster of two.
-__device__ __forceinline__ void commit_both(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
-// 4-D tiled tensor load into the same place of both CTAs of a cluster of two,
-// each one's barrier at this address counting the bytes that land there.
-__device__ __forceinline__ void tma_load_4d_both(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
-                                                 int c3, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.L2::"
-        "cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7, %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "h"(static_cast<uint16_t>(3)),
-        "l"(policy)
-        : "memory");
-}
-
 // A copy of shared memory to global memory (16-byte aligned, a multiple of 16
 // bytes), a group of its own; waits for all but N of this thread's groups to have
 // been read from shared memory, and for all of them to be done.

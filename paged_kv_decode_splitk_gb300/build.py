@@ -1,5 +1,6 @@
 """Build libpd.so (the C-ABI CUDA library) in-tree with nvcc for sm_103a, and the
-CPython module between it and torch's tensors (pd_binding.so) with g++.
+CPython module between it and torch's tensors (pd_binding.so) with g++.  Without
+PyTorch the library alone is built.
 
 Each translation unit compiles in its own nvcc process, in parallel; the
 objects and the shared library land in ``paged_kv_decode_splitk_gb300/_build``.
@@ -9,6 +10,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -63,14 +65,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     # (torch found, not imported: the machine that builds need not load it)
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
-    src, obj = os.path.join(CSRC, "pd_binding.cpp"), os.path.join(BUILD, "pd_binding.o")
-    if force or _stale(obj, [src, os.path.join(INCLUDE, "pd.h"), os.path.join(torch, "version.py")]):
-        cuda = os.path.dirname(os.path.dirname(shutil.which(nvcc) or nvcc))
-        cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-fvisibility=hidden", f"-I{INCLUDE}", "-isystem", f"{torch}/include",
-               "-isystem", f"{torch}/include/torch/csrc/api/include", "-isystem", f"{cuda}/include",
-               f"-I{sysconfig.get_paths()['include']}", "-c", src, "-o", obj]
-        procs.append(("pd_binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    torch = importlib.util.find_spec("torch")
+    if torch is not None:
+        torch = torch.submodule_search_locations[0]
+        src, obj, version = os.path.join(CSRC, "pd_binding.cpp"), os.path.join(BUILD, "pd_binding.o"), os.path.join(torch, "version.py")
+        if force or _stale(obj, [src, os.path.join(INCLUDE, "pd.h"), version]):
+            cuda = os.path.dirname(os.path.dirname(shutil.which(nvcc) or nvcc))
+            built_for = re.search(r"__version__ = ['\"](.*)['\"]", open(version).read()).group(1)
+            cmd = ["g++", "-O2", "-std=c++17", "-Wall", "-fPIC", "-fvisibility=hidden", f'-DPD_TORCH_VERSION="{built_for}"', f"-I{INCLUDE}",
+                   "-isystem", f"{torch}/include", "-isystem", f"{torch}/include/torch/csrc/api/include", "-isystem", f"{cuda}/include",
+                   f"-I{sysconfig.get_paths()['include']}", "-c", src, "-o", obj]
+            procs.append(("pd_binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -86,7 +91,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fvisibility=hidden"]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
-    if force or _stale(BINDING, [obj, LIB]):
+    if torch is not None and (force or _stale(BINDING, [obj, LIB])):
         tmp = BINDING + f".tmp{os.getpid()}"
         libs = [f"-l{name}" for name in ("torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda")]
         subprocess.run(["g++", "-shared", obj, LIB, f"-L{torch}/lib", *libs, "-Wl,-rpath,$ORIGIN", "-o", tmp], check=True)

@@ -213,4 +213,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "pd_binding", nullptr, -1, methods,
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject *PyInit_pd_binding(void) { return PyModule_Create(&module); }
+// (the torch whose tensors it reads: pd.quick() uses it with no other)
+extern "C" __attribute__((visibility("default"))) PyObject *PyInit_pd_binding(void) {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", PD_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

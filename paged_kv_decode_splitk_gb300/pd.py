@@ -175,23 +175,41 @@ def lib():
 _quick = None
 
 
+class _Declined:
+    """In the module's place where it cannot be used: declines every call."""
+
+    def __getattr__(self, name):
+        return lambda *args: NotImplemented
+
+
 def quick():
-    """The CPython module over the library (csrc/pd_binding.cpp), built beside it: api.py's first try at a call."""
+    """The CPython module over the library (csrc/pd_binding.cpp), built beside it: api.py's first try at a call.  Where it
+    is missing or was built for another torch, every call takes the ctypes binding to the same library, with a warning."""
     global _quick
     if _quick is None:
         import importlib.machinery
         import importlib.util
+        import warnings
 
-        import torch  # noqa: F401  (its libraries, which the module is linked to)
+        import torch  # (its libraries, which the module is linked to)
 
         lib()
         path = os.path.join(PKG, "_build", "pd_binding.so")
-        if not os.path.exists(path):
-            raise PdLibraryError(f"{path} is missing: build it with `python -m paged_kv_decode_splitk_gb300.build`")
-        loader = importlib.machinery.ExtensionFileLoader("pd_binding", path)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pd_binding", loader))
-        loader.exec_module(module)
-        _quick = module
+        why = "is missing"
+        if os.path.exists(path):
+            try:
+                loader = importlib.machinery.ExtensionFileLoader("pd_binding", path)
+                module = importlib.util.module_from_spec(importlib.util.spec_from_loader("pd_binding", loader))
+                loader.exec_module(module)
+                if module.built_for == torch.__version__:
+                    _quick = module
+                why = f"was built for torch {module.built_for}"
+            except ImportError as e:
+                why = f"does not load ({e})"
+        if _quick is None:
+            warnings.warn(f"{path} {why}: calls take some 10 us more; build it with `python -m paged_kv_decode_splitk_gb300.build`",
+                          RuntimeWarning, stacklevel=3)
+            _quick = _Declined()
     return _quick
 
 

@@ -170,10 +170,34 @@ def _check_rope(rotation, x, positions, out, dev: int) -> None:
         _rows("out", out, T, H, D, dev, False)
 
 
+class _Rotation(torch.autograd.Function):
+    """rope where x requires a gradient, which is the transposed map's value."""
+
+    @staticmethod
+    def forward(ctx, x, rotation, positions, inverse, stream):
+        ctx.rotation, ctx.inverse = rotation, inverse
+        ctx.save_for_backward(positions)
+        return rope(rotation, x, positions, inverse=inverse, stream=stream)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (positions,) = ctx.saved_tensors
+        # (a gradient may come broadcast, transposed or at an odd place: then its rows are laid out anew)
+        if grad.data_ptr() % 16 or grad.stride(2) != 1 or any(n > 1 and (s <= 0 or s % 8) for n, s in zip(grad.shape[:2], grad.stride())):
+            grad = grad.clone(memory_format=torch.contiguous_format)
+        return rope(ctx.rotation, grad, positions, inverse=not ctx.inverse), None, None, None, None
+
+
 def rope(rotation: pd.Rope, x, positions, out=None, inverse: bool = False, stream=None):
     """Rotary positions: x [T, H, D] BF16 (strided in tokens and heads, e.g. the q and k heads of a fused
     projection) rotated by positions [T] int32; returns out [T, H, D] (contiguous unless given; x itself
-    rotates in place).  inverse turns back: the map that takes gradients of out to gradients of x."""
+    rotates in place).  inverse applies the transposed map, the rotation back with the same factor, which takes
+    gradients of out to gradients of x; where x requires a gradient, autograd calls it (out cannot be given then; a
+    backward pass is captured into a graph, as torch wants it, while no eager graph of the same leaves lives)."""
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out: no gradient can pass through a tensor that is given; call under torch.no_grad() or let rope make it")
+        return _Rotation.apply(x, rotation, positions, inverse, stream)
     if stream is None:
         done = pd.quick().rope(pd._handle(rotation), rotation.head_dim, x, positions, out, inverse)
         if done is not NotImplemented:
@@ -213,7 +237,7 @@ def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, to
     v as they are, at the last positions of context_lens [S] (lengths after the append); q [T, Hq, D] (or
     None) rotated on the way and returned as q_out [T, Hq, D].  token_starts [S + 1] says which rows each
     sequence has; None: one each.  uint8 caches hold E4M3 codes of x / k_scale and x / v_scale.  Rows of no
-    sequence are left as they were, in q_out too."""
+    sequence are left as they were, in q_out too.  A serving call: no gradient passes through it."""
     if stream is None and q is not None:
         done = pd.quick().append_kv(pd._handle(rotation) or 0, 0 if rotation is None else rotation.head_dim, q, k, v, k_cache,
                                     v_cache, block_table, context_lens, token_starts, q_out, k_scale, v_scale)
@@ -264,7 +288,7 @@ def decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_sta
     """Decode attention behind shared prefixes: sequences group_starts[g] to group_starts[g + 1] - 1 (None: the whole
     batch, one group) attend to the prefix_lens[g] tokens prefix_table[g] names, then to their own context_lens
     tokens; a prefix is read once for its group.  Returns out [S, Hq, D] BF16.  uint8 caches are FP8 E4M3 codes
-    with per-tensor scales."""
+    with per-tensor scales.  A serving call: no gradient passes through it."""
     if stream is None:
         done = pd.quick().decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, block_table,
                                              context_lens, inv_sqrt_d, num_splits, out, ws, k_scale, v_scale)

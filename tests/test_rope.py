@@ -123,3 +123,10 @@ def test_api_refuses_tensors():
                    dict(token_starts=i32(2)), dict(q=None, q_out=bf(2, 4, 64))):
         with pytest.raises(ValueError):
             api.append_kv(None, **{**good, **change})
+
+
+def test_rope_given_outputs_take_no_gradient():
+    x = torch.zeros(2, 4, 64, dtype=torch.bfloat16, requires_grad=True)
+    rotation = type("Rotation", (), {"head_dim": 64, "handle": 1})
+    with pytest.raises(ValueError, match="gradient"):
+        api.rope(rotation, x, torch.zeros(2, dtype=torch.int32), out=torch.empty_like(x))

@@ -383,3 +383,77 @@ def test_append_then_decode_in_one_graph():
     ref = oracle.decode_attn(api.bf16_bits(q_out), api.bf16_bits(a.kc), api.bf16_bits(a.vc), tab,
                              np.asarray(lens, dtype=np.int32), D**-0.5)
     assert_within_tolerance(f64(out), ref, "append then decode")
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_gradient_by_autograd(layout):
+    """A tensor that requires a gradient gets the transposed map's, here through a slice of a fused projection; the
+    rotation is linear, so the gradient of the gradient is the rotation again."""
+    rope, freq, c = make(80, 40, layout, scaling="yarn", factor=8.0, original=2048)
+    pos = i32(np.arange(11) * 911)
+    row, g = randn(11, 5, 80, seed=5).requires_grad_(), randn(11, 3, 80, seed=6)
+    x = row[:, 1:4]
+    y = api.rope(rope, x, pos)
+    assert torch.equal(y, api.rope(rope, x.detach(), pos))
+    want = api.rope(rope, g, pos, inverse=True)
+    y.backward(g, retain_graph=True)
+    assert torch.equal(row.grad[:, 1:4], want) and not row.grad[:, [0, 4]].any()
+    ref, size = R.rotate(f64(g), np.arange(11) * 911, freq, c, layout, inverse=True)
+    check(row.grad[:, 1:4], ref, size)
+    # gradients that come broadcast, transposed, or 2 bytes off a 16-byte boundary
+    ones = torch.ones_like(g)
+    assert torch.equal(torch.autograd.grad(y.sum(), x, retain_graph=True)[0], api.rope(rope, ones, pos, inverse=True))
+    odd = torch.empty(g.numel() + 1, dtype=g.dtype, device=DEV)[1:].view_as(g).copy_(g)
+    turned = g.transpose(0, 2).contiguous().transpose(0, 2)
+    for same in (odd, turned):
+        assert torch.equal(torch.autograd.grad(y, x, same, retain_graph=True)[0], want)
+    # the inverse's gradient, and the second
+    assert torch.equal(torch.autograd.grad(api.rope(rope, x, pos, inverse=True), x, g)[0], api.rope(rope, g, pos))
+    h = g.clone().requires_grad_()
+    (back,) = torch.autograd.grad(y, x, h, create_graph=True)
+    assert torch.equal(torch.autograd.grad(back, h, g)[0], api.rope(rope, g, pos))
+    # by the difference quotient (R is linear: any step serves) of a sum in 64 bits, a column at a time
+    for col in (0, 19, 20, 39, 79):
+        e = np.zeros((11, 3, 80))
+        e[..., col] = 0.5
+        up, down = (R.rotate(f64(x) + s * e, np.arange(11) * 911, freq, c, layout)[0] for s in (1, -1))
+        diff = ((up - down) * f64(g)).sum(-1)
+        _, size = R.rotate(f64(g), np.arange(11) * 911, freq, c, layout)
+        assert np.all(np.abs(f64(row.grad)[:, 1:4, col] - diff) <= R.bf16_bound(diff, size[..., col] + 1e-6))
+
+
+def test_rope_gradient_streams_modes_and_graphs():
+    rope, *_ = make(64, 64)
+    x, g, pos = randn(40, 4, 64, seed=1).requires_grad_(), randn(40, 4, 64, seed=2), i32(range(40))
+    want = api.rope(rope, x.detach(), pos), api.rope(rope, g, pos, inverse=True)
+    with torch.no_grad():
+        assert not api.rope(rope, x, pos).requires_grad
+        out = torch.empty_like(g)
+        assert api.rope(rope, x, pos, out=out) is out and torch.equal(out, want[0])
+    with torch.inference_mode():
+        assert torch.equal(api.rope(rope, x, pos), want[0])
+    for bad in (torch.empty_like(g), x):
+        with pytest.raises(ValueError, match="gradient"):
+            api.rope(rope, x, pos, out=bad)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = api.rope(rope, x, pos, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, want[0]) and torch.equal(torch.autograd.grad(y, x, g)[0], want[1])
+    graph = torch.cuda.CUDAGraph()
+    leaf, got = x.detach().clone().requires_grad_(), None
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        y = api.rope(rope, leaf, pos)
+        (got,) = torch.autograd.grad(y, leaf, g)
+    for n in range(2):
+        with torch.no_grad():
+            leaf.copy_(randn(40, 4, 64, seed=7 + n))
+            g.copy_(randn(40, 4, 64, seed=17 + n))
+        graph.replay()
+        assert torch.equal(y, api.rope(rope, leaf.detach(), pos)) and torch.equal(got, api.rope(rope, g, pos, inverse=True))
+    pos2 = pos.clone()
+    y = api.rope(rope, x, pos2)
+    pos2.add_(1)
+    with pytest.raises(RuntimeError, match="modified"):  # the positions the gradient needs are gone
+        torch.autograd.grad(y, x, g)

@@ -436,8 +436,10 @@ int pd_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride, in
  * A token whose position is negative or beyond its block table raises
  * PD_DEV_BAD_CONTEXT_LEN and is left out (q_out too); one whose block id is
  * outside [0, num_blocks) raises PD_DEV_BAD_BLOCK_ID and its key and value are
- * left out.  Two tokens that name the same cache slot (tables that share a
- * block the batch writes) race for it: the caller keeps written blocks apart.
+ * left out.  Rows of q_out that get nothing keep what they held: where a decode
+ * reads them, its output for those rows, and no other, depends on it.  Two tokens
+ * that name the same cache slot (tables that share a block the batch writes) race
+ * for it: the caller keeps written blocks apart.
  * q, k, v, q_out and the caches are 16-B aligned.  Shape limits are
  * pd_decode_attn's.  Nothing is allocated.
  * Returns PD_OK, PD_ERR_INVALID, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */

@@ -237,7 +237,9 @@ def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, to
     v as they are, at the last positions of context_lens [S] (lengths after the append); q [T, Hq, D] (or
     None) rotated on the way and returned as q_out [T, Hq, D].  token_starts [S + 1] says which rows each
     sequence has; None: one each.  uint8 caches hold E4M3 codes of x / k_scale and x / v_scale.  Rows of no
-    sequence are left as they were, in q_out too.  A serving call: no gradient passes through it."""
+    sequence, a sequence of length 0 and a token without a place get nothing: a q_out that is given keeps what it
+    holds there, one made here holds anything (NaN among it), which reaches no other row of the attention; give a
+    zeroed q_out where such rows are read.  A serving call: no gradient passes through it."""
     if stream is None and q is not None:
         done = pd.quick().append_kv(pd._handle(rotation) or 0, 0 if rotation is None else rotation.head_dim, q, k, v, k_cache,
                                     v_cache, block_table, context_lens, token_starts, q_out, k_scale, v_scale)

@@ -416,3 +416,33 @@ def test_workspaces_elsewhere_are_refused():
             with pytest.raises(ValueError, match="ws"):
                 b.run(ws=ws, stream=stream)
         b.check(b.run(ws=torch.empty(n // 4 + 1, dtype=torch.float32, device=DEV), stream=stream))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_padded_batch_over_recycled_memory(D, fp8):
+    """Sequences of length 0 pad the batch: the append gives their rows nothing, so a q_out that it makes holds there what
+    its memory held, NaN here.  No other row's attention, behind a prefix or not, takes a bit of it."""
+    Hq, Hkv = 8, 2
+    for sizes in ([7], [70], [3, 4]):
+        S = sum(sizes)
+        lens = [0 if s % 3 == 1 else 1 + 40 * s % 290 for s in range(S)]
+        b = Batch(sizes, [333, 50][:len(sizes)], lens, Hq, Hkv, D, fp8=fp8, seed=13)
+        k, v = randn(S, Hkv, D, seed=3), randn(S, Hkv, D, seed=4)
+        table, own = i32(np.maximum(b.table, 0)), i32(lens)
+        args = (b.q, k, v, b.kc, b.vc, table, own)
+        more = dict(k_scale=b.k_scale, v_scale=b.v_scale)
+        zeroed = api.append_kv(None, *args, q_out=torch.zeros_like(b.q), **more)
+        pad = [s for s in range(S) if not lens[s]]
+        live = [s for s in range(S) if lens[s]]
+        assert not zeroed[pad].any() and torch.equal(zeroed[live], b.q[live])
+        for stream in (None, torch.cuda.current_stream()):
+            old = [torch.full_like(b.q, float("nan")) for _ in range(64)]
+            del old
+            q = api.append_kv(None, *args, stream=stream, **more)
+            assert torch.equal(q[live], b.q[live])
+            q[pad] = float("nan")  # (whatever memory it was)
+            for call in (lambda q: api.decode_attn_prefix(q, b.kc, b.vc, i32(b.ptable), i32(b.plens), i32(b.starts), table, own, b.scale, 3,
+                                                          **more),
+                         lambda q: api.decode_attn(q, b.kc, b.vc, table, own, b.scale, 2, **more)):
+                assert torch.equal(call(q)[live], call(zeroed)[live])

@@ -294,7 +294,7 @@ int pd_decode_attn_noalloc(const void *q, const void *k_cache, const void *v_cac
  * outside its table is clamped (PD_DEV_BAD_CONTEXT_LEN), a block id outside the
  * cache reads zeros (PD_DEV_BAD_BLOCK_ID).  Cache slots past a length may hold
  * anything.  The weights of prefix tokens are rounded to BF16 (f16 over an FP8
- * cache, where weights below 2^-14 of the row's largest are off by up to 2^-25
+ * cache, where weights below 2^-13 of the row's largest are off by up to 2^-24
  * of it) before they meet V.  The same call on the same data gives the same
  * bits; unlike pd_decode_attn's, they depend on the batch (how a prefix is cut
  * depends on every group).

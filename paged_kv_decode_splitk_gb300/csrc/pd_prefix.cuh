@@ -41,7 +41,9 @@
 //   * P is rounded to BF16 (half a step: 2^-9 to 2^-8 of each weight), the form
 //     the tensor core multiplies with a BF16 V; l sums the unrounded weights in
 //     FP32, S, O, m and l are FP32.  An FP8 cache is converted to f16 tiles
-//     (exactly), and P is f16 there (2^-12 to 2^-11).
+//     (exactly), and P is f16 there (2^-12 to 2^-11; a weight below 2^-14 is off by
+//     up to 2^-25, and as a raised reference may lie up to 1 above the largest score,
+//     the largest weight may be little more than a half: 2^-13 and 2^-24 of it).
 //
 // What bounds it, measured (8 KV heads, head dim 128, us per 1024 more prefix
 // tokens): 1024 rows 2.33, the tensor core (2.24 at the library product's rate); 128

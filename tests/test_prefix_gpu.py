@@ -446,3 +446,30 @@ def test_padded_batch_over_recycled_memory(D, fp8):
                                                           **more),
                          lambda q: api.decode_attn(q, b.kc, b.vc, table, own, b.scale, 2, **more)):
                 assert torch.equal(call(q)[live], call(zeroed)[live])
+
+
+def test_prefix_fp8_small_weights():
+    """f16 weights below 2^-14 are off by up to half of 2^-24, against a reference m that a raise leaves up to 1 above the
+    largest score: up to 2^-24 of the largest weight.  One key in tile 1 lifts m from 0 to 16 and scores 15.0625; the one
+    key whose value is not 0 scores -7.4140625, 1.501 units of 2^-24 below 2^16, which round to 2.  (Scores in powers of
+    two, and exact: keys of two terms.)"""
+    b = Batch([40], [8192], [0] * 40, 8, 1, 64, fp8=True, seed=1, poison=False)
+    b.k_scale = b.v_scale = 1.0
+    b.scale = math.log(2)
+    b.q.zero_()
+    b.q[:, :, :2] = 1
+    k, v = torch.zeros(8192, 64, device=DEV), torch.zeros(8192, 64, device=DEV)
+    k[128:, 0] = -16
+    k[130, 0], k[130, 1] = 15, 0.0625
+    k[200, 0], k[200, 1] = -7.5, 0.0859375
+    v[200] = 448
+    for cache, x in ((b.kc, k), (b.vc, v)):
+        codes = x.to(torch.float8_e4m3fn)
+        assert torch.equal(codes.float(), x)
+        cache[torch.tensor(b.rows[0], device=DEV)] = codes.view(torch.uint8).view(-1, 16, 1, 64)
+    got = b.run(splits=1).double()
+    w = torch.exp2(k[:, :2].double().sum(1))
+    ref = float(w[200] / w.sum() * 448)
+    assert bool(torch.isfinite(got).all())
+    # (and the output's rounding, 2^-8 of up to 2 / 1.5 of ref, beside which the FP32 sums are nothing)
+    assert float((got - ref).abs().max()) <= 2.0**-24 * float(w.max() / w.sum()) * 448 + 2.0**-8 * 1.5 * ref  # found: 2^-24.06 of the largest

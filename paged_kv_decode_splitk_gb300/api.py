@@ -236,7 +236,7 @@ def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, to
     """Append new tokens to the paged cache: k [T, Hkv, D] rotated (rotation: a pd.Rope, or None for none) and
     v as they are, at the last positions of context_lens [S] (lengths after the append); q [T, Hq, D] (or
     None) rotated on the way and returned as q_out [T, Hq, D].  token_starts [S + 1] says which rows each
-    sequence has; None: one each.  uint8 caches hold E4M3 codes of x / k_scale and x / v_scale.  Rows of no
+    sequence has; None: one each.  uint8 caches hold E4M3 codes of x * (1 / k_scale) and x * (1 / v_scale).  Rows of no
     sequence, a sequence of length 0 and a token without a place get nothing: a q_out that is given keeps what it
     holds there, one made here holds anything (NaN among it), which reaches no other row of the attention; give a
     zeroed q_out where such rows are read.  A serving call: no gradient passes through it."""

@@ -541,7 +541,7 @@ def pd_append_kv(rope, q, k, v, q_out, k_cache, v_cache, block_table, context_le
 
 def pd_append_kv_fp8(rope, q, k, v, q_out, k_cache, v_cache, k_scale: float, v_scale: float, block_table, context_lens,
                      token_starts=None, stream=None, num_blocks: int | None = None) -> int:
-    """pd_append_kv into an FP8 cache (uint8 E4M3 codes of x / k_scale and x / v_scale)."""
+    """pd_append_kv into an FP8 cache (uint8 E4M3 codes of x * (1 / k_scale) and x * (1 / v_scale))."""
     T, Hkv, D = k.shape
     nb, bs = k_cache.shape[:2]
     S, mb = block_table.shape

@@ -457,3 +457,17 @@ def test_rope_gradient_streams_modes_and_graphs():
     pos2.add_(1)
     with pytest.raises(RuntimeError, match="modified"):  # the positions the gradient needs are gone
         torch.autograd.grad(y, x, g)
+
+
+@pytest.mark.parametrize("scales", [(0.011, 0.0125), (3.0, 0.75), (0.3, 1e-3), (2.0**-9, 7.0)])
+def test_append_fp8_codes(scales):
+    """The codes of copied rows, bit for bit: x times the FP32 reciprocal of the scale, in FP32, to the nearest E4M3 value."""
+    a = Append([40, 1, 17], [3, 200, 0], 4, 2, 64, fp8=True, seed=21)
+    a.k_scale, a.v_scale = scales
+    a.run(None)
+    rows, cells = zip(*((r, (int(a.table[s, p // a.bs]), p % a.bs)) for r, s, p in a.tokens()))
+    at = tuple(torch.tensor(c, device=DEV) for c in zip(*cells))
+    for cache, x, scale in ((a.kc, a.k, a.k_scale), (a.vc, a.v, a.v_scale)):
+        reciprocal = float(np.float32(1) / np.float32(scale))
+        want = (x[list(rows)].float() * reciprocal).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(cache[at], want)

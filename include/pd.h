@@ -582,12 +582,31 @@ int pd_device_status(int *flags);
 /* ---- test hooks ----
  * Not part of the decode interface: the test suite and launch-shape
  * experiments use them.  A program that serves decode steps never needs to
- * call either. */
+ * call any. */
 
 /* TEST HOOK.  Make the next `count` device allocations of pd_tiled_create
  * (state m, l, o, then the run partials) and pd_rope_create (the table) fail as
  * if the device were out of memory (host-side fault injection). */
 void pd_debug_fail_next_allocs(int count);
+
+/* TEST HOOK.  How pd_decode_attn_prefix divides a call's work, worked out on the
+ * host by the functions that its kernels run (no CUDA): group_starts and
+ * prefix_lens in host memory, own_us the time the own tokens are taken to need on
+ * one SM, max_teams teams of two CTAs at most (1..76).
+ *   segments  [max_segments, 10]: team, CTA of the team, group, KV head, first row
+ *             (of the group's sequences x query heads of a KV head), rows, first
+ *             tile, step from tile to tile, tiles, slot of the partials.
+ *   parts     [sum over groups of num_kv_heads x rows, 3]: the partials that the
+ *             merge reads for each: how many, slots from one to the next, and the
+ *             first as slot x block rows + row.
+ *   totals    teams, units of a team at most where items have whole teams (else
+ *             0), block rows, tokens of a tile.
+ * Returns PD_OK, PD_ERR_INVALID, PD_ERR_UNSUPPORTED, PD_ERR_ALLOC, or
+ * PD_ERR_CAPACITY for more than max_segments segments. */
+int pd_debug_prefix_walk(int num_seqs, int num_groups, const int32_t *group_starts,
+                         const int32_t *prefix_lens, int num_q_heads, int num_kv_heads, int head_dim,
+                         int fp8, float own_us, int max_teams, int32_t *segments, int max_segments,
+                         int *num_segments, int64_t *parts, int32_t *totals);
 
 /* TEST HOOK.  Tuning for launch-shape experiments, applied to the following launches
  * in this process: pipeline stages per warp (1..8; 0 = built-in), where the

@@ -8,11 +8,12 @@
 #include <cfloat>
 #include <cmath>
 #include <mutex>
+#include <vector>
 
 #include "pd.h"
 #include "pd_device.cuh"
 #include "pd_internal.h"
-#include "pd_prefix.h"
+#include "pd_prefix_plan.h"
 
 namespace pd {
 namespace prefix {
@@ -23,14 +24,6 @@ static_assert(kMaxGroups == PD_MAX_PREFIX_GROUPS, "pd.h");
 constexpr int kOwnUnits = 152 * 8;  // units of the own-token pass that are enough
 constexpr int kMergeWarps = 8;
 constexpr int kMergeBatch = 4;   // partials whose o are loaded together
-
-// The team whose range [W c / C, W (c + 1) / C) holds unit u.
-__device__ __forceinline__ int team_of_unit(long long u, int C, long long W) {
-    const long long num = (u + 1) * C - 1;
-    if (num < 0x7fffffffLL)
-        return static_cast<int>(static_cast<unsigned>(num) / static_cast<unsigned>(W));
-    return static_cast<int>(num / W);
-}
 
 // DPAD / 8 lanes per (sequence, query head), 8 columns each, fold the row's
 // partials: first those of its prefix, in the order of the teams that made them
@@ -89,33 +82,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) prefix_merge_kernel(const
         f.last_teams = __shfl_sync(0xffffffffu, one.last_teams, src);
         if (below > 0) g = f;
     }
-    int nparts = 0, step = 2;      // prefix slots of the row, 2 apart, or (both CTAs') 1
-    long long first = 0;           // (slot, row) of its first partial
+    RowParts of = {0, 2, 0};
     const int x = (s - g.first_seq) * p.group + (h - kvh * p.group);
-    const bool has = W > 0 && in && g.tiles > 0 && x < g.rows;
-    {
-        constexpr int IR = item_rows(DPAD);
-        const int item = has ? x / IR : 0, r = x - item * IR;
-        const int of_item = min(IR, g.rows - item * IR), half = (of_item + 1) >> 1;
-        const bool pair = is_pair(of_item, IR);
-        const int places = pair ? g.tiles : (g.tiles + 1) >> 1;
-        const long long u = g.first_unit + kvh * g.head_units(IR) + static_cast<long long>(item) * g.tiles;
-        const int C = plan.teams;
+    if (const bool has = W > 0 && in && g.tiles > 0 && x < g.rows; __any_sync(0xffffffffu, has)) {
+        const RowPlace at = place_of<DPAD>(g, kvh, has ? x : 0);
         int c0, c1;
         if (plan.whole) {
-            c0 = g.first_team + kvh * ((g.items - 1) * g.teams + g.last_teams) + item * g.teams;
-            c1 = c0 + (item == g.items - 1 ? g.last_teams : g.teams) - 1;
+            whole_teams_of(g, kvh, at.item, c0, c1);
         } else {
-            const int c = has ? team_of_unit(sub == 0 ? u : u + places - 1, C, W) : 0;
+            const int c = has ? team_of_unit(sub == 0 ? at.u0 : at.u1, plan.teams, W) : 0;
             c0 = __shfl_sync(0xffffffffu, c, head_lane), c1 = __shfl_sync(0xffffffffu, c, head_lane + 1);
         }
-        if (has) {
-            const int second = pair && r >= half;
-            step = pair ? 2 : 1;
-            nparts = (c1 - c0 + 1) * (pair ? 1 : 2);
-            first = (2ll * (g.first_item + kvh * g.items + item + c0) + second) * BR + (second ? r - half : r);
-        }
+        if (has) of = parts_of<DPAD>(g, kvh, at, c0, c1);
     }
+    const int nparts = of.parts, step = of.step;
+    const long long first = of.first;  // (slot, row) of its first partial
     L = L < 0 ? 0 : (L > p.max_tokens ? p.max_tokens : L);
     const int chunk = split_chunk_tokens_fd(L, p.fd_split, p.fd_bs, p.min_kv_per_split);
     // (this line's share: partials way, way + ways, ...)
@@ -424,11 +405,115 @@ int decode_prefix_impl(const char *what, const void *q, const void *k_cache, con
     return report_ok();
 }
 
+// The division of a call's work as the prefix pass and the merge work it out.
+template <int DPAD, bool KV8>
+int walk(int num_seqs, int num_groups, const int32_t *group_starts, const int32_t *prefix_lens, int group, int num_kv_heads, float own_us,
+         int most, int32_t *segments, int max_segments, int *num_segments, int64_t *parts, int32_t *totals) {
+    constexpr int IR = item_rows(DPAD);
+    std::vector<GroupPlan> grp(num_groups);
+    long long W = 0;
+    int items = 0;
+    float time = 0.f;
+    for (int g = 0; g < num_groups; ++g) {
+        const int a = group_starts[g], b = group_starts[g + 1];
+        if (a < 0 || b < a || b > num_seqs || prefix_lens[g] < 0) return report(PD_ERR_INVALID, "pd_debug_prefix_walk: group %d", g);
+        GroupPlan r = plan_of<DPAD>(a, (b - a) * group, prefix_lens[g]);
+        r.first_unit = W;
+        r.first_item = items;
+        if (r.tiles > 0 && r.items > 0) {
+            const long long units = r.head_units(IR) * num_kv_heads;
+            W += units;
+            items += r.items * num_kv_heads;
+            time += units * unit_time<DPAD, KV8>(std::min(r.rows, IR));
+        }
+        grp[g] = r;
+    }
+    int C = 0, run = 0;
+    if (W > 0 && num_groups == 1) {
+        C = share_units(W, items, grp[0].last_units(IR) == quotient(W, items), time, own_us, most);
+    } else if (W > 0) {
+        C = share_units(W, items, false, time, own_us, most);
+        WholeTry t;
+        if (try_whole(num_groups, W, C, most, items, t)) {
+            int lane = 0;
+            while (lane < 32 && teams_in_all(grp.data(), num_groups, num_kv_heads, IR, t.run(lane)) > t.limit) ++lane;
+            if (lane < 32 && whole_pays(t, t.run(lane), quick_quotient(time, static_cast<float>(W)), KV8 ? 6.f : 3.f)) {
+                run = t.run(lane);
+                C = teams_in_all(grp.data(), num_groups, num_kv_heads, IR, run);
+            }
+        }
+    }
+    int n = 0;
+    for (int team = 0; team < C; ++team)
+        for (int rank = 0; rank < 2; ++rank) {
+            long long u = 0, u1 = 0;
+            if (run > 0)
+                whole_range(grp.data(), num_kv_heads, IR, run, team, u, u1);
+            else
+                line_range(W, C, team, u, u1);
+            Segment s;
+            while (next_segment<block_rows(DPAD)>(grp.data(), num_groups, u, u1, team, rank, s)) {
+                if (n == max_segments) return report(PD_ERR_CAPACITY, "pd_debug_prefix_walk: more than %d segments", n);
+                const int32_t v[10] = {team, rank, s.group, s.kvh, s.row0, s.rows, s.tile0, s.stride, s.n, s.slot};
+                std::copy(v, v + 10, segments + 10ll * n++);
+            }
+        }
+    *num_segments = n;
+    // the merge's side: of each group, KV head and row
+    for (int g = 0; g < num_groups; ++g) {
+        GroupPlan r = grp[g];
+        if (num_groups > 1) plan_whole(grp.data(), g, num_kv_heads, IR, run, r);
+        for (int kvh = 0; kvh < num_kv_heads; ++kvh)
+            for (int x = 0; x < r.rows; ++x, parts += 3) {
+                RowParts v = {0, 2, 0};
+                if (W > 0 && r.tiles > 0) {
+                    const RowPlace at = place_of<DPAD>(r, kvh, x);
+                    int c0, c1;
+                    if (run > 0) {
+                        whole_teams_of(r, kvh, at.item, c0, c1);
+                    } else {
+                        c0 = team_of_unit(at.u0, C, W);
+                        c1 = team_of_unit(at.u1, C, W);
+                    }
+                    v = parts_of<DPAD>(r, kvh, at, c0, c1);
+                }
+                parts[0] = v.parts;
+                parts[1] = v.step;
+                parts[2] = v.first;
+            }
+    }
+    totals[0] = C;
+    totals[1] = run;
+    totals[2] = block_rows(DPAD);
+    totals[3] = tile_tokens(DPAD);
+    return report_ok();
+}
+
 }  // namespace
 }  // namespace prefix
 }  // namespace pd
 
 extern "C" {
+
+int pd_debug_prefix_walk(int num_seqs, int num_groups, const int32_t *group_starts, const int32_t *prefix_lens, int num_q_heads,
+                         int num_kv_heads, int head_dim, int fp8, float own_us, int max_teams, int32_t *segments,
+                         int max_segments, int *num_segments, int64_t *parts, int32_t *totals) {
+    using namespace pd::prefix;
+    const int rc = pd::check_shape(num_q_heads, num_kv_heads, head_dim, 16);
+    if (rc != PD_OK) return rc;
+    if (num_seqs < 0 || num_groups < 1 || num_groups > kMaxGroups || max_teams < 1 || max_teams > kMaxTeams || max_segments < 0 ||
+        !group_starts || !prefix_lens || !segments || !num_segments || !parts || !totals)
+        return pd::report(PD_ERR_INVALID, "pd_debug_prefix_walk: an argument is out of range or null");
+    const int dpad = dpad_of(head_dim);
+    try {
+        const auto f = dpad == 64 ? (fp8 ? walk<64, true> : walk<64, false>) : dpad == 128 ? (fp8 ? walk<128, true> : walk<128, false>)
+                                                                                           : (fp8 ? walk<256, true> : walk<256, false>);
+        return f(num_seqs, num_groups, group_starts, prefix_lens, num_q_heads / num_kv_heads, num_kv_heads, own_us, max_teams, segments,
+                 max_segments, num_segments, parts, totals);
+    } catch (...) {  // (nothing but the host's memory can run out)
+        return pd::report(PD_ERR_ALLOC, "pd_debug_prefix_walk: out of host memory");
+    }
+}
 
 size_t pd_prefix_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
                                  int num_splits) {

@@ -60,13 +60,12 @@
 
 #include "pd.h"
 #include "pd_device.cuh"
-#include "pd_prefix.h"
+#include "pd_prefix_plan.h"
 #include "pd_tcgen05.cuh"
 
 namespace pd {
 namespace prefix {
 
-constexpr int kRowTile = 128;   // rows of one MMA
 constexpr int kRegionBars = 32;
 constexpr int kConverters = 64;  // threads that turn FP8 tiles into f16 ones
 
@@ -93,165 +92,20 @@ struct Plan {
     static constexpr int kThreads = 384;
 };
 
-// The block of rows and the run of tiles a CTA works on at a time.
-struct Segment {
-    int kvh, plen, slot;
-    int tile0, stride;  // tile j of the run is tile0 + j stride
-    int n;      // tiles of the run (0: the last place of an item taken in turn has but one, the other CTA's)
-    int row0;   // first row of this CTA within the group
-    int rows;   // rows of this CTA
-    int seq0;   // the group's first sequence
-    int group;
-    bool two;   // more than kRowTile rows: both streams use every tile
-    bool pair;  // both CTAs use the same tiles, half of the rows each
-};
 
-// a / b, in 32 bits where both fit (a fifth of the instructions).
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-    if ((a | b) >> 32 == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-    return a / b;
-}
-
-template <int BR>
-__device__ __forceinline__ bool next_segment(const GroupPlan *grp, int num_groups, long long &u, long long u1,
-                                             int team, int rank, Segment &s) {
-    if (u >= u1) return false;
-    int lo = 0, n = num_groups;  // the last group that begins at or before unit u
-    while (n > 1) {
-        const int half = n >> 1;
-        if (grp[lo + half].first_unit <= u) {
-            lo += half;
-            n -= half;
-        } else {
-            n = half;
-        }
-    }
-    const GroupPlan g = grp[lo];
-    const long long per_head = g.head_units(2 * BR);
-    const long long local = u - g.first_unit;
-    s.kvh = static_cast<int>(quotient(local, per_head));
-    const long long rem = local - s.kvh * per_head;
-    const int item = static_cast<int>(quotient(rem, g.tiles));  // (the last item may have fewer units, never more)
-    const int at = static_cast<int>(rem - static_cast<long long>(item) * g.tiles);  // place within the item
-    const int rows = min(2 * BR, g.rows - item * 2 * BR);
-    s.pair = is_pair(rows, 2 * BR);
-    const int places = s.pair ? g.tiles : (g.tiles + 1) >> 1;
-    const long long left = u1 - u;
-    const int taken = left < places - at ? static_cast<int>(left) : places - at;  // of them
-    s.stride = s.pair ? 1 : 2;
-    s.tile0 = s.pair ? at : 2 * at + rank;
-    s.n = s.tile0 + (taken - 1) * s.stride < g.tiles ? taken : taken - 1;
-    const int half = (rows + 1) >> 1;
-    s.row0 = item * 2 * BR + (s.pair && rank ? half : 0);
-    s.rows = !s.pair ? rows : rank ? rows - half : half;
-    s.plen = g.tokens;
-    s.seq0 = g.first_seq;
-    s.group = lo;
-    s.slot = 2 * (g.first_item + s.kvh * g.items + item + team) + rank;
-    s.two = s.rows > kRowTile;
-    if (taken < 1) return false;  // (never; the walk over the units ends all the same)
-    u += taken;
-    return true;
-}
-
-// How many teams share the prefixes' units.  The own-token pass runs on the SMs
-// the prefix pass leaves, and the step is shortest where both end together: with
-// n SMs, C teams, units (and the start and end of items) of B us in all and U the
-// own pass's time on one SM,
-//   B / C = U / (n - 2 C).
-// Of U's loads half is taken, since teams too few cost more than teams too many,
-// but at least what its units cost when they have next to no tokens: where all SMs
-// went to the prefixes the own pass began 4 us before the end, at theirs.  Measured
-// (us, all 76 teams -> about as many as this gives): 64 sequences behind 8192
-// tokens 47.3 -> 41.2 (24 teams; 16: 52.1), 256 behind 32768 136 -> 124 (60), six
-// groups of wide heads 32.3 -> 30.7 (48), 32 behind 16385 over FP8 51.3 -> 46.9
-// (48).  A team has four units or more beyond the first eight teams, or an item: each is a
-// partial more of all its rows to write and fold (256 units without own tokens:
-// 19.7 us on 76 teams, 17.0 on 32).  Where the items have as many units each
-// (`even`) and there are teams enough, a count that gives every item whole teams
-// spares those that would end one item and begin the next (256 units of 8 items
-// over FP8: 21.5 us on 64 teams, 26.7 on 60), if it is near or costs less than that.
-__device__ __forceinline__ int share_units(long long units, int items, bool even, float units_us, float own_us, int most) {
-    constexpr float item_us = 3.f;  // to begin and end an item
-    const float all_us = units_us + item_us * items;
-    const long long enough = max((units + 3) / 4, min(units, max(8ll, static_cast<long long>(items))));
-    int c = static_cast<int>(ceilf(__fdividef(2.f * most * all_us, own_us + 2.f * all_us)));
-    c = static_cast<int>(max(1ll, min(enough, static_cast<long long>(min(c, most)))));
-    if (even && c >= items) {
-        const int down = c - static_cast<int>(static_cast<unsigned>(c) % static_cast<unsigned>(items)), up = down + items;
-        if (down != c && up <= most && 16 * up <= 17 * c)
-            c = up;
-        else if (units_us * (c - down) <= item_us * static_cast<float>(c) * down)
-            c = down;
-    }
-    return c;
-}
-
-// Teams of an item with at most about `run` units each (no more than it has units).
-__device__ __forceinline__ int teams_of(int units, int run) {
-    return max(1, static_cast<int>(ceilf(__fmaf_rn(static_cast<float>(units), __fdividef(1.f, static_cast<float>(run)), -1e-3f))));
-}
-__device__ __forceinline__ int head_teams(const GroupPlan &g, int of_item, int run) {
-    return g.tiles && g.items ? (g.items - 1) * teams_of(g.tiles, run) + teams_of(g.last_units(of_item), run) : 0;
-}
-// a / b of whole numbers from 0 and 1 to 255
-__device__ __forceinline__ int small_quotient(int a, int b) {
-    return static_cast<int>((static_cast<float>(a) + 0.5f) * __fdividef(1.f, static_cast<float>(b)));
-}
-
-// Whole teams for every item, where there are teams enough: a team that ends one
-// item and begins the next spends 3 us on that (6 over FP8, where the ring of
-// converted tiles fills anew), often more than its share of units is worth (three
-// groups of wide FP8 heads 30.3 us on 52 teams in one line, 22 on 44 or 56 that
-// happen to end with the items; 256 units of 8 items 18.3 on 48 teams, 23 on 44).
-// The warp's lanes try the most units of a team, from the line's share on; the
-// least with no more than about c teams is taken if it costs no more than that.
-// Returns it (0: one line) and the teams.  Where teams have a unit each, the line
-// has whole teams already.
+// The most units of a team with whole teams for every item, by one warp (0: one line
+// is better), and the teams then.
 __device__ __forceinline__ int whole_teams(const GroupPlan *grp, int num_groups, int kv_heads, int of_item, long long units, int &c,
                                            int most, int items, float unit_us, float item_us, int lane) {
-    const int limit = min(most, c + c / 16);
-    if (units <= c || items > limit || num_groups > 32) return 0;
-    const float even = __fdividef(static_cast<float>(units), static_cast<float>(c));
-    const int share = static_cast<int>(ceilf(even)), run = share + lane * ((share + 15) / 16);
-    int teams = 0;
-    for (int g = 0; g < num_groups; ++g) teams += kv_heads * head_teams(grp[g], of_item, run);
-    const unsigned fits = __ballot_sync(0xffffffffu, teams <= limit);
+    WholeTry t;
+    if (!try_whole(num_groups, units, c, most, items, t)) return 0;
+    const int run = t.run(lane), teams = teams_in_all(grp, num_groups, kv_heads, of_item, run);
+    const unsigned fits = __ballot_sync(0xffffffffu, teams <= t.limit);
     if (!fits) return 0;
     const int best = __ffs(fits) - 1, least = __shfl_sync(0xffffffffu, run, best), n = __shfl_sync(0xffffffffu, teams, best);
-    if ((static_cast<float>(least) - even) * unit_us > item_us) return 0;
+    if (!whole_pays(t, least, unit_us, item_us)) return 0;
     c = n;
     return least;
-}
-
-// The units of a team where items have whole teams.
-__device__ __forceinline__ void whole_range(const GroupPlan *grp, int kv_heads, int of_item, int run, int team, long long &u,
-                                            long long &u1) {
-    int g = 0, n;
-    while (team >= (n = kv_heads * head_teams(grp[g], of_item, run))) {
-        team -= n;
-        ++g;
-    }
-    const GroupPlan r = grp[g];
-    const int last = r.last_units(of_item), of_last = teams_of(last, run);
-    const int of_one = r.items > 1 ? teams_of(r.tiles, run) : of_last, head = (r.items - 1) * of_one + of_last;
-    const int kvh = small_quotient(team, head), at = team - kvh * head;
-    const int item = min(small_quotient(at, of_one), r.items - 1);
-    const bool ends = item == r.items - 1;
-    // even shares, the first ones a unit longer
-    const int part = at - item * of_one, places = ends ? last : r.tiles, teams = ends ? of_last : of_one;
-    const int least = places / teams, longer = places - least * teams;
-    u = r.first_unit + kvh * r.head_units(of_item) + static_cast<long long>(item) * r.tiles + least * part + min(part, longer);
-    u1 = u + least + (part < longer);
-}
-
-// The time of a unit on a team, measured (us): the conversion bounds an FP8 tile;
-// two full row tiles of products a pair's; one, and memory, the others'.
-template <int DPAD, bool KV8>
-__device__ __forceinline__ float unit_time(int rows) {
-    const bool pair = is_pair(rows, item_rows(DPAD));
-    const float us = KV8 || (!pair && rows > kRowTile) ? 1.6f : pair ? (DPAD == 256 ? 0.9f : 1.4f) : DPAD == 256 ? 1.f : 1.3f;
-    return DPAD == 64 ? (KV8 ? 0.8f : 0.6f) * us : us;
 }
 
 // The groups' units and items, by one warp: running sums over chunks of 32
@@ -279,11 +133,7 @@ __device__ __forceinline__ void plan_groups(const PrefixParams &p, GroupPlan *gr
                 len = len < 0 ? 0 : most;
             }
             bad |= a < 0 || b < a || b > p.num_seqs;
-            r.first_seq = a;
-            r.rows = bad ? 0 : (b - a) * p.group;
-            r.items = (r.rows + item_rows(DPAD) - 1) / item_rows(DPAD);
-            r.tokens = len;
-            r.tiles = (len + tile_tokens(DPAD) - 1) / tile_tokens(DPAD);
+            r = plan_of<DPAD>(a, bad ? 0 : (b - a) * p.group, len);
             if (r.tiles > 0 && r.items > 0) {
                 it = r.items * p.num_kv_heads;
                 mine = r.head_units(item_rows(DPAD)) * p.num_kv_heads;
@@ -536,10 +386,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             *p.plan_total = {W, C, 0};
             p.plan_groups[0] = grp[0];
         }
-        if (team < C) {
-            u = quotient(W * team, C);
-            u1 = quotient(W * (team + 1), C);
-        }
+        if (team < C) line_range(W, C, team, u, u1);
     } else {
         if (warp == 0) {  // (by one warp: twelve would share the issue slots)
             int run = 0;
@@ -547,12 +394,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 C = share_units(W, *items_s, false, *time_s, own_us, gridDim.x / 2);
                 run = whole_teams(grp, p.num_groups, p.num_kv_heads, item_rows(DPAD), W, C, gridDim.x / 2, *items_s,
                                   __fdividef(*time_s, static_cast<float>(W)), KV8 ? 6.f : 3.f, lane);
-                if (team < C && run > 0) {
+                if (team < C && run > 0)
                     whole_range(grp, p.num_kv_heads, item_rows(DPAD), run, team, u, u1);
-                } else if (team < C) {
-                    u = quotient(W * team, C);
-                    u1 = quotient(W * (team + 1), C);
-                }
+                else if (team < C)
+                    line_range(W, C, team, u, u1);
             }
             if (lane == 0) {
                 range_s[0] = u;
@@ -570,12 +415,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             if (lane == 0) *p.plan_total = {W, C, run > 0};
             for (int g = lane; g < p.num_groups; g += 32) {
                 GroupPlan r = grp[g];
-                r.first_team = r.teams = r.last_teams = 0;
-                if (run > 0) {
-                    for (int k = 0; k < g; ++k) r.first_team += p.num_kv_heads * head_teams(grp[k], item_rows(DPAD), run);
-                    r.teams = teams_of(r.tiles, run);
-                    r.last_teams = teams_of(r.last_units(item_rows(DPAD)), run);
-                }
+                plan_whole(grp, g, p.num_kv_heads, item_rows(DPAD), run, r);
                 p.plan_groups[g] = r;
             }
             __syncwarp();

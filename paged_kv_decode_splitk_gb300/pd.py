@@ -124,6 +124,7 @@ _SIGS = {
                                    ctypes.c_float, _I, _VP, _SZ, _VP]),
     "pd_decode_attn_prefix_fp8": (_I, [_VP, _VP, _VP, ctypes.c_float, ctypes.c_float, _VP, _I, _VP, _VP, _I, _VP, _I, _VP,
                                        _VP, _I, _I, _I, _I, _I, _I, ctypes.c_float, _I, _VP, _SZ, _VP]),
+    "pd_debug_prefix_walk": (_I, [_I, _I, _VP, _VP, _I, _I, _I, _I, ctypes.c_float, _I, _VP, _I, _VP, _VP, _VP]),
     "pd_rope_frequencies": (_I, [_VP, _VP, _VP]),
     "pd_rope_create": (_I, [_VP, _VP]),
     "pd_rope_destroy": (None, [_VP]),
@@ -434,6 +435,21 @@ def pd_decode_attn_prefix_fp8(q, k_cache, v_cache, k_scale: float, v_scale: floa
         prefix_lens.data_ptr(), _ptr(group_starts), G, block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
         out.data_ptr(), S, Hq, Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d, num_splits, _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def pd_debug_prefix_walk(group_starts, prefix_lens, num_q_heads: int, num_kv_heads: int, head_dim: int, fp8: bool = False,
+                         own_us: float = 0.0, max_teams: int = 76):
+    """The division of a shared-prefix call's work (see pd.h): (segments, parts, totals), lists of tuples and a tuple."""
+    G, group = len(prefix_lens), num_q_heads // num_kv_heads
+    rows = [(b - a) * group for a, b in zip(group_starts, group_starts[1:])]
+    starts, lens = (ctypes.c_int32 * (G + 1))(*group_starts), (ctypes.c_int32 * G)(*prefix_lens)
+    most = 4 * max_teams + 2 * sum(num_kv_heads * (r // 128 + 1) for r in rows)  # (a team's run ends an item, or ends itself)
+    segments, n = (ctypes.c_int32 * (10 * most))(), ctypes.c_int()
+    parts, totals = (ctypes.c_int64 * (3 * num_kv_heads * max(1, sum(rows))))(), (ctypes.c_int32 * 4)()
+    _check(lib().pd_debug_prefix_walk(group_starts[-1], G, starts, lens, num_q_heads, num_kv_heads, head_dim, int(fp8), own_us, max_teams,
+                                      segments, most, ctypes.byref(n), parts, totals))
+    return ([tuple(segments[10 * i:10 * i + 10]) for i in range(n.value)],
+            [tuple(parts[3 * i:3 * i + 3]) for i in range(num_kv_heads * sum(rows))], tuple(totals))
 
 
 # ---- rotary positions and the append to the paged cache ------------------------------

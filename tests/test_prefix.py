@@ -164,3 +164,92 @@ def test_api_refuses_workspaces():
     here = type("T", (), {"get_device": lambda self: 0, "is_contiguous": lambda self: True, "device": "cuda:0"})
     with pytest.raises(ValueError, match="ws"):
         api._check_prefix(*args, here(), -1)
+
+
+def _check_walk(segments, parts, totals, starts, plens, G, Hkv, limit):
+    """Every (group, KV head, row, tile) is one CTA's, no two runs share a slot, and the merge of a row reads the partials of
+    exactly the runs that had it."""
+    teams, _, BR, tile = totals
+    slots = [s[9] for s in segments]
+    assert len(set(slots)) == len(slots) and (not slots or max(slots) < limit)
+    runs = {}
+    for team, rank, g, kvh, row0, rows, tile0, stride, n, slot in segments:
+        assert 0 <= team < teams and rank in (0, 1) and 0 < rows <= BR and n >= 0 and (stride, n > 0 or rank == 1) in ((1, True), (2, True))
+        runs.setdefault((g, kvh), []).append((row0, rows, range(tile0, tile0 + n * stride, stride), slot))
+    at = iter(parts)
+    for g, plen in enumerate(plens):
+        rows, tiles = (starts[g + 1] - starts[g]) * G, -(-plen // tile)
+        for kvh in range(Hkv):
+            mine = runs.pop((g, kvh), [])
+            for x in range(rows):
+                count, step, first = next(at)
+                own = [r for r in mine if r[0] <= x < r[0] + r[1]]
+                assert sorted(t for r in own for t in r[2]) == list(range(tiles))
+                assert sorted(first + i * step * BR for i in range(count)) == sorted(r[3] * BR + x - r[0] for r in own)
+            assert all(r[0] + r[1] <= rows for r in mine)
+    assert not runs and next(at, None) is None
+
+
+def _draw_walk(rng):
+    G, Hkv, D = rng.choice([1, 2, 3, 4, 7, 8, 16]), rng.choice([1, 2, 8]), rng.choice([64, 128, 256])
+    n = rng.choice([1, 1, 2, 5, 40])
+    sizes = [rng.choice([0, 1, 2, 5, 20, 33, 40, 64][:8 if n < 40 else 4]) for _ in range(n)]
+    plens = [rng.choice([0, 1, 17, 64, 100, 128, 129, 700, 3000, 200000]) for _ in range(n)]
+    starts = [sum(sizes[:i]) for i in range(n + 1)]
+    more = dict(fp8=rng.random() < 0.5, own_us=rng.choice([0.0, 30.0, 1e3, 1e5, 1e9]), max_teams=rng.choice([1, 3, 24, 76, 76]))
+    return starts, plens, G, Hkv, D, more
+
+
+def test_division_that_the_kernels_run():
+    """pd_debug_prefix_walk runs the functions of the pass and the merge on the host."""
+    kinds = set()
+    for seed in range(8):
+        rng = random.Random(seed)
+        for _ in range(40):
+            starts, plens, G, Hkv, D, more = _draw_walk(rng)
+            segments, parts, totals = pd.pd_debug_prefix_walk(starts, plens, G * Hkv, Hkv, D, **more)
+            assert totals[0] <= more["max_teams"]
+            items = Hkv * (len(plens) + starts[-1] * G // (2 * totals[2]))  # what the workspace is sized for
+            _check_walk(segments, parts, totals, starts, plens, G, Hkv, 2 * (items + 76))
+            kinds |= {(len(plens) > 1, totals[1] > 0, s[7], s[8] == 0) for s in segments}
+    # one line and whole teams, rows in halves and tiles in turn, places without a tile
+    assert {(False, False, 1, False), (False, False, 2, False), (False, False, 2, True), (True, False, 1, False), (True, True, 1, False),
+            (True, True, 2, False), (True, True, 2, True)} <= kinds
+
+
+def test_division_check_sees_mistakes():
+    """The check itself, on divisions with one mistake each."""
+    starts, plens = [0, 70, 71], [900, 129]
+    segments, parts, totals = pd.pd_debug_prefix_walk(starts, plens, 8, 2, 128)
+
+    def check(s, p):
+        _check_walk(s, p, totals, starts, plens, 4, 2, 2 * (2 * (2 + 71 * 4 // 512) + 76))
+
+    check(segments, parts)
+    for i in (0, len(segments) // 2, len(segments) - 1):
+        for change in (None, (6, 1), (8, -1), (4, 1), (5, -1), (9, 1), (3, 1)):
+            bad = list(segments)
+            if change is None:
+                del bad[i]
+            else:
+                row = list(bad[i])
+                row[change[0]] += change[1]
+                bad[i] = tuple(row)
+            with pytest.raises((AssertionError, StopIteration)):
+                check(bad, parts)
+    for i in (0, len(parts) // 2, len(parts) - 1):
+        for k, by in ((0, 1), (0, -1), (2, 1), (2, 256)):
+            row = list(parts[i])
+            row[k] += by
+            with pytest.raises(AssertionError):
+                check(segments, parts[:i] + [tuple(row)] + parts[i + 1:])
+
+
+def test_walk_refusals():
+    with pytest.raises(pd.PdError):
+        pd.pd_debug_prefix_walk([0, 3], [-1], 4, 1, 64)
+    with pytest.raises(pd.PdError):
+        pd.pd_debug_prefix_walk([0, 3], [5], 4, 1, 64, max_teams=77)
+    with pytest.raises(pd.PdError):
+        pd.pd_debug_prefix_walk([0, 3], [5], 5, 2, 64)
+    assert pd.pd_debug_prefix_walk([0, 3], [0], 4, 1, 64)[0] == []

@@ -45,11 +45,11 @@
 //     up to 2^-25, and as a raised reference may lie up to 1 above the largest score,
 //     the largest weight may be little more than a half: 2^-13 and 2^-24 of it).
 //
-// What bounds it, measured (8 KV heads, head dim 128, us per 1024 more prefix
-// tokens): 1024 rows 2.33, the tensor core (2.24 at the library product's rate); 128
-// rows 0.62 and 256 rows 0.67, HBM (0.62); FP8 0.66 at 128 and 256 rows, the two
-// warps that convert (HBM: 0.31).  The rest is the chain of three launches, 10 us of
-// the smallest step's 12.
+// What bounds it, measured (8 KV heads, head dim 128, us of a step per 1024 more
+// prefix tokens, from 8192 to 65536): 1024 rows 2.43 and 512 rows 1.22, the tensor core
+// (2.24 and 1.12 at the library product's rate); 128 rows 0.60 and 256 rows 0.68, HBM
+// (0.62); FP8 0.54 at 128 and 0.72 at 256 rows, the two warps that convert (HBM: 0.31).
+// The rest is the chain of three launches, 10 us of the smallest step's 12.
 #pragma once
 
 #include <cuda.h>

@@ -19,10 +19,11 @@ __host__ __device__ constexpr int item_rows(int dpad) { return 2 * block_rows(dp
 
 // How an item's rows go to the two CTAs of a team: as many as one CTA can take go
 // to both, which take the tiles in turn; more, half to each, with every tile for
-// both.  In turn the CTAs need not keep step (8 KV heads, 32768 tokens: 128 rows
-// 41 us in turn, 45 by halves; 256 rows 40.4 and 43.9), but make twice as many
-// partials (8192 tokens: 24.2 and 23.5); over an FP8 cache each converts half of
-// the tiles (128 rows: 67 us in turn, 89 by halves when a tile took it longer).
+// both.  In turn a tile is copied (and over an FP8 cache converted) once, but there
+// are twice as many partials.  Measured (8 KV heads of 128 columns, us a step, in turn
+// and by halves): 32768 tokens, 128 rows 34.8 and 44.0, 256 rows 40.2 and 45.4, over
+// FP8 37.6 and 53.0, 44.7 and 54.6; 8192 tokens, 128 rows 20.5 and 22.6, 256 rows
+// 24.2 and 24.1.
 __host__ __device__ constexpr bool is_pair(int rows, int of_item) { return rows > of_item / 2; }
 
 // What the prefix pass found the work to be: units in all, the teams that share

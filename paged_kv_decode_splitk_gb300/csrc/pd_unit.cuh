@@ -245,6 +245,8 @@ __global__ void __launch_bounds__(kThreads, CAP4 ? 4 : 0)
     const int C = p.cluster;
     // The own-token pass runs beside the shared-prefix pass, which let it launch
     // only after waiting for everything before it: it waits for nothing itself.
+    // (Relied on: what the wait of one grid made visible is visible to a grid that is
+    // launched after it.  The programming model says so of grids that wait themselves.)
     // One cluster more than the units need waits for the prefix pass, so that this
     // grid's end is the end of both (the merge waits for this grid).
     if (MODE == kModeOwn && blockIdx.x >= p.own_ctas) {

@@ -416,7 +416,8 @@ int walk(int num_seqs, int num_groups, const int32_t *group_starts, const int32_
     float time = 0.f;
     for (int g = 0; g < num_groups; ++g) {
         const int a = group_starts[g], b = group_starts[g + 1];
-        if (a < 0 || b < a || b > num_seqs || prefix_lens[g] < 0) return report(PD_ERR_INVALID, "pd_debug_prefix_walk: group %d", g);
+        if (a < 0 || b < a || b > num_seqs || prefix_lens[g] < 0 || prefix_lens[g] > 0x7fffffff - 256)
+            return report(PD_ERR_INVALID, "pd_debug_prefix_walk: group %d", g);
         GroupPlan r = plan_of<DPAD>(a, (b - a) * group, prefix_lens[g]);
         r.first_unit = W;
         r.first_item = items;
@@ -502,7 +503,8 @@ int pd_debug_prefix_walk(int num_seqs, int num_groups, const int32_t *group_star
     const int rc = pd::check_shape(num_q_heads, num_kv_heads, head_dim, 16);
     if (rc != PD_OK) return rc;
     if (num_seqs < 0 || num_groups < 1 || num_groups > kMaxGroups || max_teams < 1 || max_teams > kMaxTeams || max_segments < 0 ||
-        !group_starts || !prefix_lens || !segments || !num_segments || !parts || !totals)
+        static_cast<long long>(num_seqs) * num_q_heads > 0x7fffffffLL - 256 || !group_starts || !prefix_lens || !segments ||
+        !num_segments || !parts || !totals)
         return pd::report(PD_ERR_INVALID, "pd_debug_prefix_walk: an argument is out of range or null");
     const int dpad = dpad_of(head_dim);
     try {

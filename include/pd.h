@@ -295,9 +295,9 @@ int pd_decode_attn_noalloc(const void *q, const void *k_cache, const void *v_cac
  * cache reads zeros (PD_DEV_BAD_BLOCK_ID).  Cache slots past a length may hold
  * anything.  The weights of prefix tokens are rounded to BF16 (f16 over an FP8
  * cache, where weights below 2^-13 of the row's largest are off by up to 2^-24
- * of it) before they meet V; pd_decode_attn keeps 16 bits of every weight.  The same call on the same data gives the same
- * bits; unlike pd_decode_attn's, they depend on the batch (how a prefix is cut
- * depends on every group).
+ * of it) before they meet V; pd_decode_attn keeps 16 bits of every weight.  The
+ * same call on the same data gives the same bits; unlike pd_decode_attn's, they
+ * depend on the batch (how a prefix is cut depends on every group).
  * Where it pays: with one sequence a group the call takes 1 to 13 us more than
  * pd_decode_attn over whole tables (over FP8 up to twice the time); it spares the
  * reads of all sequences of a group but one.  It is the faster one from about

@@ -107,3 +107,23 @@ def test_results_are_kept_for_the_current_stream():
         api.rope(calls.rotation, calls.q, calls.positions + 1, stream=side).zero_()
     torch.cuda.synchronize()
     assert bool((kept == want).all())
+
+
+@pytest.mark.parametrize("name", ["rope", "append", "decode", "prefixed"])
+def test_forked_stream_in_a_graph(name):
+    """A captured step that forks to another stream and joins again, results allocated on the way."""
+    calls, side = Calls(), torch.cuda.Stream()
+    call = getattr(calls, name)
+    want = call()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = [call(stream=side), call(stream=side.cuda_stream)]
+        torch.cuda.current_stream().wait_stream(side)
+        twice = got[0] + got[1]
+    for _ in range(2):
+        for t in (*got, twice):
+            t.zero_()
+        graph.replay()
+        assert all(bool((t == want).all()) for t in got) and bool((twice == want + want).all())

@@ -86,7 +86,8 @@ extern "C" {
 #define PD_DEV_BAD_CONTEXT_LEN 2 /* a context length < 0 or > max_blocks_per_seq*block_size: clamped */
 #define PD_DEV_BAD_TILE_COUNT 4  /* a tile_block_counts entry < 0 or > tile_capacity: clamped */
 #define PD_DEV_WAIT_TIMEOUT 8    /* a bounded wait on a copy ran out: that output is garbage */
-#define PD_DEV_BAD_GROUPS 16     /* group_starts not non-decreasing within the batch: no prefix was read */
+#define PD_DEV_BAD_GROUPS 16     /* group_starts not non-decreasing within the batch: no prefix was read;
+                                  * pd_chunk_attn: token_starts, and that sequence was left out */
 
 /* Split-count policies (Module attn_splitk page, enum SplitkPolicy). */
 typedef enum { PD_POLICY_LEGACY = 0, PD_POLICY_AUTO = 1, PD_POLICY_PINNED = 2 } pd_policy;
@@ -334,6 +335,61 @@ int pd_decode_attn_prefix_fp8(const void *q, const void *k_cache, const void *v_
                               int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                               int num_blocks, float inv_sqrt_d, int num_splits, void *workspace,
                               size_t workspace_bytes, void *stream);
+
+/* ---- attention of new tokens over the paged cache ------------------------------
+ * pd_chunk_attn: attention of the new tokens of a batch, prompts, chunks of them,
+ * drafts or single tokens side by side, over the cache that pd_append_kv has put
+ * their keys and values into.  The token of sequence s at position p sees keys
+ * max(0, p + 1 - window) to p of its sequence:
+ *     out[t,h,:] = softmax(q[t,h,:] . K^T * inv_sqrt_d) . V,
+ *     lse[t,h]   = ln sum_j exp(q[t,h,:] . K[j] * inv_sqrt_d).
+ *   q             [num_tokens, num_q_heads, head_dim] BF16, q_token_stride elements
+ *                 from one token to the next (a multiple of 8, at least num_q_heads *
+ *                 head_dim): it may be a slice of a fused projection.
+ *   block_table, context_lens  as for pd_decode_attn: the lengths count the new tokens.
+ *   token_starts  [num_seqs + 1] int32, non-decreasing within 0..num_tokens: rows
+ *                 token_starts[s] to token_starts[s+1] - 1 are the last tokens of
+ *                 sequence s, in their order, as for pd_append_kv.  Rows of no
+ *                 sequence are left as they are, in out and lse.  NULL: one token
+ *                 per sequence (num_tokens == num_seqs).
+ *   out           [num_tokens, num_q_heads, head_dim] BF16, contiguous; shares no
+ *                 element with q.  A token that sees nothing (a sequence of length
+ *                 0, or with more new tokens than it is long) gets 0.
+ *   lse           [num_tokens, num_q_heads] FP32, or NULL: not wanted.  -infinity
+ *                 for a token that sees nothing.
+ *   window        keys a token sees at most, itself among them; 0: all.
+ *   workspace     >= pd_chunk_workspace_bytes(...) bytes, 16-B aligned, always needed;
+ *                 contents ignored on entry, scratch on return.  Calls that may
+ *                 overlap on the GPU, captured ones among them, have one each.
+ * The other arguments are pd_decode_attn's, its errors too: a length outside its
+ * table is clamped (PD_DEV_BAD_CONTEXT_LEN, which a sequence with more new tokens
+ * than it is long raises as well), a block id outside the cache reads zeros
+ * (PD_DEV_BAD_BLOCK_ID), and token_starts that name no rows of the batch raise
+ * PD_DEV_BAD_GROUPS and their sequence is left out.  Cache slots at and past a
+ * sequence's length, and those that no new token's window reaches, may hold
+ * anything, and table entries of blocks that none of their tokens is seen of are
+ * not read; the keys and values that a token of the call does see are finite.  The
+ * weights are rounded to BF16 before they meet V (f16 over an FP8 cache, where
+ * weights below 2^-13 of the row's largest are off by up to 2^-24 of it).  The same
+ * call on the same data gives the same bits; they depend on the batch (how
+ * the work is cut depends on all of it).
+ * Returns PD_OK, PD_ERR_INVALID, PD_ERR_WORKSPACE, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
+size_t pd_chunk_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim);
+
+int pd_chunk_attn(const void *q, int64_t q_token_stride, const void *k_cache, const void *v_cache,
+                  const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens,
+                  const int32_t *token_starts, void *out, float *lse, int num_tokens, int num_seqs,
+                  int num_q_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                  float inv_sqrt_d, int window, void *workspace, size_t workspace_bytes, void *stream);
+
+/* pd_chunk_attn over an FP8 cache of E4M3 codes with per-tensor scales, as
+ * pd_decode_attn_fp8 reads it (head_dim a multiple of 16). */
+int pd_chunk_attn_fp8(const void *q, int64_t q_token_stride, const void *k_cache, const void *v_cache,
+                      float k_scale, float v_scale, const int32_t *block_table, int max_blocks_per_seq,
+                      const int32_t *context_lens, const int32_t *token_starts, void *out, float *lse,
+                      int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                      int block_size, int num_blocks, float inv_sqrt_d, int window, void *workspace,
+                      size_t workspace_bytes, void *stream);
 
 /* ---- rotary positions ------------------------------------------------------
  * The rotation of a query or key row x of head_dim columns at position t: its
@@ -615,6 +671,20 @@ int pd_debug_prefix_walk(int num_seqs, int num_groups, const int32_t *group_star
                          const int32_t *prefix_lens, int num_q_heads, int num_kv_heads, int head_dim,
                          int fp8, float own_us, int max_teams, int32_t *segments, int max_segments,
                          int *num_segments, int64_t *parts, int32_t *totals);
+
+/* TEST HOOK.  How pd_chunk_attn divides a call's work, worked out on the host by the
+ * functions that its kernel runs (no CUDA): token_starts (or NULL) and context_lens in
+ * host memory, max_ctas CTAs at most (1..152).
+ *   segments  [max_segments, 11]: CTA, sequence, KV head, first query head, query heads,
+ *             first row of q, rows, first key tile, key tiles, 2 for a whole item, 1 for
+ *             its first part, 0 for another, and the CTA that has the item's last.
+ *   totals    [6]: units, CTAs, tokens of a block, keys of a tile, query heads of an
+ *             item at most, tokens of a box of queries.
+ * Returns PD_OK, PD_ERR_INVALID, PD_ERR_UNSUPPORTED, or PD_ERR_CAPACITY for more than
+ * max_segments segments. */
+int pd_debug_chunk_walk(int num_seqs, const int32_t *token_starts, const int32_t *context_lens, int num_q_heads,
+                        int num_kv_heads, int head_dim, int window, int max_ctas, int32_t *segments,
+                        int max_segments, int *num_segments, int64_t *totals);
 
 /* TEST HOOK.  Tuning for launch-shape experiments, applied to the following launches
  * in this process: pipeline stages per warp (1..8; 0 = built-in), where the

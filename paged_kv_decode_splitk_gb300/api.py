@@ -312,6 +312,59 @@ def decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_sta
     return out
 
 
+def chunk_workspace(num_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int, device, stream=None) -> torch.Tensor:
+    """The workspace of a chunk_attn; stream: of a call on another stream than the current one."""
+    return _fresh(pd.pd_chunk_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, head_dim), _U8, device, stream)
+
+
+def _check_chunk(q, k_cache, v_cache, block_table, context_lens, token_starts, out, lse, ws, dev: int) -> None:
+    _rows("q", q, None, None, q.shape[-1] if q.dim() == 3 else None, dev, True)
+    T, Hq, D = q.shape
+    _caches(k_cache, v_cache, k_cache.shape[2] if k_cache.dim() == 4 else 0, D, dev)
+    _indices("context_lens", context_lens, (None,), dev)
+    S = context_lens.shape[0]
+    _indices("block_table", block_table, (S, None), dev)
+    if token_starts is not None:
+        _indices("token_starts", token_starts, (S + 1,), dev)
+    if out is not None:
+        _rows("out", out, T, Hq, D, dev, True)
+        if not out.is_contiguous():
+            raise ValueError("out has to be contiguous")
+    if lse is not None and not (lse.dtype is torch.float32 and lse.shape == (T, Hq) and lse.is_contiguous() and lse.get_device() == dev):
+        _refuse("lse", lse, "contiguous FP32", (T, Hq), dev)
+    if ws is not None and not (ws.is_contiguous() and ws.get_device() == dev):
+        _refuse("ws", ws, "a contiguous buffer", (None,), dev)
+
+
+def chunk_attn(q, k_cache, v_cache, block_table, context_lens, inv_sqrt_d: float, token_starts=None, window: int = 0, out=None,
+               lse=None, return_lse: bool = False, ws=None, stream=None, k_scale: float = 1.0, v_scale: float = 1.0):
+    """Attention of new tokens over the paged cache that holds them already: rows token_starts[s] to token_starts[s + 1] - 1
+    of q [T, Hq, D] (None: one each) are the last tokens of sequence s, whose context_lens [S] count them, and each sees the
+    keys up to its own, the last `window` of them (0: all).  Returns out [T, Hq, D] BF16, and with return_lse (or an lse
+    that is given) also lse [T, Hq], the logarithm of each row's sum.  Rows of no sequence get nothing: an out or lse made
+    here holds anything there.  uint8 caches are FP8 E4M3 codes with per-tensor scales.  A serving call: no gradient passes
+    through it."""
+    if lse is None and return_lse and q.dim() == 3:
+        lse = _fresh(q.shape[:2], torch.float32, q.device, stream)
+    if stream is None:
+        done = pd.quick().chunk_attn(q, k_cache, v_cache, block_table, context_lens, token_starts, inv_sqrt_d, window, out, lse, ws,
+                                     k_scale, v_scale)
+        if done is not NotImplemented:
+            return done if lse is None else (done, lse)
+    _check_chunk(q, k_cache, v_cache, block_table, context_lens, token_starts, out, lse, ws, pd.current_device())
+    T, Hq, D = q.shape
+    if out is None:
+        out = _fresh(q.shape, _BF16, q.device, stream)
+    if ws is None:
+        ws = chunk_workspace(T, Hq, max(1, k_cache.shape[2]), D, q.device, stream)
+    if k_cache.dtype is _U8:
+        pd.pd_chunk_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, token_starts, out, lse, inv_sqrt_d, window,
+                             ws, stream)
+    else:
+        pd.pd_chunk_attn(q, k_cache, v_cache, block_table, context_lens, token_starts, out, lse, inv_sqrt_d, window, ws, stream)
+    return out if lse is None else (out, lse)
+
+
 class TiledInputs:
     """Device copies of a workloads.TiledWorkload."""
 

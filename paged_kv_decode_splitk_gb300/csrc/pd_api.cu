@@ -359,6 +359,34 @@ bool inject_alloc_failure() {
     }
     return inject > 0;
 }
+int sm_count_of_device() {
+    static std::mutex mu;
+    static int cached[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!cached[dev] && cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        cached[dev] = 0;
+    }
+    return cached[dev];
+}
+int encode_query_map(CUtensorMap *map, const void *q, int head_dim, int num_heads, int num_tokens, long long token_stride, int box_heads,
+                     int box_tokens) {
+    auto enc = encoder();
+    if (!enc) return cuda_fail(g_encode_err, "cuTensorMapEncodeTiled entry point");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_heads), static_cast<cuuint64_t>(num_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(token_stride) * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kBoxCols), static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PD_ERR_INVALID, "cuTensorMapEncodeTiled rejected the view of q (error %d): token stride %lld elements",
+                    static_cast<int>(r), token_stride);
+    return PD_OK;
+}
 }  // namespace pd
 
 struct pd_tiled {

@@ -203,12 +203,55 @@ PyObject *decode_attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// chunk_attn(q, k_cache, v_cache, block_table, context_lens, token_starts | None, inv_sqrt_d, window, out | None,
+//            lse | None, ws | None, k_scale, v_scale)
+PyObject *chunk_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return quick(n, 13, [&] {
+        const int dev = device();
+        const Rows q = rows(a[0], dev, true);
+        const at::Tensor &kc = cache(a[1], dev), &vc = cache(a[2], dev);
+        const at::Tensor &table = whole(a[3], 2, at::kInt, dev), &lens = whole(a[4], 1, at::kInt, dev);
+        const float scale = real(a[6]), ks = real(a[11]), vs = real(a[12]);
+        const long long window = integer(a[7]);
+        const int64_t S = lens.size(0);
+        need(kc.scalar_type() == vc.scalar_type() && kc.sizes() == vc.sizes() && kc.size(3) == q.D && table.size(0) == S && window >= 0);
+        const int32_t *starts = nullptr;
+        if (a[5] != Py_None) {
+            const at::Tensor &t = whole(a[5], 1, at::kInt, dev);
+            need(t.size(0) == S + 1);
+            starts = ints(t);
+        }
+        const int T = fits(q.T), Hq = fits(q.H), D = fits(q.D), nb = fits(kc.size(0)), bs = fits(kc.size(1)), H = fits(kc.size(2)),
+                  mb = fits(table.size(1)), seqs = fits(S), win = fits(window);
+        at::Tensor made, room;
+        if (a[8] == Py_None) made = fresh(q.t->sizes(), at::kBFloat16, dev);
+        const at::Tensor &out = a[8] == Py_None ? made : whole(a[8], 3, at::kBFloat16, dev);
+        need(out.sizes() == q.t->sizes());
+        float *lse = nullptr;
+        if (a[9] != Py_None) {
+            const at::Tensor &t = whole(a[9], 2, at::kFloat, dev);
+            need(t.size(0) == q.T && t.size(1) == q.H);
+            lse = static_cast<float *>(t.data_ptr());
+        }
+        if (a[10] == Py_None) room = fresh({static_cast<int64_t>(pd_chunk_workspace_bytes(T, Hq, H, D))}, at::kByte, dev);
+        const at::Tensor &ws = a[10] == Py_None ? room : whole(a[10], 1, at::kByte, dev);
+        const size_t bytes = static_cast<size_t>(ws.size(0));
+        const int rc = kc.scalar_type() == at::kByte
+                           ? pd_chunk_attn_fp8(q.data(), q.token, kc.data_ptr(), vc.data_ptr(), ks, vs, ints(table), mb, ints(lens), starts,
+                                               out.data_ptr(), lse, T, seqs, Hq, H, D, bs, nb, scale, win, ws.data_ptr(), bytes, stream(dev))
+                           : pd_chunk_attn(q.data(), q.token, kc.data_ptr(), vc.data_ptr(), ints(table), mb, ints(lens), starts,
+                                           out.data_ptr(), lse, T, seqs, Hq, H, D, bs, nb, scale, win, ws.data_ptr(), bytes, stream(dev));
+        need(rc == PD_OK);
+        return answer(a[8], made);
+    });
+}
+
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method<rope>("rope"), method<append_kv>("append_kv"), method<decode_attn_prefix>("decode_attn_prefix"),
-                         {nullptr, nullptr, 0, nullptr}};
+                         method<chunk_attn>("chunk_attn"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "pd_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,963 @@
+// pd_chunk.cuh -- attention of new tokens over the paged cache that holds them.
+//
+// What it computes.  For a new token at position p and each query head,
+//   out = sum_j w_j V[j] / sum_j w_j,   w_j = 2^(x_j - m),   x_j = q.K[j] scale log2(e),
+// over the keys j it sees, max(0, p + 1 - window) to p, in one pass over them: the
+// reference m is the largest score of the row's first tile with a key, raised by
+// whole numbers when a tile's weights sum past 2^15, so that no later maximum is
+// needed and the sums are scaled exactly.
+//
+// GB300 mapping.
+//   * An item is a block of new tokens with the query heads of a KV head, up to 256
+//     rows (128 at head dims above 128), and the key tiles that any of its rows sees.
+//     Items lie in one line of work units, of which every CTA (one an SM) takes the
+//     same share (pd_chunk_plan.h).  What a border cuts leaves partials of (m, l, o).
+//   * Warp 0 loads K tiles, warp 2 V tiles, by TMA boxes of 64 columns x as many
+//     tokens as lie together in a cache block, through the block table into a ring
+//     (128-byte swizzle); warp 3 an item's queries, whose rows are tokens by heads,
+//     as soon as the products of the last item's scores are done, so that a CTA goes
+//     from item to item without a pause of the tensor core longer than the first
+//     softmax.  One thread of warp 1 issues tcgen05.mma: S (128 rows x a tile) into
+//     TMEM, then O += P V with P read from TMEM.
+//   * Two groups of four warps do the softmax, a thread a row.  With more than 128
+//     rows each group has 128 of them and both meet every tile that their rows see;
+//     with fewer the groups take the tiles in turn, each with an O of its own, folded
+//     in the end.  At head dims above 128 one O fills TMEM: one group, two S.
+//   * Only tiles that hold a border of a row's keys are masked.  V rows past the
+//     sequence, or before every row's window, are zeroed, so that whatever the
+//     cache's slots hold there meets no product; boxes that lie there wholly are not
+//     read at all.
+//   * P is rounded to BF16 (half a step: 2^-8 of each weight), the form the tensor
+//     core multiplies with a BF16 V; l sums the unrounded weights in FP32, S, O, m and l
+//     are FP32.  An FP8 cache is converted to f16 tiles (exactly) by warps 2 and 3, q
+//     to f16 under a power of two for each row by the softmax warps, and P is f16
+//     there (2^-11; weights below 2^-13 of the row's largest are off by up to 2^-24
+//     of it).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include <cfloat>
+
+#include "pd.h"
+#include "pd_chunk.h"
+#include "pd_device.cuh"
+#include "pd_tcgen05.cuh"
+#include "pd_tile.cuh"
+
+namespace pd {
+namespace chunk {
+
+using namespace tile;
+
+struct ChunkMaps {
+    CUtensorMap k, v, q;
+};
+
+// Scores of the columns below the first live one become -infinity.
+template <int BN>
+__device__ __forceinline__ void mask_columns_below(uint32_t (&x)[BN], int first) {
+#pragma unroll
+    for (int i = 0; i < BN; ++i)
+        if (i < first) x[i] = 0xff800000u;
+}
+
+// Sequence s's new tokens; none where token_starts does not name rows of the batch.
+__device__ __forceinline__ Span span_of(const ChunkParams &p, int s, bool flag) {
+    Span q = {s, 1, 0, p.context_lens[s]};
+    if (p.token_starts) {
+        const int a = p.token_starts[s], b = p.token_starts[s + 1];
+        const bool bad = a < 0 || b < a || b > p.num_tokens;
+        if (bad && flag) dev::flag_status(p.status, PD_DEV_BAD_GROUPS);
+        q.first = a;
+        q.n = bad ? 0 : b - a;
+    }
+    if (q.len < 0 || q.len > p.max_tokens || (p.token_starts && q.n > q.len)) {
+        if (flag) dev::flag_status(p.status, PD_DEV_BAD_CONTEXT_LEN);
+        q.len = q.len < 0 ? 0 : (q.len > p.max_tokens ? p.max_tokens : q.len);
+    }
+    q.past = q.len - q.n;
+    return q;
+}
+
+// (loads without a cache policy: items of the same head read the same tiles, from L2)
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// A segment as warp 0 hands it to the others.
+struct Task {
+    int n;                            // key tiles; -1: no more segments
+    int tile0, two;                   // the first; more than 128 rows
+    int end0, first1;                 // two: tiles that the first 128 rows see, [0, end0), and the others, [first1, n)
+    int token, tokens, head, heads;   // rows of q and query heads
+    int pos, low, len;                // of the first token; the first key any row sees; the sequence's tokens
+    int seq, kvh;
+    int begins, whole, parts;         // has the item's first tile, has all; CTAs from this one on that have a part
+};
+constexpr int kTasks = 8;
+
+// With more than 128 rows each stream has 128 of them, and need not meet the tiles
+// that only the other's rows see.
+__device__ __forceinline__ Task task_of(const ChunkParams &p, const Segment &g, int dpad, long long W, int C) {
+    const Shape &s = p.shape;
+    Task t;
+    t.n = g.n;
+    t.tile0 = g.tile0;
+    t.two = dpad <= 128 && g.tokens * s.item_heads > kRowTile;
+    const int last = g.pos + min(fast_div(kRowTile - 1, p.fd_heads), g.tokens - 1);  // the last position of the first 128 rows
+    t.end0 = min(g.n, max(0, (last >= 0 ? last / s.tile + 1 : 0) - g.tile0));
+    t.first1 = min(g.n, max(0, first_key(s, g.pos + fast_div(kRowTile, p.fd_heads)) / s.tile - g.tile0));
+    t.token = g.token;
+    t.tokens = g.tokens;
+    t.head = g.head;
+    t.heads = g.heads;
+    t.pos = g.pos;
+    t.low = first_key(s, g.pos);
+    t.len = g.span.len;
+    t.seq = g.seq;
+    t.kvh = g.kvh;
+    t.begins = g.begins;
+    t.whole = g.whole;
+    t.parts = g.whole ? 1 : cta_of_unit(W, C, g.item_end - 1) - static_cast<int>(blockIdx.x) + 1;
+    return t;
+}
+
+// Shared-memory plan (bytes from the 1024-aligned base).
+template <int DPAD, bool KV8>
+struct Plan {
+    static constexpr bool kOne = DPAD > 128;  // one stream, S double-buffered
+    static constexpr int kTile = tile_tokens(DPAD);
+    static constexpr int kBlock = block_rows(DPAD);
+    static constexpr int kStageBytes = kTile * DPAD * 2;
+    static constexpr int kStages = KV8 ? 3 : (DPAD == 64 ? 6 : 4);
+    static constexpr int kRawBytes = KV8 ? kTile * DPAD : 0;
+    static constexpr int kRawStages = KV8 ? 3 : 0;
+    static constexpr int kOutBytes = 2048;  // of a warp: 32 rows x 64 bytes on their way out
+    static constexpr int q = 0;             // [DPAD / 64][kBlock rows][128 bytes]
+    static constexpr int ring = q + kBlock * DPAD * 2;
+    static constexpr int raw = ring + kStages * kStageBytes;
+    static constexpr int out = raw + kRawStages * kRawBytes;
+    // (over an FP8 cache the warps that load the queries are those that stage results
+    // in their place)
+    static constexpr int bars = out + (KV8 ? 0 : (kOne ? 4 : 8) * kOutBytes);
+    static constexpr int misc = bars + 56 * 8;
+    static constexpr int tasks = misc + 256;
+    static constexpr int row_scale = tasks + (kTasks * static_cast<int>(sizeof(Task)) + 15) / 16 * 16;
+    static constexpr int stream_ml = row_scale + (KV8 ? 2 * kBlock * 4 : 0);
+    static constexpr int total = 1024 + stream_ml + (kOne ? 0 : 2 * kRowTile * 8);
+    static constexpr int kThreads = 384;
+};
+
+template <int DPAD, bool KV8>
+__global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p) {
+    using L = Plan<DPAD, KV8>;
+    constexpr int BN = L::kTile;
+    constexpr int BR = L::kBlock;
+    constexpr int NST = L::kStages;
+    constexpr int NT = L::kThreads;
+    constexpr bool ONE = L::kOne;
+    constexpr int CHUNKS = DPAD / 8;  // 16-byte chunks of a 16-bit row
+    constexpr uint32_t kDescS = tc::instr_desc(KV8 ? 0 : 1, kRowTile, BN, false);
+    constexpr uint32_t kDescO = tc::instr_desc(KV8 ? 0 : 1, kRowTile, DPAD, true);
+    const float kNegInf = -__int_as_float(0x7f800000);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t base = dev::smem_addr(smem);
+    // barriers: full[NST], empty[NST], raw_full[3], raw_empty[3], landed[NST], s[2],
+    // p[2], o[2], q[2], q_free, tail, streams, task_full[8], task_free[8]
+    const uint32_t bars = base + L::bars;
+    const uint32_t bar_full = bars, bar_empty = bar_full + 8 * NST, bar_rfull = bar_empty + 8 * NST,
+                   bar_rempty = bar_rfull + 24, bar_land = bar_rempty + 24, bar_s = bar_land + 8 * NST, bar_p = bar_s + 16,
+                   bar_o = bar_p + 16, bar_q = bar_o + 16, bar_qfree = bar_q + 16, bar_tail = bar_qfree + 8, bar_x = bar_tail + 8,
+                   bar_task = bar_x + 8, bar_tfree = bar_task + 8 * kTasks;
+    static_assert(3 * NST + 6 + 8 + 3 + 2 * kTasks <= 56, "barrier region");
+    volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc);
+    uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 4);
+    int *start_seq = reinterpret_cast<int *>(smem + L::misc + 8);           // sequence, head, block
+    long long *start_rest = reinterpret_cast<long long *>(smem + L::misc + 24);
+    long long *sums = reinterpret_cast<long long *>(smem + L::misc + 32);  // [2][12] of the warps
+
+    // (the warp's number from one lane, so that the compiler knows it to be the
+    // same on all: the product warp's operands then live in uniform registers)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+    // ---- set-up that reads no global memory -----------------------------------
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            dev::mbar_init(bar_full + 8 * i, KV8 ? kConverters / 32 : 1);
+            dev::mbar_init(bar_empty + 8 * i, 1);
+            dev::mbar_init(bar_land + 8 * i, 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            dev::mbar_init(bar_rfull + 8 * i, 1);
+            dev::mbar_init(bar_rempty + 8 * i, kConverters / 32);
+        }
+        for (int i = 0; i < 2; ++i) {
+            dev::mbar_init(bar_s + 8 * i, 1);
+            dev::mbar_init(bar_p + 8 * i, 4);
+            dev::mbar_init(bar_o + 8 * i, 1);
+            dev::mbar_init(bar_q + 8 * i, KV8 ? 4 : 1);
+        }
+        dev::mbar_init(bar_qfree, 1);
+        dev::mbar_init(bar_tail, 1);
+        dev::mbar_init(bar_x, 8);
+        for (int i = 0; i < kTasks; ++i) {
+            dev::mbar_init(bar_task + 8 * i, 1);
+            dev::mbar_init(bar_tfree + 8 * i, 3 + (ONE ? 4 : 8));  // the warps that read it
+        }
+        dev::fence_mbar_init();
+        *gave_up = 0;
+        dev::prefetch_tensormap(&maps.k);
+        dev::prefetch_tensormap(&maps.v);
+        if (!KV8) dev::prefetch_tensormap(&maps.q);
+    }
+    if (warp == 1) tc::tmem_alloc_512(dev::smem_addr(tmem_s));
+    dev::griddep_wait();  // q, the caches, tables and lengths are final
+
+    // ---- the CTA's place in the line of units -----------------------------------
+    const auto spans = [&](int s) { return span_of(p, s, false); };
+    long long first = 0, all = 0;  // units of this thread's first sequence, and of all of them
+    for (int s = tid; s < p.num_seqs; s += NT) {
+        const long long u = p.shape.heads * head_units(p.shape, span_of(p, s, blockIdx.x == 0));
+        if (s == tid) first = u;
+        all += u;
+    }
+    auto warp_scan = [&](long long v) {
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, v, off);
+            if (lane >= off) v += o;
+        }
+        return v;
+    };
+    long long upto = warp_scan(first);
+    all = warp_scan(all);
+    if (lane == 31) {
+        sums[warp] = upto;
+        sums[12 + warp] = all;
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    // Everything before this grid is done: the fold may come to wait for its end.
+    dev::griddep_launch_dependents();
+    constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
+    long long W = 0;
+    for (int i = 0; i < 12; ++i) W += sums[12 + i];
+    const int C = cta_count(W, gridDim.x);
+    Walk walk = {};
+    if (static_cast<int>(blockIdx.x) < C) {
+        walk.u = cta_begin(W, C, blockIdx.x);
+        walk.end = cta_begin(W, C, blockIdx.x + 1);
+        long long before = 0;  // units of the sequences before this stripe
+        for (int s0 = 0;; s0 += NT) {
+            if (s0 > 0) {
+                __syncthreads();
+                first = s0 + tid < p.num_seqs ? p.shape.heads * head_units(p.shape, span_of(p, s0 + tid, false)) : 0;
+                upto = warp_scan(first);
+                if (lane == 31) sums[warp] = upto;
+                __syncthreads();
+            }
+            long long stripe = 0, mine = 0;
+            for (int i = 0; i < 12; ++i) {
+                if (i == warp) mine = stripe;
+                stripe += sums[i];
+            }
+            mine += before + upto - first;
+            if (mine <= walk.u && walk.u < mine + first) {
+                start_seq[0] = s0 + tid;
+                *start_rest = walk.u - mine;
+            }
+            before += stripe;
+            if (before > walk.u) break;  // (it is W in the end)
+        }
+        __syncthreads();
+        walk.seq = start_seq[0];
+        walk.span = spans(walk.seq);
+        if (warp == 0) {
+            const long long of_head = head_units(p.shape, walk.span), rest = *start_rest;
+            const int head = static_cast<int>(rest / of_head);
+            const long long in_head = rest - head * of_head;
+            int lo = 0, n = blocks_of(p.shape, walk.span.n);
+            while (n > 1) {  // the last block that begins at or before the unit
+                const int step = (n + 31) / 32, i = lane * step;
+                const bool at = i < n && units_before(p.shape, walk.span, lo + i) <= in_head;
+                const int pick = (__popc(__ballot_sync(0xffffffffu, at)) - 1) * step;
+                lo += pick;
+                n = min(step, n - pick);
+            }
+            if (lane == 0) {
+                start_seq[1] = head;
+                start_seq[2] = lo;
+                *start_rest = in_head - units_before(p.shape, walk.span, lo);
+            }
+        }
+        __syncthreads();
+        walk.head = start_seq[1];
+        walk.block = start_seq[2];
+        walk.skip = *start_rest;
+    }
+    const int bs = static_cast<int>(p.block_size.d);
+    const int IH = p.shape.item_heads;
+    // Warp 0 walks the line and hands each segment to the other warps, a few ahead.
+    Task *const tasks = reinterpret_cast<Task *>(smem + L::tasks);
+    int task = 0;           // the place of the next one
+    uint32_t task_ph = 0;
+    auto next_task = [&] {  // (the warp waits; false: there are no more)
+        if (!wait_bar(bar_task + 8 * task, task_ph, gave_up)) return false;
+        return tasks[task].n >= 0;
+    };
+    auto task_done = [&] {
+        arrive_warp(bar_tfree + 8 * task, lane);
+        if (++task == kTasks) {
+            task = 0;
+            task_ph ^= 1;
+        }
+    };
+    // Registers: a softmax thread holds a whole tile row.  384 threads were
+    // launched with 168 each: 128 x 88 + 256 x 208 is what all of them have.
+    static_assert(NT == 384 && 88 + 2 * 208 <= 3 * 168, "the shares add up to the launch's registers");
+
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+
+    if (warp == 0 || (!KV8 && warp == 2)) {
+        // ---- loads: K and V tiles in the order the products take them ------------
+        constexpr int COLS = KV8 ? (DPAD < 128 ? DPAD : 128) : kBoxCols;  // columns of a box
+        const int CT = p.box_tokens;                         // tokens of a box
+        const int NCH = BN / CT, NBOX = NCH * (DPAD / COLS);
+        constexpr int DEPTH = KV8 ? L::kRawStages : NST;
+        constexpr int BYTES = KV8 ? L::kRawBytes : L::kStageBytes;
+        const uint32_t full = KV8 ? bar_rfull : bar_full, empty = KV8 ? bar_rempty : bar_empty;
+        const uint32_t stage0 = base + (KV8 ? L::raw : L::ring);
+        const int chunk = lane % NCH, col = lane / NCH;
+        int st = 0;
+        uint32_t ph = 0;       // phase of the stage about to be filled
+        uint32_t land_ph = 0;  // of the landing barriers, a bit each
+        bool ok = true;
+        long long issued = 0;
+        auto load_all = [&](const Task &sg) {
+            const int32_t *ids = p.block_table + static_cast<long long>(sg.seq) * p.max_blocks;
+            const int ahead = sg.two ? 1 : 2;
+            const int low = sg.low, end = sg.pos + sg.tokens, len = sg.len;
+            const bool mine = lane < NBOX;  // a box a lane
+            // Block ids, 32 boxes' rows (chunks of CT tokens) at a time: lane l of `now`
+            // has chunk 32 w + l of the segment, `then` the 32 after them, asked for a
+            // window ahead.  Where no row sees a token of the chunk, and for a bad
+            // id (-1), it is one outside the cache, which reads zeros.
+            const int lg = 31 - __clz(NCH);
+            auto ids_of = [&](int w) -> int {
+                const int c = 32 * w + lane, j = c >> lg;
+                const int tok = (sg.tile0 + j) * BN + (c & (NCH - 1)) * CT;
+                if (j >= sg.n || tok >= end || tok + CT <= low) return p.num_blocks;
+                const int id = __ldg(ids + fast_div(tok, p.block_size));
+                return id >= 0 && id < p.num_blocks ? id : -1;
+            };
+            int w = 0, now = ids_of(0), then = ids_of(1), before = now;
+            auto next_stage = [&] {
+                ++issued;
+                if (++st == DEPTH) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                return true;
+            };
+            auto load = [&](bool is_v, int j) {
+                if (!KV8 && is_v != (warp == 2)) return next_stage();  // the other warp's
+                const int at = (sg.tile0 + j) * BN, tok = at + chunk * CT;
+                const int wj = j << lg >> 5;
+                if (wj > w) {
+                    w = wj;
+                    before = now;
+                    now = then;
+                    then = ids_of(w + 1);
+                }
+                int id = __shfl_sync(0xffffffffu, wj == w ? now : before, ((j << lg) + chunk) & 31);
+                if (id < 0) {
+                    if (mine) dev::flag_status(p.status, PD_DEV_BAD_BLOCK_ID);
+                    id = p.num_blocks;
+                }
+                if (!wait_bar(empty + 8 * st, ph ^ 1, gave_up)) return false;
+                const uint32_t dst = stage0 + st * BYTES;
+                // A box of live and dead tokens holds whatever the cache's slots past the
+                // sequence, or before every row's window, hold; a dead V row must not
+                // reach the product (0 x NaN), so those rows are zeroed before the
+                // tile is handed on.  It lands at a barrier of its stage.
+                const int nl = max(0, low - at), nv = min(BN, len - at);
+                const bool some = !KV8 && is_v && ((nl | nv) & (CT - 1));
+                const uint32_t bar = (some ? bar_land : full) + 8 * st;
+                if (lane == 0) dev::mbar_arrive_expect_tx(bar, BYTES);
+                __syncwarp();
+                if (mine) {
+                    const int sub = tok - fast_div(tok, p.block_size) * bs;
+                    const uint32_t to = dst + col * (BN * (KV8 ? COLS : 128)) + chunk * (CT * (KV8 ? COLS : 128));
+                    const CUtensorMap *map = is_v ? &maps.v : &maps.k;
+                    const int c1 = p.tok_dim == 1 ? sub : sg.kvh, c2 = p.tok_dim == 1 ? sg.kvh : sub;
+                    tma_load_4d(to, map, bar, col * COLS, c1, c2, id);
+                }
+                if (some) {
+                    const uint32_t lph = (land_ph >> st) & 1;
+                    land_ph ^= 1u << st;
+                    if (!wait_bar(bar, lph, gave_up)) {
+                        if (lane == 0) dev::mbar_wait_bounded(bar, lph, 100000000ull);  // (its copies land before the CTA ends)
+                        return false;
+                    }
+                    uint8_t *tile = smem + L::ring + st * BYTES;
+                    const int l0 = nl & ~(CT - 1), v1 = (nv + CT - 1) & ~(CT - 1);
+                    for (int b = 0; b < DPAD / 64; ++b) {
+                        for (int i = l0 * 8 + lane; i < nl * 8; i += 32)
+                            *reinterpret_cast<uint4 *>(tile + b * (BN * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+                        for (int i = nv * 8 + lane; i < v1 * 8; i += 32)
+                            *reinterpret_cast<uint4 *>(tile + b * (BN * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) arrive(full + 8 * st);
+                }
+                return next_stage();
+            };
+            for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
+                if (i < sg.n) ok = load(false, i);
+                const int v = i - ahead + 1;
+                if (ok && v >= 0 && sg.n > 0) ok = load(true, v);
+            }
+        };
+        if (warp == 0) {
+            Segment g;
+            for (bool more = true; ok && more;) {
+                more = next_segment(p.shape, p.num_seqs, spans, walk, g);
+                Task t = {};
+                t.n = -1;
+                if (more) t = task_of(p, g, DPAD, W, C);
+                if (!(ok = wait_bar(bar_tfree + 8 * task, task_ph ^ 1, gave_up))) break;
+                if (lane == 0) {
+                    tasks[task] = t;
+                    arrive(bar_task + 8 * task);
+                }
+                __syncwarp();
+                const Task &handed = tasks[task];
+                if (++task == kTasks) {
+                    task = 0;
+                    task_ph ^= 1;
+                }
+                if (more) load_all(handed);
+            }
+        } else {
+            while (ok && next_task()) {
+                load_all(tasks[task]);
+                task_done();
+            }
+        }
+        // every release of a stage has arrived before this CTA ends
+        for (long long i = issued < DEPTH ? 0 : issued - DEPTH; ok && i < issued; ++i)
+            ok = wait_bar(empty + 8 * static_cast<int>(i % DEPTH), static_cast<uint32_t>((i / DEPTH) & 1), gave_up);
+        if (!ok && lane == 0) {
+            // a wait ran out: let the copies in flight land before the CTA ends
+            dev::flag_status(p.status, PD_DEV_WAIT_TIMEOUT);
+            const long long last = issued < DEPTH ? issued : DEPTH;
+            for (long long i = issued - last; i < issued; ++i)
+                dev::mbar_wait_bounded(full + 8 * static_cast<int>(i % DEPTH), static_cast<uint32_t>((i / DEPTH) & 1),
+                                       100000000ull);
+        }
+    } else if (warp == 1) {
+        // ---- products: one thread issues them all, in the order S, P V, S, ... of
+        // the streams in turn.  What it waits for is looked at as early as the order
+        // allows: the queue of products is short, and whatever this thread spends
+        // between two of them the tensor core may spend idle.
+        if (tc::elect_one()) {
+            int st = 0;
+            uint32_t ph = 0, pph = 0, qph = 0;  // phases: of the ring; a bit for each stream
+            bool ok = true;
+            const uint32_t qa = base + L::q, ra = base + L::ring;
+            const uint64_t q_desc = tc::smem_desc(qa, 16), k_desc = tc::smem_desc(ra, 16), v_desc = tc::smem_desc(ra, BN * 128);
+            // (a negative scale: q as its negation, by the product itself)
+            const uint32_t desc_s = kDescS | (!KV8 && p.negative ? 1u << 13 : 0u);
+            // the next tile of the ring (K or V), once it has landed
+            auto take = [&](int &stage) {
+                stage = st;
+                if (!wait_one(bar_full + 8 * st, ph, gave_up)) return false;
+                if (++st == NST) {
+                    st = 0;
+                    ph ^= 1;
+                }
+                return true;
+            };
+            auto scores = [&](int buf, int qt, int stage) {
+                const uint64_t qd = q_desc + qt * (kRowTile * 128 / 16), kd = k_desc + stage * (L::kStageBytes / 16);
+                tc::fence_after();
+#pragma unroll
+                for (int k = 0; k < DPAD / 16; ++k)
+                    tc::mma_ss(tmem + buf * 128, qd + ((k / 4) * (BR * 128) + (k % 4) * 32) / 16,
+                               kd + ((k / 4) * (BN * 128) + (k % 4) * 32) / 16, desc_s, k > 0);
+                tc::commit(bar_s + 8 * buf);
+            };
+            auto values = [&](int buf, int o, int stage, bool accumulate, bool done) {
+                const uint64_t vd = v_desc + stage * (L::kStageBytes / 16);
+                tc::fence_after();
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k)
+                    tc::mma_ts(tmem + 256 + o * DPAD, tmem + buf * 128 + k * 8, vd + k * (2048 / 16), kDescO, accumulate || k > 0);
+                if (done) tc::commit(bar_o + 8 * o);
+            };
+            auto release = [&](int stage) { tc::commit(bar_empty + 8 * stage); };
+            auto queries_done = [&] {
+                if (!KV8) tc::commit(bar_qfree);
+            };
+            auto weights = [&](int buf) {
+                const bool got = wait_one(bar_p + 8 * buf, (pph >> buf) & 1, gave_up);
+                pph ^= 1u << buf;
+                return got;
+            };
+            auto queries = [&](int t) {  // (from boxes of q all rows come at once)
+                if (!KV8 && t > 0) return true;
+                const bool got = wait_one(bar_q + 8 * t, (qph >> t) & 1, gave_up);
+                qph ^= 1u << t;
+                return got;
+            };
+            auto task_given = [&] {
+                arrive(bar_tfree + 8 * task);
+                if (++task == kTasks) {
+                    task = 0;
+                    task_ph ^= 1;
+                }
+            };
+            for (;; task_given()) {
+                if (!(ok = wait_one(bar_task + 8 * task, task_ph, gave_up))) break;
+                const int n = tasks[task].n, two = tasks[task].two, end0 = tasks[task].end0, first1 = tasks[task].first1;
+                if (n < 0) break;
+                if (n == 0) continue;
+                int ks = 0, vs = 0;
+                if (!(ok = queries(0))) break;
+                if (!(ok = take(ks))) break;
+                if (!ONE && two) {
+                    if (end0 > 0) scores(0, 0, ks);
+                    if (!(ok = queries(1))) break;
+                    if (first1 == 0) scores(1, 1, ks);
+                    release(ks);
+                    if (n == 1) queries_done();
+                    if (!(ok = take(vs))) break;
+                    for (int j = 0; ok && j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        const int v = vs;
+                        if (more && !(ok = take(ks))) break;
+                        if (j < end0) {
+                            if (!(ok = weights(0))) break;
+                            values(0, 0, v, j > 0, j + 1 == end0);
+                        }
+                        if (more && j + 1 < end0) scores(0, 0, ks);
+                        if (j >= first1) {
+                            if (!(ok = weights(1))) break;
+                            values(1, 1, v, j > first1, !more);
+                        }
+                        release(v);  // (before the scores: a commit waits for all that came before)
+                        if (more) {
+                            if (j + 1 >= first1) scores(1, 1, ks);
+                            release(ks);
+                            if (j + 2 == n) queries_done();
+                            ok = take(vs);
+                        }
+                    }
+                } else {
+                    // scores of tile j, whose keys are the next of the ring
+                    auto next_scores = [&](int j) {
+                        scores(j & 1, 0, ks);
+                        release(ks);
+                        if (j + 1 == n) queries_done();
+                    };
+                    next_scores(0);
+                    if (n > 1) {
+                        if (!(ok = take(ks))) break;
+                        next_scores(1);
+                    }
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (!(ok = take(vs))) break;
+                        const bool next = j + 2 < n;
+                        if (next && !(ok = take(ks))) break;
+                        const int t = j & 1;
+                        if (!(ok = weights(t))) break;
+                        values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= n);
+                        release(vs);
+                        if (next) next_scores(j + 2);
+                    }
+                }
+                if (!ok) break;
+            }
+            if (!ok) {
+                // let the products in flight end before TMEM is freed
+                tc::commit(bar_tail);
+                dev::mbar_wait_bounded(bar_tail, 0, 100000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (!KV8) {
+        // ---- queries: the rows of the next item, once the last one's scores are done ----
+        uint32_t ph = 0;
+        bool ok = true, any = false;
+        for (; ok && next_task(); task_done()) {
+            const Task &sg = tasks[task];
+            if (sg.n == 0) continue;
+            if (!(ok = wait_bar(bar_qfree, ph ^ 1, gave_up))) break;
+            const int boxes = (sg.tokens + p.query_box - 1) / p.query_box, bytes = p.query_box * IH * 128;  // of 64 columns
+            if (lane == 0) dev::mbar_arrive_expect_tx(bar_q, boxes * bytes * (DPAD / 64));
+            __syncwarp();
+            for (int b = lane; b < boxes; b += 32) {
+#pragma unroll
+                for (int c = 0; c < DPAD / 64; ++c)
+                    tma_load_3d(base + L::q + c * (BR * 128) + b * bytes, &maps.q, bar_q, c * 64, sg.head, sg.token + b * p.query_box);
+            }
+            ph ^= 1;
+            any = true;
+        }
+        // the products have taken the last rows before this CTA ends
+        if (ok && any) ok = wait_bar(bar_qfree, ph ^ 1, gave_up);
+        if (!ok && any && lane == 0) dev::mbar_wait_bounded(bar_q, ph ^ 1, 100000000ull);
+    } else {
+        // ---- FP8: each landed tile of codes into an f16 tile of the ring (k_scale is in
+        // the softmax scale, v_scale in the results) ----
+        const Widen<DPAD, BN> widen(warp - 2, lane);
+        int rs = 0, st = 0;
+        uint32_t rph = 0, ph = 0;
+        bool ok = true;
+        long long handed = 0;
+        auto convert = [&](bool is_v, int low, int end) {
+            if (!wait_bar(bar_rfull + 8 * rs, rph, gave_up) || !wait_bar(bar_empty + 8 * st, ph ^ 1, gave_up)) return false;
+            const uint8_t *src = smem + L::raw + rs * L::kRawBytes;
+            uint8_t *dst = smem + L::ring + st * L::kStageBytes;
+            widen(src, dst, is_v && (low > 0 || end < BN), low, end);
+            tc::fence_async_shared();
+            arrive_warp(bar_full + 8 * st, lane);
+            arrive_warp(bar_rempty + 8 * rs, lane);  // (the reads come before the loads that refill it)
+            if (++rs == L::kRawStages) {
+                rs = 0;
+                rph ^= 1;
+            }
+            ++handed;
+            if (++st == NST) {
+                st = 0;
+                ph ^= 1;
+            }
+            return true;
+        };
+        for (; ok && next_task(); task_done()) {
+            const Task &sg = tasks[task];
+            const int ahead = sg.two ? 1 : 2, low = sg.low, len = sg.len;
+            for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
+                if (i < sg.n) ok = convert(false, 0, BN);
+                const int v = i - ahead + 1, at = (sg.tile0 + v) * BN;
+                if (ok && v >= 0 && sg.n > 0) ok = convert(true, low - at, len - at);
+            }
+        }
+        // every release of a stage has arrived before this CTA ends
+        for (long long i = handed < NST ? 0 : handed - NST; ok && i < handed; ++i)
+            ok = wait_bar(bar_empty + 8 * static_cast<int>(i % NST), static_cast<uint32_t>((i / NST) & 1), gave_up);
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (warp < (ONE ? 8 : 12)) {
+        // ---- softmax: a thread per row -----------------------------------------------
+        const int t = (warp - 4) >> 2;            // the stream
+        const int r = (warp & 3) * 32 + lane;     // the row of its tile
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t to = tmem + lanes + 256 + t * DPAD;
+        const int D = p.head_dim;
+        uint32_t sph = 0, oph = 0, xph = 0;  // phases, a bit for each buffer or stream
+        bool ok = true, cut = false;
+        // FP8: the rows' scales, in turn in two places: the other stream may still
+        // have to read the last segment's when this one's are written (it has by
+        // the time a third segment begins: its weights of the first went before)
+        float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
+        int turn = 0;
+        for (; ok && next_task(); task_done()) {
+            const Task &sg = tasks[task];  // (read again wherever it is wanted, to hold no registers)
+            const bool two = !ONE && sg.two;
+            float scale = p.scale_log2;
+            if constexpr (KV8) {
+                row_scale = reinterpret_cast<float *>(smem + L::row_scale) + turn * BR;
+                turn ^= 1;
+                // -- this stream's query rows into shared memory (128-byte swizzle); with
+                // at most 128 rows the streams share stream 0's.
+                if ((two || t == 0) && sg.n > 0) {
+                    // 32 rows x CHUNKS chunks over 32 lanes, sixteen loads in flight at once
+                    constexpr int BATCH = CHUNKS < 16 ? CHUNKS : 16;
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i0 = 0; i0 < CHUNKS; i0 += BATCH) {
+                        uint4 v[BATCH];
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i) {
+                            const int e = (i0 + i) * 32 + lane;
+                            const int gr = t * kRowTile + (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;  // row of the block, chunk
+                            const int tk = fast_div(gr, p.fd_heads), h = gr - tk * IH;
+                            v[i] = make_uint4(0, 0, 0, 0);
+                            if (tk < sg.tokens && h < sg.heads && c * 8 < D)
+                                v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (sg.token + tk) * p.q_tok +
+                                                                             static_cast<long long>(sg.head + h) * D + c * 8));
+                        }
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i) {
+                            const int e = (i0 + i) * 32 + lane;
+                            const int row = t * kRowTile + (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;
+                            if (p.negative) {
+                                v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
+                            }
+                            // f16 rows under a power of two that brings the row's largest
+                            // |q| into [2^14, 2^15), exactly but for values 2^-28 below it;
+                            // its inverse joins the row's softmax scale
+                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                            float big = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                big = fmaxf(big, fmaxf(fabsf(dev::bf16_lo_f32(w[k])), fabsf(dev::bf16_hi_f32(w[k]))));
+#pragma unroll
+                            for (int off = 1; off < CHUNKS; off <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+                            const int ex = (__float_as_int(big) >> 23) & 0xff;  // big < 2^(ex - 126)
+                            const int up = min(max(141 - ex, -126), 127);       // times 2^up: below 2^15
+                            const float f = __int_as_float((127 + up) << 23);
+                            const float down = up < 127 ? __int_as_float((127 - up) << 23) : 5.877471754111438e-39f;  // 2^-up
+                            if (c == 0) row_scale[row] = fmaxf(p.scale_log2 * down, FLT_MIN);
+                            v[i].x = dev::pack_f16x2(dev::bf16_lo_f32(w[0]) * f, dev::bf16_hi_f32(w[0]) * f);
+                            v[i].y = dev::pack_f16x2(dev::bf16_lo_f32(w[1]) * f, dev::bf16_hi_f32(w[1]) * f);
+                            v[i].z = dev::pack_f16x2(dev::bf16_lo_f32(w[2]) * f, dev::bf16_hi_f32(w[2]) * f);
+                            v[i].w = dev::pack_f16x2(dev::bf16_lo_f32(w[3]) * f, dev::bf16_hi_f32(w[3]) * f);
+                            *reinterpret_cast<uint4 *>(smem + L::q + (c / 8) * (BR * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[i];
+                        }
+                    }
+                    tc::fence_async_shared();
+                    arrive_warp(bar_q + 8 * t, lane);
+                }
+            }
+            // -- the row: its token and head, and the keys it sees.  (A row that is none,
+            // past the item's tokens or heads, goes along with the last one's keys.)
+            const int br = (two ? t * kRowTile : 0) + r;
+            const int tk = fast_div(br, p.fd_heads);
+            const bool live = tk < sg.tokens && br - tk * IH < sg.heads;
+            const int at = sg.pos + min(tk, sg.tokens - 1);  // its position
+            const int low = live ? first_key(p.shape, at) : sg.low;
+            const int end = live ? at + 1 : sg.pos + sg.tokens;
+            const int first_j = two ? (t ? sg.first1 : 0) : (ONE ? 0 : t), end_j = two && t == 0 ? sg.end0 : sg.n;
+            float m = kNegInf, l = 0.f;
+            bool begun = false;
+            const int step = ONE || two ? 1 : 2;
+            for (int j = first_j; j < end_j; j += step) {
+                const int buf = ONE ? (j & 1) : t;
+                const uint32_t ts = tmem + lanes + buf * 128;
+                if (!(ok = wait_bar(bar_s + 8 * buf, (sph >> buf) & 1, gave_up))) break;
+                sph ^= 1u << buf;
+                tc::fence_after();
+                if (KV8 && !begun) scale = row_scale[(two ? t * kRowTile : 0) + r];
+                const int nv = end - (sg.tile0 + j) * BN, nl = low - (sg.tile0 + j) * BN;
+                // -- A row's reference m is the largest score of its first tile with a key;
+                // after that no maximum is taken: weights may be as large as kLift, and
+                // only when a row's weights of a tile sum to more does its warp look
+                // at the scores again and raise m (by a whole number, so that l and O
+                // are scaled exactly).  FP32 and BF16 hold such weights as exactly as
+                // weights below 1; kLift is what f16 holds.
+                uint32_t x[BN], pk[BN / 2];
+                float sum;
+                bool fresh = live && m == kNegInf, over = false;  // rows that take, or raise, their reference now
+                bool waited = !ONE || !begun;  // the last product onto O is known to be done
+                for (int pass = 0;;) {
+                    tc::ld_columns<BN>(ts, x);
+                    if (nv < BN) mask_columns<BN>(x, nv);
+                    if (nl > 0) mask_columns_below<BN>(x, nl);
+                    if (pass == 1 || __any_sync(0xffffffffu, fresh)) {
+                        const float mx = largest_of<BN>(x) * scale;
+                        if (fresh) m = mx;
+                        if (pass == 1) {  // (the scores are read again behind this: no registers for them and O)
+                            raise_reference<DPAD>(to, mx, over, m, l);
+                            pass = 2;
+                            continue;
+                        }
+                    }
+                    sum = weigh<BN, KV8>(x, scale, m, pk);
+                    over = live && !(sum <= kLift);
+                    fresh = false;
+                    if (pass == 2 || !__any_sync(0xffffffffu, over)) break;
+                    if (!waited) {
+                        ok = wait_bar(bar_o, oph & 1, gave_up);
+                        oph ^= 1;
+                        waited = true;
+                        tc::fence_after();
+                    }
+                    pass = 1;
+                }
+                begun = true;
+                l += sum;
+                tc::st_columns<BN / 2>(ts, pk);  // over S, which has been read
+                if (ONE && !waited) {  // (each phase of the barrier is waited for, in order)
+                    ok = wait_bar(bar_o, oph & 1, gave_up) && ok;
+                    oph ^= 1;
+                }
+                if (!ok) break;
+                tc::wait_st();
+                tc::fence_before();
+                arrive_warp(bar_p + 8 * buf, lane);
+            }
+            if (!ok) break;
+
+            // -- the way out: 64 bytes of a row at a time through this warp's staging
+            // area (chunk c of row r at c xor r/2 mod 4, so that neither side hits a
+            // bank twice), four lanes a row: BF16 results, or FP32 partials.
+            uint8_t *stage = KV8 ? smem + L::q + t * (kRowTile * 128) + (warp & 3) * 4096
+                                 : smem + L::out + (t * 4 + (warp & 3)) * L::kOutBytes;
+            const int row0 = (two ? t * kRowTile : 0) + (warp & 3) * 32 + (lane >> 2);  // of the block: row0 + 8 i
+            const long long slot = 2ll * blockIdx.x + (sg.begins ? 1 : 0);
+            const int part_rows = sg.tokens * IH;
+            long long dst[4];  // of the rows' first columns in out (partials), -1: none
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + 8 * i, k = fast_div(row, p.fd_heads), h = row - k * IH;
+                if (sg.whole)
+                    dst[i] = k < sg.tokens && h < sg.heads ? (static_cast<long long>(sg.token + k) * p.num_q_heads + sg.head + h) * D : -1;
+                else
+                    dst[i] = row < part_rows ? (slot * p.slot_rows + row) * DPAD : -1;
+            }
+            // (64 bytes of this thread's row; `width` elements of them are 16 bytes)
+            auto emit = [&](uint4 a, uint4 b, uint4 c, uint4 d, int width, auto put) {
+                uint8_t *mine = stage + lane * 64;
+                const int f = (lane >> 1) & 3;
+                *reinterpret_cast<uint4 *>(mine + ((0 ^ f) << 4)) = a;
+                *reinterpret_cast<uint4 *>(mine + ((1 ^ f) << 4)) = b;
+                *reinterpret_cast<uint4 *>(mine + ((2 ^ f) << 4)) = c;
+                *reinterpret_cast<uint4 *>(mine + ((3 ^ f) << 4)) = d;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = (lane >> 2) + 8 * i;
+                    if (dst[i] >= 0)
+                        put(dst[i] + (lane & 3) * width, *reinterpret_cast<const uint4 *>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)));
+                }
+                __syncwarp();
+            };
+            // columns c to c + 31 of this thread's row, times f
+            auto store = [&](int c, const uint32_t (&x)[32], float f) {
+                if (sg.whole) {
+                    uint32_t y[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = f == 0.f ? 0u : dev::pack_bf16x2(__uint_as_float(x[2 * i]) * f, __uint_as_float(x[2 * i + 1]) * f);
+                    const bool in = c + (lane & 3) * 8 < D;
+                    emit(make_uint4(y[0], y[1], y[2], y[3]), make_uint4(y[4], y[5], y[6], y[7]), make_uint4(y[8], y[9], y[10], y[11]),
+                         make_uint4(y[12], y[13], y[14], y[15]), 8, [&](long long to_col, uint4 v) {
+                             if (in) *reinterpret_cast<uint4 *>(p.out + to_col + c) = v;
+                         });
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 16)
+                        emit(make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]), make_uint4(x[k + 4], x[k + 5], x[k + 6], x[k + 7]),
+                             make_uint4(x[k + 8], x[k + 9], x[k + 10], x[k + 11]), make_uint4(x[k + 12], x[k + 13], x[k + 14], x[k + 15]), 4,
+                             [&](long long to_col, uint4 v) { *reinterpret_cast<uint4 *>(p.part_o + to_col + c + k) = v; });
+                }
+            };
+            // the row's sum and reference: ln of the sum, or (m, l) of a partial
+            auto finish = [&](float mm, float ll) {
+                if (sg.whole) {
+                    if (p.lse && live)
+                        p.lse[static_cast<long long>(sg.token + tk) * p.num_q_heads + sg.head + (br - tk * IH)] =
+                            ll > 0.f || !(ll <= 0.f) ? (mm + log2f(ll)) * 0.6931471805599453f : kNegInf;
+                } else if (br < part_rows) {
+                    *reinterpret_cast<float2 *>(p.part_ml + (slot * p.slot_rows + br) * 2) = make_float2(mm, ll);
+                }
+            };
+            if (!sg.whole && sg.begins && tid == 128) {  // (warp 4 begins with every segment's rows 0 to 31)
+                p.cut[blockIdx.x] = {sg.token, sg.head, sg.tokens, sg.heads, sg.parts};
+                cut = true;
+            }
+            if (ONE || two) {
+                const bool some = end_j > first_j;
+                if (some) {
+                    if (!(ok = wait_bar(bar_o + 8 * t, (oph >> t) & 1, gave_up))) break;
+                    oph ^= 1u << t;
+                    tc::fence_after();
+                }
+                if (two) {  // (the other stream's phase, which this one does not wait for)
+                    if (t ? sg.end0 > 0 : sg.n > sg.first1) oph ^= 2u >> t;
+                }
+                finish(m, l);
+                const float f = l == 0.f ? 0.f : __fdiv_rn(p.v_scale, l);
+#pragma unroll 1
+                for (int c = 0; c < DPAD; c += 32) {
+                    uint32_t x[32];
+                    if (some) {
+                        tc::ld_32x32(to + c, x);
+                        tc::wait_ld(x);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = 0;
+                    }
+                    store(c, x, f);
+                }
+                tc::fence_before();
+            } else {
+                // the streams' two partials of the row, folded: each stream then writes
+                // half of the columns
+                float2 *ml = reinterpret_cast<float2 *>(smem + L::stream_ml);
+                ml[t * kRowTile + r] = make_float2(m, l);
+                arrive_warp(bar_x, lane);
+                if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
+                xph ^= 1;
+                for (int k = 0; k < 2 && ok; ++k) {
+                    if (k < sg.n) {
+                        ok = wait_bar(bar_o + 8 * k, (oph >> k) & 1, gave_up);
+                        oph ^= 1u << k;
+                    }
+                }
+                if (!ok) break;
+                tc::fence_after();
+                const float2 a = ml[r], b = ml[kRowTile + r];
+                const float M = fmaxf(a.y == 0.f ? kNegInf : a.x, b.y == 0.f ? kNegInf : b.x);
+                const float fa = a.y == 0.f ? 0.f : dev::exp2_approx(a.x - M), fb = b.y == 0.f ? 0.f : dev::exp2_approx(b.x - M);
+                const float ll = (a.y == 0.f ? 0.f : a.y * fa) + (b.y == 0.f ? 0.f : b.y * fb);
+                if (t == 0) finish(M, ll);
+                const float f = ll == 0.f ? 0.f : __fdiv_rn(p.v_scale, ll);
+#pragma unroll 1
+                for (int c = t * (DPAD / 2); c < (t + 1) * (DPAD / 2); c += 32) {
+                    uint32_t x[32], y[32];
+                    if (sg.n > 0) {
+                        tc::ld_32x32(tmem + lanes + 256 + c, x);
+                        tc::wait_ld(x);
+                    }
+                    if (sg.n > 1) {
+                        tc::ld_32x32(tmem + lanes + 256 + DPAD + c, y);
+                        tc::wait_ld(y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float xa = sg.n == 0 || fa == 0.f ? 0.f : __uint_as_float(x[i]) * fa;
+                        x[i] = __float_as_uint(sg.n > 1 && fb != 0.f ? fmaf(__uint_as_float(y[i]), fb, xa) : xa);
+                    }
+                    store(c, x, f);
+                }
+                tc::fence_before();
+                // both streams have read both O before either lets one be overwritten
+                arrive_warp(bar_x, lane);
+                if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
+                xph ^= 1;
+            }
+        }
+        if (tid == 128 && !cut) p.cut[blockIdx.x] = {0, 0, 0, 0, 0};
+    }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 1) tc::tmem_free_512(*tmem_s);
+}
+
+}  // namespace chunk
+}  // namespace pd

@@ -193,6 +193,12 @@ int report_cuda(cudaError_t e, const char *what);
 int check_shape(int num_q_heads, int num_kv_heads, int head_dim, int block_size);
 unsigned int *device_status_word(int *err);
 bool inject_alloc_failure();
+// Multiprocessors of the current device (0: none, or not to be had).
+int sm_count_of_device();
+// The tensor map of queries [num_tokens, num_heads, head_dim] with boxes of 64
+// columns x box_heads x box_tokens rows (128-byte swizzle); rows out of range read zeros.
+int encode_query_map(CUtensorMap *map, const void *q, int head_dim, int num_heads, int num_tokens, long long token_stride, int box_heads,
+                     int box_tokens);
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Dynamic shared memory a unit CTA needs (kv8: FP8 cache).

@@ -222,19 +222,6 @@ cudaError_t launch_prefix_merge(const MergeParams &p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<256>, p);
 }
 
-int sm_count_of_device() {
-    static std::mutex mu;
-    static int cached[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!cached[dev] && cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        cached[dev] = 0;
-    }
-    return cached[dev];
-}
-
 int dpad_of(int head_dim) { return head_dim <= 64 ? 64 : (head_dim <= 128 ? 128 : 256); }
 
 // Where the parts of the workspace begin, in bytes (each a multiple of 256).

@@ -125,6 +125,12 @@ _SIGS = {
     "pd_decode_attn_prefix_fp8": (_I, [_VP, _VP, _VP, ctypes.c_float, ctypes.c_float, _VP, _I, _VP, _VP, _I, _VP, _I, _VP,
                                        _VP, _I, _I, _I, _I, _I, _I, ctypes.c_float, _I, _VP, _SZ, _VP]),
     "pd_debug_prefix_walk": (_I, [_I, _I, _VP, _VP, _I, _I, _I, _I, ctypes.c_float, _I, _VP, _I, _VP, _VP, _VP]),
+    "pd_chunk_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "pd_chunk_attn": (_I, [_VP, _I64, _VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _I,
+                           _VP, _SZ, _VP]),
+    "pd_chunk_attn_fp8": (_I, [_VP, _I64, _VP, _VP, ctypes.c_float, ctypes.c_float, _VP, _I, _VP, _VP, _VP, _VP, _I, _I, _I, _I,
+                               _I, _I, _I, ctypes.c_float, _I, _VP, _SZ, _VP]),
+    "pd_debug_chunk_walk": (_I, [_I, _VP, _VP, _I, _I, _I, _I, _I, _VP, _I, _VP, _VP]),
     "pd_rope_frequencies": (_I, [_VP, _VP, _VP]),
     "pd_rope_create": (_I, [_VP, _VP]),
     "pd_rope_destroy": (None, [_VP]),
@@ -450,6 +456,51 @@ def pd_debug_prefix_walk(group_starts, prefix_lens, num_q_heads: int, num_kv_hea
                                       segments, most, ctypes.byref(n), parts, totals))
     return ([tuple(segments[10 * i:10 * i + 10]) for i in range(n.value)],
             [tuple(parts[3 * i:3 * i + 3]) for i in range(num_kv_heads * sum(rows))], tuple(totals))
+
+
+# ---- attention of new tokens over the paged cache ---------------------------------------
+
+def pd_chunk_workspace_bytes(num_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return lib().pd_chunk_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, head_dim)
+
+
+def pd_chunk_attn(q, k_cache, v_cache, block_table, context_lens, token_starts, out, lse, inv_sqrt_d: float, window: int, workspace,
+                  stream=None, num_blocks: int | None = None) -> int:
+    """out[T, Hq, D] (and lse[T, Hq], or None) <- attention of new tokens over a BF16 cache (see pd.h): q [T, Hq, D]
+    strided in tokens, token_starts [S + 1] or None (one each), the rest as for pd_decode_attn."""
+    T, Hq, D = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    S, mb = block_table.shape
+    return _check(lib().pd_chunk_attn(
+        q.data_ptr(), _token_stride(q), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb, context_lens.data_ptr(),
+        _ptr(token_starts), out.data_ptr(), _ptr(lse), T, S, Hq, Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d,
+        window, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def pd_chunk_attn_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, block_table, context_lens, token_starts, out, lse,
+                      inv_sqrt_d: float, window: int, workspace, stream=None, num_blocks: int | None = None) -> int:
+    """pd_chunk_attn over an FP8 cache (uint8 E4M3 codes, K = value * k_scale, V = value * v_scale)."""
+    T, Hq, D = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    S, mb = block_table.shape
+    return _check(lib().pd_chunk_attn_fp8(
+        q.data_ptr(), _token_stride(q), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, block_table.data_ptr(), mb,
+        context_lens.data_ptr(), _ptr(token_starts), out.data_ptr(), _ptr(lse), T, S, Hq, Hkv, D, bs,
+        nb if num_blocks is None else num_blocks, inv_sqrt_d, window, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def pd_debug_chunk_walk(token_starts, context_lens, num_q_heads: int, num_kv_heads: int, head_dim: int, window: int = 0,
+                        max_ctas: int = 152):
+    """The division of a chunk attention's work (see pd.h): (segments, totals), a list of tuples and a tuple."""
+    S = len(context_lens)
+    starts = None if token_starts is None else (ctypes.c_int32 * (S + 1))(*token_starts)
+    new = S if token_starts is None else sum(b - a for a, b in zip(token_starts, token_starts[1:]))
+    most = max_ctas + num_q_heads * (S + new)  # (an item a query head, block and sequence, and a border's cut)
+    segments, n, totals = (ctypes.c_int32 * (11 * most))(), ctypes.c_int(), (ctypes.c_int64 * 6)()
+    _check(lib().pd_debug_chunk_walk(S, starts, (ctypes.c_int32 * max(1, S))(*context_lens), num_q_heads, num_kv_heads, head_dim, window,
+                                     max_ctas, segments, most, ctypes.byref(n), totals))
+    return [tuple(segments[11 * i:11 * i + 11]) for i in range(n.value)], tuple(totals)
 
 
 # ---- rotary positions and the append to the paged cache ------------------------------

@@ -475,6 +475,46 @@ int pd_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride, in
                   const int32_t *positions, void *out, int64_t out_token_stride,
                   int64_t out_head_stride, int num_tokens, int num_heads, int inverse, void *stream);
 
+/* ---- head norms with the rotation ----------------------------------------------
+ * The RMS norm of each query or key head, which models put between the projection
+ * and the rotation, and the rotation, in one pass: a row x of head_dim columns
+ * becomes
+ *     R(x / sqrt(mean(x^2) + eps) * (weight_offset + weight)),
+ * R as above.
+ *   rope          the rotation, of the same head_dim; NULL: none.
+ *   weight        [head_dim] BF16, 16-B aligned; NULL: ones (weight_offset is ignored).
+ *   eps           finite, not negative.
+ *   weight_offset 0, or what the weight is kept relative to (1 in some models).
+ * pd_norm_rope_apply: x, out, their strides and positions as for pd_rope_apply
+ * (positions may be NULL without a rotation).  Sums and arithmetic are FP32 (a row
+ * whose mean square is above FP32's range becomes 0, and its infinities NaN), the
+ * result is rounded to BF16 once.
+ * Returns PD_OK, PD_ERR_INVALID, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
+int pd_norm_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride,
+                       int64_t x_head_stride, const void *weight, float eps, float weight_offset,
+                       const int32_t *positions, void *out, int64_t out_token_stride,
+                       int64_t out_head_stride, int num_tokens, int num_heads, int head_dim,
+                       void *stream);
+
+/* The gradients of pd_norm_rope_apply, from its x and the gradient of its out:
+ *   grad_x        [num_tokens, num_heads, head_dim] BF16, strided like an out; may be
+ *                 grad itself with grad's strides, else shares no element with it.
+ *   grad_weight   [head_dim] BF16, summed in FP32 over all rows in an order that
+ *                 only the sizes set, and rounded once (0 without a row); NULL: not
+ *                 wanted.
+ *   workspace     >= pd_norm_rope_workspace_bytes(head_dim) bytes, 16-B aligned, for
+ *                 grad_weight; contents ignored on entry, scratch on return.
+ * Returns PD_OK, PD_ERR_INVALID, PD_ERR_WORKSPACE, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
+size_t pd_norm_rope_workspace_bytes(int head_dim);
+
+int pd_norm_rope_backward(const pd_rope *rope, const void *x, int64_t x_token_stride,
+                          int64_t x_head_stride, const void *weight, float eps,
+                          float weight_offset, const int32_t *positions, const void *grad,
+                          int64_t grad_token_stride, int64_t grad_head_stride, void *grad_x,
+                          int64_t grad_x_token_stride, int64_t grad_x_head_stride,
+                          void *grad_weight, int num_tokens, int num_heads, int head_dim,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- append to the paged cache ---------------------------------------------
  * Put new tokens' keys and values into the paged cache pd_decode_attn reads,
  * rotating the keys, and the queries on the way, by their positions.
@@ -526,6 +566,26 @@ int pd_append_kv_fp8(const pd_rope *rope, const void *q, int64_t q_token_stride,
                      const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens,
                      const int32_t *token_starts, int num_tokens, int num_seqs, int num_q_heads,
                      int num_kv_heads, int head_dim, int block_size, int num_blocks, void *stream);
+
+/* pd_append_kv, and pd_append_kv_fp8, with the norm of each head of q (q_weight) and k
+ * (k_weight) before the rotation: eps, weight_offset and the weights are those of
+ * pd_norm_rope_apply, everything else is the append's. */
+int pd_append_kv_normed(const pd_rope *rope, const void *q, int64_t q_token_stride, const void *k,
+                        int64_t k_token_stride, const void *v, int64_t v_token_stride,
+                        const void *q_weight, const void *k_weight, float eps, float weight_offset,
+                        void *q_out, void *k_cache, void *v_cache, const int32_t *block_table,
+                        int max_blocks_per_seq, const int32_t *context_lens,
+                        const int32_t *token_starts, int num_tokens, int num_seqs, int num_q_heads,
+                        int num_kv_heads, int head_dim, int block_size, int num_blocks, void *stream);
+
+int pd_append_kv_normed_fp8(const pd_rope *rope, const void *q, int64_t q_token_stride, const void *k,
+                            int64_t k_token_stride, const void *v, int64_t v_token_stride,
+                            const void *q_weight, const void *k_weight, float eps, float weight_offset,
+                            void *q_out, void *k_cache, void *v_cache, float k_scale, float v_scale,
+                            const int32_t *block_table, int max_blocks_per_seq,
+                            const int32_t *context_lens, const int32_t *token_starts, int num_tokens,
+                            int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                            int block_size, int num_blocks, void *stream);
 
 /* ---- tiled decode (tiled_attention.rs page) ------------------------------ */
 

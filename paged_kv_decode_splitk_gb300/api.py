@@ -170,6 +170,13 @@ def _check_rope(rotation, x, positions, out, dev: int) -> None:
         _rows("out", out, T, H, D, dev, False)
 
 
+def _laid_out(grad):
+    """grad [T, H, D], its rows laid out anew where it comes broadcast, transposed or at an odd place."""
+    if grad.data_ptr() % 16 or grad.stride(2) != 1 or any(n > 1 and (s <= 0 or s % 8) for n, s in zip(grad.shape[:2], grad.stride())):
+        return grad.clone(memory_format=torch.contiguous_format)
+    return grad
+
+
 class _Rotation(torch.autograd.Function):
     """rope where x requires a gradient, which is the transposed map's value."""
 
@@ -182,10 +189,7 @@ class _Rotation(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         (positions,) = ctx.saved_tensors
-        # (a gradient may come broadcast, transposed or at an odd place: then its rows are laid out anew)
-        if grad.data_ptr() % 16 or grad.stride(2) != 1 or any(n > 1 and (s <= 0 or s % 8) for n, s in zip(grad.shape[:2], grad.stride())):
-            grad = grad.clone(memory_format=torch.contiguous_format)
-        return rope(ctx.rotation, grad, positions, inverse=not ctx.inverse), None, None, None, None
+        return rope(ctx.rotation, _laid_out(grad), positions, inverse=not ctx.inverse), None, None, None, None
 
 
 def rope(rotation: pd.Rope, x, positions, out=None, inverse: bool = False, stream=None):
@@ -253,6 +257,107 @@ def append_kv(rotation, q, k, v, k_cache, v_cache, block_table, context_lens, to
                             token_starts, stream)
     else:
         pd.pd_append_kv(rotation, q, k, v, q_out, k_cache, v_cache, block_table, context_lens, token_starts, stream)
+    return q_out
+
+
+def _weight(name: str, t, head_dim: int, device: int) -> None:
+    if t is not None and not (t.dtype is _BF16 and t.shape == (head_dim,) and t.is_contiguous() and t.get_device() == device):
+        _refuse(name, t, "contiguous BF16", (head_dim,), device)
+
+
+def _check_norm(rotation, x, weight, positions, dev: int) -> None:
+    _rows("x", x, None, None, rotation.head_dim if rotation is not None else (x.shape[-1] if x.dim() == 3 else None), dev, False)
+    _weight("weight", weight, x.shape[2], dev)
+    if rotation is not None:
+        if positions is None:
+            raise ValueError("positions: a rotation wants them")
+        _indices("positions", positions, (x.shape[0],), dev)
+    elif positions is not None:
+        raise ValueError("positions without a rotation")
+
+
+class _NormRotation(torch.autograd.Function):
+    """norm_rope where x or weight requires a gradient."""
+
+    @staticmethod
+    def forward(ctx, x, weight, rotation, positions, eps, weight_offset, stream):
+        ctx.rotation, ctx.eps, ctx.offset = rotation, eps, weight_offset
+        ctx.save_for_backward(x, weight, positions)
+        return norm_rope(rotation, x, weight, positions, eps, weight_offset, stream=stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        x, weight, positions = ctx.saved_tensors
+        dx, dw = norm_rope_backward(ctx.rotation, x, weight, positions, _laid_out(grad), ctx.eps, ctx.offset,
+                                    weight_grad=ctx.needs_input_grad[1])
+        return dx if ctx.needs_input_grad[0] else None, dw, None, None, None, None, None
+
+
+def norm_rope(rotation, x, weight, positions, eps: float = 1e-6, weight_offset: float = 0.0, out=None, stream=None):
+    """The RMS norm of each head and the rotary positions in one pass: each row of x [T, H, D] BF16 (strided in tokens and heads,
+    e.g. the q or the k heads of a fused projection) over its root mean square (eps under the root) times weight_offset +
+    weight [D] (None: ones), rotated by positions [T] int32 (rotation and positions None: the norm alone).  Returns out
+    [T, H, D] (contiguous unless given; x itself works in place).  Where x or weight requires a gradient, autograd calls
+    norm_rope_backward (out cannot be given then; a backward pass is captured into a graph, as torch wants it, while no eager
+    graph of the same leaves lives)."""
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)):
+        if out is not None:
+            raise ValueError("out: no gradient can pass through a tensor that is given; call under torch.no_grad() or let norm_rope make it")
+        return _NormRotation.apply(x, weight, rotation, positions, eps, weight_offset, stream)
+    if stream is None:
+        done = pd.quick().norm_rope(pd._handle(rotation) or 0, 0 if rotation is None else rotation.head_dim, x, weight, positions, out, eps,
+                                    weight_offset)
+        if done is not NotImplemented:
+            return done
+    dev = pd.current_device()
+    _check_norm(rotation, x, weight, positions, dev)
+    if out is not None:
+        _rows("out", out, *x.shape, dev, False)
+    else:
+        out = _fresh(x.shape, _BF16, x.device, stream)
+    pd.pd_norm_rope_apply(rotation, x, weight, positions, out, eps, weight_offset, stream)
+    return out
+
+
+def norm_rope_backward(rotation, x, weight, positions, grad, eps: float = 1e-6, weight_offset: float = 0.0, weight_grad: bool = True,
+                       stream=None):
+    """The gradients of norm_rope from the gradient of its out [T, H, D]: (grad_x [T, H, D], grad_weight [D]), the second None
+    where it is not wanted or there is no weight."""
+    dev = pd.current_device()
+    _check_norm(rotation, x, weight, positions, dev)
+    _rows("grad", grad, *x.shape, dev, False)
+    grad_x = _fresh(x.shape, _BF16, x.device, stream)
+    grad_weight = ws = None
+    if weight_grad and weight is not None:
+        grad_weight = _fresh(weight.shape, _BF16, x.device, stream)
+        ws = _fresh(pd.pd_norm_rope_workspace_bytes(x.shape[2]), _U8, x.device, stream)
+    pd.pd_norm_rope_backward(rotation, x, weight, positions, grad, grad_x, grad_weight, ws, eps, weight_offset, stream)
+    return grad_x, grad_weight
+
+
+def append_kv_normed(rotation, q, k, v, q_weight, k_weight, k_cache, v_cache, block_table, context_lens, token_starts=None, q_out=None,
+                     eps: float = 1e-6, weight_offset: float = 0.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """append_kv with the RMS norm of each head of q and k, as norm_rope's, before the rotation: q_weight and k_weight [D] BF16
+    (None: ones).  Everything else, the rows that get nothing among it, is append_kv's."""
+    if stream is None and q is not None:
+        done = pd.quick().append_kv_normed(pd._handle(rotation) or 0, 0 if rotation is None else rotation.head_dim, q, k, v, q_weight,
+                                           k_weight, k_cache, v_cache, block_table, context_lens, token_starts, q_out, eps, weight_offset,
+                                           k_scale, v_scale)
+        if done is not NotImplemented:
+            return done
+    dev = pd.current_device()
+    _check_append(q, k, v, k_cache, v_cache, block_table, context_lens, token_starts, q_out, dev)
+    _weight("q_weight", q_weight, k.shape[2], dev)
+    _weight("k_weight", k_weight, k.shape[2], dev)
+    if q is not None and q_out is None:
+        q_out = _fresh(q.shape, _BF16, q.device, stream)
+    if k_cache.dtype is _U8:
+        pd.pd_append_kv_normed_fp8(rotation, q, k, v, q_weight, k_weight, q_out, k_cache, v_cache, k_scale, v_scale, block_table,
+                                   context_lens, token_starts, eps, weight_offset, stream)
+    else:
+        pd.pd_append_kv_normed(rotation, q, k, v, q_weight, k_weight, q_out, k_cache, v_cache, block_table, context_lens, token_starts, eps,
+                               weight_offset, stream)
     return q_out
 
 

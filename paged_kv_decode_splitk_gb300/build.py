@@ -25,7 +25,7 @@ LIB = os.path.join(BUILD, "libpd.so")
 BINDING = os.path.join(BUILD, "pd_binding.so")
 
 SOURCES = ["pd_api.cu", "pd_small.cu", "pd_unit_d64.cu", "pd_unit_d128.cu", "pd_unit_d256.cu",
-           "pd_unit_fp8_d64.cu", "pd_unit_fp8_d128.cu", "pd_unit_fp8_d256.cu", "pd_noalloc.cu", "pd_rope.cu",
+           "pd_unit_fp8_d64.cu", "pd_unit_fp8_d128.cu", "pd_unit_fp8_d256.cu", "pd_noalloc.cu", "pd_rope.cu", "pd_norm.cu",
            "pd_unit_own_d64.cu", "pd_unit_own_d128.cu", "pd_unit_own_d256.cu", "pd_prefix.cu", "pd_prefix_d64.cu",
            "pd_prefix_d128.cu", "pd_prefix_d256.cu", "pd_chunk.cu", "pd_chunk_d64.cu", "pd_chunk_d128.cu", "pd_chunk_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

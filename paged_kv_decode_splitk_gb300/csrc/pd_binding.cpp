@@ -120,41 +120,113 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// A norm's weight, or null for None.
+const void *weight(PyObject *o, int64_t head_dim, int dev) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = whole(o, 1, at::kBFloat16, dev);
+    need(t.size(0) == head_dim);
+    return t.data_ptr();
+}
+
+// norm_rope(handle | 0, head_dim, x, weight | None, positions | None, out | None, eps, weight_offset)
+PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return quick(n, 8, [&] {
+        const int dev = device();
+        const auto handle = reinterpret_cast<const pd_rope *>(integer(a[0]));
+        const Rows x = rows(a[2], dev, false);
+        const void *w = weight(a[3], x.D, dev);
+        const float eps = real(a[6]), offset = real(a[7]);
+        const int32_t *positions = nullptr;
+        need((handle != nullptr) == (a[4] != Py_None));
+        if (handle) {
+            const at::Tensor &t = whole(a[4], 1, at::kInt, dev);
+            need(x.D == integer(a[1]) && t.size(0) == x.T);
+            positions = ints(t);
+        }
+        at::Tensor made;
+        Rows o;
+        if (a[5] == Py_None) {
+            made = fresh(x.t->sizes(), at::kBFloat16, dev);
+            o = {&made, x.T, x.H, x.D, x.H * x.D, x.D};
+        } else {
+            o = rows(a[5], dev, false);
+            need(o.T == x.T && o.H == x.H && o.D == x.D);
+        }
+        need(pd_norm_rope_apply(handle, x.data(), x.token, x.head, w, eps, offset, positions, o.data(), o.token, o.head, fits(x.T),
+                                fits(x.H), fits(x.D), stream(dev)) == PD_OK);
+        return answer(a[5], made);
+    });
+}
+
+// What append_kv and append_kv_normed have in common: the tensors from q (a[0]) to v, the caches to q_out, and the scales.
+struct Append {
+    Rows q, k, v;
+    const at::Tensor *kc, *vc, *table;
+    const int32_t *lens, *starts = nullptr;
+    at::Tensor made;
+    const at::Tensor *out;
+    float ks, vs;
+    int T, S, Hq, H, D, bs, nb, mb;
+    // rows: of q, k, v; caches: of k_cache, v_cache, block_table, context_lens, token_starts | None, q_out | None
+    Append(PyObject *const *rows_of, PyObject *const *caches, PyObject *k_scale, PyObject *v_scale, int dev)
+        : q(rows(rows_of[0], dev, true)), k(rows(rows_of[1], dev, true)), v(rows(rows_of[2], dev, true)), kc(&cache(caches[0], dev)),
+          vc(&cache(caches[1], dev)), table(&whole(caches[2], 2, at::kInt, dev)), ks(real(k_scale)), vs(real(v_scale)) {
+        const at::Tensor &l = whole(caches[3], 1, at::kInt, dev);
+        need(v.T == k.T && v.H == k.H && v.D == k.D && q.T == k.T && q.D == k.D && kc->scalar_type() == vc->scalar_type() &&
+             kc->sizes() == vc->sizes() && kc->size(2) == k.H && kc->size(3) == k.D && table->size(0) == l.size(0));
+        lens = ints(l);
+        if (caches[4] != Py_None) {
+            const at::Tensor &t = whole(caches[4], 1, at::kInt, dev);
+            need(t.size(0) == l.size(0) + 1);
+            starts = ints(t);
+        }
+        if (caches[5] == Py_None) made = fresh(q.t->sizes(), at::kBFloat16, dev);
+        out = caches[5] == Py_None ? &made : &whole(caches[5], 3, at::kBFloat16, dev);
+        need(out->sizes() == q.t->sizes());
+        T = fits(k.T), S = fits(l.size(0)), Hq = fits(q.H), H = fits(k.H), D = fits(k.D), bs = fits(kc->size(1)), nb = fits(kc->size(0)),
+        mb = fits(table->size(1));
+    }
+    bool fp8() const { return kc->scalar_type() == at::kByte; }
+};
+
 // append_kv(handle | 0, head_dim, q, k, v, k_cache, v_cache, block_table, context_lens, token_starts | None,
 //           q_out | None, k_scale, v_scale) -- with queries
 PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return quick(n, 13, [&] {
         const int dev = device();
         const auto handle = reinterpret_cast<const pd_rope *>(integer(a[0]));
-        const Rows q = rows(a[2], dev, true), k = rows(a[3], dev, true), v = rows(a[4], dev, true);
-        const at::Tensor &kc = cache(a[5], dev), &vc = cache(a[6], dev);
-        const at::Tensor &table = whole(a[7], 2, at::kInt, dev), &lens = whole(a[8], 1, at::kInt, dev);
-        const float ks = real(a[11]), vs = real(a[12]);
-        const int64_t S = lens.size(0);
-        need((!handle || k.D == integer(a[1])) && v.T == k.T && v.H == k.H && v.D == k.D && q.T == k.T && q.D == k.D &&
-             kc.scalar_type() == vc.scalar_type() && kc.sizes() == vc.sizes() && kc.size(2) == k.H && kc.size(3) == k.D &&
-             table.size(0) == S);
-        const int32_t *starts = nullptr;
-        if (a[9] != Py_None) {
-            const at::Tensor &t = whole(a[9], 1, at::kInt, dev);
-            need(t.size(0) == S + 1);
-            starts = ints(t);
-        }
-        at::Tensor made;
-        if (a[10] == Py_None) made = fresh(q.t->sizes(), at::kBFloat16, dev);
-        const at::Tensor &out = a[10] == Py_None ? made : whole(a[10], 3, at::kBFloat16, dev);
-        need(out.sizes() == q.t->sizes());
-        const int T = fits(k.T), Hq = fits(q.H), H = fits(k.H), D = fits(k.D), bs = fits(kc.size(1)), nb = fits(kc.size(0)),
-                  mb = fits(table.size(1)), seqs = fits(S);
-        const int rc = kc.scalar_type() == at::kByte
-                           ? pd_append_kv_fp8(handle, q.data(), q.token, k.data(), k.token, v.data(), v.token, out.data_ptr(),
-                                              kc.data_ptr(), vc.data_ptr(), ks, vs, ints(table), mb, ints(lens), starts, T, seqs, Hq,
-                                              H, D, bs, nb, stream(dev))
-                           : pd_append_kv(handle, q.data(), q.token, k.data(), k.token, v.data(), v.token, out.data_ptr(),
-                                          kc.data_ptr(), vc.data_ptr(), ints(table), mb, ints(lens), starts, T, seqs, Hq, H, D, bs,
-                                          nb, stream(dev));
+        const Append p(a + 2, a + 5, a[11], a[12], dev);
+        need(!handle || p.D == integer(a[1]));
+        const int rc = p.fp8() ? pd_append_kv_fp8(handle, p.q.data(), p.q.token, p.k.data(), p.k.token, p.v.data(), p.v.token,
+                                                  p.out->data_ptr(), p.kc->data_ptr(), p.vc->data_ptr(), p.ks, p.vs, ints(*p.table), p.mb,
+                                                  p.lens, p.starts, p.T, p.S, p.Hq, p.H, p.D, p.bs, p.nb, stream(dev))
+                               : pd_append_kv(handle, p.q.data(), p.q.token, p.k.data(), p.k.token, p.v.data(), p.v.token,
+                                              p.out->data_ptr(), p.kc->data_ptr(), p.vc->data_ptr(), ints(*p.table), p.mb, p.lens, p.starts,
+                                              p.T, p.S, p.Hq, p.H, p.D, p.bs, p.nb, stream(dev));
         need(rc == PD_OK);
-        return answer(a[10], made);
+        return answer(a[10], p.made);
+    });
+}
+
+// append_kv_normed(handle | 0, head_dim, q, k, v, q_weight | None, k_weight | None, k_cache, v_cache, block_table,
+//                  context_lens, token_starts | None, q_out | None, eps, weight_offset, k_scale, v_scale) -- with queries
+PyObject *append_kv_normed(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return quick(n, 17, [&] {
+        const int dev = device();
+        const auto handle = reinterpret_cast<const pd_rope *>(integer(a[0]));
+        const Append p(a + 2, a + 7, a[15], a[16], dev);
+        need(!handle || p.D == integer(a[1]));
+        const void *qw = weight(a[5], p.D, dev), *kw = weight(a[6], p.D, dev);
+        const float eps = real(a[13]), offset = real(a[14]);
+        const int rc =
+            p.fp8() ? pd_append_kv_normed_fp8(handle, p.q.data(), p.q.token, p.k.data(), p.k.token, p.v.data(), p.v.token, qw, kw, eps,
+                                              offset, p.out->data_ptr(), p.kc->data_ptr(), p.vc->data_ptr(), p.ks, p.vs, ints(*p.table), p.mb,
+                                              p.lens, p.starts, p.T, p.S, p.Hq, p.H, p.D, p.bs, p.nb, stream(dev))
+                    : pd_append_kv_normed(handle, p.q.data(), p.q.token, p.k.data(), p.k.token, p.v.data(), p.v.token, qw, kw, eps, offset,
+                                          p.out->data_ptr(), p.kc->data_ptr(), p.vc->data_ptr(), ints(*p.table), p.mb, p.lens, p.starts, p.T,
+                                          p.S, p.Hq, p.H, p.D, p.bs, p.nb, stream(dev));
+        need(rc == PD_OK);
+        return answer(a[12], p.made);
     });
 }
 
@@ -250,7 +322,8 @@ template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
-PyMethodDef methods[] = {method<rope>("rope"), method<append_kv>("append_kv"), method<decode_attn_prefix>("decode_attn_prefix"),
+PyMethodDef methods[] = {method<rope>("rope"), method<append_kv>("append_kv"), method<norm_rope>("norm_rope"),
+                         method<append_kv_normed>("append_kv_normed"), method<decode_attn_prefix>("decode_attn_prefix"),
                          method<chunk_attn>("chunk_attn"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "pd_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

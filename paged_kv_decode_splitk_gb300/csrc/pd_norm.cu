@@ -1,0 +1,651 @@
+// pd_norm.cu -- the RMS norm of each query or key head with the position rotation in
+// the same pass (pd_norm_rope_*), and both on the way into the paged cache
+// (pd_append_kv_normed[_fp8]): host side and kernels.
+//
+// Mathematics.  A row x of D columns becomes
+//   y = R (x r w'),  r = 1 / sqrt(sum x^2 / D + eps),  w' = offset + w,
+// with R the rotation by the row's position (its factor among it).  With
+// u = R^T dy (the transposed rotation of the gradient) and the sums over the row,
+//   dx = r (u w' - x r^2 sum(x u w') / D),   dw = sum over rows of u x r.
+//
+// A row is held by D / 8 lanes (rounded up to 8, 16 or 32), 8 columns each, in one
+// 16-byte load.  The sums go across its lanes by shuffles; the other column of a pair
+// is in the lane itself (neighbours) or comes through shared memory (halves apart), so
+// every rotation loads and stores whole 16 bytes.  Sines and cosines are those of the
+// block's tokens from a table in shared memory, as in pd_rope.cu, and a lane walks
+// several heads of its token with them.  All arithmetic is FP32; a result is rounded
+// once.  dw is summed in a fixed order: a lane's rows, the rows of a block, the blocks.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+#include "pd.h"
+#include "pd_device.cuh"
+#include "pd_internal.h"
+#include "pd_rope.cuh"
+
+namespace pd {
+namespace {
+
+using namespace rope;
+
+constexpr int kNormThreads = kRopeThreads;
+constexpr int kGradBlocks = 152 * 4;  // blocks of the backward pass at most
+constexpr int kGradRows = 2;          // heads a lane takes at a time there
+
+// How a row's pairs lie in its lanes' 8 columns: NEIGHBOURS whole in a lane (also
+// where nothing turns), HALVES 8 columns with 8 others, SCATTERED anywhere.
+enum Pairs { kNeighbours, kHalves, kScattered };
+
+struct Norm {
+    const __nv_bfloat16 *weight;  // null: 1 (with offset 0)
+    float offset, eps, inv_dim;
+    int head_dim;
+};
+
+struct NormParams {
+    RowPlan plan;   // units: lanes of a row
+    Norm norm;
+    const __nv_bfloat16 *x;
+    __nv_bfloat16 *out;
+    long long x_tok, x_head, o_tok, o_head;
+    const int32_t *positions;
+    int heads;
+    int threads;    // tokens * slots * units
+};
+
+struct GradParams {
+    RowPlan plan;   // (its sign makes the rotation the transposed one)
+    Norm norm;
+    const __nv_bfloat16 *x, *g;
+    __nv_bfloat16 *dx;
+    long long x_tok, x_head, g_tok, g_head, d_tok, d_head;
+    const int32_t *positions;
+    int heads;
+    int threads;
+    float *part;    // [blocks][lanes * 8]: sums of dw; null: not wanted
+};
+
+struct NormAppendParams {
+    RowPlan plan;
+    Norm norm;      // (of q)
+    const __nv_bfloat16 *k_weight;
+    const __nv_bfloat16 *q, *k, *v;
+    long long q_tok, k_tok, v_tok;
+    __nv_bfloat16 *q_out;
+    void *k_cache, *v_cache;
+    float k_scale, v_scale;   // of a code: 1 over the cache's scales
+    const int32_t *block_table, *context_lens, *token_starts;
+    int max_blocks, num_seqs, num_blocks;
+    int q_heads, kv_heads;
+    FastDiv block_size;
+    int threads;
+    unsigned int *status;
+};
+
+__device__ __forceinline__ void widen(const uint4 &v, float (&f)[8]) {
+    f[0] = dev::bf16_lo_f32(v.x), f[1] = dev::bf16_hi_f32(v.x), f[2] = dev::bf16_lo_f32(v.y), f[3] = dev::bf16_hi_f32(v.y);
+    f[4] = dev::bf16_lo_f32(v.z), f[5] = dev::bf16_hi_f32(v.z), f[6] = dev::bf16_lo_f32(v.w), f[7] = dev::bf16_hi_f32(v.w);
+}
+__device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+    return make_uint4(dev::pack_bf16x2(f[0], f[1]), dev::pack_bf16x2(f[2], f[3]), dev::pack_bf16x2(f[4], f[5]),
+                      dev::pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void load_weight(const __nv_bfloat16 *w, float offset, int d0, bool in, float (&f)[8]) {
+    if (w && in) {
+        widen(*reinterpret_cast<const uint4 *>(w + d0), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] += offset;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 1.f;
+    }
+}
+// The sum over a row's lanes.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// The turns of a lane's 8 columns: out = c y + s (the pair's other column), on the
+// columns of `live`; the others are copied.
+template <int LANES, Pairs PAIRS>
+struct Turns {
+    float c[8], s[8];
+    uint32_t live;
+    int other;        // kHalves: the column that pairs with the lane's first
+    int half;
+
+    __device__ __forceinline__ void load(const RowPlan &p, const TurnTable &tab, int token, int d0) {
+        live = 0;
+        other = 0;
+        half = p.half;
+        const float *cos = tab.c + token * p.pitch, *sin = cos + tab.span;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int col = d0 + i, pair = PAIRS == kNeighbours ? col / 2 : (col < half ? col : col - half);
+            const bool upper = PAIRS == kNeighbours ? i & 1 : col >= half;
+            const bool in = pair < half;
+            c[i] = in ? cos[pair] : 1.f;
+            s[i] = in ? (upper ? sin[pair] : -sin[pair]) : 0.f;
+            live |= in ? 1u << i : 0u;
+        }
+        if (PAIRS == kHalves) other = live ? (d0 < half ? d0 + half : d0 - half) : d0;
+    }
+    // `row`: the row's LANES * 8 floats of shared memory, columns 0 to 3 of every 8 first
+    // (so that 16-byte accesses of neighbouring lanes meet no bank twice).  All lanes
+    // of the warp take part.
+    __device__ __forceinline__ void apply(float (&y)[8], float *row, int d0) const {
+        float z[8];
+        if constexpr (PAIRS == kNeighbours) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = y[i ^ 1];
+        } else {
+            __syncwarp();
+            *reinterpret_cast<float4 *>(row + d0 / 2) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4 *>(row + LANES * 4 + d0 / 2) = make_float4(y[4], y[5], y[6], y[7]);
+            __syncwarp();
+            if constexpr (PAIRS == kHalves) {
+                const float4 a = *reinterpret_cast<const float4 *>(row + other / 2);
+                const float4 b = *reinterpret_cast<const float4 *>(row + LANES * 4 + other / 2);
+                z[0] = a.x, z[1] = a.y, z[2] = a.z, z[3] = a.w, z[4] = b.x, z[5] = b.y, z[6] = b.z, z[7] = b.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int col = d0 + i, from = (live >> i) & 1 ? (col < half ? col + half : col - half) : col;
+                    z[i] = row[(from & 4) * LANES + (from >> 3) * 4 + (from & 3)];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((live >> i) & 1) y[i] = fmaf(y[i], c[i], z[i] * s[i]);
+    }
+};
+
+// A thread's place: its line of lanes, the line's token and first head.
+template <int LANES>
+struct Place {
+    int d0, line, tok, slot, first, last;  // (first, last: of the block's tokens)
+    bool in, cols;
+    __device__ __forceinline__ Place(const RowPlan &p, int block, int threads, int head_dim) {
+        const int id = block * kNormThreads + threadIdx.x, n = id / LANES;
+        d0 = threadIdx.x % LANES * 8;
+        line = threadIdx.x / LANES;
+        tok = fast_div(n, p.slots);
+        slot = n - tok * static_cast<int>(p.slots.d);
+        first = fast_div(block * kNormThreads / LANES, p.slots);
+        last = fast_div((min(block * kNormThreads + kNormThreads, threads) - 1) / LANES, p.slots);
+        in = id < threads;
+        cols = d0 < head_dim;
+    }
+};
+
+template <int LANES, Pairs PAIRS, int ROWS>
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float rows[PAIRS == kNeighbours ? 1 : kNormThreads * 8];
+    dev::griddep_launch_dependents();
+    const Place<LANES> at(p.plan, blockIdx.x, p.threads, p.norm.head_dim);
+    const TurnTable tab = {turn_smem, (at.last - at.first + 1) * p.plan.pitch};
+    const int step = static_cast<int>(p.plan.slots.d);
+    dev::griddep_wait();
+    uint4 v[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int h = at.slot + r * step;
+        v[r] = make_uint4(0, 0, 0, 0);
+        if (at.in && at.cols && h < p.heads) v[r] = *reinterpret_cast<const uint4 *>(p.x + at.tok * p.x_tok + h * p.x_head + at.d0);
+    }
+    for (int e = threadIdx.x; e < (at.last - at.first + 1) * p.plan.half; e += kNormThreads) {
+        const int j = fast_div(e, p.plan.fd_half);
+        fill_turn(p.plan, tab, e + j * (p.plan.pitch - p.plan.half), e - j * p.plan.half, p.positions[at.first + j]);
+    }
+    float w[8];
+    load_weight(p.norm.weight, p.norm.offset, at.d0, at.cols, w);
+    __syncthreads();
+    Turns<LANES, PAIRS> turns;
+    turns.load(p.plan, tab, min(at.tok, at.last) - at.first, at.d0);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int h = at.slot + r * step;
+        float y[8], sum = 0.f;
+        widen(v[r], y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+        const float scale = rsqrtf(fmaf(row_sum<LANES>(sum), p.norm.inv_dim, p.norm.eps));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= scale * w[i];
+        turns.apply(y, rows + (PAIRS == kNeighbours ? 0 : at.line * (LANES * 8)), at.d0);
+        if (at.in && at.cols && h < p.heads) *reinterpret_cast<uint4 *>(p.out + at.tok * p.o_tok + h * p.o_head + at.d0) = narrow(y);
+    }
+}
+
+template <int LANES, Pairs PAIRS>
+__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const __grid_constant__ GradParams p) {
+    __shared__ float rows[kNormThreads * 8];
+    dev::griddep_launch_dependents();
+    const int blocks = (p.threads + kNormThreads - 1) / kNormThreads, step = static_cast<int>(p.plan.slots.d);
+    dev::griddep_wait();
+    float w[8], dw[8] = {};
+    load_weight(p.norm.weight, p.norm.offset, threadIdx.x % LANES * 8, threadIdx.x % LANES * 8 < p.norm.head_dim, w);
+    for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
+        const Place<LANES> at(p.plan, b, p.threads, p.norm.head_dim);
+        const TurnTable tab = {turn_smem, (at.last - at.first + 1) * p.plan.pitch};
+        uint4 vx[kGradRows], vg[kGradRows];
+#pragma unroll
+        for (int r = 0; r < kGradRows; ++r) {
+            const int h = at.slot + r * step;
+            vx[r] = vg[r] = make_uint4(0, 0, 0, 0);
+            if (at.in && at.cols && h < p.heads) {
+                vx[r] = *reinterpret_cast<const uint4 *>(p.x + at.tok * p.x_tok + h * p.x_head + at.d0);
+                vg[r] = *reinterpret_cast<const uint4 *>(p.g + at.tok * p.g_tok + h * p.g_head + at.d0);
+            }
+        }
+        if (b != static_cast<int>(blockIdx.x)) __syncthreads();  // (the last turn's table has been read)
+        for (int e = threadIdx.x; e < (at.last - at.first + 1) * p.plan.half; e += kNormThreads) {
+            const int j = fast_div(e, p.plan.fd_half);
+            fill_turn(p.plan, tab, e + j * (p.plan.pitch - p.plan.half), e - j * p.plan.half, p.positions[at.first + j]);
+        }
+        __syncthreads();
+        Turns<LANES, PAIRS> turns;
+        turns.load(p.plan, tab, min(at.tok, at.last) - at.first, at.d0);
+#pragma unroll
+        for (int r = 0; r < kGradRows; ++r) {
+            const int h = at.slot + r * step;
+            float x[8], u[8], xx = 0.f, xu = 0.f;
+            widen(vx[r], x);
+            widen(vg[r], u);
+            turns.apply(u, rows + at.line * (LANES * 8), at.d0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                xx = fmaf(x[i], x[i], xx);
+                xu = fmaf(x[i] * u[i], w[i], xu);
+            }
+            const float scale = rsqrtf(fmaf(row_sum<LANES>(xx), p.norm.inv_dim, p.norm.eps));
+            const float back = row_sum<LANES>(xu) * p.norm.inv_dim * scale * scale;
+            if (at.in && at.cols && h < p.heads) {
+                float d[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    d[i] = scale * fmaf(-back, x[i], u[i] * w[i]);
+                    dw[i] = fmaf(u[i], x[i] * scale, dw[i]);
+                }
+                *reinterpret_cast<uint4 *>(p.dx + at.tok * p.d_tok + h * p.d_head + at.d0) = narrow(d);
+            }
+        }
+    }
+    if (!p.part) return;
+    __syncthreads();
+    *reinterpret_cast<float4 *>(rows + threadIdx.x * 8) = make_float4(dw[0], dw[1], dw[2], dw[3]);
+    *reinterpret_cast<float4 *>(rows + threadIdx.x * 8 + 4) = make_float4(dw[4], dw[5], dw[6], dw[7]);
+    __syncthreads();
+    if (threadIdx.x < LANES * 8) {
+        float sum = 0.f;
+#pragma unroll
+        for (int l = 0; l < kNormThreads / LANES; ++l) sum += rows[l * (LANES * 8) + threadIdx.x];
+        p.part[static_cast<long long>(blockIdx.x) * (LANES * 8) + threadIdx.x] = sum;
+    }
+}
+
+// dw of 32 columns: 32 lines of threads sum the blocks' parts, every 32nd each, and the
+// lines are summed in order.
+__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *part, int blocks, int pitch, int head_dim, __nv_bfloat16 *dw) {
+    __shared__ float sums[32][33];
+    dev::griddep_launch_dependents();
+    dev::griddep_wait();
+    const int col = blockIdx.x * 32 + threadIdx.x;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int b = threadIdx.y; b < blocks; b += 32) sum += part[static_cast<long long>(b) * pitch + col];
+    sums[threadIdx.y][threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+    for (int i = 1; i < 32; ++i) sum += sums[i][threadIdx.x];
+    if (col < head_dim) dw[col] = __float2bfloat16_rn(sum);
+}
+
+template <int LANES, Pairs PAIRS, bool KV8, int ROWS>
+__global__ void __launch_bounds__(kNormThreads) norm_append_kernel(const __grid_constant__ NormAppendParams p) {
+    __shared__ float rows_s[PAIRS == kNeighbours ? 1 : kNormThreads * 8];
+    __shared__ int place[kNormThreads / LANES + 2][2];  // of the block's tokens: position (-1: left out) and cache block (-1: none)
+    dev::griddep_launch_dependents();
+    const int D = p.norm.head_dim, rows = p.q_heads + 2 * p.kv_heads, lane = threadIdx.x & 31;
+    const Place<LANES> at(p.plan, blockIdx.x, p.threads, D);
+    const int count = at.last - at.first + 1, step = static_cast<int>(p.plan.slots.d);
+    const TurnTable tab = {turn_smem, count * p.plan.pitch};
+    dev::griddep_wait();
+    uint4 v[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int h = at.slot + r * step;
+        v[r] = make_uint4(0, 0, 0, 0);
+        if (at.in && at.cols && h < rows) {
+            const int hk = h - p.q_heads, hv = hk - p.kv_heads;
+            const __nv_bfloat16 *src = hk < 0   ? p.q + at.tok * p.q_tok + h * D
+                                       : hv < 0 ? p.k + at.tok * p.k_tok + hk * D
+                                                : p.v + at.tok * p.v_tok + hv * D;
+            v[r] = *reinterpret_cast<const uint4 *>(src + at.d0);
+        }
+    }
+    find_places(p, at.first, count, lane, place);
+    __syncthreads();
+    for (int e = threadIdx.x; e < count * p.plan.half; e += kNormThreads) {
+        const int j = fast_div(e, p.plan.fd_half);
+        fill_turn(p.plan, tab, e + j * (p.plan.pitch - p.plan.half), e - j * p.plan.half, place[j][0]);
+    }
+    __syncthreads();
+    const int j = min(at.tok, at.last) - at.first, pos = at.in ? place[j][0] : -1, bid = place[j][1];
+    const int bs = static_cast<int>(p.block_size.d);
+    const long long cell = (static_cast<long long>(bid) * bs + (pos - fast_div(max(pos, 0), p.block_size) * bs)) * p.kv_heads;
+    Turns<LANES, PAIRS> turns;
+    turns.load(p.plan, tab, j, at.d0);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int h = at.slot + r * step, hk = h - p.q_heads, hv = hk - p.kv_heads;
+        float x[8], y[8], w[8], sum = 0.f;
+        widen(v[r], x);
+        load_weight(hk < 0 ? p.norm.weight : p.k_weight, p.norm.offset, at.d0, at.cols, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+        const float scale = rsqrtf(fmaf(row_sum<LANES>(sum), p.norm.inv_dim, p.norm.eps));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i] * (scale * w[i]);
+        turns.apply(y, rows_s + (PAIRS == kNeighbours ? 0 : at.line * (LANES * 8)), at.d0);
+        if (!at.cols || pos < 0 || h >= rows) continue;
+        if (hk < 0) {
+            *reinterpret_cast<uint4 *>(p.q_out + (static_cast<long long>(at.tok) * p.q_heads + h) * D + at.d0) = narrow(y);
+        } else if (bid >= 0) {
+            const long long to = (cell + (hv < 0 ? hk : hv)) * D + at.d0;
+            if constexpr (KV8) {
+                uint8_t *o = static_cast<uint8_t *>(hv < 0 ? p.k_cache : p.v_cache) + to;
+                if (hv < 0)
+                    store_e4m3<8>(o, y, p.k_scale);
+                else
+                    store_e4m3<8>(o, x, p.v_scale);
+            } else {
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(hv < 0 ? p.k_cache : p.v_cache) + to;
+                *reinterpret_cast<uint4 *>(o) = hv < 0 ? narrow(y) : v[r];
+            }
+        }
+    }
+}
+
+// ---- host side --------------------------------------------------------------------
+
+int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : (head_dim <= 128 ? 16 : 32); }
+
+RowPlan plan_norm(const pd_rope *rope, int lanes, bool transposed) {
+    RowPlan p = {};
+    p.units = make_fastdiv(lanes);
+    p.half = rope ? rope->rot_dim / 2 : 0;
+    p.fd_half = make_fastdiv(p.half);
+    p.pitch = (p.half + 3) / 4 * 4;
+    p.turns = rope ? rope->turns : nullptr;
+    p.factor = rope ? rope->factor : 1.f;
+    p.sign = transposed ? -1.f : 1.f;
+    return p;
+}
+
+Pairs pairs_of(const pd_rope *rope) {
+    if (!rope || rope->layout == PD_ROPE_INTERLEAVED) return kNeighbours;
+    return rope->rot_dim / 2 % 8 ? kScattered : kHalves;
+}
+
+// Threads of a launch, `many` heads a thread where that still fills the GPU and one
+// where the batch is small.  Returns false where they pass 31 bits.
+bool deal_heads(RowPlan *plan, int tokens, int heads, int many, bool *is_many, int *threads) {
+    const long long units = static_cast<long long>(tokens) * plan->units.d;
+    *is_many = units * heads > static_cast<long long>(many) * 152 * 2048;
+    plan->slots = make_fastdiv(*is_many ? (heads + many - 1) / many : heads);
+    const long long n = units * plan->slots.d;
+    if (n > 0x7fffffffLL - kNormThreads) return false;
+    *threads = static_cast<int>(n);
+    return true;
+}
+
+// f(lanes, pairs) with both as compile-time constants.
+template <class F>
+cudaError_t by_shape(int lanes, Pairs pairs, F f) {
+    auto with = [&](auto l) {
+        if (pairs == kNeighbours) return f(l, std::integral_constant<Pairs, kNeighbours>());
+        if (pairs == kHalves) return f(l, std::integral_constant<Pairs, kHalves>());
+        return f(l, std::integral_constant<Pairs, kScattered>());
+    };
+    if (lanes == 8) return with(std::integral_constant<int, 8>());
+    if (lanes == 16) return with(std::integral_constant<int, 16>());
+    return with(std::integral_constant<int, 32>());
+}
+
+int check_norm(const char *what, const pd_rope *rope, int head_dim, const void *w0, const void *w1, float eps, float offset) {
+    if (head_dim < 8 || head_dim > PD_MAX_HEAD_DIM || head_dim % 8)
+        return report(PD_ERR_UNSUPPORTED, "%s: head_dim %d must be a multiple of 8 in [8, %d]", what, head_dim, PD_MAX_HEAD_DIM);
+    if (!std::isfinite(eps) || eps < 0) return report(PD_ERR_INVALID, "%s: eps must be finite and not negative", what);
+    if (!std::isfinite(offset)) return report(PD_ERR_INVALID, "%s: weight_offset is not finite", what);
+    if (!aligned16(w0) || !aligned16(w1)) return report(PD_ERR_INVALID, "%s: weights must be 16-byte aligned", what);
+    if (!rope) return PD_OK;
+    if (rope->head_dim != head_dim)
+        return report(PD_ERR_INVALID, "%s: head_dim %d, the rotation's is %d", what, head_dim, rope->head_dim);
+    return check_handle(what, rope);
+}
+
+// Strides that hold 16-byte rows; rows: those of a tensor that is written do not overlap.
+int check_strides(const char *what, const char *name, int64_t tok, int64_t head, int64_t T, int64_t H, int64_t D, bool written) {
+    if (tok <= 0 || tok % 8 || head <= 0 || head % 8)
+        return report(PD_ERR_INVALID, "%s: %s's strides must be positive multiples of 8 elements (got %lld and %lld)", what, name,
+                      static_cast<long long>(tok), static_cast<long long>(head));
+    if (!written) return PD_OK;
+    const bool by_token = (H == 1 || head >= D) && (T == 1 || (tok >= D && (tok - D) / head >= H - 1));
+    const bool by_head = (T == 1 || tok >= D) && (H == 1 || (head >= D && (head - D) / tok >= T - 1));
+    if (by_token || by_head) return PD_OK;
+    return report(PD_ERR_INVALID, "%s: rows of %s overlap (strides %lld and %lld, %lld tokens of %lld heads)", what, name,
+                  static_cast<long long>(tok), static_cast<long long>(head), static_cast<long long>(T), static_cast<long long>(H));
+}
+
+Norm norm_of(const void *weight, float offset, float eps, int head_dim) {
+    return {static_cast<const __nv_bfloat16 *>(weight), weight ? offset : 0.f, eps, 1.f / static_cast<float>(head_dim), head_dim};
+}
+
+int append_impl(const char *what, const pd_rope *rope, const void *q, int64_t q_tok, const void *k, int64_t k_tok, const void *v,
+                int64_t v_tok, const void *q_weight, const void *k_weight, float eps, float offset, void *q_out, void *k_cache,
+                void *v_cache, bool kv8, float k_scale, float v_scale, const int32_t *block_table, int max_blocks,
+                const int32_t *context_lens, const int32_t *token_starts, int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads,
+                int head_dim, int block_size, int num_blocks, void *stream) {
+    int rc = check_norm(what, nullptr, head_dim, q_weight, k_weight, eps, offset);
+    if (rc != PD_OK) return rc;
+    rc = check_append(what, rope, q, q_tok, k, k_tok, v, v_tok, q_out, k_cache, v_cache, kv8, k_scale, v_scale, block_table, max_blocks,
+                      context_lens, num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                      token_starts != nullptr);
+    if (rc != PD_OK || num_tokens == 0 || num_seqs == 0) return rc;
+    int err = PD_OK;
+    NormAppendParams p = {};
+    p.status = device_status_word(&err);
+    if (!p.status) return err;
+    const int lanes = lanes_of(head_dim);
+    p.plan = plan_norm(rope, lanes, false);
+    p.norm = norm_of(q_weight, offset, eps, head_dim);
+    p.norm.offset = offset;  // (of k's weight, too)
+    p.k_weight = static_cast<const __nv_bfloat16 *>(k_weight);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_tok = q_tok;
+    p.k_tok = k_tok;
+    p.v_tok = v_tok;
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = 1.f / k_scale;
+    p.v_scale = 1.f / v_scale;
+    p.block_table = block_table;
+    p.context_lens = context_lens;
+    p.token_starts = token_starts;
+    p.max_blocks = max_blocks;
+    p.num_seqs = num_seqs;
+    p.num_blocks = num_blocks;
+    p.q_heads = q ? num_q_heads : 0;
+    p.kv_heads = num_kv_heads;
+    p.block_size = make_fastdiv(block_size);
+    bool many = false;
+    if (!deal_heads(&p.plan, num_tokens, p.q_heads + 2 * num_kv_heads, kRows, &many, &p.threads))
+        return report(PD_ERR_INVALID, "%s: launch too large (%d tokens)", what, num_tokens);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = by_shape(lanes, pairs_of(rope), [&](auto l, auto pairs) {
+        constexpr int L = decltype(l)::value;
+        constexpr Pairs P = decltype(pairs)::value;
+        if (kv8) return many ? launch_rows(norm_append_kernel<L, P, true, kRows>, p, st) : launch_rows(norm_append_kernel<L, P, true, 1>, p, st);
+        return many ? launch_rows(norm_append_kernel<L, P, false, kRows>, p, st) : launch_rows(norm_append_kernel<L, P, false, 1>, p, st);
+    });
+    if (e != cudaSuccess) return report_cuda(e, what);
+    return report_ok();
+}
+
+}  // namespace
+}  // namespace pd
+
+using namespace pd;
+
+extern "C" {
+
+int pd_norm_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride, int64_t x_head_stride, const void *weight, float eps,
+                       float weight_offset, const int32_t *positions, void *out, int64_t out_token_stride, int64_t out_head_stride,
+                       int num_tokens, int num_heads, int head_dim, void *stream) {
+    const char *what = "pd_norm_rope_apply";
+    if (num_tokens < 0 || num_heads < 0) return report(PD_ERR_INVALID, "%s: num_tokens %d, num_heads %d", what, num_tokens, num_heads);
+    int rc = check_norm(what, rope, head_dim, weight, nullptr, eps, weight_offset);
+    if (rc != PD_OK) return rc;
+    if (num_tokens == 0 || num_heads == 0) return report_ok();
+    if (!x || !out || (rope && !positions)) return report(PD_ERR_INVALID, "%s: null tensor pointer", what);
+    if (!aligned16(x) || !aligned16(out)) return report(PD_ERR_INVALID, "%s: x and out must be 16-byte aligned", what);
+    rc = check_strides(what, "x", x_token_stride, x_head_stride, num_tokens, num_heads, head_dim, false);
+    if (rc == PD_OK) rc = check_strides(what, "out", out_token_stride, out_head_stride, num_tokens, num_heads, head_dim, true);
+    if (rc != PD_OK) return rc;
+    if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+        return report(PD_ERR_INVALID, "%s: in place (out == x) needs equal strides", what);
+    NormParams p = {};
+    const int lanes = lanes_of(head_dim);
+    p.plan = plan_norm(rope, lanes, false);
+    p.norm = norm_of(weight, weight_offset, eps, head_dim);
+    p.x = static_cast<const __nv_bfloat16 *>(x);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.x_tok = x_token_stride;
+    p.x_head = x_head_stride;
+    p.o_tok = out_token_stride;
+    p.o_head = out_head_stride;
+    p.positions = positions;
+    p.heads = num_heads;
+    bool many = false;
+    if (!deal_heads(&p.plan, num_tokens, num_heads, kRows, &many, &p.threads))
+        return report(PD_ERR_INVALID, "%s: launch too large (%d tokens of %d heads)", what, num_tokens, num_heads);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = by_shape(lanes, pairs_of(rope), [&](auto l, auto pairs) {
+        constexpr int L = decltype(l)::value;
+        constexpr Pairs P = decltype(pairs)::value;
+        return many ? launch_rows(norm_kernel<L, P, kRows>, p, st) : launch_rows(norm_kernel<L, P, 1>, p, st);
+    });
+    if (e != cudaSuccess) return report_cuda(e, what);
+    return report_ok();
+}
+
+size_t pd_norm_rope_workspace_bytes(int head_dim) {
+    if (head_dim <= 0 || head_dim > PD_MAX_HEAD_DIM) return 0;
+    return static_cast<size_t>(kGradBlocks) * lanes_of(head_dim) * 8 * sizeof(float);
+}
+
+int pd_norm_rope_backward(const pd_rope *rope, const void *x, int64_t x_token_stride, int64_t x_head_stride, const void *weight, float eps,
+                          float weight_offset, const int32_t *positions, const void *grad, int64_t grad_token_stride,
+                          int64_t grad_head_stride, void *grad_x, int64_t grad_x_token_stride, int64_t grad_x_head_stride,
+                          void *grad_weight, int num_tokens, int num_heads, int head_dim, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+    const char *what = "pd_norm_rope_backward";
+    if (num_tokens < 0 || num_heads < 0) return report(PD_ERR_INVALID, "%s: num_tokens %d, num_heads %d", what, num_tokens, num_heads);
+    int rc = check_norm(what, rope, head_dim, weight, nullptr, eps, weight_offset);
+    if (rc != PD_OK) return rc;
+    if (grad_weight && !weight) return report(PD_ERR_INVALID, "%s: a weight's gradient without a weight", what);
+    const bool none = num_tokens == 0 || num_heads == 0;
+    if (none && !grad_weight) return report_ok();
+    if (!none && (!x || !grad || !grad_x || (rope && !positions))) return report(PD_ERR_INVALID, "%s: null tensor pointer", what);
+    if (!aligned16(x) || !aligned16(grad) || !aligned16(grad_x))
+        return report(PD_ERR_INVALID, "%s: x, grad and grad_x must be 16-byte aligned", what);
+    const int lanes = lanes_of(head_dim);
+    if (grad_weight && (!workspace || workspace_bytes < pd_norm_rope_workspace_bytes(head_dim)))
+        return report(PD_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", what, pd_norm_rope_workspace_bytes(head_dim),
+                      workspace ? workspace_bytes : static_cast<size_t>(0), workspace ? "" : " (null)");
+    if (!aligned16(workspace)) return report(PD_ERR_INVALID, "workspace must be 16-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int blocks = 0;
+    if (!none) {
+        rc = check_strides(what, "x", x_token_stride, x_head_stride, num_tokens, num_heads, head_dim, false);
+        if (rc == PD_OK) rc = check_strides(what, "grad", grad_token_stride, grad_head_stride, num_tokens, num_heads, head_dim, false);
+        if (rc == PD_OK) rc = check_strides(what, "grad_x", grad_x_token_stride, grad_x_head_stride, num_tokens, num_heads, head_dim, true);
+        if (rc != PD_OK) return rc;
+        GradParams p = {};
+        p.plan = plan_norm(rope, lanes, true);
+        p.norm = norm_of(weight, weight_offset, eps, head_dim);
+        p.x = static_cast<const __nv_bfloat16 *>(x);
+        p.g = static_cast<const __nv_bfloat16 *>(grad);
+        p.dx = static_cast<__nv_bfloat16 *>(grad_x);
+        p.x_tok = x_token_stride;
+        p.x_head = x_head_stride;
+        p.g_tok = grad_token_stride;
+        p.g_head = grad_head_stride;
+        p.d_tok = grad_x_token_stride;
+        p.d_head = grad_x_head_stride;
+        p.positions = positions;
+        p.heads = num_heads;
+        p.part = grad_weight ? static_cast<float *>(workspace) : nullptr;
+        p.plan.slots = make_fastdiv((num_heads + kGradRows - 1) / kGradRows);
+        const long long threads = static_cast<long long>(num_tokens) * p.plan.slots.d * lanes;
+        if (threads > 0x7fffffffLL - kNormThreads)
+            return report(PD_ERR_INVALID, "%s: launch too large (%d tokens of %d heads)", what, num_tokens, num_heads);
+        p.threads = static_cast<int>(threads);
+        blocks = static_cast<int>(std::min<long long>((threads + kNormThreads - 1) / kNormThreads, kGradBlocks));
+        const cudaError_t e = by_shape(lanes, pairs_of(rope), [&](auto l, auto pairs) {
+            return launch_rows(norm_grad_kernel<decltype(l)::value, decltype(pairs)::value>, p, st, blocks);
+        });
+        if (e != cudaSuccess) return report_cuda(e, what);
+    }
+    if (grad_weight) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>((head_dim + 31) / 32));
+        cfg.blockDim = dim3(32, 32);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_weight_grad_kernel, static_cast<const float *>(workspace), blocks, lanes * 8,
+                                                 head_dim, static_cast<__nv_bfloat16 *>(grad_weight));
+        if (e != cudaSuccess) return report_cuda(e, what);
+    }
+    return report_ok();
+}
+
+int pd_append_kv_normed(const pd_rope *rope, const void *q, int64_t q_token_stride, const void *k, int64_t k_token_stride, const void *v,
+                        int64_t v_token_stride, const void *q_weight, const void *k_weight, float eps, float weight_offset, void *q_out,
+                        void *k_cache, void *v_cache, const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens,
+                        const int32_t *token_starts, int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                        int block_size, int num_blocks, void *stream) {
+    return append_impl("pd_append_kv_normed", rope, q, q_token_stride, k, k_token_stride, v, v_token_stride, q_weight, k_weight, eps,
+                       weight_offset, q_out, k_cache, v_cache, false, 1.f, 1.f, block_table, max_blocks_per_seq, context_lens, token_starts,
+                       num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, stream);
+}
+
+int pd_append_kv_normed_fp8(const pd_rope *rope, const void *q, int64_t q_token_stride, const void *k, int64_t k_token_stride,
+                            const void *v, int64_t v_token_stride, const void *q_weight, const void *k_weight, float eps,
+                            float weight_offset, void *q_out, void *k_cache, void *v_cache, float k_scale, float v_scale,
+                            const int32_t *block_table, int max_blocks_per_seq, const int32_t *context_lens,
+                            const int32_t *token_starts, int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                            int block_size, int num_blocks, void *stream) {
+    return append_impl("pd_append_kv_normed_fp8", rope, q, q_token_stride, k, k_token_stride, v, v_token_stride, q_weight, k_weight, eps,
+                       weight_offset, q_out, k_cache, v_cache, true, k_scale, v_scale, block_table, max_blocks_per_seq, context_lens,
+                       token_starts, num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, stream);
+}
+
+}  // extern "C"

@@ -135,6 +135,14 @@ _SIGS = {
     "pd_rope_create": (_I, [_VP, _VP]),
     "pd_rope_destroy": (None, [_VP]),
     "pd_rope_apply": (_I, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _I64, _I, _I, _I, _VP]),
+    "pd_norm_rope_apply": (_I, [_VP, _VP, _I64, _I64, _VP, ctypes.c_float, ctypes.c_float, _VP, _VP, _I64, _I64, _I, _I, _I, _VP]),
+    "pd_norm_rope_workspace_bytes": (_SZ, [_I]),
+    "pd_norm_rope_backward": (_I, [_VP, _VP, _I64, _I64, _VP, ctypes.c_float, ctypes.c_float, _VP, _VP, _I64, _I64, _VP, _I64, _I64, _VP,
+                                   _I, _I, _I, _VP, _SZ, _VP]),
+    "pd_append_kv_normed": (_I, [_VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, ctypes.c_float, ctypes.c_float, _VP, _VP, _VP, _VP, _I,
+                                 _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _VP]),
+    "pd_append_kv_normed_fp8": (_I, [_VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, ctypes.c_float, ctypes.c_float, _VP, _VP, _VP,
+                                     ctypes.c_float, ctypes.c_float, _VP, _I, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _VP]),
     "pd_append_kv": (_I, [_VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I,
                           _I, _I, _I, _VP]),
     "pd_append_kv_fp8": (_I, [_VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _VP, ctypes.c_float, ctypes.c_float,
@@ -616,6 +624,61 @@ def pd_append_kv_fp8(rope, q, k, v, q_out, k_cache, v_cache, k_scale: float, v_s
         _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
         _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, block_table.data_ptr(),
         mb, context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
+        nb if num_blocks is None else num_blocks, _stream(stream)))
+
+
+def _head_stride(t) -> int:
+    """Elements from one head's row to the next of [T, H, D] (any value serves a single head)."""
+    return t.stride(1) if t.shape[1] > 1 else t.shape[2]
+
+
+def pd_norm_rope_apply(rope, x, weight, positions, out, eps: float = 1e-6, weight_offset: float = 0.0, stream=None) -> int:
+    """out [T, H, D] <- x [T, H, D], each row's RMS norm times (weight_offset + weight [D]) rotated by positions [T] (see
+    pd.h); strided in tokens and heads; rope and positions None for the norm alone, weight None for ones."""
+    T, H, D = x.shape
+    return _check(lib().pd_norm_rope_apply(_handle(rope), x.data_ptr(), _token_stride(x), _head_stride(x), _ptr(weight), eps, weight_offset,
+                                           _ptr(positions), out.data_ptr(), _token_stride(out), _head_stride(out), T, H, D,
+                                           _stream(stream)))
+
+
+def pd_norm_rope_workspace_bytes(head_dim: int) -> int:
+    return lib().pd_norm_rope_workspace_bytes(head_dim)
+
+
+def pd_norm_rope_backward(rope, x, weight, positions, grad, grad_x, grad_weight, workspace, eps: float = 1e-6, weight_offset: float = 0.0,
+                          stream=None) -> int:
+    """grad_x [T, H, D] and grad_weight [D] (or None) <- the gradients of pd_norm_rope_apply from the gradient of its out."""
+    T, H, D = x.shape
+    return _check(lib().pd_norm_rope_backward(
+        _handle(rope), x.data_ptr(), _token_stride(x), _head_stride(x), _ptr(weight), eps, weight_offset, _ptr(positions), grad.data_ptr(),
+        _token_stride(grad), _head_stride(grad), grad_x.data_ptr(), _token_stride(grad_x), _head_stride(grad_x), _ptr(grad_weight), T, H, D,
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def pd_append_kv_normed(rope, q, k, v, q_weight, k_weight, q_out, k_cache, v_cache, block_table, context_lens, token_starts=None,
+                        eps: float = 1e-6, weight_offset: float = 0.0, stream=None, num_blocks: int | None = None) -> int:
+    """pd_append_kv with the RMS norm of each head of q and k before the rotation (weights [D] BF16, or None for ones)."""
+    T, Hkv, D = k.shape
+    nb, bs = k_cache.shape[:2]
+    S, mb = block_table.shape
+    return _check(lib().pd_append_kv_normed(
+        _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(), _token_stride(v),
+        _ptr(q_weight), _ptr(k_weight), eps, weight_offset, _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
+        context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
+        nb if num_blocks is None else num_blocks, _stream(stream)))
+
+
+def pd_append_kv_normed_fp8(rope, q, k, v, q_weight, k_weight, q_out, k_cache, v_cache, k_scale: float, v_scale: float, block_table,
+                            context_lens, token_starts=None, eps: float = 1e-6, weight_offset: float = 0.0, stream=None,
+                            num_blocks: int | None = None) -> int:
+    """pd_append_kv_normed into an FP8 cache (uint8 E4M3 codes of x * (1 / k_scale) and x * (1 / v_scale))."""
+    T, Hkv, D = k.shape
+    nb, bs = k_cache.shape[:2]
+    S, mb = block_table.shape
+    return _check(lib().pd_append_kv_normed_fp8(
+        _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(), _token_stride(v),
+        _ptr(q_weight), _ptr(k_weight), eps, weight_offset, _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale,
+        block_table.data_ptr(), mb, context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
         nb if num_blocks is None else num_blocks, _stream(stream)))
 
 

@@ -1,6 +1,7 @@
 """CPU tests of the attention of new tokens: the workspace, every refusal, none of which reaches a kernel, and the
 division of its work."""
 
+import math
 import random
 
 import pytest
@@ -115,3 +116,52 @@ def test_walk_refusals():
                  ([0, 2], [9], 8, 2, 128, -1), ([0, 2], [9], 8, 2, 128, 0, 0), ([0, 2], [9], 8, 2, 128, 0, 153)):
         with pytest.raises(pd.PdError):
             pd.pd_debug_chunk_walk(*args)
+
+
+def _chunk(**change):
+    """pd_chunk_attn[_fp8] on addresses that are never followed: every call here is refused on the host."""
+    a = dict(q=4096, q_tok=512, kc=65536, vc=131072, bt=1024, mb=4, cl=2048, ts=512, out=8192, lse=None, T=6, S=2, Hq=4, Hkv=1, D=128, bs=16,
+             nb=8, scale=0.1, window=0, ws=1 << 20, ws_bytes=1 << 40, fp8=None)
+    a.update(change)
+    scales = [] if a["fp8"] is None else list(a["fp8"])
+    fn = pd.lib().pd_chunk_attn if a["fp8"] is None else pd.lib().pd_chunk_attn_fp8
+    return fn(a["q"], a["q_tok"], a["kc"], a["vc"], *scales, a["bt"], a["mb"], a["cl"], a["ts"], a["out"], a["lse"], a["T"], a["S"], a["Hq"],
+              a["Hkv"], a["D"], a["bs"], a["nb"], a["scale"], a["window"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(Hkv=0), pd.PD_ERR_INVALID), (dict(Hq=3, Hkv=2), pd.PD_ERR_INVALID), (dict(D=12), pd.PD_ERR_UNSUPPORTED),
+    (dict(D=512), pd.PD_ERR_INVALID), (dict(bs=8), pd.PD_ERR_UNSUPPORTED), (dict(T=-1), pd.PD_ERR_INVALID), (dict(S=-1), pd.PD_ERR_INVALID),
+    (dict(ts=None), pd.PD_ERR_INVALID), (dict(window=-1), pd.PD_ERR_INVALID), (dict(q=None), pd.PD_ERR_INVALID),
+    (dict(kc=None), pd.PD_ERR_INVALID), (dict(vc=None), pd.PD_ERR_INVALID), (dict(bt=None), pd.PD_ERR_INVALID),
+    (dict(cl=None), pd.PD_ERR_INVALID), (dict(out=None), pd.PD_ERR_INVALID), (dict(q=4104), pd.PD_ERR_INVALID),
+    (dict(out=8200), pd.PD_ERR_INVALID), (dict(kc=65544), pd.PD_ERR_INVALID), (dict(vc=131080), pd.PD_ERR_INVALID),
+    (dict(q_tok=504), pd.PD_ERR_INVALID), (dict(q_tok=516), pd.PD_ERR_INVALID), (dict(q_tok=-512), pd.PD_ERR_INVALID),
+    (dict(mb=0), pd.PD_ERR_INVALID), (dict(nb=0), pd.PD_ERR_INVALID), (dict(mb=1 << 27), pd.PD_ERR_INVALID),
+    (dict(T=2**31 - 100), pd.PD_ERR_INVALID), (dict(scale=math.nan), pd.PD_ERR_INVALID), (dict(scale=math.inf), pd.PD_ERR_INVALID),
+    (dict(fp8=(math.nan, 1.0)), pd.PD_ERR_INVALID), (dict(fp8=(1.0, math.inf)), pd.PD_ERR_INVALID),
+    (dict(fp8=(1.0, 1.0), D=24, q_tok=96), pd.PD_ERR_UNSUPPORTED)])
+def test_chunk_refused(change, code):
+    assert _chunk(**change) == code
+    assert pd.last_error()
+
+
+def test_chunk_of_nothing():
+    assert _chunk(T=0) == pd.PD_OK and _chunk(S=0, T=0, ts=None) == pd.PD_OK and _chunk(S=0) == pd.PD_OK
+    assert pd.last_error() == ""
+
+
+def test_api_refuses_tensors():
+    """Types, shapes and devices are refused before the library is called (the CPU stands in for the device here)."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    good = dict(q=bf(6, 4, 64), k_cache=bf(4, 16, 1, 64), v_cache=bf(4, 16, 1, 64), block_table=i32(2, 2), context_lens=i32(2),
+                token_starts=i32(3), out=None, lse=None, ws=None, dev=-1)
+    api._check_chunk(**good)
+    api._check_chunk(**{**good, "out": bf(6, 4, 64), "lse": torch.zeros(6, 4), "ws": torch.zeros(64, dtype=torch.uint8), "token_starts": None})
+    for change in (dict(q=bf(6, 64)), dict(q=torch.zeros(6, 4, 64)), dict(q=bf(4, 6, 64).transpose(0, 1)), dict(k_cache=bf(4, 16, 1, 32)),
+                   dict(v_cache=bf(5, 16, 1, 64)), dict(block_table=i32(3, 2)), dict(context_lens=i32(2).long()), dict(token_starts=i32(2)),
+                   dict(out=bf(6, 4, 32)), dict(out=bf(6, 5, 64)[:, :4]), dict(lse=torch.zeros(6, 5)), dict(lse=torch.zeros(4, 6).T),
+                   dict(lse=torch.zeros(6, 4).double()), dict(ws=torch.zeros(64, dtype=torch.uint8)[::2]), dict(dev=0)):
+        with pytest.raises(ValueError):
+            api._check_chunk(**{**good, **change})

@@ -8,13 +8,14 @@
 // u = R^T dy (the transposed rotation of the gradient) and the sums over the row,
 //   dx = r (u w' - x r^2 sum(x u w') / D),   dw = sum over rows of u x r.
 //
-// A row is held by D / 8 lanes (rounded up to 8, 16 or 32), 8 columns each, in one
-// 16-byte load.  The sums go across its lanes by shuffles; the other column of a pair
-// is in the lane itself (neighbours) or comes through shared memory (halves apart), so
-// every rotation loads and stores whole 16 bytes.  Sines and cosines are those of the
-// block's tokens from a table in shared memory, as in pd_rope.cu, and a lane walks
-// several heads of its token with them.  All arithmetic is FP32; a result is rounded
-// once.  dw is summed in a fixed order: a lane's rows, the rows of a block, the blocks.
+// A row is held by D / 16 lanes (rounded up to 4, 8 or 16), two chunks of 8 columns
+// each, in 16-byte loads: chunks that pair up where pairs are whole chunks apart, so that
+// a rotation stays in the lane and needs a sine and a cosine for two columns, neighbouring
+// chunks otherwise.  The row's sums go across its lanes by shuffles.  Sines and cosines
+// are those of the block's tokens from a table in shared memory, as in pd_rope.cu, and
+// a lane walks several heads of its token with them.  All arithmetic is FP32; a result
+// is rounded once.  dw is summed in a fixed order: a lane's rows, the rows of a block, the
+// blocks.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -34,11 +35,12 @@ namespace {
 using namespace rope;
 
 constexpr int kNormThreads = kRopeThreads;
-constexpr int kGradBlocks = 152 * 4;  // blocks of the backward pass at most
+constexpr int kGradBlocks = 152 * 2;  // blocks of the backward pass at most
 constexpr int kGradRows = 2;          // heads a lane takes at a time there
 
-// How a row's pairs lie in its lanes' 8 columns: NEIGHBOURS whole in a lane (also
-// where nothing turns), HALVES 8 columns with 8 others, SCATTERED anywhere.
+// How a row's pairs lie in its lanes' chunks: kNeighbours, two columns side by side
+// (also where nothing turns), kHalves, a lane's one chunk with its other, kScattered,
+// anywhere.
 enum Pairs { kNeighbours, kHalves, kScattered };
 
 struct Norm {
@@ -67,7 +69,7 @@ struct GradParams {
     const int32_t *positions;
     int heads;
     int threads;
-    float *part;    // [blocks][lanes * 8]: sums of dw; null: not wanted
+    float *part;    // [blocks][lanes * 16]: sums of dw, a lane's chunks side by side; null: not wanted
 };
 
 struct NormAppendParams {
@@ -87,23 +89,21 @@ struct NormAppendParams {
     unsigned int *status;
 };
 
-__device__ __forceinline__ void widen(const uint4 &v, float (&f)[8]) {
+// A lane's two chunks of a row.
+struct Chunks {
+    uint4 a, b;
+};
+__device__ __forceinline__ void widen(const uint4 &v, float *f) {
     f[0] = dev::bf16_lo_f32(v.x), f[1] = dev::bf16_hi_f32(v.x), f[2] = dev::bf16_lo_f32(v.y), f[3] = dev::bf16_hi_f32(v.y);
     f[4] = dev::bf16_lo_f32(v.z), f[5] = dev::bf16_hi_f32(v.z), f[6] = dev::bf16_lo_f32(v.w), f[7] = dev::bf16_hi_f32(v.w);
 }
-__device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+__device__ __forceinline__ uint4 narrow(const float *f) {
     return make_uint4(dev::pack_bf16x2(f[0], f[1]), dev::pack_bf16x2(f[2], f[3]), dev::pack_bf16x2(f[4], f[5]),
                       dev::pack_bf16x2(f[6], f[7]));
 }
-__device__ __forceinline__ void load_weight(const __nv_bfloat16 *w, float offset, int d0, bool in, float (&f)[8]) {
-    if (w && in) {
-        widen(*reinterpret_cast<const uint4 *>(w + d0), f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += offset;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 1.f;
-    }
+__device__ __forceinline__ void widen(const Chunks &v, float (&f)[16]) {
+    widen(v.a, f);
+    widen(v.b, f + 8);
 }
 // The sum over a row's lanes.
 template <int LANES>
@@ -113,138 +113,190 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// The turns of a lane's 8 columns: out = c y + s (the pair's other column), on the
-// columns of `live`; the others are copied.
+// A lane's columns: chunks at ca and cb, of which it has those within the row.
+template <int LANES, Pairs PAIRS>
+struct Columns {
+    int u, ca, cb;
+    bool a, b;
+    __device__ __forceinline__ Columns(const RowPlan &p, int head_dim) {
+        u = threadIdx.x % LANES;
+        ca = 16 * u;
+        cb = ca + 8;
+        if (PAIRS == kHalves) {
+            const int paired = p.half / 8;  // lanes with chunks that pair up; the others have copied ones
+            ca = u < paired ? 8 * u : 2 * p.half + 16 * (u - paired);
+            cb = u < paired ? p.half + 8 * u : ca + 8;
+        }
+        a = ca < head_dim;
+        b = cb < head_dim;
+    }
+    __device__ __forceinline__ Chunks load(const __nv_bfloat16 *row) const {
+        Chunks v = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (a) v.a = *reinterpret_cast<const uint4 *>(row + ca);
+        if (b) v.b = *reinterpret_cast<const uint4 *>(row + cb);
+        return v;
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *row, const float (&f)[16]) const {
+        if (a) *reinterpret_cast<uint4 *>(row + ca) = narrow(f);
+        if (b) *reinterpret_cast<uint4 *>(row + cb) = narrow(f + 8);
+    }
+    __device__ __forceinline__ void weight(const __nv_bfloat16 *w, float offset, float (&f)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = 1.f;
+        if (!w) return;
+        widen(load(w), f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] += offset;
+    }
+};
+
+// The turns of a lane's columns for one token.
 template <int LANES, Pairs PAIRS>
 struct Turns {
-    float c[8], s[8];
-    uint32_t live;
-    int other;        // kHalves: the column that pairs with the lane's first
-    int half;
+    float c[PAIRS == kScattered ? 1 : 8], s[PAIRS == kScattered ? 1 : 8];
+    int live;           // pairs of the lane that turn
+    const float *cos;   // kScattered: the token's table
+    int span, half;
 
-    __device__ __forceinline__ void load(const RowPlan &p, const TurnTable &tab, int token, int d0) {
-        live = 0;
-        other = 0;
+    __device__ __forceinline__ void load(const RowPlan &p, const TurnTable &tab, int token, const Columns<LANES, PAIRS> &at) {
+        cos = tab.c + token * p.pitch;
+        span = tab.span;
         half = p.half;
-        const float *cos = tab.c + token * p.pitch, *sin = cos + tab.span;
+        live = 0;
+        if constexpr (PAIRS == kScattered) return;
+        const int pair = PAIRS == kHalves ? at.ca : 8 * at.u;
+        live = PAIRS == kHalves ? (at.ca < half ? 8 : 0) : min(max(half - pair, 0), 8);
+        if (live > 0) {  // (rows of the table are multiples of 4 pairs, and begin at one)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int col = d0 + i, pair = PAIRS == kNeighbours ? col / 2 : (col < half ? col : col - half);
-            const bool upper = PAIRS == kNeighbours ? i & 1 : col >= half;
-            const bool in = pair < half;
-            c[i] = in ? cos[pair] : 1.f;
-            s[i] = in ? (upper ? sin[pair] : -sin[pair]) : 0.f;
-            live |= in ? 1u << i : 0u;
-        }
-        if (PAIRS == kHalves) other = live ? (d0 < half ? d0 + half : d0 - half) : d0;
-    }
-    // `row`: the row's LANES * 8 floats of shared memory, columns 0 to 3 of every 8 first
-    // (so that 16-byte accesses of neighbouring lanes meet no bank twice).  All lanes
-    // of the warp take part.
-    __device__ __forceinline__ void apply(float (&y)[8], float *row, int d0) const {
-        float z[8];
-        if constexpr (PAIRS == kNeighbours) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = y[i ^ 1];
-        } else {
-            __syncwarp();
-            *reinterpret_cast<float4 *>(row + d0 / 2) = make_float4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<float4 *>(row + LANES * 4 + d0 / 2) = make_float4(y[4], y[5], y[6], y[7]);
-            __syncwarp();
-            if constexpr (PAIRS == kHalves) {
-                const float4 a = *reinterpret_cast<const float4 *>(row + other / 2);
-                const float4 b = *reinterpret_cast<const float4 *>(row + LANES * 4 + other / 2);
-                z[0] = a.x, z[1] = a.y, z[2] = a.z, z[3] = a.w, z[4] = b.x, z[5] = b.y, z[6] = b.z, z[7] = b.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int col = d0 + i, from = (live >> i) & 1 ? (col < half ? col + half : col - half) : col;
-                    z[i] = row[(from & 4) * LANES + (from >> 3) * 4 + (from & 3)];
+            for (int i = 0; i < 8; i += 4) {
+                if (i < live) {
+                    const float4 x = *reinterpret_cast<const float4 *>(cos + pair + i), y = *reinterpret_cast<const float4 *>(cos + span + pair + i);
+                    c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+                    s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
                 }
             }
         }
+    }
+    // `row`: kScattered: the row's LANES * 16 floats of shared memory (all lanes of the
+    // warp take part).
+    __device__ __forceinline__ void apply(float (&y)[16], float *row, const Columns<LANES, PAIRS> &at) const {
+        if constexpr (PAIRS == kHalves) {
+            if (live == 0) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if ((live >> i) & 1) y[i] = fmaf(y[i], c[i], z[i] * s[i]);
+            for (int i = 0; i < 8; ++i) {
+                const float a = y[i], b = y[8 + i];
+                y[i] = fmaf(a, c[i], -(b * s[i]));
+                y[8 + i] = fmaf(b, c[i], a * s[i]);
+            }
+        } else if constexpr (PAIRS == kNeighbours) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = y[2 * i], b = y[2 * i + 1];
+                if (i < live) {
+                    y[2 * i] = fmaf(a, c[i], -(b * s[i]));
+                    y[2 * i + 1] = fmaf(b, c[i], a * s[i]);
+                }
+            }
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(row + at.ca + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int col = at.ca + i, pair = col < half ? col : col - half;
+                if (pair < half) {
+                    const float cc = cos[pair], ss = cos[span + pair];
+                    y[i] = col < half ? fmaf(y[i], cc, -(row[col + half] * ss)) : fmaf(y[i], cc, row[pair] * ss);
+                }
+            }
+        }
     }
 };
 
 // A thread's place: its line of lanes, the line's token and first head.
 template <int LANES>
 struct Place {
-    int d0, line, tok, slot, first, last;  // (first, last: of the block's tokens)
-    bool in, cols;
-    __device__ __forceinline__ Place(const RowPlan &p, int block, int threads, int head_dim) {
+    int line, tok, slot, first, last;  // (first, last: of the block's tokens)
+    bool in;
+    __device__ __forceinline__ Place(const RowPlan &p, int block, int threads) {
         const int id = block * kNormThreads + threadIdx.x, n = id / LANES;
-        d0 = threadIdx.x % LANES * 8;
         line = threadIdx.x / LANES;
         tok = fast_div(n, p.slots);
         slot = n - tok * static_cast<int>(p.slots.d);
         first = fast_div(block * kNormThreads / LANES, p.slots);
         last = fast_div((min(block * kNormThreads + kNormThreads, threads) - 1) / LANES, p.slots);
         in = id < threads;
-        cols = d0 < head_dim;
     }
 };
 
+// Shared memory of the scattered pairs' rows.
+template <int LANES, Pairs PAIRS>
+struct Exchange {
+    float v[PAIRS == kScattered ? kNormThreads * 16 : 4];
+    __device__ __forceinline__ float *row(int line) { return PAIRS == kScattered ? v + line * (LANES * 16) : nullptr; }
+};
+
 template <int LANES, Pairs PAIRS, int ROWS>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float rows[PAIRS == kNeighbours ? 1 : kNormThreads * 8];
+__global__ void __launch_bounds__(kNormThreads, ROWS > 1 ? 3 : 4) norm_kernel(const __grid_constant__ NormParams p) {
+    __shared__ __align__(16) Exchange<LANES, PAIRS> rows;
     dev::griddep_launch_dependents();
-    const Place<LANES> at(p.plan, blockIdx.x, p.threads, p.norm.head_dim);
+    const Place<LANES> at(p.plan, blockIdx.x, p.threads);
+    const Columns<LANES, PAIRS> cols(p.plan, p.norm.head_dim);
     const TurnTable tab = {turn_smem, (at.last - at.first + 1) * p.plan.pitch};
     const int step = static_cast<int>(p.plan.slots.d);
     dev::griddep_wait();
-    uint4 v[ROWS];
+    Chunks v[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int h = at.slot + r * step;
-        v[r] = make_uint4(0, 0, 0, 0);
-        if (at.in && at.cols && h < p.heads) v[r] = *reinterpret_cast<const uint4 *>(p.x + at.tok * p.x_tok + h * p.x_head + at.d0);
+        v[r] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (at.in && h < p.heads) v[r] = cols.load(p.x + at.tok * p.x_tok + h * p.x_head);
     }
     for (int e = threadIdx.x; e < (at.last - at.first + 1) * p.plan.half; e += kNormThreads) {
         const int j = fast_div(e, p.plan.fd_half);
         fill_turn(p.plan, tab, e + j * (p.plan.pitch - p.plan.half), e - j * p.plan.half, p.positions[at.first + j]);
     }
-    float w[8];
-    load_weight(p.norm.weight, p.norm.offset, at.d0, at.cols, w);
+    float w[16];
+    cols.weight(p.norm.weight, p.norm.offset, w);
     __syncthreads();
     Turns<LANES, PAIRS> turns;
-    turns.load(p.plan, tab, min(at.tok, at.last) - at.first, at.d0);
+    turns.load(p.plan, tab, min(at.tok, at.last) - at.first, cols);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int h = at.slot + r * step;
-        float y[8], sum = 0.f;
+        float y[16], sum = 0.f;
         widen(v[r], y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+        for (int i = 0; i < 16; ++i) sum = fmaf(y[i], y[i], sum);
         const float scale = rsqrtf(fmaf(row_sum<LANES>(sum), p.norm.inv_dim, p.norm.eps));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= scale * w[i];
-        turns.apply(y, rows + (PAIRS == kNeighbours ? 0 : at.line * (LANES * 8)), at.d0);
-        if (at.in && at.cols && h < p.heads) *reinterpret_cast<uint4 *>(p.out + at.tok * p.o_tok + h * p.o_head + at.d0) = narrow(y);
+        for (int i = 0; i < 16; ++i) y[i] *= scale * w[i];
+        turns.apply(y, rows.row(at.line), cols);
+        if (at.in && h < p.heads) cols.store(p.out + at.tok * p.o_tok + h * p.o_head, y);
     }
 }
 
 template <int LANES, Pairs PAIRS>
 __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const __grid_constant__ GradParams p) {
-    __shared__ float rows[kNormThreads * 8];
+    __shared__ __align__(16) float rows[kNormThreads * 16];
     dev::griddep_launch_dependents();
     const int blocks = (p.threads + kNormThreads - 1) / kNormThreads, step = static_cast<int>(p.plan.slots.d);
+    const Columns<LANES, PAIRS> cols(p.plan, p.norm.head_dim);
     dev::griddep_wait();
-    float w[8], dw[8] = {};
-    load_weight(p.norm.weight, p.norm.offset, threadIdx.x % LANES * 8, threadIdx.x % LANES * 8 < p.norm.head_dim, w);
+    float w[16], dw[16] = {};
+    cols.weight(p.norm.weight, p.norm.offset, w);
     for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
-        const Place<LANES> at(p.plan, b, p.threads, p.norm.head_dim);
+        const Place<LANES> at(p.plan, b, p.threads);
         const TurnTable tab = {turn_smem, (at.last - at.first + 1) * p.plan.pitch};
-        uint4 vx[kGradRows], vg[kGradRows];
+        Chunks vx[kGradRows], vg[kGradRows];
 #pragma unroll
         for (int r = 0; r < kGradRows; ++r) {
             const int h = at.slot + r * step;
-            vx[r] = vg[r] = make_uint4(0, 0, 0, 0);
-            if (at.in && at.cols && h < p.heads) {
-                vx[r] = *reinterpret_cast<const uint4 *>(p.x + at.tok * p.x_tok + h * p.x_head + at.d0);
-                vg[r] = *reinterpret_cast<const uint4 *>(p.g + at.tok * p.g_tok + h * p.g_head + at.d0);
+            vx[r] = vg[r] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (at.in && h < p.heads) {
+                vx[r] = cols.load(p.x + at.tok * p.x_tok + h * p.x_head);
+                vg[r] = cols.load(p.g + at.tok * p.g_tok + h * p.g_head);
             }
         }
         if (b != static_cast<int>(blockIdx.x)) __syncthreads();  // (the last turn's table has been read)
@@ -254,83 +306,87 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const __grid_co
         }
         __syncthreads();
         Turns<LANES, PAIRS> turns;
-        turns.load(p.plan, tab, min(at.tok, at.last) - at.first, at.d0);
+        turns.load(p.plan, tab, min(at.tok, at.last) - at.first, cols);
 #pragma unroll
         for (int r = 0; r < kGradRows; ++r) {
             const int h = at.slot + r * step;
-            float x[8], u[8], xx = 0.f, xu = 0.f;
+            float x[16], u[16], xx = 0.f, xu = 0.f;
             widen(vx[r], x);
             widen(vg[r], u);
-            turns.apply(u, rows + at.line * (LANES * 8), at.d0);
+            turns.apply(u, rows + at.line * (LANES * 16), cols);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 xx = fmaf(x[i], x[i], xx);
                 xu = fmaf(x[i] * u[i], w[i], xu);
             }
             const float scale = rsqrtf(fmaf(row_sum<LANES>(xx), p.norm.inv_dim, p.norm.eps));
             const float back = row_sum<LANES>(xu) * p.norm.inv_dim * scale * scale;
-            if (at.in && at.cols && h < p.heads) {
-                float d[8];
+            if (at.in && h < p.heads) {
+                float d[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     d[i] = scale * fmaf(-back, x[i], u[i] * w[i]);
                     dw[i] = fmaf(u[i], x[i] * scale, dw[i]);
                 }
-                *reinterpret_cast<uint4 *>(p.dx + at.tok * p.d_tok + h * p.d_head + at.d0) = narrow(d);
+                cols.store(p.dx + at.tok * p.d_tok + h * p.d_head, d);
             }
         }
     }
     if (!p.part) return;
     __syncthreads();
-    *reinterpret_cast<float4 *>(rows + threadIdx.x * 8) = make_float4(dw[0], dw[1], dw[2], dw[3]);
-    *reinterpret_cast<float4 *>(rows + threadIdx.x * 8 + 4) = make_float4(dw[4], dw[5], dw[6], dw[7]);
-    __syncthreads();
-    if (threadIdx.x < LANES * 8) {
-        float sum = 0.f;
 #pragma unroll
-        for (int l = 0; l < kNormThreads / LANES; ++l) sum += rows[l * (LANES * 8) + threadIdx.x];
-        p.part[static_cast<long long>(blockIdx.x) * (LANES * 8) + threadIdx.x] = sum;
+    for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(rows + threadIdx.x * 16 + i) = make_float4(dw[i], dw[i + 1], dw[i + 2], dw[i + 3]);
+    __syncthreads();
+    if (threadIdx.x < LANES * 16) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int l = 0; l < kNormThreads / LANES; ++l) sum += rows[l * (LANES * 16) + threadIdx.x];
+        p.part[static_cast<long long>(blockIdx.x) * (LANES * 16) + threadIdx.x] = sum;
     }
 }
 
-// dw of 32 columns: 32 lines of threads sum the blocks' parts, every 32nd each, and the
-// lines are summed in order.
-__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *part, int blocks, int pitch, int head_dim, __nv_bfloat16 *dw) {
+// dw of 32 of the lanes' columns: 32 lines of threads sum the blocks' parts, every 32nd
+// each, and the lines are summed in order.  halves: pairs are whole chunks apart, that many
+// columns (0: a lane's chunks are neighbours).
+__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *part, int blocks, int pitch, int head_dim, int halves,
+                                                                __nv_bfloat16 *dw) {
     __shared__ float sums[32][33];
     dev::griddep_launch_dependents();
     dev::griddep_wait();
-    const int col = blockIdx.x * 32 + threadIdx.x;
+    const int at = blockIdx.x * 32 + threadIdx.x;
     float sum = 0.f;
 #pragma unroll 4
-    for (int b = threadIdx.y; b < blocks; b += 32) sum += part[static_cast<long long>(b) * pitch + col];
+    for (int b = threadIdx.y; b < blocks; b += 32) sum += part[static_cast<long long>(b) * pitch + at];
     sums[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
     if (threadIdx.y > 0) return;
     for (int i = 1; i < 32; ++i) sum += sums[i][threadIdx.x];
+    int col = at;
+    if (at < 2 * halves) col = at / 16 * 8 + at % 8 + (at & 8 ? halves : 0);
     if (col < head_dim) dw[col] = __float2bfloat16_rn(sum);
 }
 
 template <int LANES, Pairs PAIRS, bool KV8, int ROWS>
-__global__ void __launch_bounds__(kNormThreads) norm_append_kernel(const __grid_constant__ NormAppendParams p) {
-    __shared__ float rows_s[PAIRS == kNeighbours ? 1 : kNormThreads * 8];
+__global__ void __launch_bounds__(kNormThreads, ROWS > 1 ? 3 : 4) norm_append_kernel(const __grid_constant__ NormAppendParams p) {
+    __shared__ __align__(16) Exchange<LANES, PAIRS> rows_s;
     __shared__ int place[kNormThreads / LANES + 2][2];  // of the block's tokens: position (-1: left out) and cache block (-1: none)
     dev::griddep_launch_dependents();
     const int D = p.norm.head_dim, rows = p.q_heads + 2 * p.kv_heads, lane = threadIdx.x & 31;
-    const Place<LANES> at(p.plan, blockIdx.x, p.threads, D);
+    const Place<LANES> at(p.plan, blockIdx.x, p.threads);
+    const Columns<LANES, PAIRS> cols(p.plan, D);
     const int count = at.last - at.first + 1, step = static_cast<int>(p.plan.slots.d);
     const TurnTable tab = {turn_smem, count * p.plan.pitch};
     dev::griddep_wait();
-    uint4 v[ROWS];
+    Chunks v[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int h = at.slot + r * step;
-        v[r] = make_uint4(0, 0, 0, 0);
-        if (at.in && at.cols && h < rows) {
+        v[r] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (at.in && h < rows) {
             const int hk = h - p.q_heads, hv = hk - p.kv_heads;
-            const __nv_bfloat16 *src = hk < 0   ? p.q + at.tok * p.q_tok + h * D
-                                       : hv < 0 ? p.k + at.tok * p.k_tok + hk * D
-                                                : p.v + at.tok * p.v_tok + hv * D;
-            v[r] = *reinterpret_cast<const uint4 *>(src + at.d0);
+            v[r] = cols.load(hk < 0   ? p.q + at.tok * p.q_tok + h * D
+                             : hv < 0 ? p.k + at.tok * p.k_tok + hk * D
+                                      : p.v + at.tok * p.v_tok + hv * D);
         }
     }
     find_places(p, at.first, count, lane, place);
@@ -344,33 +400,32 @@ __global__ void __launch_bounds__(kNormThreads) norm_append_kernel(const __grid_
     const int bs = static_cast<int>(p.block_size.d);
     const long long cell = (static_cast<long long>(bid) * bs + (pos - fast_div(max(pos, 0), p.block_size) * bs)) * p.kv_heads;
     Turns<LANES, PAIRS> turns;
-    turns.load(p.plan, tab, j, at.d0);
+    turns.load(p.plan, tab, j, cols);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int h = at.slot + r * step, hk = h - p.q_heads, hv = hk - p.kv_heads;
-        float x[8], y[8], w[8], sum = 0.f;
-        widen(v[r], x);
-        load_weight(hk < 0 ? p.norm.weight : p.k_weight, p.norm.offset, at.d0, at.cols, w);
+        float y[16], w[16], sum = 0.f;
+        widen(v[r], y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+        for (int i = 0; i < 16; ++i) sum = fmaf(y[i], y[i], sum);
         const float scale = rsqrtf(fmaf(row_sum<LANES>(sum), p.norm.inv_dim, p.norm.eps));
+        cols.weight(hk < 0 ? p.norm.weight : p.k_weight, p.norm.offset, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i] * (scale * w[i]);
-        turns.apply(y, rows_s + (PAIRS == kNeighbours ? 0 : at.line * (LANES * 8)), at.d0);
-        if (!at.cols || pos < 0 || h >= rows) continue;
+        for (int i = 0; i < 16; ++i) y[i] *= scale * w[i];
+        turns.apply(y, rows_s.row(at.line), cols);
+        if (pos < 0 || h >= rows) continue;
         if (hk < 0) {
-            *reinterpret_cast<uint4 *>(p.q_out + (static_cast<long long>(at.tok) * p.q_heads + h) * D + at.d0) = narrow(y);
+            cols.store(p.q_out + (static_cast<long long>(at.tok) * p.q_heads + h) * D, y);
         } else if (bid >= 0) {
-            const long long to = (cell + (hv < 0 ? hk : hv)) * D + at.d0;
+            const long long to = (cell + (hv < 0 ? hk : hv)) * D;
+            if (hv >= 0) widen(v[r], y);  // (values as they are)
             if constexpr (KV8) {
                 uint8_t *o = static_cast<uint8_t *>(hv < 0 ? p.k_cache : p.v_cache) + to;
-                if (hv < 0)
-                    store_e4m3<8>(o, y, p.k_scale);
-                else
-                    store_e4m3<8>(o, x, p.v_scale);
+                const float f = hv < 0 ? p.k_scale : p.v_scale;
+                if (cols.a) store_e4m3<8>(o + cols.ca, reinterpret_cast<const float(&)[8]>(y[0]), f);
+                if (cols.b) store_e4m3<8>(o + cols.cb, reinterpret_cast<const float(&)[8]>(y[8]), f);
             } else {
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(hv < 0 ? p.k_cache : p.v_cache) + to;
-                *reinterpret_cast<uint4 *>(o) = hv < 0 ? narrow(y) : v[r];
+                cols.store(static_cast<__nv_bfloat16 *>(hv < 0 ? p.k_cache : p.v_cache) + to, y);
             }
         }
     }
@@ -378,7 +433,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_append_kernel(const __grid_
 
 // ---- host side --------------------------------------------------------------------
 
-int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : (head_dim <= 128 ? 16 : 32); }
+int lanes_of(int head_dim) { return head_dim <= 64 ? 4 : (head_dim <= 128 ? 8 : 16); }
 
 RowPlan plan_norm(const pd_rope *rope, int lanes, bool transposed) {
     RowPlan p = {};
@@ -417,9 +472,9 @@ cudaError_t by_shape(int lanes, Pairs pairs, F f) {
         if (pairs == kHalves) return f(l, std::integral_constant<Pairs, kHalves>());
         return f(l, std::integral_constant<Pairs, kScattered>());
     };
+    if (lanes == 4) return with(std::integral_constant<int, 4>());
     if (lanes == 8) return with(std::integral_constant<int, 8>());
-    if (lanes == 16) return with(std::integral_constant<int, 16>());
-    return with(std::integral_constant<int, 32>());
+    return with(std::integral_constant<int, 16>());
 }
 
 int check_norm(const char *what, const pd_rope *rope, int head_dim, const void *w0, const void *w1, float eps, float offset) {
@@ -554,7 +609,7 @@ int pd_norm_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_strid
 
 size_t pd_norm_rope_workspace_bytes(int head_dim) {
     if (head_dim <= 0 || head_dim > PD_MAX_HEAD_DIM) return 0;
-    return static_cast<size_t>(kGradBlocks) * lanes_of(head_dim) * 8 * sizeof(float);
+    return static_cast<size_t>(kGradBlocks) * lanes_of(head_dim) * 16 * sizeof(float);
 }
 
 int pd_norm_rope_backward(const pd_rope *rope, const void *x, int64_t x_token_stride, int64_t x_head_stride, const void *weight, float eps,
@@ -612,7 +667,7 @@ int pd_norm_rope_backward(const pd_rope *rope, const void *x, int64_t x_token_st
     }
     if (grad_weight) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>((head_dim + 31) / 32));
+        cfg.gridDim = dim3(static_cast<unsigned>(lanes * 16 / 32));
         cfg.blockDim = dim3(32, 32);
         cfg.stream = st;
         cudaLaunchAttribute attr[1];
@@ -620,8 +675,8 @@ int pd_norm_rope_backward(const pd_rope *rope, const void *x, int64_t x_token_st
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_weight_grad_kernel, static_cast<const float *>(workspace), blocks, lanes * 8,
-                                                 head_dim, static_cast<__nv_bfloat16 *>(grad_weight));
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_weight_grad_kernel, static_cast<const float *>(workspace), blocks, lanes * 16,
+                                                 head_dim, pairs_of(rope) == kHalves ? rope->rot_dim / 2 : 0, static_cast<__nv_bfloat16 *>(grad_weight));
         if (e != cudaSuccess) return report_cuda(e, what);
     }
     return report_ok();

@@ -140,6 +140,7 @@ struct Plan {
     static constexpr bool kOne = DPAD > 128;  // one stream, S double-buffered
     static constexpr int kTile = tile_tokens(DPAD);
     static constexpr int kBlock = block_rows(DPAD);
+    static constexpr int kPart = 64;  // keys whose weights are handed on together
     static constexpr int kStageBytes = kTile * DPAD * 2;
     static constexpr int kStages = KV8 ? 3 : (DPAD == 64 ? 6 : 4);
     static constexpr int kRawBytes = KV8 ? kTile * DPAD : 0;
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     constexpr int NST = L::kStages;
     constexpr int NT = L::kThreads;
     constexpr bool ONE = L::kOne;
+    constexpr int HB = L::kPart, PARTS = BN / HB;
     constexpr int CHUNKS = DPAD / 8;  // 16-byte chunks of a 16-bit row
     constexpr uint32_t kDescS = tc::instr_desc(KV8 ? 0 : 1, kRowTile, BN, false);
     constexpr uint32_t kDescO = tc::instr_desc(KV8 ? 0 : 1, kRowTile, DPAD, true);
@@ -179,13 +181,13 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t base = dev::smem_addr(smem);
     // barriers: full[NST], empty[NST], raw_full[3], raw_empty[3], landed[NST], s[2],
-    // p[2], o[2], q[2], q_free, tail, streams, task_full[8], task_free[8]
+    // p[4], o[2], half[2], q[2], q_free, tail, streams, task_full[8], task_free[8]
     const uint32_t bars = base + L::bars;
     const uint32_t bar_full = bars, bar_empty = bar_full + 8 * NST, bar_rfull = bar_empty + 8 * NST,
                    bar_rempty = bar_rfull + 24, bar_land = bar_rempty + 24, bar_s = bar_land + 8 * NST, bar_p = bar_s + 16,
-                   bar_o = bar_p + 16, bar_q = bar_o + 16, bar_qfree = bar_q + 16, bar_tail = bar_qfree + 8, bar_x = bar_tail + 8,
+                   bar_o = bar_p + 32, bar_h = bar_o + 16, bar_q = bar_h + 16, bar_qfree = bar_q + 16, bar_tail = bar_qfree + 8, bar_x = bar_tail + 8,
                    bar_task = bar_x + 8, bar_tfree = bar_task + 8 * kTasks;
-    static_assert(3 * NST + 6 + 8 + 3 + 2 * kTasks <= 56, "barrier region");
+    static_assert(3 * NST + 6 + 12 + 3 + 2 * kTasks <= 56, "barrier region");
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 4);
     int *start_seq = reinterpret_cast<int *>(smem + L::misc + 8);           // sequence, head, block
@@ -209,8 +211,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             dev::mbar_init(bar_s + 8 * i, 1);
-            dev::mbar_init(bar_p + 8 * i, 4);
+            dev::mbar_init(bar_p + 16 * i, 4);
+            dev::mbar_init(bar_p + 16 * i + 8, 4);
             dev::mbar_init(bar_o + 8 * i, 1);
+            dev::mbar_init(bar_h + 8 * i, 1);
             dev::mbar_init(bar_q + 8 * i, KV8 ? 4 : 1);
         }
         dev::mbar_init(bar_qfree, 1);
@@ -506,22 +510,25 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                                kd + ((k / 4) * (BN * 128) + (k % 4) * 32) / 16, desc_s, k > 0);
                 tc::commit(bar_s + 8 * buf);
             };
+            // O += P V as the parts of P come: the first while the softmax is at the second
             auto values = [&](int buf, int o, int stage, bool accumulate, bool done) {
                 const uint64_t vd = v_desc + stage * (L::kStageBytes / 16);
-                tc::fence_after();
 #pragma unroll
-                for (int k = 0; k < BN / 16; ++k)
-                    tc::mma_ts(tmem + 256 + o * DPAD, tmem + buf * 128 + k * 8, vd + k * (2048 / 16), kDescO, accumulate || k > 0);
+                for (int h = 0; h < PARTS; ++h) {
+                    if (!wait_one(bar_p + 8 * (PARTS * buf + h), (pph >> buf) & 1, gave_up)) return false;
+                    tc::fence_after();
+#pragma unroll
+                    for (int k = h * (HB / 16); k < (h + 1) * (HB / 16); ++k)
+                        tc::mma_ts(tmem + 256 + o * DPAD, tmem + buf * 128 + k * 8, vd + k * (2048 / 16), kDescO, accumulate || k > 0);
+                    if (h + 1 < PARTS) tc::commit(bar_h + 8 * o);
+                }
+                pph ^= 1u << buf;
                 if (done) tc::commit(bar_o + 8 * o);
+                return true;
             };
             auto release = [&](int stage) { tc::commit(bar_empty + 8 * stage); };
             auto queries_done = [&] {
                 if (!KV8) tc::commit(bar_qfree);
-            };
-            auto weights = [&](int buf) {
-                const bool got = wait_one(bar_p + 8 * buf, (pph >> buf) & 1, gave_up);
-                pph ^= 1u << buf;
-                return got;
             };
             auto queries = [&](int t) {  // (from boxes of q all rows come at once)
                 if (!KV8 && t > 0) return true;
@@ -555,15 +562,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         const bool more = j + 1 < n;
                         const int v = vs;
                         if (more && !(ok = take(ks))) break;
-                        if (j < end0) {
-                            if (!(ok = weights(0))) break;
-                            values(0, 0, v, j > 0, j + 1 == end0);
-                        }
+                        if (j < end0 && !(ok = values(0, 0, v, j > 0, j + 1 == end0))) break;
                         if (more && j + 1 < end0) scores(0, 0, ks);
-                        if (j >= first1) {
-                            if (!(ok = weights(1))) break;
-                            values(1, 1, v, j > first1, !more);
-                        }
+                        if (j >= first1 && !(ok = values(1, 1, v, j > first1, !more))) break;
                         release(v);  // (before the scores: a commit waits for all that came before)
                         if (more) {
                             if (j + 1 >= first1) scores(1, 1, ks);
@@ -589,8 +590,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         const bool next = j + 2 < n;
                         if (next && !(ok = take(ks))) break;
                         const int t = j & 1;
-                        if (!(ok = weights(t))) break;
-                        values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= n);
+                        if (!(ok = values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= n))) break;
                         release(vs);
                         if (next) next_scores(j + 2);
                     }
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t to = tmem + lanes + 256 + t * DPAD;
         const int D = p.head_dim;
-        uint32_t sph = 0, oph = 0, xph = 0;  // phases, a bit for each buffer or stream
+        uint32_t sph = 0, oph = 0, hph = 0, xph = 0;  // phases, a bit for each buffer or stream
         bool ok = true, cut = false;
         // FP8: the rows' scales, in turn in two places: the other stream may still
         // have to read the last segment's when this one's are written (it has by
@@ -750,8 +750,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const int low = live ? first_key(p.shape, at) : sg.low;
             const int end = live ? at + 1 : sg.pos + sg.tokens;
             const int first_j = two ? (t ? sg.first1 : 0) : (ONE ? 0 : t), end_j = two && t == 0 ? sg.end0 : sg.n;
+            const int end_all = __reduce_min_sync(0xffffffffu, end), low_all = __reduce_max_sync(0xffffffffu, low);  // of the warp's rows
             float m = kNegInf, l = 0.f;
-            bool begun = false;
+            bool begun = false, settled = false;  // a tile was seen; every row has its reference
             const int step = ONE || two ? 1 : 2;
             for (int j = first_j; j < end_j; j += step) {
                 const int buf = ONE ? (j & 1) : t;
@@ -760,53 +761,88 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 sph ^= 1u << buf;
                 tc::fence_after();
                 if (KV8 && !begun) scale = row_scale[(two ? t * kRowTile : 0) + r];
-                const int nv = end - (sg.tile0 + j) * BN, nl = low - (sg.tile0 + j) * BN;
-                // -- A row's reference m is the largest score of its first tile with a key;
-                // after that no maximum is taken: weights may be as large as kLift, and
-                // only when a row's weights of a tile sum to more does its warp look
-                // at the scores again and raise m (by a whole number, so that l and O
+                // -- A row's reference m is the largest score of its first part of a tile with
+                // a key; after that no maximum is taken: weights may be as large as
+                // kLift, and only when a row's weights of a part sum to more does its warp
+                // look at the scores again and raise m (by a whole number, so that l and O
                 // are scaled exactly).  FP32 and BF16 hold such weights as exactly as
-                // weights below 1; kLift is what f16 holds.
-                uint32_t x[BN], pk[BN / 2];
-                float sum;
-                bool fresh = live && m == kNegInf, over = false;  // rows that take, or raise, their reference now
+                // weights below 1; kLift is what f16 holds.  Each part goes to the product
+                // as it is done.
+                const int tile_at = (sg.tile0 + j) * BN;
+                auto hand = [&](const uint32_t (&pk)[HB / 2], int h) {
+                    tc::st_columns<HB / 2>(ts + h * (HB / 2), pk);  // over scores that have been read
+                    tc::wait_st();
+                    tc::fence_before();
+                    arrive_warp(bar_p + 8 * (PARTS * buf + h), lane);
+                };
                 bool waited = !ONE || !begun;  // the last product onto O is known to be done
-                for (int pass = 0;;) {
+                int part = 0;                  // the first that is not handed on
+                if (settled && tile_at + BN <= end_all && tile_at >= low_all) {
+                    // every row sees the whole tile
+                    uint32_t x[BN];
                     tc::ld_columns<BN>(ts, x);
-                    if (nv < BN) mask_columns<BN>(x, nv);
-                    if (nl > 0) mask_columns_below<BN>(x, nl);
-                    if (pass == 1 || __any_sync(0xffffffffu, fresh)) {
-                        const float mx = largest_of<BN>(x) * scale;
-                        if (fresh) m = mx;
-                        if (pass == 1) {  // (the scores are read again behind this: no registers for them and O)
-                            raise_reference<DPAD>(to, mx, over, m, l);
-                            pass = 2;
-                            continue;
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h) {
+                        uint32_t pk[HB / 2];
+                        const float sum = weigh<HB, KV8>(reinterpret_cast<const uint32_t(&)[HB]>(x[h * HB]), scale, m, pk);
+                        if (__any_sync(0xffffffffu, live && !(sum <= kLift))) break;
+                        l += sum;
+                        if (ONE) {
+                            ok = wait_bar(bar_o, oph & 1, gave_up);  // (each phase of the barrier is waited for, in order)
+                            oph ^= 1;
+                            waited = true;
                         }
+                        hand(pk, h);
+                        part = h + 1;
                     }
-                    sum = weigh<BN, KV8>(x, scale, m, pk);
-                    over = live && !(sum <= kLift);
-                    fresh = false;
-                    if (pass == 2 || !__any_sync(0xffffffffu, over)) break;
-                    if (!waited) {
-                        ok = wait_bar(bar_o, oph & 1, gave_up);
-                        oph ^= 1;
-                        waited = true;
+                }
+#pragma unroll 1
+                for (; part < PARTS; ++part) {
+                    const int at_part = tile_at + part * HB, nv = end - at_part, nl = low - at_part;
+                    uint32_t x[HB], pk[HB / 2];
+                    bool fresh = live && m == kNegInf, over = false;  // rows that take, or raise, their reference now
+                    float sum;
+                    for (int pass = 0;;) {
+                        tc::ld_columns<HB>(ts + part * HB, x);
+                        if (nv < HB) mask_columns<HB>(x, nv);
+                        if (nl > 0) mask_columns_below<HB>(x, nl);
+                        if (pass == 1 || __any_sync(0xffffffffu, fresh)) {
+                            const float mx = largest_of<HB>(x) * scale;
+                            if (fresh) m = mx;
+                            if (pass == 1) {  // (the scores are read again behind this: no registers for them and O)
+                                raise_reference<DPAD>(to, mx, over, m, l);
+                                pass = 2;
+                                continue;
+                            }
+                        }
+                        sum = weigh<HB, KV8>(x, scale, m, pk);
+                        over = live && !(sum <= kLift);
+                        fresh = false;
+                        if (pass == 2 || !__any_sync(0xffffffffu, over)) break;
+                        // O is to be scaled: the products onto it have to be done, those of the
+                        // last tile (with two streams they are where this one's scores are)
+                        // and of the part before
+                        if (part > 0) {
+                            ok = wait_bar(bar_h + 8 * t, (hph >> t) & 1, gave_up) && ok;
+                        } else if (!waited) {
+                            ok = wait_bar(bar_o, oph & 1, gave_up) && ok;
+                            oph ^= 1;
+                            waited = true;
+                        }
                         tc::fence_after();
+                        pass = 1;
                     }
-                    pass = 1;
+                    l += sum;
+                    if (ONE && !waited) {
+                        ok = wait_bar(bar_o, oph & 1, gave_up) && ok;
+                        oph ^= 1;
+                    }
+                    hand(pk, part);
+                    settled = __all_sync(0xffffffffu, !live || m > kNegInf);
                 }
                 begun = true;
-                l += sum;
-                tc::st_columns<BN / 2>(ts, pk);  // over S, which has been read
-                if (ONE && !waited) {  // (each phase of the barrier is waited for, in order)
-                    ok = wait_bar(bar_o, oph & 1, gave_up) && ok;
-                    oph ^= 1;
-                }
+                hph ^= 1u << t;
                 if (!ok) break;
-                tc::wait_st();
-                tc::fence_before();
-                arrive_warp(bar_p + 8 * buf, lane);
             }
             if (!ok) break;
 

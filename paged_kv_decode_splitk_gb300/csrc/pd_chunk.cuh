@@ -145,20 +145,18 @@ struct Plan {
     static constexpr int kStages = KV8 ? 3 : (DPAD == 64 ? 6 : 4);
     static constexpr int kRawBytes = KV8 ? kTile * DPAD : 0;
     static constexpr int kRawStages = KV8 ? 3 : 0;
-    static constexpr int kOutBytes = 2048;  // of a warp: 32 rows x 64 bytes on their way out
+    static constexpr int kOutBytes = 64;  // of each of a warp's 32 rows on their way out
     static constexpr int q = 0;             // [DPAD / 64][kBlock rows][128 bytes]
     static constexpr int ring = q + kBlock * DPAD * 2;
     static constexpr int raw = ring + kStages * kStageBytes;
     static constexpr int out = raw + kRawStages * kRawBytes;
-    // (over an FP8 cache the warps that load the queries are those that stage results
-    // in their place)
-    static constexpr int bars = out + (KV8 ? 0 : (kOne ? 4 : 8) * kOutBytes);
-    static constexpr int misc = bars + 56 * 8;
-    static constexpr int tasks = misc + 256;
+    static constexpr int bars = out + 4 * 32 * kOutBytes;
+    static constexpr int misc = bars + 64 * 8;
+    static constexpr int tasks = misc + 32 + 2 * 16 * 8;
     static constexpr int row_scale = tasks + (kTasks * static_cast<int>(sizeof(Task)) + 15) / 16 * 16;
     static constexpr int stream_ml = row_scale + (KV8 ? 2 * kBlock * 4 : 0);
-    static constexpr int total = 1024 + stream_ml + (kOne ? 0 : 2 * kRowTile * 8);
-    static constexpr int kThreads = 384;
+    static constexpr int total = 1024 + stream_ml + 2 * 2 * kRowTile * 8;
+    static constexpr int kThreads = 512;
 };
 
 template <int DPAD, bool KV8>
@@ -181,18 +179,18 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t base = dev::smem_addr(smem);
     // barriers: full[NST], empty[NST], raw_full[3], raw_empty[3], landed[NST], s[2],
-    // p[4], o[2], half[2], q[2], q_free, tail, streams, task_full[8], task_free[8]
+    // p[4], o, half[2], q[2], q_free, tail, done[2], o_free[2], ml[4], task_full[8], task_free[8]
     const uint32_t bars = base + L::bars;
     const uint32_t bar_full = bars, bar_empty = bar_full + 8 * NST, bar_rfull = bar_empty + 8 * NST,
                    bar_rempty = bar_rfull + 24, bar_land = bar_rempty + 24, bar_s = bar_land + 8 * NST, bar_p = bar_s + 16,
-                   bar_o = bar_p + 32, bar_h = bar_o + 16, bar_q = bar_h + 16, bar_qfree = bar_q + 16, bar_tail = bar_qfree + 8, bar_x = bar_tail + 8,
-                   bar_task = bar_x + 8, bar_tfree = bar_task + 8 * kTasks;
-    static_assert(3 * NST + 6 + 12 + 3 + 2 * kTasks <= 56, "barrier region");
+                   bar_o = bar_p + 32, bar_h = bar_o + 8, bar_q = bar_h + 16, bar_qfree = bar_q + 16, bar_tail = bar_qfree + 8, bar_done = bar_tail + 8,
+                   bar_ofree = bar_done + 16, bar_ml = bar_ofree + 16, bar_task = bar_ml + 32, bar_tfree = bar_task + 8 * kTasks;
+    static_assert(3 * NST + 6 + 13 + 8 + 2 * kTasks <= 64, "barrier region");
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 4);
     int *start_seq = reinterpret_cast<int *>(smem + L::misc + 8);           // sequence, head, block
     long long *start_rest = reinterpret_cast<long long *>(smem + L::misc + 24);
-    long long *sums = reinterpret_cast<long long *>(smem + L::misc + 32);  // [2][12] of the warps
+    long long *sums = reinterpret_cast<long long *>(smem + L::misc + 32);  // [2][NT / 32] of the warps
 
     // (the warp's number from one lane, so that the compiler knows it to be the
     // same on all: the product warp's operands then live in uniform registers)
@@ -213,16 +211,19 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             dev::mbar_init(bar_s + 8 * i, 1);
             dev::mbar_init(bar_p + 16 * i, 4);
             dev::mbar_init(bar_p + 16 * i + 8, 4);
-            dev::mbar_init(bar_o + 8 * i, 1);
             dev::mbar_init(bar_h + 8 * i, 1);
+            dev::mbar_init(bar_done + 8 * i, 1);
+            dev::mbar_init(bar_ofree + 8 * i, 4);
+            dev::mbar_init(bar_ml + 8 * i, 4);
+            dev::mbar_init(bar_ml + 16 + 8 * i, 4);
             dev::mbar_init(bar_q + 8 * i, KV8 ? 4 : 1);
         }
         dev::mbar_init(bar_qfree, 1);
         dev::mbar_init(bar_tail, 1);
-        dev::mbar_init(bar_x, 8);
+        dev::mbar_init(bar_o, 1);
         for (int i = 0; i < kTasks; ++i) {
             dev::mbar_init(bar_task + 8 * i, 1);
-            dev::mbar_init(bar_tfree + 8 * i, 3 + (ONE ? 4 : 8));  // the warps that read it
+            dev::mbar_init(bar_tfree + 8 * i, 3 + (ONE ? 4 : 8) + 4);  // the warps that read it
         }
         dev::fence_mbar_init();
         *gave_up = 0;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     all = warp_scan(all);
     if (lane == 31) {
         sums[warp] = upto;
-        sums[12 + warp] = all;
+        sums[NT / 32 + warp] = all;
     }
     tc::fence_before();
     __syncthreads();
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     dev::griddep_launch_dependents();
     constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
     long long W = 0;
-    for (int i = 0; i < 12; ++i) W += sums[12 + i];
+    for (int i = 0; i < NT / 32; ++i) W += sums[NT / 32 + i];
     const int C = cta_count(W, gridDim.x);
     Walk walk = {};
     if (static_cast<int>(blockIdx.x) < C) {
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 __syncthreads();
             }
             long long stripe = 0, mine = 0;
-            for (int i = 0; i < 12; ++i) {
+            for (int i = 0; i < NT / 32; ++i) {
                 if (i == warp) mine = stripe;
                 stripe += sums[i];
             }
@@ -333,9 +334,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             task_ph ^= 1;
         }
     };
-    // Registers: a softmax thread holds a whole tile row.  384 threads were
-    // launched with 168 each: 128 x 88 + 256 x 208 is what all of them have.
-    static_assert(NT == 384 && 88 + 2 * 208 <= 3 * 168, "the shares add up to the launch's registers");
+    // Registers: 512 threads were launched with 128 each, and 128 x 88 + 256 x 144 + 128 x
+    // 136 is what all of them have.
+    static_assert(NT == 512 && 88 + 2 * 144 + 136 <= 4 * 128, "the shares add up to the launch's registers");
 
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         // between two of them the tensor core may spend idle.
         if (tc::elect_one()) {
             int st = 0;
-            uint32_t ph = 0, pph = 0, qph = 0;  // phases: of the ring; a bit for each stream
+            uint32_t ph = 0, pph = 0, qph = 0, fph = 0;  // phases: of the ring; a bit for each stream
             bool ok = true;
             const uint32_t qa = base + L::q, ra = base + L::ring;
             const uint64_t q_desc = tc::smem_desc(qa, 16), k_desc = tc::smem_desc(ra, 16), v_desc = tc::smem_desc(ra, BN * 128);
@@ -513,6 +514,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             // O += P V as the parts of P come: the first while the softmax is at the second
             auto values = [&](int buf, int o, int stage, bool accumulate, bool done) {
                 const uint64_t vd = v_desc + stage * (L::kStageBytes / 16);
+                if (!accumulate) {  // (the last item's O has left)
+                    if (!wait_one(bar_ofree + 8 * o, ((fph >> o) & 1) ^ 1, gave_up)) return false;
+                    fph ^= 1u << o;
+                }
 #pragma unroll
                 for (int h = 0; h < PARTS; ++h) {
                     if (!wait_one(bar_p + 8 * (PARTS * buf + h), (pph >> buf) & 1, gave_up)) return false;
@@ -523,13 +528,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     if (h + 1 < PARTS) tc::commit(bar_h + 8 * o);
                 }
                 pph ^= 1u << buf;
-                if (done) tc::commit(bar_o + 8 * o);
+                if (ONE) tc::commit(bar_o);
+                if (done) tc::commit(bar_done + 8 * o);
                 return true;
             };
             auto release = [&](int stage) { tc::commit(bar_empty + 8 * stage); };
-            auto queries_done = [&] {
-                if (!KV8) tc::commit(bar_qfree);
-            };
+            auto queries_done = [&] { tc::commit(bar_qfree); };
             auto queries = [&](int t) {  // (from boxes of q all rows come at once)
                 if (!KV8 && t > 0) return true;
                 const bool got = wait_one(bar_q + 8 * t, (qph >> t) & 1, gave_up);
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         const bool next = j + 2 < n;
                         if (next && !(ok = take(ks))) break;
                         const int t = j & 1;
-                        if (!(ok = values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), ONE || j + 2 >= n))) break;
+                        if (!(ok = values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), j + (ONE ? 1 : 2) >= n))) break;
                         release(vs);
                         if (next) next_scores(j + 2);
                     }
@@ -666,8 +670,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         for (long long i = handed < NST ? 0 : handed - NST; ok && i < handed; ++i)
             ok = wait_bar(bar_empty + 8 * static_cast<int>(i % NST), static_cast<uint32_t>((i / NST) & 1), gave_up);
     }
-    } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     if (warp < (ONE ? 8 : 12)) {
         // ---- softmax: a thread per row -----------------------------------------------
         const int t = (warp - 4) >> 2;            // the stream
@@ -675,22 +679,25 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t to = tmem + lanes + 256 + t * DPAD;
         const int D = p.head_dim;
-        uint32_t sph = 0, oph = 0, hph = 0, xph = 0;  // phases, a bit for each buffer or stream
-        bool ok = true, cut = false;
+        uint32_t sph = 0, oph = 0, hph = 0, qph = 0;  // phases, a bit for each buffer or stream
+        bool ok = true, any = false;
         // FP8: the rows' scales, in turn in two places: the other stream may still
         // have to read the last segment's when this one's are written (it has by
         // the time a third segment begins: its weights of the first went before)
         float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
-        int turn = 0;
+        int turn = 0, out_turn = 0;
         for (; ok && next_task(); task_done()) {
             const Task &sg = tasks[task];  // (read again wherever it is wanted, to hold no registers)
             const bool two = !ONE && sg.two;
             float scale = p.scale_log2;
             if constexpr (KV8) {
                 row_scale = reinterpret_cast<float *>(smem + L::row_scale) + turn * BR;
-                turn ^= 1;
                 // -- this stream's query rows into shared memory (128-byte swizzle); with
                 // at most 128 rows the streams share stream 0's.
+                if (sg.n > 0) {
+                    if (!(ok = wait_bar(bar_qfree, qph ^ 1, gave_up))) break;
+                    qph ^= 1;
+                }
                 if ((two || t == 0) && sg.n > 0) {
                     // 32 rows x CHUNKS chunks over 32 lanes, sixteen loads in flight at once
                     constexpr int BATCH = CHUNKS < 16 ? CHUNKS : 16;
@@ -775,16 +782,15 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     tc::fence_before();
                     arrive_warp(bar_p + 8 * (PARTS * buf + h), lane);
                 };
-                bool waited = !ONE || !begun;  // the last product onto O is known to be done
+                bool waited = !ONE || !any;  // the last product onto O (that of the last item, too) is known to be done
                 int part = 0;                  // the first that is not handed on
                 if (settled && tile_at + BN <= end_all && tile_at >= low_all) {
                     // every row sees the whole tile
-                    uint32_t x[BN];
-                    tc::ld_columns<BN>(ts, x);
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < PARTS; ++h) {
-                        uint32_t pk[HB / 2];
-                        const float sum = weigh<HB, KV8>(reinterpret_cast<const uint32_t(&)[HB]>(x[h * HB]), scale, m, pk);
+                        uint32_t x[HB], pk[HB / 2];
+                        tc::ld_columns<HB>(ts + h * HB, x);
+                        const float sum = weigh<HB, KV8>(x, scale, m, pk);
                         if (__any_sync(0xffffffffu, live && !(sum <= kLift))) break;
                         l += sum;
                         if (ONE) {
@@ -840,154 +846,168 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     hand(pk, part);
                     settled = __all_sync(0xffffffffu, !live || m > kNegInf);
                 }
-                begun = true;
+                begun = any = true;
                 hph ^= 1u << t;
                 if (!ok) break;
             }
             if (!ok) break;
 
-            // -- the way out: 64 bytes of a row at a time through this warp's staging
-            // area (chunk c of row r at c xor r/2 mod 4, so that neither side hits a
-            // bank twice), four lanes a row: BF16 results, or FP32 partials.
-            uint8_t *stage = KV8 ? smem + L::q + t * (kRowTile * 128) + (warp & 3) * 4096
-                                 : smem + L::out + (t * 4 + (warp & 3)) * L::kOutBytes;
-            const int row0 = (two ? t * kRowTile : 0) + (warp & 3) * 32 + (lane >> 2);  // of the block: row0 + 8 i
-            const long long slot = 2ll * blockIdx.x + (sg.begins ? 1 : 0);
-            const int part_rows = sg.tokens * IH;
-            long long dst[4];  // of the rows' first columns in out (partials), -1: none
+            // -- the row's reference and sum for the way out, of the items that the stream had a
+            // tile of, in turn in two places with a barrier each: by the time of a third the
+            // first has been read, whose O had to leave before the second's products
+            turn ^= 1;
+            if (end_j > first_j) {
+                reinterpret_cast<float2 *>(smem + L::stream_ml)[(out_turn * 2 + t) * kRowTile + r] = make_float2(m, l);
+                arrive_warp(bar_ml + 8 * (2 * out_turn + t), lane);
+                out_turn ^= 1;
+            }
+        }
+    }
+    } else {
+    // ---- the way out: an item's O, as soon as its products are done, while the softmax
+    // warps are at the next item ----------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int r = (warp & 3) * 32 + lane, D = p.head_dim;
+    // RB bytes of a row at a time go through this warp's staging area (16-byte chunk c of row
+    // r at c xor r, or r / 2 where a row has 4, so that neither side hits a bank twice), RC
+    // lanes a row: BF16 results, or FP32 partials.
+    constexpr int RB = L::kOutBytes, RC = RB / 16, RPI = 32 / RC;
+    uint8_t *stage = smem + L::out + (warp & 3) * (32 * RB);
+    const auto swizzle = [](int row) { return RC == 8 ? row & 7 : (row >> 1) & 3; };
+    const float2 *mls = reinterpret_cast<const float2 *>(smem + L::stream_ml);
+    uint32_t mph = 0, dph = 0;  // phases of the streams' (m, l), a bit for each place, and O
+    int turn = 0;               // the streams' places, a bit each
+    bool ok = true, cut = false;
+    while (ok && next_task()) {
+        const Task &sg = tasks[task];
+        const int n = sg.n, token = sg.token, tokens = sg.tokens, head = sg.head, heads = sg.heads;
+        const bool two = !ONE && sg.two, whole = sg.whole;
+        const int used = ONE ? (n > 0) : two ? (sg.end0 > 0 ? 1 : 0) | (n > sg.first1 ? 2 : 0) : (n > 0 ? 1 : 0) | (n > 1 ? 2 : 0);  // streams' O
+        const long long slot = 2ll * blockIdx.x + (sg.begins ? 1 : 0);
+        if (!whole && sg.begins && tid == 384) {
+            p.cut[blockIdx.x] = {token, head, tokens, heads, sg.parts};
+            cut = true;
+        }
+        task_done();
+        for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
+            // (with at most 128 rows the streams' two partials of a row are folded)
+            const int k1 = ONE || two ? t + 1 : 2;
+            float2 ml[2] = {make_float2(kNegInf, 0.f), make_float2(kNegInf, 0.f)};
+            for (int k = t; ok && k < k1; ++k) {
+                if (!((used >> k) & 1)) continue;
+                const int at = 2 * ((turn >> k) & 1) + k;
+                ok = wait_bar(bar_ml + 8 * at, (mph >> at) & 1, gave_up);
+                mph ^= 1u << at;
+                turn ^= 1 << k;
+                ml[k - t] = mls[at * kRowTile + r];
+                ok = wait_bar(bar_done + 8 * k, (dph >> k) & 1, gave_up) && ok;
+                dph ^= 1u << k;
+            }
+            if (!ok) break;
+            tc::fence_after();
+            const bool has0 = (used >> t) & 1 && ml[0].y != 0.f, has1 = k1 > t + 1 && (used >> 1) & 1 && ml[1].y != 0.f;
+            const float M = fmaxf(has0 ? ml[0].x : kNegInf, has1 ? ml[1].x : kNegInf);
+            const float f0 = !has0 ? 0.f : has1 ? dev::exp2_approx(ml[0].x - M) : 1.f, f1 = !has1 ? 0.f : has0 ? dev::exp2_approx(ml[1].x - M) : 1.f;
+            const float l = (has0 ? ml[0].y * f0 : 0.f) + (has1 ? ml[1].y * f1 : 0.f);
+            const float f = !whole ? 1.f : l == 0.f ? 0.f : __fdiv_rn(p.v_scale, l);
+            const float g0 = f0 * f, g1 = f1 * f;
+            // the row's sum: ln of it, or (m, l) of a partial
+            const int br = t * kRowTile + r, tk = fast_div(br, p.fd_heads), part_rows = tokens * IH;
+            if (whole) {
+                if (p.lse && tk < tokens && br - tk * IH < heads)
+                    p.lse[static_cast<long long>(token + tk) * p.num_q_heads + head + (br - tk * IH)] =
+                        l == 0.f ? kNegInf : (M + log2f(l)) * 0.6931471805599453f;
+            } else if (br < part_rows) {
+                *reinterpret_cast<float2 *>(p.part_ml + (slot * p.slot_rows + br) * 2) = make_float2(M, l);
+            }
+            // where the rows that this lane writes begin, in out or the partials (-1: none)
+            long long dst[RC];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 8 * i, k = fast_div(row, p.fd_heads), h = row - k * IH;
-                if (sg.whole)
-                    dst[i] = k < sg.tokens && h < sg.heads ? (static_cast<long long>(sg.token + k) * p.num_q_heads + sg.head + h) * D : -1;
+            for (int i = 0; i < RC; ++i) {
+                const int row = t * kRowTile + (warp & 3) * 32 + i * RPI + lane / RC, k = fast_div(row, p.fd_heads), h = row - k * IH;
+                if (whole)
+                    dst[i] = k < tokens && h < heads ? (static_cast<long long>(token + k) * p.num_q_heads + head + h) * D : -1;
                 else
                     dst[i] = row < part_rows ? (slot * p.slot_rows + row) * DPAD : -1;
             }
-            // (64 bytes of this thread's row; `width` elements of them are 16 bytes)
-            auto emit = [&](uint4 a, uint4 b, uint4 c, uint4 d, int width, auto put) {
-                uint8_t *mine = stage + lane * 64;
-                const int f = (lane >> 1) & 3;
-                *reinterpret_cast<uint4 *>(mine + ((0 ^ f) << 4)) = a;
-                *reinterpret_cast<uint4 *>(mine + ((1 ^ f) << 4)) = b;
-                *reinterpret_cast<uint4 *>(mine + ((2 ^ f) << 4)) = c;
-                *reinterpret_cast<uint4 *>(mine + ((3 ^ f) << 4)) = d;
+            // 32 columns of this thread's row, scaled
+            const uint32_t from = tmem + lanes + 256 + t * DPAD;
+            const bool any0 = (used >> t) & 1, any1 = k1 > t + 1 && (used >> 1) & 1;
+            auto fetch = [&](int c, uint32_t (&x)[32]) {
+                if (any0) {
+                    tc::ld_32x32(from + c, x);
+                    tc::wait_ld(x);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = has0 ? __float_as_uint(__uint_as_float(x[i]) * g0) : 0u;
+                if (any1) {
+                    uint32_t y[32];
+                    tc::ld_32x32(from + DPAD + c, y);
+                    tc::wait_ld(y);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (has1) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), g1, __uint_as_float(x[i])));
+                }
+            };
+            // all rows' RB bytes, this thread's in y, to column c on
+            auto put = [&](const uint32_t *y, auto store) {
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = (lane >> 2) + 8 * i;
-                    if (dst[i] >= 0)
-                        put(dst[i] + (lane & 3) * width, *reinterpret_cast<const uint4 *>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)));
-                }
+                for (int k = 0; k < RC; ++k)
+                    *reinterpret_cast<uint4 *>(stage + lane * RB + ((k ^ swizzle(lane)) << 4)) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
                 __syncwarp();
-            };
-            // columns c to c + 31 of this thread's row, times f
-            auto store = [&](int c, const uint32_t (&x)[32], float f) {
-                if (sg.whole) {
-                    uint32_t y[16];
+                uint4 v[RC];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        y[i] = f == 0.f ? 0u : dev::pack_bf16x2(__uint_as_float(x[2 * i]) * f, __uint_as_float(x[2 * i + 1]) * f);
-                    const bool in = c + (lane & 3) * 8 < D;
-                    emit(make_uint4(y[0], y[1], y[2], y[3]), make_uint4(y[4], y[5], y[6], y[7]), make_uint4(y[8], y[9], y[10], y[11]),
-                         make_uint4(y[12], y[13], y[14], y[15]), 8, [&](long long to_col, uint4 v) {
-                             if (in) *reinterpret_cast<uint4 *>(p.out + to_col + c) = v;
-                         });
-                } else {
+                for (int i = 0; i < RC; ++i) {
+                    const int row = i * RPI + lane / RC;
+                    v[i] = *reinterpret_cast<const uint4 *>(stage + row * RB + (((lane % RC) ^ swizzle(row)) << 4));
+                }
 #pragma unroll
-                    for (int k = 0; k < 32; k += 16)
-                        emit(make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]), make_uint4(x[k + 4], x[k + 5], x[k + 6], x[k + 7]),
-                             make_uint4(x[k + 8], x[k + 9], x[k + 10], x[k + 11]), make_uint4(x[k + 12], x[k + 13], x[k + 14], x[k + 15]), 4,
-                             [&](long long to_col, uint4 v) { *reinterpret_cast<uint4 *>(p.part_o + to_col + c + k) = v; });
+                for (int i = 0; i < RC; ++i)
+                    if (dst[i] >= 0) store(dst[i], v[i]);
+            };
+            auto left = [&] {  // O has been read
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    for (int k = t; k < k1; ++k)
+                        if ((used >> k) & 1) arrive(bar_ofree + 8 * k);
                 }
             };
-            // the row's sum and reference: ln of the sum, or (m, l) of a partial
-            auto finish = [&](float mm, float ll) {
-                if (sg.whole) {
-                    if (p.lse && live)
-                        p.lse[static_cast<long long>(sg.token + tk) * p.num_q_heads + sg.head + (br - tk * IH)] =
-                            ll > 0.f || !(ll <= 0.f) ? (mm + log2f(ll)) * 0.6931471805599453f : kNegInf;
-                } else if (br < part_rows) {
-                    *reinterpret_cast<float2 *>(p.part_ml + (slot * p.slot_rows + br) * 2) = make_float2(mm, ll);
+            if (whole) {
+                constexpr int WC = RB / 2;  // columns
+#pragma unroll 1
+                for (int c = 0; c < DPAD; c += WC) {
+                    uint32_t y[WC / 2];
+#pragma unroll
+                    for (int b = 0; b < WC; b += 32) {
+                        uint32_t x[32];
+                        fetch(c + b, x);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[b / 2 + i] = dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                    }
+                    if (c + WC >= DPAD) left();
+                    const int col = c + (lane % RC) * 8;
+                    put(y, [&](long long at, const uint4 &v) {
+                        if (col < D) *reinterpret_cast<uint4 *>(p.out + at + col) = v;
+                    });
                 }
-            };
-            if (!sg.whole && sg.begins && tid == 128) {  // (warp 4 begins with every segment's rows 0 to 31)
-                p.cut[blockIdx.x] = {sg.token, sg.head, sg.tokens, sg.heads, sg.parts};
-                cut = true;
-            }
-            if (ONE || two) {
-                const bool some = end_j > first_j;
-                if (some) {
-                    if (!(ok = wait_bar(bar_o + 8 * t, (oph >> t) & 1, gave_up))) break;
-                    oph ^= 1u << t;
-                    tc::fence_after();
-                }
-                if (two) {  // (the other stream's phase, which this one does not wait for)
-                    if (t ? sg.end0 > 0 : sg.n > sg.first1) oph ^= 2u >> t;
-                }
-                finish(m, l);
-                const float f = l == 0.f ? 0.f : __fdiv_rn(p.v_scale, l);
+            } else {
+                constexpr int PC = RB / 4;
 #pragma unroll 1
                 for (int c = 0; c < DPAD; c += 32) {
                     uint32_t x[32];
-                    if (some) {
-                        tc::ld_32x32(to + c, x);
-                        tc::wait_ld(x);
-                    } else {
+                    fetch(c, x);
+                    if (c + 32 >= DPAD) left();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = 0;
-                    }
-                    store(c, x, f);
+                    for (int b = 0; b < 32; b += PC)
+                        put(x + b, [&](long long at, const uint4 &v) { *reinterpret_cast<uint4 *>(p.part_o + at + c + b + (lane % RC) * 4) = v; });
                 }
-                tc::fence_before();
-            } else {
-                // the streams' two partials of the row, folded: each stream then writes
-                // half of the columns
-                float2 *ml = reinterpret_cast<float2 *>(smem + L::stream_ml);
-                ml[t * kRowTile + r] = make_float2(m, l);
-                arrive_warp(bar_x, lane);
-                if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
-                xph ^= 1;
-                for (int k = 0; k < 2 && ok; ++k) {
-                    if (k < sg.n) {
-                        ok = wait_bar(bar_o + 8 * k, (oph >> k) & 1, gave_up);
-                        oph ^= 1u << k;
-                    }
-                }
-                if (!ok) break;
-                tc::fence_after();
-                const float2 a = ml[r], b = ml[kRowTile + r];
-                const float M = fmaxf(a.y == 0.f ? kNegInf : a.x, b.y == 0.f ? kNegInf : b.x);
-                const float fa = a.y == 0.f ? 0.f : dev::exp2_approx(a.x - M), fb = b.y == 0.f ? 0.f : dev::exp2_approx(b.x - M);
-                const float ll = (a.y == 0.f ? 0.f : a.y * fa) + (b.y == 0.f ? 0.f : b.y * fb);
-                if (t == 0) finish(M, ll);
-                const float f = ll == 0.f ? 0.f : __fdiv_rn(p.v_scale, ll);
-#pragma unroll 1
-                for (int c = t * (DPAD / 2); c < (t + 1) * (DPAD / 2); c += 32) {
-                    uint32_t x[32], y[32];
-                    if (sg.n > 0) {
-                        tc::ld_32x32(tmem + lanes + 256 + c, x);
-                        tc::wait_ld(x);
-                    }
-                    if (sg.n > 1) {
-                        tc::ld_32x32(tmem + lanes + 256 + DPAD + c, y);
-                        tc::wait_ld(y);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float xa = sg.n == 0 || fa == 0.f ? 0.f : __uint_as_float(x[i]) * fa;
-                        x[i] = __float_as_uint(sg.n > 1 && fb != 0.f ? fmaf(__uint_as_float(y[i]), fb, xa) : xa);
-                    }
-                    store(c, x, f);
-                }
-                tc::fence_before();
-                // both streams have read both O before either lets one be overwritten
-                arrive_warp(bar_x, lane);
-                if (!(ok = wait_bar(bar_x, xph, gave_up))) break;
-                xph ^= 1;
             }
         }
-        if (tid == 128 && !cut) p.cut[blockIdx.x] = {0, 0, 0, 0, 0};
     }
+    if (tid == 384 && !cut) p.cut[blockIdx.x] = {0, 0, 0, 0, 0};
     }
     tc::fence_before();
     __syncthreads();

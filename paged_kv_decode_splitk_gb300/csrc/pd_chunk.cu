@@ -238,9 +238,10 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     }
     // no more CTAs than the most units these sizes can make would be shared by
     const long long items = static_cast<long long>(num_seqs) + num_tokens / p.shape.block_tokens;
-    const long long most = items * p.shape.heads * (kItemUnits + p.max_tokens / p.shape.tile + 1);
+    const long long most = items * p.shape.heads * (kItemUnits + (p.max_tokens >> p.shape.tile_log2) + 1);
     const int sms = sm_count_of_device();
-    const int ctas = std::max(1, cta_count(most, std::min(sms, kMaxCtas)));
+    const int ctas = static_cast<int>(std::min<long long>(std::max(1, std::min(sms, kMaxCtas)), (most + kCtaUnits - 1) / kCtaUnits));
+    p.inverse = inverse_of(std::max(ctas, 2));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = kv8 ? dispatch<true>(dpad, &view.k, &view.v, &tq, p, ctas, st) : dispatch<false>(dpad, &view.k, &view.v, &tq, p, ctas, st);
     if (e != cudaSuccess) return report_cuda(e, "chunk attention launch");
@@ -318,18 +319,20 @@ int pd_debug_chunk_walk(int num_seqs, const int32_t *token_starts, const int32_t
     };
     long long W = 0;
     for (int i = 0; i < num_seqs; ++i) W += s.heads * head_units(s, spans(i));
-    const int C = cta_count(W, max_ctas);
+    const long long share = cta_units(W, max_ctas, inverse_of(std::max(max_ctas, 2)));
+    const int C = static_cast<int>((W + share - 1) / share);
     int n = 0;
     for (int c = 0; c < C; ++c) {
         Walk w = {};
-        w.u = cta_begin(W, C, c);
-        w.end = cta_begin(W, C, c + 1);
+        w.u = c * share;
+        w.end = std::min(W, (c + 1) * share);
         long long rest = w.u;
         while (rest >= s.heads * head_units(s, spans(w.seq))) rest -= s.heads * head_units(s, spans(w.seq++));
         w.span = spans(w.seq);
         const long long of_head = head_units(s, w.span);
-        w.head = static_cast<int>(rest / of_head);
-        rest -= w.head * of_head;
+        w.kvh = static_cast<int>(rest / of_head) / s.head_parts;
+        w.part = static_cast<int>(rest / of_head) % s.head_parts;
+        rest %= of_head;
         for (int n = blocks_of(s, w.span.n); n > 1;) {  // (by halves where a warp takes 32nds)
             const int step = (n + 1) / 2;
             const bool up = units_before(s, w.span, w.block + step) <= rest;
@@ -341,7 +344,7 @@ int pd_debug_chunk_walk(int num_seqs, const int32_t *token_starts, const int32_t
         while (next_segment(s, num_seqs, spans, w, g)) {
             if (n == max_segments) return pd::report(PD_ERR_CAPACITY, "pd_debug_chunk_walk: more than %d segments", n);
             const int32_t v[11] = {c, g.seq, g.kvh, g.head, g.heads, g.token, g.tokens, g.tile0, g.n, g.begins ? (g.whole ? 2 : 1) : 0,
-                                   cta_of_unit(W, C, g.item_end - 1)};
+                                   static_cast<int32_t>(g.item_last / share)};
             std::copy(v, v + 11, segments + 11ll * n++);
         }
     }
@@ -349,7 +352,7 @@ int pd_debug_chunk_walk(int num_seqs, const int32_t *token_starts, const int32_t
     totals[0] = W;
     totals[1] = C;
     totals[2] = s.block_tokens;
-    totals[3] = s.tile;
+    totals[3] = 1 << s.tile_log2;
     totals[4] = s.item_heads;
     totals[5] = query_box_tokens(s);
     return pd::report_ok();

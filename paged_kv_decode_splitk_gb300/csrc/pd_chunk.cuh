@@ -110,15 +110,15 @@ constexpr int kTasks = 8;
 
 // With more than 128 rows each stream has 128 of them, and need not meet the tiles
 // that only the other's rows see.
-__device__ __forceinline__ Task task_of(const ChunkParams &p, const Segment &g, int dpad, long long W, int C) {
+__device__ __forceinline__ Task task_of(const ChunkParams &p, const Segment &g, int dpad, long long end, long long share) {
     const Shape &s = p.shape;
     Task t;
     t.n = g.n;
     t.tile0 = g.tile0;
     t.two = dpad <= 128 && g.tokens * s.item_heads > kRowTile;
     const int last = g.pos + min(fast_div(kRowTile - 1, p.fd_heads), g.tokens - 1);  // the last position of the first 128 rows
-    t.end0 = min(g.n, max(0, (last >= 0 ? last / s.tile + 1 : 0) - g.tile0));
-    t.first1 = min(g.n, max(0, first_key(s, g.pos + fast_div(kRowTile, p.fd_heads)) / s.tile - g.tile0));
+    t.end0 = min(g.n, max(0, (last >= 0 ? (last >> s.tile_log2) + 1 : 0) - g.tile0));
+    t.first1 = min(g.n, max(0, (first_key(s, g.pos + fast_div(kRowTile, p.fd_heads)) >> s.tile_log2) - g.tile0));
     t.token = g.token;
     t.tokens = g.tokens;
     t.head = g.head;
@@ -130,7 +130,9 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, const Segment &g, 
     t.kvh = g.kvh;
     t.begins = g.begins;
     t.whole = g.whole;
-    t.parts = g.whole ? 1 : cta_of_unit(W, C, g.item_end - 1) - static_cast<int>(blockIdx.x) + 1;
+    t.parts = 1;
+#pragma unroll 1
+    for (long long u = end; g.begins && u <= g.item_last; u += share) ++t.parts;  // (once a CTA at most)
     return t;
 }
 
@@ -152,7 +154,7 @@ struct Plan {
     static constexpr int out = raw + kRawStages * kRawBytes;
     static constexpr int bars = out + 4 * 32 * kOutBytes;
     static constexpr int misc = bars + 64 * 8;
-    static constexpr int tasks = misc + 32 + 2 * 16 * 8;
+    static constexpr int tasks = misc + 32 + 16 * 8;
     static constexpr int row_scale = tasks + (kTasks * static_cast<int>(sizeof(Task)) + 15) / 16 * 16;
     static constexpr int stream_ml = row_scale + (KV8 ? 2 * kBlock * 4 : 0);
     static constexpr int total = 1024 + stream_ml + 2 * 2 * kRowTile * 8;
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 4);
     int *start_seq = reinterpret_cast<int *>(smem + L::misc + 8);           // sequence, head, block
     long long *start_rest = reinterpret_cast<long long *>(smem + L::misc + 24);
-    long long *sums = reinterpret_cast<long long *>(smem + L::misc + 32);  // [2][NT / 32] of the warps
+    long long *sums = reinterpret_cast<long long *>(smem + L::misc + 32);  // [NT / 32] of the warps
 
     // (the warp's number from one lane, so that the compiler knows it to be the
     // same on all: the product warp's operands then live in uniform registers)
@@ -235,88 +237,86 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     dev::griddep_wait();  // q, the caches, tables and lengths are final
 
     // ---- the CTA's place in the line of units -----------------------------------
+    // (the units of all sequences are summed by all threads, and those of the stripe of
+    // sequences that has the CTA's first unit again; one warp finds the block)
     const auto spans = [&](int s) { return span_of(p, s, false); };
-    long long first = 0, all = 0;  // units of this thread's first sequence, and of all of them
-    for (int s = tid; s < p.num_seqs; s += NT) {
-        const long long u = p.shape.heads * head_units(p.shape, span_of(p, s, blockIdx.x == 0));
-        if (s == tid) first = u;
-        all += u;
-    }
-    auto warp_scan = [&](long long v) {
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, v, off);
-            if (lane >= off) v += o;
-        }
-        return v;
-    };
-    long long upto = warp_scan(first);
-    all = warp_scan(all);
-    if (lane == 31) {
-        sums[warp] = upto;
-        sums[NT / 32 + warp] = all;
-    }
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
-    // Everything before this grid is done: the fold may come to wait for its end.
-    dev::griddep_launch_dependents();
-    constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
-    long long W = 0;
-    for (int i = 0; i < NT / 32; ++i) W += sums[NT / 32 + i];
-    const int C = cta_count(W, gridDim.x);
     Walk walk = {};
-    if (static_cast<int>(blockIdx.x) < C) {
-        walk.u = cta_begin(W, C, blockIdx.x);
-        walk.end = cta_begin(W, C, blockIdx.x + 1);
-        long long before = 0;  // units of the sequences before this stripe
-        for (int s0 = 0;; s0 += NT) {
-            if (s0 > 0) {
-                __syncthreads();
-                first = s0 + tid < p.num_seqs ? p.shape.heads * head_units(p.shape, span_of(p, s0 + tid, false)) : 0;
-                upto = warp_scan(first);
-                if (lane == 31) sums[warp] = upto;
-                __syncthreads();
+    long long share = 0;
+    {
+        long long all = 0;     // units of this thread's sequences
+        long long before = 0;  // of the stripes before
+        const int stripes = (p.num_seqs + NT - 1) / NT;
+        bool found = false;
+        // the first round counts, the second looks for the place, which the first does
+        // where there is one stripe alone
+#pragma unroll 1
+        for (int i = 0; i < 2 * stripes && !found; ++i) {
+            const bool look = i >= stripes || stripes == 1;
+            const int s = (i < stripes ? i : i - stripes) * NT + tid;
+            const long long mine = s < p.num_seqs ? p.shape.heads * head_units(p.shape, span_of(p, s, blockIdx.x == 0 && i < stripes)) : 0;
+            all += mine;
+            if (!look && i + 1 < stripes) continue;
+            long long upto = look ? mine : all;  // with those of the threads before it in the warp
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += o;
             }
-            long long stripe = 0, mine = 0;
-            for (int i = 0; i < NT / 32; ++i) {
-                if (i == warp) mine = stripe;
-                stripe += sums[i];
+            if (lane == 31) sums[warp] = upto;
+            tc::fence_before();
+            __syncthreads();
+            tc::fence_after();
+            long long from = before + upto - mine, stripe = 0;
+#pragma unroll 1
+            for (int w = 0; w < NT / 32; ++w) {
+                if (w < warp) from += sums[w];
+                stripe += sums[w];
             }
-            mine += before + upto - first;
-            if (mine <= walk.u && walk.u < mine + first) {
-                start_seq[0] = s0 + tid;
-                *start_rest = walk.u - mine;
+            if (i == stripes - 1) {  // all units
+                share = cta_units(stripe, gridDim.x, p.inverse);
+                walk.u = blockIdx.x * share;
+                walk.end = min(stripe, walk.u + share);
+                if (walk.u >= walk.end) walk.u = walk.end = 0;
             }
-            before += stripe;
-            if (before > walk.u) break;  // (it is W in the end)
+            if (look) {
+                if (from <= walk.u && walk.u < from + mine) {
+                    start_seq[0] = s;
+                    *start_rest = walk.u - from;
+                }
+                before += stripe;
+                found = before > walk.u || walk.end == 0;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        walk.seq = start_seq[0];
-        walk.span = spans(walk.seq);
-        if (warp == 0) {
-            const long long of_head = head_units(p.shape, walk.span), rest = *start_rest;
-            const int head = static_cast<int>(rest / of_head);
-            const long long in_head = rest - head * of_head;
-            int lo = 0, n = blocks_of(p.shape, walk.span.n);
-            while (n > 1) {  // the last block that begins at or before the unit
+        // Everything before this grid is done: the fold may come to wait for its end.
+        dev::griddep_launch_dependents();
+        if (warp == 0 && walk.end > 0) {
+            walk.seq = start_seq[0];
+            walk.span = spans(walk.seq);
+            long long rest = *start_rest;
+            const long long of_head = head_units(p.shape, walk.span);
+#pragma unroll 1
+            for (; rest >= of_head; rest -= of_head) {
+                if (++walk.part == p.shape.head_parts) {
+                    walk.part = 0;
+                    ++walk.kvh;
+                }
+            }
+#pragma unroll 1
+            for (int n = blocks_of(p.shape, walk.span.n);;) {  // the last block that begins at or before the unit
                 const int step = (n + 31) / 32, i = lane * step;
-                const bool at = i < n && units_before(p.shape, walk.span, lo + i) <= in_head;
-                const int pick = (__popc(__ballot_sync(0xffffffffu, at)) - 1) * step;
-                lo += pick;
-                n = min(step, n - pick);
-            }
-            if (lane == 0) {
-                start_seq[1] = head;
-                start_seq[2] = lo;
-                *start_rest = in_head - units_before(p.shape, walk.span, lo);
+                const long long at = units_before(p.shape, walk.span, walk.block + min(i, n - 1));
+                const int pick = __popc(__ballot_sync(0xffffffffu, i < n && at <= rest)) - 1;
+                walk.block += pick * step;
+                n = min(step, n - pick * step);
+                if (n == 1) {
+                    walk.skip = rest - __shfl_sync(0xffffffffu, at, pick);
+                    break;
+                }
             }
         }
-        __syncthreads();
-        walk.head = start_seq[1];
-        walk.block = start_seq[2];
-        walk.skip = *start_rest;
     }
+    constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
     const int bs = static_cast<int>(p.block_size.d);
     const int IH = p.shape.item_heads;
     // Warp 0 walks the line and hands each segment to the other warps, a few ahead.
@@ -424,9 +424,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     }
                     uint8_t *tile = smem + L::ring + st * BYTES;
                     const int l0 = nl & ~(CT - 1), v1 = (nv + CT - 1) & ~(CT - 1);
+#pragma unroll 1
                     for (int b = 0; b < DPAD / 64; ++b) {
+#pragma unroll 1
                         for (int i = l0 * 8 + lane; i < nl * 8; i += 32)
                             *reinterpret_cast<uint4 *>(tile + b * (BN * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
                         for (int i = nv * 8 + lane; i < v1 * 8; i += 32)
                             *reinterpret_cast<uint4 *>(tile + b * (BN * 128) + i * 16) = make_uint4(0, 0, 0, 0);
                     }
@@ -436,10 +439,13 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 }
                 return next_stage();
             };
-            for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
-                if (i < sg.n) ok = load(false, i);
-                const int v = i - ahead + 1;
-                if (ok && v >= 0 && sg.n > 0) ok = load(true, v);
+            // (a step of two loads as two turns of the loop: the code of one)
+            const int n = sg.n;
+#pragma unroll 1
+            for (int i = 0; ok && i < 2 * (n + ahead - 1); ++i) {
+                const bool is_v = i & 1;
+                const int j = (i >> 1) - (is_v ? ahead - 1 : 0);
+                if (j >= 0 && j < n) ok = load(is_v, j);
             }
         };
         if (warp == 0) {
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 more = next_segment(p.shape, p.num_seqs, spans, walk, g);
                 Task t = {};
                 t.n = -1;
-                if (more) t = task_of(p, g, DPAD, W, C);
+                if (more) t = task_of(p, g, DPAD, walk.end, share);
                 if (!(ok = wait_bar(bar_tfree + 8 * task, task_ph ^ 1, gave_up))) break;
                 if (lane == 0) {
                     tasks[task] = t;
@@ -469,12 +475,14 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             }
         }
         // every release of a stage has arrived before this CTA ends
+#pragma unroll 1
         for (long long i = issued < DEPTH ? 0 : issued - DEPTH; ok && i < issued; ++i)
             ok = wait_bar(empty + 8 * static_cast<int>(i % DEPTH), static_cast<uint32_t>((i / DEPTH) & 1), gave_up);
         if (!ok && lane == 0) {
             // a wait ran out: let the copies in flight land before the CTA ends
             dev::flag_status(p.status, PD_DEV_WAIT_TIMEOUT);
             const long long last = issued < DEPTH ? issued : DEPTH;
+#pragma unroll 1
             for (long long i = issued - last; i < issued; ++i)
                 dev::mbar_wait_bounded(full + 8 * static_cast<int>(i % DEPTH), static_cast<uint32_t>((i / DEPTH) & 1),
                                        100000000ull);
@@ -562,6 +570,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     release(ks);
                     if (n == 1) queries_done();
                     if (!(ok = take(vs))) break;
+#pragma unroll 1
                     for (int j = 0; ok && j < n; ++j) {
                         const bool more = j + 1 < n;
                         const int v = vs;
@@ -589,6 +598,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         if (!(ok = take(ks))) break;
                         next_scores(1);
                     }
+#pragma unroll 1
                     for (int j = 0; ok && j < n; ++j) {
                         if (!(ok = take(vs))) break;
                         const bool next = j + 2 < n;
@@ -619,8 +629,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const int boxes = (sg.tokens + p.query_box - 1) / p.query_box, bytes = p.query_box * IH * 128;  // of 64 columns
             if (lane == 0) dev::mbar_arrive_expect_tx(bar_q, boxes * bytes * (DPAD / 64));
             __syncwarp();
+#pragma unroll 1
             for (int b = lane; b < boxes; b += 32) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < DPAD / 64; ++c)
                     tma_load_3d(base + L::q + c * (BR * 128) + b * bytes, &maps.q, bar_q, c * 64, sg.head, sg.token + b * p.query_box);
             }
@@ -660,13 +671,16 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         for (; ok && next_task(); task_done()) {
             const Task &sg = tasks[task];
             const int ahead = sg.two ? 1 : 2, low = sg.low, len = sg.len;
-            for (int i = 0; ok && i < sg.n + ahead - 1; ++i) {
-                if (i < sg.n) ok = convert(false, 0, BN);
-                const int v = i - ahead + 1, at = (sg.tile0 + v) * BN;
-                if (ok && v >= 0 && sg.n > 0) ok = convert(true, low - at, len - at);
+            const int n = sg.n;
+#pragma unroll 1
+            for (int i = 0; ok && i < 2 * (n + ahead - 1); ++i) {
+                const bool is_v = i & 1;
+                const int j = (i >> 1) - (is_v ? ahead - 1 : 0), at = (sg.tile0 + j) * BN;
+                if (j >= 0 && j < n) ok = convert(is_v, low - at, len - at);
             }
         }
         // every release of a stage has arrived before this CTA ends
+#pragma unroll 1
         for (long long i = handed < NST ? 0 : handed - NST; ok && i < handed; ++i)
             ok = wait_bar(bar_empty + 8 * static_cast<int>(i % NST), static_cast<uint32_t>((i / NST) & 1), gave_up);
     }
@@ -761,6 +775,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             float m = kNegInf, l = 0.f;
             bool begun = false, settled = false;  // a tile was seen; every row has its reference
             const int step = ONE || two ? 1 : 2;
+#pragma unroll 1
             for (int j = first_j; j < end_j; j += step) {
                 const int buf = ONE ? (j & 1) : t;
                 const uint32_t ts = tmem + lanes + buf * 128;
@@ -890,6 +905,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             cut = true;
         }
         task_done();
+#pragma unroll 1
         for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
             // (with at most 128 rows the streams' two partials of a row are folded)
             const int k1 = ONE || two ? t + 1 : 2;
@@ -950,8 +966,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         if (has1) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), g1, __uint_as_float(x[i])));
                 }
             };
-            // all rows' RB bytes, this thread's in y, to column c on
-            auto put = [&](const uint32_t *y, auto store) {
+            // all rows' RB bytes, this thread's in y, to `to` (this lane's 16 bytes of a row) on
+            auto put = [&](const uint32_t (&y)[16], uint8_t *to, int elem, bool in) {
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < RC; ++k)
@@ -965,7 +981,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < RC; ++i)
-                    if (dst[i] >= 0) store(dst[i], v[i]);
+                    if (dst[i] >= 0 && in) *reinterpret_cast<uint4 *>(to + dst[i] * elem) = v[i];
             };
             auto left = [&] {  // O has been read
                 tc::fence_before();
@@ -975,34 +991,21 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         if ((used >> k) & 1) arrive(bar_ofree + 8 * k);
                 }
             };
-            if (whole) {
-                constexpr int WC = RB / 2;  // columns
+            // 32 columns at a time: a row's RB bytes as BF16, twice that as FP32
+            static_assert(RB == 64, "32 columns of BF16, 16 of FP32");
 #pragma unroll 1
-                for (int c = 0; c < DPAD; c += WC) {
-                    uint32_t y[WC / 2];
-#pragma unroll
-                    for (int b = 0; b < WC; b += 32) {
-                        uint32_t x[32];
-                        fetch(c + b, x);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[b / 2 + i] = dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                    }
-                    if (c + WC >= DPAD) left();
-                    const int col = c + (lane % RC) * 8;
-                    put(y, [&](long long at, const uint4 &v) {
-                        if (col < D) *reinterpret_cast<uint4 *>(p.out + at + col) = v;
-                    });
-                }
-            } else {
-                constexpr int PC = RB / 4;
+            for (int c = 0; c < DPAD; c += 32) {
+                uint32_t x[32], y[16];
+                fetch(c, x);
+                if (c + 32 >= DPAD) left();
 #pragma unroll 1
-                for (int c = 0; c < DPAD; c += 32) {
-                    uint32_t x[32];
-                    fetch(c, x);
-                    if (c + 32 >= DPAD) left();
+                for (int h = 0; h < (whole ? 1 : 2); ++h) {
 #pragma unroll
-                    for (int b = 0; b < 32; b += PC)
-                        put(x + b, [&](long long at, const uint4 &v) { *reinterpret_cast<uint4 *>(p.part_o + at + c + b + (lane % RC) * 4) = v; });
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = whole ? dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])) : h ? x[16 + i] : x[i];
+                    const int col = c + (lane % RC) * (whole ? 8 : 4) + 16 * h;
+                    uint8_t *to = whole ? reinterpret_cast<uint8_t *>(p.out + col) : reinterpret_cast<uint8_t *>(p.part_o + col);
+                    put(y, to, whole ? 2 : 4, col < (whole ? D : DPAD));
                 }
             }
         }

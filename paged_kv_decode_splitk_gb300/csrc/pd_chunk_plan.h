@@ -5,11 +5,11 @@
 // head: up to block_rows query rows that meet the same keys, from the first that
 // any of them sees to the last.  Items lie in one line, by sequence, head and block;
 // an item has one unit for each key tile and kItemUnits in front of them for what
-// it costs besides.  CTA c of C takes units [W c / C, W (c + 1) / C), so every SM
-// gets the same work whatever the shapes; an item that a border cuts leaves
-// partials, which a second kernel folds, all others leave results.  Units before a
-// block are a sum of rounded-up quotients, which floor_sum gives without a walk
-// over the blocks.
+// it costs besides.  Every CTA takes the same number of units that follow one
+// another, so every SM gets the same work whatever the shapes; an item that a border
+// cuts leaves partials, which a second kernel folds, all others leave results.  Units
+// before a block are a sum of rounded-up quotients, which floor_sum gives without a
+// walk over the blocks.
 #pragma once
 
 #include <stdint.h>
@@ -38,9 +38,12 @@ struct Shape {
     int group;        // query heads of a KV head
     int item_heads;   // of them an item has (all, where they fit its rows)
     int head_parts;   // items that a token block's query heads make
+    int kv_heads;
     int heads;        // KV heads x head_parts
     int block_tokens; // new tokens of a block
-    int tile;         // keys of a tile
+    FastDiv fd_block; // block_tokens
+    int tile_log2;    // of the keys of a tile
+    int period_log2;  // blocks after which their ends lie alike in their tiles
     int window;       // keys a token sees at most, itself among them; 0: all
 };
 
@@ -49,10 +52,14 @@ inline Shape make_shape(int num_q_heads, int num_kv_heads, int dpad, int window)
     s.group = num_q_heads / num_kv_heads;
     s.head_parts = (s.group + block_rows(dpad) - 1) / block_rows(dpad);
     s.item_heads = (s.group + s.head_parts - 1) / s.head_parts;
+    s.kv_heads = num_kv_heads;
     s.heads = num_kv_heads * s.head_parts;
     s.block_tokens = block_rows(dpad) / s.item_heads;
     if (s.block_tokens > 1) s.block_tokens &= ~1;  // (even, so that boxes of several tokens divide it)
-    s.tile = tile_tokens(dpad);
+    s.fd_block = make_fastdiv(s.block_tokens);
+    s.tile_log2 = dpad > 128 ? 6 : 7;
+    s.period_log2 = s.tile_log2;
+    for (int t = s.block_tokens; s.period_log2 > 0 && t % 2 == 0; t /= 2) --s.period_log2;
     s.window = window;
     return s;
 }
@@ -71,32 +78,22 @@ struct Span {
     int first, n, past, len;
 };
 
-// sum over i < n of floor((a + i b) / m), by the steps of Euclid's algorithm: whole
-// multiples of m leave b and a, then the lattice points under the line are counted
-// along the other axis, where the line's slope is m / b.
-__host__ __device__ inline long long floor_sum(uint32_t n, uint32_t a, uint32_t b, uint32_t m) {
-    unsigned long long sum = 0;
-    while (n > 0) {
-        if (b >= m) {
-            sum += static_cast<unsigned long long>(n) * (n - 1) / 2 * (b / m);
-            b %= m;
-        }
-        if (a >= m) {
-            sum += static_cast<unsigned long long>(n) * (a / m);
-            a %= m;
-        }
-        const unsigned long long top = static_cast<unsigned long long>(b) * n + a;
-        if (top < m) break;
-        n = static_cast<uint32_t>(top / m);
-        a = static_cast<uint32_t>(top % m);
-        const uint32_t t = m;
-        m = b;
-        b = t;
+// sum over i < n of floor((a + i b) / 2^m), where b 2^p is a multiple of 2^m: after 2^p
+// terms the quotients come again, all larger by b 2^p / 2^m.
+__host__ __device__ inline long long floor_sum(uint32_t n, uint32_t a, uint32_t b, int m, int p) {
+    const uint32_t period = 1u << p, rest = n & (period - 1);
+    const long long whole = n >> p, step = (static_cast<long long>(b) << p) >> m;
+    long long all = 0, some = 0;  // of the first period's terms, and of its first `rest`
+#pragma unroll 1
+    for (uint32_t i = 0; i < (whole > 0 ? period : rest); ++i) {
+        const uint32_t v = (a + i * b) >> m;
+        all += v;
+        some += i < rest ? v : 0;
     }
-    return static_cast<long long>(sum);
+    return whole * all + step * (period * (whole * (whole - 1) / 2) + whole * rest) + some;
 }
 
-__host__ __device__ inline int blocks_of(const Shape &s, int n) { return (n + s.block_tokens - 1) / s.block_tokens; }
+__host__ __device__ inline int blocks_of(const Shape &s, int n) { return fast_div(n + s.block_tokens - 1, s.fd_block); }
 
 // Position that the first of a block's keys has, and one past its last.
 __host__ __device__ inline int first_key(const Shape &s, int position) {
@@ -108,10 +105,10 @@ __host__ __device__ inline int end_key(const Shape &s, const Span &q, int block)
     return end > 0 ? end : 0;
 }
 __host__ __device__ inline int first_tile(const Shape &s, const Span &q, int block) {
-    return first_key(s, q.past + block * s.block_tokens) / s.tile;
+    return first_key(s, q.past + block * s.block_tokens) >> s.tile_log2;
 }
 __host__ __device__ inline int tiles_of(const Shape &s, const Span &q, int block) {
-    const int end = (end_key(s, q, block) + s.tile - 1) / s.tile;
+    const int end = (end_key(s, q, block) + (1 << s.tile_log2) - 1) >> s.tile_log2;
     return end > 0 ? end - first_tile(s, q, block) : 0;
 }
 
@@ -120,17 +117,14 @@ __host__ __device__ inline long long units_before(const Shape &s, const Span &q,
     const int TB = s.block_tokens;
     long long u = static_cast<long long>(blocks) * kItemUnits;
     // ends: blocks from i0 on end past position 0
-    const int i0 = q.past >= 0 ? 0 : -q.past / TB;
+    const int i0 = q.past >= 0 ? 0 : fast_div(-q.past, s.fd_block);
     if (blocks > i0)
-        u += floor_sum(static_cast<uint32_t>(blocks - i0), static_cast<uint32_t>(q.past + (i0 + 1) * TB + s.tile - 1), static_cast<uint32_t>(TB),
-                       static_cast<uint32_t>(s.tile));
+        u += floor_sum(blocks - i0, q.past + (i0 + 1) * TB + (1 << s.tile_log2) - 1, TB, s.tile_log2, s.period_log2);
     if (s.window > 0) {
         // firsts: blocks from j0 on begin past key 0
         const long long before = static_cast<long long>(s.window) - 1 - q.past;
-        const long long j0 = before > 0 ? (before + TB - 1) / TB : 0;
-        if (blocks > j0)
-            u -= floor_sum(static_cast<uint32_t>(blocks - j0), static_cast<uint32_t>(q.past + j0 * TB + 1 - s.window), static_cast<uint32_t>(TB),
-                           static_cast<uint32_t>(s.tile));
+        const int j0 = before > 0 ? fast_div(static_cast<int>(before < 0x7ffffe00 ? before : 0x7ffffe00) + TB - 1, s.fd_block) : 0;
+        if (blocks > j0) u -= floor_sum(blocks - j0, q.past + j0 * TB + 1 - s.window, TB, s.tile_log2, s.period_log2);
     }
     return u;
 }
@@ -141,14 +135,18 @@ __host__ __device__ inline long long head_units(const Shape &s, const Span &q) {
     return (last > 0 ? units_before(s, q, last) : 0) + kItemUnits + tiles_of(s, q, last);
 }
 
-// CTAs that share W units, and the CTA that has unit u.
-__host__ __device__ inline int cta_count(long long W, int most) {
-    const long long c = (W + kCtaUnits - 1) / kCtaUnits;
-    return static_cast<int>(c < most ? c : most);
-}
-__host__ __device__ inline long long cta_begin(long long W, int C, int c) { return W / C * c + W % C * c / C; }
-__host__ __device__ inline int cta_of_unit(long long W, int C, long long u) {
-    return static_cast<int>(((u + 1) * C - 1) / W);  // the last c with W c / C < u + 1
+// Units of a CTA, but for the last one's, which may be fewer: those of `most` CTAs that
+// share W, and kCtaUnits at least.  (The quotient by a product: inverse is 2^64 / most
+// rounded up, so for W below 2^49 it is too large by less than 1 / most.)
+inline uint64_t inverse_of(int most) { return ~uint64_t{0} / static_cast<uint64_t>(most) + 1; }  // most > 1
+__host__ __device__ inline long long cta_units(long long W, int most, uint64_t inverse) {
+    const uint64_t up = static_cast<uint64_t>(W) + most - 1;
+#ifdef __CUDA_ARCH__
+    const long long share = most > 1 ? static_cast<long long>(__umul64hi(up, inverse)) : W;
+#else
+    const long long share = most > 1 ? static_cast<long long>(static_cast<unsigned __int128>(up) * inverse >> 64) : W;
+#endif
+    return share > kCtaUnits ? share : kCtaUnits;
 }
 
 // What a CTA does at a time: an item, or the part of its tiles that the CTA has.
@@ -160,32 +158,32 @@ struct Segment {
     int tile0, n;              // key tiles
     int of_item;               // tiles of the item
     int begins, whole;         // has the item's first tile; has all of them
-    long long item_end;        // unit after the item's last
+    long long item_last;       // unit, of the item
 };
 
 // A CTA's place in the line.
 struct Walk {
     long long u, end;  // the next unit, and the one after the CTA's last
-    int seq, head, block;
-    long long skip;    // units of the item before u
+    int seq, kvh, part, block;  // part: of the KV head's query heads
+    long long skip;             // units of the item before u
     Span span;
 };
 
 // The next segment (false: none is left).  spans(s) gives sequence s.
 template <class Spans>
 __host__ __device__ inline bool next_segment(const Shape &s, int num_seqs, const Spans &spans, Walk &w, Segment &g) {
+#pragma unroll 1
     while (w.u < w.end) {
         const int tiles = tiles_of(s, w.span, w.block), units = kItemUnits + tiles;
         const long long left = units - w.skip, mine = w.end - w.u < left ? w.end - w.u : left;
         const int from = w.skip > kItemUnits ? static_cast<int>(w.skip) - kItemUnits : 0;
         const int to = w.skip + mine > kItemUnits ? static_cast<int>(w.skip + mine) - kItemUnits : 0;
         const bool nothing = tiles == 0 && w.skip == 0;  // an item without keys: its rows are zeroed
-        const int part = w.head % s.head_parts;
         g.span = w.span;
         g.seq = w.seq;
-        g.kvh = w.head / s.head_parts;
-        g.head = g.kvh * s.group + part * s.item_heads;
-        g.heads = s.group - part * s.item_heads < s.item_heads ? s.group - part * s.item_heads : s.item_heads;
+        g.kvh = w.kvh;
+        g.head = g.kvh * s.group + w.part * s.item_heads;
+        g.heads = s.group - w.part * s.item_heads < s.item_heads ? s.group - w.part * s.item_heads : s.item_heads;
         g.token = w.span.first + w.block * s.block_tokens;
         g.tokens = w.span.n - w.block * s.block_tokens < s.block_tokens ? w.span.n - w.block * s.block_tokens : s.block_tokens;
         g.pos = w.span.past + w.block * s.block_tokens;
@@ -194,7 +192,7 @@ __host__ __device__ inline bool next_segment(const Shape &s, int num_seqs, const
         g.of_item = tiles;
         g.begins = from == 0;
         g.whole = g.n == tiles;
-        g.item_end = w.u + left;
+        g.item_last = w.u + left - 1;
         // on to the next item
         w.u += mine;
         w.skip = 0;
@@ -202,8 +200,12 @@ __host__ __device__ inline bool next_segment(const Shape &s, int num_seqs, const
             ++w.block;
         } else if (w.u < w.end) {
             w.block = 0;
-            if (++w.head == s.heads) {
-                w.head = 0;
+            if (++w.part == s.head_parts) {
+                w.part = 0;
+                ++w.kvh;
+            }
+            if (w.kvh == s.kv_heads) {
+                w.kvh = 0;
                 do {
                     if (++w.seq >= num_seqs) {
                         w.u = w.end;

@@ -38,7 +38,8 @@ def _check_walk(starts, lens, Hq, Hkv, D, window, ctas):
     restated, need = _restated(starts, lens, Hq, Hkv, D, window)
     G = Hq // Hkv
     assert tile == restated and block * item_heads <= (128 if D > 128 else 256) and block % box == 0 and box * item_heads <= max(32, item_heads)
-    assert C <= ctas and (C == ctas or units <= 5 * ctas)
+    share = max(5, -(-units // ctas))
+    assert C == -(-units // share) <= ctas
     items = {}
     for cta, seq, kvh, head, heads, row, rows, tile0, n, part, last in segs:
         assert head // G == kvh == (head + heads - 1) // G and heads <= item_heads and 0 < rows <= block and 0 <= cta <= last < C
@@ -70,9 +71,8 @@ def _check_walk(starts, lens, Hq, Hkv, D, window, ctas):
     for c in range(C):
         mine = [s for s in segs if s[0] == c]
         assert sum(s[9] == 0 for s in mine) <= 1 and sum(s[9] == 1 for s in mine) <= 1
-    if C > 1:  # the shares: tiles and two units an item
-        cost = [sum(s[8] for s in segs if s[0] == c) for c in range(C)]
-        assert max(cost) <= units // C + 1
+    cost = [sum(s[8] for s in segs if s[0] == c) for c in range(C)]  # tiles, beside two units an item
+    assert all(c <= share for c in cost)
 
 
 def test_walk_of_batches():
@@ -107,8 +107,8 @@ def test_walk_of_a_long_prompt():
     segs, (units, C, block, tile, _, _) = pd.pd_debug_chunk_walk([0, T], [T + 70000], 64, 8, 128)
     assert units == 8 * sum(2 + -(-(70000 + t + block) // tile) for t in range(0, T, block)) and C == 152
     assert sum(s[8] for s in segs) == units - 2 * 8 * T // block
-    shares = [sum(s[8] + 2 for s in segs if s[0] == c) for c in range(C)]
-    assert max(shares) - min(shares) <= 5
+    shares = [sum(s[8] + 2 * (s[9] > 0) for s in segs if s[0] == c) for c in range(C)]
+    assert max(shares) - min(shares[:-1]) <= 4 and shares[-1] <= max(shares)  # (two units of an item may be its neighbour's)
 
 
 def test_walk_refusals():

@@ -239,9 +239,10 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     // no more CTAs than the most units these sizes can make would be shared by
     const long long items = static_cast<long long>(num_seqs) + num_tokens / p.shape.block_tokens;
     const long long most = items * p.shape.heads * (kItemUnits + (p.max_tokens >> p.shape.tile_log2) + 1);
+    if (most > kMaxUnits) return report(PD_ERR_INVALID, "%s: launch too large (%d tokens, tables of %d)", what, num_tokens, p.max_tokens);
     const int sms = sm_count_of_device();
     const int ctas = static_cast<int>(std::min<long long>(std::max(1, std::min(sms, kMaxCtas)), (most + kCtaUnits - 1) / kCtaUnits));
-    p.inverse = inverse_of(std::max(ctas, 2));
+    p.ctas = make_fastdiv(ctas);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = kv8 ? dispatch<true>(dpad, &view.k, &view.v, &tq, p, ctas, st) : dispatch<false>(dpad, &view.k, &view.v, &tq, p, ctas, st);
     if (e != cudaSuccess) return report_cuda(e, "chunk attention launch");
@@ -317,21 +318,25 @@ int pd_debug_chunk_walk(int num_seqs, const int32_t *token_starts, const int32_t
         q.past = q.len - q.n;
         return q;
     };
-    long long W = 0;
+    // (bounded as the launch is, by each sequence's length)
+    long long most = 0;
+    for (int i = 0; i < num_seqs; ++i)
+        most += (1ll + spans(i).n / s.block_tokens) * s.heads * (kItemUnits + (context_lens[i] >> s.tile_log2) + 1);
+    if (most > kMaxUnits) return pd::report(PD_ERR_INVALID, "pd_debug_chunk_walk: too large");
+    int W = 0;
     for (int i = 0; i < num_seqs; ++i) W += s.heads * head_units(s, spans(i));
-    const long long share = cta_units(W, max_ctas, inverse_of(std::max(max_ctas, 2)));
-    const int C = static_cast<int>((W + share - 1) / share);
+    const int share = cta_units(W, pd::make_fastdiv(max_ctas)), C = (W + share - 1) / share;
     int n = 0;
     for (int c = 0; c < C; ++c) {
         Walk w = {};
         w.u = c * share;
         w.end = std::min(W, (c + 1) * share);
-        long long rest = w.u;
+        int rest = w.u;
         while (rest >= s.heads * head_units(s, spans(w.seq))) rest -= s.heads * head_units(s, spans(w.seq++));
         w.span = spans(w.seq);
-        const long long of_head = head_units(s, w.span);
-        w.kvh = static_cast<int>(rest / of_head) / s.head_parts;
-        w.part = static_cast<int>(rest / of_head) % s.head_parts;
+        const int of_head = head_units(s, w.span);
+        w.kvh = rest / of_head / s.head_parts;
+        w.part = rest / of_head % s.head_parts;
         rest %= of_head;
         for (int n = blocks_of(s, w.span.n); n > 1;) {  // (by halves where a warp takes 32nds)
             const int step = (n + 1) / 2;
@@ -344,7 +349,7 @@ int pd_debug_chunk_walk(int num_seqs, const int32_t *token_starts, const int32_t
         while (next_segment(s, num_seqs, spans, w, g)) {
             if (n == max_segments) return pd::report(PD_ERR_CAPACITY, "pd_debug_chunk_walk: more than %d segments", n);
             const int32_t v[11] = {c, g.seq, g.kvh, g.head, g.heads, g.token, g.tokens, g.tile0, g.n, g.begins ? (g.whole ? 2 : 1) : 0,
-                                   static_cast<int32_t>(g.item_last / share)};
+                                   g.item_last / share};
             std::copy(v, v + 11, segments + 11ll * n++);
         }
     }

@@ -56,12 +56,12 @@ struct ChunkMaps {
     CUtensorMap k, v, q;
 };
 
-// Scores of the columns below the first live one become -infinity.
+// Scores of the columns outside [first, end) become -infinity.
 template <int BN>
-__device__ __forceinline__ void mask_columns_below(uint32_t (&x)[BN], int first) {
+__device__ __forceinline__ void mask_outside(uint32_t (&x)[BN], int first, int end) {
 #pragma unroll
     for (int i = 0; i < BN; ++i)
-        if (i < first) x[i] = 0xff800000u;
+        if (i < first || i >= end) x[i] = 0xff800000u;
 }
 
 // Sequence s's new tokens; none where token_starts does not name rows of the batch.
@@ -110,7 +110,7 @@ constexpr int kTasks = 8;
 
 // With more than 128 rows each stream has 128 of them, and need not meet the tiles
 // that only the other's rows see.
-__device__ __forceinline__ Task task_of(const ChunkParams &p, const Segment &g, int dpad, long long end, long long share) {
+__device__ __forceinline__ Task task_of(const ChunkParams &p, const Segment &g, int dpad, int end, int share) {
     const Shape &s = p.shape;
     Task t;
     t.n = g.n;
@@ -132,7 +132,7 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, const Segment &g, 
     t.whole = g.whole;
     t.parts = 1;
 #pragma unroll 1
-    for (long long u = end; g.begins && u <= g.item_last; u += share) ++t.parts;  // (once a CTA at most)
+    for (int u = end; g.begins && u <= g.item_last; u += share) ++t.parts;  // (once a CTA at most)
     return t;
 }
 
@@ -154,7 +154,7 @@ struct Plan {
     static constexpr int out = raw + kRawStages * kRawBytes;
     static constexpr int bars = out + 4 * 32 * kOutBytes;
     static constexpr int misc = bars + 64 * 8;
-    static constexpr int tasks = misc + 32 + 16 * 8;
+    static constexpr int tasks = misc + 32 + 16 * 4;
     static constexpr int row_scale = tasks + (kTasks * static_cast<int>(sizeof(Task)) + 15) / 16 * 16;
     static constexpr int stream_ml = row_scale + (KV8 ? 2 * kBlock * 4 : 0);
     static constexpr int total = 1024 + stream_ml + 2 * 2 * kRowTile * 8;
@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 4);
     int *start_seq = reinterpret_cast<int *>(smem + L::misc + 8);           // sequence, head, block
-    long long *start_rest = reinterpret_cast<long long *>(smem + L::misc + 24);
-    long long *sums = reinterpret_cast<long long *>(smem + L::misc + 32);  // [NT / 32] of the warps
+    int *start_rest = reinterpret_cast<int *>(smem + L::misc + 24);
+    int *sums = reinterpret_cast<int *>(smem + L::misc + 32);               // [NT / 32] of the warps
 
     // (the warp's number from one lane, so that the compiler knows it to be the
     // same on all: the product warp's operands then live in uniform registers)
@@ -241,10 +241,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     // sequences that has the CTA's first unit again; one warp finds the block)
     const auto spans = [&](int s) { return span_of(p, s, false); };
     Walk walk = {};
-    long long share = 0;
+    int share = 0;
     {
-        long long all = 0;     // units of this thread's sequences
-        long long before = 0;  // of the stripes before
+        int all = 0;     // units of this thread's sequences
+        int before = 0;  // of the stripes before
         const int stripes = (p.num_seqs + NT - 1) / NT;
         bool found = false;
         // the first round counts, the second looks for the place, which the first does
@@ -253,27 +253,27 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         for (int i = 0; i < 2 * stripes && !found; ++i) {
             const bool look = i >= stripes || stripes == 1;
             const int s = (i < stripes ? i : i - stripes) * NT + tid;
-            const long long mine = s < p.num_seqs ? p.shape.heads * head_units(p.shape, span_of(p, s, blockIdx.x == 0 && i < stripes)) : 0;
+            const int mine = s < p.num_seqs ? p.shape.heads * head_units(p.shape, span_of(p, s, blockIdx.x == 0 && i < stripes)) : 0;
             all += mine;
             if (!look && i + 1 < stripes) continue;
-            long long upto = look ? mine : all;  // with those of the threads before it in the warp
+            int upto = look ? mine : all;  // with those of the threads before it in the warp
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, upto, off);
+                const int o = __shfl_up_sync(0xffffffffu, upto, off);
                 if (lane >= off) upto += o;
             }
             if (lane == 31) sums[warp] = upto;
             tc::fence_before();
             __syncthreads();
             tc::fence_after();
-            long long from = before + upto - mine, stripe = 0;
+            int from = before + upto - mine, stripe = 0;
 #pragma unroll 1
             for (int w = 0; w < NT / 32; ++w) {
                 if (w < warp) from += sums[w];
                 stripe += sums[w];
             }
             if (i == stripes - 1) {  // all units
-                share = cta_units(stripe, gridDim.x, p.inverse);
+                share = cta_units(stripe, p.ctas);
                 walk.u = blockIdx.x * share;
                 walk.end = min(stripe, walk.u + share);
                 if (walk.u >= walk.end) walk.u = walk.end = 0;
@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         if (warp == 0 && walk.end > 0) {
             walk.seq = start_seq[0];
             walk.span = spans(walk.seq);
-            long long rest = *start_rest;
-            const long long of_head = head_units(p.shape, walk.span);
+            int rest = *start_rest;
+            const int of_head = head_units(p.shape, walk.span);
 #pragma unroll 1
             for (; rest >= of_head; rest -= of_head) {
                 if (++walk.part == p.shape.head_parts) {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
 #pragma unroll 1
             for (int n = blocks_of(p.shape, walk.span.n);;) {  // the last block that begins at or before the unit
                 const int step = (n + 31) / 32, i = lane * step;
-                const long long at = units_before(p.shape, walk.span, walk.block + min(i, n - 1));
+                const int at = units_before(p.shape, walk.span, walk.block + min(i, n - 1));
                 const int pick = __popc(__ballot_sync(0xffffffffu, i < n && at <= rest)) - 1;
                 walk.block += pick * step;
                 n = min(step, n - pick * step);
@@ -448,30 +448,29 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (j >= 0 && j < n) ok = load(is_v, j);
             }
         };
-        if (warp == 0) {
-            Segment g;
-            for (bool more = true; ok && more;) {
-                more = next_segment(p.shape, p.num_seqs, spans, walk, g);
+        // (warp 0 makes the tasks as it goes)
+#pragma unroll 1
+        while (ok) {
+            const bool makes = warp == 0;
+            if (makes) {
+                Segment g;
                 Task t = {};
                 t.n = -1;
-                if (more) t = task_of(p, g, DPAD, walk.end, share);
+                if (next_segment(p.shape, p.num_seqs, spans, walk, g)) t = task_of(p, g, DPAD, walk.end, share);
                 if (!(ok = wait_bar(bar_tfree + 8 * task, task_ph ^ 1, gave_up))) break;
                 if (lane == 0) {
                     tasks[task] = t;
                     arrive(bar_task + 8 * task);
                 }
                 __syncwarp();
-                const Task &handed = tasks[task];
-                if (++task == kTasks) {
-                    task = 0;
-                    task_ph ^= 1;
-                }
-                if (more) load_all(handed);
             }
-        } else {
-            while (ok && next_task()) {
-                load_all(tasks[task]);
-                task_done();
+            if (!makes && !wait_bar(bar_task + 8 * task, task_ph, gave_up)) break;
+            if (tasks[task].n < 0) break;
+            load_all(tasks[task]);
+            if (!makes) arrive_warp(bar_tfree + 8 * task, lane);
+            if (++task == kTasks) {
+                task = 0;
+                task_ph ^= 1;
             }
         }
         // every release of a stage has arrived before this CTA ends
@@ -773,6 +772,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const int first_j = two ? (t ? sg.first1 : 0) : (ONE ? 0 : t), end_j = two && t == 0 ? sg.end0 : sg.n;
             const int end_all = __reduce_min_sync(0xffffffffu, end), low_all = __reduce_max_sync(0xffffffffu, low);  // of the warp's rows
             float m = kNegInf, l = 0.f;
+            const float lift = live ? kLift : -kNegInf;
             bool begun = false, settled = false;  // a tile was seen; every row has its reference
             const int step = ONE || two ? 1 : 2;
 #pragma unroll 1
@@ -798,68 +798,65 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     arrive_warp(bar_p + 8 * (PARTS * buf + h), lane);
                 };
                 bool waited = !ONE || !any;  // the last product onto O (that of the last item, too) is known to be done
-                int part = 0;                  // the first that is not handed on
-                if (settled && tile_at + BN <= end_all && tile_at >= low_all) {
-                    // every row sees the whole tile
+                // Tiles that hold a border of a row's keys, or are the first of a row: scores
+                // outside become -infinity in tensor memory, and rows take their reference.
+                const bool inside = tile_at + BN <= end_all && tile_at >= low_all;
+                if (!settled || !inside) {
+                    float mx = kNegInf;
 #pragma unroll 1
-                    for (int h = 0; h < PARTS; ++h) {
-                        uint32_t x[HB], pk[HB / 2];
-                        tc::ld_columns<HB>(ts + h * HB, x);
-                        const float sum = weigh<HB, KV8>(x, scale, m, pk);
-                        if (__any_sync(0xffffffffu, live && !(sum <= kLift))) break;
-                        l += sum;
-                        if (ONE) {
-                            ok = wait_bar(bar_o, oph & 1, gave_up);  // (each phase of the barrier is waited for, in order)
-                            oph ^= 1;
-                            waited = true;
+                    for (int c = 0; c < BN; c += 32) {
+                        uint32_t x[32];
+                        tc::ld_32x32(ts + c, x);
+                        tc::wait_ld(x);
+                        if (!inside) {
+                            mask_outside<32>(x, low - tile_at - c, end - tile_at - c);
+                            tc::st_32x32(ts + c, x);
                         }
-                        hand(pk, h);
-                        part = h + 1;
+                        mx = fmaxf(mx, largest_of<32>(x));
                     }
+                    tc::wait_st();
+                    if (live && m == kNegInf) m = mx * scale;
+                    settled = __all_sync(0xffffffffu, !live || m > kNegInf);
                 }
+                int part = 0;
+                for (float most = lift;;) {
 #pragma unroll 1
-                for (; part < PARTS; ++part) {
-                    const int at_part = tile_at + part * HB, nv = end - at_part, nl = low - at_part;
-                    uint32_t x[HB], pk[HB / 2];
-                    bool fresh = live && m == kNegInf, over = false;  // rows that take, or raise, their reference now
-                    float sum;
-                    for (int pass = 0;;) {
+                    for (; part < PARTS; ++part) {
+                        uint32_t x[HB], pk[HB / 2];
                         tc::ld_columns<HB>(ts + part * HB, x);
-                        if (nv < HB) mask_columns<HB>(x, nv);
-                        if (nl > 0) mask_columns_below<HB>(x, nl);
-                        if (pass == 1 || __any_sync(0xffffffffu, fresh)) {
-                            const float mx = largest_of<HB>(x) * scale;
-                            if (fresh) m = mx;
-                            if (pass == 1) {  // (the scores are read again behind this: no registers for them and O)
-                                raise_reference<DPAD>(to, mx, over, m, l);
-                                pass = 2;
-                                continue;
-                            }
-                        }
-                        sum = weigh<HB, KV8>(x, scale, m, pk);
-                        over = live && !(sum <= kLift);
-                        fresh = false;
-                        if (pass == 2 || !__any_sync(0xffffffffu, over)) break;
-                        // O is to be scaled: the products onto it have to be done, those of the
-                        // last tile (with two streams they are where this one's scores are)
-                        // and of the part before
-                        if (part > 0) {
-                            ok = wait_bar(bar_h + 8 * t, (hph >> t) & 1, gave_up) && ok;
-                        } else if (!waited) {
-                            ok = wait_bar(bar_o, oph & 1, gave_up) && ok;
+                        const float sum = weigh<HB, KV8>(x, scale, m, pk);
+                        if (__any_sync(0xffffffffu, sum > most)) break;
+                        most = lift;
+                        l += sum;
+                        if (ONE && !waited) {
+                            ok = wait_bar(bar_o, oph & 1, gave_up) && ok;  // (each phase of the barrier is waited for, in order)
                             oph ^= 1;
-                            waited = true;
                         }
-                        tc::fence_after();
-                        pass = 1;
+                        hand(pk, part);
                     }
-                    l += sum;
-                    if (ONE && !waited) {
+                    if (part == PARTS) break;
+                    // Rows raise their references: the products onto O have to be done, those of
+                    // the last tile (with two streams they are where this one's scores are) and
+                    // of the part before.  What their weights then sum to is taken as it is.
+                    if (part > 0) {
+                        ok = wait_bar(bar_h + 8 * t, (hph >> t) & 1, gave_up) && ok;
+                    } else if (!waited) {
                         ok = wait_bar(bar_o, oph & 1, gave_up) && ok;
                         oph ^= 1;
+                        waited = true;
                     }
-                    hand(pk, part);
-                    settled = __all_sync(0xffffffffu, !live || m > kNegInf);
+                    tc::fence_after();
+                    float mx = kNegInf, sum = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < HB; c += 32) {
+                        uint32_t x[32], pk[16];
+                        tc::ld_32x32(ts + part * HB + c, x);
+                        tc::wait_ld(x);
+                        mx = fmaxf(mx, largest_of<32>(x));
+                        sum += weigh<32, KV8>(x, scale, m, pk);
+                    }
+                    raise_reference<DPAD>(to, mx * scale, sum > lift, m, l);
+                    most = -kNegInf;
                 }
                 begun = any = true;
                 hph ^= 1u << t;

@@ -23,7 +23,7 @@ struct ChunkParams {
     float scale_log2;              // |scale| log2(e) (times k_scale), above 0
     int negative;                  // the scale is negative: q changes sign instead
     float v_scale;
-    uint64_t inverse;              // of the launch's CTAs (inverse_of)
+    FastDiv ctas;                  // of the launch
     int slot_rows;                 // rows of a slot: a block's at most, a multiple of 32
     CutItem *cut;                  // [CTAs]
     float *part_ml;                // [slot][slot_rows] (m, l); CTA c has slots 2 c (it begins inside

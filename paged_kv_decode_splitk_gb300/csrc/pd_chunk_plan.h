@@ -32,6 +32,8 @@ __host__ __device__ constexpr int block_rows(int dpad) { return dpad > 128 ? 128
 constexpr int kItemUnits = 2;
 // Units that are worth a CTA of their own.
 constexpr int kCtaUnits = 5;
+// Units of a launch are fewer (they and their sums are 32-bit numbers).
+constexpr long long kMaxUnits = 0x7fffffffll - 4096;
 
 // What all items of a launch share.
 struct Shape {
@@ -80,17 +82,16 @@ struct Span {
 
 // sum over i < n of floor((a + i b) / 2^m), where b 2^p is a multiple of 2^m: after 2^p
 // terms the quotients come again, all larger by b 2^p / 2^m.
-__host__ __device__ inline long long floor_sum(uint32_t n, uint32_t a, uint32_t b, int m, int p) {
-    const uint32_t period = 1u << p, rest = n & (period - 1);
-    const long long whole = n >> p, step = (static_cast<long long>(b) << p) >> m;
-    long long all = 0, some = 0;  // of the first period's terms, and of its first `rest`
+__host__ __device__ inline int floor_sum(uint32_t n, uint32_t a, uint32_t b, int m, int p) {
+    const uint32_t period = 1u << p, rest = n & (period - 1), whole = n >> p, step = (b << p) >> m;
+    uint32_t all = 0, some = 0;  // of the first period's terms, and of its first `rest`
 #pragma unroll 1
     for (uint32_t i = 0; i < (whole > 0 ? period : rest); ++i) {
         const uint32_t v = (a + i * b) >> m;
         all += v;
         some += i < rest ? v : 0;
     }
-    return whole * all + step * (period * (whole * (whole - 1) / 2) + whole * rest) + some;
+    return static_cast<int>(whole * all + step * (period * (whole * (whole - 1) / 2) + whole * rest) + some);
 }
 
 __host__ __device__ inline int blocks_of(const Shape &s, int n) { return fast_div(n + s.block_tokens - 1, s.fd_block); }
@@ -113,9 +114,9 @@ __host__ __device__ inline int tiles_of(const Shape &s, const Span &q, int block
 }
 
 // Units of the first `blocks` blocks of a head, all of them whole.
-__host__ __device__ inline long long units_before(const Shape &s, const Span &q, int blocks) {
+__host__ __device__ inline int units_before(const Shape &s, const Span &q, int blocks) {
     const int TB = s.block_tokens;
-    long long u = static_cast<long long>(blocks) * kItemUnits;
+    int u = blocks * kItemUnits;
     // ends: blocks from i0 on end past position 0
     const int i0 = q.past >= 0 ? 0 : fast_div(-q.past, s.fd_block);
     if (blocks > i0)
@@ -129,23 +130,16 @@ __host__ __device__ inline long long units_before(const Shape &s, const Span &q,
     return u;
 }
 // Units of a head in all.
-__host__ __device__ inline long long head_units(const Shape &s, const Span &q) {
+__host__ __device__ inline int head_units(const Shape &s, const Span &q) {
     if (q.n <= 0) return 0;
     const int last = blocks_of(s, q.n) - 1;
     return (last > 0 ? units_before(s, q, last) : 0) + kItemUnits + tiles_of(s, q, last);
 }
 
 // Units of a CTA, but for the last one's, which may be fewer: those of `most` CTAs that
-// share W, and kCtaUnits at least.  (The quotient by a product: inverse is 2^64 / most
-// rounded up, so for W below 2^49 it is too large by less than 1 / most.)
-inline uint64_t inverse_of(int most) { return ~uint64_t{0} / static_cast<uint64_t>(most) + 1; }  // most > 1
-__host__ __device__ inline long long cta_units(long long W, int most, uint64_t inverse) {
-    const uint64_t up = static_cast<uint64_t>(W) + most - 1;
-#ifdef __CUDA_ARCH__
-    const long long share = most > 1 ? static_cast<long long>(__umul64hi(up, inverse)) : W;
-#else
-    const long long share = most > 1 ? static_cast<long long>(static_cast<unsigned __int128>(up) * inverse >> 64) : W;
-#endif
+// share W, and kCtaUnits at least.
+__host__ __device__ inline int cta_units(int W, const FastDiv &most) {
+    const int share = fast_div(W + static_cast<int>(most.d) - 1, most);
     return share > kCtaUnits ? share : kCtaUnits;
 }
 
@@ -158,14 +152,14 @@ struct Segment {
     int tile0, n;              // key tiles
     int of_item;               // tiles of the item
     int begins, whole;         // has the item's first tile; has all of them
-    long long item_last;       // unit, of the item
+    int item_last;             // unit, of the item
 };
 
 // A CTA's place in the line.
 struct Walk {
-    long long u, end;  // the next unit, and the one after the CTA's last
+    int u, end;                 // the next unit, and the one after the CTA's last
     int seq, kvh, part, block;  // part: of the KV head's query heads
-    long long skip;             // units of the item before u
+    int skip;                   // units of the item before u
     Span span;
 };
 
@@ -175,9 +169,9 @@ __host__ __device__ inline bool next_segment(const Shape &s, int num_seqs, const
 #pragma unroll 1
     while (w.u < w.end) {
         const int tiles = tiles_of(s, w.span, w.block), units = kItemUnits + tiles;
-        const long long left = units - w.skip, mine = w.end - w.u < left ? w.end - w.u : left;
-        const int from = w.skip > kItemUnits ? static_cast<int>(w.skip) - kItemUnits : 0;
-        const int to = w.skip + mine > kItemUnits ? static_cast<int>(w.skip + mine) - kItemUnits : 0;
+        const int left = units - w.skip, mine = w.end - w.u < left ? w.end - w.u : left;
+        const int from = w.skip > kItemUnits ? w.skip - kItemUnits : 0;
+        const int to = w.skip + mine > kItemUnits ? w.skip + mine - kItemUnits : 0;
         const bool nothing = tiles == 0 && w.skip == 0;  // an item without keys: its rows are zeroed
         g.span = w.span;
         g.seq = w.seq;

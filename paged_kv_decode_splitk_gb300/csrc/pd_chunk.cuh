@@ -56,12 +56,12 @@ struct ChunkMaps {
     CUtensorMap k, v, q;
 };
 
-// Scores of the columns outside [first, end) become -infinity.
+// Scores of the columns below the first live one become -infinity.
 template <int BN>
-__device__ __forceinline__ void mask_outside(uint32_t (&x)[BN], int first, int end) {
+__device__ __forceinline__ void mask_columns_below(uint32_t (&x)[BN], int first) {
 #pragma unroll
     for (int i = 0; i < BN; ++i)
-        if (i < first || i >= end) x[i] = 0xff800000u;
+        if (i < first) x[i] = 0xff800000u;
 }
 
 // Sequence s's new tokens; none where token_starts does not name rows of the batch.
@@ -147,12 +147,11 @@ struct Plan {
     static constexpr int kStages = KV8 ? 3 : (DPAD == 64 ? 6 : 4);
     static constexpr int kRawBytes = KV8 ? kTile * DPAD : 0;
     static constexpr int kRawStages = KV8 ? 3 : 0;
-    static constexpr int kOutBytes = 64;  // of each of a warp's 32 rows on their way out
     static constexpr int q = 0;             // [DPAD / 64][kBlock rows][128 bytes]
     static constexpr int ring = q + kBlock * DPAD * 2;
     static constexpr int raw = ring + kStages * kStageBytes;
-    static constexpr int out = raw + kRawStages * kRawBytes;
-    static constexpr int bars = out + 4 * 32 * kOutBytes;
+    static constexpr int out = raw + kRawStages * kRawBytes;  // of four warps: 32 rows x 64 bytes on their way out
+    static constexpr int bars = out + (KV8 || kOne ? 4 * 2048 : 0);
     static constexpr int misc = bars + 64 * 8;
     static constexpr int tasks = misc + 32 + 16 * 4;
     static constexpr int row_scale = tasks + (kTasks * static_cast<int>(sizeof(Task)) + 15) / 16 * 16;
@@ -783,8 +782,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 sph ^= 1u << buf;
                 tc::fence_after();
                 if (KV8 && !begun) scale = row_scale[(two ? t * kRowTile : 0) + r];
-                // -- A row's reference m is the largest score of its first part of a tile with
-                // a key; after that no maximum is taken: weights may be as large as
+                // -- A row's reference m is the largest score of its first 32 columns with a
+                // key; after that no maximum is taken: weights may be as large as
                 // kLift, and only when a row's weights of a part sum to more does its warp
                 // look at the scores again and raise m (by a whole number, so that l and O
                 // are scaled exactly).  FP32 and BF16 hold such weights as exactly as
@@ -798,25 +797,27 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     arrive_warp(bar_p + 8 * (PARTS * buf + h), lane);
                 };
                 bool waited = !ONE || !any;  // the last product onto O (that of the last item, too) is known to be done
-                // Tiles that hold a border of a row's keys, or are the first of a row: scores
-                // outside become -infinity in tensor memory, and rows take their reference.
-                const bool inside = tile_at + BN <= end_all && tile_at >= low_all;
-                if (!settled || !inside) {
-                    float mx = kNegInf;
+                // What of a tile holds a border of some row's keys, 32 columns at a time: scores
+                // outside become -infinity in tensor memory.  And rows without one take their
+                // reference, from the first columns that they see any of.
+                if (!settled || tile_at + BN > end_all || tile_at < low_all) {
 #pragma unroll 1
                     for (int c = 0; c < BN; c += 32) {
+                        const bool over = tile_at + c + 32 > end_all, under = tile_at + c < low_all;
+                        if (settled && !over && !under) continue;
                         uint32_t x[32];
                         tc::ld_32x32(ts + c, x);
                         tc::wait_ld(x);
-                        if (!inside) {
-                            mask_outside<32>(x, low - tile_at - c, end - tile_at - c);
-                            tc::st_32x32(ts + c, x);
+                        if (over) mask_columns<32>(x, end - tile_at - c);
+                        if (under) mask_columns_below<32>(x, low - tile_at - c);
+                        if (over || under) tc::st_32x32(ts + c, x);
+                        if (!settled) {
+                            const float mx = largest_of<32>(x) * scale;
+                            if (live && m == kNegInf) m = mx;
+                            settled = __all_sync(0xffffffffu, !live || m > kNegInf);
                         }
-                        mx = fmaxf(mx, largest_of<32>(x));
                     }
                     tc::wait_st();
-                    if (live && m == kNegInf) m = mx * scale;
-                    settled = __all_sync(0xffffffffu, !live || m > kNegInf);
                 }
                 int part = 0;
                 for (float most = lift;;) {
@@ -855,7 +856,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         mx = fmaxf(mx, largest_of<32>(x));
                         sum += weigh<32, KV8>(x, scale, m, pk);
                     }
-                    raise_reference<DPAD>(to, mx * scale, sum > lift, m, l);
+                    if (begun || part > 0)
+                        raise_reference<DPAD>(to, mx * scale, sum > lift, m, l);
+                    else if (sum > lift)
+                        m = mx * scale;  // (no O yet: the last item's may still be on its way out)
                     most = -kNegInf;
                 }
                 begun = any = true;
@@ -881,12 +885,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int r = (warp & 3) * 32 + lane, D = p.head_dim;
-    // RB bytes of a row at a time go through this warp's staging area (16-byte chunk c of row
-    // r at c xor r, or r / 2 where a row has 4, so that neither side hits a bank twice), RC
-    // lanes a row: BF16 results, or FP32 partials.
-    constexpr int RB = L::kOutBytes, RC = RB / 16, RPI = 32 / RC;
-    uint8_t *stage = smem + L::out + (warp & 3) * (32 * RB);
-    const auto swizzle = [](int row) { return RC == 8 ? row & 7 : (row >> 1) & 3; };
+    uint4 *const stage = reinterpret_cast<uint4 *>(smem + L::out + (warp & 3) * 2048);
     const float2 *mls = reinterpret_cast<const float2 *>(smem + L::stream_ml);
     uint32_t mph = 0, dph = 0;  // phases of the streams' (m, l), a bit for each place, and O
     int turn = 0;               // the streams' places, a bit each
@@ -924,7 +923,6 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const float f0 = !has0 ? 0.f : has1 ? dev::exp2_approx(ml[0].x - M) : 1.f, f1 = !has1 ? 0.f : has0 ? dev::exp2_approx(ml[1].x - M) : 1.f;
             const float l = (has0 ? ml[0].y * f0 : 0.f) + (has1 ? ml[1].y * f1 : 0.f);
             const float f = !whole ? 1.f : l == 0.f ? 0.f : __fdiv_rn(p.v_scale, l);
-            const float g0 = f0 * f, g1 = f1 * f;
             // the row's sum: ln of it, or (m, l) of a partial
             const int br = t * kRowTile + r, tk = fast_div(br, p.fd_heads), part_rows = tokens * IH;
             if (whole) {
@@ -934,75 +932,100 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             } else if (br < part_rows) {
                 *reinterpret_cast<float2 *>(p.part_ml + (slot * p.slot_rows + br) * 2) = make_float2(M, l);
             }
-            // where the rows that this lane writes begin, in out or the partials (-1: none)
-            long long dst[RC];
-#pragma unroll
-            for (int i = 0; i < RC; ++i) {
-                const int row = t * kRowTile + (warp & 3) * 32 + i * RPI + lane / RC, k = fast_div(row, p.fd_heads), h = row - k * IH;
-                if (whole)
-                    dst[i] = k < tokens && h < heads ? (static_cast<long long>(token + k) * p.num_q_heads + head + h) * D : -1;
-                else
-                    dst[i] = row < part_rows ? (slot * p.slot_rows + row) * DPAD : -1;
-            }
-            // 32 columns of this thread's row, scaled
+            // 32 columns of this thread's row, scaled.  (A sum of 0 is one of no keys, whose O is 0.)
             const uint32_t from = tmem + lanes + 256 + t * DPAD;
             const bool any0 = (used >> t) & 1, any1 = k1 > t + 1 && (used >> 1) & 1;
-            auto fetch = [&](int c, uint32_t (&x)[32]) {
+            const uint64_t g0 = tc::pack_f32x2(f0 * f, f0 * f), g1 = tc::pack_f32x2(f1 * f, f1 * f);
+            auto fetch = [&](int c, uint64_t (&v)[16]) {
+                uint32_t x[32];
                 if (any0) {
                     tc::ld_32x32(from + c, x);
                     tc::wait_ld(x);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = 0;
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = has0 ? __float_as_uint(__uint_as_float(x[i]) * g0) : 0u;
+                for (int i = 0; i < 16; ++i) v[i] = tc::mul_f32x2(tc::pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), g0);
                 if (any1) {
-                    uint32_t y[32];
-                    tc::ld_32x32(from + DPAD + c, y);
-                    tc::wait_ld(y);
+                    tc::ld_32x32(from + DPAD + c, x);
+                    tc::wait_ld(x);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (has1) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), g1, __uint_as_float(x[i])));
+                    for (int i = 0; i < 16; ++i) v[i] = tc::fma_f32x2(tc::pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), g1, v[i]);
                 }
-            };
-            // all rows' RB bytes, this thread's in y, to `to` (this lane's 16 bytes of a row) on
-            auto put = [&](const uint32_t (&y)[16], uint8_t *to, int elem, bool in) {
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < RC; ++k)
-                    *reinterpret_cast<uint4 *>(stage + lane * RB + ((k ^ swizzle(lane)) << 4)) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                __syncwarp();
-                uint4 v[RC];
-#pragma unroll
-                for (int i = 0; i < RC; ++i) {
-                    const int row = i * RPI + lane / RC;
-                    v[i] = *reinterpret_cast<const uint4 *>(stage + row * RB + (((lane % RC) ^ swizzle(row)) << 4));
-                }
-#pragma unroll
-                for (int i = 0; i < RC; ++i)
-                    if (dst[i] >= 0 && in) *reinterpret_cast<uint4 *>(to + dst[i] * elem) = v[i];
-            };
-            auto left = [&] {  // O has been read
-                tc::fence_before();
+                if (c + 32 < DPAD) return;
+                tc::fence_before();  // O has been read
                 __syncwarp();
                 if (lane == 0) {
-                    for (int k = t; k < k1; ++k)
-                        if ((used >> k) & 1) arrive(bar_ofree + 8 * k);
+                    if (any0) arrive(bar_ofree + 8 * t);
+                    if (any1) arrive(bar_ofree + 8);
                 }
             };
-            // 32 columns at a time: a row's RB bytes as BF16, twice that as FP32
-            static_assert(RB == 64, "32 columns of BF16, 16 of FP32");
-#pragma unroll 1
-            for (int c = 0; c < DPAD; c += 32) {
-                uint32_t x[32], y[16];
-                fetch(c, x);
-                if (c + 32 >= DPAD) left();
-#pragma unroll 1
-                for (int h = 0; h < (whole ? 1 : 2); ++h) {
+            if (whole) {
+                const bool live = tk < tokens && br - tk * IH < heads;
+                if constexpr (KV8 || ONE) {
+                    // 64 bytes of a row at a time through this warp's staging area (16-byte chunk c
+                    // of row r at c xor r / 2 mod 4, so that neither side hits a bank twice), then
+                    // four lanes a row.  Half the time in the pipe that shared memory shares, and
+                    // twice the instructions, of what is below: FP8 chunks take 276 us so and 296
+                    // below, a prompt of wide heads 470 and 481, a prompt of 8192 tokens 363 and 358.
+                    const int rel = live ? (tk * p.num_q_heads + br - tk * IH) * (D / 8) : -1;  // in 16 bytes
+                    uint4 *o = reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(token) * p.num_q_heads + head) * D);
+                    int to[4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        y[i] = whole ? dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])) : h ? x[16 + i] : x[i];
-                    const int col = c + (lane % RC) * (whole ? 8 : 4) + 16 * h;
-                    uint8_t *to = whole ? reinterpret_cast<uint8_t *>(p.out + col) : reinterpret_cast<uint8_t *>(p.part_o + col);
-                    put(y, to, whole ? 2 : 4, col < (whole ? D : DPAD));
+                    for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, rel, i * 8 + lane / 4);
+#pragma unroll 1
+                    for (int c = 0; c < DPAD; c += 32) {
+                        uint64_t v[16];
+                        uint32_t y[16];
+                        fetch(c, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float a, b;
+                            tc::unpack_f32x2(v[i], a, b);
+                            y[i] = dev::pack_bf16x2(a, b);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            stage[lane * 4 + (k ^ ((lane >> 1) & 3))] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                        __syncwarp();
+                        const int col = c + lane % 4 * 8;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 z = stage[(i * 8 + lane / 4) * 4 + ((lane ^ (lane >> 3)) & 3)];
+                            if (to[i] >= 0 && col < D) o[to[i] + col / 8] = z;
+                        }
+                    }
+                } else {
+                    // Each thread its own row, 64 bytes at a time.
+                    __nv_bfloat16 *o = p.out + (static_cast<long long>(token + tk) * p.num_q_heads + head + (br - tk * IH)) * D;
+#pragma unroll 1
+                    for (int c = 0; c < DPAD; c += 32) {
+                        uint64_t v[16];
+                        uint32_t y[16];
+                        fetch(c, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float a, b;
+                            tc::unpack_f32x2(v[i], a, b);
+                            y[i] = dev::pack_bf16x2(a, b);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (live && c + k * 8 < D)
+                                *reinterpret_cast<uint4 *>(o + c + k * 8) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    }
+                }
+            } else {
+                float *o = p.part_o + (slot * p.slot_rows + br) * DPAD;
+#pragma unroll 1
+                for (int c = 0; c < DPAD; c += 32) {
+                    uint64_t v[16];
+                    fetch(c, v);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2)
+                        if (br < part_rows) *reinterpret_cast<ulonglong2 *>(o + c + k * 2) = make_ulonglong2(v[k], v[k + 1]);
                 }
             }
         }

@@ -936,8 +936,14 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const uint32_t from = tmem + lanes + 256 + t * DPAD;
             const bool any0 = (used >> t) & 1, any1 = k1 > t + 1 && (used >> 1) & 1;
             const uint64_t g0 = tc::pack_f32x2(f0 * f, f0 * f), g1 = tc::pack_f32x2(f1 * f, f1 * f);
-            auto fetch = [&](int c, uint64_t (&v)[16]) {
-                uint32_t x[32];
+            auto scaled = [](uint32_t &a, uint32_t &b, uint64_t f, uint64_t plus, bool add) {
+                const uint64_t x = tc::pack_f32x2(__uint_as_float(a), __uint_as_float(b));
+                float u, v;
+                tc::unpack_f32x2(add ? tc::fma_f32x2(x, f, plus) : tc::mul_f32x2(x, f), u, v);
+                a = __float_as_uint(u);
+                b = __float_as_uint(v);
+            };
+            auto fetch = [&](int c, uint32_t (&x)[32]) {
                 if (any0) {
                     tc::ld_32x32(from + c, x);
                     tc::wait_ld(x);
@@ -946,12 +952,19 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     for (int i = 0; i < 32; ++i) x[i] = 0;
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = tc::mul_f32x2(tc::pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), g0);
+                for (int i = 0; i < 32; i += 2) scaled(x[i], x[i + 1], g0, 0, false);
                 if (any1) {
-                    tc::ld_32x32(from + DPAD + c, x);
-                    tc::wait_ld(x);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = tc::fma_f32x2(tc::pack_f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), g1, v[i]);
+                    for (int h = 0; h < 32; h += 16) {
+                        uint32_t y[16];
+                        tc::ld_32x16(from + DPAD + c + h, y);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            scaled(y[i], y[i + 1], g1, tc::pack_f32x2(__uint_as_float(x[h + i]), __uint_as_float(x[h + i + 1])), true);
+                            x[h + i] = y[i];
+                            x[h + i + 1] = y[i + 1];
+                        }
+                    }
                 }
                 if (c + 32 < DPAD) return;
                 tc::fence_before();  // O has been read
@@ -976,15 +989,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, rel, i * 8 + lane / 4);
 #pragma unroll 1
                     for (int c = 0; c < DPAD; c += 32) {
-                        uint64_t v[16];
-                        uint32_t y[16];
-                        fetch(c, v);
+                        uint32_t x[32], y[16];
+                        fetch(c, x);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float a, b;
-                            tc::unpack_f32x2(v[i], a, b);
-                            y[i] = dev::pack_bf16x2(a, b);
-                        }
+                        for (int i = 0; i < 16; ++i) y[i] = dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
                         __syncwarp();
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -1002,15 +1010,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     __nv_bfloat16 *o = p.out + (static_cast<long long>(token + tk) * p.num_q_heads + head + (br - tk * IH)) * D;
 #pragma unroll 1
                     for (int c = 0; c < DPAD; c += 32) {
-                        uint64_t v[16];
-                        uint32_t y[16];
-                        fetch(c, v);
+                        uint32_t x[32], y[16];
+                        fetch(c, x);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float a, b;
-                            tc::unpack_f32x2(v[i], a, b);
-                            y[i] = dev::pack_bf16x2(a, b);
-                        }
+                        for (int i = 0; i < 16; ++i) y[i] = dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (live && c + k * 8 < D)
@@ -1021,11 +1024,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 float *o = p.part_o + (slot * p.slot_rows + br) * DPAD;
 #pragma unroll 1
                 for (int c = 0; c < DPAD; c += 32) {
-                    uint64_t v[16];
-                    fetch(c, v);
+                    uint32_t x[32];
+                    fetch(c, x);
 #pragma unroll
-                    for (int k = 0; k < 16; k += 2)
-                        if (br < part_rows) *reinterpret_cast<ulonglong2 *>(o + c + k * 2) = make_ulonglong2(v[k], v[k + 1]);
+                    for (int k = 0; k < 32; k += 4)
+                        if (br < part_rows) *reinterpret_cast<uint4 *>(o + c + k) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                 }
             }
         }

@@ -53,6 +53,17 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
                  :
                  : "memory");
 }
+// The same with 16 columns, loaded and waited for.
+__device__ __forceinline__ void ld_32x16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
 // No instruction: r's values were waited for (by another register's wait).
 __device__ __forceinline__ void hold(uint32_t (&r)[32]) {
     asm volatile(""

@@ -304,6 +304,11 @@ def norm_rope(rotation, x, weight, positions, eps: float = 1e-6, weight_offset: 
     if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)):
         if out is not None:
             raise ValueError("out: no gradient can pass through a tensor that is given; call under torch.no_grad() or let norm_rope make it")
+        if stream is None:
+            done = pd.quick().norm_rope_grad(pd._handle(rotation) or 0, 0 if rotation is None else rotation.head_dim, rotation, x, weight,
+                                             positions, eps, weight_offset)
+            if done is not NotImplemented:
+                return done
         return _NormRotation.apply(x, weight, rotation, positions, eps, weight_offset, stream)
     if stream is None:
         done = pd.quick().norm_rope(pd._handle(rotation) or 0, 0 if rotation is None else rotation.head_dim, x, weight, positions, out, eps,

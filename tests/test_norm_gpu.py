@@ -1,5 +1,8 @@
 """GPU tests of the head norms with the rotation, their gradients and their append, against the definitions in 64 bits."""
 
+import gc
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -171,9 +174,12 @@ def test_norm_strided_and_in_place(layout):
     assert torch.equal(g, dx)
 
 
-def test_norm_autograd():
+@pytest.mark.parametrize("quick", [True, False], ids=["module", "binding"])
+def test_norm_autograd(quick, monkeypatch):
     """Through a slice of a fused projection; gradients that come broadcast, transposed or at an odd place; of the weight
-    alone; and what cannot be had."""
+    alone; and what cannot be had.  (Through the CPython module's node, and through the ctypes binding.)"""
+    if not quick:
+        monkeypatch.setattr(pd, "_quick", pd._Declined())
     rope, freq, c = make(80, 40, "half", scaling="yarn", factor=8.0, original=2048)
     pos = i32(np.arange(11) * 911)
     row, w, g = randn(11, 5, 80, seed=5).requires_grad_(), weight(80, 0.0).requires_grad_(), randn(11, 3, 80, seed=6)
@@ -202,6 +208,27 @@ def test_norm_autograd():
     (back,) = torch.autograd.grad(y, x, h, create_graph=True)
     with pytest.raises(RuntimeError):  # no second gradient
         torch.autograd.grad(back.float().sum(), h)
+    y = api.norm_rope(rope, x, w, pos)
+    kept = weakref.ref(rope)
+    del rope  # (the gradient keeps the rotation)
+    gc.collect()
+    assert kept() is not None and torch.equal(torch.autograd.grad(y, x, g, retain_graph=True)[0], want[0])
+    pos.add_(1)
+    with pytest.raises(RuntimeError, match="modified"):  # the positions the gradient needs are gone
+        torch.autograd.grad(y, x, g)
+    del y
+    gc.collect()
+    assert kept() is None
+    y = api.norm_rope(None, x, w, None)
+    with torch.no_grad():
+        w.mul_(2)
+    with pytest.raises(RuntimeError, match="modified"):
+        torch.autograd.grad(y, x, g)
+    both = torch.randn(11, 3, 80, device=DEV, dtype=torch.bfloat16).requires_grad_()
+    y = api.norm_rope(None, both, None, None)
+    torch.autograd.grad(y, both, g)
+    with pytest.raises(RuntimeError):  # its tensors were given back
+        torch.autograd.grad(y, both, g)
 
 
 def test_norm_nothing_streams_and_graphs():

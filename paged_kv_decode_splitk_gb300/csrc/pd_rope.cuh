@@ -154,11 +154,10 @@ __device__ __forceinline__ void find_places(const Params &p, int first, int coun
     }
 }
 
-// (blocks: of a kernel that loops over them; 0: all at once)
 template <class Params, class Kernel>
-cudaError_t launch_rows(Kernel kern, const Params &p, cudaStream_t stream, int blocks = 0) {
+cudaError_t launch_rows(Kernel kern, const Params &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks > 0 ? blocks : (p.threads + kRopeThreads - 1) / kRopeThreads));
+    cfg.gridDim = dim3(static_cast<unsigned>((p.threads + kRopeThreads - 1) / kRopeThreads));
     cfg.blockDim = dim3(kRopeThreads);
     const int per = static_cast<int>(p.plan.units.d * p.plan.slots.d);
     cfg.dynamicSmemBytes = static_cast<size_t>(block_tokens(per)) * p.plan.pitch * 2 * sizeof(float);

@@ -103,6 +103,24 @@ def test_norm_rope_backward(T, H, D, rot, layout):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)  # the order of the sums is fixed
 
 
+# So many rows that blocks walk them: tokens whose turns pass the room for them (248 columns), one head (more tokens a block
+# than are held at a time), pairs anywhere, tokens that the blocks do not divide.
+@pytest.mark.parametrize("T,H,D,rot,layout", [(20011, 8, 256, 248, "half"), (160001, 1, 256, 20, "half"), (50003, 13, 64, 62, "half"),
+                                              (20011, 16, 128, 128, "half"), (9001, 40, 128, 64, "interleaved")])
+def test_norm_of_many_rows(T, H, D, rot, layout):
+    rope, freq, c = make(D, rot, layout)
+    x, w, g = randn(T, H, D, seed=T, scale=3.0), weight(D, 0.0), randn(T, H, D, seed=T + 1)
+    pos = np.random.default_rng(T).integers(0, 131072, T)
+    got = api.norm_rope(rope, x, w, i32(pos))
+    dx, dw = api.norm_rope_backward(rope, x, w, i32(pos), g)
+    torch.cuda.synchronize()
+    ref, size = value(f64(x), f64(w), 0.0, 1e-6, pos, freq, c, layout)
+    check(got, ref, bound(ref, size))
+    rx, bx, rw, bw = gradients(f64(x), f64(w), 0.0, 1e-6, pos, freq, c, layout, f64(g))
+    check(dx, rx, bx)
+    check(dw, rw, bw)
+
+
 def test_norm_gradient_by_differences():
     """<y(x + h e) - y(x - h e), g> / 2h in 64 bits: off by h^2 / 6 of the third derivative, here below 1e-7 of the sizes."""
     rope, freq, c = make(80, 40, "half")
@@ -318,6 +336,17 @@ def test_append_normed(case, rot, layout, fp8):
     assert got.data_ptr() == q_out.data_ptr()
     a.check(freq, c, layout, got, before)
     assert torch.all(got[:lead] == 9) and torch.all(got[a.T - tail:] == 9)  # rows of no sequence
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D,rot,layout", [(8, 4, 256, 248, "half"), (32, 4, 128, 128, "half"), (30, 3, 128, 64, "interleaved")])
+def test_append_normed_of_many_rows(Hq, Hkv, D, rot, layout, fp8):
+    rope, freq, c = make(D, rot, layout)
+    a = NormedAppend([6000, 1, 0, 4005], [0, 5, 9, 13], Hq, Hkv, D, 16, fp8, 3, 2, seed=D)
+    before = a.kc.clone(), a.vc.clone()
+    q_out = torch.full((a.T, Hq, D), 9.0, dtype=torch.bfloat16, device=DEV)
+    a.check(freq, c, layout, a.run(rope, q_out=q_out), before)
+    assert torch.all(q_out[:3] == 9) and torch.all(q_out[-2:] == 9)
 
 
 def test_append_normed_single_tokens_streams_and_bits():

@@ -87,7 +87,8 @@ extern "C" {
 #define PD_DEV_BAD_TILE_COUNT 4  /* a tile_block_counts entry < 0 or > tile_capacity: clamped */
 #define PD_DEV_WAIT_TIMEOUT 8    /* a bounded wait on a copy ran out: that output is garbage */
 #define PD_DEV_BAD_GROUPS 16     /* group_starts not non-decreasing within the batch: no prefix was read;
-                                  * pd_chunk_attn: token_starts, and that sequence was left out */
+                                  * pd_chunk_attn: token_starts, and that sequence was left out
+                                  * (all are where their rows overlap and make more work than the batch could) */
 
 /* Split-count policies (Module attn_splitk page, enum SplitkPolicy). */
 typedef enum { PD_POLICY_LEGACY = 0, PD_POLICY_AUTO = 1, PD_POLICY_PINNED = 2 } pd_policy;

@@ -243,6 +243,7 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     const int sms = sm_count_of_device();
     const int ctas = static_cast<int>(std::min<long long>(std::max(1, std::min(sms, kMaxCtas)), (most + kCtaUnits - 1) / kCtaUnits));
     p.ctas = make_fastdiv(ctas);
+    p.most_units = static_cast<int>(most);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = kv8 ? dispatch<true>(dpad, &view.k, &view.v, &tq, p, ctas, st) : dispatch<false>(dpad, &view.k, &view.v, &tq, p, ctas, st);
     if (e != cudaSuccess) return report_cuda(e, "chunk attention launch");

@@ -253,13 +253,13 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const bool look = i >= stripes || stripes == 1;
             const int s = (i < stripes ? i : i - stripes) * NT + tid;
             const int mine = s < p.num_seqs ? p.shape.heads * head_units(p.shape, span_of(p, s, blockIdx.x == 0 && i < stripes)) : 0;
-            all += mine;
+            all = add_units(all, mine);
             if (!look && i + 1 < stripes) continue;
             int upto = look ? mine : all;  // with those of the threads before it in the warp
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int o = __shfl_up_sync(0xffffffffu, upto, off);
-                if (lane >= off) upto += o;
+                if (lane >= off) upto = add_units(upto, o);
             }
             if (lane == 31) sums[warp] = upto;
             tc::fence_before();
@@ -268,14 +268,15 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             int from = before + upto - mine, stripe = 0;
 #pragma unroll 1
             for (int w = 0; w < NT / 32; ++w) {
-                if (w < warp) from += sums[w];
-                stripe += sums[w];
+                if (w < warp) from = add_units(from, sums[w]);
+                stripe = add_units(stripe, sums[w]);
             }
             if (i == stripes - 1) {  // all units
                 share = cta_units(stripe, p.ctas);
                 walk.u = blockIdx.x * share;
                 walk.end = min(stripe, walk.u + share);
-                if (walk.u >= walk.end) walk.u = walk.end = 0;
+                if (stripe > p.most_units && tid == 0 && blockIdx.x == 0) dev::flag_status(p.status, PD_DEV_BAD_GROUPS);
+                if (walk.u >= walk.end || stripe > p.most_units) walk.u = walk.end = 0;  // (too many: sequences overlap)
             }
             if (look) {
                 if (from <= walk.u && walk.u < from + mine) {
@@ -563,7 +564,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (!(ok = take(ks))) break;
                 if (!ONE && two) {
                     if (end0 > 0) scores(0, 0, ks);
-                    if (!(ok = queries(1))) break;
+                    ok = queries(1);
+                    if (!ok) break;
                     if (first1 == 0) scores(1, 1, ks);
                     release(ks);
                     if (n == 1) queries_done();

@@ -24,6 +24,7 @@ struct ChunkParams {
     int negative;                  // the scale is negative: q changes sign instead
     float v_scale;
     FastDiv ctas;                  // of the launch
+    int most_units;                // that sequences without a row in common can make
     int slot_rows;                 // rows of a slot: a block's at most, a multiple of 32
     CutItem *cut;                  // [CTAs]
     float *part_ml;                // [slot][slot_rows] (m, l); CTA c has slots 2 c (it begins inside

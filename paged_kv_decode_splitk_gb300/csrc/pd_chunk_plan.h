@@ -32,8 +32,15 @@ __host__ __device__ constexpr int block_rows(int dpad) { return dpad > 128 ? 128
 constexpr int kItemUnits = 2;
 // Units that are worth a CTA of their own.
 constexpr int kCtaUnits = 5;
-// Units of a launch are fewer (they and their sums are 32-bit numbers).
-constexpr long long kMaxUnits = 0x7fffffffll - 4096;
+// Units of a launch are no more (they and their sums are 32-bit numbers).
+constexpr int kMaxUnits = 0x3fffffff;
+
+// Units of two parts of the batch, or more than kMaxUnits where they are more.  (Sequences
+// whose rows overlap may pass any bound.)
+__host__ __device__ inline int add_units(int a, int b) {
+    const uint32_t sum = static_cast<uint32_t>(a) + static_cast<uint32_t>(b);
+    return static_cast<int>(sum < kMaxUnits + 1u ? sum : kMaxUnits + 1u);
+}
 
 // What all items of a launch share.
 struct Shape {

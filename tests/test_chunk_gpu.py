@@ -311,6 +311,19 @@ def test_chunk_flags():
     assert torch.equal(b.run(), good)
 
 
+def test_chunk_sequences_that_overlap():
+    """2000 sequences in turn of all 256000 rows and of -256000: more units than 32 bits hold.  Nothing is done."""
+    S, T, bs, width = 2001, 256000, 256, 4096
+    q = torch.zeros(T, 1, 64, dtype=torch.bfloat16, device=DEV)
+    kc = torch.zeros(1, bs, 1, 64, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(S, width, dtype=torch.int32, device=DEV)
+    out = torch.full_like(q, 5.0)
+    starts = i32([T * (s % 2) for s in range(S + 1)])
+    api.chunk_attn(q, kc, kc.clone(), table, i32([width * bs] * S), 0.1, token_starts=starts, out=out)
+    assert pd.pd_device_status() == pd.PD_DEV_BAD_GROUPS
+    assert torch.all(out == 5)
+
+
 def test_chunk_streams_graph_and_workspaces():
     a, b = (Chunks([300, 1, 30], [500, 900, 0], 8, 2, 128, seed=s) for s in (6, 7))
     want = a.run(), b.run()

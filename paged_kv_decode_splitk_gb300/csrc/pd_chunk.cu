@@ -1,6 +1,10 @@
 // pd_chunk.cu -- pd_chunk_attn[_fp8]: attention of new tokens over the paged cache
 // that holds them.  Host side, and the fold of the items that several CTAs had; the
 // pass itself is pd_chunk.cuh.
+//
+// The fold is a launch of its own behind the pass, one block for every CTA and few rows: a
+// cut item has as many partials as CTAs had a part, and most calls cut about one item a
+// CTA.  It is bound by latency (what it reads is below 1 MB for 64 single tokens of 32 heads).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -154,6 +158,27 @@ Layout layout_of(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim
     return l;
 }
 
+// Single tokens alone, without a window or their sums' logarithms, are what
+// pd_decode_attn computes, by units of a few heads and keys instead of a product's rows.
+// It takes them over FP8 (16 behind 1024 tokens 27.3 us here, 15.3 there; 64 behind 4096
+// 166 and 96; 200 behind 700 160 and 65), and over BF16 for at most four query heads a KV
+// head (32 over 8 of 128: 19.5 and 14, 169 and 155, 102 and 94; 16 over 16 of 64: 23 and
+// 20, 239 and 193, 138 and 101).  With more heads products have fuller rows: 32 over 2 of
+// 128, 256 behind 2048, 93 us here and 132 there, 64 behind 4096 54 and 60.
+bool tokens_alone(int group, bool kv8) { return kv8 ? group <= 16 : group <= 4; }
+
+// Its splits: as many as give every multiprocessor four of a sequence's KV heads, no more
+// than two for each multiprocessor and query head (as the Auto rule for one sequence: 1
+// behind 8192 tokens takes 15.4 us with 10 and 17.5 with 16, over FP8 behind 32768 21.4 and
+// 28.6), and no more than the workspace holds.
+int token_splits(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, size_t workspace_bytes) {
+    const long long units = static_cast<long long>(num_seqs) * num_kv_heads;
+    const int most = std::max(1, std::min(PD_SPLITK_TARGET_WAVES * kMaxCtas / num_q_heads, PD_MAX_DECODE_SPLITS));
+    int n = static_cast<int>(std::min<long long>(std::max<long long>(4 * kMaxCtas / units, 1), most));
+    while (n > 1 && pd_workspace_bytes(num_seqs, num_q_heads, head_dim, n) > workspace_bytes) n /= 2;
+    return n;
+}
+
 template <bool KV8>
 cudaError_t dispatch(int dpad, const CUtensorMap *tk, const CUtensorMap *tv, const CUtensorMap *tq, const ChunkParams &p, int ctas,
                      cudaStream_t st) {
@@ -181,6 +206,23 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     if (static_cast<long long>(max_blocks) * block_size > 0x7fffffffLL - 256)
         return report(PD_ERR_INVALID, "%s: max_blocks_per_seq * block_size overflows int32", what);
     if (num_tokens > 0x7fffffff - 256) return report(PD_ERR_INVALID, "%s: launch too large (%d tokens)", what, num_tokens);
+    const Layout lay = layout_of(num_tokens, num_q_heads, num_kv_heads, head_dim);
+    if (!workspace || workspace_bytes < lay.end)
+        return report(PD_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", what, lay.end,
+                      workspace ? workspace_bytes : static_cast<size_t>(0), workspace ? "" : " (null)");
+    if (!aligned16(workspace)) return report(PD_ERR_INVALID, "workspace must be 16-byte aligned");
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+
+    if (!token_starts && !lse && (window == 0 || window >= static_cast<long long>(max_blocks) * block_size) && inv_sqrt_d > 0 &&
+        q_tok == static_cast<int64_t>(num_q_heads) * head_dim && tokens_alone(num_q_heads / num_kv_heads, kv8)) {
+        const int splits = token_splits(num_seqs, num_q_heads, num_kv_heads, head_dim, workspace_bytes);
+        return kv8 ? pd_decode_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, max_blocks, context_lens, out, num_seqs,
+                                        num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, inv_sqrt_d, splits, workspace,
+                                        workspace_bytes, PD_GQA_PACK_OFF, stream)
+                   : pd_decode_attn(q, k_cache, v_cache, block_table, max_blocks, context_lens, out, num_seqs, num_q_heads, num_kv_heads,
+                                    head_dim, block_size, num_blocks, inv_sqrt_d, splits, workspace, workspace_bytes, PD_GQA_PACK_OFF,
+                                    stream);
+    }
     const int dpad = dpad_of(head_dim);
     KvView view;
     view.box_tokens = 16;  // as many as divide a block and a tile: fewer, larger boxes
@@ -189,12 +231,6 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     rc = launch_own_partials(q, k_cache, v_cache, block_table, max_blocks, context_lens, out, num_seqs, num_q_heads, num_kv_heads,
                              head_dim, block_size, num_blocks, inv_sqrt_d, 1, nullptr, nullptr, stream, kv8, k_scale, v_scale, &view);
     if (rc != PD_OK) return rc;
-    const Layout lay = layout_of(num_tokens, num_q_heads, num_kv_heads, head_dim);
-    if (!workspace || workspace_bytes < lay.end)
-        return report(PD_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", what, lay.end,
-                      workspace ? workspace_bytes : static_cast<size_t>(0), workspace ? "" : " (null)");
-    if (!aligned16(workspace)) return report(PD_ERR_INVALID, "workspace must be 16-byte aligned");
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
 
     int err = PD_OK;
     ChunkParams p = {};
@@ -339,11 +375,11 @@ int pd_debug_chunk_walk(int num_seqs, const int32_t *token_starts, const int32_t
         w.kvh = rest / of_head / s.head_parts;
         w.part = rest / of_head % s.head_parts;
         rest %= of_head;
-        for (int n = blocks_of(s, w.span.n); n > 1;) {  // (by halves where a warp takes 32nds)
-            const int step = (n + 1) / 2;
+        for (int of = blocks_of(s, w.span.n); of > 1;) {  // (by halves where a warp takes 32nds)
+            const int step = (of + 1) / 2;
             const bool up = units_before(s, w.span, w.block + step) <= rest;
             w.block += up ? step : 0;
-            n = up ? n - step : step;
+            of = up ? of - step : step;
         }
         w.skip = rest - units_before(s, w.span, w.block);
         Segment g;

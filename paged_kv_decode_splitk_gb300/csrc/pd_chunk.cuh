@@ -3,36 +3,51 @@
 // What it computes.  For a new token at position p and each query head,
 //   out = sum_j w_j V[j] / sum_j w_j,   w_j = 2^(x_j - m),   x_j = q.K[j] scale log2(e),
 // over the keys j it sees, max(0, p + 1 - window) to p, in one pass over them: the
-// reference m is the largest score of the row's first tile with a key, raised by
-// whole numbers when a tile's weights sum past 2^15, so that no later maximum is
-// needed and the sums are scaled exactly.
+// reference m is the largest score of the first 32 columns that hold a key of the row's,
+// raised by whole numbers when the weights of 64 keys sum past 2^15, so that no other
+// maximum is taken and the sums are scaled exactly.
 //
 // GB300 mapping.
 //   * An item is a block of new tokens with the query heads of a KV head, up to 256
 //     rows (128 at head dims above 128), and the key tiles that any of its rows sees.
 //     Items lie in one line of work units, of which every CTA (one an SM) takes the
 //     same share (pd_chunk_plan.h).  What a border cuts leaves partials of (m, l, o).
-//   * Warp 0 loads K tiles, warp 2 V tiles, by TMA boxes of 64 columns x as many
-//     tokens as lie together in a cache block, through the block table into a ring
-//     (128-byte swizzle); warp 3 an item's queries, whose rows are tokens by heads,
-//     as soon as the products of the last item's scores are done, so that a CTA goes
-//     from item to item without a pause of the tensor core longer than the first
-//     softmax.  One thread of warp 1 issues tcgen05.mma: S (128 rows x a tile) into
-//     TMEM, then O += P V with P read from TMEM.
+//   * Warp 0 walks the CTA's part of the line and hands each segment to the other warps,
+//     up to eight ahead; it loads K tiles, warp 2 V tiles, by TMA boxes of 64 columns x as
+//     many tokens as lie together in a cache block, through the block table into a ring
+//     (128-byte swizzle); warp 3 an item's queries, whose rows are tokens by heads, as soon
+//     as the products of the last item's scores are done.  One thread of warp 1 issues
+//     tcgen05.mma: S (128 rows x a tile) into TMEM, then O += P V with P read from TMEM,
+//     64 keys at a time, while the softmax is at the next 64.
 //   * Two groups of four warps do the softmax, a thread a row.  With more than 128
 //     rows each group has 128 of them and both meet every tile that their rows see;
 //     with fewer the groups take the tiles in turn, each with an O of its own, folded
-//     in the end.  At head dims above 128 one O fills TMEM: one group, two S.
-//   * Only tiles that hold a border of a row's keys are masked.  V rows past the
-//     sequence, or before every row's window, are zeroed, so that whatever the
-//     cache's slots hold there meets no product; boxes that lie there wholly are not
-//     read at all.
+//     on the way out.  At head dims above 128 one O fills TMEM: one group, two S.
+//   * Four warps take O out, to the results or the partials, while the softmax and the
+//     products are at the next item.
+//   * Only the 32 columns of a tile that hold a border of a row's keys are masked, in
+//     TMEM, in front of the one code that weighs: code is what an SM's instruction cache
+//     holds least of (171 KB of it, with a path for each kind of tile, took 370 us where
+//     86 KB take 345).  V rows past the sequence, or before every row's window, are zeroed,
+//     so that whatever the cache's slots hold there meets no product; boxes that lie there
+//     wholly are not read at all.
 //   * P is rounded to BF16 (half a step: 2^-8 of each weight), the form the tensor
 //     core multiplies with a BF16 V; l sums the unrounded weights in FP32, S, O, m and l
 //     are FP32.  An FP8 cache is converted to f16 tiles (exactly) by warps 2 and 3, q
 //     to f16 under a power of two for each row by the softmax warps, and P is f16
 //     there (2^-11; weights below 2^-13 of the row's largest are off by up to 2^-24
 //     of it).
+//
+// What bounds it.  Long prompts: the tensor core (a prompt of 8192 tokens, 32 heads of 128
+// over 8: 345 us, 1594 TFLOP/s, 84% of a library product's; eight query heads a KV head and
+// a chunk behind 32768 tokens 1650 to 1670).  A tile of 256 rows takes 2048 cycles of
+// products at D = 128, 1075 of softmax, 2048 of shared memory.  D = 64: the softmax (870
+// TFLOP/s).  D = 256: one O, so that scores wait for weights (1150).  FP8: shared memory,
+// 320 KB a tile (1140; four converting warps more take 5% longer).  Single tokens: HBM (a
+// step of 256 behind 4096 tokens 6660 GB/s), over FP8 three landing tiles a CTA (3200).  Small
+// calls: the way there, 3 us of it code that is not in the caches yet, and the fold.  Short
+// items: about 4000 cycles of way out a stream, which overlaps the next item's first
+// tiles alone (eight prompts of 1024 tokens 86 us).
 #pragma once
 
 #include <cuda.h>

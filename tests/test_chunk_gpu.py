@@ -218,6 +218,24 @@ def test_chunk_single_tokens_agree_with_decode():
     assert bool(((got.double() - whole.double()).abs() <= 2 * b.reference()[1]).all())
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("S,longest,Hq,Hkv,D", [(1, 500, 32, 8, 128), (1, 9000, 4, 1, 64), (5, 1500, 8, 2, 256), (16, 1024, 16, 16, 64),
+                                                (200, 700, 8, 8, 128), (30, 900, 16, 2, 128), (30, 900, 32, 2, 64), (300, 40, 6, 2, 80),
+                                                (9, 300, 34, 2, 128)])
+def test_chunk_single_tokens_alone(S, longest, Hq, Hkv, D, fp8):
+    """Without lse and window, contiguous and not: whichever kernel takes them."""
+    past = np.random.default_rng(S).integers(0, longest, S)
+    past[0] = longest - 1
+    a = Chunks([1] * S, past.tolist(), Hq, Hkv, D, fp8=fp8, single=True, seed=S)
+    a.check(a.run(), "contiguous")
+    b = Chunks([1] * S, past.tolist(), Hq, Hkv, D, fp8=fp8, single=True, seed=S, stride=1)
+    b.check(b.run(), "strided")
+    b.q = b.q.contiguous()
+    for scale in (-0.1, 0.0):
+        b.scale = scale
+        b.check(b.run(), "scale")
+
+
 def test_chunk_is_the_prompt_in_pieces():
     """A prompt at once, and in chunks of odd lengths over the same cache: the same tokens, so within both bounds."""
     b = Chunks([900], [0], 8, 2, 128, seed=4)

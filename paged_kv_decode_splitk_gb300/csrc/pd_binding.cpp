@@ -171,7 +171,7 @@ struct NormRotation : torch::autograd::Node {
     float eps = 0, offset = 0;
 
     ~NormRotation() override {
-        if (!rotation) return;
+        if (!rotation || !Py_IsInitialized()) return;  // (at the interpreter's end it may leak)
         const PyGILState_STATE state = PyGILState_Ensure();
         Py_DECREF(rotation);
         PyGILState_Release(state);

@@ -201,11 +201,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                    bar_rempty = bar_rfull + 24, bar_land = bar_rempty + 24, bar_s = bar_land + 8 * NST, bar_p = bar_s + 16,
                    bar_o = bar_p + 32, bar_h = bar_o + 8, bar_q = bar_h + 16, bar_qfree = bar_q + 16, bar_tail = bar_qfree + 8, bar_done = bar_tail + 8,
                    bar_ofree = bar_done + 16, bar_ml = bar_ofree + 16, bar_task = bar_ml + 32, bar_tfree = bar_task + 8 * kTasks;
-    static_assert(3 * NST + 6 + 13 + 8 + 2 * kTasks <= 64, "barrier region");
+    static_assert(3 * NST + 6 + 21 + 2 * kTasks <= 64, "barrier region");
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 4);
-    int *start_seq = reinterpret_cast<int *>(smem + L::misc + 8);           // sequence, head, block
-    int *start_rest = reinterpret_cast<int *>(smem + L::misc + 24);
+    int *start_seq = reinterpret_cast<int *>(smem + L::misc + 8);   // the CTA's first sequence, and its units
+    int *start_rest = reinterpret_cast<int *>(smem + L::misc + 12);  // before the CTA's first
     int *sums = reinterpret_cast<int *>(smem + L::misc + 32);               // [NT / 32] of the warps
 
     // (the warp's number from one lane, so that the compiler knows it to be the
@@ -213,35 +213,27 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     // ---- set-up that reads no global memory -----------------------------------
-    if (tid == 0) {
-        for (int i = 0; i < NST; ++i) {
-            dev::mbar_init(bar_full + 8 * i, KV8 ? kConverters / 32 : 1);
-            dev::mbar_init(bar_empty + 8 * i, 1);
-            dev::mbar_init(bar_land + 8 * i, 1);
-        }
-        for (int i = 0; i < 3; ++i) {
-            dev::mbar_init(bar_rfull + 8 * i, 1);
-            dev::mbar_init(bar_rempty + 8 * i, kConverters / 32);
-        }
-        for (int i = 0; i < 2; ++i) {
-            dev::mbar_init(bar_s + 8 * i, 1);
-            dev::mbar_init(bar_p + 16 * i, 4);
-            dev::mbar_init(bar_p + 16 * i + 8, 4);
-            dev::mbar_init(bar_h + 8 * i, 1);
-            dev::mbar_init(bar_done + 8 * i, 1);
-            dev::mbar_init(bar_ofree + 8 * i, 4);
-            dev::mbar_init(bar_ml + 8 * i, 4);
-            dev::mbar_init(bar_ml + 16 + 8 * i, 4);
-            dev::mbar_init(bar_q + 8 * i, KV8 ? 4 : 1);
-        }
-        dev::mbar_init(bar_qfree, 1);
-        dev::mbar_init(bar_tail, 1);
-        dev::mbar_init(bar_o, 1);
-        for (int i = 0; i < kTasks; ++i) {
-            dev::mbar_init(bar_task + 8 * i, 1);
-            dev::mbar_init(bar_tfree + 8 * i, 3 + (ONE ? 4 : 8) + 4);  // the warps that read it
-        }
+    if (warp == 0) {
+        // (arrivals of each barrier, in the order above; the first set has 32 of them at most)
+        constexpr int kReaders = 3 + (ONE ? 4 : 8) + 4;  // warps that read a task
+        auto count = [](int i) {
+            if (i < NST) return KV8 ? kConverters / 32 : 1;  // full
+            if (i < 2 * NST + 3) return 1;                   // empty, raw_full
+            if (i < 2 * NST + 6) return kConverters / 32;    // raw_empty
+            i -= 3 * NST + 6;
+            if (i < 2) return 1;    // landed, s
+            if (i < 6) return 4;    // p
+            if (i < 9) return 1;    // o, half
+            if (i < 11) return KV8 ? 4 : 1;  // q
+            if (i < 15) return 1;   // q_free, tail, done
+            if (i < 21) return 4;   // o_free, ml
+            return i < 21 + kTasks ? 1 : kReaders;  // task_full, task_free
+        };
+#pragma unroll
+        for (int i = lane; i < 3 * NST + 6 + 21 + 2 * kTasks; i += 32) dev::mbar_init(bars + 8 * i, count(i));
         dev::fence_mbar_init();
+    }
+    if (tid == 0) {
         *gave_up = 0;
         dev::prefetch_tensormap(&maps.k);
         dev::prefetch_tensormap(&maps.v);
@@ -280,12 +272,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             tc::fence_before();
             __syncthreads();
             tc::fence_after();
-            int from = before + upto - mine, stripe = 0;
-#pragma unroll 1
-            for (int w = 0; w < NT / 32; ++w) {
-                if (w < warp) from = add_units(from, sums[w]);
-                stripe = add_units(stripe, sums[w]);
-            }
+            // (the warps' sums added by one instruction, their upper bits to see whether that overflows)
+            const int of_warp = lane < NT / 32 ? sums[lane] : 0;
+            const bool over = __reduce_add_sync(0xffffffffu, of_warp >> 10) > kMaxUnits >> 10;
+            const int stripe = over ? kMaxUnits + 1 : __reduce_add_sync(0xffffffffu, of_warp);
+            const int from = before + upto - mine + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0);
             if (i == stripes - 1) {  // all units
                 share = cta_units(stripe, p.ctas);
                 walk.u = blockIdx.x * share;
@@ -295,7 +286,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             }
             if (look) {
                 if (from <= walk.u && walk.u < from + mine) {
-                    start_seq[0] = s;
+                    *start_seq = s;
                     *start_rest = walk.u - from;
                 }
                 before += stripe;
@@ -306,17 +297,14 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         // Everything before this grid is done: the fold may come to wait for its end.
         dev::griddep_launch_dependents();
         if (warp == 0 && walk.end > 0) {
-            walk.seq = start_seq[0];
+            walk.seq = *start_seq;
             walk.span = spans(walk.seq);
             int rest = *start_rest;
             const int of_head = head_units(p.shape, walk.span);
-#pragma unroll 1
-            for (; rest >= of_head; rest -= of_head) {
-                if (++walk.part == p.shape.head_parts) {
-                    walk.part = 0;
-                    ++walk.kvh;
-                }
-            }
+            const int head = rest / of_head;
+            rest -= head * of_head;
+            walk.kvh = head / p.shape.head_parts;
+            walk.part = head - walk.kvh * p.shape.head_parts;
 #pragma unroll 1
             for (int n = blocks_of(p.shape, walk.span.n);;) {  // the last block that begins at or before the unit
                 const int step = (n + 31) / 32, i = lane * step;

@@ -204,8 +204,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     static_assert(3 * NST + 6 + 21 + 2 * kTasks <= 64, "barrier region");
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 4);
-    int *start_seq = reinterpret_cast<int *>(smem + L::misc + 8);   // the CTA's first sequence, and its units
-    int *start_rest = reinterpret_cast<int *>(smem + L::misc + 12);  // before the CTA's first
+    int *start = reinterpret_cast<int *>(smem + L::misc + 8);  // the CTA's first sequence, its units before the CTA's first, a head's units
     int *sums = reinterpret_cast<int *>(smem + L::misc + 32);               // [NT / 32] of the warps
 
     // (the warp's number from one lane, so that the compiler knows it to be the
@@ -259,7 +258,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         for (int i = 0; i < 2 * stripes && !found; ++i) {
             const bool look = i >= stripes || stripes == 1;
             const int s = (i < stripes ? i : i - stripes) * NT + tid;
-            const int mine = s < p.num_seqs ? p.shape.heads * head_units(p.shape, span_of(p, s, blockIdx.x == 0 && i < stripes)) : 0;
+            const int of_head = s < p.num_seqs ? head_units(p.shape, span_of(p, s, blockIdx.x == 0 && i < stripes)) : 0;
+            const int mine = p.shape.heads * of_head;
             all = add_units(all, mine);
             if (!look && i + 1 < stripes) continue;
             int upto = look ? mine : all;  // with those of the threads before it in the warp
@@ -286,8 +286,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             }
             if (look) {
                 if (from <= walk.u && walk.u < from + mine) {
-                    *start_seq = s;
-                    *start_rest = walk.u - from;
+                    start[0] = s;
+                    start[1] = walk.u - from;
+                    start[2] = of_head;
                 }
                 before += stripe;
                 found = before > walk.u || walk.end == 0;
@@ -297,25 +298,29 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         // Everything before this grid is done: the fold may come to wait for its end.
         dev::griddep_launch_dependents();
         if (warp == 0 && walk.end > 0) {
-            walk.seq = *start_seq;
+            walk.seq = start[0];
             walk.span = spans(walk.seq);
-            int rest = *start_rest;
-            const int of_head = head_units(p.shape, walk.span);
-            const int head = rest / of_head;
-            rest -= head * of_head;
-            walk.kvh = head / p.shape.head_parts;
+            const int of_head = start[2];
+            int head = static_cast<int>(__fdividef(static_cast<float>(start[1]), static_cast<float>(of_head)));  // (or one beside it)
+            int rest = start[1] - head * of_head;
+            if (rest < 0) {
+                --head;
+                rest += of_head;
+            } else if (rest >= of_head) {
+                ++head;
+                rest -= of_head;
+            }
+            walk.kvh = p.shape.head_parts == 1 ? head : head / p.shape.head_parts;
             walk.part = head - walk.kvh * p.shape.head_parts;
+            walk.skip = rest;
 #pragma unroll 1
-            for (int n = blocks_of(p.shape, walk.span.n);;) {  // the last block that begins at or before the unit
+            for (int n = blocks_of(p.shape, walk.span.n); n > 1;) {  // the last block that begins at or before the unit
                 const int step = (n + 31) / 32, i = lane * step;
                 const int at = units_before(p.shape, walk.span, walk.block + min(i, n - 1));
                 const int pick = __popc(__ballot_sync(0xffffffffu, i < n && at <= rest)) - 1;
                 walk.block += pick * step;
                 n = min(step, n - pick * step);
-                if (n == 1) {
-                    walk.skip = rest - __shfl_sync(0xffffffffu, at, pick);
-                    break;
-                }
+                walk.skip = rest - __shfl_sync(0xffffffffu, at, pick);
             }
         }
     }

@@ -26,8 +26,8 @@ constexpr int kFoldThreads = 256;
 constexpr int kFoldBatch = 4;  // partials whose o are loaded together
 
 // Block (c, y) folds rows of the item that CTA c began and did not end: its part in
-// slot 2 c + 1, the others in slots 2 (c + i), i = 1, 2, ...  DPAD / 8 lanes a row, 8
-// columns each; with M the largest reference and w_i = 2^(m_i - M),
+// slot 2 c + 1, the others in slots 2 (c + i), i = 1, 2, ...  DPAD / 8 threads a row, 8
+// columns each, a warp 8 rows x 4 of them (128 bytes of a partial, 64 of a result); with M the largest reference and w_i = 2^(m_i - M),
 //   out = sum_i w_i o_i / sum_i w_i l_i,   lse = ln 2 (M + log2 sum_i w_i l_i).
 // Where rows are few, several lines of lanes share a row's partials.  Bound by
 // latency: the item, then m, l and o together.
@@ -44,9 +44,11 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const __grid_constan
     if (it.parts == 0 || rows <= 0) return;
     int of_row = 1;  // rows a block takes at once: a power of two
     while (of_row < rows) of_row *= 2;
-    const int ways = LINES / of_row, line = threadIdx.x / LPR, way = line / of_row;
-    const int row = blockIdx.y * LINES + line % of_row, d0 = threadIdx.x % LPR * 8;
-    const int k = fast_div(row, p.fd_heads), h = row - k * p.item_heads;
+    const int octet = threadIdx.x / 32 / (LPR / 4), quad = threadIdx.x / 32 % (LPR / 4);
+    const int line = octet * 8 + threadIdx.x % 8, chunk = quad * 4 + threadIdx.x / 8 % 4, me = line * LPR + chunk;
+    const int ways = LINES / of_row, way = line / of_row;
+    const int row = blockIdx.y * LINES + line % of_row, d0 = chunk * 8;
+    const int k = fast_div(row, p.fd_heads), h = row - k * p.item_heads, step = partial_rows(it.tokens * p.item_heads);
     const bool in = row < p.slot_rows && k < it.tokens && h < it.heads;
     float M = kNegInf, l = 0.f, acc[8] = {};
     for (int i0 = way; in && i0 < it.parts; i0 += ways * kFoldBatch) {
@@ -57,10 +59,11 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const __grid_constan
             const int i = i0 + j * ways;
             ml[j] = make_float2(kNegInf, 0.f);
             if (i < it.parts) {
-                const long long at = (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.slot_rows + row;
-                ml[j] = *reinterpret_cast<const float2 *>(p.part_ml + at * 2);
-                o[j][0] = *reinterpret_cast<const float4 *>(p.part_o + at * DPAD + d0);
-                o[j][1] = *reinterpret_cast<const float4 *>(p.part_o + at * DPAD + d0 + 4);
+                const long long slot = (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * p.slot_rows;
+                const float *of = p.part_o + slot * DPAD + (d0 * step + row * 4);
+                ml[j] = *reinterpret_cast<const float2 *>(p.part_ml + (slot + row) * 2);
+                o[j][0] = *reinterpret_cast<const float4 *>(of);
+                o[j][1] = *reinterpret_cast<const float4 *>(of + 4 * step);
             }
         }
         float top = M;  // (a partial without a key has l = 0)
@@ -83,9 +86,9 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const __grid_constan
         }
     }
     if (ways > 1) {  // the lines of a row, folded in order by its first
-        if (threadIdx.x % LPR == 0) fold_ml[line] = make_float2(M, l);
+        if (d0 == 0) fold_ml[line] = make_float2(M, l);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) fold[threadIdx.x][c] = acc[c];
+        for (int c = 0; c < 8; ++c) fold[me][c] = acc[c];
         __syncthreads();
         if (way > 0) return;
         float top = M;
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kFoldThreads) fold_kernel(const __grid_constan
             const float f = ml.x == kNegInf ? 0.f : dev::exp2_approx(ml.x - M);
             l = fmaf(ml.y, f, l);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) acc[c] = fmaf(fold[threadIdx.x + w * of_row * LPR][c], f, acc[c]);
+            for (int c = 0; c < 8; ++c) acc[c] = fmaf(fold[me + w * of_row * LPR][c], f, acc[c]);
         }
     }
     if (!in) return;

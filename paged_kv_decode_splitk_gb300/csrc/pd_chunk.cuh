@@ -1031,14 +1031,16 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     }
                 }
             } else {
-                float *o = p.part_o + (slot * p.slot_rows + br) * DPAD;
+                // (four columns of 32 rows side by side: whole lines of memory)
+                float *o = p.part_o + slot * p.slot_rows * DPAD + br * 4;
+                const int step = partial_rows(part_rows);
 #pragma unroll 1
                 for (int c = 0; c < DPAD; c += 32) {
                     uint32_t x[32];
                     fetch(c, x);
 #pragma unroll
                     for (int k = 0; k < 32; k += 4)
-                        if (br < part_rows) *reinterpret_cast<uint4 *>(o + c + k) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                        if (br < part_rows) *reinterpret_cast<uint4 *>(o + (c + k) * step) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                 }
             }
         }

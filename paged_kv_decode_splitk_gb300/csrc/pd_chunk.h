@@ -28,9 +28,12 @@ struct ChunkParams {
     int slot_rows;                 // rows of a slot: a block's at most, a multiple of 32
     CutItem *cut;                  // [CTAs]
     float *part_ml;                // [slot][slot_rows] (m, l); CTA c has slots 2 c (it begins inside
-    float *part_o;                 // [slot][slot_rows][dpad]  an item) and 2 c + 1 (it ends inside one)
+    float *part_o;                 // [slot][dpad / 4][item's rows][4]  an item) and 2 c + 1 (it ends inside one)
     unsigned int *status;
 };
+
+// Rows of an item's partials.
+__device__ __forceinline__ int partial_rows(int rows) { return (rows + 7) & ~7; }
 
 struct FoldParams {
     const CutItem *cut;

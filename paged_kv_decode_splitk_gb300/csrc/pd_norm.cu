@@ -10,9 +10,11 @@
 //
 // A row is held by D / 16 lanes (rounded up to 4, 8 or 16), two chunks of 8 columns
 // each, in 16-byte loads: chunks that pair up where pairs are whole chunks apart, so that
-// a rotation stays in the lane and needs a sine and a cosine for two columns, neighbouring
-// chunks otherwise.  The row's sums go across its lanes by shuffles.  Sines and cosines
-// are those of the block's tokens from a table in shared memory, as in pd_rope.cu, and
+// a rotation stays in the lane and needs a sine and a cosine for two columns; chunks half
+// a row apart where pairs are neighbours (32 bytes side by side for a lane took an append
+// of wide heads 131 us for 117); neighbouring chunks otherwise.  The row's sums go across
+// its lanes by shuffles.  Sines and cosines are those of the block's tokens from a table in
+// shared memory, as in pd_rope.cu, and
 // a lane walks several heads of its token with them.  All arithmetic is FP32; a result
 // is rounded once.  dw is summed in a fixed order: a lane's rows, the rows of a block, the
 // blocks.
@@ -21,9 +23,9 @@
 // blocks that fit the GPU share the tokens out evenly, and a line of lanes walks the rows of
 // its block with the loads of the next few rows in flight all the time.  16384 x 32 heads of
 // 128 columns forward 46.6 us (5760 GB/s, 85% of a copy's rate), backward 74 (81%), an append
-// of 32784 tokens with wide heads 132 (75%); a row a line with a block for each few of them
-// measured 46.6, 79.8 and 148, turns that are made for the rows in flight alone 50, 82 and
-// 148, three blocks a multiprocessor with half the loads 46.4, 87.7 and 146.
+// of 32784 tokens with wide heads 117 (85%); a row a line with a block for each few of them
+// measured 46.6, 79.8 and 148 (for 131 then), turns that are made for the rows in flight
+// alone 50, 82 and 148, three blocks a multiprocessor with half the loads 46.4, 87.7 and 146.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -137,7 +139,11 @@ struct Columns {
         u = threadIdx.x % LANES;
         ca = 16 * u;
         cb = ca + 8;
-        if (PAIRS == kHalves) {
+        if (PAIRS == kNeighbours) {  // (16 bytes of neighbouring lanes side by side)
+            const int first = (head_dim + 8) / 16 * 8;
+            ca = 8 * u < first ? 8 * u : head_dim;
+            cb = ca + first;
+        } else if (PAIRS == kHalves) {
             const int paired = p.half / 8;  // lanes with chunks that pair up; the others have copied ones
             ca = u < paired ? 8 * u : 2 * p.half + 16 * (u - paired);
             cb = u < paired ? p.half + 8 * u : ca + 8;
@@ -180,7 +186,7 @@ __device__ __forceinline__ void scale_row(float (&y)[16], const float (&w)[16], 
 template <int LANES, Pairs PAIRS>
 struct Turns {
     float c[PAIRS == kScattered ? 1 : 8], s[PAIRS == kScattered ? 1 : 8];
-    int live;           // pairs of the lane that turn
+    int live;           // pairs of the lane that turn (kNeighbours: of its chunks, 4 bits each)
     const float *cos;   // kScattered: the token's table
     int span, half;
 
@@ -190,13 +196,13 @@ struct Turns {
         half = p.half;
         live = 0;
         if constexpr (PAIRS == kScattered) return;
-        const int pair = PAIRS == kHalves ? at.ca : 8 * at.u;
-        live = PAIRS == kHalves ? (at.ca < half ? 8 : 0) : min(max(half - pair, 0), 8);
+        live = PAIRS == kHalves ? (at.ca < half ? 8 : 0) : min(max(half - at.ca / 2, 0), 4) + (min(max(half - at.cb / 2, 0), 4) << 4);
         if (live > 0) {  // (rows of the table are multiples of 4 pairs, and begin at one)
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
-                if (i < live) {
-                    const float4 x = *reinterpret_cast<const float4 *>(cos + pair + i), y = *reinterpret_cast<const float4 *>(cos + span + pair + i);
+                const int pair = PAIRS == kHalves ? at.ca + i : (i ? at.cb : at.ca) / 2;
+                if (pair < half) {
+                    const float4 x = *reinterpret_cast<const float4 *>(cos + pair), y = *reinterpret_cast<const float4 *>(cos + span + pair);
                     c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
                     s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
                 }
@@ -218,7 +224,7 @@ struct Turns {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float a = y[2 * i], b = y[2 * i + 1];
-                if (i < live) {
+                if (i < 4 ? i < (live & 15) : i - 4 < live >> 4) {
                     y[2 * i] = fmaf(a, c[i], -(b * s[i]));
                     y[2 * i + 1] = fmaf(b, c[i], a * s[i]);
                 }
@@ -426,8 +432,9 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_kernel(const __grid
 }
 
 // dw of 32 of the lanes' columns: 32 lines of threads sum the blocks' parts, every 32nd
-// each, and the lines are summed in order.  halves: pairs are whole chunks apart, that many
-// columns (0: a lane's chunks are neighbours).
+// each, and the lines are summed in order.  halves: the first so many columns lie in the
+// first chunks of as many lanes, as many more in their second ones (0: a lane's chunks are
+// neighbours).
 __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *part, int blocks, int pitch, int head_dim, int halves,
                                                                 __nv_bfloat16 *dw) {
     __shared__ float sums[32][33];
@@ -847,6 +854,8 @@ int pd_norm_rope_backward(const pd_rope *rope, const void *x, int64_t x_token_st
         if (e != cudaSuccess) return report_cuda(e, what);
     }
     if (grad_weight) {
+        const Pairs pairs = pairs_of(rope);
+        const int halves = pairs == kHalves ? rope->rot_dim / 2 : (pairs == kNeighbours ? (head_dim + 8) / 16 * 8 : 0);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(lanes * 16 / 32));
         cfg.blockDim = dim3(32, 32);
@@ -857,7 +866,7 @@ int pd_norm_rope_backward(const pd_rope *rope, const void *x, int64_t x_token_st
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_weight_grad_kernel, static_cast<const float *>(workspace), blocks, lanes * 16,
-                                                 head_dim, pairs_of(rope) == kHalves ? rope->rot_dim / 2 : 0, static_cast<__nv_bfloat16 *>(grad_weight));
+                                                 head_dim, halves, static_cast<__nv_bfloat16 *>(grad_weight));
         if (e != cudaSuccess) return report_cuda(e, what);
     }
     return report_ok();

@@ -165,8 +165,7 @@ struct Plan {
     static constexpr int q = 0;             // [DPAD / 64][kBlock rows][128 bytes]
     static constexpr int ring = q + kBlock * DPAD * 2;
     static constexpr int raw = ring + kStages * kStageBytes;
-    static constexpr int out = raw + kRawStages * kRawBytes;  // of four warps: 32 rows x 64 bytes on their way out
-    static constexpr int bars = out + (KV8 || kOne ? 4 * 2048 : 0);
+    static constexpr int bars = raw + kRawStages * kRawBytes;
     static constexpr int misc = bars + 64 * 8;
     static constexpr int tasks = misc + 32 + 16 * 4;
     static constexpr int row_scale = tasks + (kTasks * static_cast<int>(sizeof(Task)) + 15) / 16 * 16;
@@ -895,7 +894,6 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int r = (warp & 3) * 32 + lane, D = p.head_dim;
-    uint4 *const stage = reinterpret_cast<uint4 *>(smem + L::out + (warp & 3) * 2048);
     const float2 *mls = reinterpret_cast<const float2 *>(smem + L::stream_ml);
     uint32_t mph = 0, dph = 0;  // phases of the streams' (m, l), a bit for each place, and O
     int turn = 0;               // the streams' places, a bit each
@@ -986,48 +984,32 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             };
             if (whole) {
                 const bool live = tk < tokens && br - tk * IH < heads;
-                if constexpr (KV8 || ONE) {
-                    // 64 bytes of a row at a time through this warp's staging area (16-byte chunk c
-                    // of row r at c xor r / 2 mod 4, so that neither side hits a bank twice), then
-                    // four lanes a row.  Half the time in the pipe that shared memory shares, and
-                    // twice the instructions, of what is below: FP8 chunks take 276 us so and 296
-                    // below, a prompt of wide heads 470 and 481, a prompt of 8192 tokens 363 and 358.
-                    const int rel = live ? (tk * p.num_q_heads + br - tk * IH) * (D / 8) : -1;  // in 16 bytes
-                    uint4 *o = reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(token) * p.num_q_heads + head) * D);
-                    int to[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, rel, i * 8 + lane / 4);
+                // Two threads their two rows, 32 bytes of one at a time (a whole sector).  (Each its
+                // own row, 16 bytes at a time, takes eight prompts of 1024 tokens 82.3 us for 79.0;
+                // four threads, 64 bytes, 79.7; through shared memory FP8 chunks and wide heads
+                // take as long, the others longer.)
+                const bool odd = lane & 1;
+                const int own = live ? (tk * p.num_q_heads + br - tk * IH) * (D / 8) : -1, other = __shfl_xor_sync(0xffffffffu, own, 1);
+                const int at0 = odd ? other : own, at1 = odd ? own : other;
+                uint4 *o = reinterpret_cast<uint4 *>(p.out + (static_cast<long long>(token) * p.num_q_heads + head) * D);
 #pragma unroll 1
-                    for (int c = 0; c < DPAD; c += 32) {
-                        uint32_t x[32], y[16];
-                        fetch(c, x);
+                for (int c = 0; c < DPAD; c += 32) {
+                    uint32_t x[32], y[16];
+                    fetch(c, x);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                        __syncwarp();
+                    for (int i = 0; i < 16; ++i) y[i] = dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            stage[lane * 4 + (k ^ ((lane >> 1) & 3))] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                        __syncwarp();
-                        const int col = c + lane % 4 * 8;
+                    for (int k = 0; k < 4; k += 2) {
+                        uint32_t u[4], v[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint4 z = stage[(i * 8 + lane / 4) * 4 + ((lane ^ (lane >> 3)) & 3)];
-                            if (to[i] >= 0 && col < D) o[to[i] + col / 8] = z;
+                            const uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? y[4 * k + i] : y[4 * k + 4 + i], 1);
+                            u[i] = odd ? r : y[4 * k + i];
+                            v[i] = odd ? y[4 * k + 4 + i] : r;
                         }
-                    }
-                } else {
-                    // Each thread its own row, 64 bytes at a time.
-                    __nv_bfloat16 *o = p.out + (static_cast<long long>(token + tk) * p.num_q_heads + head + (br - tk * IH)) * D;
-#pragma unroll 1
-                    for (int c = 0; c < DPAD; c += 32) {
-                        uint32_t x[32], y[16];
-                        fetch(c, x);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = dev::pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (live && c + k * 8 < D)
-                                *reinterpret_cast<uint4 *>(o + c + k * 8) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                        const int col = c + (k + odd) * 8;
+                        if (at0 >= 0 && col < D) o[at0 + col / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (at1 >= 0 && col < D) o[at1 + col / 8] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
             } else {

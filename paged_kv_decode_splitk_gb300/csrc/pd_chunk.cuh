@@ -568,24 +568,19 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 if (n == 0) continue;
                 int ks = 0, vs = 0;
                 if (!(ok = queries(0))) break;
-                if (!(ok = take(ks))) break;
+                // (an item's first scores by the loop's own code: a copy of it is not in the
+                // instruction cache when its turn comes, 1500 cycles an item)
                 if (!ONE && two) {
-                    if (end0 > 0) scores(0, 0, ks);
-                    ok = queries(1);
-                    if (!ok) break;
-                    if (first1 == 0) scores(1, 1, ks);
-                    release(ks);
-                    if (n == 1) queries_done();
-                    if (!(ok = take(vs))) break;
 #pragma unroll 1
-                    for (int j = 0; ok && j < n; ++j) {
+                    for (int j = -1; ok && j < n; ++j) {
                         const bool more = j + 1 < n;
                         const int v = vs;
                         if (more && !(ok = take(ks))) break;
-                        if (j < end0 && !(ok = values(0, 0, v, j > 0, j + 1 == end0))) break;
+                        if (j >= 0 && j < end0 && !(ok = values(0, 0, v, j > 0, j + 1 == end0))) break;
                         if (more && j + 1 < end0) scores(0, 0, ks);
+                        if (KV8 && j < 0 && !(ok = queries(1))) break;
                         if (j >= first1 && !(ok = values(1, 1, v, j > first1, !more))) break;
-                        release(v);  // (before the scores: a commit waits for all that came before)
+                        if (j >= 0) release(v);  // (before the scores: a commit waits for all that came before)
                         if (more) {
                             if (j + 1 >= first1) scores(1, 1, ks);
                             release(ks);
@@ -594,26 +589,21 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         }
                     }
                 } else {
-                    // scores of tile j, whose keys are the next of the ring
-                    auto next_scores = [&](int j) {
-                        scores(j & 1, 0, ks);
-                        release(ks);
-                        if (j + 1 == n) queries_done();
-                    };
-                    next_scores(0);
-                    if (n > 1) {
-                        if (!(ok = take(ks))) break;
-                        next_scores(1);
-                    }
 #pragma unroll 1
-                    for (int j = 0; ok && j < n; ++j) {
-                        if (!(ok = take(vs))) break;
+                    for (int j = -2; ok && j < n; ++j) {
                         const bool next = j + 2 < n;
-                        if (next && !(ok = take(ks))) break;
                         const int t = j & 1;
-                        if (!(ok = values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), j + (ONE ? 1 : 2) >= n))) break;
-                        release(vs);
-                        if (next) next_scores(j + 2);
+                        if (j >= 0 && !(ok = take(vs))) break;
+                        if (next && !(ok = take(ks))) break;
+                        if (j >= 0) {
+                            if (!(ok = values(t, ONE ? 0 : t, vs, j > (ONE ? 0 : 1), j + (ONE ? 1 : 2) >= n))) break;
+                            release(vs);
+                        }
+                        if (next) {  // scores of tile j + 2, whose keys are the next of the ring
+                            scores(t, 0, ks);
+                            release(ks);
+                            if (j + 3 == n) queries_done();
+                        }
                     }
                 }
                 if (!ok) break;

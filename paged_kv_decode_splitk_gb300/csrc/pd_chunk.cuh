@@ -3,7 +3,7 @@
 // What it computes.  For a new token at position p and each query head,
 //   out = sum_j w_j V[j] / sum_j w_j,   w_j = 2^(x_j - m),   x_j = q.K[j] scale log2(e),
 // over the keys j it sees, max(0, p + 1 - window) to p, in one pass over them: the
-// reference m is the largest score of the first 32 columns that hold a key of the row's,
+// reference m is the largest score of the first 64 columns that hold a key of the row's,
 // raised by whole numbers when the weights of 64 keys sum past 2^15, so that no other
 // maximum is taken and the sums are scaled exactly.
 //
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 sph ^= 1u << buf;
                 tc::fence_after();
                 if (KV8 && !begun) scale = row_scale[(two ? t * kRowTile : 0) + r];
-                // -- A row's reference m is the largest score of its first 32 columns with a
+                // -- A row's reference m is the largest score of its first 64 columns with a
                 // key; after that no maximum is taken: weights may be as large as
                 // kLift, and only when a row's weights of a part sum to more does its warp
                 // look at the scores again and raise m (by a whole number, so that l and O
@@ -797,24 +797,18 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 };
                 bool waited = !ONE || !any;  // the last product onto O (that of the last item, too) is known to be done
                 // What of a tile holds a border of some row's keys, 32 columns at a time: scores
-                // outside become -infinity in tensor memory.  And rows without one take their
-                // reference, from the first columns that they see any of.
-                if (!settled || tile_at + BN > end_all || tile_at < low_all) {
+                // outside become -infinity in tensor memory.
+                if (tile_at + BN > end_all || tile_at < low_all) {
 #pragma unroll 1
                     for (int c = 0; c < BN; c += 32) {
                         const bool over = tile_at + c + 32 > end_all, under = tile_at + c < low_all;
-                        if (settled && !over && !under) continue;
+                        if (!over && !under) continue;
                         uint32_t x[32];
                         tc::ld_32x32(ts + c, x);
                         tc::wait_ld(x);
                         if (over) mask_columns<32>(x, end - tile_at - c);
                         if (under) mask_columns_below<32>(x, low - tile_at - c);
-                        if (over || under) tc::st_32x32(ts + c, x);
-                        if (!settled) {
-                            const float mx = largest_of<32>(x) * scale;
-                            if (live && m == kNegInf) m = mx;
-                            settled = __all_sync(0xffffffffu, !live || m > kNegInf);
-                        }
+                        tc::st_32x32(ts + c, x);
                     }
                     tc::wait_st();
                 }
@@ -824,6 +818,11 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     for (; part < PARTS; ++part) {
                         uint32_t x[HB], pk[HB / 2];
                         tc::ld_columns<HB>(ts + part * HB, x);
+                        if (!settled) {  // rows without a reference take it, where they see any of the columns
+                            const float mx = largest_of<HB>(x) * scale;
+                            if (live && m == kNegInf) m = mx;
+                            settled = __all_sync(0xffffffffu, !live || m > kNegInf);
+                        }
                         const float sum = weigh<HB, KV8>(x, scale, m, pk);
                         if (__any_sync(0xffffffffu, sum > most)) break;
                         most = lift;
@@ -855,10 +854,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                         mx = fmaxf(mx, largest_of<32>(x));
                         sum += weigh<32, KV8>(x, scale, m, pk);
                     }
-                    if (begun || part > 0)
-                        raise_reference<DPAD>(to, mx * scale, sum > lift, m, l);
-                    else if (sum > lift)
-                        m = mx * scale;  // (no O yet: the last item's may still be on its way out)
+                    // (a row's first 64 columns, with which there is no O yet, weigh 64 at most)
+                    if (begun || part > 0) raise_reference<DPAD>(to, mx * scale, sum > lift, m, l);
                     most = -kNegInf;
                 }
                 begun = any = true;

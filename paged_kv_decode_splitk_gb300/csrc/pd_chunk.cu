@@ -271,10 +271,8 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     p.part_ml = reinterpret_cast<float *>(ws + lay.part_ml);
     p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
     CUtensorMap tq = {};
-    if (!kv8) {
-        rc = encode_query_map(&tq, q, head_dim, num_q_heads, num_tokens, q_tok, p.shape.item_heads, p.query_box);
-        if (rc != PD_OK) return rc;
-    }
+    rc = encode_query_map(&tq, q, head_dim, num_q_heads, num_tokens, q_tok, p.shape.item_heads, p.query_box);
+    if (rc != PD_OK) return rc;
     // no more CTAs than the most units these sizes can make would be shared by
     const long long items = static_cast<long long>(num_seqs) + num_tokens / p.shape.block_tokens;
     const long long most = items * p.shape.heads * (kItemUnits + (p.max_tokens >> p.shape.tile_log2) + 1);

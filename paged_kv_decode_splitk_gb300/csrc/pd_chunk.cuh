@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         *gave_up = 0;
         dev::prefetch_tensormap(&maps.k);
         dev::prefetch_tensormap(&maps.v);
-        if (!KV8) dev::prefetch_tensormap(&maps.q);
+        dev::prefetch_tensormap(&maps.q);
     }
     if (warp == 1) tc::tmem_alloc_512(dev::smem_addr(tmem_s));
     dev::griddep_wait();  // q, the caches, tables and lengths are final
@@ -339,6 +339,18 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         if (++task == kTasks) {
             task = 0;
             task_ph ^= 1;
+        }
+    };
+    // An item's queries into shared memory, by `lanes` threads.
+    auto load_queries = [&](const Task &sg, uint32_t bar, int lane, int lanes) {
+        const int boxes = (sg.tokens + p.query_box - 1) / p.query_box, bytes = p.query_box * IH * 128;  // of 64 columns
+        if (lane == 0) dev::mbar_arrive_expect_tx(bar, boxes * bytes * (DPAD / 64));
+        if (lanes > 1) __syncwarp();
+#pragma unroll 1
+        for (int b = lane; b < boxes; b += lanes) {
+#pragma unroll 1
+            for (int c = 0; c < DPAD / 64; ++c)
+                tma_load_3d(base + L::q + c * (BR * 128) + b * bytes, &maps.q, bar, c * 64, sg.head, sg.token + b * p.query_box);
         }
     };
     // Registers: 512 threads were launched with 128 each, and 128 x 88 + 256 x 144 + 128 x
@@ -547,7 +559,9 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 return true;
             };
             auto release = [&](int stage) { tc::commit(bar_empty + 8 * stage); };
-            auto queries_done = [&] { tc::commit(bar_qfree); };
+            auto queries_done = [&] {
+                if (!KV8) tc::commit(bar_qfree);
+            };
             auto queries = [&](int t) {  // (from boxes of q all rows come at once)
                 if (!KV8 && t > 0) return true;
                 const bool got = wait_one(bar_q + 8 * t, (qph >> t) & 1, gave_up);
@@ -561,12 +575,17 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     task_ph ^= 1;
                 }
             };
+            int asked = 0;  // items whose queries this thread asked for
             for (;; task_given()) {
                 if (!(ok = wait_one(bar_task + 8 * task, task_ph, gave_up))) break;
                 const int n = tasks[task].n, two = tasks[task].two, end0 = tasks[task].end0, first1 = tasks[task].first1;
                 if (n < 0) break;
                 if (n == 0) continue;
                 int ks = 0, vs = 0;
+                if (KV8) {  // (what read the last item's is done: its weights have come)
+                    load_queries(tasks[task], bar_qfree, 0, 1);
+                    ++asked;
+                }
                 if (!(ok = queries(0))) break;
                 // (an item's first scores by the loop's own code: a copy of it is not in the
                 // instruction cache when its turn comes, 1500 cycles an item)
@@ -612,6 +631,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 // let the products in flight end before TMEM is freed
                 tc::commit(bar_tail);
                 dev::mbar_wait_bounded(bar_tail, 0, 100000000ull);
+                if (asked > 0) dev::mbar_wait_bounded(bar_qfree, (asked - 1) & 1, 100000000ull);
             }
         }
         __syncwarp();
@@ -623,15 +643,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const Task &sg = tasks[task];
             if (sg.n == 0) continue;
             if (!(ok = wait_bar(bar_qfree, ph ^ 1, gave_up))) break;
-            const int boxes = (sg.tokens + p.query_box - 1) / p.query_box, bytes = p.query_box * IH * 128;  // of 64 columns
-            if (lane == 0) dev::mbar_arrive_expect_tx(bar_q, boxes * bytes * (DPAD / 64));
-            __syncwarp();
-#pragma unroll 1
-            for (int b = lane; b < boxes; b += 32) {
-#pragma unroll 1
-                for (int c = 0; c < DPAD / 64; ++c)
-                    tma_load_3d(base + L::q + c * (BR * 128) + b * bytes, &maps.q, bar_q, c * 64, sg.head, sg.token + b * p.query_box);
-            }
+            load_queries(sg, bar_q, lane, 32);
             ph ^= 1;
             any = true;
         }
@@ -703,57 +715,40 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             float scale = p.scale_log2;
             if constexpr (KV8) {
                 row_scale = reinterpret_cast<float *>(smem + L::row_scale) + turn * BR;
-                // -- this stream's query rows into shared memory (128-byte swizzle); with
-                // at most 128 rows the streams share stream 0's.
+                // -- this stream's query rows, a thread each, become f16 under a power of two that
+                // brings the row's largest |q| into [2^14, 2^15), exactly but for values 2^-28
+                // below it; its inverse joins the row's softmax scale.  With at most 128 rows
+                // the streams share stream 0's.  (Rows from memory through registers, with the
+                // largest by shuffles, took 12000 cycles an item.)
                 if (sg.n > 0) {
-                    if (!(ok = wait_bar(bar_qfree, qph ^ 1, gave_up))) break;
+                    if (!(ok = wait_bar(bar_qfree, qph, gave_up))) break;
                     qph ^= 1;
                 }
                 if ((two || t == 0) && sg.n > 0) {
-                    // 32 rows x CHUNKS chunks over 32 lanes, sixteen loads in flight at once
-                    constexpr int BATCH = CHUNKS < 16 ? CHUNKS : 16;
-                    __syncwarp();
-#pragma unroll 1
-                    for (int i0 = 0; i0 < CHUNKS; i0 += BATCH) {
-                        uint4 v[BATCH];
-#pragma unroll
-                        for (int i = 0; i < BATCH; ++i) {
-                            const int e = (i0 + i) * 32 + lane;
-                            const int gr = t * kRowTile + (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;  // row of the block, chunk
-                            const int tk = fast_div(gr, p.fd_heads), h = gr - tk * IH;
-                            v[i] = make_uint4(0, 0, 0, 0);
-                            if (tk < sg.tokens && h < sg.heads && c * 8 < D)
-                                v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (sg.token + tk) * p.q_tok +
-                                                                             static_cast<long long>(sg.head + h) * D + c * 8));
-                        }
-#pragma unroll
-                        for (int i = 0; i < BATCH; ++i) {
-                            const int e = (i0 + i) * 32 + lane;
-                            const int row = t * kRowTile + (warp & 3) * 32 + e / CHUNKS, c = e % CHUNKS;
-                            if (p.negative) {
-                                v[i].x ^= 0x80008000u, v[i].y ^= 0x80008000u, v[i].z ^= 0x80008000u, v[i].w ^= 0x80008000u;
-                            }
-                            // f16 rows under a power of two that brings the row's largest
-                            // |q| into [2^14, 2^15), exactly but for values 2^-28 below it;
-                            // its inverse joins the row's softmax scale
-                            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                            float big = 0.f;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                big = fmaxf(big, fmaxf(fabsf(dev::bf16_lo_f32(w[k])), fabsf(dev::bf16_hi_f32(w[k]))));
-#pragma unroll
-                            for (int off = 1; off < CHUNKS; off <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-                            const int ex = (__float_as_int(big) >> 23) & 0xff;  // big < 2^(ex - 126)
-                            const int up = min(max(141 - ex, -126), 127);       // times 2^up: below 2^15
-                            const float f = __int_as_float((127 + up) << 23);
-                            const float down = up < 127 ? __int_as_float((127 - up) << 23) : 5.877471754111438e-39f;  // 2^-up
-                            if (c == 0) row_scale[row] = fmaxf(p.scale_log2 * down, FLT_MIN);
-                            v[i].x = dev::pack_f16x2(dev::bf16_lo_f32(w[0]) * f, dev::bf16_hi_f32(w[0]) * f);
-                            v[i].y = dev::pack_f16x2(dev::bf16_lo_f32(w[1]) * f, dev::bf16_hi_f32(w[1]) * f);
-                            v[i].z = dev::pack_f16x2(dev::bf16_lo_f32(w[2]) * f, dev::bf16_hi_f32(w[2]) * f);
-                            v[i].w = dev::pack_f16x2(dev::bf16_lo_f32(w[3]) * f, dev::bf16_hi_f32(w[3]) * f);
-                            *reinterpret_cast<uint4 *>(smem + L::q + (c / 8) * (BR * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[i];
-                        }
+                    const int row = t * kRowTile + r;
+                    auto chunk = [&](int c) {
+                        return reinterpret_cast<uint4 *>(smem + L::q + (c / 8) * (BR * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+                    };
+                    uint32_t big = 0;
+#pragma unroll 4
+                    for (int c = 0; c < CHUNKS; ++c) {
+                        const uint4 v = *chunk(c);
+                        big = __vmaxu2(__vmaxu2(big, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                    }
+                    const int ex = static_cast<int>(max(big & 0xffff, big >> 16) >> 7);  // |q| < 2^(ex - 126)
+                    const int up = min(max(141 - ex, -126), 127);                        // times 2^up: below 2^15
+                    const float f = __int_as_float((127 + up) << 23 | (p.negative ? 1u << 31 : 0u));
+                    const float down = up < 127 ? __int_as_float((127 - up) << 23) : 5.877471754111438e-39f;  // 2^-up
+                    row_scale[row] = fmaxf(p.scale_log2 * down, FLT_MIN);
+#pragma unroll 4
+                    for (int c = 0; c < CHUNKS; ++c) {
+                        uint4 v = *chunk(c);
+                        v.x = dev::pack_f16x2(dev::bf16_lo_f32(v.x) * f, dev::bf16_hi_f32(v.x) * f);
+                        v.y = dev::pack_f16x2(dev::bf16_lo_f32(v.y) * f, dev::bf16_hi_f32(v.y) * f);
+                        v.z = dev::pack_f16x2(dev::bf16_lo_f32(v.z) * f, dev::bf16_hi_f32(v.z) * f);
+                        v.w = dev::pack_f16x2(dev::bf16_lo_f32(v.w) * f, dev::bf16_hi_f32(v.w) * f);
+                        *chunk(c) = v;
                     }
                     tc::fence_async_shared();
                     arrive_warp(bar_q + 8 * t, lane);

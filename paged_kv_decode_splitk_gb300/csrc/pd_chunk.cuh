@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
     const uint32_t bar_full = bars, bar_empty = bar_full + 8 * NST, bar_rfull = bar_empty + 8 * NST,
                    bar_rempty = bar_rfull + 24, bar_land = bar_rempty + 24, bar_s = bar_land + 8 * NST, bar_p = bar_s + 16,
                    bar_o = bar_p + 32, bar_h = bar_o + 8, bar_q = bar_h + 16, bar_qfree = bar_q + 16, bar_tail = bar_qfree + 8, bar_done = bar_tail + 8,
-                   bar_ofree = bar_done + 16, bar_ml = bar_ofree + 16, bar_task = bar_ml + 32, bar_tfree = bar_task + 8 * kTasks;
+                   bar_ofree = bar_done + 16, bar_ml = bar_ofree + 16, bar_task = bar_ml + 32, bar_tfree = bar_task + 8 * kTasks,
+                   bar_qraw = bar_land;  // (FP8: no tile lands apart)
     static_assert(3 * NST + 6 + 21 + 2 * kTasks <= 64, "barrier region");
     volatile int *gave_up = reinterpret_cast<int *>(smem + L::misc);
     uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + L::misc + 4);
@@ -341,16 +342,15 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             task_ph ^= 1;
         }
     };
-    // An item's queries into shared memory, by `lanes` threads.
-    auto load_queries = [&](const Task &sg, uint32_t bar, int lane, int lanes) {
+    // An item's queries into shared memory, by a warp.
+    auto load_queries = [&](const Task &sg, uint32_t bar) {
         const int boxes = (sg.tokens + p.query_box - 1) / p.query_box, bytes = p.query_box * IH * 128;  // of 64 columns
         if (lane == 0) dev::mbar_arrive_expect_tx(bar, boxes * bytes * (DPAD / 64));
-        if (lanes > 1) __syncwarp();
+        __syncwarp();
 #pragma unroll 1
-        for (int b = lane; b < boxes; b += lanes) {
-#pragma unroll 1
-            for (int c = 0; c < DPAD / 64; ++c)
-                tma_load_3d(base + L::q + c * (BR * 128) + b * bytes, &maps.q, bar, c * 64, sg.head, sg.token + b * p.query_box);
+        for (int b = lane; b < boxes * (DPAD / 64); b += 32) {
+            const int c = b % (DPAD / 64), at = b / (DPAD / 64);
+            tma_load_3d(base + L::q + c * (BR * 128) + at * bytes, &maps.q, bar, c * 64, sg.head, sg.token + at * p.query_box);
         }
     };
     // Registers: 512 threads were launched with 128 each, and 128 x 88 + 256 x 144 + 128 x
@@ -559,9 +559,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 return true;
             };
             auto release = [&](int stage) { tc::commit(bar_empty + 8 * stage); };
-            auto queries_done = [&] {
-                if (!KV8) tc::commit(bar_qfree);
-            };
+            auto queries_done = [&] { tc::commit(bar_qfree); };
             auto queries = [&](int t) {  // (from boxes of q all rows come at once)
                 if (!KV8 && t > 0) return true;
                 const bool got = wait_one(bar_q + 8 * t, (qph >> t) & 1, gave_up);
@@ -575,17 +573,12 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     task_ph ^= 1;
                 }
             };
-            int asked = 0;  // items whose queries this thread asked for
             for (;; task_given()) {
                 if (!(ok = wait_one(bar_task + 8 * task, task_ph, gave_up))) break;
                 const int n = tasks[task].n, two = tasks[task].two, end0 = tasks[task].end0, first1 = tasks[task].first1;
                 if (n < 0) break;
                 if (n == 0) continue;
                 int ks = 0, vs = 0;
-                if (KV8) {  // (what read the last item's is done: its weights have come)
-                    load_queries(tasks[task], bar_qfree, 0, 1);
-                    ++asked;
-                }
                 if (!(ok = queries(0))) break;
                 // (an item's first scores by the loop's own code: a copy of it is not in the
                 // instruction cache when its turn comes, 1500 cycles an item)
@@ -631,7 +624,6 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 // let the products in flight end before TMEM is freed
                 tc::commit(bar_tail);
                 dev::mbar_wait_bounded(bar_tail, 0, 100000000ull);
-                if (asked > 0) dev::mbar_wait_bounded(bar_qfree, (asked - 1) & 1, 100000000ull);
             }
         }
         __syncwarp();
@@ -643,7 +635,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             const Task &sg = tasks[task];
             if (sg.n == 0) continue;
             if (!(ok = wait_bar(bar_qfree, ph ^ 1, gave_up))) break;
-            load_queries(sg, bar_q, lane, 32);
+            load_queries(sg, bar_q);
             ph ^= 1;
             any = true;
         }
@@ -721,7 +713,13 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                 // the streams share stream 0's.  (Rows from memory through registers, with the
                 // largest by shuffles, took 12000 cycles an item.)
                 if (sg.n > 0) {
-                    if (!(ok = wait_bar(bar_qfree, qph, gave_up))) break;
+                    if (warp == 4) {
+                        if (!(ok = wait_bar(bar_qfree, qph ^ 1, gave_up))) break;
+                        load_queries(sg, bar_qraw);
+                    }
+                    ok = wait_bar(bar_qraw, qph, gave_up);
+                    if (!ok && tid == 128) dev::mbar_wait_bounded(bar_qraw, qph, 100000000ull);  // (its copies land before the CTA ends)
+                    if (!ok) break;
                     qph ^= 1;
                 }
                 if ((two || t == 0) && sg.n > 0) {
@@ -729,19 +727,21 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
                     auto chunk = [&](int c) {
                         return reinterpret_cast<uint4 *>(smem + L::q + (c / 8) * (BR * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
                     };
-                    uint32_t big = 0;
-#pragma unroll 4
+                    __nv_bfloat162 big2 = __float2bfloat162_rn(0.f);
+#pragma unroll 8
                     for (int c = 0; c < CHUNKS; ++c) {
                         const uint4 v = *chunk(c);
-                        big = __vmaxu2(__vmaxu2(big, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
-                                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) big2 = __hmax2(big2, __habs2(reinterpret_cast<const __nv_bfloat162 &>(w[k])));
                     }
-                    const int ex = static_cast<int>(max(big & 0xffff, big >> 16) >> 7);  // |q| < 2^(ex - 126)
+                    const float big = fmaxf(__low2float(big2), __high2float(big2));
+                    const int ex = (__float_as_int(big) >> 23) & 0xff;                   // |q| < 2^(ex - 126)
                     const int up = min(max(141 - ex, -126), 127);                        // times 2^up: below 2^15
                     const float f = __int_as_float((127 + up) << 23 | (p.negative ? 1u << 31 : 0u));
                     const float down = up < 127 ? __int_as_float((127 - up) << 23) : 5.877471754111438e-39f;  // 2^-up
                     row_scale[row] = fmaxf(p.scale_log2 * down, FLT_MIN);
-#pragma unroll 4
+#pragma unroll 8
                     for (int c = 0; c < CHUNKS; ++c) {
                         uint4 v = *chunk(c);
                         v.x = dev::pack_f16x2(dev::bf16_lo_f32(v.x) * f, dev::bf16_hi_f32(v.x) * f);

@@ -15,8 +15,8 @@
 //   * Warp 0 walks the CTA's part of the line and hands each segment to the other warps,
 //     up to eight ahead; it loads K tiles, warp 2 V tiles, by TMA boxes of 64 columns x as
 //     many tokens as lie together in a cache block, through the block table into a ring
-//     (128-byte swizzle); warp 3 an item's queries, whose rows are tokens by heads, as soon
-//     as the products of the last item's scores are done.  One thread of warp 1 issues
+//     (128-byte swizzle); warp 3 (over FP8 the first of the softmax) an item's queries,
+//     whose rows are tokens by heads, as soon as the last item's scores are done.  One thread of warp 1 issues
 //     tcgen05.mma: S (128 rows x a tile) into TMEM, then O += P V with P read from TMEM,
 //     64 keys at a time, while the softmax is at the next 64.
 //   * Two groups of four warps do the softmax, a thread a row.  With more than 128
@@ -26,11 +26,11 @@
 //   * Four warps take O out, to the results or the partials, while the softmax and the
 //     products are at the next item.
 //   * Only the 32 columns of a tile that hold a border of a row's keys are masked, in
-//     TMEM, in front of the one code that weighs: code is what an SM's instruction cache
-//     holds least of (171 KB of it, with a path for each kind of tile, took 370 us where
-//     86 KB take 345).  V rows past the sequence, or before every row's window, are zeroed,
-//     so that whatever the cache's slots hold there meets no product; boxes that lie there
-//     wholly are not read at all.
+//     TMEM, in front of the one code that weighs.  Code is what an SM's instruction cache
+//     holds least of, so there is one copy of each part: at two thirds of its first room
+//     single tokens took 100 us for 105 and FP8 chunks 306 for 341.  V rows past the
+//     sequence, or before every row's window, are zeroed, so that whatever the cache's slots
+//     hold there meets no product; boxes that lie there wholly are not read at all.
 //   * P is rounded to BF16 (half a step: 2^-8 of each weight), the form the tensor
 //     core multiplies with a BF16 V; l sums the unrounded weights in FP32, S, O, m and l
 //     are FP32.  An FP8 cache is converted to f16 tiles (exactly) by warps 2 and 3, q
@@ -39,15 +39,15 @@
 //     of it).
 //
 // What bounds it.  Long prompts: the tensor core (a prompt of 8192 tokens, 32 heads of 128
-// over 8: 345 us, 1594 TFLOP/s, 84% of a library product's; eight query heads a KV head and
-// a chunk behind 32768 tokens 1650 to 1670).  A tile of 256 rows takes 2048 cycles of
-// products at D = 128, 1075 of softmax, 2048 of shared memory.  D = 64: the softmax (870
-// TFLOP/s).  D = 256: one O, so that scores wait for weights (1150).  FP8: shared memory,
-// 320 KB a tile (1140; four converting warps more take 5% longer).  Single tokens: HBM (a
-// step of 256 behind 4096 tokens 6660 GB/s), over FP8 three landing tiles a CTA (3200).  Small
-// calls: the way there, 3 us of it code that is not in the caches yet, and the fold.  Short
-// items: about 4000 cycles of way out a stream, which overlaps the next item's first
-// tiles alone (eight prompts of 1024 tokens 86 us).
+// over 8: 336 us, 1640 TFLOP/s, 86% of a library product's; with eight query heads a KV head
+// 1675), whose operands at D = 128 also fill shared memory: a tile of 256 rows takes 2048
+// cycles of products, 2048 of shared memory and 1075 of softmax, and 2300 in all.  D = 64:
+// the softmax (870 TFLOP/s).  D = 256: one O, so that scores wait for weights (1160).  FP8:
+// shared memory, 320 KB a tile, and its conversion (1340; four converting warps more take 5%
+// longer).  Single tokens: HBM (a step of 256 behind 2048 tokens 6140 GB/s).  Small calls:
+// the way to the first tile, 4 us of it code that is not in the caches yet, and the fold.
+// Short items: the way out, 2500 cycles a stream, beside the next item's first tiles (eight
+// prompts of 1024 tokens 76.5 us, 900 TFLOP/s).
 #pragma once
 
 #include <cuda.h>

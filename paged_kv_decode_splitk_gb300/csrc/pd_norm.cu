@@ -22,7 +22,7 @@
 // What bounds it is memory: 4 bytes an element forward, 6 backward.  Where rows are many, the
 // blocks that fit the GPU share the tokens out evenly, and a line of lanes walks the rows of
 // its block with the loads of the next few rows in flight all the time.  16384 x 32 heads of
-// 128 columns forward 46.6 us (5760 GB/s, 85% of a copy's rate), backward 74 (81%), an append
+// 128 columns forward 46.6 us (5760 GB/s, 85% of a copy's rate), backward 73 (82%), an append
 // of 32784 tokens with wide heads 117 (85%); a row a line with a block for each few of them
 // measured 46.6, 79.8 and 148 (for 131 then), turns that are made for the rows in flight
 // alone 50, 82 and 148, three blocks a multiprocessor with half the loads 46.4, 87.7 and 146.

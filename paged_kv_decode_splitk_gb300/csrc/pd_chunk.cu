@@ -216,7 +216,8 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     if (!aligned16(workspace)) return report(PD_ERR_INVALID, "workspace must be 16-byte aligned");
     uint8_t *ws = static_cast<uint8_t *>(workspace);
 
-    if (!token_starts && !lse && (window == 0 || window >= static_cast<long long>(max_blocks) * block_size) && inv_sqrt_d > 0 &&
+    const double scale = static_cast<double>(inv_sqrt_d) * (kv8 ? static_cast<double>(k_scale) : 1.0) * 1.4426950408889634;
+    if (!token_starts && !lse && (window == 0 || window >= static_cast<long long>(max_blocks) * block_size) && scale >= FLT_MIN &&
         q_tok == static_cast<int64_t>(num_q_heads) * head_dim && tokens_alone(num_q_heads / num_kv_heads, kv8)) {
         const int splits = token_splits(num_seqs, num_q_heads, num_kv_heads, head_dim, workspace_bytes);
         return kv8 ? pd_decode_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, max_blocks, context_lens, out, num_seqs,
@@ -239,7 +240,6 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     ChunkParams p = {};
     p.status = device_status_word(&err);
     if (!p.status) return err;
-    const double scale = static_cast<double>(inv_sqrt_d) * (kv8 ? static_cast<double>(k_scale) : 1.0) * 1.4426950408889634;
     p.max_tokens = max_blocks * block_size;
     // (a window no table can fill is none)
     p.shape = make_shape(num_q_heads, num_kv_heads, dpad, window < p.max_tokens ? window : 0);

@@ -42,7 +42,7 @@
 // over 8: 336 us, 1640 TFLOP/s, 86% of a library product's; with eight query heads a KV head
 // 1675), whose operands at D = 128 also fill shared memory: a tile of 256 rows takes 2048
 // cycles of products, 2048 of shared memory and 1075 of softmax, and 2300 in all.  D = 64:
-// the softmax (870 TFLOP/s).  D = 256: one O, so that scores wait for weights (1160).  FP8:
+// the softmax (900 TFLOP/s).  D = 256: one O, so that scores wait for weights (1160).  FP8:
 // shared memory, 320 KB a tile, and its conversion (1340; four converting warps more take 5%
 // longer).  Single tokens: HBM (a step of 256 behind 2048 tokens 6140 GB/s).  Small calls:
 // the way to the first tile, 4 us of it code that is not in the caches yet, and the fold.

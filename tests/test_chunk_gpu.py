@@ -234,6 +234,9 @@ def test_chunk_single_tokens_alone(S, longest, Hq, Hkv, D, fp8):
     for scale in (-0.1, 0.0):
         b.scale = scale
         b.check(b.run(), "scale")
+    if fp8:
+        b.scale, b.k_scale = 0.1, -0.25
+        b.check(b.run(), "scale of the keys")
 
 
 def test_chunk_is_the_prompt_in_pieces():
@@ -418,3 +421,22 @@ def test_quick_calls_take_what_fits_and_leave_the_rest():
                    (10, torch.empty(16, dtype=torch.uint8, device=DEV)), (11, None)):
         assert quick.chunk_attn(*args[:i], bad, *args[i + 1:]) is NotImplemented, (i, bad)
     assert quick.chunk_attn(*args[:-1]) is NotImplemented
+
+
+@pytest.mark.parametrize("lse", [False, True])
+def test_chunk_of_70000_sequences(lse):
+    """One token each, behind none or one: its own value, or between the two."""
+    S = 70000
+    q, kc, vc = randn(S, 1, 64, seed=1), randn(S // 8, 16, 1, 64, seed=2), randn(S // 8, 16, 1, 64, seed=3)
+    table = (torch.arange(S, device=DEV, dtype=torch.int32) // 8)[:, None].contiguous()
+    lens = (torch.arange(S, device=DEV, dtype=torch.int32) % 3)
+    got = api.chunk_attn(q, kc, vc, table, lens, 0.125, return_lse=lse)
+    out = got[0] if lse else got
+    k, v = kc[table[:, 0].long(), :2, 0].double(), vc[table[:, 0].long(), :2, 0].double()
+    z = (q.double() @ k.transpose(1, 2))[:, 0] * 0.125
+    z[lens == 1, 1] = -float("inf")
+    w = torch.softmax(z, -1) * (lens > 0)[:, None]
+    ref, size = (w[:, :, None] * v).sum(1), (w[:, :, None] * v.abs()).sum(1)
+    # weights and the output rounded to BF16 (2^-8 each), scores off by 72 additions of products (2^-24 each) of at most 2^8
+    assert bool(((out[:, 0].double() - ref).abs() <= 2.0**-8 * (size + ref.abs()) + 2.0**-9 * size + 2.0**-100).all())
+    assert not bool(out[lens == 0].any())

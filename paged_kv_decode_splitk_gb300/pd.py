@@ -472,6 +472,11 @@ def pd_chunk_workspace_bytes(num_tokens: int, num_q_heads: int, num_kv_heads: in
     return lib().pd_chunk_workspace_bytes(num_tokens, num_q_heads, num_kv_heads, head_dim)
 
 
+def _window(window: int) -> int:
+    """A window as the library takes it: one above 31 bits is more than any table holds."""
+    return max(-1, min(window, 2**31 - 1))
+
+
 def pd_chunk_attn(q, k_cache, v_cache, block_table, context_lens, token_starts, out, lse, inv_sqrt_d: float, window: int, workspace,
                   stream=None, num_blocks: int | None = None) -> int:
     """out[T, Hq, D] (and lse[T, Hq], or None) <- attention of new tokens over a BF16 cache (see pd.h): q [T, Hq, D]
@@ -482,7 +487,7 @@ def pd_chunk_attn(q, k_cache, v_cache, block_table, context_lens, token_starts, 
     return _check(lib().pd_chunk_attn(
         q.data_ptr(), _token_stride(q), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb, context_lens.data_ptr(),
         _ptr(token_starts), out.data_ptr(), _ptr(lse), T, S, Hq, Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d,
-        window, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        _window(window), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def pd_chunk_attn_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, block_table, context_lens, token_starts, out, lse,
@@ -494,7 +499,7 @@ def pd_chunk_attn_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, block
     return _check(lib().pd_chunk_attn_fp8(
         q.data_ptr(), _token_stride(q), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, block_table.data_ptr(), mb,
         context_lens.data_ptr(), _ptr(token_starts), out.data_ptr(), _ptr(lse), T, S, Hq, Hkv, D, bs,
-        nb if num_blocks is None else num_blocks, inv_sqrt_d, window, _ptr(workspace),
+        nb if num_blocks is None else num_blocks, inv_sqrt_d, _window(window), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
 
 

@@ -440,3 +440,15 @@ def test_chunk_of_70000_sequences(lse):
     # weights and the output rounded to BF16 (2^-8 each), scores off by 72 additions of products (2^-24 each) of at most 2^8
     assert bool(((out[:, 0].double() - ref).abs() <= 2.0**-8 * (size + ref.abs()) + 2.0**-9 * size + 2.0**-100).all())
     assert not bool(out[lens == 0].any())
+
+
+def test_chunk_windows_past_31_bits():
+    a = Chunks([40], [300], 4, 2, 64, window=0)
+    want = a.run()
+    for window in (2**31 - 1, 2**31, 2**32 + 5, 2**40):
+        a.window = window
+        assert torch.equal(a.run(), want)
+    for window in (-1, -(2**32) + 5):
+        a.window = window
+        with pytest.raises(pd.PdError):
+            a.run()

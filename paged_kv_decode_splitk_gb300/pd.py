@@ -571,9 +571,9 @@ class Rope:
         return pd_rope_frequencies(self.desc)
 
     def close(self):
-        if self.handle:
-            pd_rope_destroy(self.handle)
-            self.handle = None
+        handle, self.handle = self.handle, None  # (from here on nobody is given it)
+        if handle:
+            pd_rope_destroy(handle)
 
     def __del__(self):
         try:

@@ -1,0 +1,54 @@
+"""GPU tests of norm_rope between autograd's other parts: closed rotations, the caller's hooks on saved tensors, checkpoints,
+second and forward-mode gradients.  Each through the CPython module's node and through the ctypes binding."""
+
+import numpy as np
+import pytest
+import torch
+import torch.autograd.forward_ad as fwd
+from torch.autograd.graph import saved_tensors_hooks
+from torch.utils.checkpoint import checkpoint
+
+from paged_kv_decode_splitk_gb300 import api, pd
+from test_norm_gpu import weight
+from test_rope_gpu import i32, make, randn
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+T, H, D = 11, 3, 80
+
+
+@pytest.fixture(autouse=True)
+def no_flags():
+    yield
+    assert pd.pd_device_status() == 0
+
+
+@pytest.fixture(params=["module", "binding"], autouse=True)
+def way(request, monkeypatch):
+    if request.param == "binding":
+        monkeypatch.setattr(pd, "_quick", pd._Declined())
+
+
+class Call:
+    def __init__(self):
+        self.rope = make(D, 40)[0]
+        self.pos = i32(np.arange(T) * 911)
+        self.x, self.w, self.g = randn(T, H, D, seed=5).requires_grad_(), weight(D, 0.0).requires_grad_(), randn(T, H, D, seed=6)
+
+    def __call__(self, **more):
+        return api.norm_rope(self.rope, self.x, self.w, self.pos, **more)
+
+    def want(self):
+        return api.norm_rope_backward(self.rope, self.x.detach(), self.w.detach(), self.pos, self.g)
+
+
+def test_closed_rotation():
+    """A rotation that is closed is refused on the host, by the call and by the gradient of an earlier one."""
+    c = Call()
+    y = c()
+    c.rope.close()
+    with pytest.raises(ValueError, match="closed"):
+        torch.autograd.grad(y, (c.x, c.w), c.g)
+    with pytest.raises(ValueError, match="closed"):
+        c()

@@ -171,10 +171,20 @@ def _check_rope(rotation, x, positions, out, dev: int) -> None:
 
 
 def _laid_out(grad):
-    """grad [T, H, D], its rows laid out anew where it comes broadcast, transposed or at an odd place."""
+    """grad (or what a hook on saved tensors gave back) [T, H, D], its rows laid out anew where it comes broadcast, transposed
+    or at an odd place."""
+    if grad.dim() != 3:
+        return grad
     if grad.data_ptr() % 16 or grad.stride(2) != 1 or any(n > 1 and (s <= 0 or s % 8) for n, s in zip(grad.shape[:2], grad.stride())):
         return grad.clone(memory_format=torch.contiguous_format)
     return grad
+
+
+def _in_order(t):
+    """t (or None) contiguous, at a place that a row may have."""
+    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 class _Rotation(torch.autograd.Function):
@@ -288,8 +298,8 @@ class _NormRotation(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        x, weight, positions = ctx.saved_tensors
-        dx, dw = norm_rope_backward(ctx.rotation, x, weight, positions, _laid_out(grad), ctx.eps, ctx.offset,
+        x, weight, positions = ctx.saved_tensors  # (which the caller's hooks may give back in another layout)
+        dx, dw = norm_rope_backward(ctx.rotation, _laid_out(x), _in_order(weight), _in_order(positions), _laid_out(grad), ctx.eps, ctx.offset,
                                     weight_grad=ctx.needs_input_grad[1])
         return dx if ctx.needs_input_grad[0] else None, dw, None, None, None, None, None
 

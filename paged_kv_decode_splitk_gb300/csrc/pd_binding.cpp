@@ -162,6 +162,24 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// A tensor that was saved, as the caller's hooks on saved tensors gave it back: of the type, sizes and device that it had.
+const at::Tensor &unpacked(const char *name, const at::Tensor &t, at::ScalarType dtype, at::IntArrayRef sizes, int dev) {
+    TORCH_CHECK_VALUE(t.scalar_type() == dtype && t.layout() == at::kStrided && t.is_cuda() && t.get_device() == dev && t.sizes() == sizes,
+                      "norm_rope's ", name, ": saved as ", dtype, " ", sizes, " on cuda:", dev, ", given back as ", t.scalar_type(), " ",
+                      t.sizes(), " on ", t.device());
+    return t;
+}
+// Rows [T, H, D], laid out anew where they come broadcast, transposed or at an odd place.
+at::Tensor laid_out(const at::Tensor &t) {
+    bool fits_rows = reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 && t.stride(2) == 1;
+    for (int i = 0; i < 2; ++i) fits_rows = fits_rows && (t.size(i) <= 1 || (t.stride(i) > 0 && t.stride(i) % 8 == 0));
+    return fits_rows ? t : t.clone(at::MemoryFormat::Contiguous);
+}
+// The same for what has to be contiguous.
+at::Tensor in_order(const at::Tensor &t) {
+    return t.is_contiguous() && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 ? t : t.clone(at::MemoryFormat::Contiguous);
+}
+
 // The interpreter's lock while it lives.
 struct Gil {
     const PyGILState_STATE state = PyGILState_Ensure();
@@ -204,14 +222,13 @@ struct NormRotation : torch::autograd::Node {
         torch::autograd::variable_list out(2);
         {
             at::AutoGradMode off(false);
-            const at::Tensor v = x.unpack(), w = weight.unpack(), pos = positions.unpack();
-            at::Tensor g = grads[0];
-            // (a gradient may come broadcast, transposed or at an odd place: then its rows are laid out anew)
-            bool fits_rows = reinterpret_cast<uintptr_t>(g.data_ptr()) % 16 == 0 && g.stride(2) == 1;
-            for (int i = 0; i < 2; ++i) fits_rows = fits_rows && (g.size(i) <= 1 || (g.stride(i) > 0 && g.stride(i) % 8 == 0));
-            if (!fits_rows) g = g.clone(at::MemoryFormat::Contiguous);
-            const int dev = static_cast<int>(v.get_device());
-            const int64_t T = v.size(0), H = v.size(1), D = v.size(2);
+            const at::Tensor g = laid_out(grads[0]);
+            const int dev = static_cast<int>(g.get_device());
+            const int64_t T = g.size(0), H = g.size(1), D = g.size(2);
+            const at::Tensor v = laid_out(unpacked("x", x.unpack(), at::kBFloat16, {T, H, D}, dev));
+            at::Tensor w = weight.unpack(), pos = positions.unpack();
+            if (w.defined()) w = in_order(unpacked("weight", w, at::kBFloat16, {D}, dev));
+            if (pos.defined()) pos = in_order(unpacked("positions", pos, at::kInt, {T}, dev));
             auto token = [&](const at::Tensor &t) { return T > 1 ? t.stride(0) : H * D; };
             auto head = [&](const at::Tensor &t) { return H > 1 ? t.stride(1) : D; };
             out[0] = fresh({T, H, D}, at::kBFloat16, dev);

@@ -52,3 +52,44 @@ def test_closed_rotation():
         torch.autograd.grad(y, (c.x, c.w), c.g)
     with pytest.raises(ValueError, match="closed"):
         c()
+
+
+def test_hooks_that_give_back_another_layout():
+    """The same values in other places: laid out anew."""
+    c = Call()
+    want = c.want()
+
+    def turned(t):
+        return t.transpose(0, -1).contiguous().transpose(0, -1) if t.dim() > 1 else torch.stack([t, t], 1)[:, 0]
+
+    def odd(t):
+        return torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:].view_as(t).copy_(t)
+
+    def broadcast(t):
+        return t.mean(0, keepdim=True).expand_as(t) if t.dim() == 3 else t
+
+    for unpack in (turned, odd):
+        with saved_tensors_hooks(lambda t: t.detach(), unpack):
+            y = c()
+        assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(y, (c.x, c.w), c.g), want))
+    with saved_tensors_hooks(lambda t: t.detach(), broadcast):
+        y = c()
+    got = torch.autograd.grad(y, (c.x, c.w), c.g)
+    want = api.norm_rope_backward(c.rope, broadcast(c.x.detach()).contiguous(), c.w.detach(), c.pos, c.g)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.autograd.graph.save_on_cpu():
+        y = c()
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(y, (c.x, c.w), c.g), c.want()))
+
+
+@pytest.mark.parametrize("which", ["x", "weight", "positions"])
+def test_hooks_that_give_back_something_else(which):
+    """Another type, shape or device: refused on the host."""
+    c = Call()
+    mine = {"x": c.x, "weight": c.w, "positions": c.pos}[which].shape
+    for change in (lambda t: t.double(), lambda t: t[:1], lambda t: t[None], lambda t: t[0], lambda t: t.cpu(),
+                   lambda t: torch.cat([t, t], -1)):
+        with saved_tensors_hooks(lambda t: t.detach(), lambda t: change(t) if t.shape == mine else t):
+            y = c()
+        with pytest.raises(ValueError):
+            torch.autograd.grad(y, (c.x, c.w), c.g)

@@ -696,9 +696,10 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
         const int D = p.head_dim;
         uint32_t sph = 0, oph = 0, hph = 0, qph = 0;  // phases, a bit for each buffer or stream
         bool ok = true, any = false;
-        // FP8: the rows' scales, in turn in two places: the other stream may still
-        // have to read the last segment's when this one's are written (it has by
-        // the time a third segment begins: its weights of the first went before)
+        // FP8: the rows' scales, by the segments that have keys in turn in two places: the
+        // other stream may still have to read the last one's when this one's are written (it
+        // has by the time of a third: the queries of that come behind the second's last
+        // scores, which were asked for behind all of the first's weights)
         float *row_scale = reinterpret_cast<float *>(smem + L::row_scale);
         int turn = 0, out_turn = 0;
         for (; ok && next_task(); task_done()) {
@@ -862,7 +863,7 @@ __global__ void __launch_bounds__(Plan<DPAD, KV8>::kThreads, 1)
             // -- the row's reference and sum for the way out, of the items that the stream had a
             // tile of, in turn in two places with a barrier each: by the time of a third the
             // first has been read, whose O had to leave before the second's products
-            turn ^= 1;
+            if (sg.n > 0) turn ^= 1;
             if (end_j > first_j) {
                 reinterpret_cast<float2 *>(smem + L::stream_ml)[(out_turn * 2 + t) * kRowTile + r] = make_float2(m, l);
                 arrive_warp(bar_ml + 8 * (2 * out_turn + t), lane);

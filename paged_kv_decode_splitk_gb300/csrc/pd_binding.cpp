@@ -11,6 +11,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/functions/utils.h>
@@ -253,34 +254,41 @@ struct NormRotation : torch::autograd::Node {
 // norm_rope_grad(handle | 0, head_dim, rotation | None, x, weight | None, positions | None, eps, weight_offset) -- of an x or
 // a weight that requires a gradient
 PyObject *norm_rope_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return quick(n, 8, [&] {
+    const std::shared_ptr<NormRotation> node(new NormRotation, torch::autograd::deleteNode);
+    at::Tensor x, weights, positions, made;
+    PyObject *declined = quick(n, 8, [&]() -> PyObject * {
         const int dev = device();
         const auto handle = reinterpret_cast<const pd_rope *>(integer(a[0]));
-        const Rows x = rows(a[3], dev, false);
-        const void *w = weight(a[4], x.D, dev);
+        const Rows r = rows(a[3], dev, false);
+        const void *w = weight(a[4], r.D, dev);
         need((handle != nullptr) == (a[5] != Py_None) && (handle != nullptr) == (a[2] != Py_None));
-        at::Tensor positions, weights;
+        x = *r.t;
         if (w) weights = THPVariable_Unpack(a[4]);
         if (handle) {
             positions = whole(a[5], 1, at::kInt, dev);
-            need(x.D == integer(a[1]) && positions.size(0) == x.T);
+            need(r.D == integer(a[1]) && positions.size(0) == r.T);
         }
-        const std::shared_ptr<NormRotation> node(new NormRotation, torch::autograd::deleteNode);
         node->eps = real(a[6]);
         node->offset = real(a[7]);
-        const at::Tensor made = fresh(x.t->sizes(), at::kBFloat16, dev);
-        need(pd_norm_rope_apply(handle, x.data(), x.token, x.head, w, node->eps, node->offset, handle ? ints(positions) : nullptr,
-                                made.data_ptr(), x.H * x.D, x.D, fits(x.T), fits(x.H), fits(x.D), stream(dev)) == PD_OK);
-        node->x = torch::autograd::SavedVariable(*x.t, false);
-        if (w) node->weight = torch::autograd::SavedVariable(weights, false);
-        if (handle) {
-            node->positions = torch::autograd::SavedVariable(positions, false);
-            node->rotation = Py_NewRef(a[2]);
-        }
-        node->set_next_edges(torch::autograd::collect_next_edges(*x.t, weights));
-        torch::autograd::set_history(made, node);
-        return THPVariable_Wrap(made);
+        made = fresh(x.sizes(), at::kBFloat16, dev);
+        need(pd_norm_rope_apply(handle, r.data(), r.token, r.head, w, node->eps, node->offset, handle ? ints(positions) : nullptr,
+                                made.data_ptr(), r.H * r.D, r.D, fits(r.T), fits(r.H), fits(r.D), stream(dev)) == PD_OK);
+        return nullptr;
     });
+    if (declined) return declined;
+    // Saving a tensor runs the caller's hooks.  What they raise is not a refusal to be tried again but the caller's to see:
+    // torch's checkpoints end a recomputation so.
+    HANDLE_TH_ERRORS
+    node->x = torch::autograd::SavedVariable(x, false);
+    if (weights.defined()) node->weight = torch::autograd::SavedVariable(weights, false);
+    if (positions.defined()) {
+        node->positions = torch::autograd::SavedVariable(positions, false);
+        node->rotation = Py_NewRef(a[2]);
+    }
+    node->set_next_edges(torch::autograd::collect_next_edges(x, weights));
+    torch::autograd::set_history(made, node);
+    return THPVariable_Wrap(made);
+    END_HANDLE_TH_ERRORS
 }
 
 // What append_kv and append_kv_normed have in common: the tensors from q (a[0]) to v, the caches to q_out, and the scales.

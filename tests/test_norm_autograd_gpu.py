@@ -93,3 +93,39 @@ def test_hooks_that_give_back_something_else(which):
             y = c()
         with pytest.raises(ValueError):
             torch.autograd.grad(y, (c.x, c.w), c.g)
+
+
+def projection(x, m, rope, w, pos):
+    return api.norm_rope(rope, (x @ m).view(len(x), H, D), w, pos)
+
+
+def test_checkpointed():
+    """A projection with its norm, whose recomputation torch ends from inside the norm's last saved tensor."""
+    c = Call()
+    x, m = randn(T, 64, seed=1).requires_grad_(), randn(64, H * D, seed=2, scale=0.1).requires_grad_()
+    want = torch.autograd.grad(projection(x, m, c.rope, c.w, c.pos), (x, m, c.w), c.g)
+    for _ in range(2):
+        y = checkpoint(projection, x, m, c.rope, c.w, c.pos, use_reentrant=False)
+        got = torch.autograd.grad(y, (x, m, c.w), c.g)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_errors_of_hooks_pass():
+    c = Call()
+
+    class Full(Exception):
+        pass
+
+    packed = []
+
+    def pack(t):
+        packed.append(t)
+        raise Full("no room")
+
+    with saved_tensors_hooks(pack, lambda t: t), pytest.raises(Full):
+        c()
+    assert len(packed) == 1
+    with saved_tensors_hooks(lambda t: t.detach(), lambda t: pack(t)):
+        y = c()
+    with pytest.raises(Full):
+        torch.autograd.grad(y, c.x, c.g)

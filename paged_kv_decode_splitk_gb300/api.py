@@ -286,6 +286,18 @@ def _check_norm(rotation, x, weight, positions, dev: int) -> None:
         raise ValueError("positions without a rotation")
 
 
+class _Last(torch.autograd.Function):
+    """A gradient of norm_rope, which has none itself: an error where one is asked for."""
+
+    @staticmethod
+    def forward(ctx, t):
+        return t.view_as(t)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("norm_rope has no second gradient")
+
+
 class _NormRotation(torch.autograd.Function):
     """norm_rope where x or weight requires a gradient."""
 
@@ -296,11 +308,13 @@ class _NormRotation(torch.autograd.Function):
         return norm_rope(rotation, x, weight, positions, eps, weight_offset, stream=stream)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         x, weight, positions = ctx.saved_tensors  # (which the caller's hooks may give back in another layout)
-        dx, dw = norm_rope_backward(ctx.rotation, _laid_out(x), _in_order(weight), _in_order(positions), _laid_out(grad), ctx.eps, ctx.offset,
-                                    weight_grad=ctx.needs_input_grad[1])
+        with torch.no_grad():
+            dx, dw = norm_rope_backward(ctx.rotation, _laid_out(x), _in_order(weight), _in_order(positions), _laid_out(grad), ctx.eps,
+                                        ctx.offset, weight_grad=ctx.needs_input_grad[1])
+        if torch.is_grad_enabled():
+            dx, dw = (None if t is None else _Last.apply(t.requires_grad_()) for t in (dx, dw))
         return dx if ctx.needs_input_grad[0] else None, dw, None, None, None, None, None
 
 

@@ -246,8 +246,13 @@ struct NormRotation : torch::autograd::Node {
                                                  room.defined() ? static_cast<size_t>(room.size(0)) : 0, ::stream(dev));
             TORCH_CHECK(rc == PD_OK, "libpd error ", rc, ": ", pd_last_error());
         }
-        if (!again) return out;
-        return torch::autograd::DelayedError("norm_rope has no second gradient", 2)(std::move(out));
+        // (asked for a gradient that can be differentiated: an error where it is, which only what requires a gradient carries)
+        for (at::Tensor &t : out) {
+            if (!again || !t.defined()) continue;
+            t.set_requires_grad(true);
+            t = torch::autograd::DelayedError("norm_rope has no second gradient", 1)({t})[0];
+        }
+        return out;
     }
 };
 

@@ -129,3 +129,22 @@ def test_errors_of_hooks_pass():
         y = c()
     with pytest.raises(Full):
         torch.autograd.grad(y, c.x, c.g)
+
+
+def test_no_second_gradient():
+    """A gradient made with create_graph carries an error, whatever it came from, instead of no history."""
+    c = Call()
+    for grad in (c.g, c.g.clone().requires_grad_()):
+        y = c()
+        dx, dw = torch.autograd.grad(y, (c.x, c.w), grad, create_graph=True)
+        assert dx.requires_grad and dw.requires_grad and all(torch.equal(a, b) for a, b in zip((dx, dw), c.want()))
+        for more in (dx, dw):
+            with pytest.raises(RuntimeError, match="no second gradient"):  # not the first one alone
+                ((y.float() ** 2).sum() + more.float().pow(2).sum()).backward(retain_graph=True)
+    y = api.norm_rope(None, c.x, None, None)
+    (dx,) = torch.autograd.grad(y, c.x, c.g, create_graph=True)
+    assert torch.equal(dx, api.norm_rope_backward(None, c.x.detach(), None, None, c.g)[0])
+    with pytest.raises(RuntimeError, match="no second gradient"):
+        dx.float().sum().backward()
+    got = torch.autograd.grad(c(), (c.x, c.w), c.g)
+    assert not any(t.requires_grad for t in got)

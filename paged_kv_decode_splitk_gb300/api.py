@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import numpy as np
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import pd
 
@@ -187,6 +188,12 @@ def _in_order(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+def _no_tangent(what: str, *tensors) -> None:
+    """Refuses forward-mode tangents, which no call here carries on."""
+    if any([t is not None and unpack_dual(t).tangent is not None for t in tensors]):
+        raise RuntimeError(f"{what} has no forward-mode derivative")
+
+
 class _Rotation(torch.autograd.Function):
     """rope where x requires a gradient, which is the transposed map's value."""
 
@@ -211,11 +218,13 @@ def rope(rotation: pd.Rope, x, positions, out=None, inverse: bool = False, strea
     if x.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out: no gradient can pass through a tensor that is given; call under torch.no_grad() or let rope make it")
+        _no_tangent("rope", x)
         return _Rotation.apply(x, rotation, positions, inverse, stream)
     if stream is None:
         done = pd.quick().rope(pd._handle(rotation), rotation.head_dim, x, positions, out, inverse)
         if done is not NotImplemented:
             return done
+    _no_tangent("rope", x)
     _check_rope(rotation, x, positions, out, pd.current_device())
     if out is None:
         out = _fresh(x.shape, _BF16, x.device, stream)
@@ -309,6 +318,7 @@ class _NormRotation(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad):
+        _no_tangent("norm_rope's gradient", grad)
         x, weight, positions = ctx.saved_tensors  # (which the caller's hooks may give back in another layout)
         with torch.no_grad():
             dx, dw = norm_rope_backward(ctx.rotation, _laid_out(x), _in_order(weight), _in_order(positions), _laid_out(grad), ctx.eps,
@@ -333,12 +343,14 @@ def norm_rope(rotation, x, weight, positions, eps: float = 1e-6, weight_offset: 
                                              positions, eps, weight_offset)
             if done is not NotImplemented:
                 return done
+        _no_tangent("norm_rope", x, weight)
         return _NormRotation.apply(x, weight, rotation, positions, eps, weight_offset, stream)
     if stream is None:
         done = pd.quick().norm_rope(pd._handle(rotation) or 0, 0 if rotation is None else rotation.head_dim, x, weight, positions, out, eps,
                                     weight_offset)
         if done is not NotImplemented:
             return done
+    _no_tangent("norm_rope", x, weight)
     dev = pd.current_device()
     _check_norm(rotation, x, weight, positions, dev)
     if out is not None:

@@ -65,6 +65,9 @@ Rows rows(PyObject *o, int dev, bool side) {
     return r;
 }
 
+// A forward-mode tangent, which no call here carries on (api.py refuses it).
+bool has_tangent(const at::Tensor &t) { return t._fw_grad(0).defined(); }
+
 int fits(int64_t v) {
     need(v >= 0 && v <= 0x7fffffff);
     return static_cast<int>(v);
@@ -109,7 +112,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Rows x = rows(a[2], dev, false);
         const at::Tensor &pos = whole(a[3], 1, at::kInt, dev);
         const long long inverse = integer(a[5]);
-        need(handle && x.D == integer(a[1]) && pos.size(0) == x.T && (inverse == 0 || inverse == 1));
+        need(!has_tangent(*x.t) && handle && x.D == integer(a[1]) && pos.size(0) == x.T && (inverse == 0 || inverse == 1));
         at::Tensor made;
         Rows o;
         if (a[4] == Py_None) {
@@ -129,7 +132,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
 const void *weight(PyObject *o, int64_t head_dim, int dev) {
     if (o == Py_None) return nullptr;
     const at::Tensor &t = whole(o, 1, at::kBFloat16, dev);
-    need(t.size(0) == head_dim);
+    need(t.size(0) == head_dim && !has_tangent(t));
     return t.data_ptr();
 }
 
@@ -142,7 +145,7 @@ PyObject *norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const void *w = weight(a[3], x.D, dev);
         const float eps = real(a[6]), offset = real(a[7]);
         const int32_t *positions = nullptr;
-        need((handle != nullptr) == (a[4] != Py_None));
+        need(!has_tangent(*x.t) && (handle != nullptr) == (a[4] != Py_None));
         if (handle) {
             const at::Tensor &t = whole(a[4], 1, at::kInt, dev);
             need(x.D == integer(a[1]) && t.size(0) == x.T);
@@ -219,6 +222,7 @@ struct NormRotation : torch::autograd::Node {
 
     torch::autograd::variable_list apply(torch::autograd::variable_list &&grads) override {
         if (!grads[0].defined()) return {at::Tensor(), at::Tensor()};
+        TORCH_CHECK(!has_tangent(grads[0]), "norm_rope's gradient has no forward-mode derivative");
         const bool again = at::GradMode::is_enabled();
         torch::autograd::variable_list out(2);
         {
@@ -266,7 +270,7 @@ PyObject *norm_rope_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const auto handle = reinterpret_cast<const pd_rope *>(integer(a[0]));
         const Rows r = rows(a[3], dev, false);
         const void *w = weight(a[4], r.D, dev);
-        need((handle != nullptr) == (a[5] != Py_None) && (handle != nullptr) == (a[2] != Py_None));
+        need(!has_tangent(*r.t) && (handle != nullptr) == (a[5] != Py_None) && (handle != nullptr) == (a[2] != Py_None));
         x = *r.t;
         if (w) weights = THPVariable_Unpack(a[4]);
         if (handle) {

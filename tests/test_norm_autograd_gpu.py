@@ -148,3 +148,32 @@ def test_no_second_gradient():
         dx.float().sum().backward()
     got = torch.autograd.grad(c(), (c.x, c.w), c.g)
     assert not any(t.requires_grad for t in got)
+
+
+@pytest.mark.parametrize("leaf", [True, False])
+def test_forward_mode_is_refused(leaf):
+    """A tangent, which neither call carries on, is not lost in silence."""
+    c = Call()
+    x, w = (t.detach().clone().requires_grad_(leaf) for t in (c.x, c.w))
+    with fwd.dual_level():
+        for a, b in ((fwd.make_dual(x, torch.ones_like(x)), c.w.detach()), (c.x.detach(), fwd.make_dual(w, torch.ones_like(w)))):
+            for out in (None,) if leaf else (None, torch.empty_like(x)):
+                with pytest.raises(RuntimeError, match="forward"):
+                    api.norm_rope(c.rope, a, b, c.pos, out=out)
+        with pytest.raises(RuntimeError, match="forward"):
+            api.rope(c.rope, fwd.make_dual(x, torch.ones_like(x)), c.pos)
+        assert torch.equal(api.norm_rope(c.rope, x.detach(), w.detach(), c.pos), c().detach())  # (no tangent, nothing to lose)
+    assert torch.equal(api.norm_rope(c.rope, x, w, c.pos), c().detach())
+
+
+def test_gradients_of_tangents_are_refused():
+    """Forward mode over a backward pass: what comes back to the call has a tangent, and its answer would not."""
+    c = Call()
+    y = c()
+    z = api.rope(c.rope, c.x, c.pos)
+    with fwd.dual_level():
+        g = fwd.make_dual(c.g, torch.ones_like(c.g))
+        for out in (y, z):
+            with pytest.raises(RuntimeError, match="forward"):
+                torch.autograd.grad(out, c.x, g, retain_graph=True)
+    assert torch.equal(torch.autograd.grad(y, c.x, c.g)[0], c.want()[0])

@@ -101,8 +101,19 @@ PyObject *quick(Py_ssize_t n, Py_ssize_t want, F body) {
     Py_RETURN_NOTIMPLEMENTED;
 }
 
-// `given`, or for None the tensor made here.
-PyObject *answer(PyObject *given, const at::Tensor &made) { return given == Py_None ? THPVariable_Wrap(made) : Py_NewRef(given); }
+// A tensor of the caller's has been written: a gradient that has saved it learns so by its version.  (Tensors of the
+// inference mode have none.)
+void wrote(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void wrote(PyObject *given) {
+    if (given != Py_None) wrote(THPVariable_Unpack(given));
+}
+// `given`, which has been written, or for None the tensor made here.
+PyObject *answer(PyObject *given, const at::Tensor &made) {
+    wrote(given);
+    return given == Py_None ? THPVariable_Wrap(made) : Py_NewRef(given);
+}
 
 // rope(handle, head_dim, x, positions, out | None, inverse)
 PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -329,6 +340,10 @@ struct Append {
         mb = fits(table->size(1));
     }
     bool fp8() const { return kc->scalar_type() == at::kByte; }
+    void wrote_caches() const {
+        wrote(*kc);
+        wrote(*vc);
+    }
 };
 
 // append_kv(handle | 0, head_dim, q, k, v, k_cache, v_cache, block_table, context_lens, token_starts | None,
@@ -346,6 +361,7 @@ PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                               p.out->data_ptr(), p.kc->data_ptr(), p.vc->data_ptr(), ints(*p.table), p.mb, p.lens, p.starts,
                                               p.T, p.S, p.Hq, p.H, p.D, p.bs, p.nb, stream(dev));
         need(rc == PD_OK);
+        p.wrote_caches();
         return answer(a[10], p.made);
     });
 }
@@ -368,6 +384,7 @@ PyObject *append_kv_normed(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                           p.out->data_ptr(), p.kc->data_ptr(), p.vc->data_ptr(), ints(*p.table), p.mb, p.lens, p.starts, p.T,
                                           p.S, p.Hq, p.H, p.D, p.bs, p.nb, stream(dev));
         need(rc == PD_OK);
+        p.wrote_caches();
         return answer(a[12], p.made);
     });
 }
@@ -413,6 +430,7 @@ PyObject *decode_attn_prefix(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                                    g, ints(table), mb, ints(lens), out.data_ptr(), S, Hq, H, D, bs, nb, scale, sp,
                                                    ws.data_ptr(), bytes, stream(dev));
         need(rc == PD_OK);
+        wrote(a[11]);
         return answer(a[10], made);
     });
 }
@@ -456,6 +474,8 @@ PyObject *chunk_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
                            : pd_chunk_attn(q.data(), q.token, kc.data_ptr(), vc.data_ptr(), ints(table), mb, ints(lens), starts,
                                            out.data_ptr(), lse, T, seqs, Hq, H, D, bs, nb, scale, win, ws.data_ptr(), bytes, stream(dev));
         need(rc == PD_OK);
+        wrote(a[9]);
+        wrote(a[10]);
         return answer(a[8], made);
     });
 }

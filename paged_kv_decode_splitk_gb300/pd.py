@@ -251,6 +251,17 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _wrote(rc: int, *tensors) -> int:
+    """_check, and torch learns of the caller's tensors that the library has written, as of its own writes: a gradient that
+    has saved one refuses it.  (Tensors of the inference mode have no version.)"""
+    if _check(rc) == PD_OK:
+        from torch.autograd.graph import increment_version
+        for t in tensors:
+            if t is not None and not t.is_inference():
+                increment_version(t)
+    return rc
+
+
 _torch_device = None  # () -> the current device's number
 _torch_stream = None  # (device) -> its current stream's address
 
@@ -378,7 +389,7 @@ def pd_decode_attn(q, k_cache, v_cache, block_table, context_lens, out, inv_sqrt
                               D, bs, nb if num_blocks is None else num_blocks, float(inv_sqrt_d),
                               int(num_splits), _ptr(workspace), ws_bytes, int(gqa_pack),
                               _stream(stream))
-    return _check(rc)
+    return _wrote(rc, out, workspace)
 
 
 def pd_decode_attn_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, block_table, context_lens,
@@ -396,7 +407,7 @@ def pd_decode_attn_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, bloc
                                   S, Hq, Hkv, D, bs, nb if num_blocks is None else num_blocks,
                                   float(inv_sqrt_d), int(num_splits), _ptr(workspace), ws_bytes,
                                   int(gqa_pack), _stream(stream))
-    return _check(rc)
+    return _wrote(rc, out, workspace)
 
 
 def pd_decode_attn_noalloc(q, k_cache, v_cache, block_table, context_lens, out, inv_sqrt_d: float,
@@ -413,7 +424,7 @@ def pd_decode_attn_noalloc(q, k_cache, v_cache, block_table, context_lens, out, 
                                       Hkv, D, bs, nb if num_blocks is None else num_blocks,
                                       float(inv_sqrt_d), int(num_splits), int(gqa_pack),
                                       _stream(stream))
-    return _check(rc)
+    return _wrote(rc, out)
 
 
 # ---- decode behind shared prefixes ----------------------------------------------------
@@ -430,11 +441,11 @@ def pd_decode_attn_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, group_
     S, Hq, D = q.shape
     nb, bs, Hkv, _ = k_cache.shape
     G, mpb = prefix_table.shape
-    return _check(lib().pd_decode_attn_prefix(
+    return _wrote(lib().pd_decode_attn_prefix(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_table.data_ptr(), mpb, prefix_lens.data_ptr(),
         _ptr(group_starts), G, block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), out.data_ptr(), S, Hq,
         Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d, num_splits, _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)), out, workspace)
 
 
 def pd_decode_attn_prefix_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, prefix_table, prefix_lens, group_starts,
@@ -444,11 +455,11 @@ def pd_decode_attn_prefix_fp8(q, k_cache, v_cache, k_scale: float, v_scale: floa
     S, Hq, D = q.shape
     nb, bs, Hkv, _ = k_cache.shape
     G, mpb = prefix_table.shape
-    return _check(lib().pd_decode_attn_prefix_fp8(
+    return _wrote(lib().pd_decode_attn_prefix_fp8(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, prefix_table.data_ptr(), mpb,
         prefix_lens.data_ptr(), _ptr(group_starts), G, block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
         out.data_ptr(), S, Hq, Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d, num_splits, _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)), out, workspace)
 
 
 def pd_debug_prefix_walk(group_starts, prefix_lens, num_q_heads: int, num_kv_heads: int, head_dim: int, fp8: bool = False,
@@ -484,10 +495,11 @@ def pd_chunk_attn(q, k_cache, v_cache, block_table, context_lens, token_starts, 
     T, Hq, D = q.shape
     nb, bs, Hkv, _ = k_cache.shape
     S, mb = block_table.shape
-    return _check(lib().pd_chunk_attn(
+    return _wrote(lib().pd_chunk_attn(
         q.data_ptr(), _token_stride(q), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb, context_lens.data_ptr(),
         _ptr(token_starts), out.data_ptr(), _ptr(lse), T, S, Hq, Hkv, D, bs, nb if num_blocks is None else num_blocks, inv_sqrt_d,
-        _window(window), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        _window(window), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
+        out, lse, workspace)
 
 
 def pd_chunk_attn_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, block_table, context_lens, token_starts, out, lse,
@@ -496,11 +508,11 @@ def pd_chunk_attn_fp8(q, k_cache, v_cache, k_scale: float, v_scale: float, block
     T, Hq, D = q.shape
     nb, bs, Hkv, _ = k_cache.shape
     S, mb = block_table.shape
-    return _check(lib().pd_chunk_attn_fp8(
+    return _wrote(lib().pd_chunk_attn_fp8(
         q.data_ptr(), _token_stride(q), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, block_table.data_ptr(), mb,
         context_lens.data_ptr(), _ptr(token_starts), out.data_ptr(), _ptr(lse), T, S, Hq, Hkv, D, bs,
         nb if num_blocks is None else num_blocks, inv_sqrt_d, _window(window), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)), out, lse, workspace)
 
 
 def pd_debug_chunk_walk(token_starts, context_lens, num_q_heads: int, num_kv_heads: int, head_dim: int, window: int = 0,
@@ -600,9 +612,9 @@ def _token_stride(t) -> int:
 def pd_rope_apply(rope, x, positions, out, inverse: bool = False, stream=None) -> int:
     """out [T, H, D] <- x [T, H, D] rotated by positions [T] (see pd.h); strided in tokens and heads."""
     T, H, D = x.shape
-    return _check(lib().pd_rope_apply(_handle(rope), x.data_ptr(), _token_stride(x), x.stride(1) if H > 1 else D,
+    return _wrote(lib().pd_rope_apply(_handle(rope), x.data_ptr(), _token_stride(x), x.stride(1) if H > 1 else D,
                                       positions.data_ptr(), out.data_ptr(), _token_stride(out),
-                                      out.stride(1) if H > 1 else D, T, H, inverse, _stream(stream)))
+                                      out.stride(1) if H > 1 else D, T, H, inverse, _stream(stream)), out)
 
 
 def pd_append_kv(rope, q, k, v, q_out, k_cache, v_cache, block_table, context_lens, token_starts=None, stream=None,
@@ -612,11 +624,11 @@ def pd_append_kv(rope, q, k, v, q_out, k_cache, v_cache, block_table, context_le
     T, Hkv, D = k.shape
     nb, bs = k_cache.shape[:2]
     S, mb = block_table.shape
-    return _check(lib().pd_append_kv(
+    return _wrote(lib().pd_append_kv(
         _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
         _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
         context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
-        nb if num_blocks is None else num_blocks, _stream(stream)))
+        nb if num_blocks is None else num_blocks, _stream(stream)), q_out, k_cache, v_cache)
 
 
 def pd_append_kv_fp8(rope, q, k, v, q_out, k_cache, v_cache, k_scale: float, v_scale: float, block_table, context_lens,
@@ -625,11 +637,11 @@ def pd_append_kv_fp8(rope, q, k, v, q_out, k_cache, v_cache, k_scale: float, v_s
     T, Hkv, D = k.shape
     nb, bs = k_cache.shape[:2]
     S, mb = block_table.shape
-    return _check(lib().pd_append_kv_fp8(
+    return _wrote(lib().pd_append_kv_fp8(
         _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(),
         _token_stride(v), _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, block_table.data_ptr(),
         mb, context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
-        nb if num_blocks is None else num_blocks, _stream(stream)))
+        nb if num_blocks is None else num_blocks, _stream(stream)), q_out, k_cache, v_cache)
 
 
 def _head_stride(t) -> int:
@@ -641,9 +653,9 @@ def pd_norm_rope_apply(rope, x, weight, positions, out, eps: float = 1e-6, weigh
     """out [T, H, D] <- x [T, H, D], each row's RMS norm times (weight_offset + weight [D]) rotated by positions [T] (see
     pd.h); strided in tokens and heads; rope and positions None for the norm alone, weight None for ones."""
     T, H, D = x.shape
-    return _check(lib().pd_norm_rope_apply(_handle(rope), x.data_ptr(), _token_stride(x), _head_stride(x), _ptr(weight), eps, weight_offset,
+    return _wrote(lib().pd_norm_rope_apply(_handle(rope), x.data_ptr(), _token_stride(x), _head_stride(x), _ptr(weight), eps, weight_offset,
                                            _ptr(positions), out.data_ptr(), _token_stride(out), _head_stride(out), T, H, D,
-                                           _stream(stream)))
+                                           _stream(stream)), out)
 
 
 def pd_norm_rope_workspace_bytes(head_dim: int) -> int:
@@ -654,10 +666,11 @@ def pd_norm_rope_backward(rope, x, weight, positions, grad, grad_x, grad_weight,
                           stream=None) -> int:
     """grad_x [T, H, D] and grad_weight [D] (or None) <- the gradients of pd_norm_rope_apply from the gradient of its out."""
     T, H, D = x.shape
-    return _check(lib().pd_norm_rope_backward(
+    return _wrote(lib().pd_norm_rope_backward(
         _handle(rope), x.data_ptr(), _token_stride(x), _head_stride(x), _ptr(weight), eps, weight_offset, _ptr(positions), grad.data_ptr(),
         _token_stride(grad), _head_stride(grad), grad_x.data_ptr(), _token_stride(grad_x), _head_stride(grad_x), _ptr(grad_weight), T, H, D,
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
+        grad_x, grad_weight, workspace)
 
 
 def pd_append_kv_normed(rope, q, k, v, q_weight, k_weight, q_out, k_cache, v_cache, block_table, context_lens, token_starts=None,
@@ -666,11 +679,11 @@ def pd_append_kv_normed(rope, q, k, v, q_weight, k_weight, q_out, k_cache, v_cac
     T, Hkv, D = k.shape
     nb, bs = k_cache.shape[:2]
     S, mb = block_table.shape
-    return _check(lib().pd_append_kv_normed(
+    return _wrote(lib().pd_append_kv_normed(
         _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(), _token_stride(v),
         _ptr(q_weight), _ptr(k_weight), eps, weight_offset, _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mb,
         context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
-        nb if num_blocks is None else num_blocks, _stream(stream)))
+        nb if num_blocks is None else num_blocks, _stream(stream)), q_out, k_cache, v_cache)
 
 
 def pd_append_kv_normed_fp8(rope, q, k, v, q_weight, k_weight, q_out, k_cache, v_cache, k_scale: float, v_scale: float, block_table,
@@ -680,11 +693,11 @@ def pd_append_kv_normed_fp8(rope, q, k, v, q_weight, k_weight, q_out, k_cache, v
     T, Hkv, D = k.shape
     nb, bs = k_cache.shape[:2]
     S, mb = block_table.shape
-    return _check(lib().pd_append_kv_normed_fp8(
+    return _wrote(lib().pd_append_kv_normed_fp8(
         _handle(rope), _ptr(q), 0 if q is None else _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr(), _token_stride(v),
         _ptr(q_weight), _ptr(k_weight), eps, weight_offset, _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale,
         block_table.data_ptr(), mb, context_lens.data_ptr(), _ptr(token_starts), T, S, 0 if q is None else q.shape[1], Hkv, D, bs,
-        nb if num_blocks is None else num_blocks, _stream(stream)))
+        nb if num_blocks is None else num_blocks, _stream(stream)), q_out, k_cache, v_cache)
 
 
 # ---- tiled ---------------------------------------------------------------------------
@@ -795,12 +808,12 @@ def pd_tiled_run(handle: int, q, sources, out, num_seqs: int, stream=None) -> in
     for i, (k, v, tb, tc, strides, lbvs) in enumerate(sources):
         blk, tok, kvh = (int(x) for x in strides)
         arr[i] = pd_tiled_source(_ptr(k), _ptr(v), _ptr(tb), _ptr(tc), blk, tok, kvh, int(lbvs))
-    return _check(lib().pd_tiled_run(handle, _ptr(q), ctypes.cast(arr, _VP) if sources else None,
-                                     len(sources), _ptr(out), num_seqs, _stream(stream)))
+    return _wrote(lib().pd_tiled_run(handle, _ptr(q), ctypes.cast(arr, _VP) if sources else None,
+                                     len(sources), _ptr(out), num_seqs, _stream(stream)), out)
 
 
 def pd_tiled_finalize(handle: int, out, num_seqs: int, stream=None) -> int:
-    return _check(lib().pd_tiled_finalize(handle, _ptr(out), num_seqs, _stream(stream)))
+    return _wrote(lib().pd_tiled_finalize(handle, _ptr(out), num_seqs, _stream(stream)), out)
 
 
 # ---- diagnostics -------------------------------------------------------------------

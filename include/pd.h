@@ -378,7 +378,8 @@ int pd_decode_attn_prefix_fp8(const void *q, const void *k_cache, const void *v_
  * above 0) are given to pd_decode_attn's kernels where those are faster (over an FP8
  * cache, or at most four query heads a KV head): the same function, whose weights keep
  * 16 bits.
- * More work than 2^30 key tiles, by the sizes alone, is refused (PD_ERR_INVALID).
+ * More work than 2^30 key tiles, by the sizes and the window alone, is refused
+ * (PD_ERR_INVALID).
  * Returns PD_OK, PD_ERR_INVALID, PD_ERR_WORKSPACE, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
 size_t pd_chunk_workspace_bytes(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim);
 

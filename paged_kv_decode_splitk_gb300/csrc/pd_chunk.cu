@@ -275,8 +275,9 @@ int chunk_impl(const char *what, const void *q, int64_t q_tok, const void *k_cac
     if (rc != PD_OK) return rc;
     // no more CTAs than the most units these sizes can make would be shared by
     const long long items = static_cast<long long>(num_seqs) + num_tokens / p.shape.block_tokens;
-    const long long most = items * p.shape.heads * (kItemUnits + (p.max_tokens >> p.shape.tile_log2) + 1);
-    if (most > kMaxUnits) return report(PD_ERR_INVALID, "%s: launch too large (%d tokens, tables of %d)", what, num_tokens, p.max_tokens);
+    const long long most = items * p.shape.heads * most_block_units(p.shape, p.max_tokens);
+    if (most > kMaxUnits)
+        return report(PD_ERR_INVALID, "%s: launch too large (%d tokens, tables of %d, a window of %d)", what, num_tokens, p.max_tokens, window);
     const int sms = sm_count_of_device();
     const int ctas = static_cast<int>(std::min<long long>(std::max(1, std::min(sms, kMaxCtas)), (most + kCtaUnits - 1) / kCtaUnits));
     p.ctas = make_fastdiv(ctas);
@@ -359,7 +360,7 @@ int pd_debug_chunk_walk(int num_seqs, const int32_t *token_starts, const int32_t
     // (bounded as the launch is, by each sequence's length)
     long long most = 0;
     for (int i = 0; i < num_seqs; ++i)
-        most += (1ll + spans(i).n / s.block_tokens) * s.heads * (kItemUnits + (context_lens[i] >> s.tile_log2) + 1);
+        most += (1ll + spans(i).n / s.block_tokens) * s.heads * most_block_units(s, context_lens[i]);
     if (most > kMaxUnits) return pd::report(PD_ERR_INVALID, "pd_debug_chunk_walk: too large");
     int W = 0;
     for (int i = 0; i < num_seqs; ++i) W += s.heads * head_units(s, spans(i));

@@ -98,7 +98,9 @@ __host__ __device__ inline int floor_sum(uint32_t n, uint32_t a, uint32_t b, int
         all += v;
         some += i < rest ? v : 0;
     }
-    return static_cast<int>(whole * all + step * (period * (whole * (whole - 1) / 2) + whole * rest) + some);
+    // (the pairs of periods pass 32 bits for prompts of 2^24 tokens and more, which a window makes few units of)
+    const uint32_t pairs = static_cast<uint32_t>(static_cast<uint64_t>(whole) * (whole - 1) / 2);
+    return static_cast<int>(whole * all + step * (period * pairs + whole * rest) + some);
 }
 
 __host__ __device__ inline int blocks_of(const Shape &s, int n) { return fast_div(n + s.block_tokens - 1, s.fd_block); }
@@ -120,10 +122,18 @@ __host__ __device__ inline int tiles_of(const Shape &s, const Span &q, int block
     return end > 0 ? end - first_tile(s, q, block) : 0;
 }
 
+// Units of a block at most, in tables of max_tokens: a window and the block's tokens behind it touch a tile more at
+// either end than they fill.
+inline long long most_block_units(const Shape &s, int max_tokens) {
+    const long long all = (max_tokens >> s.tile_log2) + 1ll;
+    const long long seen = ((static_cast<long long>(s.window) + s.block_tokens) >> s.tile_log2) + 2;
+    return kItemUnits + (s.window > 0 && seen < all ? seen : all);
+}
+
 // Units of the first `blocks` blocks of a head, all of them whole.
 __host__ __device__ inline int units_before(const Shape &s, const Span &q, int blocks) {
     const int TB = s.block_tokens;
-    int u = blocks * kItemUnits;
+    uint32_t u = static_cast<uint32_t>(blocks) * kItemUnits;  // (what a window takes away again may pass 32 bits)
     // ends: blocks from i0 on end past position 0
     const int i0 = q.past >= 0 ? 0 : fast_div(-q.past, s.fd_block);
     if (blocks > i0)
@@ -134,7 +144,7 @@ __host__ __device__ inline int units_before(const Shape &s, const Span &q, int b
         const int j0 = before > 0 ? fast_div(static_cast<int>(before < 0x7ffffe00 ? before : 0x7ffffe00) + TB - 1, s.fd_block) : 0;
         if (blocks > j0) u -= floor_sum(blocks - j0, q.past + j0 * TB + 1 - s.window, TB, s.tile_log2, s.period_log2);
     }
-    return u;
+    return static_cast<int>(u);
 }
 // Units of a head in all.
 __host__ __device__ inline int head_units(const Shape &s, const Span &q) {

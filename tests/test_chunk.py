@@ -165,3 +165,21 @@ def test_api_refuses_tensors():
                    dict(lse=torch.zeros(6, 4).double()), dict(ws=torch.zeros(64, dtype=torch.uint8)[::2]), dict(dev=0)):
         with pytest.raises(ValueError):
             api._check_chunk(**{**good, **change})
+
+
+def test_walk_of_a_long_prompt_behind_a_window():
+    """2^27 tokens that see 128 keys each: 2^19 blocks of 256, of three tiles but for the first, although their keys before
+    the window would make 2^39 units."""
+    T, most = 2**27, 2**20
+    segments, n, totals = (pd.ctypes.c_int32 * (11 * most))(), pd.ctypes.c_int(), (pd.ctypes.c_int64 * 6)()
+    starts, lens = (pd.ctypes.c_int32 * 2)(0, T), (pd.ctypes.c_int32 * 1)(T)
+    pd._check(pd.lib().pd_debug_chunk_walk(1, starts, lens, 1, 1, 64, 128, 152, segments, most, pd.ctypes.byref(n), totals))
+    assert totals[2] == 256 and totals[3] == 128 and totals[0] == 5 * 2**19 - 1 and totals[1] == 152
+    segs = torch.frombuffer(segments, dtype=torch.int32).view(-1, 11)[:n.value].long()
+    rows, tile0, tiles = segs[:, 5], segs[:, 7], segs[:, 8]
+    first, last = (rows - 127).clamp(min=0) // 128, (rows + 255) // 128
+    assert int(tiles.sum()) == 3 * 2**19 - 1 and torch.equal(rows.unique(), torch.arange(0, T, 256))
+    whole = segs[:, 9] == 2
+    assert torch.equal(tile0[whole], first[whole]) and torch.equal(tiles[whole], (last - first + 1)[whole])
+    begun = segs[:, 9] == 1  # a border's item: its first part, and the other ones behind it
+    assert int((~whole).sum()) <= 2 * 151 and torch.equal(tile0[begun], first[begun])

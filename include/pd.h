@@ -377,7 +377,8 @@ int pd_decode_attn_prefix_fp8(const void *q, const void *k_cache, const void *v_
  * Single tokens alone (token_starts NULL, no window, lse NULL, contiguous q, a scale
  * above 0) are given to pd_decode_attn's kernels where those are faster (over an FP8
  * cache, or at most four query heads a KV head): the same function, whose weights keep
- * 16 bits.
+ * 16 bits (so a call may differ in its last bits from the same call with token_starts,
+ * a window or lse, by no more than the rounding above).
  * More work than 2^30 key tiles, by the sizes and the window alone, is refused
  * (PD_ERR_INVALID).
  * Returns PD_OK, PD_ERR_INVALID, PD_ERR_WORKSPACE, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
@@ -494,8 +495,10 @@ int pd_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride, in
  *   weight_offset 0, or what the weight is kept relative to (1 in some models).
  * pd_norm_rope_apply: x, out, their strides and positions as for pd_rope_apply
  * (positions may be NULL without a rotation).  Sums and arithmetic are FP32 (a row
- * whose mean square is above FP32's range becomes 0, and its infinities NaN), the
- * result is rounded to BF16 once.
+ * whose mean square is above FP32's range becomes 0, and its infinities NaN; where
+ * squares are below its normal numbers they lose bits or count as 0, so that eps
+ * alone scales the row, and an eps of 0 makes it infinite or NaN), the result is
+ * rounded to BF16 once.
  * Returns PD_OK, PD_ERR_INVALID, PD_ERR_UNSUPPORTED or PD_ERR_CUDA. */
 int pd_norm_rope_apply(const pd_rope *rope, const void *x, int64_t x_token_stride,
                        int64_t x_head_stride, const void *weight, float eps, float weight_offset,

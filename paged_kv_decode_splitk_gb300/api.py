@@ -334,7 +334,8 @@ def norm_rope(rotation, x, weight, positions, eps: float = 1e-6, weight_offset: 
     weight [D] (None: ones), rotated by positions [T] int32 (rotation and positions None: the norm alone).  Returns out
     [T, H, D] (contiguous unless given; x itself works in place).  Where x or weight requires a gradient, autograd calls
     norm_rope_backward (out cannot be given then; a backward pass is captured into a graph, as torch wants it, while no eager
-    graph of the same leaves lives)."""
+    graph of the same leaves lives); the rotation has to be open still when it does.  There is no second gradient and no
+    forward-mode one: both are refused."""
     if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)):
         if out is not None:
             raise ValueError("out: no gradient can pass through a tensor that is given; call under torch.no_grad() or let norm_rope make it")
@@ -364,7 +365,7 @@ def norm_rope(rotation, x, weight, positions, eps: float = 1e-6, weight_offset: 
 def norm_rope_backward(rotation, x, weight, positions, grad, eps: float = 1e-6, weight_offset: float = 0.0, weight_grad: bool = True,
                        stream=None):
     """The gradients of norm_rope from the gradient of its out [T, H, D]: (grad_x [T, H, D], grad_weight [D]), the second None
-    where it is not wanted or there is no weight."""
+    where it is not wanted or there is no weight.  No gradient passes through it."""
     dev = pd.current_device()
     _check_norm(rotation, x, weight, positions, dev)
     _rows("grad", grad, *x.shape, dev, False)
@@ -488,8 +489,9 @@ def chunk_attn(q, k_cache, v_cache, block_table, context_lens, inv_sqrt_d: float
     of q [T, Hq, D] (None: one each) are the last tokens of sequence s, whose context_lens [S] count them, and each sees the
     keys up to its own, the last `window` of them (0: all).  Returns out [T, Hq, D] BF16, and with return_lse (or an lse
     that is given) also lse [T, Hq], the logarithm of each row's sum.  Rows of no sequence get nothing: an out or lse made
-    here holds anything there.  uint8 caches are FP8 E4M3 codes with per-tensor scales.  A serving call: no gradient passes
-    through it."""
+    here holds anything there.  uint8 caches are FP8 E4M3 codes with per-tensor scales.  Keys and values that a token of the
+    call sees are finite; weights are rounded to BF16 (over FP8 to f16) before they meet V, but for single tokens alone that go
+    to the decode's kernels, which keep 16 bits.  A serving call: no gradient passes through it."""
     if lse is None and return_lse and q.dim() == 3:
         lse = _fresh(q.shape[:2], torch.float32, q.device, stream)
     if stream is None:

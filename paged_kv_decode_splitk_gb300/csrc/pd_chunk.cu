@@ -165,9 +165,22 @@ Layout layout_of(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim
 // pd_decode_attn computes, by units of a few heads and keys instead of a product's rows.
 // It takes them over FP8 (16 behind 1024 tokens 27.3 us here, 15.3 there; 64 behind 4096
 // 166 and 96; 200 behind 700 160 and 65), and over BF16 for at most four query heads a KV
-// head (32 over 8 of 128: 19.5 and 14, 169 and 155, 102 and 94; 16 over 16 of 64: 23 and
-// 20, 239 and 193, 138 and 101).  With more heads products have fuller rows: 32 over 2 of
-// 128, 256 behind 2048, 93 us here and 132 there, 64 behind 4096 54 and 60.
+// head, here and there (us):
+//                        1 x 500    16 x 1024  16 x 8192  64 x 300   64 x 4096  200 x 700
+//   16 over 16 of 64    12.2  7.6  22.8 25.1  131  141   37.1 20.2  247  191   138  101
+//   16 over 8 of 128    13.0 10.1  18.8 14.4  91.5 82.6  27.8 14.5  172  154   102  92.9
+//   32 over 8 of 128    12.8  9.8  18.6 15.0  92.1 83.2  28.8 14.6  172  156   103  94.0
+//   16 over 4 of 256    14.1 12.0  19.1 15.0  92.4 95.4  23.3 25.0  172  198   101  93.7
+// (it loses a little to the pass at some of the last and first head dims' sizes).  With 16
+// heads a KV head products have rows enough for the pass to be the faster one in most places,
+// with 8 in half of them at head dims of 64 and 256, but with 5 to 8 at 128 in none of these:
+// such calls could be given away too.
+//   40 over 8 of 128    12.8 10.1  18.7 15.3  91.8 83.9  28.8 14.7  173  155   103  94.6
+//   64 over 8 of 128    12.9  9.9  18.7 15.9  92.0 84.6  28.7 15.0  173  157   105  98.4
+//   32 over 4 of 128    12.8  9.7  15.4 15.0  51.4 46.1  19.1 16.5  93.7 85.5  58.3 58.3
+//   32 over 4 of 64     10.8  8.0  12.8 10.0  32.8 40.5  16.2 17.7  69.8 78.5  43.9 34.0
+//   16 over 2 of 256    13.3 12.9  15.2 18.1  52.3 54.2  16.5 20.9  93.7 110   57.4 48.8
+//   32 over 2 of 128    11.6 10.8  14.4 16.1  31.8 37.6  14.0 20.4  53.6 79.2  36.8 31.1
 bool tokens_alone(int group, bool kv8) { return kv8 ? group <= 16 : group <= 4; }
 
 // Its splits: as many as give every multiprocessor four of a sequence's KV heads, no more

@@ -39,12 +39,15 @@
 //     of it).
 //
 // What bounds it.  Long prompts: the tensor core (a prompt of 8192 tokens, 32 heads of 128
-// over 8: 336 us, 1640 TFLOP/s, 86% of a library product's; with eight query heads a KV head
-// 1675), whose operands at D = 128 also fill shared memory: a tile of 256 rows takes 2048
-// cycles of products, 2048 of shared memory and 1075 of softmax, and 2300 in all.  D = 64:
-// the softmax (900 TFLOP/s).  D = 256: one O, so that scores wait for weights (1160).  FP8:
-// shared memory, 320 KB a tile, and its conversion (1340; four converting warps more take 5%
-// longer).  Single tokens: HBM (a step of 256 behind 2048 tokens 6140 GB/s).  Small calls:
+// over 8: 327 to 340 us in a graph, 1620 to 1680 TFLOP/s, 85 to 89% of a library product's;
+// call after call, at the card's power limit, 337 to 366), whose operands at D = 128 also fill
+// shared memory: a tile of 256 rows takes 2048 cycles of products, 2048 of shared memory and
+// 1075 of softmax, and 2300 in all.  D = 64: nothing is full (900 TFLOP/s, 2600 cycles a tile:
+// products and shared memory 1024 each, softmax 1075); a stream's scores, softmax and values
+// follow one another, since P lies over S.  D = 256: nor there (1150, 2150 cycles for 128 rows
+// and 64 keys: products 1024, shared memory 1536); two S and one O of 128 rows fill TMEM, whose
+// softmax one group of four warps does.  FP8: shared memory, 320 KB a tile, and its conversion
+// (1330; four converting warps more take 5% longer).  Single tokens: HBM (a step of 256 behind 2048 tokens 6140 GB/s).  Small calls:
 // the way to the first tile, 4 us of it code that is not in the caches yet, and the fold.
 // Short items: the way out, 2500 cycles a stream, beside the next item's first tiles (eight
 // prompts of 1024 tokens 76.5 us, 900 TFLOP/s).
